@@ -30,6 +30,15 @@ ABI calls one to one on torch tensors.
 is the forward-only per-octave stage (2x box-downscaled octaves; per octave the
 luminance term l, the contrast-structure term cs and S = l * cs, their maps and
 per-image means).
+
+The rest of a training step, beside the loss:
+
+    grad_norm(grads, norm_type=2.0)
+    clip_grads(grads, max_norm, norm_type=2.0, out=None)
+    clip_grad_norm_(parameters, max_norm, norm_type=2.0)
+
+are the global norm of many gradient tensors and clipping by it, in place or
+into other tensors.
 """
 from __future__ import annotations
 
@@ -37,6 +46,7 @@ import torch
 
 from . import _abi
 from ._abi import SAME, VALID, GbssimError
+from ._grad_clip import clip_grad_norm_, clip_grads, grad_norm
 
 __all__ = [
     "fused_ssim",
@@ -52,6 +62,9 @@ __all__ = [
     "workspace_bytes",
     "saved_bytes",
     "window",
+    "grad_norm",
+    "clip_grads",
+    "clip_grad_norm_",
     "GbssimError",
     "VALID",
     "SAME",

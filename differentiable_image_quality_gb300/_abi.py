@@ -11,10 +11,13 @@ import ctypes
 import os
 import threading
 
+import torch
+
 from . import _build
 
 VALID, SAME = 0, 1
 PADDING = {"valid": VALID, "same": SAME}
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # gbssim_dtype
 
 _lock = threading.Lock()
 _lib = None       # the product library
@@ -23,6 +26,7 @@ _active = None    # the library the package's calls go to (None: the product lib
 
 # names the header declares, with (restype, argtypes)
 _vp, _sz, _i, _fp = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_void_p
+_f = ctypes.c_float
 SIGNATURES = {
     "gbssim_abi_version": (_i, []),
     "gbssim_strerror": (ctypes.c_char_p, [_i]),
@@ -44,6 +48,9 @@ SIGNATURES = {
     "ssim3d_fwd": (_i, [_fp, _fp, _i, _i, _i, _i, _i, _i, _fp, _fp, _fp, _sz, _i, _vp, _sz, _vp]),
     "ssim3d_bwd": (_i, [_fp, _fp, _fp, _i, _i, _i, _i, _i, _i, _fp, _sz, _fp, _fp, _vp, _sz,
                         _vp]),
+    "gbssim_grad_workspace_bytes": (_sz, [_i]),
+    "gbssim_grad_norm": (_i, [_vp, _vp, _vp, _i, _i, _fp, _vp, _sz, _vp]),
+    "gbssim_grad_clip": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _f, _fp, _vp, _sz, _vp]),
 }
 # exported only by the test build (libgbssim_test.so, csrc/gbssim_test_hooks.h):
 # forced row segments, the staging modes that drive the tests of the bounded-wait

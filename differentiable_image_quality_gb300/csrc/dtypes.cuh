@@ -1,0 +1,130 @@
+// Element types of the operators that take more than float32 (gbssim_dtype),
+// and 16-byte accesses to them.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "gbssim.h"
+
+namespace gbssim {
+
+using bf16 = __nv_bfloat16;
+using f16 = __half;
+
+__host__ __device__ constexpr bool dtype_ok(int t) { return t >= GBSSIM_F32 && t <= GBSSIM_F16; }
+__host__ __device__ constexpr int dtype_bytes(int t) { return t == GBSSIM_F32 ? 4 : 2; }
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(f16 v) { return __half2float(v); }
+
+// One rounding (to nearest even) from the 32-bit result.
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ bf16 from_f32<bf16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ f16 from_f32<f16>(float v) { return __float2half_rn(v); }
+
+// The two 16-bit values of a 32-bit word.
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<bf16>(uint32_t w)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<f16>(uint32_t w)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<bf16>(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<f16>(float a, float b)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// 16 bytes that this kernel reads once (or whose reuse is in L2): no line kept
+// in L1.
+__device__ __forceinline__ uint4 ld_stream16(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Eight consecutive elements as they lie in memory: one 16-byte word of a
+// 16-bit type, two of float32.
+template <typename T>
+struct Raw8 {
+    uint4 w[sizeof(T) == 4 ? 2 : 1];
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw8<T> &r, float (&v)[8])
+{
+    if constexpr (sizeof(T) == 4) {
+        v[0] = __uint_as_float(r.w[0].x); v[1] = __uint_as_float(r.w[0].y);
+        v[2] = __uint_as_float(r.w[0].z); v[3] = __uint_as_float(r.w[0].w);
+        v[4] = __uint_as_float(r.w[1].x); v[5] = __uint_as_float(r.w[1].y);
+        v[6] = __uint_as_float(r.w[1].z); v[7] = __uint_as_float(r.w[1].w);
+    } else {
+        const float2 a = unpack2<T>(r.w[0].x), b = unpack2<T>(r.w[0].y);
+        const float2 c = unpack2<T>(r.w[0].z), d = unpack2<T>(r.w[0].w);
+        v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+        v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> pack8(const float (&v)[8])
+{
+    Raw8<T> r;
+    if constexpr (sizeof(T) == 4) {
+        r.w[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                            __float_as_uint(v[3]));
+        r.w[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                            __float_as_uint(v[7]));
+    } else {
+        r.w[0] = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]),
+                            pack2<T>(v[6], v[7]));
+    }
+    return r;
+}
+
+// p: 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ Raw8<T> ld8_stream(const T *p)
+{
+    Raw8<T> r;
+    r.w[0] = ld_stream16(p);
+    if constexpr (sizeof(T) == 4) r.w[1] = ld_stream16(p + 4);
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void st8(T *p, const Raw8<T> &r)
+{
+    reinterpret_cast<uint4 *>(p)[0] = r.w[0];
+    if constexpr (sizeof(T) == 4) reinterpret_cast<uint4 *>(p)[1] = r.w[1];
+}
+
+}  // namespace gbssim

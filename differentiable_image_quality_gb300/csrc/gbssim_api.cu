@@ -7,9 +7,8 @@
 #include <queue>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "gbssim.h"
+#include "api_host.cuh"
 #include "common.cuh"
 #include "ssim2d.cuh"
 #include "ssim3d.cuh"
@@ -33,26 +32,9 @@ struct DeviceInfo {
     int occ3d[5] = {0, 0, 0, 0, 0};  // 3D: xy; z forward, gradient, + grad2; adjoint
 };
 
-// An NVTX range named after the entry point, open for the call's host-side work
-// (argument checks, planning, launches), so that a profiler's timeline shows
-// which call issued which kernels.  With no profiler attached both NVTX calls
-// return at once.
-struct CallRange {
-    explicit CallRange(const char *name) { nvtxRangePushA(name); }
-    ~CallRange() { nvtxRangePop(); }
-    CallRange(const CallRange &) = delete;
-    CallRange &operator=(const CallRange &) = delete;
-};
-
 std::mutex g_mutex;
 DeviceInfo g_dev[kMaxDevices];
 int g_seg_rows_override = 0;  // tuning: 0 = planner's choice
-
-int cuda_fail(cudaError_t e)
-{
-    (void)cudaGetLastError();  // clear a sticky launch error so the next call starts clean
-    return e == cudaSuccess ? GBSSIM_OK : GBSSIM_ECUDA;
-}
 
 // Per-device launch facts, filled once per device with that device current.
 int device_info(DeviceInfo **out)
@@ -125,15 +107,6 @@ int extent_ok(int n, int padding)
 }
 
 int out_extent(int n, int padding) { return padding == GBSSIM_VALID ? n - (kTaps - 1) : n; }
-
-bool overlaps(const void *a, size_t na, const void *b, size_t nb)
-{
-    if (!a || !b) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
-long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // Launch plan of the 2D streaming kernel: per plane, `per_plane` blocks over the
 // column strips; strips [0, extra) get base + 1 row segments, the rest base.

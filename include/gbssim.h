@@ -241,6 +241,44 @@ int ssim3d_fwd_bwd(const float *img1, const float *img2, int N, int C, int D, in
                    float *grad_img1, float *grad_img2_or_null, void *workspace,
                    size_t workspace_bytes, void *stream);
 
+/* ------------------------------------- gradient norm and clipping --------- */
+/* What a training step does between the loss's backward and the optimizer: the
+ * global norm of all gradients, and clipping by it.  The tensors may be of
+ * different types and lengths, each dense in memory (n, their order and their
+ * shapes do not matter), aligned to its element size:
+ *   S    = sum over all elements of g^2 (NORM_2) or |g| (NORM_1), max |g| (NORM_INF)
+ *   norm = sqrt(S) (NORM_2), S (otherwise); 0 when there is no element
+ *   c    = min(1, max_norm / (norm + 1e-6)),   out = g * c
+ * Sums of squares are accumulated in float32 over at most 64 values, beyond
+ * that in double; values whose squares leave float32's range are summed in
+ * double throughout.  g * c is formed in float32 and rounded once.  A NaN
+ * anywhere makes norm and c NaN; an infinity makes norm infinite and c zero
+ * (so finite gradients become 0, infinite ones NaN): the caller decides, from
+ * the norm, whether to skip the step. */
+
+typedef enum { GBSSIM_F32 = 0, GBSSIM_BF16 = 1, GBSSIM_F16 = 2 } gbssim_dtype;
+typedef enum { GBSSIM_NORM_INF = 0, GBSSIM_NORM_1 = 1, GBSSIM_NORM_2 = 2 } gbssim_norm_type;
+
+/* Workspace bytes for n tensors.  Same zero-fill rule as gbssim_workspace_bytes;
+ * 16-byte aligned. */
+size_t gbssim_grad_workspace_bytes(int n);
+
+/* grads, counts, dtypes: HOST arrays of n device addresses, element counts and
+ * gbssim_dtype codes (they are copied before the call returns).  out_norm: one
+ * float32 on the device.  Up to 1024 tensors go through one launch. */
+int gbssim_grad_norm(const void *const *grads, const long long *counts,
+                     const unsigned char *dtypes, int n, int norm_type, float *out_norm,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* The norm, and every gradient scaled by c.  outs[i] may be grads[i] (in place,
+ * same type) or another tensor of counts[i] elements of type out_dtypes[i], e.g.
+ * a float32 main gradient of a 16-bit one.  Outputs must not overlap one another
+ * or any other gradient.  max_norm: not negative. */
+int gbssim_grad_clip(const void *const *grads, void *const *outs, const long long *counts,
+                     const unsigned char *dtypes, const unsigned char *out_dtypes, int n,
+                     int norm_type, float max_norm, float *out_norm, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
