@@ -38,7 +38,14 @@ The rest of a training step, beside the loss:
     clip_grad_norm_(parameters, max_norm, norm_type=2.0)
 
 are the global norm of many gradient tensors and clipping by it, in place or
-into other tensors.
+into other tensors; and
+
+    fused_residual_norm(x, y, gate, post_norm=..., pre_norm=..., ...)
+
+is what a transformer block does around its residual sum -- the norm after the
+block, its gate, the scaled sum, the norm before the next block -- in one pass,
+with its backward; residual_norm_fwd / residual_norm_bwd are the two calls
+without autograd.  These take float32, bfloat16 and float16.
 """
 from __future__ import annotations
 
@@ -47,6 +54,7 @@ import torch
 from . import _abi
 from ._abi import SAME, VALID, GbssimError
 from ._grad_clip import clip_grad_norm_, clip_grads, grad_norm
+from ._residual_norm import fused_residual_norm, residual_norm_bwd, residual_norm_fwd
 
 __all__ = [
     "fused_ssim",
@@ -65,6 +73,9 @@ __all__ = [
     "grad_norm",
     "clip_grads",
     "clip_grad_norm_",
+    "fused_residual_norm",
+    "residual_norm_fwd",
+    "residual_norm_bwd",
     "GbssimError",
     "VALID",
     "SAME",

@@ -51,6 +51,9 @@ SIGNATURES = {
     "gbssim_grad_workspace_bytes": (_sz, [_i]),
     "gbssim_grad_norm": (_i, [_vp, _vp, _vp, _i, _i, _fp, _vp, _sz, _vp]),
     "gbssim_grad_clip": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _f, _fp, _vp, _sz, _vp]),
+    "gbssim_residual_norm_fwd": (_i, [_vp, _vp, _vp, _fp, _vp]),
+    "gbssim_residual_norm_workspace_bytes": (_sz, [_vp]),
+    "gbssim_residual_norm_bwd": (_i, [_vp, _vp, _vp, _fp, _vp, _vp, _sz, _vp]),
 }
 # exported only by the test build (libgbssim_test.so, csrc/gbssim_test_hooks.h):
 # forced row segments, the staging modes that drive the tests of the bounded-wait

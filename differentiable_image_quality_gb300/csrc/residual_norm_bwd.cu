@@ -1,0 +1,306 @@
+// Backward of the residual norm.  With G = dL/dx', V = dL/du:
+//   dx^ = V (w2 + o),  T = G + r2 (dx^ - mean(dx^) - x^ mean(dx^ x^)),   dx = s T,
+//   q = T g,  dy^ = q (w1 + o),  dy = r1 (dy^ - mean(dy^) - y^ mean(dy^ y^)),
+// (no mean(.) terms for the root-mean-square norm, dy = q without a post norm),
+// and over the rows that share a parameter
+//   dw2 = sum V x^,  db2 = sum V,  dw1 = sum q y^,  db1 = sum q,
+//   dg = sum T (y^ (w1 + o) + b1).
+// A gate that is shared by rows factors out of the sums: with A = sum T y^ and
+// F = sum T, dg = (w1 + o) A + b1 F, dw1 = g A, db1 = g F -- two column sums
+// serve three gradients.  A gate of its own per row has its gradient written
+// row by row, and A = sum q y^, F = sum q.
+//
+// Bound by memory: x, y, G and V are read once, dx and dy written once.  x^ and
+// y^ are formed again from x, y and the saved statistics, not stored.  Column
+// sums stay in registers over a block's rows (float32), go to a partial per
+// block, and a second kernel adds the partials in a fixed order.
+#include <algorithm>
+
+#include "residual_norm.cuh"
+#include "common.cuh"
+
+namespace gbssim {
+namespace {
+
+// One column sum of the block to its partial: over the block's teams first.
+template <bool ALIGNED>
+__device__ __forceinline__ void write_sum(const ResidualNormArgs &a, const Cols<ALIGNED> &c,
+                                          int place, float (&v)[8], float *scratch)
+{
+    if (place < 0) return;
+    const int item = int(blockIdx.x) / a.plan.cluster;
+    float *dst = a.partials + ((long long)item * a.sums + place) * a.dim;
+    if (a.plan.teams > 1) {
+        // teams of a warp by shuffles, then the warps through shared memory
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tpr = a.plan.tpr;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            for (int o = tpr; o < 32; o <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
+            if (lane < tpr) scratch[(warp * 32 + lane) * 8 + e] = v[e];
+        }
+        __syncthreads();
+        if (int(threadIdx.x) < tpr) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float s = 0.0f;
+                for (int w = 0; w < kSmallBlock / 32; ++w) s += scratch[(w * 32 + lane) * 8 + e];
+                if (c.has(e)) dst[c.col(e)] = s;
+            }
+        }
+        __syncthreads();
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (c.has(e)) dst[c.col(e)] = v[e];
+}
+
+// FULL: a gate of its own per row.  BIAS: either norm has a bias.
+template <typename R, typename Y, bool ALIGNED, bool FULL, bool BIAS>
+__global__ void __launch_bounds__(kMaxTeamThreads, 1)
+    residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a)
+{
+    __shared__ float2 slots[2][16];
+    __shared__ float2 cluster_slots[2][4];
+    __shared__ float scratch[kSmallBlock * 8];
+    const Cols<ALIGNED> c(a);
+    const BlockRows rows(a.plan);
+    TeamSum sum{slots, cluster_slots, 0, a.plan.tpr, a.plan.teams > 1 ? 1 : a.plan.threads / 32,
+                a.plan.cluster};
+    const int team = a.plan.teams > 1 ? int(threadIdx.x) / a.plan.tpr : 0;
+    // no block writes into another's shared memory before that block runs
+    if (a.plan.cluster > 1) cooperative_groups::this_cluster().sync();
+
+    float w1[8], b1[8], w2[8];  // with the gate of the column in w1 and b1, unless FULL
+    load_param(a.w1, rows.group, c, a.offset, 1.0f, w1);
+    load_param(a.w2, rows.group, c, a.offset, 1.0f, w2);
+    if (BIAS) load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
+    if (!FULL && a.gate.p) {
+        float g[8];
+        load_param(a.gate, rows.group, c, 0.0f, 1.0f, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            w1[e] *= g[e];
+            if (BIAS) b1[e] *= g[e];
+        }
+    }
+    float sa[8] = {}, sf[8] = {}, sc[8] = {}, se[8] = {};
+
+    for (int r0 = rows.r0; r0 < rows.r1; r0 += a.plan.teams) {
+        const int r = r0 + team;
+        const bool active = r < rows.r1;
+        const int b = r / a.tokens, t = r - b * a.tokens;
+        float4 st = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+        if (active) st = a.stats[r];
+        float yh[8], xh[8], T[8], V[8], g[8];
+        load_row(static_cast<const R *>(a.x.p) + row_offset(a.x, b, t), c, active, xh);
+        if (a.y.p)
+            load_row(static_cast<const Y *>(a.y.p) + row_offset(a.y, b, t), c, active, yh);
+        if (a.gx.p)
+            load_row(static_cast<const R *>(a.gx.p) + row_offset(a.gx, b, t), c, active, T);
+        if (a.gu.p)
+            load_row(static_cast<const Y *>(a.gu.p) + row_offset(a.gu, b, t), c, active, V);
+        if (FULL)
+            load_row(static_cast<const Y *>(a.gate_rows.p) + row_offset(a.gate_rows, b, t), c,
+                     active, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (!a.gx.p) T[e] = 0.0f;
+            if (!a.gu.p) V[e] = 0.0f;
+        }
+        if (a.y.p) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                yh[e] = c.has(e) ? (yh[e] - st.x) * st.y : 0.0f;
+                float z = BIAS ? fmaf(yh[e], w1[e], b1[e]) : yh[e] * w1[e];
+                if (FULL) z *= g[e];
+                xh[e] = fmaf(a.scale, xh[e], z);
+            }
+        }
+        if (a.gu.p) {
+            float2 m = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xh[e] = c.has(e) ? (xh[e] - st.z) * st.w : 0.0f;
+                sc[e] = fmaf(V[e], xh[e], sc[e]);
+                if (BIAS) se[e] += V[e];
+                V[e] *= w2[e];
+                m.x += V[e];
+                m.y = fmaf(V[e], xh[e], m.y);
+            }
+            if (a.pre != GBSSIM_ROW_NONE) {
+                m = sum(m);
+                const float m1 = a.pre == GBSSIM_ROW_LAYER ? m.x * a.inv_dim : 0.0f;
+                const float m2 = m.y * a.inv_dim;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    T[e] = fmaf(st.w, V[e] - fmaf(xh[e], m2, m1), T[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) T[e] += V[e];
+            }
+        }
+        float dx[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dx[e] = a.y.p ? a.scale * T[e] : T[e];
+        store_row(static_cast<R *>(a.dx) + (long long)r * a.dim, c, active && a.dx, dx);
+        if (!a.y.p) continue;
+        if (FULL && a.dgate_rows) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                dx[e] = T[e] * (BIAS ? fmaf(yh[e], w1[e], b1[e]) : yh[e] * w1[e]);
+            store_row(static_cast<Y *>(a.dgate_rows) + (long long)r * a.dim, c, active, dx);
+        }
+        float2 d = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (FULL) T[e] *= g[e];
+            if (!active || !c.has(e)) T[e] = 0.0f;
+            sa[e] = fmaf(T[e], yh[e], sa[e]);
+            if (BIAS) sf[e] += T[e];
+            T[e] *= w1[e];
+            d.x += T[e];
+            d.y = fmaf(T[e], yh[e], d.y);
+        }
+        if (a.post != GBSSIM_ROW_NONE) {
+            d = sum(d);
+            const float d1 = a.post == GBSSIM_ROW_LAYER ? d.x * a.inv_dim : 0.0f;
+            const float d2 = d.y * a.inv_dim;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) T[e] = st.y * (T[e] - fmaf(yh[e], d2, d1));
+        }
+        store_row(static_cast<Y *>(a.dy) + (long long)r * a.dim, c, active && a.dy, T);
+    }
+    write_sum(a, c, a.sum_a, sa, scratch);
+    write_sum(a, c, a.sum_c, sc, scratch);
+    if (BIAS) {
+        write_sum(a, c, a.sum_f, sf, scratch);
+        write_sum(a, c, a.sum_e, se, scratch);
+    }
+}
+
+// ------------------------------------------------------- the parameters' gradients
+
+constexpr int kFinishCols = 32, kFinishLanes = 32;
+
+__device__ __forceinline__ void store_param(const ParamGrad &g, int group, int dim, int col, float v)
+{
+    if (!g.p) return;
+    const long long i = (g.per_sample ? (long long)group * dim : 0) + col;
+    if (g.type == GBSSIM_F32) static_cast<float *>(g.p)[i] = v;
+    else if (g.type == GBSSIM_BF16) static_cast<bf16 *>(g.p)[i] = from_f32<bf16>(v);
+    else static_cast<f16 *>(g.p)[i] = from_f32<f16>(v);
+}
+
+// Adds the blocks' partials: a block takes 32 columns, its warps every 32nd
+// partial each, then the warps' sums in order.  blockIdx.y < groups: the
+// gradients that each group has of its own; the last: those shared by all.
+__global__ void __launch_bounds__(kFinishCols * kFinishLanes)
+    residual_norm_finish_kernel(const __grid_constant__ ResidualNormArgs a,
+                                const __grid_constant__ ParamGrads g, int shared_block)
+{
+    __shared__ float part[5][kFinishLanes][kFinishCols + 1];
+    pdl_wait();
+    const int cx = threadIdx.x & 31, lane = threadIdx.x >> 5;
+    const int col = int(blockIdx.x) * kFinishCols + cx;
+    const bool shared = int(blockIdx.y) == shared_block;
+    const int p0 = shared ? 0 : int(blockIdx.y) * a.plan.splits;
+    const int p1 = shared ? a.plan.groups * a.plan.splits : p0 + a.plan.splits;
+    const bool full = a.gate_rows.p != nullptr;
+    // dg, dw1, db1, dw2, db2
+    float v[5] = {};
+    if (col < a.dim) {
+        for (int p = p0 + lane; p < p1; p += kFinishLanes) {
+            const float *src = a.partials + (long long)p * a.sums * a.dim + col;
+            const int group = p / a.plan.splits;
+            const float A = a.sum_a >= 0 ? src[(long long)a.sum_a * a.dim] : 0.0f;
+            const float F = a.sum_f >= 0 ? src[(long long)a.sum_f * a.dim] : 0.0f;
+            const float gate = a.gate.p && !full ? param_at(a.gate, group, col) : 1.0f;
+            if (g.gate.p) {
+                const float w = a.w1.p ? param_at(a.w1, group, col) + a.offset : 1.0f;
+                const float b = a.b1.p ? param_at(a.b1, group, col) : 0.0f;
+                v[0] += fmaf(w, A, b * F);
+            }
+            v[1] = fmaf(gate, A, v[1]);
+            v[2] = fmaf(gate, F, v[2]);
+            if (a.sum_c >= 0) v[3] += src[(long long)a.sum_c * a.dim];
+            if (a.sum_e >= 0) v[4] += src[(long long)a.sum_e * a.dim];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 5; ++k) part[k][lane][cx] = v[k];
+    __syncthreads();
+    if (lane < 5 && col < a.dim) {
+        float s = 0.0f;
+        for (int l = 0; l < kFinishLanes; ++l) s += part[lane][l][cx];
+        const ParamGrad &out = lane == 0   ? g.gate
+                               : lane == 1 ? g.w1
+                               : lane == 2 ? g.b1
+                               : lane == 3 ? g.w2
+                                           : g.b2;
+        if (bool(out.per_sample) != shared) store_param(out, int(blockIdx.y), a.dim, col, s);
+    }
+}
+
+template <typename R, typename Y, bool ALIGNED, bool FULL, bool BIAS>
+cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.plan.grid);
+    cfg.blockDim = dim3(unsigned(a.plan.threads));
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(a.plan.cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.plan.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, residual_norm_bwd_kernel<R, Y, ALIGNED, FULL, BIAS>, a);
+}
+
+template <typename R, typename Y>
+cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
+{
+    const bool bias = a.b1.p || a.sum_e >= 0 || a.sum_f >= 0, full = a.gate_rows.p != nullptr;
+    if (a.plan.aligned) {
+        if (full) return bias ? launch<R, Y, true, true, true>(a, s) : launch<R, Y, true, true, false>(a, s);
+        return bias ? launch<R, Y, true, false, true>(a, s) : launch<R, Y, true, false, false>(a, s);
+    }
+    if (full) return bias ? launch<R, Y, false, true, true>(a, s) : launch<R, Y, false, true, false>(a, s);
+    return bias ? launch<R, Y, false, false, true>(a, s) : launch<R, Y, false, false, false>(a, s);
+}
+
+}  // namespace
+
+cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk,
+                                     const ParamGrads &g, cudaStream_t s)
+{
+    cudaError_t e = cudaSuccess;
+    if (a.plan.grid > 0) {
+        if (res == GBSSIM_F32) {
+            e = blk == GBSSIM_F32    ? launch<float, float>(a, s)
+                : blk == GBSSIM_BF16 ? launch<float, bf16>(a, s)
+                                     : launch<float, f16>(a, s);
+        } else {
+            e = res == GBSSIM_BF16 ? launch<bf16, bf16>(a, s) : launch<f16, f16>(a, s);
+        }
+    }
+    if (e != cudaSuccess || a.sums == 0) return e;
+    bool own = false, shared = false;
+    for (const ParamGrad *p : {&g.gate, &g.w1, &g.b1, &g.w2, &g.b2})
+        if (p->p) (p->per_sample ? own : shared) = true;
+    const int shared_block = own ? a.plan.groups : 0;
+    const unsigned ny = unsigned(shared_block + (shared ? 1 : 0));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned((a.dim + kFinishCols - 1) / kFinishCols), ny);
+    cfg.blockDim = dim3(kFinishCols * kFinishLanes);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, residual_norm_finish_kernel, a, g, shared_block);
+}
+
+}  // namespace gbssim

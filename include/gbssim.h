@@ -279,6 +279,87 @@ int gbssim_grad_clip(const void *const *grads, void *const *outs, const long lon
                      int norm_type, float max_norm, float *out_norm, void *workspace,
                      size_t workspace_bytes, void *stream);
 
+/* ---------------------------- the norms around a residual block, fused ---- */
+/* One pass over what a transformer block does between its matrix products and
+ * the residual stream: the norm after the block, its gate, the scaled residual
+ * sum, and the norm before the next block.  Per row (one token) of dim columns,
+ * x the residual stream and y the block's output:
+ *   y^ = (y - m1) r1,   z = y^ (post_weight + o) + post_bias,
+ *   x' = s x + gate z,
+ *   x^ = (x' - m2) r2,  u = x^ (pre_weight + o) + pre_bias,
+ * with m the row's mean (LAYER; zero for RMS) and r = 1 / sqrt(mean((. - m)^2) +
+ * eps); ROW_NONE leaves a norm out (m = 0, r = 1).  A missing weight is 1
+ * (without o), a missing bias 0, a missing gate 1.  s is residual_scale, o is
+ * weight_offset (1 for weights stored as a difference from one).
+ *
+ * Types: x and x' are res_dtype; y, u and a gate of its own per row blk_dtype;
+ * res_dtype is blk_dtype or float32.  Each parameter has its own type.
+ * Arithmetic is float32; each output is rounded once, and u is formed from x'
+ * before x' is rounded.  Rows that hold a NaN or an infinity affect no others.
+ *
+ * Shapes: batch x tokens rows, either of which may be 0 or 1; dim from 1 to
+ * 16384.  Inputs may have any non-negative strides between rows (element
+ * counts); the columns of a row are neighbours.  Outputs are dense. */
+
+typedef enum { GBSSIM_ROW_NONE = 0, GBSSIM_ROW_RMS = 1, GBSSIM_ROW_LAYER = 2 } gbssim_row_norm;
+
+/* A [batch, tokens, dim] tensor; data NULL: absent. */
+typedef struct {
+    const void *data;
+    long long batch_stride, token_stride;
+} gbssim_rows;
+
+/* A [dim] parameter, or with per_sample != 0 a [batch, dim] one whose samples lie
+ * sample_stride elements apart (>= 0); data NULL: absent. */
+typedef struct {
+    const void *data;
+    int dtype, per_sample;
+    long long sample_stride;
+} gbssim_param;
+
+typedef struct {
+    int batch, tokens, dim;
+    int res_dtype, blk_dtype;     /* gbssim_dtype */
+    int post_norm, pre_norm;      /* gbssim_row_norm */
+    float residual_scale, weight_offset, eps;
+    gbssim_rows x, y;             /* y absent: x' = x, and only the pre norm is taken */
+    gbssim_rows gate_rows;        /* a gate per row, or */
+    gbssim_param gate;            /* a gate per column */
+    gbssim_param post_weight, post_bias, pre_weight, pre_bias;
+} gbssim_residual_norm;
+
+/* Forward.
+ *   x_out  [batch, tokens, dim] of res_dtype, given if and only if y is; may be x
+ *          itself where x is dense.
+ *   u      [batch, tokens, dim] of blk_dtype, or NULL: x' alone.
+ *   stats  [batch * tokens][4] float32, 16-byte aligned, or NULL: m1, r1, m2, r2 of
+ *          each row, which the backward needs.
+ * One launch; no workspace. */
+int gbssim_residual_norm_fwd(const gbssim_residual_norm *desc, void *x_out_or_null,
+                             void *u_or_null, float *stats_or_null, void *stream);
+
+/* Where the backward writes; NULL: not wanted.  x, y and the gradient of a gate per
+ * row are dense [batch, tokens, dim] of their tensors' types; parameters' gradients
+ * have their parameters' types and shapes, dense (summed over the rows that share
+ * them). */
+typedef struct {
+    void *x, *y, *gate, *post_weight, *post_bias, *pre_weight, *pre_bias;
+} gbssim_residual_norm_grads;
+
+/* Workspace bytes of the backward (0 without rows, or for an invalid description);
+ * 16-byte aligned, contents arbitrary. */
+size_t gbssim_residual_norm_workspace_bytes(const gbssim_residual_norm *desc);
+
+/* Backward from the gradients of x' (res_dtype) and u (blk_dtype); either may be NULL
+ * (zero).  desc is the forward's, stats what it wrote.  Outputs are overwritten, and
+ * must not overlap any input or one another.  Without rows, the parameters'
+ * gradients are zero. */
+int gbssim_residual_norm_bwd(const gbssim_residual_norm *desc,
+                             const gbssim_rows *grad_x_out_or_null,
+                             const gbssim_rows *grad_u_or_null, const float *stats,
+                             const gbssim_residual_norm_grads *grads, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
