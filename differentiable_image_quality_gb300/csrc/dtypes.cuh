@@ -127,4 +127,57 @@ __device__ __forceinline__ void st8(T *p, const Raw8<T> &r)
     if constexpr (sizeof(T) == 4) reinterpret_cast<uint4 *>(p)[1] = r.w[1];
 }
 
+// ---------------------------------------------- eight elements at any alignment
+
+// Eight elements that begin `s` elements into consecutive 16-byte words: one
+// word more than eight elements fill.
+template <typename T>
+struct Wide8 {
+    static constexpr int kUnits = sizeof(T) == 4 ? 3 : 2;
+    uint32_t w[kUnits * 4];
+};
+
+// The eight elements from element s on (s < 16 / sizeof(T)).
+template <typename T>
+__device__ __forceinline__ Raw8<T> shift_down(const Wide8<T> &in, int s)
+{
+    uint32_t w[12];
+#pragma unroll
+    for (int i = 0; i < Wide8<T>::kUnits * 4; ++i) w[i] = in.w[i];
+    Raw8<T> r;
+    uint32_t *o = reinterpret_cast<uint32_t *>(&r);
+    if constexpr (sizeof(T) == 4) {
+        if (s & 2) {
+#pragma unroll
+            for (int i = 0; i < 10; ++i) w[i] = w[i + 2];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = s & 1 ? w[i + 1] : w[i];
+    } else {
+        if (s & 4) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        }
+        if (s & 2) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+        const unsigned half = (s & 1) * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(w[i], w[i + 1], half);
+    }
+    return r;
+}
+
+// 16 bytes to shared memory without passing through registers; L1 keeps the
+// line where a neighbour's copy overlaps.
+__device__ __forceinline__ void copy16_async(void *smem, const void *gmem, bool keep_l1)
+{
+    const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(smem));
+    if (keep_l1)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(s), "l"(gmem) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(gmem) : "memory");
+}
+
 }  // namespace gbssim

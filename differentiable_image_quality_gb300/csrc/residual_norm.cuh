@@ -7,6 +7,8 @@
 // norm) and 1 / sqrt(mean((. - m)^2) + eps).
 #pragma once
 
+#include <algorithm>
+
 #include <cooperative_groups.h>
 
 #include "gbssim.h"
@@ -27,6 +29,7 @@ constexpr int kMaxDim = 4 * kMaxTeamThreads * kColsPerThread;
 struct RowPtr {
     const void *p;
     long long sb, st;  // elements between batches and between tokens
+    const void *end;   // past the last row's last element
 };
 
 struct ParamPtr {
@@ -39,7 +42,8 @@ struct ParamPtr {
 // after another, `splits` of them to a group of group_rows consecutive rows: a
 // group is the rows that share the per-sample parameters, or all rows.
 struct RowPlan {
-    int aligned;       // 16-byte accesses everywhere
+    int aligned;       // every thread's columns lie on 16-byte boundaries in every row
+    int stages;        // rows of each thread in flight
     int cluster;       // blocks of a cluster (1, 2, 4)
     int block_cols;    // columns of a block: a multiple of 8
     int tpr;           // threads of a team in a block
@@ -81,55 +85,153 @@ cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk
 
 #ifdef __CUDACC__
 
-// The columns of this thread: eight neighbours where rows are aligned, eight
-// that lie a team's width apart otherwise (neighbouring lanes then still read
-// neighbouring elements).
+// The eight neighbouring columns of this thread.
 template <bool ALIGNED>
 struct Cols {
-    int first, n;  // the block's columns
-    int t, tpr;
+    int first;  // of the thread
+    int count;  // how many of the eight the row has; all or none where ALIGNED
+    int t;      // place in the team
+    bool last;  // the thread whose right neighbour has no column of the row
     __device__ __forceinline__ Cols(const ResidualNormArgs &a)
     {
         const int rank = a.plan.cluster > 1 ? int(blockIdx.x) % a.plan.cluster : 0;
-        first = rank * a.plan.block_cols;
-        n = min(a.plan.block_cols, a.dim - first);
-        tpr = a.plan.tpr;
-        t = a.plan.teams > 1 ? threadIdx.x & (tpr - 1) : threadIdx.x;
+        t = a.plan.teams > 1 ? threadIdx.x & (a.plan.tpr - 1) : threadIdx.x;
+        first = rank * a.plan.block_cols + t * kColsPerThread;
+        const int end = min(a.dim, (rank + 1) * a.plan.block_cols);
+        count = max(0, min(kColsPerThread, end - first));
+        last = count > 0 && first + kColsPerThread >= end;
     }
-    __device__ __forceinline__ int col(int e) const
+    __device__ __forceinline__ bool has(int e) const { return ALIGNED ? count > 0 : e < count; }
+};
+
+// Rows on their way through shared memory: every thread copies its own columns
+// of a row some rows ahead (cp.async) and reads them back itself, so the copies
+// need no barrier.  A stage holds, per tensor, 16-byte words [word][thread].
+//
+// Where rows do not start on 16-byte boundaries a thread copies the aligned
+// words that its columns lie in -- one more than they fill -- and shifts.  A word
+// that reaches over the tensor's first or last element is put together from
+// single elements.
+template <typename T, bool ALIGNED>
+struct Staged {
+    static constexpr int kUnits = (sizeof(T) == 4 ? 2 : 1) + (ALIGNED ? 0 : 1);
+
+    // Of a row whose first column is at `row`; slot: the thread's first word.
+    static __device__ __forceinline__ void fetch(const RowPtr &p, const T *row, int first,
+                                                 int count, uint4 *slot, int threads)
     {
-        return first + (ALIGNED ? t * kColsPerThread + e : e * tpr + t);
+        const unsigned char *at = reinterpret_cast<const unsigned char *>(row + first);
+        if constexpr (ALIGNED) {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) copy16_async(slot + u * threads, at + u * 16, false);
+        } else {
+            const unsigned char *stop = at + count * sizeof(T);
+            const unsigned char *word = at - (reinterpret_cast<uintptr_t>(at) & 15);
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u, word += 16) {
+                if (word >= stop) continue;
+                if (word >= p.p && word + 16 <= p.end) {
+                    copy16_async(slot + u * threads, word, true);
+                } else {
+                    const T *from = reinterpret_cast<const T *>(word);
+                    T *to = reinterpret_cast<T *>(slot + u * threads);
+                    for (int i = 0; i < int(16 / sizeof(T)); ++i)
+                        if (reinterpret_cast<const unsigned char *>(from + i) >= at &&
+                            reinterpret_cast<const unsigned char *>(from + i) < stop)
+                            to[i] = from[i];
+                }
+            }
+        }
     }
-    __device__ __forceinline__ bool has(int e) const
+
+    static __device__ __forceinline__ void read(const T *row, const Cols<ALIGNED> &c, bool active,
+                                                const uint4 *slot, int threads, float (&v)[8])
     {
-        return ALIGNED ? t * kColsPerThread < n : e * tpr + t < n;
+        if (!active || c.count == 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+            return;
+        }
+        if constexpr (ALIGNED) {
+            Raw8<T> r;
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) r.w[u] = slot[u * threads];
+            unpack8<T>(r, v);
+        } else {
+            Wide8<T> w;
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u)
+                reinterpret_cast<uint4 *>(w.w)[u] = slot[u * threads];
+            const int s = int(reinterpret_cast<uintptr_t>(row + c.first) & 15) / int(sizeof(T));
+            unpack8<T>(shift_down<T>(w, s), v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c.has(e) ? v[e] : 0.0f;
+        }
     }
 };
 
-template <bool ALIGNED, typename T>
-__device__ __forceinline__ void load_row(const T *row, const Cols<ALIGNED> &c, bool active,
-                                         float (&v)[8])
+__device__ __forceinline__ void staged_commit()
 {
-    if constexpr (ALIGNED) {
-        Raw8<T> r{};
-        if (active && c.has(0)) r = ld8_stream(row + c.col(0));
-        unpack8<T>(r, v);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = active && c.has(e) ? to_f32(row[c.col(e)]) : 0.0f;
-    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-template <bool ALIGNED, typename T>
+// Waits until at most stages - 1 of this thread's latest groups are in flight.
+__device__ __forceinline__ void staged_wait(int stages)
+{
+    if (stages >= 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Stores the thread's columns of a row.  Where the row does not start on a
+// 16-byte boundary, a thread takes the last `s` elements of its left neighbour
+// (by shuffle) in front of its own first 8 - s and stores those as whole words;
+// the first lane of a run stores its own first elements, the last its own last
+// ones, one by one.  All lanes of a warp call together.
+template <typename T, bool ALIGNED>
 __device__ __forceinline__ void store_row(T *row, const Cols<ALIGNED> &c, bool active,
                                           const float (&v)[8])
 {
+    T *at = row + c.first;
     if constexpr (ALIGNED) {
-        if (active && c.has(0)) st8(row + c.col(0), pack8<T>(v));
+        if (active && c.count > 0) st8(at, pack8<T>(v));
     } else {
+        const Raw8<T> own = pack8<T>(v);
+        const uint32_t *ow = reinterpret_cast<const uint32_t *>(&own);
+        constexpr int W = 2 * sizeof(T);                 // words of eight elements
+        constexpr int P = sizeof(T) == 4 ? 4 : 4;        // words of the neighbour that may be needed
+        constexpr int G = 16 / int(sizeof(T));           // elements of a 16-byte word
+        Wide8<T> both;                                   // neighbour's last word, then own
+#pragma unroll
+        for (int i = 0; i < P; ++i) both.w[i] = __shfl_up_sync(0xffffffffu, ow[W - P + i], 1);
+#pragma unroll
+        for (int i = 0; i < W; ++i) both.w[P + i] = ow[i];
+        if (!active || c.count == 0) return;
+        const int s = int(reinterpret_cast<uintptr_t>(at) & 15) / int(sizeof(T));
+        const bool head = c.t == 0 || (threadIdx.x & 31) == 0;
+        const bool tail = c.last || (threadIdx.x & 31) == 31;
+        if (s == 0 ? c.count == 8 : (!head && c.count >= 8 - s)) {
+            // elements [-s, 8 - s): from element G - s of `both`; s = 0 is own, unshifted
+            st8(at - s, s == 0 ? own : shift_down<T>(both, G - s));
+            if (s == 0 || !tail) return;
+#pragma unroll
+            for (int e = 1; e < 8; ++e)
+                if (e >= 8 - s && e < c.count) at[e] = from_f32<T>(v[e]);
+            return;
+        }
+        // the left neighbour's last elements, unless the neighbour stores them itself
+        if (s > 0 && !head) {
+            const T *left = reinterpret_cast<const T *>(both.w);
+#pragma unroll
+            for (int i = 1; i < G; ++i)
+                if (i >= G - s) at[i - G] = left[i];
+        }
+        // own elements: the right neighbour stores those from 8 - s on, unless this is a run's end
+        const int stop = s == 0 || tail ? c.count : min(c.count, 8 - s);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (active && c.has(e)) row[c.col(e)] = from_f32<T>(v[e]);
+            if (e < stop) at[e] = from_f32<T>(v[e]);
     }
 }
 
@@ -155,62 +257,68 @@ __device__ __forceinline__ void load_param(const ParamPtr &p, int group, const C
 {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        v[e] = !p.p ? missing : (c.has(e) ? param_at(p, group, c.col(e)) + offset : 0.0f);
+        v[e] = !p.p ? missing : (c.has(e) ? param_at(p, group, c.first + e) + offset : 0.0f);
 }
 
-// Element offset of row r of a tensor.
-__device__ __forceinline__ long long row_offset(const RowPtr &p, int b, int t)
+// Row r of a tensor.
+template <typename T>
+__device__ __forceinline__ const T *row_of(const RowPtr &p, int tokens, int r)
 {
-    return b * p.sb + t * p.st;
+    const int b = r / tokens, t = r - b * tokens;
+    return static_cast<const T *>(p.p) + (b * p.sb + t * p.st);
 }
 
-// Sums over a team.  All teams of a block call together.
+// Sums of N values over a team.  All threads of a block call together.
 struct TeamSum {
-    float2 (*slots)[16];         // [2][16]: one per warp
-    float2 (*cluster_slots)[4];  // [2][4]: one per block of the cluster
+    float (*slots)[2][16];         // [2][N][warp]
+    float (*cluster_slots)[2][4];  // [2][N][block of the cluster]
     int parity, tpr, warps, cluster;
 
-    __device__ __forceinline__ float2 operator()(float2 v)
+    template <int N>
+    __device__ __forceinline__ void operator()(float (&v)[N])
     {
         if (tpr < 32) {
-            for (int o = tpr >> 1; o > 0; o >>= 1) {
-                v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-                v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-            }
-            return v;
+            for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            return;
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-        }
-        if (warps == 1) return v;
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        if (warps == 1) return;
         // one barrier a sum: the slots alternate, and a thread that writes a
         // slot again has passed the barrier of the sum in between, which every
         // thread reaches only after it has read this one
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        if (lane == 0) slots[parity][warp] = v;
-        __syncthreads();
-        v = (lane & 15) < warps ? slots[parity][lane & 15] : make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-        }
+        for (int k = 0; k < N; ++k)
+            if (lane == k) slots[parity][k][warp] = v[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            v[k] = (lane & 15) < warps ? slots[parity][k][lane & 15] : 0.0f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
         if (cluster > 1) {
             namespace cg = cooperative_groups;
             cg::cluster_group cl = cg::this_cluster();
-            if (int(threadIdx.x) < cluster)
-                cl.map_shared_rank(&cluster_slots[parity][0], threadIdx.x)[cl.block_rank()] = v;
+            if (int(threadIdx.x) < cluster) {
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    cl.map_shared_rank(&cluster_slots[parity][k][0], threadIdx.x)[cl.block_rank()] = v[k];
+            }
             cl.sync();
-            v = make_float2(0.0f, 0.0f);
-            for (int r = 0; r < cluster; ++r) {
-                v.x += cluster_slots[parity][r].x;
-                v.y += cluster_slots[parity][r].y;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                v[k] = 0.0f;
+                for (int r = 0; r < cluster; ++r) v[k] += cluster_slots[parity][k][r];
             }
         }
         parity ^= 1;
-        return v;
     }
 };
 
@@ -226,6 +334,36 @@ struct BlockRows {
         r1 = group * p.group_rows + int((s + 1) * p.group_rows / p.splits);
     }
 };
+
+// Launches a kernel with its ring of staged rows: as many stages as leave
+// `per_sm` blocks of the largest team (or as many threads of smaller ones) room
+// on an SM, one at least.
+template <class Kernel>
+cudaError_t launch_staged(Kernel kernel, ResidualNormArgs &a, int units, int per_sm, cudaStream_t s)
+{
+    constexpr int kSmemPerSm = 200 * 1024, kMaxStages = 4, kMaxBlockSmem = 220 * 1024;
+    const int stage = units * 16 * a.plan.threads;
+    const int blocks = per_sm * kMaxTeamThreads / a.plan.threads;
+    a.plan.stages = std::max(1, std::min(kMaxStages, kSmemPerSm / (stage * blocks)));
+    const int smem = a.plan.stages * stage;
+    // one attribute for all sizes: every launch of the kernel sets the same
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kMaxBlockSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.plan.grid);
+    cfg.blockDim = dim3(unsigned(a.plan.threads));
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(a.plan.cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.plan.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
 
 #endif
 

@@ -164,15 +164,19 @@ bool dense(const gbssim_residual_norm &d, const gbssim_rows &r)
            (d.batch < 2 || r.batch_stride == (long long)d.tokens * d.dim);
 }
 
-RowPtr row_ptr(const gbssim_rows &r) { return {r.data, r.batch_stride, r.token_stride}; }
+RowPtr row_ptr(const gbssim_residual_norm &d, const gbssim_rows &r, int dtype)
+{
+    const Extent e = rows_extent(d, r, dtype);
+    return {r.data, r.batch_stride, r.token_stride, static_cast<const char *>(e.p) + e.bytes};
+}
 ParamPtr param_ptr(const gbssim_param &p) { return {p.data, p.dtype, p.per_sample != 0, p.per_sample ? p.sample_stride : 0}; }
 
 ResidualNormArgs make_args(const gbssim_residual_norm &d)
 {
     ResidualNormArgs a{};
-    a.x = row_ptr(d.x);
-    a.y = row_ptr(d.y);
-    a.gate_rows = row_ptr(d.gate_rows);
+    a.x = row_ptr(d, d.x, d.res_dtype);
+    a.y = row_ptr(d, d.y, d.blk_dtype);
+    a.gate_rows = row_ptr(d, d.gate_rows, d.blk_dtype);
     a.gate = param_ptr(d.gate);
     a.w1 = param_ptr(d.post_weight);
     a.b1 = param_ptr(d.post_bias);
@@ -328,8 +332,8 @@ extern "C" int gbssim_residual_norm_bwd(const gbssim_residual_norm *d,
     const cudaError_t e = current_sm_count(&sm_count);
     if (e != cudaSuccess) return cuda_fail(e);
     ResidualNormArgs a = make_args(*d);
-    a.gx = row_ptr(gx);
-    a.gu = row_ptr(gu);
+    a.gx = row_ptr(*d, gx, d->res_dtype);
+    a.gu = row_ptr(*d, gu, d->blk_dtype);
     a.plan = make_plan(*d, kBwdThreadsPerSm, std::min(sm_count, kMaxPlanSms));
     if (!grid_fits(a.plan)) return GBSSIM_ESHAPE;
     a.plan.aligned = inputs_aligned(*d) && rows_aligned(*d, gx, d->res_dtype) &&

@@ -44,7 +44,7 @@ __device__ __forceinline__ void write_sum(const ResidualNormArgs &a, const Cols<
             for (int e = 0; e < 8; ++e) {
                 float s = 0.0f;
                 for (int w = 0; w < kSmallBlock / 32; ++w) s += scratch[(w * 32 + lane) * 8 + e];
-                if (c.has(e)) dst[c.col(e)] = s;
+                if (c.has(e)) dst[c.first + e] = s;
             }
         }
         __syncthreads();
@@ -52,7 +52,7 @@ __device__ __forceinline__ void write_sum(const ResidualNormArgs &a, const Cols<
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        if (c.has(e)) dst[c.col(e)] = v[e];
+        if (c.has(e)) dst[c.first + e] = v[e];
 }
 
 // FULL: a gate of its own per row.  BIAS: either norm has a bias.
@@ -60,16 +60,43 @@ template <typename R, typename Y, bool ALIGNED, bool FULL, bool BIAS>
 __global__ void __launch_bounds__(kMaxTeamThreads, 1)
     residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a)
 {
-    __shared__ float2 slots[2][16];
-    __shared__ float2 cluster_slots[2][4];
+    using SR = Staged<R, ALIGNED>;
+    using SY = Staged<Y, ALIGNED>;
+    extern __shared__ uint4 ring[];
+    __shared__ float slots[2][2][16];
+    __shared__ float cluster_slots[2][2][4];
     __shared__ float scratch[kSmallBlock * 8];
     const Cols<ALIGNED> c(a);
     const BlockRows rows(a.plan);
     TeamSum sum{slots, cluster_slots, 0, a.plan.tpr, a.plan.teams > 1 ? 1 : a.plan.threads / 32,
                 a.plan.cluster};
     const int team = a.plan.teams > 1 ? int(threadIdx.x) / a.plan.tpr : 0;
+    const int threads = a.plan.threads, stages = a.plan.stages;
+    const int stage_words = (2 * SR::kUnits + (FULL ? 3 : 2) * SY::kUnits) * threads;
+    uint4 *const mine = ring + threadIdx.x;
     // no block writes into another's shared memory before that block runs
     if (a.plan.cluster > 1) cooperative_groups::this_cluster().sync();
+
+    // the words of a stage: x, G, y, V, gate
+    const int at_gx = SR::kUnits * threads, at_y = 2 * at_gx, at_gu = at_y + SY::kUnits * threads,
+              at_gate = at_gu + SY::kUnits * threads;
+    const auto fetch = [&](int r, uint4 *slot) {
+        if (r < rows.r1 && c.count > 0) {
+            SR::fetch(a.x, row_of<R>(a.x, a.tokens, r), c.first, c.count, slot, threads);
+            if (a.gx.p)
+                SR::fetch(a.gx, row_of<R>(a.gx, a.tokens, r), c.first, c.count, slot + at_gx, threads);
+            if (a.y.p)
+                SY::fetch(a.y, row_of<Y>(a.y, a.tokens, r), c.first, c.count, slot + at_y, threads);
+            if (a.gu.p)
+                SY::fetch(a.gu, row_of<Y>(a.gu, a.tokens, r), c.first, c.count, slot + at_gu, threads);
+            if (FULL)
+                SY::fetch(a.gate_rows, row_of<Y>(a.gate_rows, a.tokens, r), c.first, c.count,
+                          slot + at_gate, threads);
+        }
+        staged_commit();
+    };
+    for (int i = 0; i < stages - 1; ++i)
+        fetch(rows.r0 + i * a.plan.teams + team, mine + i * stage_words);
 
     float w1[8], b1[8], w2[8];  // with the gate of the column in w1 and b1, unless FULL
     load_param(a.w1, rows.group, c, a.offset, 1.0f, w1);
@@ -85,30 +112,26 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
         }
     }
     float sa[8] = {}, sf[8] = {}, sc[8] = {}, se[8] = {};
-
+    int now = 0;
     for (int r0 = rows.r0; r0 < rows.r1; r0 += a.plan.teams) {
         const int r = r0 + team;
         const bool active = r < rows.r1;
-        const int b = r / a.tokens, t = r - b * a.tokens;
         float4 st = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
         if (active) st = a.stats[r];
-        float yh[8], xh[8], T[8], V[8], g[8];
-        load_row(static_cast<const R *>(a.x.p) + row_offset(a.x, b, t), c, active, xh);
-        if (a.y.p)
-            load_row(static_cast<const Y *>(a.y.p) + row_offset(a.y, b, t), c, active, yh);
-        if (a.gx.p)
-            load_row(static_cast<const R *>(a.gx.p) + row_offset(a.gx, b, t), c, active, T);
-        if (a.gu.p)
-            load_row(static_cast<const Y *>(a.gu.p) + row_offset(a.gu, b, t), c, active, V);
-        if (FULL)
-            load_row(static_cast<const Y *>(a.gate_rows.p) + row_offset(a.gate_rows, b, t), c,
-                     active, g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (!a.gx.p) T[e] = 0.0f;
-            if (!a.gu.p) V[e] = 0.0f;
+        {
+            const int ahead = now == 0 ? stages - 1 : now - 1;
+            fetch(r + (stages - 1) * a.plan.teams, mine + ahead * stage_words);
         }
+        staged_wait(stages);
+        const uint4 *slot = mine + now * stage_words;
+        now = now + 1 == stages ? 0 : now + 1;
+
+        float yh[8], xh[8], T[8], V[8], g[8];
+        SR::read(row_of<R>(a.x, a.tokens, r), c, active, slot, threads, xh);
         if (a.y.p) {
+            SY::read(row_of<Y>(a.y, a.tokens, r), c, active, slot + at_y, threads, yh);
+            if (FULL)
+                SY::read(row_of<Y>(a.gate_rows, a.tokens, r), c, active, slot + at_gate, threads, g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 yh[e] = c.has(e) ? (yh[e] - st.x) * st.y : 0.0f;
@@ -117,41 +140,53 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
                 xh[e] = fmaf(a.scale, xh[e], z);
             }
         }
+        if (a.gx.p) {
+            SR::read(row_of<R>(a.gx, a.tokens, r), c, active, slot + at_gx, threads, T);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) T[e] = 0.0f;
+        }
         if (a.gu.p) {
-            float2 m = make_float2(0.0f, 0.0f);
+            SY::read(row_of<Y>(a.gu, a.tokens, r), c, active, slot + at_gu, threads, V);
+            float m[2] = {};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 xh[e] = c.has(e) ? (xh[e] - st.z) * st.w : 0.0f;
                 sc[e] = fmaf(V[e], xh[e], sc[e]);
                 if (BIAS) se[e] += V[e];
                 V[e] *= w2[e];
-                m.x += V[e];
-                m.y = fmaf(V[e], xh[e], m.y);
+                m[0] = fmaf(V[e], xh[e], m[0]);
+                m[1] += V[e];
             }
-            if (a.pre != GBSSIM_ROW_NONE) {
-                m = sum(m);
-                const float m1 = a.pre == GBSSIM_ROW_LAYER ? m.x * a.inv_dim : 0.0f;
-                const float m2 = m.y * a.inv_dim;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    T[e] = fmaf(st.w, V[e] - fmaf(xh[e], m2, m1), T[e]);
+            if (a.pre == GBSSIM_ROW_LAYER) {
+                sum(m);
+            } else if (a.pre == GBSSIM_ROW_RMS) {
+                float q[1] = {m[0]};
+                sum(q);
+                m[0] = q[0];
+                m[1] = 0.0f;
             } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) T[e] += V[e];
+                m[0] = m[1] = 0.0f;
             }
-        }
-        float dx[8];
+            const float m0 = m[0] * a.inv_dim, m1 = m[1] * a.inv_dim;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dx[e] = a.y.p ? a.scale * T[e] : T[e];
-        store_row(static_cast<R *>(a.dx) + (long long)r * a.dim, c, active && a.dx, dx);
+            for (int e = 0; e < 8; ++e) T[e] = fmaf(st.w, V[e] - fmaf(xh[e], m0, m1), T[e]);
+        }
+        if (a.dx) {
+            float dx[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dx[e] = a.y.p ? a.scale * T[e] : T[e];
+            store_row(static_cast<R *>(a.dx) + (long long)r * a.dim, c, active, dx);
+        }
         if (!a.y.p) continue;
         if (FULL && a.dgate_rows) {
+            float dg[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                dx[e] = T[e] * (BIAS ? fmaf(yh[e], w1[e], b1[e]) : yh[e] * w1[e]);
-            store_row(static_cast<Y *>(a.dgate_rows) + (long long)r * a.dim, c, active, dx);
+                dg[e] = T[e] * (BIAS ? fmaf(yh[e], w1[e], b1[e]) : yh[e] * w1[e]);
+            store_row(static_cast<Y *>(a.dgate_rows) + (long long)r * a.dim, c, active, dg);
         }
-        float2 d = make_float2(0.0f, 0.0f);
+        float d[2] = {};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (FULL) T[e] *= g[e];
@@ -159,17 +194,24 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
             sa[e] = fmaf(T[e], yh[e], sa[e]);
             if (BIAS) sf[e] += T[e];
             T[e] *= w1[e];
-            d.x += T[e];
-            d.y = fmaf(T[e], yh[e], d.y);
+            d[0] = fmaf(T[e], yh[e], d[0]);
+            d[1] += T[e];
         }
-        if (a.post != GBSSIM_ROW_NONE) {
-            d = sum(d);
-            const float d1 = a.post == GBSSIM_ROW_LAYER ? d.x * a.inv_dim : 0.0f;
-            const float d2 = d.y * a.inv_dim;
+        if (!a.dy) continue;
+        if (a.post == GBSSIM_ROW_LAYER) {
+            sum(d);
+        } else if (a.post == GBSSIM_ROW_RMS) {
+            float q[1] = {d[0]};
+            sum(q);
+            d[0] = q[0];
+            d[1] = 0.0f;
+        } else {
+            d[0] = d[1] = 0.0f;
+        }
+        const float d0 = d[0] * a.inv_dim, d1 = d[1] * a.inv_dim;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) T[e] = st.y * (T[e] - fmaf(yh[e], d2, d1));
-        }
-        store_row(static_cast<Y *>(a.dy) + (long long)r * a.dim, c, active && a.dy, T);
+        for (int e = 0; e < 8; ++e) T[e] = st.y * (T[e] - fmaf(yh[e], d0, d1));
+        store_row(static_cast<Y *>(a.dy) + (long long)r * a.dim, c, active, T);
     }
     write_sum(a, c, a.sum_a, sa, scratch);
     write_sum(a, c, a.sum_c, sc, scratch);
@@ -243,19 +285,10 @@ __global__ void __launch_bounds__(kFinishCols * kFinishLanes)
 }
 
 template <typename R, typename Y, bool ALIGNED, bool FULL, bool BIAS>
-cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
+cudaError_t launch(ResidualNormArgs a, cudaStream_t s)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.plan.grid);
-    cfg.blockDim = dim3(unsigned(a.plan.threads));
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(a.plan.cluster);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.plan.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, residual_norm_bwd_kernel<R, Y, ALIGNED, FULL, BIAS>, a);
+    const int units = 2 * Staged<R, ALIGNED>::kUnits + (FULL ? 3 : 2) * Staged<Y, ALIGNED>::kUnits;
+    return launch_staged(residual_norm_bwd_kernel<R, Y, ALIGNED, FULL, BIAS>, a, units, 1, s);
 }
 
 template <typename R, typename Y>

@@ -16,106 +16,140 @@ __device__ __forceinline__ float2 row_stats(const float (&v)[8], const Cols<ALIG
     if (kind == GBSSIM_ROW_NONE) return make_float2(0.0f, 1.0f);
     float mean = 0.0f;
     if (kind == GBSSIM_ROW_LAYER) {
-        float s = 0.0f;
+        float s[1] = {0.0f};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += c.has(e) ? v[e] : 0.0f;
-        mean = sum(make_float2(s, 0.0f)).x * a.inv_dim;
+        for (int e = 0; e < 8; ++e) s[0] += c.has(e) ? v[e] : 0.0f;
+        sum(s);
+        mean = s[0] * a.inv_dim;
     }
-    float q = 0.0f;
+    float q[1] = {0.0f};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float d = c.has(e) ? v[e] - mean : 0.0f;
-        q = fmaf(d, d, q);
+        q[0] = fmaf(d, d, q[0]);
     }
-    const float var = sum(make_float2(q, 0.0f)).x * a.inv_dim;
-    return make_float2(mean, 1.0f / sqrtf(var + a.eps));
+    sum(q);
+    return make_float2(mean, 1.0f / sqrtf(q[0] * a.inv_dim + a.eps));
 }
 
-template <typename R, typename Y, bool ALIGNED>
+// BIAS: either norm has a bias.
+template <typename R, typename Y, bool ALIGNED, bool BIAS>
 __global__ void __launch_bounds__(kMaxTeamThreads, 2)
     residual_norm_fwd_kernel(const __grid_constant__ ResidualNormArgs a)
 {
-    __shared__ float2 slots[2][16];
-    __shared__ float2 cluster_slots[2][4];
+    using SR = Staged<R, ALIGNED>;
+    using SY = Staged<Y, ALIGNED>;
+    extern __shared__ uint4 ring[];
+    __shared__ float slots[2][2][16];
+    __shared__ float cluster_slots[2][2][4];
     const Cols<ALIGNED> c(a);
     const BlockRows rows(a.plan);
     TeamSum sum{slots, cluster_slots, 0, a.plan.tpr, a.plan.teams > 1 ? 1 : a.plan.threads / 32,
                 a.plan.cluster};
     const int team = a.plan.teams > 1 ? int(threadIdx.x) / a.plan.tpr : 0;
+    const int threads = a.plan.threads, stages = a.plan.stages;
+    const int stage_words = (SR::kUnits + SY::kUnits * (a.gate_rows.p ? 2 : 1)) * threads;
+    uint4 *const mine = ring + threadIdx.x;
     // no block writes into another's shared memory before that block runs
     if (a.plan.cluster > 1) cooperative_groups::this_cluster().sync();
 
-    // post and gate of a column in one factor and one summand, except that a
-    // gate of its own per row stays apart
+    const auto fetch = [&](int r, uint4 *slot) {
+        if (r < rows.r1 && c.count > 0) {
+            SR::fetch(a.x, row_of<R>(a.x, a.tokens, r), c.first, c.count, slot, threads);
+            slot += SR::kUnits * threads;
+            if (a.y.p) SY::fetch(a.y, row_of<Y>(a.y, a.tokens, r), c.first, c.count, slot, threads);
+            slot += SY::kUnits * threads;
+            if (a.gate_rows.p)
+                SY::fetch(a.gate_rows, row_of<Y>(a.gate_rows, a.tokens, r), c.first, c.count, slot,
+                          threads);
+        }
+        staged_commit();
+    };
+    for (int i = 0; i < stages - 1; ++i)
+        fetch(rows.r0 + i * a.plan.teams + team, mine + i * stage_words);
+
+    // post and gate of a column in one factor and one summand; a gate of its
+    // own per row stays apart
     float w1[8], b1[8], w2[8], b2[8];
     load_param(a.w1, rows.group, c, a.offset, 1.0f, w1);
-    load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
     load_param(a.w2, rows.group, c, a.offset, 1.0f, w2);
-    load_param(a.b2, rows.group, c, 0.0f, 0.0f, b2);
+    if (BIAS) {
+        load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
+        load_param(a.b2, rows.group, c, 0.0f, 0.0f, b2);
+    }
     if (a.gate.p) {
         float g[8];
         load_param(a.gate, rows.group, c, 0.0f, 1.0f, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             w1[e] *= g[e];
-            b1[e] *= g[e];
+            if (BIAS) b1[e] *= g[e];
         }
     }
+    int now = 0;
     // every team of the block takes part in every sum, with a row or without
     for (int r0 = rows.r0; r0 < rows.r1; r0 += a.plan.teams) {
         const int r = r0 + team;
         const bool active = r < rows.r1;
-        const int b = r / a.tokens, t = r - b * a.tokens;
-        float x[8], y[8];
-        load_row(static_cast<const R *>(a.x.p) + row_offset(a.x, b, t), c, active, x);
+        {
+            const int ahead = now == 0 ? stages - 1 : now - 1;
+            fetch(r + (stages - 1) * a.plan.teams, mine + ahead * stage_words);
+        }
+        staged_wait(stages);
+        const uint4 *slot = mine + now * stage_words;
+        now = now + 1 == stages ? 0 : now + 1;
+        float x[8];
+        SR::read(row_of<R>(a.x, a.tokens, r), c, active, slot, threads, x);
+        slot += SR::kUnits * threads;
         float2 s1 = make_float2(0.0f, 1.0f);
         if (a.y.p) {
-            load_row(static_cast<const Y *>(a.y.p) + row_offset(a.y, b, t), c, active, y);
+            float y[8];
+            SY::read(row_of<Y>(a.y, a.tokens, r), c, active, slot, threads, y);
             s1 = row_stats(y, c, a.post, a, sum);
-            float g[8];
-            if (a.gate_rows.p)
-                load_row(static_cast<const Y *>(a.gate_rows.p) + row_offset(a.gate_rows, b, t), c,
-                         active, g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float z = fmaf((y[e] - s1.x) * s1.y, w1[e], b1[e]);
-                if (a.gate_rows.p) z *= g[e];
-                x[e] = fmaf(a.scale, x[e], z);
+                const float h = (y[e] - s1.x) * s1.y;
+                y[e] = BIAS ? fmaf(h, w1[e], b1[e]) : h * w1[e];
             }
+            if (a.gate_rows.p) {
+                float g[8];
+                SY::read(row_of<Y>(a.gate_rows, a.tokens, r), c, active, slot + SY::kUnits * threads,
+                         threads, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] *= g[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = fmaf(a.scale, x[e], y[e]);
             store_row(static_cast<R *>(a.x_out) + (long long)r * a.dim, c, active, x);
         }
         float2 s2 = make_float2(0.0f, 1.0f);
         if (a.u) {
             s2 = row_stats(x, c, a.pre, a, sum);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = fmaf((x[e] - s2.x) * s2.y, w2[e], b2[e]);
+            for (int e = 0; e < 8; ++e) {
+                const float h = (x[e] - s2.x) * s2.y;
+                x[e] = BIAS ? fmaf(h, w2[e], b2[e]) : h * w2[e];
+            }
             store_row(static_cast<Y *>(a.u) + (long long)r * a.dim, c, active, x);
         }
-        if (a.stats && active && c.t == 0 && c.first == 0)
-            a.stats[r] = make_float4(s1.x, s1.y, s2.x, s2.y);
+        if (a.stats && active && c.first == 0) a.stats[r] = make_float4(s1.x, s1.y, s2.x, s2.y);
     }
 }
 
-template <typename R, typename Y, bool ALIGNED>
-cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
+template <typename R, typename Y, bool ALIGNED, bool BIAS>
+cudaError_t launch(ResidualNormArgs a, cudaStream_t s)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.plan.grid);
-    cfg.blockDim = dim3(unsigned(a.plan.threads));
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(a.plan.cluster);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.plan.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, residual_norm_fwd_kernel<R, Y, ALIGNED>, a);
+    const int units = Staged<R, ALIGNED>::kUnits +
+                      Staged<Y, ALIGNED>::kUnits * (a.gate_rows.p ? 2 : 1);
+    return launch_staged(residual_norm_fwd_kernel<R, Y, ALIGNED, BIAS>, a, units, 2, s);
 }
 
 template <typename R, typename Y>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    return a.plan.aligned ? launch<R, Y, true>(a, s) : launch<R, Y, false>(a, s);
+    const bool bias = a.b1.p || a.b2.p;
+    if (a.plan.aligned) return bias ? launch<R, Y, true, true>(a, s) : launch<R, Y, true, false>(a, s);
+    return bias ? launch<R, Y, false, true>(a, s) : launch<R, Y, false, false>(a, s);
 }
 
 }  // namespace
