@@ -38,25 +38,30 @@ struct ParamPtr {
     long long stride;  // elements between samples; 0: one for all
 };
 
-// How rows and columns fall onto blocks.  Blocks (or clusters) take groups one
-// after another, `splits` of them to a group of group_rows consecutive rows: a
-// group is the rows that share the per-sample parameters, or all rows.
+// How rows and columns fall onto blocks.  A group is group_rows consecutive rows:
+// those that share the per-sample parameters, or all rows.  Dense rows of D
+// columns start D mod 8 elements further past a 16-byte boundary (of eight
+// elements) from one to the next; a block takes only rows of one such class
+// (row number mod `classes`), whose columns its threads cut alike, so that eight
+// columns of a thread are whole aligned words in every row.  `splits` blocks (or
+// clusters) share a class of a group.
 struct RowPlan {
-    int aligned;       // every thread's columns lie on 16-byte boundaries in every row
+    int aligned;       // rows start on 16-byte boundaries in every tensor
+    int classes;       // 8 / gcd(8, D); 1 also where a group has too few rows to part
     int stages;        // rows of each thread in flight
     int cluster;       // blocks of a cluster (1, 2, 4)
-    int block_cols;    // columns of a block: a multiple of 8
+    int block_cols;    // columns of a block: a multiple of 8 (counted from the shift)
     int tpr;           // threads of a team in a block
     int teams;         // teams of a block
     int groups, group_rows, splits;
     int threads;
-    unsigned grid;     // groups * splits * cluster
+    unsigned grid;     // groups * classes * splits * cluster
 };
 
 struct ResidualNormArgs {
     RowPtr x, y, gate_rows;
     ParamPtr gate, w1, b1, w2, b2;
-    int tokens, dim;
+    int tokens, dim;   // tokens: 0 where one stride reaches every row of every tensor
     int post, pre;     // gbssim_row_norm
     float scale, offset, eps, inv_dim;
     RowPlan plan;
@@ -66,7 +71,7 @@ struct ResidualNormArgs {
     // backward
     RowPtr gx, gu;
     void *dx, *dy, *dgate_rows;
-    float *partials;   // [groups * splits][sums][dim]
+    float *partials;   // [groups * classes * splits][sums][dim]
     int sum_a, sum_f, sum_c, sum_e, sums;  // places of the column sums, -1: not wanted
 };
 
@@ -85,87 +90,124 @@ cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk
 
 #ifdef __CUDACC__
 
-// The eight neighbouring columns of this thread.
+// The rows of this block (or cluster): first + i * step, i < count, of one class
+// of group `group`.
+struct BlockRows {
+    int group, first, count, step;
+    int shift;  // columns that the class's rows start past a multiple of eight elements
+    __device__ __forceinline__ BlockRows(const ResidualNormArgs &a)
+    {
+        const RowPlan &p = a.plan;
+        const int item = int(blockIdx.x) / p.cluster;
+        const int cls = item / p.splits, split = item - cls * p.splits;
+        group = cls / p.classes;
+        const int k = cls - group * p.classes;
+        const int begin = group * p.group_rows;
+        const int skip = (k - begin) & (p.classes - 1);
+        const long long n = skip < p.group_rows ? (p.group_rows - skip + p.classes - 1) / p.classes : 0;
+        const int i0 = int(split * n / p.splits);
+        count = int((split + 1) * n / p.splits) - i0;
+        step = p.classes;
+        first = begin + skip + i0 * step;
+        shift = p.classes > 1 ? (k * (a.dim & 7)) & 7 : 0;
+    }
+};
+
+// The eight neighbouring columns of this thread; first may be negative, and the
+// row has those from `from` up to `upto`.  ALIGNED: all eight or none.
 template <bool ALIGNED>
 struct Cols {
-    int first;  // of the thread
-    int count;  // how many of the eight the row has; all or none where ALIGNED
-    int t;      // place in the team
-    bool last;  // the thread whose right neighbour has no column of the row
-    __device__ __forceinline__ Cols(const ResidualNormArgs &a)
+    int first, from, upto;
+    int t;  // place in the team
+    __device__ __forceinline__ Cols(const ResidualNormArgs &a, int shift)
     {
         const int rank = a.plan.cluster > 1 ? int(blockIdx.x) % a.plan.cluster : 0;
         t = a.plan.teams > 1 ? threadIdx.x & (a.plan.tpr - 1) : threadIdx.x;
-        first = rank * a.plan.block_cols + t * kColsPerThread;
-        const int end = min(a.dim, (rank + 1) * a.plan.block_cols);
-        count = max(0, min(kColsPerThread, end - first));
-        last = count > 0 && first + kColsPerThread >= end;
+        first = rank * a.plan.block_cols + t * kColsPerThread - (ALIGNED ? 0 : shift);
+        from = max(0, -first);
+        upto = t * kColsPerThread < a.plan.block_cols ? max(0, min(kColsPerThread, a.dim - first)) : 0;
     }
-    __device__ __forceinline__ bool has(int e) const { return ALIGNED ? count > 0 : e < count; }
+    __device__ __forceinline__ bool any() const { return from < upto; }
+    __device__ __forceinline__ bool all() const { return ALIGNED ? upto > 0 : upto - from == 8; }
+    __device__ __forceinline__ bool has(int e) const
+    {
+        return ALIGNED ? upto > 0 : e >= from && e < upto;
+    }
 };
 
 // Rows on their way through shared memory: every thread copies its own columns
 // of a row some rows ahead (cp.async) and reads them back itself, so the copies
 // need no barrier.  A stage holds, per tensor, 16-byte words [word][thread].
 //
-// Where rows do not start on 16-byte boundaries a thread copies the aligned
-// words that its columns lie in -- one more than they fill -- and shifts.  A word
-// that reaches over the tensor's first or last element is put together from
-// single elements.
+// Where a tensor's rows are not aligned as the block's columns are, a thread
+// copies the aligned words that its columns lie in -- one more than they fill --
+// and shifts.  A word that reaches over the tensor's first or last element is
+// put together from single elements.
 template <typename T, bool ALIGNED>
 struct Staged {
     static constexpr int kUnits = (sizeof(T) == 4 ? 2 : 1) + (ALIGNED ? 0 : 1);
 
-    // Of a row whose first column is at `row`; slot: the thread's first word.
-    static __device__ __forceinline__ void fetch(const RowPtr &p, const T *row, int first,
-                                                 int count, uint4 *slot, int threads)
+    // Of the row at `row`; slot: the thread's first word.
+    static __device__ __forceinline__ void fetch(const RowPtr &p, const T *row,
+                                                 const Cols<ALIGNED> &c, uint4 *slot, int threads)
     {
-        const unsigned char *at = reinterpret_cast<const unsigned char *>(row + first);
+        const unsigned char *at = reinterpret_cast<const unsigned char *>(row + c.first);
         if constexpr (ALIGNED) {
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) copy16_async(slot + u * threads, at + u * 16, false);
         } else {
-            const unsigned char *stop = at + count * sizeof(T);
+            const unsigned char *from = at + c.from * int(sizeof(T));
+            const unsigned char *stop = at + c.upto * int(sizeof(T));
             const unsigned char *word = at - (reinterpret_cast<uintptr_t>(at) & 15);
 #pragma unroll
             for (int u = 0; u < kUnits; ++u, word += 16) {
-                if (word >= stop) continue;
+                if (word >= stop || word + 16 <= from) continue;
                 if (word >= p.p && word + 16 <= p.end) {
                     copy16_async(slot + u * threads, word, true);
                 } else {
-                    const T *from = reinterpret_cast<const T *>(word);
+                    const T *e = reinterpret_cast<const T *>(word);
                     T *to = reinterpret_cast<T *>(slot + u * threads);
+#pragma unroll 1
                     for (int i = 0; i < int(16 / sizeof(T)); ++i)
-                        if (reinterpret_cast<const unsigned char *>(from + i) >= at &&
-                            reinterpret_cast<const unsigned char *>(from + i) < stop)
-                            to[i] = from[i];
+                        if (reinterpret_cast<const unsigned char *>(e + i) >= from &&
+                            reinterpret_cast<const unsigned char *>(e + i) < stop)
+                            to[i] = e[i];
                 }
             }
         }
     }
 
+    // The thread's columns, zero where the row has none.
     static __device__ __forceinline__ void read(const T *row, const Cols<ALIGNED> &c, bool active,
                                                 const uint4 *slot, int threads, float (&v)[8])
     {
-        if (!active || c.count == 0) {
+        if (!active || !c.any()) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = 0.0f;
             return;
         }
+        Raw8<T> r;
         if constexpr (ALIGNED) {
-            Raw8<T> r;
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) r.w[u] = slot[u * threads];
             unpack8<T>(r, v);
         } else {
-            Wide8<T> w;
-#pragma unroll
-            for (int u = 0; u < kUnits; ++u)
-                reinterpret_cast<uint4 *>(w.w)[u] = slot[u * threads];
             const int s = int(reinterpret_cast<uintptr_t>(row + c.first) & 15) / int(sizeof(T));
-            unpack8<T>(shift_down<T>(w, s), v);
+            if (s == 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = c.has(e) ? v[e] : 0.0f;
+                for (int u = 0; u < kUnits - 1; ++u) r.w[u] = slot[u * threads];
+            } else {
+                Wide8<T> w;
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u)
+                    reinterpret_cast<uint4 *>(w.w)[u] = slot[u * threads];
+                r = shift_down<T>(w, s);
+            }
+            unpack8<T>(r, v);
+            if (!c.all()) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = c.has(e) ? v[e] : 0.0f;
+            }
         }
     }
 };
@@ -184,54 +226,24 @@ __device__ __forceinline__ void staged_wait(int stages)
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Stores the thread's columns of a row.  Where the row does not start on a
-// 16-byte boundary, a thread takes the last `s` elements of its left neighbour
-// (by shuffle) in front of its own first 8 - s and stores those as whole words;
-// the first lane of a run stores its own first elements, the last its own last
-// ones, one by one.  All lanes of a warp call together.
+// Stores the thread's columns of a row: in whole words where it has all eight
+// and they are aligned, one by one at a row's ends.
 template <typename T, bool ALIGNED>
 __device__ __forceinline__ void store_row(T *row, const Cols<ALIGNED> &c, bool active,
                                           const float (&v)[8])
 {
     T *at = row + c.first;
     if constexpr (ALIGNED) {
-        if (active && c.count > 0) st8(at, pack8<T>(v));
+        if (active && c.any()) st8(at, pack8<T>(v));
     } else {
-        const Raw8<T> own = pack8<T>(v);
-        const uint32_t *ow = reinterpret_cast<const uint32_t *>(&own);
-        constexpr int W = 2 * sizeof(T);                 // words of eight elements
-        constexpr int P = sizeof(T) == 4 ? 4 : 4;        // words of the neighbour that may be needed
-        constexpr int G = 16 / int(sizeof(T));           // elements of a 16-byte word
-        Wide8<T> both;                                   // neighbour's last word, then own
+        if (!active) return;
+        if (c.all() && (reinterpret_cast<uintptr_t>(at) & 15) == 0) {
+            st8(at, pack8<T>(v));
+        } else {
 #pragma unroll
-        for (int i = 0; i < P; ++i) both.w[i] = __shfl_up_sync(0xffffffffu, ow[W - P + i], 1);
-#pragma unroll
-        for (int i = 0; i < W; ++i) both.w[P + i] = ow[i];
-        if (!active || c.count == 0) return;
-        const int s = int(reinterpret_cast<uintptr_t>(at) & 15) / int(sizeof(T));
-        const bool head = c.t == 0 || (threadIdx.x & 31) == 0;
-        const bool tail = c.last || (threadIdx.x & 31) == 31;
-        if (s == 0 ? c.count == 8 : (!head && c.count >= 8 - s)) {
-            // elements [-s, 8 - s): from element G - s of `both`; s = 0 is own, unshifted
-            st8(at - s, s == 0 ? own : shift_down<T>(both, G - s));
-            if (s == 0 || !tail) return;
-#pragma unroll
-            for (int e = 1; e < 8; ++e)
-                if (e >= 8 - s && e < c.count) at[e] = from_f32<T>(v[e]);
-            return;
+            for (int e = 0; e < 8; ++e)
+                if (c.has(e)) at[e] = from_f32<T>(v[e]);
         }
-        // the left neighbour's last elements, unless the neighbour stores them itself
-        if (s > 0 && !head) {
-            const T *left = reinterpret_cast<const T *>(both.w);
-#pragma unroll
-            for (int i = 1; i < G; ++i)
-                if (i >= G - s) at[i - G] = left[i];
-        }
-        // own elements: the right neighbour stores those from 8 - s on, unless this is a run's end
-        const int stop = s == 0 || tail ? c.count : min(c.count, 8 - s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < stop) at[e] = from_f32<T>(v[e]);
     }
 }
 
@@ -264,8 +276,10 @@ __device__ __forceinline__ void load_param(const ParamPtr &p, int group, const C
 template <typename T>
 __device__ __forceinline__ const T *row_of(const RowPtr &p, int tokens, int r)
 {
+    const T *base = static_cast<const T *>(p.p);
+    if (tokens == 0) return base + r * p.st;
     const int b = r / tokens, t = r - b * tokens;
-    return static_cast<const T *>(p.p) + (b * p.sb + t * p.st);
+    return base + (b * p.sb + t * p.st);
 }
 
 // Sums of N values over a team.  All threads of a block call together.
@@ -319,19 +333,6 @@ struct TeamSum {
             }
         }
         parity ^= 1;
-    }
-};
-
-// The rows of this block (or cluster): of group `group`, rows [r0, r1).
-struct BlockRows {
-    int group, r0, r1;
-    __device__ __forceinline__ BlockRows(const RowPlan &p)
-    {
-        const int item = int(blockIdx.x) / p.cluster;
-        group = item / p.splits;
-        const long long s = item - group * p.splits;
-        r0 = group * p.group_rows + int(s * p.group_rows / p.splits);
-        r1 = group * p.group_rows + int((s + 1) * p.group_rows / p.splits);
     }
 };
 

@@ -74,7 +74,7 @@ int check_desc(const gbssim_residual_norm *d)
         if (kind < GBSSIM_ROW_NONE || kind > GBSSIM_ROW_LAYER) return GBSSIM_EINVAL;
     if (!(d->eps >= 0.0f)) return GBSSIM_EINVAL;
     if (d->batch < 0 || d->tokens < 0 || d->dim < 1 || d->dim > kMaxDim) return GBSSIM_ESHAPE;
-    if (row_count(*d) > INT_MAX - kSmallBlock) return GBSSIM_ESHAPE;
+    if (row_count(*d) > INT_MAX - 4096) return GBSSIM_ESHAPE;
     const bool some = row_count(*d) > 0;
     if (some && !d->x.data) return GBSSIM_EINVAL;
     // without a block's output there is nothing to normalise or gate
@@ -125,7 +125,18 @@ constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512;
 RowPlan make_plan(const gbssim_residual_norm &d, int threads_per_sm, int sm_count)
 {
     RowPlan p{};
-    const int chunks = (d.dim + kColsPerThread - 1) / kColsPerThread;
+    bool own = false;
+    for (const gbssim_param *q : {&d.gate, &d.post_weight, &d.post_bias, &d.pre_weight, &d.pre_bias})
+        own = own || (q->data && q->per_sample);
+    const long long rows = row_count(d);
+    p.groups = own ? d.batch : 1;
+    p.group_rows = own ? d.tokens : int(rows);
+    // Parting rows into classes costs a set of partial sums per class: not where
+    // a class would have only a few rows.  The widest rows fill a cluster's threads
+    // without a shift.
+    p.classes = d.dim % 8 == 0 ? 1 : d.dim % 4 == 0 ? 2 : d.dim % 2 == 0 ? 4 : 8;
+    if (p.group_rows < 8 * p.classes || d.dim + 7 > kMaxDim) p.classes = 1;
+    const int chunks = (d.dim + (p.classes > 1 ? 7 : 0) + kColsPerThread - 1) / kColsPerThread;
     p.cluster = chunks <= kMaxTeamThreads ? 1 : chunks <= 2 * kMaxTeamThreads ? 2 : 4;
     const int per = (chunks + p.cluster - 1) / p.cluster;
     p.block_cols = per * kColsPerThread;
@@ -138,17 +149,13 @@ RowPlan make_plan(const gbssim_residual_norm &d, int threads_per_sm, int sm_coun
         p.tpr = p.threads = (per + 31) / 32 * 32;
         p.teams = 1;
     }
-    bool own = false;
-    for (const gbssim_param *q : {&d.gate, &d.post_weight, &d.post_bias, &d.pre_weight, &d.pre_bias})
-        own = own || (q->data && q->per_sample);
-    const long long rows = row_count(d);
-    p.groups = own ? d.batch : 1;
-    p.group_rows = own ? d.tokens : int(rows);
     if (rows == 0) return p;
     const long long blocks = (long long)sm_count * (threads_per_sm / p.threads) / p.cluster;
+    const long long items = (long long)p.groups * p.classes;
     p.splits = int(std::max<long long>(
-        1, std::min<long long>(ceil_div(blocks, p.groups), ceil_div(p.group_rows, p.teams))));
-    p.grid = unsigned(p.groups) * unsigned(p.splits) * unsigned(p.cluster);
+        1, std::min<long long>(ceil_div(blocks, items),
+                               ceil_div(ceil_div(p.group_rows, p.classes), p.teams))));
+    p.grid = unsigned(items) * unsigned(p.splits) * unsigned(p.cluster);
     return p;
 }
 
@@ -194,7 +201,7 @@ ResidualNormArgs make_args(const gbssim_residual_norm &d)
 
 bool grid_fits(const RowPlan &p)
 {
-    return (long long)p.groups * p.splits * p.cluster <= INT_MAX;
+    return (long long)p.groups * p.classes * p.splits * p.cluster <= INT_MAX;
 }
 
 // Which column sums the backward has to keep: A and F for the gate and the post
@@ -252,7 +259,7 @@ extern "C" int gbssim_residual_norm_fwd(const gbssim_residual_norm *d, void *x_o
     if (!grid_fits(a.plan)) return GBSSIM_ESHAPE;
     a.plan.aligned = inputs_aligned(*d) && multiple16(x_out_or_null) && multiple16(u_or_null);
     a.tokens = one_stride(*d, d->x) && one_stride(*d, d->y) && one_stride(*d, d->gate_rows)
-                   ? INT_MAX
+                   ? 0
                    : d->tokens;
     a.x_out = x_out_or_null;
     a.u = u_or_null;
@@ -265,7 +272,7 @@ extern "C" size_t gbssim_residual_norm_workspace_bytes(const gbssim_residual_nor
 {
     if (check_desc(d) != GBSSIM_OK || row_count(*d) == 0) return 0;
     const RowPlan p = make_plan(*d, kBwdThreadsPerSm, kMaxPlanSms);
-    return size_t(p.groups) * p.splits * kMaxSums * d->dim * sizeof(float);
+    return size_t(p.groups) * p.classes * p.splits * kMaxSums * d->dim * sizeof(float);
 }
 
 extern "C" int gbssim_residual_norm_bwd(const gbssim_residual_norm *d,
@@ -341,7 +348,7 @@ extern "C" int gbssim_residual_norm_bwd(const gbssim_residual_norm *d,
                      multiple16(grads->y) && (!d->gate_rows.data || multiple16(grads->gate));
     a.tokens = one_stride(*d, d->x) && one_stride(*d, d->y) && one_stride(*d, d->gate_rows) &&
                        one_stride(*d, gx) && one_stride(*d, gu)
-                   ? INT_MAX
+                   ? 0
                    : d->tokens;
     a.stats = const_cast<float4 *>(reinterpret_cast<const float4 *>(stats));
     a.dx = grads->x;

@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
     __shared__ float slots[2][2][16];
     __shared__ float cluster_slots[2][2][4];
     __shared__ float scratch[kSmallBlock * 8];
-    const Cols<ALIGNED> c(a);
-    const BlockRows rows(a.plan);
+    const BlockRows rows(a);
+    const Cols<ALIGNED> c(a, rows.shift);
     TeamSum sum{slots, cluster_slots, 0, a.plan.tpr, a.plan.teams > 1 ? 1 : a.plan.threads / 32,
                 a.plan.cluster};
     const int team = a.plan.teams > 1 ? int(threadIdx.x) / a.plan.tpr : 0;
@@ -80,23 +80,20 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
     // the words of a stage: x, G, y, V, gate
     const int at_gx = SR::kUnits * threads, at_y = 2 * at_gx, at_gu = at_y + SY::kUnits * threads,
               at_gate = at_gu + SY::kUnits * threads;
-    const auto fetch = [&](int r, uint4 *slot) {
-        if (r < rows.r1 && c.count > 0) {
-            SR::fetch(a.x, row_of<R>(a.x, a.tokens, r), c.first, c.count, slot, threads);
-            if (a.gx.p)
-                SR::fetch(a.gx, row_of<R>(a.gx, a.tokens, r), c.first, c.count, slot + at_gx, threads);
-            if (a.y.p)
-                SY::fetch(a.y, row_of<Y>(a.y, a.tokens, r), c.first, c.count, slot + at_y, threads);
-            if (a.gu.p)
-                SY::fetch(a.gu, row_of<Y>(a.gu, a.tokens, r), c.first, c.count, slot + at_gu, threads);
+    const auto fetch = [&](int i, uint4 *slot) {
+        if (i < rows.count && c.any()) {
+            const int r = rows.first + i * rows.step;
+            SR::fetch(a.x, row_of<R>(a.x, a.tokens, r), c, slot, threads);
+            if (a.gx.p) SR::fetch(a.gx, row_of<R>(a.gx, a.tokens, r), c, slot + at_gx, threads);
+            if (a.y.p) SY::fetch(a.y, row_of<Y>(a.y, a.tokens, r), c, slot + at_y, threads);
+            if (a.gu.p) SY::fetch(a.gu, row_of<Y>(a.gu, a.tokens, r), c, slot + at_gu, threads);
             if (FULL)
-                SY::fetch(a.gate_rows, row_of<Y>(a.gate_rows, a.tokens, r), c.first, c.count,
-                          slot + at_gate, threads);
+                SY::fetch(a.gate_rows, row_of<Y>(a.gate_rows, a.tokens, r), c, slot + at_gate,
+                          threads);
         }
         staged_commit();
     };
-    for (int i = 0; i < stages - 1; ++i)
-        fetch(rows.r0 + i * a.plan.teams + team, mine + i * stage_words);
+    for (int i = 0; i < stages - 1; ++i) fetch(i * a.plan.teams + team, mine + i * stage_words);
 
     float w1[8], b1[8], w2[8];  // with the gate of the column in w1 and b1, unless FULL
     load_param(a.w1, rows.group, c, a.offset, 1.0f, w1);
@@ -111,16 +108,19 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
             if (BIAS) b1[e] *= g[e];
         }
     }
+    // Columns that a row does not have hold zeros of x, y, G, V and of w1 and b1:
+    // whatever a mean makes of y^, x^ and T there meets a zero factor before it
+    // enters a sum over the row, and their own sums are not stored.
     float sa[8] = {}, sf[8] = {}, sc[8] = {}, se[8] = {};
     int now = 0;
-    for (int r0 = rows.r0; r0 < rows.r1; r0 += a.plan.teams) {
-        const int r = r0 + team;
-        const bool active = r < rows.r1;
+    for (int i0 = 0; i0 < rows.count; i0 += a.plan.teams) {
+        const int i = i0 + team, r = rows.first + i * rows.step;
+        const bool active = i < rows.count;
         float4 st = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
         if (active) st = a.stats[r];
         {
             const int ahead = now == 0 ? stages - 1 : now - 1;
-            fetch(r + (stages - 1) * a.plan.teams, mine + ahead * stage_words);
+            fetch(i + (stages - 1) * a.plan.teams, mine + ahead * stage_words);
         }
         staged_wait(stages);
         const uint4 *slot = mine + now * stage_words;
@@ -132,9 +132,10 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
             SY::read(row_of<Y>(a.y, a.tokens, r), c, active, slot + at_y, threads, yh);
             if (FULL)
                 SY::read(row_of<Y>(a.gate_rows, a.tokens, r), c, active, slot + at_gate, threads, g);
+            const float m1 = -st.x * st.y;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                yh[e] = c.has(e) ? (yh[e] - st.x) * st.y : 0.0f;
+                yh[e] = fmaf(yh[e], st.y, m1);
                 float z = BIAS ? fmaf(yh[e], w1[e], b1[e]) : yh[e] * w1[e];
                 if (FULL) z *= g[e];
                 xh[e] = fmaf(a.scale, xh[e], z);
@@ -149,33 +150,36 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
         if (a.gu.p) {
             SY::read(row_of<Y>(a.gu, a.tokens, r), c, active, slot + at_gu, threads, V);
             float m[2] = {};
+            const float m2 = -st.z * st.w;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                xh[e] = c.has(e) ? (xh[e] - st.z) * st.w : 0.0f;
+                xh[e] = fmaf(xh[e], st.w, m2);
                 sc[e] = fmaf(V[e], xh[e], sc[e]);
                 if (BIAS) se[e] += V[e];
                 V[e] *= w2[e];
                 m[0] = fmaf(V[e], xh[e], m[0]);
-                m[1] += V[e];
             }
             if (a.pre == GBSSIM_ROW_LAYER) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m[1] += V[e];
                 sum(m);
             } else if (a.pre == GBSSIM_ROW_RMS) {
                 float q[1] = {m[0]};
                 sum(q);
                 m[0] = q[0];
-                m[1] = 0.0f;
             } else {
-                m[0] = m[1] = 0.0f;
+                m[0] = 0.0f;
             }
-            const float m0 = m[0] * a.inv_dim, m1 = m[1] * a.inv_dim;
+            // T += r2 (dx^ - m1 - x^ m0)
+            const float m0 = -m[0] * a.inv_dim, m1 = -m[1] * a.inv_dim;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) T[e] = fmaf(st.w, V[e] - fmaf(xh[e], m0, m1), T[e]);
+            for (int e = 0; e < 8; ++e) T[e] = fmaf(st.w, fmaf(xh[e], m0, V[e] + m1), T[e]);
         }
         if (a.dx) {
+            const float s = a.y.p ? a.scale : 1.0f;
             float dx[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dx[e] = a.y.p ? a.scale * T[e] : T[e];
+            for (int e = 0; e < 8; ++e) dx[e] = s * T[e];
             store_row(static_cast<R *>(a.dx) + (long long)r * a.dim, c, active, dx);
         }
         if (!a.y.p) continue;
@@ -190,27 +194,26 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (FULL) T[e] *= g[e];
-            if (!active || !c.has(e)) T[e] = 0.0f;
             sa[e] = fmaf(T[e], yh[e], sa[e]);
             if (BIAS) sf[e] += T[e];
             T[e] *= w1[e];
             d[0] = fmaf(T[e], yh[e], d[0]);
-            d[1] += T[e];
         }
         if (!a.dy) continue;
         if (a.post == GBSSIM_ROW_LAYER) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[1] += T[e];
             sum(d);
         } else if (a.post == GBSSIM_ROW_RMS) {
             float q[1] = {d[0]};
             sum(q);
             d[0] = q[0];
-            d[1] = 0.0f;
         } else {
-            d[0] = d[1] = 0.0f;
+            d[0] = 0.0f;
         }
-        const float d0 = d[0] * a.inv_dim, d1 = d[1] * a.inv_dim;
+        const float d0 = -d[0] * a.inv_dim, d1 = -d[1] * a.inv_dim;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) T[e] = st.y * (T[e] - fmaf(yh[e], d0, d1));
+        for (int e = 0; e < 8; ++e) T[e] = st.y * fmaf(yh[e], d0, T[e] + d1);
         store_row(static_cast<Y *>(a.dy) + (long long)r * a.dim, c, active, T);
     }
     write_sum(a, c, a.sum_a, sa, scratch);
@@ -246,15 +249,16 @@ __global__ void __launch_bounds__(kFinishCols * kFinishLanes)
     const int cx = threadIdx.x & 31, lane = threadIdx.x >> 5;
     const int col = int(blockIdx.x) * kFinishCols + cx;
     const bool shared = int(blockIdx.y) == shared_block;
-    const int p0 = shared ? 0 : int(blockIdx.y) * a.plan.splits;
-    const int p1 = shared ? a.plan.groups * a.plan.splits : p0 + a.plan.splits;
+    const int each = a.plan.classes * a.plan.splits;  // partials of a group
+    const int p0 = shared ? 0 : int(blockIdx.y) * each;
+    const int p1 = shared ? a.plan.groups * each : p0 + each;
     const bool full = a.gate_rows.p != nullptr;
     // dg, dw1, db1, dw2, db2
     float v[5] = {};
     if (col < a.dim) {
         for (int p = p0 + lane; p < p1; p += kFinishLanes) {
             const float *src = a.partials + (long long)p * a.sums * a.dim + col;
-            const int group = p / a.plan.splits;
+            const int group = p / each;
             const float A = a.sum_a >= 0 ? src[(long long)a.sum_a * a.dim] : 0.0f;
             const float F = a.sum_f >= 0 ? src[(long long)a.sum_f * a.dim] : 0.0f;
             const float gate = a.gate.p && !full ? param_at(a.gate, group, col) : 1.0f;

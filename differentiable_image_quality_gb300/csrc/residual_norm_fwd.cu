@@ -8,28 +8,38 @@
 namespace gbssim {
 namespace {
 
-// Mean and 1 / deviation of the team's row; columns outside it must not count.
+// (mean / deviation, 1 / deviation, mean) of the team's row, so that a normalised
+// value is one fused multiply-add: v * y - x.
+struct RowStats {
+    float scaled_mean, rstd, mean;
+};
+
+// Columns that the row does not have hold zero: they add nothing to a sum of
+// squares, but must not count about a mean.
 template <bool ALIGNED>
-__device__ __forceinline__ float2 row_stats(const float (&v)[8], const Cols<ALIGNED> &c, int kind,
-                                            const ResidualNormArgs &a, TeamSum &sum)
+__device__ __forceinline__ RowStats row_stats(const float (&v)[8], const Cols<ALIGNED> &c, int kind,
+                                              const ResidualNormArgs &a, TeamSum &sum)
 {
-    if (kind == GBSSIM_ROW_NONE) return make_float2(0.0f, 1.0f);
-    float mean = 0.0f;
+    if (kind == GBSSIM_ROW_NONE) return {0.0f, 1.0f, 0.0f};
+    float q[1] = {0.0f}, mean = 0.0f;
     if (kind == GBSSIM_ROW_LAYER) {
         float s[1] = {0.0f};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] += c.has(e) ? v[e] : 0.0f;
+        for (int e = 0; e < 8; ++e) s[0] += v[e];
         sum(s);
         mean = s[0] * a.inv_dim;
-    }
-    float q[1] = {0.0f};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float d = c.has(e) ? v[e] - mean : 0.0f;
-        q[0] = fmaf(d, d, q[0]);
+        for (int e = 0; e < 8; ++e) {
+            const float d = c.has(e) ? v[e] - mean : 0.0f;
+            q[0] = fmaf(d, d, q[0]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[0] = fmaf(v[e], v[e], q[0]);
     }
     sum(q);
-    return make_float2(mean, 1.0f / sqrtf(q[0] * a.inv_dim + a.eps));
+    const float rstd = rsqrtf(fmaf(q[0], a.inv_dim, a.eps));
+    return {mean * rstd, rstd, mean};
 }
 
 // BIAS: either norm has a bias.
@@ -42,8 +52,8 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
     extern __shared__ uint4 ring[];
     __shared__ float slots[2][2][16];
     __shared__ float cluster_slots[2][2][4];
-    const Cols<ALIGNED> c(a);
-    const BlockRows rows(a.plan);
+    const BlockRows rows(a);
+    const Cols<ALIGNED> c(a, rows.shift);
     TeamSum sum{slots, cluster_slots, 0, a.plan.tpr, a.plan.teams > 1 ? 1 : a.plan.threads / 32,
                 a.plan.cluster};
     const int team = a.plan.teams > 1 ? int(threadIdx.x) / a.plan.tpr : 0;
@@ -53,20 +63,19 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
     // no block writes into another's shared memory before that block runs
     if (a.plan.cluster > 1) cooperative_groups::this_cluster().sync();
 
-    const auto fetch = [&](int r, uint4 *slot) {
-        if (r < rows.r1 && c.count > 0) {
-            SR::fetch(a.x, row_of<R>(a.x, a.tokens, r), c.first, c.count, slot, threads);
+    const auto fetch = [&](int i, uint4 *slot) {
+        if (i < rows.count && c.any()) {
+            const int r = rows.first + i * rows.step;
+            SR::fetch(a.x, row_of<R>(a.x, a.tokens, r), c, slot, threads);
             slot += SR::kUnits * threads;
-            if (a.y.p) SY::fetch(a.y, row_of<Y>(a.y, a.tokens, r), c.first, c.count, slot, threads);
+            if (a.y.p) SY::fetch(a.y, row_of<Y>(a.y, a.tokens, r), c, slot, threads);
             slot += SY::kUnits * threads;
             if (a.gate_rows.p)
-                SY::fetch(a.gate_rows, row_of<Y>(a.gate_rows, a.tokens, r), c.first, c.count, slot,
-                          threads);
+                SY::fetch(a.gate_rows, row_of<Y>(a.gate_rows, a.tokens, r), c, slot, threads);
         }
         staged_commit();
     };
-    for (int i = 0; i < stages - 1; ++i)
-        fetch(rows.r0 + i * a.plan.teams + team, mine + i * stage_words);
+    for (int i = 0; i < stages - 1; ++i) fetch(i * a.plan.teams + team, mine + i * stage_words);
 
     // post and gate of a column in one factor and one summand; a gate of its
     // own per row stays apart
@@ -88,12 +97,12 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
     }
     int now = 0;
     // every team of the block takes part in every sum, with a row or without
-    for (int r0 = rows.r0; r0 < rows.r1; r0 += a.plan.teams) {
-        const int r = r0 + team;
-        const bool active = r < rows.r1;
+    for (int i0 = 0; i0 < rows.count; i0 += a.plan.teams) {
+        const int i = i0 + team, r = rows.first + i * rows.step;
+        const bool active = i < rows.count;
         {
             const int ahead = now == 0 ? stages - 1 : now - 1;
-            fetch(r + (stages - 1) * a.plan.teams, mine + ahead * stage_words);
+            fetch(i + (stages - 1) * a.plan.teams, mine + ahead * stage_words);
         }
         staged_wait(stages);
         const uint4 *slot = mine + now * stage_words;
@@ -101,14 +110,14 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
         float x[8];
         SR::read(row_of<R>(a.x, a.tokens, r), c, active, slot, threads, x);
         slot += SR::kUnits * threads;
-        float2 s1 = make_float2(0.0f, 1.0f);
+        RowStats s1 = {0.0f, 1.0f, 0.0f}, s2 = {0.0f, 1.0f, 0.0f};
         if (a.y.p) {
             float y[8];
             SY::read(row_of<Y>(a.y, a.tokens, r), c, active, slot, threads, y);
             s1 = row_stats(y, c, a.post, a, sum);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float h = (y[e] - s1.x) * s1.y;
+                const float h = fmaf(y[e], s1.rstd, -s1.scaled_mean);
                 y[e] = BIAS ? fmaf(h, w1[e], b1[e]) : h * w1[e];
             }
             if (a.gate_rows.p) {
@@ -122,17 +131,17 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
             for (int e = 0; e < 8; ++e) x[e] = fmaf(a.scale, x[e], y[e]);
             store_row(static_cast<R *>(a.x_out) + (long long)r * a.dim, c, active, x);
         }
-        float2 s2 = make_float2(0.0f, 1.0f);
         if (a.u) {
             s2 = row_stats(x, c, a.pre, a, sum);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float h = (x[e] - s2.x) * s2.y;
+                const float h = fmaf(x[e], s2.rstd, -s2.scaled_mean);
                 x[e] = BIAS ? fmaf(h, w2[e], b2[e]) : h * w2[e];
             }
             store_row(static_cast<Y *>(a.u) + (long long)r * a.dim, c, active, x);
         }
-        if (a.stats && active && c.first == 0) a.stats[r] = make_float4(s1.x, s1.y, s2.x, s2.y);
+        if (a.stats && active && c.first <= 0 && c.any())
+            a.stats[r] = make_float4(s1.mean, s1.rstd, s2.mean, s2.rstd);
     }
 }
 

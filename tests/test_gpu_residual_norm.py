@@ -220,7 +220,9 @@ def test_norms_and_gates(pkg, post, pre, gate, bias):
 
 @pytest.mark.parametrize("shape", [(1, 1, 64), (1, 1, 4096), (1, 1, 16384), (5, 1, 128), (1, 300, 24),
                                    (3, 1000, 64), (40, 2, 512), (2, 3, 5, 4, 80), (200, 48), (33,),
-                                   (1, 2500, 1024)], ids=str)
+                                   (1, 2500, 1024), (1, 70, 4091), (2, 100, 9001), (1, 80, 16377),
+                                   (1, 80, 16383), (3, 333, 45), (1, 999, 1002), (2, 90, 260)],
+                         ids=str)
 @pytest.mark.parametrize("per_sample", [False, True])
 def test_shapes(pkg, shape, per_sample):
     if per_sample and len(shape) < 3:
@@ -238,23 +240,23 @@ def test_no_rows(pkg):
         assert all(bool((v == 0).all()) for v in grads[2:])
 
 
-@pytest.mark.parametrize("dim", [64, 520, 1001])
-def test_strides_and_alignment(pkg, dim):
+@pytest.mark.parametrize("dim,tokens", [(64, 10), (520, 10), (1001, 10), (1001, 70), (1002, 50)])
+def test_strides_and_alignment(pkg, dim, tokens):
     """Tokens cut out of longer sequences, halves of wider products, odd starts,
     chunks of a modulation, gates in another order of samples and tokens."""
-    t, g, how = make((3, 10, dim), F32, BF16, pre="layer", per_sample=True)
-    t["x"] = torch.cat([t["x"], t["x"]], 1)[:, 3:13]
+    t, g, how = make((3, tokens, dim), F32, BF16, pre="layer", per_sample=True)
+    t["x"] = torch.cat([t["x"], t["x"]], 1)[:, 3:3 + tokens]
     t["y"] = torch.cat([t["y"], t["y"]], -1)[..., dim:]
     mod = torch.randn(3, 5 * dim, device="cuda")
     for i, k in enumerate(NAMES[2:]):
         t[k] = mod[:, i * dim:(i + 1) * dim]
     check(pkg, t, g, how)
-    t["gate"] = torch.randn(10, 3, dim, device="cuda").to(BF16).transpose(0, 1)
+    t["gate"] = torch.randn(tokens, 3, dim, device="cuda").to(BF16).transpose(0, 1)
     check(pkg, t, g, how)
-    t["x"] = torch.randn(3 * 10 * dim + 1, device="cuda")[1:].view(3, 10, dim)
+    t["x"] = torch.randn(3 * tokens * dim + 1, device="cuda")[1:].view(3, tokens, dim)
     check(pkg, t, g, how)
-    g = {"x": torch.randn(dim, device="cuda").expand(3, 10, dim),
-         "u": torch.randn(3, dim, 10, device="cuda").to(BF16).transpose(1, 2)}
+    g = {"x": torch.randn(dim, device="cuda").expand(3, tokens, dim),
+         "u": torch.randn(3, dim, tokens, device="cuda").to(BF16).transpose(1, 2)}
     check(pkg, t, g, how)
 
 
@@ -373,8 +375,9 @@ def test_one_bad_row(pkg, dim, value):
     assert bool(grads[3].isnan().all())
 
 
-def test_in_place_and_streams(pkg):
-    t, g, how = make((2, 50, 1152), BF16, BF16)
+@pytest.mark.parametrize("dim", [1152, 1001, 45])
+def test_in_place_and_streams(pkg, dim):
+    t, g, how = make((2, 70, dim), BF16, BF16)
     args = {k: t[k] for k in NAMES[2:]}
     x_out, u, _ = pkg.residual_norm_fwd(t["x"], t["y"], **args, **how)
     x = t["x"].clone()
