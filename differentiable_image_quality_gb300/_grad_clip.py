@@ -31,31 +31,46 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
-def _tensors(name: str, tensors) -> list:
-    """The tensors as a list, checked: CUDA, one device, a known type, dense."""
-    ts = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
-    if not all(isinstance(t, torch.Tensor) for t in ts):
-        raise TypeError(f"{name} must be tensors")
-    if not all([t.is_cuda for t in ts]):
-        raise TypeError(f"{name} must be CUDA tensors")
-    if len(set(map(torch.Tensor.get_device, ts))) > 1:
-        raise ValueError(f"{name} must be on one device")
-    for t in ts:
-        if t.layout != torch.strided or not (t.is_contiguous() or t.numel() == 0 or _dense(t)):
-            raise ValueError(f"{name} must be dense in memory, got shape {tuple(t.shape)} "
-                             f"with layout {t.layout}")
-    return ts
+_is_contiguous, _numel, _get_device, _data_ptr = (
+    torch.Tensor.is_contiguous, torch.Tensor.numel, torch.Tensor.get_device, torch.Tensor.data_ptr)
 
 
-def _codes(name: str, ts: list) -> bytes:
-    try:
-        return bytes([_abi.DTYPES[t.dtype] for t in ts])
-    except KeyError as e:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {e.args[0]}") from None
+class _List:
+    """Tensors checked (CUDA, one device, a known type, dense) and as the arrays
+    the library takes.  Passes over the tensors are C loops: a call's own time
+    is mostly this."""
 
+    __slots__ = ("tensors", "device", "addresses", "counts", "codes", "contiguous")
 
-def _addresses(ts: list) -> array:
-    return array("Q", [t.data_ptr() for t in ts])
+    def __init__(self, name: str, tensors):
+        ts = self.tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+        if not ts:
+            raise ValueError(f"{name} is empty: a norm needs a device to be computed on")
+        try:
+            devices = set(map(_get_device, ts))
+            if -1 in devices:
+                raise TypeError(f"{name} must be CUDA tensors")
+        except TypeError:
+            raise TypeError(f"{name} must be CUDA tensors") from None
+        if len(devices) > 1:
+            raise ValueError(f"{name} must be on one device")
+        self.device = devices.pop()
+        try:
+            self.codes = bytes(map(_abi.DTYPES.__getitem__, [t.dtype for t in ts]))
+        except KeyError as e:
+            raise TypeError(f"{name} must be float32, bfloat16 or float16, got {e.args[0]}") \
+                from None
+        try:
+            self.contiguous = all(map(_is_contiguous, ts))
+        except RuntimeError:  # a layout without strides
+            self.contiguous = False
+        if not self.contiguous:
+            for t in ts:
+                if not (t.layout == torch.strided and (t.numel() == 0 or _dense(t))):
+                    raise ValueError(f"{name} must be dense in memory, got shape "
+                                     f"{tuple(t.shape)} with layout {t.layout}")
+        self.addresses = array("Q", map(_data_ptr, ts))
+        self.counts = array("q", map(_numel, ts))
 
 
 def _at(a: array) -> int:
@@ -69,25 +84,19 @@ def grad_norm(grads, norm_type=2.0) -> torch.Tensor:
     float16 may be mixed; any shapes, dense in memory).  norm_type: 2, 1 or inf.
     Nothing is copied to the host."""
     p = _norm_type(norm_type)
-    ts = _tensors("grads", grads)
-    if not ts:
-        raise ValueError("grads is empty: a norm needs a device to be computed on")
-    codes, addresses = _codes("grads", ts), _addresses(ts)
-    counts = array("q", [t.numel() for t in ts])
+    ts = _List("grads", grads)
+    n = len(ts.tensors)
     lib = _abi.load()
-    device = ts[0].device
-    with _memory.on_device(device.index):
-        out = torch.empty((), dtype=torch.float32, device=device)
-        stream = _memory.stream_of(device.index)
-        nbytes = lib.gbssim_grad_workspace_bytes(len(ts))
-        ws = _memory.zeroed_scratch(device, stream, nbytes)
-        st = lib.gbssim_grad_norm(_at(addresses), _at(counts), codes, len(ts), p, out.data_ptr(),
-                                  ws.data_ptr(), ws.numel(), stream)
+    with _memory.on_device(ts.device):
+        out = torch.empty((), dtype=torch.float32, device=ts.tensors[0].device)
+        stream = _memory.stream_of(ts.device)
+        ws = _memory.zeroed_scratch(out.device, stream, lib.gbssim_grad_workspace_bytes(n))
+        st = lib.gbssim_grad_norm(_at(ts.addresses), _at(ts.counts), ts.codes, n, p,
+                                  out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
     _abi.check("gbssim_grad_norm", st)
     return out
 
 
-@torch.no_grad()
 def clip_grads(grads, max_norm: float, norm_type=2.0, out=None) -> torch.Tensor:
     """Scales all gradients by min(1, max_norm / (norm + 1e-6)) and returns their
     norm before that, a 0-dim float32 CUDA tensor.
@@ -102,36 +111,29 @@ def clip_grads(grads, max_norm: float, norm_type=2.0, out=None) -> torch.Tensor:
     limit = float(max_norm)
     if not limit >= 0.0:
         raise ValueError(f"max_norm must not be negative, got {max_norm!r}")
-    ts = _tensors("grads", grads)
-    if not ts:
-        raise ValueError("grads is empty: a norm needs a device to be computed on")
-    codes, addresses = _codes("grads", ts), _addresses(ts)
-    counts = array("q", [t.numel() for t in ts])
-    outs, out_codes, out_addresses = ts, codes, addresses
+    ts = _List("grads", grads)
+    n, outs = len(ts.tensors), ts
     if out is not None:
-        outs = _tensors("out", out)
-        if len(outs) != len(ts):
-            raise ValueError(f"out must have {len(ts)} tensors, got {len(outs)}")
-        for g, o in zip(ts, outs):
-            if o.shape != g.shape or (o.stride() != g.stride() and not
-                                      (o.is_contiguous() and g.is_contiguous())):
+        outs = _List("out", out)
+        if len(outs.tensors) != n:
+            raise ValueError(f"out must have {n} tensors, got {len(outs.tensors)}")
+        if outs.device != ts.device:
+            raise ValueError("grads and out must be on one device")
+        for g, o in zip(ts.tensors, outs.tensors):
+            if o.shape != g.shape or (not (ts.contiguous and outs.contiguous)
+                                      and o.stride() != g.stride()):
                 raise ValueError(f"out must have the gradients' shapes and strides: {tuple(o.shape)}"
                                  f" {o.stride()} for {tuple(g.shape)} {g.stride()}")
-        if outs[0].device != ts[0].device:
-            raise ValueError("grads and out must be on one device")
-        out_codes, out_addresses = _codes("out", outs), _addresses(outs)
     lib = _abi.load()
-    device = ts[0].device
-    with _memory.on_device(device.index):
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        stream = _memory.stream_of(device.index)
-        nbytes = lib.gbssim_grad_workspace_bytes(len(ts))
-        ws = _memory.zeroed_scratch(device, stream, nbytes)
-        st = lib.gbssim_grad_clip(_at(addresses), _at(out_addresses), _at(counts), codes,
-                                  out_codes, len(ts), p, limit, norm.data_ptr(), ws.data_ptr(),
+    with _memory.on_device(ts.device):
+        norm = torch.empty((), dtype=torch.float32, device=ts.tensors[0].device)
+        stream = _memory.stream_of(ts.device)
+        ws = _memory.zeroed_scratch(norm.device, stream, lib.gbssim_grad_workspace_bytes(n))
+        st = lib.gbssim_grad_clip(_at(ts.addresses), _at(outs.addresses), _at(ts.counts), ts.codes,
+                                  outs.codes, n, p, limit, norm.data_ptr(), ws.data_ptr(),
                                   ws.numel(), stream)
     _abi.check("gbssim_grad_clip", st)
-    torch.autograd.graph.increment_version(outs)
+    torch.autograd.graph.increment_version(outs.tensors)
     return norm
 
 

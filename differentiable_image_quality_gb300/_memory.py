@@ -16,7 +16,14 @@ def on_device(index: int):
 
 
 def stream_of(index: int) -> int:
-    return torch.cuda.current_stream(index).cuda_stream
+    # the raw handle: a Stream object costs more than the rest of a small call
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def empty_like(t: torch.Tensor) -> torch.Tensor:
+    """A dense tensor of t's shape, type and device."""
+    return torch.empty_like(t, requires_grad=False) if t.is_contiguous() else \
+        torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def zeroed_scratch(device: torch.device, stream: int, nbytes: int) -> torch.Tensor:

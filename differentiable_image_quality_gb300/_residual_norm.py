@@ -26,13 +26,16 @@ def _kind(name: str, kind) -> int:
         raise ValueError(f"{name} must be 'rms', 'layer' or None, got {kind!r}") from None
 
 
-def _check(name: str, t, device) -> None:
+def _check(name: str, t, index) -> int:
+    """The type's code of a CUDA tensor on device `index` (any, where that is None)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _abi.DTYPES:
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    code = _abi.DTYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return code
 
 
 def _extents(x: torch.Tensor) -> tuple:
@@ -77,81 +80,76 @@ def _rows(name: str, t: torch.Tensor, ext: tuple) -> tuple:
     return t.data_ptr(), (stride[0] if len(shape) > 2 and batch > 1 else tokens * step), step
 
 
-def _param(name: str, p, x, ext, device) -> tuple:
+def _param(name: str, p, ndim, ext, index) -> tuple:
     if p is None:
         return _NO_PARAM
-    _check(name, p, device)
+    code = _check(name, p, index)
     batch, _, dim = ext
-    code = _abi.DTYPES[p.dtype]
     shape = p.shape
     if len(shape) == 1 and shape[0] == dim:
         if dim > 1 and p.stride(0) != 1:
             raise ValueError(f"{name} must be contiguous")
         return p.data_ptr(), code, 0, 0
-    if (x.dim() >= 3 and shape[0] == batch and shape[-1] == dim and len(shape) in (2, x.dim())
+    if (ndim >= 3 and shape[0] == batch and shape[-1] == dim and len(shape) in (2, ndim)
             and p.numel() == batch * dim):
         if dim > 1 and p.stride(-1) != 1:
             raise ValueError(f"the last dimension of {name} must have stride 1")
         return p.data_ptr(), code, 1, p.stride(0) if batch > 1 else 0
-    raise ValueError(f"{name} must have shape ({dim},) or ({batch}, {dim}) beside x of shape "
-                     f"{tuple(x.shape)}, got {tuple(shape)}")
+    raise ValueError(f"{name} must have shape ({dim},) or ({batch}, {dim}) beside x of "
+                     f"{ndim} dimensions, got {tuple(shape)}")
 
 
-class _Call:
-    """One description of the operator, checked: the packed struct and what the
-    outputs need."""
-
-    __slots__ = ("desc", "ext", "device", "blk", "res", "gate_is_rows")
-
-    def __init__(self, x, y, gate, post_norm, post_weight, post_bias, pre_norm, pre_weight,
-                 pre_bias, residual_scale, weight_offset, eps, u_dtype):
-        _check("x", x, None)
-        device = x.device
-        self.ext = ext = _extents(x)
-        if not 1 <= ext[2] <= _MAX_DIM:
-            raise ValueError(f"the last dimension must be 1 to {_MAX_DIM}, got {ext[2]}")
-        kinds = _kind("post_norm", post_norm), _kind("pre_norm", pre_norm)
-        y_rows, gate_rows, gate_param = _NO_ROWS, _NO_ROWS, _NO_PARAM
-        self.gate_is_rows = False
-        if y is None:
-            if gate is not None or kinds[0] or post_weight is not None or post_bias is not None:
-                raise ValueError("without y there is nothing to gate or to normalise before the "
-                                 "residual sum")
-            if residual_scale != 1.0:
-                raise ValueError("without y the residual scale must be 1")
-            self.blk = x.dtype if u_dtype is None else u_dtype
-        else:
-            _check("y", y, device)
-            if y.shape != x.shape:
-                raise ValueError(f"x and y must have one shape, got {tuple(x.shape)} and "
-                                 f"{tuple(y.shape)}")
-            if u_dtype is not None and u_dtype != y.dtype:
-                raise ValueError("u has the type of y")
-            self.blk = y.dtype
-            y_rows = _rows("y", y, ext)
-            if gate is not None:
-                if isinstance(gate, torch.Tensor) and gate.dim() > 1 and gate.shape == x.shape:
-                    _check("gate", gate, device)
-                    if gate.dtype != y.dtype:
-                        raise TypeError(f"a gate per row must have the type of y, got {gate.dtype}")
-                    gate_rows = _rows("gate", gate, ext)
-                    self.gate_is_rows = True
-                else:
-                    gate_param = _param("gate", gate, x, ext, device)
-        if self.blk not in _abi.DTYPES or (x.dtype != self.blk and x.dtype != torch.float32):
-            raise TypeError(f"x must be float32 or have the type of y and u, got {x.dtype} and "
-                            f"{self.blk}")
-        self.device, self.res = device, x.dtype
-        self.desc = _DESC.pack(
-            *ext, _abi.DTYPES[x.dtype], _abi.DTYPES[self.blk], *kinds, residual_scale,
-            weight_offset, eps, *_rows("x", x, ext), *y_rows, *gate_rows, *gate_param,
-            *_param("post_weight", post_weight, x, ext, device),
-            *_param("post_bias", post_bias, x, ext, device),
-            *_param("pre_weight", pre_weight, x, ext, device),
-            *_param("pre_bias", pre_bias, x, ext, device))
+def _describe(x, y, gate, post_norm, post_weight, post_bias, pre_norm, pre_weight, pre_bias,
+              residual_scale, weight_offset, eps, u_dtype):
+    """(packed description, extents, device index, type of u), all checked."""
+    res = _check("x", x, None)
+    index = x.get_device()
+    ext = _extents(x)
+    ndim, dim = x.dim(), ext[2]
+    if not 1 <= dim <= _MAX_DIM:
+        raise ValueError(f"the last dimension must be 1 to {_MAX_DIM}, got {dim}")
+    post, pre = _kind("post_norm", post_norm), _kind("pre_norm", pre_norm)
+    y_rows, gate_rows, gate_param = _NO_ROWS, _NO_ROWS, _NO_PARAM
+    if y is None:
+        if gate is not None or post or post_weight is not None or post_bias is not None:
+            raise ValueError("without y there is nothing to gate or to normalise before the "
+                             "residual sum")
+        if residual_scale != 1.0:
+            raise ValueError("without y the residual scale must be 1")
+        u_type = x.dtype if u_dtype is None else u_dtype
+        blk = _abi.DTYPES.get(u_type)
+    else:
+        blk = _check("y", y, index)
+        if y.shape != x.shape:
+            raise ValueError(f"x and y must have one shape, got {tuple(x.shape)} and "
+                             f"{tuple(y.shape)}")
+        u_type = y.dtype
+        if u_dtype is not None and u_dtype != u_type:
+            raise ValueError("u has the type of y")
+        y_rows = _rows("y", y, ext)
+        if gate is not None:
+            if _gate_is_rows(gate, x):
+                if _check("gate", gate, index) != blk:
+                    raise TypeError(f"a gate per row must have the type of y, got {gate.dtype}")
+                gate_rows = _rows("gate", gate, ext)
+            else:
+                gate_param = _param("gate", gate, ndim, ext, index)
+    if blk is None or (res != blk and res != 0):
+        raise TypeError(f"x must be float32 or have the type of y and u, got {x.dtype} and "
+                        f"{u_type}")
+    desc = _DESC.pack(*ext, res, blk, post, pre, residual_scale, weight_offset, eps,
+                      *_rows("x", x, ext), *y_rows, *gate_rows, *gate_param,
+                      *_param("post_weight", post_weight, ndim, ext, index),
+                      *_param("post_bias", post_bias, ndim, ext, index),
+                      *_param("pre_weight", pre_weight, ndim, ext, index),
+                      *_param("pre_bias", pre_bias, ndim, ext, index))
+    return desc, ext, index, u_type
 
 
-@torch.no_grad()
+def _gate_is_rows(gate, x) -> bool:
+    return isinstance(gate, torch.Tensor) and gate.dim() > 1 and gate.shape == x.shape
+
+
 def residual_norm_fwd(x, y=None, gate=None, *, post_norm=None, post_weight=None, post_bias=None,
                       pre_norm="rms", pre_weight=None, pre_bias=None, residual_scale=1.0,
                       weight_offset=0.0, eps=1e-6, u_dtype=None, x_out=None, want_stats=False):
@@ -163,43 +161,45 @@ def residual_norm_fwd(x, y=None, gate=None, *, post_norm=None, post_weight=None,
     needs: per row the mean and 1/deviation of the post norm and of the pre norm,
     float32 of shape [..., 4].  x_out is x where y is None, u is None where
     pre_norm is."""
-    c = _Call(x, y, gate, post_norm, post_weight, post_bias, pre_norm, pre_weight, pre_bias,
-              residual_scale, weight_offset, eps, u_dtype)
-    device = c.device
-    with _memory.on_device(device.index):
-        if y is not None:
-            if x_out is None:
-                x_out = torch.empty(x.shape, dtype=c.res, device=device)
-            else:
-                _check("x_out", x_out, device)
-                if x_out.shape != x.shape or x_out.dtype != c.res or not x_out.is_contiguous():
-                    raise ValueError("x_out must be contiguous and have the shape and type of x")
-        elif x_out is not None:
-            raise ValueError("without y there is no x_out")
-        kind = _KINDS[pre_norm]
-        wants_u = bool(kind) or pre_weight is not None or pre_bias is not None
-        if not wants_u and y is None:
-            raise ValueError("neither y nor a norm: nothing to compute")
-        u = torch.empty(x.shape, dtype=c.blk, device=device) if wants_u else None
+    desc, _, index, u_type = _describe(x, y, gate, post_norm, post_weight, post_bias, pre_norm,
+                                       pre_weight, pre_bias, residual_scale, weight_offset, eps,
+                                       u_dtype)
+    if y is None and x_out is not None:
+        raise ValueError("without y there is no x_out")
+    wants_u = _KINDS[pre_norm] != 0 or pre_weight is not None or pre_bias is not None
+    if not wants_u and y is None:
+        raise ValueError("neither y nor a norm: nothing to compute")
+    if x_out is not None:
+        _check("x_out", x_out, index)
+        if x_out.shape != x.shape or x_out.dtype != x.dtype or not x_out.is_contiguous():
+            raise ValueError("x_out must be contiguous and have the shape and type of x")
+    with _memory.on_device(index):
+        if x_out is None and y is not None:
+            x_out = _memory.empty_like(x)
+        u = None
+        if wants_u:
+            u = _memory.empty_like(y) if y is not None else \
+                torch.empty(x.shape, dtype=u_type, device=x.device)
         stats = None
         if want_stats:
-            stats = torch.empty((*x.shape[:-1], 4), dtype=torch.float32, device=device)
-        if x.numel():
-            st = _abi.load().gbssim_residual_norm_fwd(
-                c.desc, _abi.ptr(x_out), _abi.ptr(u), _abi.ptr(stats),
-                _memory.stream_of(device.index))
-            _abi.check("gbssim_residual_norm_fwd", st)
-    if y is not None and x_out is x:
+            stats = torch.empty((*x.shape[:-1], 4), dtype=torch.float32, device=x.device)
+        st = _abi.load().gbssim_residual_norm_fwd(
+            desc, None if x_out is None else x_out.data_ptr(), None if u is None else u.data_ptr(),
+            None if stats is None else stats.data_ptr(), _memory.stream_of(index))
+    _abi.check("gbssim_residual_norm_fwd", st)
+    if y is None:
+        return x, u, stats
+    if x_out is x:
         torch.autograd.graph.increment_version(x)
-    return (x if y is None else x_out), u, stats
+    return x_out, u, stats
 
 
-def _grad_rows(name, g, like_shape, dtype, ext, device):
+def _grad_rows(name, g, like, dtype, ext, index):
     if g is None:
         return None, None
-    _check(name, g, device)
-    if g.shape != like_shape or g.dtype != dtype:
-        raise ValueError(f"{name} must have shape {tuple(like_shape)} and type {dtype}, got "
+    _check(name, g, index)
+    if g.shape != like.shape or g.dtype != dtype:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)} and type {dtype}, got "
                          f"{tuple(g.shape)} and {g.dtype}")
     try:
         return _ROWS.pack(*_rows(name, g, ext)), g
@@ -208,7 +208,6 @@ def _grad_rows(name, g, like_shape, dtype, ext, device):
         return _ROWS.pack(*_rows(name, g, ext)), g
 
 
-@torch.no_grad()
 def residual_norm_bwd(g_x, g_u, x, y, stats, gate=None, *, post_norm=None, post_weight=None,
                       post_bias=None, pre_norm="rms", pre_weight=None, pre_bias=None,
                       residual_scale=1.0, weight_offset=0.0, eps=1e-6, u_dtype=None, needs=None):
@@ -217,29 +216,32 @@ def residual_norm_bwd(g_x, g_u, x, y, stats, gate=None, *, post_norm=None, post_
     (x, y, gate, post_weight, post_bias, pre_weight, pre_bias), dense, of their
     tensors' types and shapes; None for what was not given, or where ``needs``
     (seven truth values) is false."""
-    c = _Call(x, y, gate, post_norm, post_weight, post_bias, pre_norm, pre_weight, pre_bias,
-              residual_scale, weight_offset, eps, u_dtype)
-    device, ext = c.device, c.ext
-    rows = ext[0] * ext[1]
+    desc, ext, index, u_type = _describe(x, y, gate, post_norm, post_weight, post_bias, pre_norm,
+                                         pre_weight, pre_bias, residual_scale, weight_offset, eps,
+                                         u_dtype)
     if g_x is None and g_u is None:
         raise ValueError("one of g_x and g_u must be given")
-    if not isinstance(stats, torch.Tensor) or stats.device != device or \
-            stats.dtype != torch.float32 or not stats.is_contiguous() or stats.numel() != rows * 4:
-        raise ValueError(f"stats must be the forward's: contiguous float32, {rows} x 4")
-    inputs = (x, y, gate, post_weight, post_bias, pre_weight, pre_bias)
-    needs = (True,) * 7 if needs is None else needs
-    with _memory.on_device(device.index):
-        lib = _abi.load()
-        gx, keep_x = _grad_rows("g_x", g_x, x.shape, c.res, ext, device)
-        gu, keep_u = _grad_rows("g_u", g_u, x.shape, c.blk, ext, device)
-        grads = [None if t is None or not want else
-                 torch.empty(t.shape, dtype=t.dtype, device=device)
-                 for t, want in zip(inputs, needs)]
-        nbytes = lib.gbssim_residual_norm_workspace_bytes(c.desc)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        packed = _GRADS.pack(*[0 if g is None else g.data_ptr() for g in grads])
-        st = lib.gbssim_residual_norm_bwd(c.desc, gx, gu, _abi.ptr(stats), packed, ws.data_ptr(),
-                                          nbytes, _memory.stream_of(device.index))
+    if not isinstance(stats, torch.Tensor) or stats.get_device() != index or \
+            stats.dtype != torch.float32 or not stats.is_contiguous() or \
+            stats.numel() != ext[0] * ext[1] * 4:
+        raise ValueError(f"stats must be the forward's: contiguous float32, {ext[0] * ext[1]} x 4")
+    lib = _abi.load()
+    empty_like = _memory.empty_like
+    with _memory.on_device(index):
+        gx, keep_x = _grad_rows("g_x", g_x, x, x.dtype, ext, index)
+        gu, keep_u = _grad_rows("g_u", g_u, x, u_type, ext, index)
+        inputs = (x, y, gate, post_weight, post_bias, pre_weight, pre_bias)
+        if needs is None:
+            grads = [None if t is None else empty_like(t) for t in inputs]
+        else:
+            grads = [empty_like(t) if n and t is not None else None
+                     for t, n in zip(inputs, needs)]
+        nbytes = lib.gbssim_residual_norm_workspace_bytes(desc)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        st = lib.gbssim_residual_norm_bwd(
+            desc, gx, gu, stats.data_ptr(),
+            _GRADS.pack(*[0 if g is None else g.data_ptr() for g in grads]), ws.data_ptr(), nbytes,
+            _memory.stream_of(index))
     _abi.check("gbssim_residual_norm_bwd", st)
     return tuple(grads)
 
@@ -247,8 +249,9 @@ def residual_norm_bwd(g_x, g_u, x, y, stats, gate=None, *, post_norm=None, post_
 class _FusedResidualNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, y, gate, post_weight, post_bias, pre_weight, pre_bias, how):
-        args = dict(zip(_PARAMS, (gate, post_weight, post_bias, pre_weight, pre_bias)), **how)
-        x_out, u, stats = residual_norm_fwd(x, y, **args, want_stats=any(ctx.needs_input_grad))
+        x_out, u, stats = residual_norm_fwd(
+            x, y, gate, post_weight=post_weight, post_bias=post_bias, pre_weight=pre_weight,
+            pre_bias=pre_bias, want_stats=True in ctx.needs_input_grad, **how)
         ctx.set_materialize_grads(False)
         ctx.how = how
         ctx.save_for_backward(x, y, stats, gate, post_weight, post_bias, pre_weight, pre_bias)
@@ -258,15 +261,12 @@ class _FusedResidualNorm(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, g_x, g_u):
-        x, y, stats, *params = ctx.saved_tensors
         if g_x is None and g_u is None:
             return (None,) * 8
-        grads = residual_norm_bwd(g_x, g_u, x, y, stats, **dict(zip(_PARAMS, params)), **ctx.how,
-                                  needs=ctx.needs_input_grad)
-        return (*grads, None)
-
-
-_PARAMS = ("gate", "post_weight", "post_bias", "pre_weight", "pre_bias")
+        x, y, stats, gate, post_weight, post_bias, pre_weight, pre_bias = ctx.saved_tensors
+        return (*residual_norm_bwd(
+            g_x, g_u, x, y, stats, gate, post_weight=post_weight, post_bias=post_bias,
+            pre_weight=pre_weight, pre_bias=pre_bias, needs=ctx.needs_input_grad, **ctx.how), None)
 
 
 def fused_residual_norm(x, y=None, gate=None, *, post_norm=None, post_weight=None, post_bias=None,

@@ -1,6 +1,7 @@
 // Host-side helpers shared by the entry points of the C ABI.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -36,13 +37,19 @@ inline bool overlaps(const void *a, size_t na, const void *b, size_t nb)
 
 inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// Number of SMs of the current device.
-inline cudaError_t current_sm_count(int *out)
+// Number of SMs of the current device (a launch fact, read once per device).
+inline cudaError_t current_sm_count(int *out, int *device = nullptr)
 {
+    constexpr int kMost = 64;
+    static std::atomic<int> known[kMost];
     int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    return cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
+    if (device) *device = dev;
+    if (dev < kMost && (*out = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev < kMost) known[dev].store(*out, std::memory_order_relaxed);
+    return e;
 }
 
 }  // namespace gbssim

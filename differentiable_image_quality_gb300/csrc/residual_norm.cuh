@@ -347,11 +347,12 @@ cudaError_t launch_staged(Kernel kernel, ResidualNormArgs &a, int units, int per
     const int blocks = per_sm * kMaxTeamThreads / a.plan.threads;
     a.plan.stages = std::max(1, std::min(kMaxStages, kSmemPerSm / (stage * blocks)));
     const int smem = a.plan.stages * stage;
-    // one attribute for all sizes: every launch of the kernel sets the same
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kMaxBlockSmem);
-    if (e != cudaSuccess) return e;
+    if (smem > 40 * 1024) {  // with the static arrays: above what needs no asking for
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kMaxBlockSmem);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.plan.grid);
     cfg.blockDim = dim3(unsigned(a.plan.threads));
