@@ -169,15 +169,90 @@ __device__ __forceinline__ Raw8<T> shift_down(const Wide8<T> &in, int s)
     return r;
 }
 
-// 16 bytes to shared memory without passing through registers; L1 keeps the
-// line where a neighbour's copy overlaps.
-__device__ __forceinline__ void copy16_async(void *smem, const void *gmem, bool keep_l1)
+// 16 bytes to shared memory (a 32-bit shared address) without passing through
+// registers; KEEP: L1 keeps the line, for a neighbour's copy that overlaps.
+template <bool KEEP>
+__device__ __forceinline__ void copy16_async(unsigned smem, const void *gmem)
 {
-    const unsigned s = static_cast<unsigned>(__cvta_generic_to_shared(smem));
-    if (keep_l1)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(s), "l"(gmem) : "memory");
+    if constexpr (KEEP)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
     else
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(gmem) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared16(unsigned smem)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(smem)
+                 : "memory");
+    return v;
+}
+
+// ------------------------------------------------------------ pairs of floats
+// Two float32 in one 64-bit register: one instruction does both (fma.rn.f32x2;
+// each half rounds as the scalar instruction does).
+
+using f32x2 = unsigned long long;
+
+__device__ __forceinline__ f32x2 pair(float lo, float hi)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ f32x2 both(float v) { return pair(v, v); }
+__device__ __forceinline__ float2 halves(f32x2 v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float sum2(f32x2 v)
+{
+    const float2 h = halves(v);
+    return h.x + h.y;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw8<T> &r, f32x2 (&v)[4])
+{
+    float f[8];
+    unpack8<T>(r, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pair(f[2 * i], f[2 * i + 1]);
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> pack8(const f32x2 (&v)[4])
+{
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 h = halves(v[i]);
+        f[2 * i] = h.x;
+        f[2 * i + 1] = h.y;
+    }
+    return pack8<T>(f);
 }
 
 }  // namespace gbssim

@@ -30,6 +30,7 @@ struct RowPtr {
     const void *p;
     long long sb, st;  // elements between batches and between tokens
     const void *end;   // past the last row's last element
+    int row_bytes;     // from one row to the next, where one stride reaches all rows
 };
 
 struct ParamPtr {
@@ -135,6 +136,16 @@ struct Cols {
     }
 };
 
+// Column `col` of row r of a tensor.
+template <typename T>
+__device__ __forceinline__ const unsigned char *row_at(const RowPtr &p, int tokens, int r, int col)
+{
+    const unsigned char *base = static_cast<const unsigned char *>(p.p) + col * int(sizeof(T));
+    if (tokens == 0) return base + (long long)r * p.row_bytes;
+    const int b = r / tokens, t = r - b * tokens;
+    return base + (b * p.sb + t * p.st) * int(sizeof(T));
+}
+
 // Rows on their way through shared memory: every thread copies its own columns
 // of a row some rows ahead (cp.async) and reads them back itself, so the copies
 // need no barrier.  A stage holds, per tensor, 16-byte words [word][thread].
@@ -147,67 +158,71 @@ template <typename T, bool ALIGNED>
 struct Staged {
     static constexpr int kUnits = (sizeof(T) == 4 ? 2 : 1) + (ALIGNED ? 0 : 1);
 
-    // Of the row at `row`; slot: the thread's first word.
-    static __device__ __forceinline__ void fetch(const RowPtr &p, const T *row,
-                                                 const Cols<ALIGNED> &c, uint4 *slot, int threads)
+    // at: the thread's first column; slot: its first word, `pitch` bytes from word to word.
+    static __device__ __forceinline__ void fetch(const RowPtr &p, const unsigned char *at,
+                                                 const Cols<ALIGNED> &c, unsigned slot, int pitch)
     {
-        const unsigned char *at = reinterpret_cast<const unsigned char *>(row + c.first);
         if constexpr (ALIGNED) {
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u) copy16_async(slot + u * threads, at + u * 16, false);
+            for (int u = 0; u < kUnits; ++u) copy16_async<false>(slot + u * pitch, at + u * 16);
         } else {
             const unsigned char *from = at + c.from * int(sizeof(T));
             const unsigned char *stop = at + c.upto * int(sizeof(T));
             const unsigned char *word = at - (reinterpret_cast<uintptr_t>(at) & 15);
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u, word += 16) {
+            for (int u = 0; u < kUnits; ++u, word += 16, slot += pitch) {
                 if (word >= stop || word + 16 <= from) continue;
                 if (word >= p.p && word + 16 <= p.end) {
-                    copy16_async(slot + u * threads, word, true);
+                    copy16_async<true>(slot, word);
                 } else {
-                    const T *e = reinterpret_cast<const T *>(word);
-                    T *to = reinterpret_cast<T *>(slot + u * threads);
+                    T *to = static_cast<T *>(__cvta_shared_to_generic(slot));
 #pragma unroll 1
-                    for (int i = 0; i < int(16 / sizeof(T)); ++i)
-                        if (reinterpret_cast<const unsigned char *>(e + i) >= from &&
-                            reinterpret_cast<const unsigned char *>(e + i) < stop)
-                            to[i] = e[i];
+                    for (int i = 0; i < 16; i += int(sizeof(T)))
+                        if (word + i >= from && word + i < stop)
+                            to[i / int(sizeof(T))] = *reinterpret_cast<const T *>(word + i);
                 }
             }
         }
     }
 
-    // The thread's columns, zero where the row has none.
-    static __device__ __forceinline__ void read(const T *row, const Cols<ALIGNED> &c, bool active,
-                                                const uint4 *slot, int threads, float (&v)[8])
+    // The thread's columns of a row, zero where the row has none.
+    static __device__ __forceinline__ void read(const RowPtr &p, int tokens, int row,
+                                                const Cols<ALIGNED> &c, bool active, unsigned slot,
+                                                int pitch, f32x2 (&v)[4])
     {
-        if (!active || !c.any()) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-            return;
-        }
-        Raw8<T> r;
+        Raw8<T> r{};
         if constexpr (ALIGNED) {
+            if (active && c.any()) {
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u) r.w[u] = slot[u * threads];
+                for (int u = 0; u < kUnits; ++u) r.w[u] = ld_shared16(slot + u * pitch);
+            }
             unpack8<T>(r, v);
         } else {
-            const int s = int(reinterpret_cast<uintptr_t>(row + c.first) & 15) / int(sizeof(T));
-            if (s == 0) {
+            if (active && c.any()) {
+                const int s = int(reinterpret_cast<uintptr_t>(row_at<T>(p, tokens, row, c.first)) & 15) /
+                              int(sizeof(T));
+                if (s == 0) {
 #pragma unroll
-                for (int u = 0; u < kUnits - 1; ++u) r.w[u] = slot[u * threads];
-            } else {
-                Wide8<T> w;
+                    for (int u = 0; u < kUnits - 1; ++u) r.w[u] = ld_shared16(slot + u * pitch);
+                } else {
+                    Wide8<T> w;
 #pragma unroll
-                for (int u = 0; u < kUnits; ++u)
-                    reinterpret_cast<uint4 *>(w.w)[u] = slot[u * threads];
-                r = shift_down<T>(w, s);
+                    for (int u = 0; u < kUnits; ++u) {
+                        const uint4 q = ld_shared16(slot + u * pitch);
+                        w.w[4 * u] = q.x; w.w[4 * u + 1] = q.y;
+                        w.w[4 * u + 2] = q.z; w.w[4 * u + 3] = q.w;
+                    }
+                    r = shift_down<T>(w, s);
+                }
             }
-            unpack8<T>(r, v);
+            float f[8];
+            unpack8<T>(r, f);
             if (!c.all()) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = c.has(e) ? v[e] : 0.0f;
+                for (int e = 0; e < 8; ++e) f[e] = c.has(e) ? f[e] : 0.0f;
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
         }
     }
 };
@@ -226,23 +241,24 @@ __device__ __forceinline__ void staged_wait(int stages)
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Stores the thread's columns of a row: in whole words where it has all eight
-// and they are aligned, one by one at a row's ends.
+// Stores the thread's columns of a row, the first at `to`: in whole words where
+// it has all eight and they are aligned, one by one at a row's ends.
 template <typename T, bool ALIGNED>
-__device__ __forceinline__ void store_row(T *row, const Cols<ALIGNED> &c, bool active,
-                                          const float (&v)[8])
+__device__ __forceinline__ void store_cols(T *to, const Cols<ALIGNED> &c, bool active,
+                                           const f32x2 (&v)[4])
 {
-    T *at = row + c.first;
     if constexpr (ALIGNED) {
-        if (active && c.any()) st8(at, pack8<T>(v));
+        if (active && c.any()) st8(to, pack8<T>(v));
     } else {
         if (!active) return;
-        if (c.all() && (reinterpret_cast<uintptr_t>(at) & 15) == 0) {
-            st8(at, pack8<T>(v));
+        if (c.all() && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+            st8(to, pack8<T>(v));
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c.has(e)) at[e] = from_f32<T>(v[e]);
+            for (int e = 0; e < 8; ++e) {
+                const float2 h = halves(v[e / 2]);
+                if (c.has(e)) to[e] = from_f32<T>(e & 1 ? h.y : h.x);
+            }
         }
     }
 }
@@ -264,34 +280,27 @@ __device__ __forceinline__ float param_at(const ParamPtr &p, int group, int col)
 // The thread's eight values of a parameter plus `offset`; `missing` where it is null.
 template <bool ALIGNED>
 __device__ __forceinline__ void load_param(const ParamPtr &p, int group, const Cols<ALIGNED> &c,
-                                           float offset, float missing,
-                                           float (&v)[8])
+                                           float offset, float missing, f32x2 (&v)[4])
 {
+    float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        v[e] = !p.p ? missing : (c.has(e) ? param_at(p, group, c.first + e) + offset : 0.0f);
+        f[e] = !p.p ? missing : (c.has(e) ? param_at(p, group, c.first + e) + offset : 0.0f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
 }
 
-// Row r of a tensor.
-template <typename T>
-__device__ __forceinline__ const T *row_of(const RowPtr &p, int tokens, int r)
-{
-    const T *base = static_cast<const T *>(p.p);
-    if (tokens == 0) return base + r * p.st;
-    const int b = r / tokens, t = r - b * tokens;
-    return base + (b * p.sb + t * p.st);
-}
-
-// Sums of N values over a team.  All threads of a block call together.
+// Sums over a team, of one value or of two.  All threads of a block call together.
 struct TeamSum {
-    float (*slots)[2][16];         // [2][N][warp]
-    float (*cluster_slots)[2][4];  // [2][N][block of the cluster]
+    float2 (*slots)[16];         // [2][warp]
+    float2 (*cluster_slots)[4];  // [2][block of the cluster]
     int parity, tpr, warps, cluster;
 
     template <int N>
     __device__ __forceinline__ void operator()(float (&v)[N])
     {
         if (tpr < 32) {
+#pragma unroll 1
             for (int o = tpr >> 1; o > 0; o >>= 1)
 #pragma unroll
                 for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
@@ -306,13 +315,16 @@ struct TeamSum {
         // slot again has passed the barrier of the sum in between, which every
         // thread reaches only after it has read this one
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-            if (lane == k) slots[parity][k][warp] = v[k];
+        float2 *const mine = slots[parity];
+        if (lane == 0) {
+            mine[warp].x = v[0];
+            if (N == 2) mine[warp].y = v[N - 1];
+        }
         __syncthreads();
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-            v[k] = (lane & 15) < warps ? slots[parity][k][lane & 15] : 0.0f;
+        float2 got = make_float2(0.0f, 0.0f);
+        if ((lane & 15) < warps) got = mine[lane & 15];
+        v[0] = got.x;
+        if (N == 2) v[N - 1] = got.y;
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
@@ -320,19 +332,25 @@ struct TeamSum {
         if (cluster > 1) {
             namespace cg = cooperative_groups;
             cg::cluster_group cl = cg::this_cluster();
-            if (int(threadIdx.x) < cluster) {
-#pragma unroll
-                for (int k = 0; k < N; ++k)
-                    cl.map_shared_rank(&cluster_slots[parity][k][0], threadIdx.x)[cl.block_rank()] = v[k];
-            }
+            if (int(threadIdx.x) < cluster)
+                cl.map_shared_rank(&cluster_slots[parity][0], threadIdx.x)[cl.block_rank()] =
+                    make_float2(v[0], v[N - 1]);
             cl.sync();
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                v[k] = 0.0f;
-                for (int r = 0; r < cluster; ++r) v[k] += cluster_slots[parity][k][r];
+            v[0] = v[N - 1] = 0.0f;
+            for (int r = 0; r < cluster; ++r) {
+                const float2 c = cluster_slots[parity][r];
+                v[0] += c.x;
+                if (N == 2) v[N - 1] += c.y;
             }
         }
         parity ^= 1;
+    }
+
+    __device__ __forceinline__ float one(float v)
+    {
+        float a[1] = {v};
+        (*this)(a);
+        return a[0];
     }
 };
 

@@ -74,7 +74,7 @@ int check_desc(const gbssim_residual_norm *d)
         if (kind < GBSSIM_ROW_NONE || kind > GBSSIM_ROW_LAYER) return GBSSIM_EINVAL;
     if (!(d->eps >= 0.0f)) return GBSSIM_EINVAL;
     if (d->batch < 0 || d->tokens < 0 || d->dim < 1 || d->dim > kMaxDim) return GBSSIM_ESHAPE;
-    if (row_count(*d) > INT_MAX - 4096) return GBSSIM_ESHAPE;
+    if (row_count(*d) > INT_MAX - 65536) return GBSSIM_ESHAPE;
     const bool some = row_count(*d) > 0;
     if (some && !d->x.data) return GBSSIM_EINVAL;
     // without a block's output there is nothing to normalise or gate
@@ -159,10 +159,12 @@ RowPlan make_plan(const gbssim_residual_norm &d, int threads_per_sm, int sm_coun
     return p;
 }
 
-// Rows are addressed by batch and token, in one step where that is the same.
+// Rows are addressed by batch and token, in one step where that is the same (and
+// the step fits 32 bits).
 bool one_stride(const gbssim_residual_norm &d, const gbssim_rows &r)
 {
-    return !r.data || d.batch < 2 || r.batch_stride == d.tokens * r.token_stride;
+    return !r.data || ((d.batch < 2 || r.batch_stride == d.tokens * r.token_stride) &&
+                       r.token_stride <= INT_MAX / 4);
 }
 
 bool dense(const gbssim_residual_norm &d, const gbssim_rows &r)
@@ -174,7 +176,8 @@ bool dense(const gbssim_residual_norm &d, const gbssim_rows &r)
 RowPtr row_ptr(const gbssim_residual_norm &d, const gbssim_rows &r, int dtype)
 {
     const Extent e = rows_extent(d, r, dtype);
-    return {r.data, r.batch_stride, r.token_stride, static_cast<const char *>(e.p) + e.bytes};
+    return {r.data, r.batch_stride, r.token_stride, static_cast<const char *>(e.p) + e.bytes,
+            int(r.token_stride * dtype_bytes(dtype))};
 }
 ParamPtr param_ptr(const gbssim_param &p) { return {p.data, p.dtype, p.per_sample != 0, p.per_sample ? p.sample_stride : 0}; }
 

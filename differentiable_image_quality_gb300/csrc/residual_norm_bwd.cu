@@ -16,8 +16,8 @@
 // block, and a second kernel adds the partials in a fixed order.
 #include <algorithm>
 
-#include "residual_norm.cuh"
 #include "common.cuh"
+#include "residual_norm.cuh"
 
 namespace gbssim {
 namespace {
@@ -25,9 +25,16 @@ namespace {
 // One column sum of the block to its partial: over the block's teams first.
 template <bool ALIGNED>
 __device__ __forceinline__ void write_sum(const ResidualNormArgs &a, const Cols<ALIGNED> &c,
-                                          int place, float (&v)[8], float *scratch)
+                                          int place, const f32x2 (&sums)[4], float *scratch)
 {
     if (place < 0) return;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 h = halves(sums[e]);
+        v[2 * e] = h.x;
+        v[2 * e + 1] = h.y;
+    }
     const int item = int(blockIdx.x) / a.plan.cluster;
     float *dst = a.partials + ((long long)item * a.sums + place) * a.dim;
     if (a.plan.teams > 1) {
@@ -63,158 +70,159 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
     using SR = Staged<R, ALIGNED>;
     using SY = Staged<Y, ALIGNED>;
     extern __shared__ uint4 ring[];
-    __shared__ float slots[2][2][16];
-    __shared__ float cluster_slots[2][2][4];
+    __shared__ float2 slots[2][16];
+    __shared__ float2 cluster_slots[2][4];
     __shared__ float scratch[kSmallBlock * 8];
     const BlockRows rows(a);
     const Cols<ALIGNED> c(a, rows.shift);
     TeamSum sum{slots, cluster_slots, 0, a.plan.tpr, a.plan.teams > 1 ? 1 : a.plan.threads / 32,
                 a.plan.cluster};
     const int team = a.plan.teams > 1 ? int(threadIdx.x) / a.plan.tpr : 0;
-    const int threads = a.plan.threads, stages = a.plan.stages;
-    const int stage_words = (2 * SR::kUnits + (FULL ? 3 : 2) * SY::kUnits) * threads;
-    uint4 *const mine = ring + threadIdx.x;
+    const int step = rows.step * a.plan.teams;  // rows from one of the team's to its next
+    const int pitch = a.plan.threads * 16, stages = a.plan.stages;
+    const bool has_y = a.y.p, has_gx = a.gx.p, has_gu = a.gu.p;
+    // the words of a stage: x, G, y, V, gate
+    const int at_gx = SR::kUnits * pitch, at_y = 2 * at_gx, at_gu = at_y + SY::kUnits * pitch,
+              at_gate = at_gu + SY::kUnits * pitch;
+    const int stage_bytes = at_gate + (FULL ? SY::kUnits * pitch : 0);
+    const unsigned mine = smem_u32(ring) + threadIdx.x * 16, over = mine + stages * stage_bytes;
     // no block writes into another's shared memory before that block runs
     if (a.plan.cluster > 1) cooperative_groups::this_cluster().sync();
 
-    // the words of a stage: x, G, y, V, gate
-    const int at_gx = SR::kUnits * threads, at_y = 2 * at_gx, at_gu = at_y + SY::kUnits * threads,
-              at_gate = at_gu + SY::kUnits * threads;
-    const auto fetch = [&](int i, uint4 *slot) {
-        if (i < rows.count && c.any()) {
-            const int r = rows.first + i * rows.step;
-            SR::fetch(a.x, row_of<R>(a.x, a.tokens, r), c, slot, threads);
-            if (a.gx.p) SR::fetch(a.gx, row_of<R>(a.gx, a.tokens, r), c, slot + at_gx, threads);
-            if (a.y.p) SY::fetch(a.y, row_of<Y>(a.y, a.tokens, r), c, slot + at_y, threads);
-            if (a.gu.p) SY::fetch(a.gu, row_of<Y>(a.gu, a.tokens, r), c, slot + at_gu, threads);
+    int r = rows.first + team * rows.step, left = rows.count - team;  // the team's row; none if <= 0
+    int ahead = r, ahead_left = left;
+    unsigned to = mine;
+    const auto fetch = [&] {
+        if (ahead_left > 0 && c.any()) {
+            SR::fetch(a.x, row_at<R>(a.x, a.tokens, ahead, c.first), c, to, pitch);
+            if (has_gx)
+                SR::fetch(a.gx, row_at<R>(a.gx, a.tokens, ahead, c.first), c, to + at_gx, pitch);
+            if (has_y) SY::fetch(a.y, row_at<Y>(a.y, a.tokens, ahead, c.first), c, to + at_y, pitch);
+            if (has_gu)
+                SY::fetch(a.gu, row_at<Y>(a.gu, a.tokens, ahead, c.first), c, to + at_gu, pitch);
             if (FULL)
-                SY::fetch(a.gate_rows, row_of<Y>(a.gate_rows, a.tokens, r), c, slot + at_gate,
-                          threads);
+                SY::fetch(a.gate_rows, row_at<Y>(a.gate_rows, a.tokens, ahead, c.first), c,
+                          to + at_gate, pitch);
         }
         staged_commit();
+        ahead += step;
+        ahead_left -= a.plan.teams;
+        to += stage_bytes;
+        if (to == over) to = mine;
     };
-    for (int i = 0; i < stages - 1; ++i) fetch(i * a.plan.teams + team, mine + i * stage_words);
+    for (int i = 0; i < stages - 1; ++i) fetch();
 
-    float w1[8], b1[8], w2[8];  // with the gate of the column in w1 and b1, unless FULL
+    f32x2 w1[4], b1[4], w2[4];  // with the gate of the column in w1 and b1, unless FULL
     load_param(a.w1, rows.group, c, a.offset, 1.0f, w1);
     load_param(a.w2, rows.group, c, a.offset, 1.0f, w2);
     if (BIAS) load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
     if (!FULL && a.gate.p) {
-        float g[8];
+        f32x2 g[4];
         load_param(a.gate, rows.group, c, 0.0f, 1.0f, g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w1[e] *= g[e];
-            if (BIAS) b1[e] *= g[e];
+        for (int e = 0; e < 4; ++e) {
+            w1[e] = mul2(w1[e], g[e]);
+            if (BIAS) b1[e] = mul2(b1[e], g[e]);
         }
     }
+    const f32x2 scale = both(a.scale);
+    unsigned at = mine;
     // Columns that a row does not have hold zeros of x, y, G, V and of w1 and b1:
     // whatever a mean makes of y^, x^ and T there meets a zero factor before it
     // enters a sum over the row, and their own sums are not stored.
-    float sa[8] = {}, sf[8] = {}, sc[8] = {}, se[8] = {};
-    int now = 0;
-    for (int i0 = 0; i0 < rows.count; i0 += a.plan.teams) {
-        const int i = i0 + team, r = rows.first + i * rows.step;
-        const bool active = i < rows.count;
+    f32x2 sa[4] = {}, sf[4] = {}, sc[4] = {}, se[4] = {};
+    for (int i = 0; i < rows.count; i += a.plan.teams) {
+        const bool active = left > 0;
         float4 st = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
         if (active) st = a.stats[r];
-        {
-            const int ahead = now == 0 ? stages - 1 : now - 1;
-            fetch(i + (stages - 1) * a.plan.teams, mine + ahead * stage_words);
-        }
+        fetch();
         staged_wait(stages);
-        const uint4 *slot = mine + now * stage_words;
-        now = now + 1 == stages ? 0 : now + 1;
 
-        float yh[8], xh[8], T[8], V[8], g[8];
-        SR::read(row_of<R>(a.x, a.tokens, r), c, active, slot, threads, xh);
-        if (a.y.p) {
-            SY::read(row_of<Y>(a.y, a.tokens, r), c, active, slot + at_y, threads, yh);
-            if (FULL)
-                SY::read(row_of<Y>(a.gate_rows, a.tokens, r), c, active, slot + at_gate, threads, g);
-            const float m1 = -st.x * st.y;
+        f32x2 yh[4], xh[4], T[4], g[4];
+        SR::read(a.x, a.tokens, r, c, active, at, pitch, xh);
+        if (has_y) {
+            SY::read(a.y, a.tokens, r, c, active, at + at_y, pitch, yh);
+            if (FULL) SY::read(a.gate_rows, a.tokens, r, c, active, at + at_gate, pitch, g);
+            const f32x2 v = both(st.y), m = both(-st.x * st.y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                yh[e] = fmaf(yh[e], st.y, m1);
-                float z = BIAS ? fmaf(yh[e], w1[e], b1[e]) : yh[e] * w1[e];
-                if (FULL) z *= g[e];
-                xh[e] = fmaf(a.scale, xh[e], z);
+            for (int e = 0; e < 4; ++e) {
+                yh[e] = fma2(yh[e], v, m);
+                f32x2 z = BIAS ? fma2(yh[e], w1[e], b1[e]) : mul2(yh[e], w1[e]);
+                if (FULL) z = mul2(z, g[e]);
+                xh[e] = fma2(scale, xh[e], z);
             }
         }
-        if (a.gx.p) {
-            SR::read(row_of<R>(a.gx, a.tokens, r), c, active, slot + at_gx, threads, T);
+        if (has_gx) {
+            SR::read(a.gx, a.tokens, r, c, active, at + at_gx, pitch, T);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) T[e] = 0.0f;
+            for (int e = 0; e < 4; ++e) T[e] = 0;
         }
-        if (a.gu.p) {
-            SY::read(row_of<Y>(a.gu, a.tokens, r), c, active, slot + at_gu, threads, V);
-            float m[2] = {};
-            const float m2 = -st.z * st.w;
+        if (has_gu) {
+            f32x2 V[4], q = 0;
+            SY::read(a.gu, a.tokens, r, c, active, at + at_gu, pitch, V);
+            const f32x2 v = both(st.w), m = both(-st.z * st.w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                xh[e] = fmaf(xh[e], st.w, m2);
-                sc[e] = fmaf(V[e], xh[e], sc[e]);
-                if (BIAS) se[e] += V[e];
-                V[e] *= w2[e];
-                m[0] = fmaf(V[e], xh[e], m[0]);
+            for (int e = 0; e < 4; ++e) {
+                xh[e] = fma2(xh[e], v, m);
+                sc[e] = fma2(V[e], xh[e], sc[e]);
+                if (BIAS) se[e] = add2(se[e], V[e]);
+                V[e] = mul2(V[e], w2[e]);
+                q = fma2(V[e], xh[e], q);
             }
+            float d[2] = {sum2(q), 0.0f};
             if (a.pre == GBSSIM_ROW_LAYER) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m[1] += V[e];
-                sum(m);
-            } else if (a.pre == GBSSIM_ROW_RMS) {
-                float q[1] = {m[0]};
-                sum(q);
-                m[0] = q[0];
+                d[1] = sum2(add2(add2(V[0], V[1]), add2(V[2], V[3])));
+                sum(d);
             } else {
-                m[0] = 0.0f;
+                d[0] = a.pre == GBSSIM_ROW_RMS ? sum.one(d[0]) : 0.0f;
             }
-            // T += r2 (dx^ - m1 - x^ m0)
-            const float m0 = -m[0] * a.inv_dim, m1 = -m[1] * a.inv_dim;
+            // T += r2 (dx^ - mean(dx^) - x^ mean(dx^ x^))
+            const f32x2 d0 = both(-d[0] * a.inv_dim), d1 = both(-d[1] * a.inv_dim);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) T[e] = fmaf(st.w, fmaf(xh[e], m0, V[e] + m1), T[e]);
+            for (int e = 0; e < 4; ++e) T[e] = fma2(v, fma2(xh[e], d0, add2(V[e], d1)), T[e]);
         }
         if (a.dx) {
-            const float s = a.y.p ? a.scale : 1.0f;
-            float dx[8];
+            f32x2 dx[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dx[e] = s * T[e];
-            store_row(static_cast<R *>(a.dx) + (long long)r * a.dim, c, active, dx);
+            for (int e = 0; e < 4; ++e) dx[e] = has_y ? mul2(scale, T[e]) : T[e];
+            store_cols(static_cast<R *>(a.dx) + ((long long)r * a.dim + c.first), c, active, dx);
         }
-        if (!a.y.p) continue;
-        if (FULL && a.dgate_rows) {
-            float dg[8];
+        if (has_y) {
+            if (FULL && a.dgate_rows) {
+                f32x2 dg[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                dg[e] = T[e] * (BIAS ? fmaf(yh[e], w1[e], b1[e]) : yh[e] * w1[e]);
-            store_row(static_cast<Y *>(a.dgate_rows) + (long long)r * a.dim, c, active, dg);
+                for (int e = 0; e < 4; ++e)
+                    dg[e] = mul2(T[e], BIAS ? fma2(yh[e], w1[e], b1[e]) : mul2(yh[e], w1[e]));
+                store_cols(static_cast<Y *>(a.dgate_rows) + ((long long)r * a.dim + c.first), c, active, dg);
+            }
+            f32x2 q = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (FULL) T[e] = mul2(T[e], g[e]);
+                sa[e] = fma2(T[e], yh[e], sa[e]);
+                if (BIAS) sf[e] = add2(sf[e], T[e]);
+                T[e] = mul2(T[e], w1[e]);
+                q = fma2(T[e], yh[e], q);
+            }
+            if (a.dy) {
+                float d[2] = {sum2(q), 0.0f};
+                if (a.post == GBSSIM_ROW_LAYER) {
+                    d[1] = sum2(add2(add2(T[0], T[1]), add2(T[2], T[3])));
+                    sum(d);
+                } else {
+                    d[0] = a.post == GBSSIM_ROW_RMS ? sum.one(d[0]) : 0.0f;
+                }
+                const f32x2 v = both(st.y), d0 = both(-d[0] * a.inv_dim), d1 = both(-d[1] * a.inv_dim);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) T[e] = mul2(v, fma2(yh[e], d0, add2(T[e], d1)));
+                store_cols(static_cast<Y *>(a.dy) + ((long long)r * a.dim + c.first), c, active, T);
+            }
         }
-        float d[2] = {};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (FULL) T[e] *= g[e];
-            sa[e] = fmaf(T[e], yh[e], sa[e]);
-            if (BIAS) sf[e] += T[e];
-            T[e] *= w1[e];
-            d[0] = fmaf(T[e], yh[e], d[0]);
-        }
-        if (!a.dy) continue;
-        if (a.post == GBSSIM_ROW_LAYER) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[1] += T[e];
-            sum(d);
-        } else if (a.post == GBSSIM_ROW_RMS) {
-            float q[1] = {d[0]};
-            sum(q);
-            d[0] = q[0];
-        } else {
-            d[0] = 0.0f;
-        }
-        const float d0 = -d[0] * a.inv_dim, d1 = -d[1] * a.inv_dim;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) T[e] = st.y * fmaf(yh[e], d0, T[e] + d1);
-        store_row(static_cast<Y *>(a.dy) + (long long)r * a.dim, c, active, T);
+        r += step;
+        left -= a.plan.teams;
+        at += stage_bytes;
+        if (at == over) at = mine;
     }
     write_sum(a, c, a.sum_a, sa, scratch);
     write_sum(a, c, a.sum_c, sc, scratch);

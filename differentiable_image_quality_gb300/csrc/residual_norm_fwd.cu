@@ -3,43 +3,47 @@
 // Bound by memory: x and y are read once, x' and u written once, and both
 // norms' statistics are taken from the row held in registers, in float32.  u
 // comes from x' before its rounding.
+#include "common.cuh"
 #include "residual_norm.cuh"
 
 namespace gbssim {
 namespace {
 
-// (mean / deviation, 1 / deviation, mean) of the team's row, so that a normalised
-// value is one fused multiply-add: v * y - x.
 struct RowStats {
-    float scaled_mean, rstd, mean;
+    float mean, rstd;
 };
 
-// Columns that the row does not have hold zero: they add nothing to a sum of
-// squares, but must not count about a mean.
+// Mean and 1 / deviation of the team's row.  Columns that the row does not have
+// hold zero: they add nothing to a sum of squares, but must not count about a mean.
 template <bool ALIGNED>
-__device__ __forceinline__ RowStats row_stats(const float (&v)[8], const Cols<ALIGNED> &c, int kind,
+__device__ __forceinline__ RowStats row_stats(const f32x2 (&v)[4], const Cols<ALIGNED> &c, int kind,
                                               const ResidualNormArgs &a, TeamSum &sum)
 {
-    if (kind == GBSSIM_ROW_NONE) return {0.0f, 1.0f, 0.0f};
-    float q[1] = {0.0f}, mean = 0.0f;
+    if (kind == GBSSIM_ROW_NONE) return {0.0f, 1.0f};
+    f32x2 q = 0;
+    float mean = 0.0f;
     if (kind == GBSSIM_ROW_LAYER) {
-        float s[1] = {0.0f};
+        mean = sum.one(sum2(add2(add2(v[0], v[1]), add2(v[2], v[3])))) * a.inv_dim;
+        const f32x2 m = both(-mean);
+        if (c.all()) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] += v[e];
-        sum(s);
-        mean = s[0] * a.inv_dim;
+            for (int e = 0; e < 4; ++e) {
+                const f32x2 d = add2(v[e], m);
+                q = fma2(d, d, q);
+            }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = c.has(e) ? v[e] - mean : 0.0f;
-            q[0] = fmaf(d, d, q[0]);
+            for (int e = 0; e < 8; ++e) {
+                const float2 h = halves(add2(v[e / 2], m));
+                const float d = c.has(e) ? (e & 1 ? h.y : h.x) : 0.0f;
+                q = fma2(pair(d, 0.0f), pair(d, 0.0f), q);
+            }
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[0] = fmaf(v[e], v[e], q[0]);
+        for (int e = 0; e < 4; ++e) q = fma2(v[e], v[e], q);
     }
-    sum(q);
-    const float rstd = rsqrtf(fmaf(q[0], a.inv_dim, a.eps));
-    return {mean * rstd, rstd, mean};
+    return {mean, rsqrtf(fmaf(sum.one(sum2(q)), a.inv_dim, a.eps))};
 }
 
 // BIAS: either norm has a bias.
@@ -50,36 +54,45 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
     using SR = Staged<R, ALIGNED>;
     using SY = Staged<Y, ALIGNED>;
     extern __shared__ uint4 ring[];
-    __shared__ float slots[2][2][16];
-    __shared__ float cluster_slots[2][2][4];
+    __shared__ float2 slots[2][16];
+    __shared__ float2 cluster_slots[2][4];
     const BlockRows rows(a);
     const Cols<ALIGNED> c(a, rows.shift);
     TeamSum sum{slots, cluster_slots, 0, a.plan.tpr, a.plan.teams > 1 ? 1 : a.plan.threads / 32,
                 a.plan.cluster};
     const int team = a.plan.teams > 1 ? int(threadIdx.x) / a.plan.tpr : 0;
-    const int threads = a.plan.threads, stages = a.plan.stages;
-    const int stage_words = (SR::kUnits + SY::kUnits * (a.gate_rows.p ? 2 : 1)) * threads;
-    uint4 *const mine = ring + threadIdx.x;
+    const int step = rows.step * a.plan.teams;  // rows from one of the team's to its next
+    const int pitch = a.plan.threads * 16, stages = a.plan.stages;
+    const bool has_y = a.y.p, has_gates = a.gate_rows.p;
+    const int stage_bytes = (SR::kUnits + SY::kUnits * (has_gates ? 2 : 1)) * pitch;
+    const unsigned mine = smem_u32(ring) + threadIdx.x * 16, over = mine + stages * stage_bytes;
     // no block writes into another's shared memory before that block runs
     if (a.plan.cluster > 1) cooperative_groups::this_cluster().sync();
 
-    const auto fetch = [&](int i, uint4 *slot) {
-        if (i < rows.count && c.any()) {
-            const int r = rows.first + i * rows.step;
-            SR::fetch(a.x, row_of<R>(a.x, a.tokens, r), c, slot, threads);
-            slot += SR::kUnits * threads;
-            if (a.y.p) SY::fetch(a.y, row_of<Y>(a.y, a.tokens, r), c, slot, threads);
-            slot += SY::kUnits * threads;
-            if (a.gate_rows.p)
-                SY::fetch(a.gate_rows, row_of<Y>(a.gate_rows, a.tokens, r), c, slot, threads);
+    int r = rows.first + team * rows.step, left = rows.count - team;  // the team's row; none if <= 0
+    int ahead = r, ahead_left = left;
+    unsigned to = mine;
+    const auto fetch = [&] {
+        if (ahead_left > 0 && c.any()) {
+            SR::fetch(a.x, row_at<R>(a.x, a.tokens, ahead, c.first), c, to, pitch);
+            if (has_y)
+                SY::fetch(a.y, row_at<Y>(a.y, a.tokens, ahead, c.first), c, to + SR::kUnits * pitch,
+                          pitch);
+            if (has_gates)
+                SY::fetch(a.gate_rows, row_at<Y>(a.gate_rows, a.tokens, ahead, c.first), c,
+                          to + (SR::kUnits + SY::kUnits) * pitch, pitch);
         }
         staged_commit();
+        ahead += step;
+        ahead_left -= a.plan.teams;
+        to += stage_bytes;
+        if (to == over) to = mine;
     };
-    for (int i = 0; i < stages - 1; ++i) fetch(i * a.plan.teams + team, mine + i * stage_words);
+    for (int i = 0; i < stages - 1; ++i) fetch();
 
     // post and gate of a column in one factor and one summand; a gate of its
     // own per row stays apart
-    float w1[8], b1[8], w2[8], b2[8];
+    f32x2 w1[4], b1[4], w2[4], b2[4];
     load_param(a.w1, rows.group, c, a.offset, 1.0f, w1);
     load_param(a.w2, rows.group, c, a.offset, 1.0f, w2);
     if (BIAS) {
@@ -87,61 +100,61 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
         load_param(a.b2, rows.group, c, 0.0f, 0.0f, b2);
     }
     if (a.gate.p) {
-        float g[8];
+        f32x2 g[4];
         load_param(a.gate, rows.group, c, 0.0f, 1.0f, g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w1[e] *= g[e];
-            if (BIAS) b1[e] *= g[e];
+        for (int e = 0; e < 4; ++e) {
+            w1[e] = mul2(w1[e], g[e]);
+            if (BIAS) b1[e] = mul2(b1[e], g[e]);
         }
     }
-    int now = 0;
+    const f32x2 scale = both(a.scale);
+    unsigned at = mine;
     // every team of the block takes part in every sum, with a row or without
-    for (int i0 = 0; i0 < rows.count; i0 += a.plan.teams) {
-        const int i = i0 + team, r = rows.first + i * rows.step;
-        const bool active = i < rows.count;
-        {
-            const int ahead = now == 0 ? stages - 1 : now - 1;
-            fetch(i + (stages - 1) * a.plan.teams, mine + ahead * stage_words);
-        }
+    for (int i = 0; i < rows.count; i += a.plan.teams) {
+        const bool active = left > 0;
+        fetch();
         staged_wait(stages);
-        const uint4 *slot = mine + now * stage_words;
-        now = now + 1 == stages ? 0 : now + 1;
-        float x[8];
-        SR::read(row_of<R>(a.x, a.tokens, r), c, active, slot, threads, x);
-        slot += SR::kUnits * threads;
-        RowStats s1 = {0.0f, 1.0f, 0.0f}, s2 = {0.0f, 1.0f, 0.0f};
-        if (a.y.p) {
-            float y[8];
-            SY::read(row_of<Y>(a.y, a.tokens, r), c, active, slot, threads, y);
+        f32x2 x[4];
+        SR::read(a.x, a.tokens, r, c, active, at, pitch, x);
+        RowStats s1 = {0.0f, 1.0f}, s2 = {0.0f, 1.0f};
+        if (has_y) {
+            f32x2 y[4];
+            SY::read(a.y, a.tokens, r, c, active, at + SR::kUnits * pitch, pitch, y);
             s1 = row_stats(y, c, a.post, a, sum);
+            const f32x2 v = both(s1.rstd), m = both(-s1.mean * s1.rstd);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float h = fmaf(y[e], s1.rstd, -s1.scaled_mean);
-                y[e] = BIAS ? fmaf(h, w1[e], b1[e]) : h * w1[e];
+            for (int e = 0; e < 4; ++e) {
+                y[e] = fma2(y[e], v, m);
+                y[e] = BIAS ? fma2(y[e], w1[e], b1[e]) : mul2(y[e], w1[e]);
             }
-            if (a.gate_rows.p) {
-                float g[8];
-                SY::read(row_of<Y>(a.gate_rows, a.tokens, r), c, active, slot + SY::kUnits * threads,
-                         threads, g);
+            if (has_gates) {
+                f32x2 g[4];
+                SY::read(a.gate_rows, a.tokens, r, c, active, at + (SR::kUnits + SY::kUnits) * pitch,
+                         pitch, g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] *= g[e];
+                for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], g[e]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = fmaf(a.scale, x[e], y[e]);
-            store_row(static_cast<R *>(a.x_out) + (long long)r * a.dim, c, active, x);
+            for (int e = 0; e < 4; ++e) x[e] = fma2(scale, x[e], y[e]);
+            store_cols(static_cast<R *>(a.x_out) + ((long long)r * a.dim + c.first), c, active, x);
         }
         if (a.u) {
             s2 = row_stats(x, c, a.pre, a, sum);
+            const f32x2 v = both(s2.rstd), m = both(-s2.mean * s2.rstd);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float h = fmaf(x[e], s2.rstd, -s2.scaled_mean);
-                x[e] = BIAS ? fmaf(h, w2[e], b2[e]) : h * w2[e];
+            for (int e = 0; e < 4; ++e) {
+                x[e] = fma2(x[e], v, m);
+                x[e] = BIAS ? fma2(x[e], w2[e], b2[e]) : mul2(x[e], w2[e]);
             }
-            store_row(static_cast<Y *>(a.u) + (long long)r * a.dim, c, active, x);
+            store_cols(static_cast<Y *>(a.u) + ((long long)r * a.dim + c.first), c, active, x);
         }
         if (a.stats && active && c.first <= 0 && c.any())
             a.stats[r] = make_float4(s1.mean, s1.rstd, s2.mean, s2.rstd);
+        r += step;
+        left -= a.plan.teams;
+        at += stage_bytes;
+        if (at == over) at = mine;
     }
 }
 
