@@ -10,6 +10,7 @@
 #include "gbssim.h"
 #include "api_host.cuh"
 #include "common.cuh"
+#include "residual_norm.cuh"
 #include "ssim2d.cuh"
 #include "ssim3d.cuh"
 
@@ -509,12 +510,14 @@ int gbssim_device_status(unsigned *flags_out)
 {
     if (!flags_out) return GBSSIM_EINVAL;
     *flags_out = 0;
-    unsigned f3 = 0;
-    const cudaError_t e = ssim2d_staging_status(flags_out, true);
-    if (e != cudaSuccess) return cuda_fail(e);
-    const cudaError_t e3 = ssim3d_staging_status(&f3, true);
-    *flags_out |= f3;
-    return cuda_fail(e3);
+    for (const auto status : {ssim2d_staging_status, ssim3d_staging_status, residual_norm_fwd_status,
+                              residual_norm_bwd_status}) {
+        unsigned f = 0;
+        const cudaError_t e = status(&f, true);
+        if (e != cudaSuccess) return cuda_fail(e);
+        *flags_out |= f;
+    }
+    return GBSSIM_OK;
 }
 
 size_t gbssim_workspace_bytes(int N, int C, int H, int W, int padding)

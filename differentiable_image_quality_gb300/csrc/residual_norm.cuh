@@ -12,6 +12,7 @@
 #include <cooperative_groups.h>
 
 #include "gbssim.h"
+#include "common.cuh"
 #include "dtypes.cuh"
 
 namespace gbssim {
@@ -49,7 +50,6 @@ struct ParamPtr {
 struct RowPlan {
     int aligned;       // rows start on 16-byte boundaries in every tensor
     int classes;       // 8 / gcd(8, D); 1 also where a group has too few rows to part
-    int stages;        // rows of each thread in flight
     int cluster;       // blocks of a cluster (1, 2, 4)
     int block_cols;    // columns of a block: a multiple of 8 (counted from the shift)
     int tpr;           // threads of a team in a block
@@ -66,6 +66,7 @@ struct ResidualNormArgs {
     int post, pre;     // gbssim_row_norm
     float scale, offset, eps, inv_dim;
     RowPlan plan;
+    unsigned exchange_extra;  // test hook: see TeamSum
     // forward
     void *x_out, *u;
     float4 *stats;     // (m1, r1, m2, r2) of each row
@@ -85,9 +86,18 @@ struct ParamGrads {
     ParamGrad gate, w1, b1, w2, b2;
 };
 
+// How many clusters of 2 and of 4 blocks the current device holds at one block an SM.
+struct ClusterRoom {
+    int of2, of4;
+};
+cudaError_t residual_norm_cluster_room(ClusterRoom *room);
+
 cudaError_t residual_norm_fwd_launch(const ResidualNormArgs &a, int res, int blk, cudaStream_t s);
 cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk,
                                      const ParamGrads &g, cudaStream_t s);
+// Kernel-side failures on the current device since the last call that cleared them.
+cudaError_t residual_norm_fwd_status(unsigned *flags, bool clear);
+cudaError_t residual_norm_bwd_status(unsigned *flags, bool clear);
 
 #ifdef __CUDACC__
 
@@ -96,10 +106,10 @@ cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk
 struct BlockRows {
     int group, first, count, step;
     int shift;  // columns that the class's rows start past a multiple of eight elements
-    __device__ __forceinline__ BlockRows(const ResidualNormArgs &a)
+    __device__ __forceinline__ BlockRows(const ResidualNormArgs &a, int cluster)
     {
         const RowPlan &p = a.plan;
-        const int item = int(blockIdx.x) / p.cluster;
+        const int item = int(blockIdx.x) / cluster;
         const int cls = item / p.splits, split = item - cls * p.splits;
         group = cls / p.classes;
         const int k = cls - group * p.classes;
@@ -120,9 +130,9 @@ template <bool ALIGNED>
 struct Cols {
     int first, from, upto;
     int t;  // place in the team
-    __device__ __forceinline__ Cols(const ResidualNormArgs &a, int shift)
+    __device__ __forceinline__ Cols(const ResidualNormArgs &a, int cluster, int shift)
     {
-        const int rank = a.plan.cluster > 1 ? int(blockIdx.x) % a.plan.cluster : 0;
+        const int rank = int(blockIdx.x) % cluster;
         t = a.plan.teams > 1 ? threadIdx.x & (a.plan.tpr - 1) : threadIdx.x;
         first = rank * a.plan.block_cols + t * kColsPerThread - (ALIGNED ? 0 : shift);
         from = max(0, -first);
@@ -136,12 +146,12 @@ struct Cols {
     }
 };
 
-// Column `col` of row r of a tensor.
-template <typename T>
+// Column `col` of row r of a tensor; ANY: of one whose rows may need two strides.
+template <typename T, bool ANY>
 __device__ __forceinline__ const unsigned char *row_at(const RowPtr &p, int tokens, int r, int col)
 {
     const unsigned char *base = static_cast<const unsigned char *>(p.p) + col * int(sizeof(T));
-    if (tokens == 0) return base + (long long)r * p.row_bytes;
+    if (!ANY || tokens == 0) return base + (long long)r * p.row_bytes;
     const int b = r / tokens, t = r - b * tokens;
     return base + (b * p.sb + t * p.st) * int(sizeof(T));
 }
@@ -152,9 +162,9 @@ __device__ __forceinline__ const unsigned char *row_at(const RowPtr &p, int toke
 //
 // Where a tensor's rows are not aligned as the block's columns are, a thread
 // copies the aligned words that its columns lie in -- one more than they fill --
-// and shifts.  A word that reaches over the tensor's first or last element is
-// put together from single elements.
-template <typename T, bool ALIGNED>
+// and shifts.  Near the tensor's first and last element the words are put
+// together from single elements instead: nothing outside the tensor is read.
+template <typename T, bool ALIGNED, bool ANY>
 struct Staged {
     static constexpr int kUnits = (sizeof(T) == 4 ? 2 : 1) + (ALIGNED ? 0 : 1);
 
@@ -166,15 +176,19 @@ struct Staged {
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) copy16_async<false>(slot + u * pitch, at + u * 16);
         } else {
-            const unsigned char *from = at + c.from * int(sizeof(T));
-            const unsigned char *stop = at + c.upto * int(sizeof(T));
             const unsigned char *word = at - (reinterpret_cast<uintptr_t>(at) & 15);
+            if (c.all() && word == at) {
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u, word += 16, slot += pitch) {
-                if (word >= stop || word + 16 <= from) continue;
-                if (word >= p.p && word + 16 <= p.end) {
-                    copy16_async<true>(slot, word);
-                } else {
+                for (int u = 0; u < kUnits - 1; ++u) copy16_async<false>(slot + u * pitch, at + u * 16);
+            } else if (word >= p.p && word + 16 * kUnits <= p.end) {
+                // the ends of the row before and after, where they come along, are not looked at
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) copy16_async<true>(slot + u * pitch, word + u * 16);
+            } else {
+                const unsigned char *from = at + c.from * int(sizeof(T));
+                const unsigned char *stop = at + c.upto * int(sizeof(T));
+#pragma unroll 1
+                for (int u = 0; u < kUnits; ++u, word += 16, slot += pitch) {
                     T *to = static_cast<T *>(__cvta_shared_to_generic(slot));
 #pragma unroll 1
                     for (int i = 0; i < 16; i += int(sizeof(T)))
@@ -199,7 +213,7 @@ struct Staged {
             unpack8<T>(r, v);
         } else {
             if (active && c.any()) {
-                const int s = int(reinterpret_cast<uintptr_t>(row_at<T>(p, tokens, row, c.first)) & 15) /
+                const int s = int(reinterpret_cast<uintptr_t>(row_at<T, ANY>(p, tokens, row, c.first)) & 15) /
                               int(sizeof(T));
                 if (s == 0) {
 #pragma unroll
@@ -232,13 +246,11 @@ __device__ __forceinline__ void staged_commit()
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// Waits until at most stages - 1 of this thread's latest groups are in flight.
-__device__ __forceinline__ void staged_wait(int stages)
+// Waits until at most PENDING of this thread's latest groups are in flight.
+template <int PENDING>
+__device__ __forceinline__ void staged_wait()
 {
-    if (stages >= 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
 // Stores the thread's columns of a row, the first at `to`: in whole words where
@@ -290,58 +302,145 @@ __device__ __forceinline__ void load_param(const ParamPtr &p, int group, const C
     for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
 }
 
+// ------------------------------------------------------ sums over a team
+
+__device__ __forceinline__ unsigned peer_address(unsigned shared, int rank)
+{
+    unsigned r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(shared), "r"(rank));
+    return r;
+}
+
+// Writes two floats to a block of the cluster and counts them on its barrier.
+__device__ __forceinline__ void send8(unsigned to, float2 v, unsigned bar)
+{
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
+        "f"(v.x), "f"(v.y), "r"(bar)
+        : "memory");
+}
+
+// What the warps of a block tell one another, and the blocks of a cluster: every
+// block sends its sums to all, as bytes that the receiver's barrier counts.  (A
+// cluster-wide barrier would first wait for the rows that the blocks have just
+// stored.)
+struct TeamSlots {
+    float warps[2][2][16];     // [parity][value][warp]
+    float2 blocks[2][4];       // [parity][block]
+    uint64_t arrived[2];
+    float columns[16];         // of each warp
+    float block_columns[4];
+};
+
+// About a second: an exchange that takes longer has failed.
+constexpr long long kExchangeCycles = 2000000000ll;
+
+// Kernel-side failures of this file's kernels (bit 1: an exchange ran out of time).
+static __device__ unsigned g_exchange_status;
+
 // Sums over a team, of one value or of two.  All threads of a block call together.
+// CLUSTER: a row may be shared by blocks of a cluster.
+template <bool CLUSTER>
 struct TeamSum {
-    float2 (*slots)[16];         // [2][warp]
-    float2 (*cluster_slots)[4];  // [2][block of the cluster]
+    TeamSlots &slots;
     int parity, tpr, warps, cluster;
+    unsigned phases;      // of arrived[0] and arrived[1], one bit each
+    unsigned extra;       // test hook: bytes announced beyond those sent (0)
+    bool dead;            // an exchange ran out of time: wait for no other
+    float inv_columns;    // 1 / columns of the team's lanes in this warp (count_columns)
+
+    __device__ __forceinline__ TeamSum(TeamSlots &s, const ResidualNormArgs &a)
+        : slots(s), parity(0), tpr(a.plan.tpr), warps(a.plan.teams > 1 ? 1 : a.plan.threads / 32),
+          cluster(CLUSTER ? a.plan.cluster : 1), phases(0), extra(a.exchange_extra), dead(false), inv_columns(0.0f)
+    {
+        if (cluster == 1) return;
+        if (threadIdx.x == 0) {
+            mbar_init(&slots.arrived[0], 1);
+            mbar_init(&slots.arrived[1], 1);
+            mbar_init_fence();
+        }
+        cooperative_groups::this_cluster().sync();  // before anyone sends
+    }
+
+    // Sum over the team's lanes of this warp.
+    __device__ __forceinline__ float lanes(float v) const
+    {
+        if (tpr < 32) {
+#pragma unroll 1
+            for (int o = tpr >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            return v;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+
+    // Sum over 16 lanes that hold the warps' values.
+    __device__ __forceinline__ float sixteen(float v) const
+    {
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+
+    // The warps' values a (and b), one warp to each lane of a half warp.  One
+    // barrier: the slots alternate, and a thread that writes a slot again has
+    // passed the barrier of the sum in between, which every thread reaches only
+    // after it has read this one.
+    __device__ __forceinline__ float2 of_warps(float a, float b, bool two)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (lane == 0) {
+            slots.warps[parity][0][warp] = a;
+            if (two) slots.warps[parity][1][warp] = b;
+        }
+        __syncthreads();
+        float2 v = make_float2(0.0f, 0.0f);
+        if ((lane & 15) < warps) {
+            v.x = slots.warps[parity][0][lane & 15];
+            if (two) v.y = slots.warps[parity][1][lane & 15];
+        }
+        return v;
+    }
+
+    // This block's values to all blocks, and all blocks' into slots.blocks.  A
+    // block sends its next values only after its threads have read all of these,
+    // and nobody gets further than one exchange ahead of the others: two sets of
+    // slots are enough.
+    __device__ __forceinline__ void exchange(float2 v)
+    {
+        uint64_t *bar = &slots.arrived[parity];
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, unsigned(cluster) * 8u + extra);
+        if (int(threadIdx.x) < cluster) {
+            const int rank = int(cooperative_groups::this_cluster().block_rank());
+            send8(peer_address(smem_u32(&slots.blocks[parity][rank]), threadIdx.x), v,
+                  peer_address(smem_u32(bar), threadIdx.x));
+        }
+        if (!dead && !mbar_wait_bounded(bar, (phases >> parity) & 1u, kExchangeCycles)) {
+            dead = true;
+            atomicOr(&g_exchange_status, 2u);
+        }
+        phases ^= 1u << parity;
+    }
 
     template <int N>
     __device__ __forceinline__ void operator()(float (&v)[N])
     {
-        if (tpr < 32) {
-#pragma unroll 1
-            for (int o = tpr >> 1; o > 0; o >>= 1)
 #pragma unroll
-                for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-            return;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-        if (warps == 1) return;
-        // one barrier a sum: the slots alternate, and a thread that writes a
-        // slot again has passed the barrier of the sum in between, which every
-        // thread reaches only after it has read this one
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        float2 *const mine = slots[parity];
-        if (lane == 0) {
-            mine[warp].x = v[0];
-            if (N == 2) mine[warp].y = v[N - 1];
-        }
-        __syncthreads();
-        float2 got = make_float2(0.0f, 0.0f);
-        if ((lane & 15) < warps) got = mine[lane & 15];
-        v[0] = got.x;
-        if (N == 2) v[N - 1] = got.y;
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-            for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        for (int k = 0; k < N; ++k) v[k] = lanes(v[k]);
+        if (warps == 1 && cluster == 1) return;
+        const float2 w = of_warps(v[0], v[N - 1], N == 2);
+        v[0] = sixteen(w.x);
+        if (N == 2) v[N - 1] = sixteen(w.y);
         if (cluster > 1) {
-            namespace cg = cooperative_groups;
-            cg::cluster_group cl = cg::this_cluster();
-            if (int(threadIdx.x) < cluster)
-                cl.map_shared_rank(&cluster_slots[parity][0], threadIdx.x)[cl.block_rank()] =
-                    make_float2(v[0], v[N - 1]);
-            cl.sync();
-            v[0] = v[N - 1] = 0.0f;
+            exchange(make_float2(v[0], v[N - 1]));
+            float2 s = make_float2(0.0f, 0.0f);
             for (int r = 0; r < cluster; ++r) {
-                const float2 c = cluster_slots[parity][r];
-                v[0] += c.x;
-                if (N == 2) v[N - 1] += c.y;
+                s.x += slots.blocks[parity][r].x;
+                s.y += slots.blocks[parity][r].y;
             }
+            v[0] = s.x;
+            if (N == 2) v[N - 1] = s.y;
         }
         parity ^= 1;
     }
@@ -352,23 +451,95 @@ struct TeamSum {
         (*this)(a);
         return a[0];
     }
+
+    // Once, before join_squares: how many columns the lanes, warps and blocks have.
+    __device__ __forceinline__ void count_columns(int mine)
+    {
+        const float n = lanes(float(max(0, mine)));
+        inv_columns = n > 0.0f ? 1.0f / n : 0.0f;
+        if (warps == 1 && cluster == 1) return;
+        const int lane = threadIdx.x & 31;
+        const float2 w = of_warps(n, 0.0f, false);
+        if (threadIdx.x < 16) slots.columns[lane] = w.x;
+        const float block = sixteen(w.x);
+        if (cluster > 1) {
+            exchange(make_float2(block, 0.0f));
+            if (int(threadIdx.x) < cluster) slots.block_columns[lane] = slots.blocks[parity][lane].x;
+        }
+        parity ^= 1;
+        __syncthreads();
+    }
+
+    // From the sum s of the team's columns in this warp and the sum q of their
+    // squares about their own mean: the row's sum, and its squares about its mean.
+    // With n columns of mean m = s / n apiece, q joins as q + n (m - row mean)^2.
+    __device__ __forceinline__ float2 join_squares(float s, float q, float inv_dim)
+    {
+        if (warps == 1 && cluster == 1) return make_float2(s, q);
+        const int lane = threadIdx.x & 31;
+        const float2 w = of_warps(s, q, true);
+        const float n = (lane & 15) < warps ? slots.columns[lane & 15] : 0.0f;
+        const float block = sixteen(w.x);
+        // about the block's mean (the row's, where one block has all of it)
+        const float all = cluster > 1 ? sixteen(n) : 0.0f;
+        const float mean = cluster > 1 ? (all > 0.0f ? block / all : 0.0f) : block * inv_dim;
+        const float d = n > 0.0f ? w.x / n - mean : 0.0f;
+        float2 r = make_float2(block, sixteen(fmaf(n * d, d, w.y)));
+        if (cluster > 1) {
+            exchange(r);
+            float total = 0.0f;
+            for (int k = 0; k < cluster; ++k) total += slots.blocks[parity][k].x;
+            const float row = total * inv_dim;
+            r = make_float2(total, 0.0f);
+            for (int k = 0; k < cluster; ++k) {
+                const float2 v = slots.blocks[parity][k];
+                const float nk = slots.block_columns[k], dk = nk > 0.0f ? v.x / nk - row : 0.0f;
+                r.y += fmaf(nk * dk, dk, v.y);
+            }
+        }
+        parity ^= 1;
+        return r;
+    }
+
+    // No block leaves while another might still send to it.
+    __device__ __forceinline__ void finish()
+    {
+        if (cluster > 1) cooperative_groups::this_cluster().sync();
+    }
 };
 
-// Launches a kernel with its ring of staged rows: as many stages as leave
-// `per_sm` blocks of the largest team (or as many threads of smaller ones) room
-// on an SM, one at least.
-template <class Kernel>
-cudaError_t launch_staged(Kernel kernel, ResidualNormArgs &a, int units, int per_sm, cudaStream_t s)
+// The flags of this file's kernels on the current device; clear: and zero them.
+inline cudaError_t exchange_status(unsigned *flags, bool clear)
 {
-    constexpr int kSmemPerSm = 200 * 1024, kMaxStages = 4, kMaxBlockSmem = 220 * 1024;
-    const int stage = units * 16 * a.plan.threads;
-    const int blocks = per_sm * kMaxTeamThreads / a.plan.threads;
-    a.plan.stages = std::max(1, std::min(kMaxStages, kSmemPerSm / (stage * blocks)));
-    const int smem = a.plan.stages * stage;
+    cudaError_t e = cudaMemcpyFromSymbol(flags, g_exchange_status, sizeof(unsigned));
+    if (e == cudaSuccess && clear && *flags) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(g_exchange_status, &zero, sizeof(unsigned));
+    }
+    return e;
+}
+
+// Shared memory of an SM that rings of staged rows share.
+constexpr int kStagedSmem = 200 * 1024, kStagedBlock = 220 * 1024;
+
+// The stages of a ring of staged rows, of `units` 16-byte words a thread each: as
+// many (up to four) as leave room for `per_sm` blocks of 512 threads, or as many
+// threads of smaller ones, on an SM.
+constexpr int stages_of(int units, int per_sm)
+{
+    const int fit = kStagedSmem / (units * 16 * 512 * per_sm);
+    return fit < 1 ? 1 : fit > 4 ? 4 : fit;
+}
+
+template <class Kernel>
+cudaError_t launch_staged(Kernel kernel, const ResidualNormArgs &a, int units, int stages,
+                          cudaStream_t s)
+{
+    const int smem = stages * units * 16 * a.plan.threads;
     if (smem > 40 * 1024) {  // with the static arrays: above what needs no asking for
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kMaxBlockSmem);
+                                                   kStagedBlock);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

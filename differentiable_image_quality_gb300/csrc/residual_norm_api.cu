@@ -1,6 +1,7 @@
 // Entry points of the residual norm: argument checks and launch planning.
 #include <algorithm>
 #include <climits>
+#include <mutex>
 
 #include "api_host.cuh"
 #include "residual_norm.cuh"
@@ -122,7 +123,39 @@ bool inputs_aligned(const gbssim_residual_norm &d)
 // Resident threads of an SM that a plan counts on (64 or 128 registers each).
 constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512;
 
-RowPlan make_plan(const gbssim_residual_norm &d, int threads_per_sm, int sm_count)
+// SMs that a plan counts on at most: bounds the partial sums on any device.
+constexpr int kMaxPlanSms = 256;
+
+// What a plan has to know of the device.
+struct Room {
+    int sms, clusters2, clusters4;
+};
+
+// Read once per device.
+int device_room(Room *out)
+{
+    constexpr int kMost = 64;
+    static std::mutex mutex;
+    static Room known[kMost];
+    int dev = 0, sms = 0;
+    cudaError_t e = current_sm_count(&sms, &dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    std::lock_guard<std::mutex> lock(mutex);
+    Room fresh{}, &r = dev < kMost ? known[dev] : fresh;
+    if (r.sms == 0) {
+        ClusterRoom c{};
+        e = residual_norm_cluster_room(&c);
+        if (e != cudaSuccess) return cuda_fail(e);
+        if (c.of2 < 1 || c.of4 < 1) return cuda_fail(cudaErrorInvalidConfiguration);
+        r = {std::min(sms, kMaxPlanSms), std::min(c.of2, kMaxPlanSms / 2), std::min(c.of4, kMaxPlanSms / 4)};
+    }
+    *out = r;
+    return GBSSIM_OK;
+}
+
+// Blocks are planned to run all at once: a block works through its rows in a
+// loop, so that any left over would double the time.
+RowPlan make_plan(const gbssim_residual_norm &d, int threads_per_sm, const Room &room)
 {
     RowPlan p{};
     bool own = false;
@@ -150,7 +183,9 @@ RowPlan make_plan(const gbssim_residual_norm &d, int threads_per_sm, int sm_coun
         p.teams = 1;
     }
     if (rows == 0) return p;
-    const long long blocks = (long long)sm_count * (threads_per_sm / p.threads) / p.cluster;
+    const long long blocks =
+        (long long)(p.cluster == 4 ? room.clusters4 : p.cluster == 2 ? room.clusters2 : room.sms) *
+        (threads_per_sm / p.threads);
     const long long items = (long long)p.groups * p.classes;
     p.splits = int(std::max<long long>(
         1, std::min<long long>(ceil_div(blocks, items),
@@ -221,9 +256,7 @@ int wanted_sums(const gbssim_residual_norm &d, const gbssim_residual_norm_grads 
     return n;
 }
 
-// SMs that a backward plans for at most: bounds the partial sums on any device.
-constexpr int kMaxPlanSms = 256;
-constexpr int kMaxSums = 4;
+constexpr int kMaxSums = 4;  // of a backward's partials
 
 }  // namespace
 
@@ -254,11 +287,10 @@ extern "C" int gbssim_residual_norm_fwd(const gbssim_residual_norm *d, void *x_o
         for (int j = 0; j < i; ++j)
             if (out[j].p && meet(out[i], out[j])) return GBSSIM_EINVAL;
     }
-    int sm_count = 0;
-    const cudaError_t e = current_sm_count(&sm_count);
-    if (e != cudaSuccess) return cuda_fail(e);
+    Room room{};
+    if ((rc = device_room(&room))) return rc;
     ResidualNormArgs a = make_args(*d);
-    a.plan = make_plan(*d, kFwdThreadsPerSm, sm_count);
+    a.plan = make_plan(*d, kFwdThreadsPerSm, room);
     if (!grid_fits(a.plan)) return GBSSIM_ESHAPE;
     a.plan.aligned = inputs_aligned(*d) && multiple16(x_out_or_null) && multiple16(u_or_null);
     a.tokens = one_stride(*d, d->x) && one_stride(*d, d->y) && one_stride(*d, d->gate_rows)
@@ -274,7 +306,7 @@ extern "C" int gbssim_residual_norm_fwd(const gbssim_residual_norm *d, void *x_o
 extern "C" size_t gbssim_residual_norm_workspace_bytes(const gbssim_residual_norm *d)
 {
     if (check_desc(d) != GBSSIM_OK || row_count(*d) == 0) return 0;
-    const RowPlan p = make_plan(*d, kBwdThreadsPerSm, kMaxPlanSms);
+    const RowPlan p = make_plan(*d, kBwdThreadsPerSm, {kMaxPlanSms, kMaxPlanSms / 2, kMaxPlanSms / 4});
     return size_t(p.groups) * p.classes * p.splits * kMaxSums * d->dim * sizeof(float);
 }
 
@@ -338,13 +370,12 @@ extern "C" int gbssim_residual_norm_bwd(const gbssim_residual_norm *d,
             if (meet(out[i], out[j])) return GBSSIM_EINVAL;
     }
 
-    int sm_count = 0;
-    const cudaError_t e = current_sm_count(&sm_count);
-    if (e != cudaSuccess) return cuda_fail(e);
+    Room room{};
+    if ((rc = device_room(&room))) return rc;
     ResidualNormArgs a = make_args(*d);
     a.gx = row_ptr(*d, gx, d->res_dtype);
     a.gu = row_ptr(*d, gu, d->blk_dtype);
-    a.plan = make_plan(*d, kBwdThreadsPerSm, std::min(sm_count, kMaxPlanSms));
+    a.plan = make_plan(*d, kBwdThreadsPerSm, room);
     if (!grid_fits(a.plan)) return GBSSIM_ESHAPE;
     a.plan.aligned = inputs_aligned(*d) && rows_aligned(*d, gx, d->res_dtype) &&
                      rows_aligned(*d, gu, d->blk_dtype) && multiple16(grads->x) &&

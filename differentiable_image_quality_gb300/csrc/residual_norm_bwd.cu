@@ -16,11 +16,23 @@
 // block, and a second kernel adds the partials in a fixed order.
 #include <algorithm>
 
-#include "common.cuh"
 #include "residual_norm.cuh"
 
 namespace gbssim {
 namespace {
+
+// 16-byte words a thread stages of a row: x, G, y, V and a gate per row.
+template <typename R, typename Y, bool ALIGNED, bool FULL>
+constexpr int bwd_units()
+{
+    return 2 * Staged<R, ALIGNED, true>::kUnits + (FULL ? 3 : 2) * Staged<Y, ALIGNED, true>::kUnits;
+}
+
+template <typename R, typename Y, bool ALIGNED, bool FULL>
+constexpr int bwd_stages()
+{
+    return stages_of(bwd_units<R, Y, ALIGNED, FULL>(), 1);
+}
 
 // One column sum of the block to its partial: over the block's teams first.
 template <bool ALIGNED>
@@ -62,46 +74,49 @@ __device__ __forceinline__ void write_sum(const ResidualNormArgs &a, const Cols<
         if (c.has(e)) dst[c.first + e] = v[e];
 }
 
-// FULL: a gate of its own per row.  BIAS: either norm has a bias.
-template <typename R, typename Y, bool ALIGNED, bool FULL, bool BIAS>
+// FULL: a gate of its own per row.  LAYER: a norm may subtract the mean or have
+// a bias.  ANY: whatever a call may ask for; without it all four inputs and both
+// outputs are there, one stride reaches every row, and a block has whole rows.
+template <typename R, typename Y, bool ALIGNED, bool FULL, bool LAYER, bool ANY>
 __global__ void __launch_bounds__(kMaxTeamThreads, 1)
     residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a)
 {
-    using SR = Staged<R, ALIGNED>;
-    using SY = Staged<Y, ALIGNED>;
+    using SR = Staged<R, ALIGNED, ANY>;
+    using SY = Staged<Y, ALIGNED, ANY>;
+    constexpr int kStages = bwd_stages<R, Y, ALIGNED, FULL>();
     extern __shared__ uint4 ring[];
-    __shared__ float2 slots[2][16];
-    __shared__ float2 cluster_slots[2][4];
+    __shared__ TeamSlots slots;
     __shared__ float scratch[kSmallBlock * 8];
-    const BlockRows rows(a);
-    const Cols<ALIGNED> c(a, rows.shift);
-    TeamSum sum{slots, cluster_slots, 0, a.plan.tpr, a.plan.teams > 1 ? 1 : a.plan.threads / 32,
-                a.plan.cluster};
+    if (a.sums) pdl_trigger();  // the kernel that adds the partials waits for all of this one
+    const int cluster = ANY ? a.plan.cluster : 1;
+    const BlockRows rows(a, cluster);
+    const Cols<ALIGNED> c(a, cluster, rows.shift);
+    TeamSum<ANY> sum(slots, a);
     const int team = a.plan.teams > 1 ? int(threadIdx.x) / a.plan.tpr : 0;
     const int step = rows.step * a.plan.teams;  // rows from one of the team's to its next
-    const int pitch = a.plan.threads * 16, stages = a.plan.stages;
-    const bool has_y = a.y.p, has_gx = a.gx.p, has_gu = a.gu.p;
+    const int pitch = a.plan.threads * 16;
+    const bool has_y = !ANY || a.y.p, has_gx = !ANY || a.gx.p, has_gu = !ANY || a.gu.p;
+    const bool wants_x = !ANY || a.dx, wants_y = !ANY || a.dy, wants_g = FULL && a.dgate_rows;
     // the words of a stage: x, G, y, V, gate
     const int at_gx = SR::kUnits * pitch, at_y = 2 * at_gx, at_gu = at_y + SY::kUnits * pitch,
               at_gate = at_gu + SY::kUnits * pitch;
-    const int stage_bytes = at_gate + (FULL ? SY::kUnits * pitch : 0);
-    const unsigned mine = smem_u32(ring) + threadIdx.x * 16, over = mine + stages * stage_bytes;
-    // no block writes into another's shared memory before that block runs
-    if (a.plan.cluster > 1) cooperative_groups::this_cluster().sync();
+    const int stage_bytes = bwd_units<R, Y, ALIGNED, FULL>() * pitch;
+    const unsigned mine = smem_u32(ring) + threadIdx.x * 16, over = mine + kStages * stage_bytes;
 
     int r = rows.first + team * rows.step, left = rows.count - team;  // the team's row; none if <= 0
-    int ahead = r, ahead_left = left;
+    int ahead = r, ahead_left = c.any() ? left : 0;
     unsigned to = mine;
     const auto fetch = [&] {
-        if (ahead_left > 0 && c.any()) {
-            SR::fetch(a.x, row_at<R>(a.x, a.tokens, ahead, c.first), c, to, pitch);
+        if (ahead_left > 0) {
+            SR::fetch(a.x, row_at<R, ANY>(a.x, a.tokens, ahead, c.first), c, to, pitch);
             if (has_gx)
-                SR::fetch(a.gx, row_at<R>(a.gx, a.tokens, ahead, c.first), c, to + at_gx, pitch);
-            if (has_y) SY::fetch(a.y, row_at<Y>(a.y, a.tokens, ahead, c.first), c, to + at_y, pitch);
+                SR::fetch(a.gx, row_at<R, ANY>(a.gx, a.tokens, ahead, c.first), c, to + at_gx, pitch);
+            if (has_y)
+                SY::fetch(a.y, row_at<Y, ANY>(a.y, a.tokens, ahead, c.first), c, to + at_y, pitch);
             if (has_gu)
-                SY::fetch(a.gu, row_at<Y>(a.gu, a.tokens, ahead, c.first), c, to + at_gu, pitch);
+                SY::fetch(a.gu, row_at<Y, ANY>(a.gu, a.tokens, ahead, c.first), c, to + at_gu, pitch);
             if (FULL)
-                SY::fetch(a.gate_rows, row_at<Y>(a.gate_rows, a.tokens, ahead, c.first), c,
+                SY::fetch(a.gate_rows, row_at<Y, ANY>(a.gate_rows, a.tokens, ahead, c.first), c,
                           to + at_gate, pitch);
         }
         staged_commit();
@@ -110,19 +125,19 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
         to += stage_bytes;
         if (to == over) to = mine;
     };
-    for (int i = 0; i < stages - 1; ++i) fetch();
+    for (int i = 0; i < kStages - 1; ++i) fetch();
 
     f32x2 w1[4], b1[4], w2[4];  // with the gate of the column in w1 and b1, unless FULL
     load_param(a.w1, rows.group, c, a.offset, 1.0f, w1);
     load_param(a.w2, rows.group, c, a.offset, 1.0f, w2);
-    if (BIAS) load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
+    if (LAYER) load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
     if (!FULL && a.gate.p) {
         f32x2 g[4];
         load_param(a.gate, rows.group, c, 0.0f, 1.0f, g);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             w1[e] = mul2(w1[e], g[e]);
-            if (BIAS) b1[e] = mul2(b1[e], g[e]);
+            if (LAYER) b1[e] = mul2(b1[e], g[e]);
         }
     }
     const f32x2 scale = both(a.scale);
@@ -136,7 +151,7 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
         float4 st = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
         if (active) st = a.stats[r];
         fetch();
-        staged_wait(stages);
+        staged_wait<kStages - 1>();
 
         f32x2 yh[4], xh[4], T[4], g[4];
         SR::read(a.x, a.tokens, r, c, active, at, pitch, xh);
@@ -146,8 +161,8 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
             const f32x2 v = both(st.y), m = both(-st.x * st.y);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                yh[e] = fma2(yh[e], v, m);
-                f32x2 z = BIAS ? fma2(yh[e], w1[e], b1[e]) : mul2(yh[e], w1[e]);
+                yh[e] = LAYER ? fma2(yh[e], v, m) : mul2(yh[e], v);
+                f32x2 z = LAYER ? fma2(yh[e], w1[e], b1[e]) : mul2(yh[e], w1[e]);
                 if (FULL) z = mul2(z, g[e]);
                 xh[e] = fma2(scale, xh[e], z);
             }
@@ -164,14 +179,14 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
             const f32x2 v = both(st.w), m = both(-st.z * st.w);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                xh[e] = fma2(xh[e], v, m);
+                xh[e] = LAYER ? fma2(xh[e], v, m) : mul2(xh[e], v);
                 sc[e] = fma2(V[e], xh[e], sc[e]);
-                if (BIAS) se[e] = add2(se[e], V[e]);
+                if (LAYER) se[e] = add2(se[e], V[e]);
                 V[e] = mul2(V[e], w2[e]);
                 q = fma2(V[e], xh[e], q);
             }
             float d[2] = {sum2(q), 0.0f};
-            if (a.pre == GBSSIM_ROW_LAYER) {
+            if (LAYER && a.pre == GBSSIM_ROW_LAYER) {
                 d[1] = sum2(add2(add2(V[0], V[1]), add2(V[2], V[3])));
                 sum(d);
             } else {
@@ -180,20 +195,20 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
             // T += r2 (dx^ - mean(dx^) - x^ mean(dx^ x^))
             const f32x2 d0 = both(-d[0] * a.inv_dim), d1 = both(-d[1] * a.inv_dim);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) T[e] = fma2(v, fma2(xh[e], d0, add2(V[e], d1)), T[e]);
+            for (int e = 0; e < 4; ++e) T[e] = fma2(v, fma2(xh[e], d0, LAYER ? add2(V[e], d1) : V[e]), T[e]);
         }
-        if (a.dx) {
+        if (wants_x) {
             f32x2 dx[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) dx[e] = has_y ? mul2(scale, T[e]) : T[e];
             store_cols(static_cast<R *>(a.dx) + ((long long)r * a.dim + c.first), c, active, dx);
         }
         if (has_y) {
-            if (FULL && a.dgate_rows) {
+            if (wants_g) {
                 f32x2 dg[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    dg[e] = mul2(T[e], BIAS ? fma2(yh[e], w1[e], b1[e]) : mul2(yh[e], w1[e]));
+                    dg[e] = mul2(T[e], LAYER ? fma2(yh[e], w1[e], b1[e]) : mul2(yh[e], w1[e]));
                 store_cols(static_cast<Y *>(a.dgate_rows) + ((long long)r * a.dim + c.first), c, active, dg);
             }
             f32x2 q = 0;
@@ -201,13 +216,13 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
             for (int e = 0; e < 4; ++e) {
                 if (FULL) T[e] = mul2(T[e], g[e]);
                 sa[e] = fma2(T[e], yh[e], sa[e]);
-                if (BIAS) sf[e] = add2(sf[e], T[e]);
+                if (LAYER) sf[e] = add2(sf[e], T[e]);
                 T[e] = mul2(T[e], w1[e]);
                 q = fma2(T[e], yh[e], q);
             }
-            if (a.dy) {
+            if (wants_y) {
                 float d[2] = {sum2(q), 0.0f};
-                if (a.post == GBSSIM_ROW_LAYER) {
+                if (LAYER && a.post == GBSSIM_ROW_LAYER) {
                     d[1] = sum2(add2(add2(T[0], T[1]), add2(T[2], T[3])));
                     sum(d);
                 } else {
@@ -215,7 +230,7 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
                 }
                 const f32x2 v = both(st.y), d0 = both(-d[0] * a.inv_dim), d1 = both(-d[1] * a.inv_dim);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) T[e] = mul2(v, fma2(yh[e], d0, add2(T[e], d1)));
+                for (int e = 0; e < 4; ++e) T[e] = mul2(v, fma2(yh[e], d0, LAYER ? add2(T[e], d1) : T[e]));
                 store_cols(static_cast<Y *>(a.dy) + ((long long)r * a.dim + c.first), c, active, T);
             }
         }
@@ -224,9 +239,10 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
         at += stage_bytes;
         if (at == over) at = mine;
     }
+    sum.finish();
     write_sum(a, c, a.sum_a, sa, scratch);
     write_sum(a, c, a.sum_c, sc, scratch);
-    if (BIAS) {
+    if (LAYER) {
         write_sum(a, c, a.sum_f, sf, scratch);
         write_sum(a, c, a.sum_e, se, scratch);
     }
@@ -234,7 +250,7 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
 
 // ------------------------------------------------------- the parameters' gradients
 
-constexpr int kFinishCols = 32, kFinishLanes = 32;
+constexpr int kFinishCols = 8, kFinishLanes = 64;
 
 __device__ __forceinline__ void store_param(const ParamGrad &g, int group, int dim, int col, float v)
 {
@@ -245,77 +261,98 @@ __device__ __forceinline__ void store_param(const ParamGrad &g, int group, int d
     else static_cast<f16 *>(g.p)[i] = from_f32<f16>(v);
 }
 
-// Adds the blocks' partials: a block takes 32 columns, its warps every 32nd
-// partial each, then the warps' sums in order.  blockIdx.y < groups: the
-// gradients that each group has of its own; the last: those shared by all.
+// Adds the blocks' partials.  A block takes 8 columns (one sector of each
+// partial), 64 threads of a column every 64th partial each, then their sums in
+// order.  blockIdx.y < groups: the gradients that each group has of its own; the
+// last: those shared by all.
 __global__ void __launch_bounds__(kFinishCols * kFinishLanes)
     residual_norm_finish_kernel(const __grid_constant__ ResidualNormArgs a,
                                 const __grid_constant__ ParamGrads g, int shared_block)
 {
-    __shared__ float part[5][kFinishLanes][kFinishCols + 1];
-    pdl_wait();
-    const int cx = threadIdx.x & 31, lane = threadIdx.x >> 5;
+    __shared__ float part[5][kFinishLanes][kFinishCols];
+    const int cx = threadIdx.x % kFinishCols, lane = threadIdx.x / kFinishCols;
     const int col = int(blockIdx.x) * kFinishCols + cx;
     const bool shared = int(blockIdx.y) == shared_block;
     const int each = a.plan.classes * a.plan.splits;  // partials of a group
     const int p0 = shared ? 0 : int(blockIdx.y) * each;
     const int p1 = shared ? a.plan.groups * each : p0 + each;
     const bool full = a.gate_rows.p != nullptr;
+    // sums of A, F, C, E over partials whose factors are the same; the factors
+    const auto factors = [&](int group, float &gate, float &w, float &b) {
+        gate = a.gate.p && !full ? param_at(a.gate, group, col) : 1.0f;
+        w = a.w1.p ? param_at(a.w1, group, col) + a.offset : 1.0f;
+        b = a.b1.p ? param_at(a.b1, group, col) : 0.0f;
+    };
     // dg, dw1, db1, dw2, db2
     float v[5] = {};
-    if (col < a.dim) {
-        for (int p = p0 + lane; p < p1; p += kFinishLanes) {
-            const float *src = a.partials + (long long)p * a.sums * a.dim + col;
-            const int group = p / each;
-            const float A = a.sum_a >= 0 ? src[(long long)a.sum_a * a.dim] : 0.0f;
-            const float F = a.sum_f >= 0 ? src[(long long)a.sum_f * a.dim] : 0.0f;
-            const float gate = a.gate.p && !full ? param_at(a.gate, group, col) : 1.0f;
-            if (g.gate.p) {
-                const float w = a.w1.p ? param_at(a.w1, group, col) + a.offset : 1.0f;
-                const float b = a.b1.p ? param_at(a.b1, group, col) : 0.0f;
-                v[0] += fmaf(w, A, b * F);
-            }
+    pdl_wait();
+    if (col < a.dim && p0 < p1) {
+        const bool vary = shared && (a.gate.stride || a.w1.stride || a.b1.stride);
+        float gate, w, b;
+        if (!vary) factors(p0 / each, gate, w, b);
+        const long long pitch = (long long)a.sums * a.dim;
+        const float *src = a.partials + (p0 + lane) * pitch + col;
+#pragma unroll 4
+        for (int p = p0 + lane; p < p1; p += kFinishLanes, src += kFinishLanes * pitch) {
+            const float A = a.sum_a >= 0 ? __ldcg(src + (long long)a.sum_a * a.dim) : 0.0f;
+            const float F = a.sum_f >= 0 ? __ldcg(src + (long long)a.sum_f * a.dim) : 0.0f;
+            const float C = a.sum_c >= 0 ? __ldcg(src + (long long)a.sum_c * a.dim) : 0.0f;
+            const float E = a.sum_e >= 0 ? __ldcg(src + (long long)a.sum_e * a.dim) : 0.0f;
+            if (vary) factors(p / each, gate, w, b);
+            v[0] += fmaf(w, A, b * F);
             v[1] = fmaf(gate, A, v[1]);
             v[2] = fmaf(gate, F, v[2]);
-            if (a.sum_c >= 0) v[3] += src[(long long)a.sum_c * a.dim];
-            if (a.sum_e >= 0) v[4] += src[(long long)a.sum_e * a.dim];
+            v[3] += C;
+            v[4] += E;
         }
     }
 #pragma unroll
     for (int k = 0; k < 5; ++k) part[k][lane][cx] = v[k];
     __syncthreads();
-    if (lane < 5 && col < a.dim) {
+    if (threadIdx.x < 5 * kFinishCols) {
+        const int k = threadIdx.x / kFinishCols, x = threadIdx.x % kFinishCols;
+        const int to = int(blockIdx.x) * kFinishCols + x;
         float s = 0.0f;
-        for (int l = 0; l < kFinishLanes; ++l) s += part[lane][l][cx];
-        const ParamGrad &out = lane == 0   ? g.gate
-                               : lane == 1 ? g.w1
-                               : lane == 2 ? g.b1
-                               : lane == 3 ? g.w2
-                                           : g.b2;
-        if (bool(out.per_sample) != shared) store_param(out, int(blockIdx.y), a.dim, col, s);
+#pragma unroll 16
+        for (int l = 0; l < kFinishLanes; ++l) s += part[k][l][x];
+        const ParamGrad &out = k == 0 ? g.gate : k == 1 ? g.w1 : k == 2 ? g.b1 : k == 3 ? g.w2 : g.b2;
+        if (to < a.dim && bool(out.per_sample) != shared) store_param(out, int(blockIdx.y), a.dim, to, s);
     }
 }
 
-template <typename R, typename Y, bool ALIGNED, bool FULL, bool BIAS>
-cudaError_t launch(ResidualNormArgs a, cudaStream_t s)
+template <typename R, typename Y, bool ALIGNED, bool FULL, bool LAYER, bool ANY>
+cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    const int units = 2 * Staged<R, ALIGNED>::kUnits + (FULL ? 3 : 2) * Staged<Y, ALIGNED>::kUnits;
-    return launch_staged(residual_norm_bwd_kernel<R, Y, ALIGNED, FULL, BIAS>, a, units, 1, s);
+    return launch_staged(residual_norm_bwd_kernel<R, Y, ALIGNED, FULL, LAYER, ANY>, a,
+                         bwd_units<R, Y, ALIGNED, FULL>(), bwd_stages<R, Y, ALIGNED, FULL>(), s);
+}
+
+// A kernel that can do everything has to ask, row for row, what it is to do: the
+// usual calls have kernels of their own.
+template <typename R, typename Y, bool ALIGNED>
+cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
+{
+    const bool any = !a.y.p || !a.gx.p || !a.gu.p || !a.dx || !a.dy || a.tokens != 0 ||
+                     a.plan.cluster > 1;
+    const bool layer = a.post == GBSSIM_ROW_LAYER || a.pre == GBSSIM_ROW_LAYER || a.b1.p ||
+                       a.sum_e >= 0 || a.sum_f >= 0;
+    if (a.gate_rows.p)
+        return any || layer ? launch<R, Y, ALIGNED, true, true, true>(a, s)
+                            : launch<R, Y, ALIGNED, true, false, false>(a, s);
+    return any     ? launch<R, Y, ALIGNED, false, true, true>(a, s)
+           : layer ? launch<R, Y, ALIGNED, false, true, false>(a, s)
+                   : launch<R, Y, ALIGNED, false, false, false>(a, s);
 }
 
 template <typename R, typename Y>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    const bool bias = a.b1.p || a.sum_e >= 0 || a.sum_f >= 0, full = a.gate_rows.p != nullptr;
-    if (a.plan.aligned) {
-        if (full) return bias ? launch<R, Y, true, true, true>(a, s) : launch<R, Y, true, true, false>(a, s);
-        return bias ? launch<R, Y, true, false, true>(a, s) : launch<R, Y, true, false, false>(a, s);
-    }
-    if (full) return bias ? launch<R, Y, false, true, true>(a, s) : launch<R, Y, false, true, false>(a, s);
-    return bias ? launch<R, Y, false, false, true>(a, s) : launch<R, Y, false, false, false>(a, s);
+    return a.plan.aligned ? launch<R, Y, true>(a, s) : launch<R, Y, false>(a, s);
 }
 
 }  // namespace
+
+cudaError_t residual_norm_bwd_status(unsigned *flags, bool clear) { return exchange_status(flags, clear); }
 
 cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk,
                                      const ParamGrads &g, cudaStream_t s)

@@ -3,11 +3,23 @@
 // Bound by memory: x and y are read once, x' and u written once, and both
 // norms' statistics are taken from the row held in registers, in float32.  u
 // comes from x' before its rounding.
-#include "common.cuh"
 #include "residual_norm.cuh"
 
 namespace gbssim {
 namespace {
+
+// 16-byte words a thread stages of a row: x, y and a gate per row.
+template <typename R, typename Y, bool ALIGNED, bool ANY>
+constexpr int fwd_units()
+{
+    return Staged<R, ALIGNED, ANY>::kUnits + Staged<Y, ALIGNED, ANY>::kUnits * (ANY ? 2 : 1);
+}
+
+template <typename R, typename Y, bool ALIGNED, bool ANY>
+constexpr int fwd_stages()
+{
+    return stages_of(fwd_units<R, Y, ALIGNED, ANY>(), 2);
+}
 
 struct RowStats {
     float mean, rstd;
@@ -15,71 +27,76 @@ struct RowStats {
 
 // Mean and 1 / deviation of the team's row.  Columns that the row does not have
 // hold zero: they add nothing to a sum of squares, but must not count about a mean.
-template <bool ALIGNED>
+template <bool LAYER, bool ALIGNED, bool CLUSTER>
 __device__ __forceinline__ RowStats row_stats(const f32x2 (&v)[4], const Cols<ALIGNED> &c, int kind,
-                                              const ResidualNormArgs &a, TeamSum &sum)
+                                              const ResidualNormArgs &a, TeamSum<CLUSTER> &sum)
 {
     if (kind == GBSSIM_ROW_NONE) return {0.0f, 1.0f};
+    if (!LAYER || kind == GBSSIM_ROW_RMS) {
+        f32x2 q = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q = fma2(v[e], v[e], q);
+        return {0.0f, rsqrtf(fmaf(sum.one(sum2(q)), a.inv_dim, a.eps))};
+    }
+    // the squares about the mean of the lanes' own columns, in registers; the
+    // lanes' means about the row's when the warps are joined
+    float lanes = sum2(add2(add2(v[0], v[1]), add2(v[2], v[3])));
+    lanes = sum.lanes(lanes);
+    const f32x2 m = both(-lanes * sum.inv_columns);
     f32x2 q = 0;
-    float mean = 0.0f;
-    if (kind == GBSSIM_ROW_LAYER) {
-        mean = sum.one(sum2(add2(add2(v[0], v[1]), add2(v[2], v[3])))) * a.inv_dim;
-        const f32x2 m = both(-mean);
-        if (c.all()) {
+    if (c.all()) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const f32x2 d = add2(v[e], m);
-                q = fma2(d, d, q);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 h = halves(add2(v[e / 2], m));
-                const float d = c.has(e) ? (e & 1 ? h.y : h.x) : 0.0f;
-                q = fma2(pair(d, 0.0f), pair(d, 0.0f), q);
-            }
+        for (int e = 0; e < 4; ++e) {
+            const f32x2 d = add2(v[e], m);
+            q = fma2(d, d, q);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) q = fma2(v[e], v[e], q);
+        for (int e = 0; e < 8; ++e) {
+            const float2 h = halves(add2(v[e / 2], m));
+            const float d = c.has(e) ? (e & 1 ? h.y : h.x) : 0.0f;
+            q = fma2(pair(d, 0.0f), pair(d, 0.0f), q);
+        }
     }
-    return {mean, rsqrtf(fmaf(sum.one(sum2(q)), a.inv_dim, a.eps))};
+    const float2 both_sums = sum.join_squares(lanes, sum.lanes(sum2(q)), a.inv_dim);
+    return {both_sums.x * a.inv_dim, rsqrtf(fmaf(both_sums.y, a.inv_dim, a.eps))};
 }
 
-// BIAS: either norm has a bias.
-template <typename R, typename Y, bool ALIGNED, bool BIAS>
+// LAYER: a norm may subtract the mean or have a bias.  ANY: whatever a call may
+// ask for; without it y and u are there, gates are columns', one stride reaches
+// every row, and a block has whole rows.
+template <typename R, typename Y, bool ALIGNED, bool LAYER, bool ANY>
 __global__ void __launch_bounds__(kMaxTeamThreads, 2)
     residual_norm_fwd_kernel(const __grid_constant__ ResidualNormArgs a)
 {
-    using SR = Staged<R, ALIGNED>;
-    using SY = Staged<Y, ALIGNED>;
+    using SR = Staged<R, ALIGNED, ANY>;
+    using SY = Staged<Y, ALIGNED, ANY>;
+    constexpr int kStages = fwd_stages<R, Y, ALIGNED, ANY>();
     extern __shared__ uint4 ring[];
-    __shared__ float2 slots[2][16];
-    __shared__ float2 cluster_slots[2][4];
-    const BlockRows rows(a);
-    const Cols<ALIGNED> c(a, rows.shift);
-    TeamSum sum{slots, cluster_slots, 0, a.plan.tpr, a.plan.teams > 1 ? 1 : a.plan.threads / 32,
-                a.plan.cluster};
+    __shared__ TeamSlots slots;
+    const int cluster = ANY ? a.plan.cluster : 1;
+    const BlockRows rows(a, cluster);
+    const Cols<ALIGNED> c(a, cluster, rows.shift);
+    TeamSum<ANY> sum(slots, a);
+    if (LAYER) sum.count_columns(c.upto - c.from);
     const int team = a.plan.teams > 1 ? int(threadIdx.x) / a.plan.tpr : 0;
     const int step = rows.step * a.plan.teams;  // rows from one of the team's to its next
-    const int pitch = a.plan.threads * 16, stages = a.plan.stages;
-    const bool has_y = a.y.p, has_gates = a.gate_rows.p;
-    const int stage_bytes = (SR::kUnits + SY::kUnits * (has_gates ? 2 : 1)) * pitch;
-    const unsigned mine = smem_u32(ring) + threadIdx.x * 16, over = mine + stages * stage_bytes;
-    // no block writes into another's shared memory before that block runs
-    if (a.plan.cluster > 1) cooperative_groups::this_cluster().sync();
+    const int pitch = a.plan.threads * 16;
+    const bool has_y = !ANY || a.y.p, has_gates = ANY && a.gate_rows.p, has_u = !ANY || a.u;
+    const int stage_bytes = fwd_units<R, Y, ALIGNED, ANY>() * pitch;
+    const unsigned mine = smem_u32(ring) + threadIdx.x * 16, over = mine + kStages * stage_bytes;
 
     int r = rows.first + team * rows.step, left = rows.count - team;  // the team's row; none if <= 0
-    int ahead = r, ahead_left = left;
+    int ahead = r, ahead_left = c.any() ? left : 0;
     unsigned to = mine;
     const auto fetch = [&] {
-        if (ahead_left > 0 && c.any()) {
-            SR::fetch(a.x, row_at<R>(a.x, a.tokens, ahead, c.first), c, to, pitch);
+        if (ahead_left > 0) {
+            SR::fetch(a.x, row_at<R, ANY>(a.x, a.tokens, ahead, c.first), c, to, pitch);
             if (has_y)
-                SY::fetch(a.y, row_at<Y>(a.y, a.tokens, ahead, c.first), c, to + SR::kUnits * pitch,
-                          pitch);
+                SY::fetch(a.y, row_at<Y, ANY>(a.y, a.tokens, ahead, c.first), c,
+                          to + SR::kUnits * pitch, pitch);
             if (has_gates)
-                SY::fetch(a.gate_rows, row_at<Y>(a.gate_rows, a.tokens, ahead, c.first), c,
+                SY::fetch(a.gate_rows, row_at<Y, ANY>(a.gate_rows, a.tokens, ahead, c.first), c,
                           to + (SR::kUnits + SY::kUnits) * pitch, pitch);
         }
         staged_commit();
@@ -88,14 +105,14 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
         to += stage_bytes;
         if (to == over) to = mine;
     };
-    for (int i = 0; i < stages - 1; ++i) fetch();
+    for (int i = 0; i < kStages - 1; ++i) fetch();
 
     // post and gate of a column in one factor and one summand; a gate of its
     // own per row stays apart
     f32x2 w1[4], b1[4], w2[4], b2[4];
     load_param(a.w1, rows.group, c, a.offset, 1.0f, w1);
     load_param(a.w2, rows.group, c, a.offset, 1.0f, w2);
-    if (BIAS) {
+    if (LAYER) {
         load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
         load_param(a.b2, rows.group, c, 0.0f, 0.0f, b2);
     }
@@ -105,7 +122,7 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             w1[e] = mul2(w1[e], g[e]);
-            if (BIAS) b1[e] = mul2(b1[e], g[e]);
+            if (LAYER) b1[e] = mul2(b1[e], g[e]);
         }
     }
     const f32x2 scale = both(a.scale);
@@ -114,20 +131,18 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
     for (int i = 0; i < rows.count; i += a.plan.teams) {
         const bool active = left > 0;
         fetch();
-        staged_wait(stages);
+        staged_wait<kStages - 1>();
         f32x2 x[4];
         SR::read(a.x, a.tokens, r, c, active, at, pitch, x);
         RowStats s1 = {0.0f, 1.0f}, s2 = {0.0f, 1.0f};
         if (has_y) {
             f32x2 y[4];
             SY::read(a.y, a.tokens, r, c, active, at + SR::kUnits * pitch, pitch, y);
-            s1 = row_stats(y, c, a.post, a, sum);
+            s1 = row_stats<LAYER>(y, c, a.post, a, sum);
             const f32x2 v = both(s1.rstd), m = both(-s1.mean * s1.rstd);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[e] = fma2(y[e], v, m);
-                y[e] = BIAS ? fma2(y[e], w1[e], b1[e]) : mul2(y[e], w1[e]);
-            }
+            for (int e = 0; e < 4; ++e)
+                y[e] = LAYER ? fma2(fma2(y[e], v, m), w1[e], b1[e]) : mul2(mul2(y[e], v), w1[e]);
             if (has_gates) {
                 f32x2 g[4];
                 SY::read(a.gate_rows, a.tokens, r, c, active, at + (SR::kUnits + SY::kUnits) * pitch,
@@ -139,14 +154,12 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
             for (int e = 0; e < 4; ++e) x[e] = fma2(scale, x[e], y[e]);
             store_cols(static_cast<R *>(a.x_out) + ((long long)r * a.dim + c.first), c, active, x);
         }
-        if (a.u) {
-            s2 = row_stats(x, c, a.pre, a, sum);
+        if (has_u) {
+            s2 = row_stats<LAYER>(x, c, a.pre, a, sum);
             const f32x2 v = both(s2.rstd), m = both(-s2.mean * s2.rstd);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[e] = fma2(x[e], v, m);
-                x[e] = BIAS ? fma2(x[e], w2[e], b2[e]) : mul2(x[e], w2[e]);
-            }
+            for (int e = 0; e < 4; ++e)
+                x[e] = LAYER ? fma2(fma2(x[e], v, m), w2[e], b2[e]) : mul2(mul2(x[e], v), w2[e]);
             store_cols(static_cast<Y *>(a.u) + ((long long)r * a.dim + c.first), c, active, x);
         }
         if (a.stats && active && c.first <= 0 && c.any())
@@ -156,25 +169,57 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
         at += stage_bytes;
         if (at == over) at = mine;
     }
+    sum.finish();
 }
 
-template <typename R, typename Y, bool ALIGNED, bool BIAS>
-cudaError_t launch(ResidualNormArgs a, cudaStream_t s)
+template <typename R, typename Y, bool ALIGNED, bool LAYER, bool ANY>
+cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    const int units = Staged<R, ALIGNED>::kUnits +
-                      Staged<Y, ALIGNED>::kUnits * (a.gate_rows.p ? 2 : 1);
-    return launch_staged(residual_norm_fwd_kernel<R, Y, ALIGNED, BIAS>, a, units, 2, s);
+    return launch_staged(residual_norm_fwd_kernel<R, Y, ALIGNED, LAYER, ANY>, a,
+                         fwd_units<R, Y, ALIGNED, ANY>(), fwd_stages<R, Y, ALIGNED, ANY>(), s);
 }
 
+// A kernel that can do everything has to ask, row for row, what it is to do: the
+// usual calls have kernels of their own.
 template <typename R, typename Y>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    const bool bias = a.b1.p || a.b2.p;
-    if (a.plan.aligned) return bias ? launch<R, Y, true, true>(a, s) : launch<R, Y, true, false>(a, s);
-    return bias ? launch<R, Y, false, true>(a, s) : launch<R, Y, false, false>(a, s);
+    const bool any = !a.y.p || !a.u || a.gate_rows.p || a.tokens != 0 || a.plan.cluster > 1;
+    const bool layer = a.post == GBSSIM_ROW_LAYER || a.pre == GBSSIM_ROW_LAYER || a.b1.p || a.b2.p;
+    if (a.plan.aligned)
+        return any     ? launch<R, Y, true, true, true>(a, s)
+               : layer ? launch<R, Y, true, true, false>(a, s)
+                       : launch<R, Y, true, false, false>(a, s);
+    return any     ? launch<R, Y, false, true, true>(a, s)
+           : layer ? launch<R, Y, false, true, false>(a, s)
+                   : launch<R, Y, false, false, false>(a, s);
 }
 
 }  // namespace
+
+cudaError_t residual_norm_cluster_room(ClusterRoom *room)
+{
+    const auto kernel = residual_norm_fwd_kernel<float, float, true, true, true>;
+    constexpr int kAlone = 120 * 1024;  // shared memory that leaves an SM room for one block
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedBlock);
+    for (int size = 2; size <= 4 && e == cudaSuccess; size *= 2) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(size));
+        cfg.blockDim = dim3(kMaxTeamThreads);
+        cfg.dynamicSmemBytes = kAlone;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = unsigned(size);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(size == 2 ? &room->of2 : &room->of4, kernel, &cfg);
+    }
+    return e;
+}
+
+cudaError_t residual_norm_fwd_status(unsigned *flags, bool clear) { return exchange_status(flags, clear); }
 
 cudaError_t residual_norm_fwd_launch(const ResidualNormArgs &a, int res, int blk, cudaStream_t s)
 {

@@ -81,9 +81,13 @@ void gbssim_window(float w[11]);
  *   its staged input rows without them arriving; its blocks stopped early, so
  *   that call's gradients and map are not valid, and the mean of each image
  *   with a stopped block is NaN.
+ *   bit 1 (GBSSIM_DEV_EXCHANGE_TIMEOUT): blocks of a residual norm that share a
+ *   row (more than 4096 columns) waited about a second for one another's sums;
+ *   that call's outputs are not valid.
  * Synchronises the device: a diagnostic, not part of the hot path.  Returns
  * GBSSIM_OK, GBSSIM_EINVAL (null flags_out) or GBSSIM_ECUDA. */
 #define GBSSIM_DEV_STAGING_TIMEOUT 1u
+#define GBSSIM_DEV_EXCHANGE_TIMEOUT 2u
 int gbssim_device_status(unsigned *flags_out);
 
 /* ------------------------------------------------------------------ 2D ----- */
