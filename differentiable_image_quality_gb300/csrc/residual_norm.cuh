@@ -49,6 +49,7 @@ struct ParamPtr {
 // clusters) share a class of a group.
 struct RowPlan {
     int aligned;       // rows start on 16-byte boundaries in every tensor
+    int uneven;        // a tensor's rows change their alignment within a block
     int classes;       // 8 / gcd(8, D); 1 also where a group has too few rows to part
     int cluster;       // blocks of a cluster (1, 2, 4)
     int block_cols;    // columns of a block: a multiple of 8 (counted from the shift)
@@ -199,8 +200,19 @@ struct Staged {
         }
     }
 
-    // The thread's columns of a row, zero where the row has none.
-    static __device__ __forceinline__ void read(const RowPtr &p, int tokens, int row,
+    // By how many elements the thread's columns of a row lie past a 16-byte
+    // boundary.  The same in every row of a block, unless ANY.
+    static __device__ __forceinline__ int shift_of(const RowPtr &p, int tokens, int row,
+                                                   const Cols<ALIGNED> &c)
+    {
+        if (ALIGNED || !p.p) return 0;
+        return int(reinterpret_cast<uintptr_t>(row_at<T, ANY>(p, tokens, row, c.first)) & 15) /
+               int(sizeof(T));
+    }
+
+    // The thread's columns of a row, zero where the row has none; known: its shift
+    // where that is the same in every row.
+    static __device__ __forceinline__ void read(const RowPtr &p, int tokens, int row, int known,
                                                 const Cols<ALIGNED> &c, bool active, unsigned slot,
                                                 int pitch, f32x2 (&v)[4])
     {
@@ -213,8 +225,7 @@ struct Staged {
             unpack8<T>(r, v);
         } else {
             if (active && c.any()) {
-                const int s = int(reinterpret_cast<uintptr_t>(row_at<T, ANY>(p, tokens, row, c.first)) & 15) /
-                              int(sizeof(T));
+                const int s = ANY ? shift_of(p, tokens, row, c) : known;
                 if (s == 0) {
 #pragma unroll
                     for (int u = 0; u < kUnits - 1; ++u) r.w[u] = ld_shared16(slot + u * pitch);
@@ -311,12 +322,12 @@ __device__ __forceinline__ unsigned peer_address(unsigned shared, int rank)
     return r;
 }
 
-// Writes two floats to a block of the cluster and counts them on its barrier.
-__device__ __forceinline__ void send8(unsigned to, float2 v, unsigned bar)
+// Writes four floats to a block of the cluster and counts them on its barrier.
+__device__ __forceinline__ void send16(unsigned to, float4 v, unsigned bar)
 {
     asm volatile(
-        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
-        "f"(v.x), "f"(v.y), "r"(bar)
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+        "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
         : "memory");
 }
 
@@ -325,11 +336,11 @@ __device__ __forceinline__ void send8(unsigned to, float2 v, unsigned bar)
 // cluster-wide barrier would first wait for the rows that the blocks have just
 // stored.)
 struct TeamSlots {
-    float warps[2][2][16];     // [parity][value][warp]
-    float2 blocks[2][4];       // [parity][block]
+    float warps[2][4][16];     // [parity][value][warp]
+    float4 blocks[2][4];       // [parity][block]
     uint64_t arrived[2];
-    float columns[16];         // of each warp
-    float block_columns[4];
+    float2 columns[16];        // of each warp: how many, and 1 / that
+    float2 block_columns[4];   // of each block
 };
 
 // About a second: an exchange that takes longer has failed.
@@ -348,10 +359,11 @@ struct TeamSum {
     unsigned extra;       // test hook: bytes announced beyond those sent (0)
     bool dead;            // an exchange ran out of time: wait for no other
     float inv_columns;    // 1 / columns of the team's lanes in this warp (count_columns)
+    float inv_block;      // 1 / columns of the block
 
     __device__ __forceinline__ TeamSum(TeamSlots &s, const ResidualNormArgs &a)
         : slots(s), parity(0), tpr(a.plan.tpr), warps(a.plan.teams > 1 ? 1 : a.plan.threads / 32),
-          cluster(CLUSTER ? a.plan.cluster : 1), phases(0), extra(a.exchange_extra), dead(false), inv_columns(0.0f)
+          cluster(CLUSTER ? a.plan.cluster : 1), phases(0), extra(a.exchange_extra), dead(false), inv_columns(0.0f), inv_block(0.0f)
     {
         if (cluster == 1) return;
         if (threadIdx.x == 0) {
@@ -383,38 +395,36 @@ struct TeamSum {
         return v;
     }
 
-    // The warps' values a (and b), one warp to each lane of a half warp.  One
-    // barrier: the slots alternate, and a thread that writes a slot again has
-    // passed the barrier of the sum in between, which every thread reaches only
-    // after it has read this one.
-    __device__ __forceinline__ float2 of_warps(float a, float b, bool two)
+    // The warps' values, one warp to each lane of a half warp.  One barrier: the
+    // slots alternate, and a thread that writes a slot again has passed the
+    // barrier of the sum in between, which every thread reaches only after it has
+    // read this one.
+    template <int N>
+    __device__ __forceinline__ void of_warps(float (&v)[N])
     {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         if (lane == 0) {
-            slots.warps[parity][0][warp] = a;
-            if (two) slots.warps[parity][1][warp] = b;
+#pragma unroll
+            for (int k = 0; k < N; ++k) slots.warps[parity][k][warp] = v[k];
         }
         __syncthreads();
-        float2 v = make_float2(0.0f, 0.0f);
-        if ((lane & 15) < warps) {
-            v.x = slots.warps[parity][0][lane & 15];
-            if (two) v.y = slots.warps[parity][1][lane & 15];
-        }
-        return v;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            v[k] = (lane & 15) < warps ? slots.warps[parity][k][lane & 15] : 0.0f;
     }
 
     // This block's values to all blocks, and all blocks' into slots.blocks.  A
     // block sends its next values only after its threads have read all of these,
     // and nobody gets further than one exchange ahead of the others: two sets of
     // slots are enough.
-    __device__ __forceinline__ void exchange(float2 v)
+    __device__ __forceinline__ void exchange(float4 v)
     {
         uint64_t *bar = &slots.arrived[parity];
-        if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, unsigned(cluster) * 8u + extra);
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, unsigned(cluster) * 16u + extra);
         if (int(threadIdx.x) < cluster) {
             const int rank = int(cooperative_groups::this_cluster().block_rank());
-            send8(peer_address(smem_u32(&slots.blocks[parity][rank]), threadIdx.x), v,
-                  peer_address(smem_u32(bar), threadIdx.x));
+            send16(peer_address(smem_u32(&slots.blocks[parity][rank]), threadIdx.x), v,
+                   peer_address(smem_u32(bar), threadIdx.x));
         }
         if (!dead && !mbar_wait_bounded(bar, (phases >> parity) & 1u, kExchangeCycles)) {
             dead = true;
@@ -429,18 +439,21 @@ struct TeamSum {
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] = lanes(v[k]);
         if (warps == 1 && cluster == 1) return;
-        const float2 w = of_warps(v[0], v[N - 1], N == 2);
-        v[0] = sixteen(w.x);
-        if (N == 2) v[N - 1] = sixteen(w.y);
+        of_warps(v);
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = sixteen(v[k]);
         if (cluster > 1) {
-            exchange(make_float2(v[0], v[N - 1]));
-            float2 s = make_float2(0.0f, 0.0f);
-            for (int r = 0; r < cluster; ++r) {
-                s.x += slots.blocks[parity][r].x;
-                s.y += slots.blocks[parity][r].y;
+            exchange(make_float4(v[0], v[N > 1 ? 1 : 0], v[N > 2 ? 2 : 0], v[N > 3 ? 3 : 0]));
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 b = r < cluster ? slots.blocks[parity][r] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                v[0] += b.x;
+                if (N > 1) v[N > 1 ? 1 : 0] += b.y;
+                if (N > 2) v[N > 2 ? 2 : 0] += b.z;
+                if (N > 3) v[N > 3 ? 3 : 0] += b.w;
             }
-            v[0] = s.x;
-            if (N == 2) v[N - 1] = s.y;
         }
         parity ^= 1;
     }
@@ -452,19 +465,28 @@ struct TeamSum {
         return a[0];
     }
 
+    static __device__ __forceinline__ float2 with_inverse(float n)
+    {
+        return make_float2(n, n > 0.0f ? 1.0f / n : 0.0f);
+    }
+
     // Once, before join_squares: how many columns the lanes, warps and blocks have.
     __device__ __forceinline__ void count_columns(int mine)
     {
         const float n = lanes(float(max(0, mine)));
-        inv_columns = n > 0.0f ? 1.0f / n : 0.0f;
+        inv_columns = with_inverse(n).y;
         if (warps == 1 && cluster == 1) return;
         const int lane = threadIdx.x & 31;
-        const float2 w = of_warps(n, 0.0f, false);
-        if (threadIdx.x < 16) slots.columns[lane] = w.x;
-        const float block = sixteen(w.x);
+        float w[1] = {n};
+        of_warps(w);
+        if (threadIdx.x < 16) slots.columns[lane] = with_inverse(w[0]);
+        const float block = sixteen(w[0]);
+        inv_block = with_inverse(block).y;
         if (cluster > 1) {
-            exchange(make_float2(block, 0.0f));
-            if (int(threadIdx.x) < cluster) slots.block_columns[lane] = slots.blocks[parity][lane].x;
+            exchange(make_float4(block, 0.0f, 0.0f, 0.0f));
+            if (threadIdx.x < 4)
+                slots.block_columns[lane] =
+                    lane < cluster ? with_inverse(slots.blocks[parity][lane].x) : make_float2(0.0f, 0.0f);
         }
         parity ^= 1;
         __syncthreads();
@@ -477,24 +499,29 @@ struct TeamSum {
     {
         if (warps == 1 && cluster == 1) return make_float2(s, q);
         const int lane = threadIdx.x & 31;
-        const float2 w = of_warps(s, q, true);
-        const float n = (lane & 15) < warps ? slots.columns[lane & 15] : 0.0f;
-        const float block = sixteen(w.x);
-        // about the block's mean (the row's, where one block has all of it)
-        const float all = cluster > 1 ? sixteen(n) : 0.0f;
-        const float mean = cluster > 1 ? (all > 0.0f ? block / all : 0.0f) : block * inv_dim;
-        const float d = n > 0.0f ? w.x / n - mean : 0.0f;
-        float2 r = make_float2(block, sixteen(fmaf(n * d, d, w.y)));
+        float w[2] = {s, q};
+        of_warps(w);
+        const float2 n = (lane & 15) < warps ? slots.columns[lane & 15] : make_float2(0.0f, 0.0f);
+        const float block = sixteen(w[0]);
+        const float d = fmaf(w[0], n.y, -block * inv_block);
+        float2 r = make_float2(block, sixteen(fmaf(n.x * d, d, w[1])));
         if (cluster > 1) {
-            exchange(r);
+            exchange(make_float4(r.x, r.y, 0.0f, 0.0f));
+            float2 v[4], c[4];
             float total = 0.0f;
-            for (int k = 0; k < cluster; ++k) total += slots.blocks[parity][k].x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                c[k] = slots.block_columns[k];
+                const float4 b = k < cluster ? slots.blocks[parity][k] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                v[k] = make_float2(b.x, b.y);
+                total += b.x;
+            }
             const float row = total * inv_dim;
             r = make_float2(total, 0.0f);
-            for (int k = 0; k < cluster; ++k) {
-                const float2 v = slots.blocks[parity][k];
-                const float nk = slots.block_columns[k], dk = nk > 0.0f ? v.x / nk - row : 0.0f;
-                r.y += fmaf(nk * dk, dk, v.y);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float dk = fmaf(v[k].x, c[k].y, -row);
+                r.y += fmaf(c[k].x * dk, dk, v[k].y);
             }
         }
         parity ^= 1;
@@ -522,13 +549,14 @@ inline cudaError_t exchange_status(unsigned *flags, bool clear)
 // Shared memory of an SM that rings of staged rows share.
 constexpr int kStagedSmem = 200 * 1024, kStagedBlock = 220 * 1024;
 
-// The stages of a ring of staged rows, of `units` 16-byte words a thread each: as
-// many (up to four) as leave room for `per_sm` blocks of 512 threads, or as many
-// threads of smaller ones, on an SM.
+// The stages of a ring of staged rows, of `units` 16-byte words a thread each: two
+// where they leave room for `per_sm` blocks of 512 threads, or as many threads of
+// smaller ones, on an SM.  More rows in flight made the widest forward slower:
+// 65536 x 4096 bfloat16 took 332 us with two stages, 346 with three, 372 with four.
 constexpr int stages_of(int units, int per_sm)
 {
     const int fit = kStagedSmem / (units * 16 * 512 * per_sm);
-    return fit < 1 ? 1 : fit > 4 ? 4 : fit;
+    return fit < 1 ? 1 : fit > 2 ? 2 : fit;
 }
 
 template <class Kernel>

@@ -202,6 +202,13 @@ bool one_stride(const gbssim_residual_norm &d, const gbssim_rows &r)
                        r.token_stride <= INT_MAX / 4);
 }
 
+// Whether a tensor's rows that a block meets, `classes` apart, all lie alike to a
+// 16-byte boundary.
+bool even(const RowPtr &p, const RowPlan &plan)
+{
+    return !p.p || (long long)p.row_bytes * plan.classes % 16 == 0;
+}
+
 bool dense(const gbssim_residual_norm &d, const gbssim_rows &r)
 {
     return (d.tokens < 2 || r.token_stride == d.dim) &&
@@ -296,6 +303,7 @@ extern "C" int gbssim_residual_norm_fwd(const gbssim_residual_norm *d, void *x_o
     a.tokens = one_stride(*d, d->x) && one_stride(*d, d->y) && one_stride(*d, d->gate_rows)
                    ? 0
                    : d->tokens;
+    a.plan.uneven = !(even(a.x, a.plan) && even(a.y, a.plan));
     a.x_out = x_out_or_null;
     a.u = u_or_null;
     a.stats = reinterpret_cast<float4 *>(stats_or_null);
@@ -384,6 +392,8 @@ extern "C" int gbssim_residual_norm_bwd(const gbssim_residual_norm *d,
                        one_stride(*d, gx) && one_stride(*d, gu)
                    ? 0
                    : d->tokens;
+    a.plan.uneven = !(even(a.x, a.plan) && even(a.y, a.plan) && even(a.gate_rows, a.plan) &&
+                      even(a.gx, a.plan) && even(a.gu, a.plan));
     a.stats = const_cast<float4 *>(reinterpret_cast<const float4 *>(stats));
     a.dx = grads->x;
     a.dy = grads->y;

@@ -74,16 +74,17 @@ __device__ __forceinline__ void write_sum(const ResidualNormArgs &a, const Cols<
         if (c.has(e)) dst[c.first + e] = v[e];
 }
 
-// FULL: a gate of its own per row.  LAYER: a norm may subtract the mean or have
-// a bias.  ANY: whatever a call may ask for; without it all four inputs and both
+// FULL: a gate of its own per row.  NORMS: 0 neither subtracts a mean nor has a
+// bias, 1 they may but for a bias of the post norm, 2 they may.  ANY: whatever a call may ask for; without it all four inputs and both
 // outputs are there, one stride reaches every row, and a block has whole rows.
-template <typename R, typename Y, bool ALIGNED, bool FULL, bool LAYER, bool ANY>
+template <typename R, typename Y, bool ALIGNED, bool FULL, int NORMS, bool ANY>
 __global__ void __launch_bounds__(kMaxTeamThreads, 1)
     residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a)
 {
     using SR = Staged<R, ALIGNED, ANY>;
     using SY = Staged<Y, ALIGNED, ANY>;
     constexpr int kStages = bwd_stages<R, Y, ALIGNED, FULL>();
+    constexpr bool LAYER = NORMS > 0, BIAS1 = NORMS == 2;
     extern __shared__ uint4 ring[];
     __shared__ TeamSlots slots;
     __shared__ float scratch[kSmallBlock * 8];
@@ -104,6 +105,11 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
     const unsigned mine = smem_u32(ring) + threadIdx.x * 16, over = mine + kStages * stage_bytes;
 
     int r = rows.first + team * rows.step, left = rows.count - team;  // the team's row; none if <= 0
+    const int shift_x = SR::shift_of(a.x, a.tokens, rows.first, c),
+              shift_y = SY::shift_of(a.y, a.tokens, rows.first, c),
+              shift_gx = SR::shift_of(a.gx, a.tokens, rows.first, c),
+              shift_gu = SY::shift_of(a.gu, a.tokens, rows.first, c),
+              shift_g = SY::shift_of(a.gate_rows, a.tokens, rows.first, c);
     int ahead = r, ahead_left = c.any() ? left : 0;
     unsigned to = mine;
     const auto fetch = [&] {
@@ -130,14 +136,14 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
     f32x2 w1[4], b1[4], w2[4];  // with the gate of the column in w1 and b1, unless FULL
     load_param(a.w1, rows.group, c, a.offset, 1.0f, w1);
     load_param(a.w2, rows.group, c, a.offset, 1.0f, w2);
-    if (LAYER) load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
+    if (BIAS1) load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
     if (!FULL && a.gate.p) {
         f32x2 g[4];
         load_param(a.gate, rows.group, c, 0.0f, 1.0f, g);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             w1[e] = mul2(w1[e], g[e]);
-            if (LAYER) b1[e] = mul2(b1[e], g[e]);
+            if (BIAS1) b1[e] = mul2(b1[e], g[e]);
         }
     }
     const f32x2 scale = both(a.scale);
@@ -146,36 +152,38 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
     // whatever a mean makes of y^, x^ and T there meets a zero factor before it
     // enters a sum over the row, and their own sums are not stored.
     f32x2 sa[4] = {}, sf[4] = {}, sc[4] = {}, se[4] = {};
+    // the statistics of the row after this one (neutral ones where there is none)
+    float4 st_next = left > 0 ? a.stats[r] : make_float4(0.0f, 1.0f, 0.0f, 1.0f);
     for (int i = 0; i < rows.count; i += a.plan.teams) {
         const bool active = left > 0;
-        float4 st = make_float4(0.0f, 1.0f, 0.0f, 1.0f);
-        if (active) st = a.stats[r];
+        const float4 st = st_next;
+        st_next = left > a.plan.teams ? a.stats[r + step] : make_float4(0.0f, 1.0f, 0.0f, 1.0f);
         fetch();
         staged_wait<kStages - 1>();
 
         f32x2 yh[4], xh[4], T[4], g[4];
-        SR::read(a.x, a.tokens, r, c, active, at, pitch, xh);
+        SR::read(a.x, a.tokens, r, shift_x, c, active, at, pitch, xh);
         if (has_y) {
-            SY::read(a.y, a.tokens, r, c, active, at + at_y, pitch, yh);
-            if (FULL) SY::read(a.gate_rows, a.tokens, r, c, active, at + at_gate, pitch, g);
+            SY::read(a.y, a.tokens, r, shift_y, c, active, at + at_y, pitch, yh);
+            if (FULL) SY::read(a.gate_rows, a.tokens, r, shift_g, c, active, at + at_gate, pitch, g);
             const f32x2 v = both(st.y), m = both(-st.x * st.y);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 yh[e] = LAYER ? fma2(yh[e], v, m) : mul2(yh[e], v);
-                f32x2 z = LAYER ? fma2(yh[e], w1[e], b1[e]) : mul2(yh[e], w1[e]);
+                f32x2 z = BIAS1 ? fma2(yh[e], w1[e], b1[e]) : mul2(yh[e], w1[e]);
                 if (FULL) z = mul2(z, g[e]);
                 xh[e] = fma2(scale, xh[e], z);
             }
         }
         if (has_gx) {
-            SR::read(a.gx, a.tokens, r, c, active, at + at_gx, pitch, T);
+            SR::read(a.gx, a.tokens, r, shift_gx, c, active, at + at_gx, pitch, T);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) T[e] = 0;
         }
         if (has_gu) {
             f32x2 V[4], q = 0;
-            SY::read(a.gu, a.tokens, r, c, active, at + at_gu, pitch, V);
+            SY::read(a.gu, a.tokens, r, shift_gu, c, active, at + at_gu, pitch, V);
             const f32x2 v = both(st.w), m = both(-st.z * st.w);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -208,7 +216,7 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
                 f32x2 dg[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    dg[e] = mul2(T[e], LAYER ? fma2(yh[e], w1[e], b1[e]) : mul2(yh[e], w1[e]));
+                    dg[e] = mul2(T[e], BIAS1 ? fma2(yh[e], w1[e], b1[e]) : mul2(yh[e], w1[e]));
                 store_cols(static_cast<Y *>(a.dgate_rows) + ((long long)r * a.dim + c.first), c, active, dg);
             }
             f32x2 q = 0;
@@ -216,7 +224,7 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
             for (int e = 0; e < 4; ++e) {
                 if (FULL) T[e] = mul2(T[e], g[e]);
                 sa[e] = fma2(T[e], yh[e], sa[e]);
-                if (LAYER) sf[e] = add2(sf[e], T[e]);
+                if (BIAS1) sf[e] = add2(sf[e], T[e]);
                 T[e] = mul2(T[e], w1[e]);
                 q = fma2(T[e], yh[e], q);
             }
@@ -242,10 +250,8 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
     sum.finish();
     write_sum(a, c, a.sum_a, sa, scratch);
     write_sum(a, c, a.sum_c, sc, scratch);
-    if (LAYER) {
-        write_sum(a, c, a.sum_f, sf, scratch);
-        write_sum(a, c, a.sum_e, se, scratch);
-    }
+    if (BIAS1) write_sum(a, c, a.sum_f, sf, scratch);
+    if (LAYER) write_sum(a, c, a.sum_e, se, scratch);
 }
 
 // ------------------------------------------------------- the parameters' gradients
@@ -320,10 +326,10 @@ __global__ void __launch_bounds__(kFinishCols * kFinishLanes)
     }
 }
 
-template <typename R, typename Y, bool ALIGNED, bool FULL, bool LAYER, bool ANY>
+template <typename R, typename Y, bool ALIGNED, bool FULL, int NORMS, bool ANY>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    return launch_staged(residual_norm_bwd_kernel<R, Y, ALIGNED, FULL, LAYER, ANY>, a,
+    return launch_staged(residual_norm_bwd_kernel<R, Y, ALIGNED, FULL, NORMS, ANY>, a,
                          bwd_units<R, Y, ALIGNED, FULL>(), bwd_stages<R, Y, ALIGNED, FULL>(), s);
 }
 
@@ -333,15 +339,17 @@ template <typename R, typename Y, bool ALIGNED>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
     const bool any = !a.y.p || !a.gx.p || !a.gu.p || !a.dx || !a.dy || a.tokens != 0 ||
-                     a.plan.cluster > 1;
-    const bool layer = a.post == GBSSIM_ROW_LAYER || a.pre == GBSSIM_ROW_LAYER || a.b1.p ||
-                       a.sum_e >= 0 || a.sum_f >= 0;
+                     a.plan.cluster > 1 || a.plan.uneven;
+    const int norms = a.b1.p || a.sum_f >= 0 ? 2
+                      : a.post == GBSSIM_ROW_LAYER || a.pre == GBSSIM_ROW_LAYER || a.sum_e >= 0 ? 1
+                                                                                              : 0;
     if (a.gate_rows.p)
-        return any || layer ? launch<R, Y, ALIGNED, true, true, true>(a, s)
-                            : launch<R, Y, ALIGNED, true, false, false>(a, s);
-    return any     ? launch<R, Y, ALIGNED, false, true, true>(a, s)
-           : layer ? launch<R, Y, ALIGNED, false, true, false>(a, s)
-                   : launch<R, Y, ALIGNED, false, false, false>(a, s);
+        return any || norms > 0 ? launch<R, Y, ALIGNED, true, 2, true>(a, s)
+                                : launch<R, Y, ALIGNED, true, 0, false>(a, s);
+    return any          ? launch<R, Y, ALIGNED, false, 2, true>(a, s)
+           : norms == 2 ? launch<R, Y, ALIGNED, false, 2, false>(a, s)
+           : norms == 1 ? launch<R, Y, ALIGNED, false, 1, false>(a, s)
+                        : launch<R, Y, ALIGNED, false, 0, false>(a, s);
 }
 
 template <typename R, typename Y>

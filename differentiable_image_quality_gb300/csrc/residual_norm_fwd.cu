@@ -62,16 +62,17 @@ __device__ __forceinline__ RowStats row_stats(const f32x2 (&v)[4], const Cols<AL
     return {both_sums.x * a.inv_dim, rsqrtf(fmaf(both_sums.y, a.inv_dim, a.eps))};
 }
 
-// LAYER: a norm may subtract the mean or have a bias.  ANY: whatever a call may
-// ask for; without it y and u are there, gates are columns', one stride reaches
+// NORMS: 0 neither subtracts a mean nor has a bias, 1 they may but for a bias of
+// the post norm, 2 they may.  ANY: whatever a call may ask for; without it y and u are there, gates are columns', one stride reaches
 // every row, and a block has whole rows.
-template <typename R, typename Y, bool ALIGNED, bool LAYER, bool ANY>
+template <typename R, typename Y, bool ALIGNED, int NORMS, bool ANY>
 __global__ void __launch_bounds__(kMaxTeamThreads, 2)
     residual_norm_fwd_kernel(const __grid_constant__ ResidualNormArgs a)
 {
     using SR = Staged<R, ALIGNED, ANY>;
     using SY = Staged<Y, ALIGNED, ANY>;
     constexpr int kStages = fwd_stages<R, Y, ALIGNED, ANY>();
+    constexpr bool LAYER = NORMS > 0, BIAS1 = NORMS == 2;
     extern __shared__ uint4 ring[];
     __shared__ TeamSlots slots;
     const int cluster = ANY ? a.plan.cluster : 1;
@@ -87,6 +88,9 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
     const unsigned mine = smem_u32(ring) + threadIdx.x * 16, over = mine + kStages * stage_bytes;
 
     int r = rows.first + team * rows.step, left = rows.count - team;  // the team's row; none if <= 0
+    const int shift_x = SR::shift_of(a.x, a.tokens, rows.first, c),
+              shift_y = SY::shift_of(a.y, a.tokens, rows.first, c),
+              shift_g = SY::shift_of(a.gate_rows, a.tokens, rows.first, c);
     int ahead = r, ahead_left = c.any() ? left : 0;
     unsigned to = mine;
     const auto fetch = [&] {
@@ -112,17 +116,15 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
     f32x2 w1[4], b1[4], w2[4], b2[4];
     load_param(a.w1, rows.group, c, a.offset, 1.0f, w1);
     load_param(a.w2, rows.group, c, a.offset, 1.0f, w2);
-    if (LAYER) {
-        load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
-        load_param(a.b2, rows.group, c, 0.0f, 0.0f, b2);
-    }
+    if (BIAS1) load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
+    if (LAYER) load_param(a.b2, rows.group, c, 0.0f, 0.0f, b2);
     if (a.gate.p) {
         f32x2 g[4];
         load_param(a.gate, rows.group, c, 0.0f, 1.0f, g);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             w1[e] = mul2(w1[e], g[e]);
-            if (LAYER) b1[e] = mul2(b1[e], g[e]);
+            if (BIAS1) b1[e] = mul2(b1[e], g[e]);
         }
     }
     const f32x2 scale = both(a.scale);
@@ -133,19 +135,21 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
         fetch();
         staged_wait<kStages - 1>();
         f32x2 x[4];
-        SR::read(a.x, a.tokens, r, c, active, at, pitch, x);
+        SR::read(a.x, a.tokens, r, shift_x, c, active, at, pitch, x);
         RowStats s1 = {0.0f, 1.0f}, s2 = {0.0f, 1.0f};
         if (has_y) {
             f32x2 y[4];
-            SY::read(a.y, a.tokens, r, c, active, at + SR::kUnits * pitch, pitch, y);
+            SY::read(a.y, a.tokens, r, shift_y, c, active, at + SR::kUnits * pitch, pitch, y);
             s1 = row_stats<LAYER>(y, c, a.post, a, sum);
             const f32x2 v = both(s1.rstd), m = both(-s1.mean * s1.rstd);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                y[e] = LAYER ? fma2(fma2(y[e], v, m), w1[e], b1[e]) : mul2(mul2(y[e], v), w1[e]);
+            for (int e = 0; e < 4; ++e) {
+                y[e] = LAYER ? fma2(y[e], v, m) : mul2(y[e], v);
+                y[e] = BIAS1 ? fma2(y[e], w1[e], b1[e]) : mul2(y[e], w1[e]);
+            }
             if (has_gates) {
                 f32x2 g[4];
-                SY::read(a.gate_rows, a.tokens, r, c, active, at + (SR::kUnits + SY::kUnits) * pitch,
+                SY::read(a.gate_rows, a.tokens, r, shift_g, c, active, at + (SR::kUnits + SY::kUnits) * pitch,
                          pitch, g);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], g[e]);
@@ -172,34 +176,37 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
     sum.finish();
 }
 
-template <typename R, typename Y, bool ALIGNED, bool LAYER, bool ANY>
+template <typename R, typename Y, bool ALIGNED, int NORMS, bool ANY>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    return launch_staged(residual_norm_fwd_kernel<R, Y, ALIGNED, LAYER, ANY>, a,
+    return launch_staged(residual_norm_fwd_kernel<R, Y, ALIGNED, NORMS, ANY>, a,
                          fwd_units<R, Y, ALIGNED, ANY>(), fwd_stages<R, Y, ALIGNED, ANY>(), s);
 }
 
 // A kernel that can do everything has to ask, row for row, what it is to do: the
 // usual calls have kernels of their own.
+template <typename R, typename Y, bool ALIGNED>
+cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
+{
+    if (!a.y.p || !a.u || a.gate_rows.p || a.tokens != 0 || a.plan.cluster > 1 || a.plan.uneven)
+        return launch<R, Y, ALIGNED, 2, true>(a, s);
+    if (a.b1.p) return launch<R, Y, ALIGNED, 2, false>(a, s);
+    if (a.post == GBSSIM_ROW_LAYER || a.pre == GBSSIM_ROW_LAYER || a.b2.p)
+        return launch<R, Y, ALIGNED, 1, false>(a, s);
+    return launch<R, Y, ALIGNED, 0, false>(a, s);
+}
+
 template <typename R, typename Y>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    const bool any = !a.y.p || !a.u || a.gate_rows.p || a.tokens != 0 || a.plan.cluster > 1;
-    const bool layer = a.post == GBSSIM_ROW_LAYER || a.pre == GBSSIM_ROW_LAYER || a.b1.p || a.b2.p;
-    if (a.plan.aligned)
-        return any     ? launch<R, Y, true, true, true>(a, s)
-               : layer ? launch<R, Y, true, true, false>(a, s)
-                       : launch<R, Y, true, false, false>(a, s);
-    return any     ? launch<R, Y, false, true, true>(a, s)
-           : layer ? launch<R, Y, false, true, false>(a, s)
-                   : launch<R, Y, false, false, false>(a, s);
+    return a.plan.aligned ? launch<R, Y, true>(a, s) : launch<R, Y, false>(a, s);
 }
 
 }  // namespace
 
 cudaError_t residual_norm_cluster_room(ClusterRoom *room)
 {
-    const auto kernel = residual_norm_fwd_kernel<float, float, true, true, true>;
+    const auto kernel = residual_norm_fwd_kernel<float, float, true, 2, true>;
     constexpr int kAlone = 120 * 1024;  // shared memory that leaves an SM room for one block
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedBlock);
