@@ -57,13 +57,13 @@ struct ScaleTable {
     long long count[CAP];
     unsigned first[CAP + 1];
     unsigned char type[CAP], out_type[CAP];
-    unsigned char pad[CAP];  // elements by which chunks are shifted, or kScalar
+    unsigned char pad[CAP];  // elements by which chunks are shifted, and kApart
     int n;
     int in_place;  // every output is its gradient
     const float *coef;
 };
 
-constexpr unsigned char kScalar = 255;
+constexpr unsigned char kApart = 8;  // gradient and output are not aligned alike
 constexpr int kCapSmall = 32, kCapLarge = 1024;
 static_assert(sizeof(ScaleTable<kCapLarge>) <= 32764, "kernel parameter space");
 static_assert(sizeof(NormTable<kCapLarge>) <= 32764, "kernel parameter space");
@@ -249,33 +249,118 @@ __global__ void __launch_bounds__(kThreads)
 
 // ------------------------------------------------------------------ the scaling
 
+// Groups of V consecutive elements: 8 where both types have 16 bits, else 4, so
+// that a lane's access is at most 16 bytes and a warp's whole lines.
+template <typename T, typename O>
+constexpr int kGroup = sizeof(T) == 2 && sizeof(O) == 2 ? 8 : 4;
+
+template <typename T, int V>
+struct Group {
+    static constexpr int kWords = V * int(sizeof(T)) / 4;
+    uint32_t w[kWords];
+};
+
+template <typename T, int V>
+__device__ __forceinline__ Group<T, V> load_group(const T *p)
+{
+    Group<T, V> g;
+    if constexpr (Group<T, V>::kWords == 4) {
+        const uint4 q = ld_stream16(p);
+        g.w[0] = q.x; g.w[1] = q.y; g.w[2] = q.z; g.w[3] = q.w;
+    } else {
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(g.w[0]), "=r"(g.w[1])
+                     : "l"(p));
+    }
+    return g;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack_group(const Group<T, V> &g, float (&v)[V])
+{
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = __uint_as_float(g.w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 h = unpack2<T>(g.w[i]);
+            v[2 * i] = h.x;
+            v[2 * i + 1] = h.y;
+        }
+    }
+}
+
+template <typename O, int V>
+__device__ __forceinline__ void store_group(O *p, const float (&v)[V])
+{
+    uint32_t w[V * int(sizeof(O)) / 4];
+    if constexpr (sizeof(O) == 4) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) w[i] = pack2<O>(v[2 * i], v[2 * i + 1]);
+    }
+    if constexpr (V * sizeof(O) == 16) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+}
+
 // Chunk k: elements [k E - pad, (k + 1) E - pad) of the tensor, E = kScaleElems.
-// Whole chunks whose groups of eight lie on 16-byte boundaries in both tensors
-// take 16-byte accesses; the first and last chunk of a tensor, and all chunks
-// where gradient and output reach a boundary at different elements, one element
-// a lane, which still fills whole lines a warp.
+// Whole chunks whose groups are aligned in both tensors take one access a group.
+// Where 16-bit gradients and their output reach a group's boundary at different
+// elements (apart), the gradients' own aligned words go through shared memory and
+// come out again as the output's groups.  The first and last chunk of a tensor,
+// and float32 gradients apart from their output, take one element a lane, which
+// still fills whole lines a warp.
 template <typename T, typename O>
 __device__ __noinline__ void scale_chunk(const void *gv, void *ov, long long n, unsigned k,
-                                            int pad, float c)
+                                         int pad, bool apart, float c, uint4 *stage)
 {
-    constexpr int kEach = kScaleElems / kThreads;
+    constexpr int kEach = kScaleElems / kThreads, V = kGroup<T, O>;
     const T *g = static_cast<const T *>(gv);
     O *o = static_cast<O *>(ov);
-    const bool scalar = pad == kScalar;
-    long long e0 = (long long)k * kScaleElems - (scalar ? 0 : pad);
-    if (!scalar && e0 >= 0 && e0 + kScaleElems <= n) {
-        g += e0 + threadIdx.x * 8;
-        o += e0 + threadIdx.x * 8;
-        Raw8<T> r[kEach / 8];
+    long long e0 = (long long)k * kScaleElems - pad;
+    if constexpr (sizeof(T) == 2) {
+        constexpr int kWords = kScaleElems * 2 / 16;
+        if (apart && e0 >= 8 && e0 + kScaleElems + 8 <= n) {
+            const uintptr_t at = reinterpret_cast<uintptr_t>(g + e0);
+            const T *word = reinterpret_cast<const T *>(at & ~uintptr_t(15));
+            const int shift = int(at & 15) / 2;
+            uint4 r[kWords / kThreads];
 #pragma unroll
-        for (int j = 0; j < kEach / 8; ++j) r[j] = ld8_stream(g + j * (kThreads * 8));
+            for (int j = 0; j < kWords / kThreads; ++j)
+                r[j] = ld_stream16(word + (threadIdx.x + j * kThreads) * 8);
+            __syncthreads();  // the chunk before has been read out
 #pragma unroll
-        for (int j = 0; j < kEach / 8; ++j) {
-            float v[8];
-            unpack8<T>(r[j], v);
+            for (int j = 0; j < kWords / kThreads; ++j) stage[threadIdx.x + j * kThreads] = r[j];
+            if (threadIdx.x == 0) stage[kWords] = ld_stream16(word + kWords * 8);
+            __syncthreads();
+            const T *in = reinterpret_cast<const T *>(stage) + shift + threadIdx.x * V;
+            o += e0 + threadIdx.x * V;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= c;
-            st8(o + j * (kThreads * 8), pack8<O>(v));
+            for (int j = 0; j < kEach / V; ++j) {
+                float v[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = to_f32(in[j * (kThreads * V) + i]) * c;
+                store_group<O, V>(o + j * (kThreads * V), v);
+            }
+            return;
+        }
+    }
+    if (!apart && e0 >= 0 && e0 + kScaleElems <= n) {
+        g += e0 + threadIdx.x * V;
+        o += e0 + threadIdx.x * V;
+        Group<T, V> r[kEach / V];
+#pragma unroll
+        for (int j = 0; j < kEach / V; ++j) r[j] = load_group<T, V>(g + j * (kThreads * V));
+#pragma unroll
+        for (int j = 0; j < kEach / V; ++j) {
+            float v[V];
+            unpack_group<T, V>(r[j], v);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] *= c;
+            store_group<O, V>(o + j * (kThreads * V), v);
         }
         return;
     }
@@ -299,35 +384,38 @@ __device__ __noinline__ void scale_chunk(const void *gv, void *ov, long long n, 
 
 template <typename T>
 __device__ __forceinline__ void scale_chunk_to(int out_type, const void *g, void *o, long long n,
-                                               unsigned k, int pad, float c)
+                                               unsigned k, int pad, bool apart, float c,
+                                               uint4 *stage)
 {
-    if (out_type == GBSSIM_F32) scale_chunk<T, float>(g, o, n, k, pad, c);
-    else if (out_type == GBSSIM_BF16) scale_chunk<T, bf16>(g, o, n, k, pad, c);
-    else scale_chunk<T, f16>(g, o, n, k, pad, c);
+    if (out_type == GBSSIM_F32) scale_chunk<T, float>(g, o, n, k, pad, apart, c, stage);
+    else if (out_type == GBSSIM_BF16) scale_chunk<T, bf16>(g, o, n, k, pad, apart, c, stage);
+    else scale_chunk<T, f16>(g, o, n, k, pad, apart, c, stage);
 }
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, 4)
     grad_scale_kernel(const __grid_constant__ ScaleTable<CAP> t)
 {
-    unsigned c0, c1;
-    block_run(t.first[t.n], c0, c1);
+    __shared__ uint4 stage[kScaleElems * 2 / 16 + 1];
     pdl_wait();
     const float c = __ldcg(t.coef);
     if (t.in_place && c == 1.0f) return;  // 1 * g is g, to the bit
-    if (c0 >= c1) return;
-    // from the end: the norm's blocks read their runs forwards, so the last
-    // chunks are those that L2 still holds
-    int i = tensor_of(t, c1 - 1);
-    for (unsigned q = c1; q-- > c0;) {
-        while (t.first[i] > q) --i;
+    const unsigned chunks = t.first[t.n];
+    // neighbouring chunks by neighbouring blocks: reading and writing at once,
+    // blocks in runs of their own took 142 us for 59 M float32, these 116.  From
+    // the end, which the norm read last.
+    for (unsigned done = blockIdx.x; done < chunks; done += gridDim.x) {
+        const unsigned q = chunks - 1 - done;
+        const int i = tensor_of(t, q);
         const unsigned k = q - t.first[i];
+        const int pad = t.pad[i] & 7;
+        const bool apart = t.pad[i] & kApart;
         if (t.type[i] == GBSSIM_F32)
-            scale_chunk_to<float>(t.out_type[i], t.g[i], t.out[i], t.count[i], k, t.pad[i], c);
+            scale_chunk_to<float>(t.out_type[i], t.g[i], t.out[i], t.count[i], k, pad, apart, c, stage);
         else if (t.type[i] == GBSSIM_BF16)
-            scale_chunk_to<bf16>(t.out_type[i], t.g[i], t.out[i], t.count[i], k, t.pad[i], c);
+            scale_chunk_to<bf16>(t.out_type[i], t.g[i], t.out[i], t.count[i], k, pad, apart, c, stage);
         else
-            scale_chunk_to<f16>(t.out_type[i], t.g[i], t.out[i], t.count[i], k, t.pad[i], c);
+            scale_chunk_to<f16>(t.out_type[i], t.g[i], t.out[i], t.count[i], k, pad, apart, c, stage);
     }
 }
 
@@ -354,21 +442,16 @@ long long norm_chunks(const void *g, long long count, int type)
     return ceil_div(ceil_div(count + pad, v), kChunkWords);
 }
 
-// Elements from the 16-byte boundary at or before p to p.
-int lead(const void *p, int type)
+// The shift of a tensor's chunks that aligns the groups of its output, and whether
+// it leaves those of its gradient unaligned.
+unsigned char chunk_pad(const void *g, int type, const void *o, int out_type)
 {
-    return int(reinterpret_cast<uintptr_t>(p) & 15) / dtype_bytes(type);
-}
-
-// The shift of a tensor's chunks that puts both its gradient's and its
-// output's groups of eight on 16-byte boundaries, if there is one.
-unsigned char shared_pad(const void *g, int type, const void *o, int out_type)
-{
-    const int a = lead(g, type), b = lead(o, out_type);
-    if (type != GBSSIM_F32 && out_type != GBSSIM_F32) return a == b ? a : kScalar;
-    if (type == GBSSIM_F32 && out_type == GBSSIM_F32) return a == b ? a : kScalar;
-    const int wide = type == GBSSIM_F32 ? b : a, narrow = type == GBSSIM_F32 ? a : b;
-    return (wide & 3) == narrow ? wide : kScalar;
+    const int group = type != GBSSIM_F32 && out_type != GBSSIM_F32 ? 8 : 4;
+    const auto lead = [&](const void *p, int t) {
+        return int(reinterpret_cast<uintptr_t>(p) / dtype_bytes(t) % group);
+    };
+    const int pad = lead(o, out_type);
+    return (unsigned char)(lead(g, type) == pad ? pad : pad | kApart);
 }
 
 unsigned grid_for(long long chunks, int sm_count)
@@ -432,10 +515,10 @@ cudaError_t launch_scale(const List &l, int i0, int n, bool in_place, int sm_cou
         t.count[i] = l.count[i0 + i];
         t.type[i] = l.type[i0 + i];
         t.out_type[i] = l.out_type[i0 + i];
-        t.pad[i] = shared_pad(t.g[i], t.type[i], t.out[i], t.out_type[i]);
+        t.pad[i] = chunk_pad(t.g[i], t.type[i], t.out[i], t.out_type[i]);
         t.first[i] = unsigned(chunks);
         if (t.count[i] > 0)
-            chunks += ceil_div(t.count[i] + (t.pad[i] == kScalar ? 0 : t.pad[i]), kScaleElems);
+            chunks += ceil_div(t.count[i] + (t.pad[i] & 7), kScaleElems);
     }
     t.first[n] = unsigned(chunks);
     t.in_place = in_place;
