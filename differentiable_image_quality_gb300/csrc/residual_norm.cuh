@@ -130,7 +130,9 @@ struct BlockRows {
 template <bool ALIGNED>
 struct Cols {
     int first, from, upto;
-    int t;  // place in the team
+    int t;            // place in the team
+    int lane, lanes;  // and in its lanes of this warp
+    int words;        // 16-byte words of float32 that those lanes have of a row (ALIGNED)
     __device__ __forceinline__ Cols(const ResidualNormArgs &a, int cluster, int shift)
     {
         const int rank = int(blockIdx.x) % cluster;
@@ -138,6 +140,10 @@ struct Cols {
         first = rank * a.plan.block_cols + t * kColsPerThread - (ALIGNED ? 0 : shift);
         from = max(0, -first);
         upto = t * kColsPerThread < a.plan.block_cols ? max(0, min(kColsPerThread, a.dim - first)) : 0;
+        lanes = min(a.plan.tpr, 32);
+        lane = t & (lanes - 1);
+        const int group = (t - lane) * kColsPerThread;  // columns of the block ahead of these lanes
+        words = max(0, min(a.plan.block_cols - group, a.dim - (first - lane * kColsPerThread))) / 4;
     }
     __device__ __forceinline__ bool any() const { return from < upto; }
     __device__ __forceinline__ bool all() const { return ALIGNED ? upto > 0 : upto - from == 8; }
@@ -161,6 +167,11 @@ __device__ __forceinline__ const unsigned char *row_at(const RowPtr &p, int toke
 // of a row some rows ahead (cp.async) and reads them back itself, so the copies
 // need no barrier.  A stage holds, per tensor, 16-byte words [word][thread].
 //
+// Eight float32 columns are two words.  Aligned rows: the lanes of a team in a warp
+// copy one another's, so that a copy of the warp covers whole lines: lane g takes
+// words g and g + lanes, word w being the (w % 2)th of lane w / 2.  (Each lane its
+// own two words, 32 bytes apart, would ask L2 for every sector twice.)
+//
 // Where a tensor's rows are not aligned as the block's columns are, a thread
 // copies the aligned words that its columns lie in -- one more than they fill --
 // and shifts.  Near the tensor's first and last element the words are put
@@ -173,10 +184,18 @@ struct Staged {
     static __device__ __forceinline__ void fetch(const RowPtr &p, const unsigned char *at,
                                                  const Cols<ALIGNED> &c, unsigned slot, int pitch)
     {
-        if constexpr (ALIGNED) {
+        if constexpr (ALIGNED && sizeof(T) == 4) {
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u) copy16_async<false>(slot + u * pitch, at + u * 16);
+            for (int u = 0; u < 2; ++u) {
+                const int w = c.lane + u * c.lanes, other = w / 2 - c.lane;
+                if (w < c.words)
+                    copy16_async<false>(slot + other * 16 + (w & 1) * pitch,
+                                        at + (w - 2 * c.lane) * 16);
+            }
+        } else if constexpr (ALIGNED) {
+            if (c.any()) copy16_async<false>(slot, at);
         } else {
+            if (!c.any()) return;
             const unsigned char *word = at - (reinterpret_cast<uintptr_t>(at) & 15);
             if (c.all() && word == at) {
 #pragma unroll
@@ -271,11 +290,11 @@ __device__ __forceinline__ void store_cols(T *to, const Cols<ALIGNED> &c, bool a
                                            const f32x2 (&v)[4])
 {
     if constexpr (ALIGNED) {
-        if (active && c.any()) st8(to, pack8<T>(v));
+        if (active && c.any()) st8_whole(to, pack8<T>(v));
     } else {
         if (!active) return;
-        if (c.all() && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
-            st8(to, pack8<T>(v));
+        if (c.all() && reinterpret_cast<uintptr_t>(to) % (8 * sizeof(T)) == 0) {
+            st8_whole(to, pack8<T>(v));
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {

@@ -107,6 +107,12 @@ int inputs_of(const gbssim_residual_norm &d, Extent *e)
 
 bool multiple16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// Eight elements of an output are stored at once.
+bool out_aligned(const void *p, int dtype)
+{
+    return reinterpret_cast<uintptr_t>(p) % (8 * dtype_bytes(dtype)) == 0;
+}
+
 bool rows_aligned(const gbssim_residual_norm &d, const gbssim_rows &r, int dtype)
 {
     const int v = 16 / dtype_bytes(dtype);
@@ -299,7 +305,8 @@ extern "C" int gbssim_residual_norm_fwd(const gbssim_residual_norm *d, void *x_o
     ResidualNormArgs a = make_args(*d);
     a.plan = make_plan(*d, kFwdThreadsPerSm, room);
     if (!grid_fits(a.plan)) return GBSSIM_ESHAPE;
-    a.plan.aligned = inputs_aligned(*d) && multiple16(x_out_or_null) && multiple16(u_or_null);
+    a.plan.aligned = inputs_aligned(*d) && out_aligned(x_out_or_null, d->res_dtype) &&
+                     out_aligned(u_or_null, d->blk_dtype);
     a.tokens = one_stride(*d, d->x) && one_stride(*d, d->y) && one_stride(*d, d->gate_rows)
                    ? 0
                    : d->tokens;
@@ -386,8 +393,9 @@ extern "C" int gbssim_residual_norm_bwd(const gbssim_residual_norm *d,
     a.plan = make_plan(*d, kBwdThreadsPerSm, room);
     if (!grid_fits(a.plan)) return GBSSIM_ESHAPE;
     a.plan.aligned = inputs_aligned(*d) && rows_aligned(*d, gx, d->res_dtype) &&
-                     rows_aligned(*d, gu, d->blk_dtype) && multiple16(grads->x) &&
-                     multiple16(grads->y) && (!d->gate_rows.data || multiple16(grads->gate));
+                     rows_aligned(*d, gu, d->blk_dtype) && out_aligned(grads->x, d->res_dtype) &&
+                     out_aligned(grads->y, d->blk_dtype) &&
+                     (!d->gate_rows.data || out_aligned(grads->gate, d->blk_dtype));
     a.tokens = one_stride(*d, d->x) && one_stride(*d, d->y) && one_stride(*d, d->gate_rows) &&
                        one_stride(*d, gx) && one_stride(*d, gu)
                    ? 0

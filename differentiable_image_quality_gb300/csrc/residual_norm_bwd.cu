@@ -110,9 +110,11 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
               shift_gx = SR::shift_of(a.gx, a.tokens, rows.first, c),
               shift_gu = SY::shift_of(a.gu, a.tokens, rows.first, c),
               shift_g = SY::shift_of(a.gate_rows, a.tokens, rows.first, c);
-    int ahead = r, ahead_left = c.any() ? left : 0;
+    int ahead = r, ahead_left = left;
     unsigned to = mine;
+    constexpr bool kShared = sizeof(R) == 4 || sizeof(Y) == 4;  // lanes copy for one another
     const auto fetch = [&] {
+        if (kShared) __syncwarp();  // the stage has been read by all lanes
         if (ahead_left > 0) {
             SR::fetch(a.x, row_at<R, ANY>(a.x, a.tokens, ahead, c.first), c, to, pitch);
             if (has_gx)
@@ -160,6 +162,7 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 1)
         st_next = left > a.plan.teams ? a.stats[r + step] : make_float4(0.0f, 1.0f, 0.0f, 1.0f);
         fetch();
         staged_wait<kStages - 1>();
+        if (kShared) __syncwarp();
 
         f32x2 yh[4], xh[4], T[4], g[4];
         SR::read(a.x, a.tokens, r, shift_x, c, active, at, pitch, xh);

@@ -91,9 +91,11 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
     const int shift_x = SR::shift_of(a.x, a.tokens, rows.first, c),
               shift_y = SY::shift_of(a.y, a.tokens, rows.first, c),
               shift_g = SY::shift_of(a.gate_rows, a.tokens, rows.first, c);
-    int ahead = r, ahead_left = c.any() ? left : 0;
+    int ahead = r, ahead_left = left;
     unsigned to = mine;
+    constexpr bool kShared = sizeof(R) == 4 || sizeof(Y) == 4;  // lanes copy for one another
     const auto fetch = [&] {
+        if (kShared) __syncwarp();  // the stage has been read by all lanes
         if (ahead_left > 0) {
             SR::fetch(a.x, row_at<R, ANY>(a.x, a.tokens, ahead, c.first), c, to, pitch);
             if (has_y)
@@ -134,6 +136,7 @@ __global__ void __launch_bounds__(kMaxTeamThreads, 2)
         const bool active = left > 0;
         fetch();
         staged_wait<kStages - 1>();
+        if (kShared) __syncwarp();
         f32x2 x[4];
         SR::read(a.x, a.tokens, r, shift_x, c, active, at, pitch, x);
         RowStats s1 = {0.0f, 1.0f}, s2 = {0.0f, 1.0f};
