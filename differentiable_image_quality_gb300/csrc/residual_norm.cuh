@@ -20,12 +20,12 @@ namespace gbssim {
 // Every thread owns eight columns of a row for the whole kernel, so that the
 // parameters of its columns and their gradients' sums stay in registers.  A row
 // belongs to a team: `tpr` lanes of a warp (a power of two) for rows of up to
-// 256 columns, a block of up to 512 threads for up to 4096, a cluster of two or
-// four such blocks above.
+// 256 columns, else a block, and a cluster of blocks for rows that are wider than
+// a block's threads (64 registers each in the forward, 128 in the backward).
 constexpr int kColsPerThread = 8;
-constexpr int kMaxTeamThreads = 512;
+constexpr int kFwdThreads = 1024, kBwdThreads = 512;  // of a block, at most
 constexpr int kSmallBlock = 128;  // threads of a block that holds several teams
-constexpr int kMaxDim = 4 * kMaxTeamThreads * kColsPerThread;
+constexpr int kMaxDim = 16384;    // 2 forward or 4 backward blocks
 
 struct RowPtr {
     const void *p;
@@ -355,10 +355,10 @@ __device__ __forceinline__ void send16(unsigned to, float4 v, unsigned bar)
 // cluster-wide barrier would first wait for the rows that the blocks have just
 // stored.)
 struct TeamSlots {
-    float warps[2][4][16];     // [parity][value][warp]
+    float warps[2][4][32];     // [parity][value][warp]
     float4 blocks[2][4];       // [parity][block]
     uint64_t arrived[2];
-    float2 columns[16];        // of each warp: how many, and 1 / that
+    float2 columns[32];        // of each warp: how many, and 1 / that
     float2 block_columns[4];   // of each block
 };
 
@@ -406,15 +406,22 @@ struct TeamSum {
         return v;
     }
 
-    // Sum over 16 lanes that hold the warps' values.
-    __device__ __forceinline__ float sixteen(float v) const
+    // Sum over the lanes that hold the warps' values: all, or each half alike.
+    __device__ __forceinline__ float over_warps(float v) const
     {
+        if (warps > 16) v += __shfl_xor_sync(0xffffffffu, v, 16);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     }
 
-    // The warps' values, one warp to each lane of a half warp.  One barrier: the
+    // The warp whose value this lane takes.
+    __device__ __forceinline__ int my_warp() const
+    {
+        return threadIdx.x & (warps > 16 ? 31 : 15);
+    }
+
+    // The warps' values, one warp to each lane of a warp or of a half.  One barrier: the
     // slots alternate, and a thread that writes a slot again has passed the
     // barrier of the sum in between, which every thread reaches only after it has
     // read this one.
@@ -429,7 +436,7 @@ struct TeamSum {
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            v[k] = (lane & 15) < warps ? slots.warps[parity][k][lane & 15] : 0.0f;
+            v[k] = my_warp() < warps ? slots.warps[parity][k][my_warp()] : 0.0f;
     }
 
     // This block's values to all blocks, and all blocks' into slots.blocks.  A
@@ -460,7 +467,7 @@ struct TeamSum {
         if (warps == 1 && cluster == 1) return;
         of_warps(v);
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = sixteen(v[k]);
+        for (int k = 0; k < N; ++k) v[k] = over_warps(v[k]);
         if (cluster > 1) {
             exchange(make_float4(v[0], v[N > 1 ? 1 : 0], v[N > 2 ? 2 : 0], v[N > 3 ? 3 : 0]));
 #pragma unroll
@@ -498,8 +505,8 @@ struct TeamSum {
         const int lane = threadIdx.x & 31;
         float w[1] = {n};
         of_warps(w);
-        if (threadIdx.x < 16) slots.columns[lane] = with_inverse(w[0]);
-        const float block = sixteen(w[0]);
+        if (threadIdx.x < 32) slots.columns[lane] = with_inverse(w[0]);
+        const float block = over_warps(w[0]);
         inv_block = with_inverse(block).y;
         if (cluster > 1) {
             exchange(make_float4(block, 0.0f, 0.0f, 0.0f));
@@ -517,13 +524,12 @@ struct TeamSum {
     __device__ __forceinline__ float2 join_squares(float s, float q, float inv_dim)
     {
         if (warps == 1 && cluster == 1) return make_float2(s, q);
-        const int lane = threadIdx.x & 31;
         float w[2] = {s, q};
         of_warps(w);
-        const float2 n = (lane & 15) < warps ? slots.columns[lane & 15] : make_float2(0.0f, 0.0f);
-        const float block = sixteen(w[0]);
+        const float2 n = slots.columns[my_warp()];
+        const float block = over_warps(w[0]);
         const float d = fmaf(w[0], n.y, -block * inv_block);
-        float2 r = make_float2(block, sixteen(fmaf(n.x * d, d, w[1])));
+        float2 r = make_float2(block, over_warps(fmaf(n.x * d, d, w[1])));
         if (cluster > 1) {
             exchange(make_float4(r.x, r.y, 0.0f, 0.0f));
             float2 v[4], c[4];

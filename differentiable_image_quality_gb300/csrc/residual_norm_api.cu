@@ -126,8 +126,8 @@ bool inputs_aligned(const gbssim_residual_norm &d)
            rows_aligned(d, d.y, d.blk_dtype) && rows_aligned(d, d.gate_rows, d.blk_dtype);
 }
 
-// Resident threads of an SM that a plan counts on (64 or 128 registers each).
-constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512;
+// A block's most threads are also the resident threads of an SM that a plan counts
+// on: 64 registers each in the forward, 128 in the backward.
 
 // SMs that a plan counts on at most: bounds the partial sums on any device.
 constexpr int kMaxPlanSms = 256;
@@ -161,7 +161,7 @@ int device_room(Room *out)
 
 // Blocks are planned to run all at once: a block works through its rows in a
 // loop, so that any left over would double the time.
-RowPlan make_plan(const gbssim_residual_norm &d, int threads_per_sm, const Room &room)
+RowPlan make_plan(const gbssim_residual_norm &d, int most_threads, const Room &room)
 {
     RowPlan p{};
     bool own = false;
@@ -176,7 +176,10 @@ RowPlan make_plan(const gbssim_residual_norm &d, int threads_per_sm, const Room 
     p.classes = d.dim % 8 == 0 ? 1 : d.dim % 4 == 0 ? 2 : d.dim % 2 == 0 ? 4 : 8;
     if (p.group_rows < 8 * p.classes || d.dim + 7 > kMaxDim) p.classes = 1;
     const int chunks = (d.dim + (p.classes > 1 ? 7 : 0) + kColsPerThread - 1) / kColsPerThread;
-    p.cluster = chunks <= kMaxTeamThreads ? 1 : chunks <= 2 * kMaxTeamThreads ? 2 : 4;
+    // A cluster's blocks have 512 threads at most, so that the forward has two on an
+    // SM: 4000 x 13000 took 152 us with four blocks a row, 185 with two.
+    const int most_shared = std::min(most_threads, 512);
+    p.cluster = chunks <= most_threads ? 1 : chunks <= 2 * most_shared ? 2 : 4;
     const int per = (chunks + p.cluster - 1) / p.cluster;
     p.block_cols = per * kColsPerThread;
     if (per <= 32) {
@@ -191,7 +194,7 @@ RowPlan make_plan(const gbssim_residual_norm &d, int threads_per_sm, const Room 
     if (rows == 0) return p;
     const long long blocks =
         (long long)(p.cluster == 4 ? room.clusters4 : p.cluster == 2 ? room.clusters2 : room.sms) *
-        (threads_per_sm / p.threads);
+        (most_threads / p.threads);
     const long long items = (long long)p.groups * p.classes;
     p.splits = int(std::max<long long>(
         1, std::min<long long>(ceil_div(blocks, items),
@@ -303,7 +306,7 @@ extern "C" int gbssim_residual_norm_fwd(const gbssim_residual_norm *d, void *x_o
     Room room{};
     if ((rc = device_room(&room))) return rc;
     ResidualNormArgs a = make_args(*d);
-    a.plan = make_plan(*d, kFwdThreadsPerSm, room);
+    a.plan = make_plan(*d, kFwdThreads, room);
     if (!grid_fits(a.plan)) return GBSSIM_ESHAPE;
     a.plan.aligned = inputs_aligned(*d) && out_aligned(x_out_or_null, d->res_dtype) &&
                      out_aligned(u_or_null, d->blk_dtype);
@@ -321,7 +324,7 @@ extern "C" int gbssim_residual_norm_fwd(const gbssim_residual_norm *d, void *x_o
 extern "C" size_t gbssim_residual_norm_workspace_bytes(const gbssim_residual_norm *d)
 {
     if (check_desc(d) != GBSSIM_OK || row_count(*d) == 0) return 0;
-    const RowPlan p = make_plan(*d, kBwdThreadsPerSm, {kMaxPlanSms, kMaxPlanSms / 2, kMaxPlanSms / 4});
+    const RowPlan p = make_plan(*d, kBwdThreads, {kMaxPlanSms, kMaxPlanSms / 2, kMaxPlanSms / 4});
     return size_t(p.groups) * p.classes * p.splits * kMaxSums * d->dim * sizeof(float);
 }
 
@@ -390,7 +393,7 @@ extern "C" int gbssim_residual_norm_bwd(const gbssim_residual_norm *d,
     ResidualNormArgs a = make_args(*d);
     a.gx = row_ptr(*d, gx, d->res_dtype);
     a.gu = row_ptr(*d, gu, d->blk_dtype);
-    a.plan = make_plan(*d, kBwdThreadsPerSm, room);
+    a.plan = make_plan(*d, kBwdThreads, room);
     if (!grid_fits(a.plan)) return GBSSIM_ESHAPE;
     a.plan.aligned = inputs_aligned(*d) && rows_aligned(*d, gx, d->res_dtype) &&
                      rows_aligned(*d, gu, d->blk_dtype) && out_aligned(grads->x, d->res_dtype) &&

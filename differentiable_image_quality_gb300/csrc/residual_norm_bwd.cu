@@ -78,7 +78,7 @@ __device__ __forceinline__ void write_sum(const ResidualNormArgs &a, const Cols<
 // bias, 1 they may but for a bias of the post norm, 2 they may.  ANY: whatever a call may ask for; without it all four inputs and both
 // outputs are there, one stride reaches every row, and a block has whole rows.
 template <typename R, typename Y, bool ALIGNED, bool FULL, int NORMS, bool ANY>
-__global__ void __launch_bounds__(kMaxTeamThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a)
 {
     using SR = Staged<R, ALIGNED, ANY>;
@@ -347,8 +347,9 @@ cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
                       : a.post == GBSSIM_ROW_LAYER || a.pre == GBSSIM_ROW_LAYER || a.sum_e >= 0 ? 1
                                                                                               : 0;
     if (a.gate_rows.p)
-        return any || norms > 0 ? launch<R, Y, ALIGNED, true, 2, true>(a, s)
-                                : launch<R, Y, ALIGNED, true, 0, false>(a, s);
+        return any         ? launch<R, Y, ALIGNED, true, 2, true>(a, s)
+               : norms > 0 ? launch<R, Y, ALIGNED, true, 2, false>(a, s)
+                           : launch<R, Y, ALIGNED, true, 0, false>(a, s);
     return any          ? launch<R, Y, ALIGNED, false, 2, true>(a, s)
            : norms == 2 ? launch<R, Y, ALIGNED, false, 2, false>(a, s)
            : norms == 1 ? launch<R, Y, ALIGNED, false, 1, false>(a, s)

@@ -66,7 +66,7 @@ __device__ __forceinline__ RowStats row_stats(const f32x2 (&v)[4], const Cols<AL
 // the post norm, 2 they may.  ANY: whatever a call may ask for; without it y and u are there, gates are columns', one stride reaches
 // every row, and a block has whole rows.
 template <typename R, typename Y, bool ALIGNED, int NORMS, bool ANY>
-__global__ void __launch_bounds__(kMaxTeamThreads, 2)
+__global__ void __launch_bounds__(kFwdThreads, 1)
     residual_norm_fwd_kernel(const __grid_constant__ ResidualNormArgs a)
 {
     using SR = Staged<R, ALIGNED, ANY>;
@@ -216,7 +216,7 @@ cudaError_t residual_norm_cluster_room(ClusterRoom *room)
     for (int size = 2; size <= 4 && e == cudaSuccess; size *= 2) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(unsigned(size));
-        cfg.blockDim = dim3(kMaxTeamThreads);
+        cfg.blockDim = dim3(512);
         cfg.dynamicSmemBytes = kAlone;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
