@@ -56,12 +56,13 @@ SIGNATURES = {
     "gbssim_residual_norm_bwd": (_i, [_vp, _vp, _vp, _fp, _vp, _vp, _sz, _vp]),
 }
 # exported only by the test build (libgbssim_test.so, csrc/gbssim_test_hooks.h):
-# forced row segments, the staging modes that drive the tests of the bounded-wait
-# failure path, and the per-stage statistics dump
+# forced row segments, the staging and exchange modes that drive the tests of the
+# bounded-wait failure paths, and the per-stage statistics dump
 TEST_SIGNATURES = {
     "gbssim_tune_seg_rows": (None, [_i]),
     "gbssim_tune_staging": (None, [_i]),
     "gbssim_tune_fwd_split": (None, [_i]),
+    "gbssim_tune_exchange": (None, [_i]),
     "gbssim_test_stage_dump2d": (_i, [_fp, _fp, _i, _i, _i, _i, _i, _fp, _fp, _fp, _fp, _vp]),
 }
 

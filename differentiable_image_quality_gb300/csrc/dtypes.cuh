@@ -194,13 +194,16 @@ __device__ __forceinline__ void copy16_async(unsigned smem, const void *gmem)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
 }
 
-__device__ __forceinline__ uint4 ld_shared16(unsigned smem)
+// Zeros, and nothing read, where `wanted` is false (a predicate, no branch).
+__device__ __forceinline__ uint4 ld_shared16(unsigned smem, bool wanted)
 {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(smem)
-                 : "memory");
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n"
+        " @p ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+        : "r"(smem), "r"(unsigned(wanted))
+        : "memory");
     return v;
 }
 

@@ -511,7 +511,7 @@ int gbssim_device_status(unsigned *flags_out)
     if (!flags_out) return GBSSIM_EINVAL;
     *flags_out = 0;
     for (const auto status : {ssim2d_staging_status, ssim3d_staging_status, residual_norm_fwd_status,
-                              residual_norm_bwd_status}) {
+                              residual_norm_bwd_f32_status, residual_norm_bwd_16_status}) {
         unsigned f = 0;
         const cudaError_t e = status(&f, true);
         if (e != cudaSuccess) return cuda_fail(e);

@@ -26,6 +26,12 @@ void gbssim_tune_staging(int mode);
  * inputs allow tensor copies (on = 1, the default). */
 void gbssim_tune_fwd_split(int on);
 
+/* Bytes that every later exchange of sums between blocks of a residual norm
+ * announces beyond those it sends: more than 0, and the bounded waits of rows
+ * that several blocks share run out (the failure path: NaN outputs, the device
+ * status bit).  0 restores the product behaviour. */
+void gbssim_tune_exchange(int extra_bytes);
+
 /* Stage-by-stage parity of the 2D gradient kernel: one run of the kernel of
  * ssim_fwd's stored variant with grad2 on img1 / img2 ([N, C, H, W] float32,
  * device) that also writes, for every output pixel of [N, C, Ho, Wo]:

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads)
     grad_norm_kernel(const __grid_constant__ NormTable<CAP> t)
 {
     __shared__ double scratch[kThreads / 32];
-    if (t.coef) pdl_trigger();  // only the scaling kernel starts early
+    if (t.coef && t.first[t.n]) pdl_trigger();  // only the scaling kernel starts early
     unsigned c0, c1;
     block_run(t.first[t.n], c0, c1);
     double sum = 0.0;

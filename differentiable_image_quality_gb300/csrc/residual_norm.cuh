@@ -50,6 +50,7 @@ struct ParamPtr {
 struct RowPlan {
     int aligned;       // rows start on 16-byte boundaries in every tensor
     int uneven;        // a tensor's rows change their alignment within a block
+    int even_out;      // a block's columns of an output are aligned in groups of eight
     int classes;       // 8 / gcd(8, D); 1 also where a group has too few rows to part
     int cluster;       // blocks of a cluster (1, 2, 4)
     int block_cols;    // columns of a block: a multiple of 8 (counted from the shift)
@@ -96,9 +97,12 @@ cudaError_t residual_norm_cluster_room(ClusterRoom *room);
 cudaError_t residual_norm_fwd_launch(const ResidualNormArgs &a, int res, int blk, cudaStream_t s);
 cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk,
                                      const ParamGrads &g, cudaStream_t s);
+cudaError_t residual_norm_bwd_f32_launch(const ResidualNormArgs &a, int blk, cudaStream_t s);
+cudaError_t residual_norm_bwd_16_launch(const ResidualNormArgs &a, int blk, cudaStream_t s);
 // Kernel-side failures on the current device since the last call that cleared them.
 cudaError_t residual_norm_fwd_status(unsigned *flags, bool clear);
-cudaError_t residual_norm_bwd_status(unsigned *flags, bool clear);
+cudaError_t residual_norm_bwd_f32_status(unsigned *flags, bool clear);
+cudaError_t residual_norm_bwd_16_status(unsigned *flags, bool clear);
 
 #ifdef __CUDACC__
 
@@ -133,6 +137,7 @@ struct Cols {
     int t;            // place in the team
     int lane, lanes;  // and in its lanes of this warp
     int words;        // 16-byte words of float32 that those lanes have of a row (ALIGNED)
+    bool whole;       // all eight, and outputs' groups of eight are aligned
     __device__ __forceinline__ Cols(const ResidualNormArgs &a, int cluster, int shift)
     {
         const int rank = int(blockIdx.x) % cluster;
@@ -140,6 +145,7 @@ struct Cols {
         first = rank * a.plan.block_cols + t * kColsPerThread - (ALIGNED ? 0 : shift);
         from = max(0, -first);
         upto = t * kColsPerThread < a.plan.block_cols ? max(0, min(kColsPerThread, a.dim - first)) : 0;
+        whole = upto - from == kColsPerThread && a.plan.even_out;
         lanes = min(a.plan.tpr, 32);
         lane = t & (lanes - 1);
         const int group = (t - lane) * kColsPerThread;  // columns of the block ahead of these lanes
@@ -219,45 +225,41 @@ struct Staged {
         }
     }
 
-    // By how many elements the thread's columns of a row lie past a 16-byte
-    // boundary.  The same in every row of a block, unless ANY.
-    static __device__ __forceinline__ int shift_of(const RowPtr &p, int tokens, int row,
-                                                   const Cols<ALIGNED> &c)
+    // By how many elements a block's columns of a row (`from` is the first) lie past
+    // a 16-byte boundary; the same for all its threads.
+    static __device__ __forceinline__ int shift_of(const RowPtr &p, int tokens, int row, int from)
     {
         if (ALIGNED || !p.p) return 0;
-        return int(reinterpret_cast<uintptr_t>(row_at<T, ANY>(p, tokens, row, c.first)) & 15) /
+        return int(reinterpret_cast<uintptr_t>(row_at<T, ANY>(p, tokens, row, from)) & 15) /
                int(sizeof(T));
     }
 
-    // The thread's columns of a row, zero where the row has none; known: its shift
-    // where that is the same in every row.
+    // The thread's columns of a row, zero where the row has none.  known: the shift,
+    // where that is the same in all rows of a block (it is unless ANY).
     static __device__ __forceinline__ void read(const RowPtr &p, int tokens, int row, int known,
                                                 const Cols<ALIGNED> &c, bool active, unsigned slot,
                                                 int pitch, f32x2 (&v)[4])
     {
-        Raw8<T> r{};
+        Raw8<T> r;
+        const bool wanted = active && c.any();
         if constexpr (ALIGNED) {
-            if (active && c.any()) {
 #pragma unroll
-                for (int u = 0; u < kUnits; ++u) r.w[u] = ld_shared16(slot + u * pitch);
-            }
+            for (int u = 0; u < kUnits; ++u) r.w[u] = ld_shared16(slot + u * pitch, wanted);
             unpack8<T>(r, v);
         } else {
-            if (active && c.any()) {
-                const int s = ANY ? shift_of(p, tokens, row, c) : known;
-                if (s == 0) {
+            const int s = ANY ? shift_of(p, tokens, row, c.first) : known;
+            if (s == 0) {
 #pragma unroll
-                    for (int u = 0; u < kUnits - 1; ++u) r.w[u] = ld_shared16(slot + u * pitch);
-                } else {
-                    Wide8<T> w;
+                for (int u = 0; u < kUnits - 1; ++u) r.w[u] = ld_shared16(slot + u * pitch, wanted);
+            } else {
+                Wide8<T> w;
 #pragma unroll
-                    for (int u = 0; u < kUnits; ++u) {
-                        const uint4 q = ld_shared16(slot + u * pitch);
-                        w.w[4 * u] = q.x; w.w[4 * u + 1] = q.y;
-                        w.w[4 * u + 2] = q.z; w.w[4 * u + 3] = q.w;
-                    }
-                    r = shift_down<T>(w, s);
+                for (int u = 0; u < kUnits; ++u) {
+                    const uint4 q = ld_shared16(slot + u * pitch, wanted);
+                    w.w[4 * u] = q.x; w.w[4 * u + 1] = q.y;
+                    w.w[4 * u + 2] = q.z; w.w[4 * u + 3] = q.w;
                 }
+                r = shift_down<T>(w, s);
             }
             float f[8];
             unpack8<T>(r, f);
@@ -283,8 +285,8 @@ __device__ __forceinline__ void staged_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-// Stores the thread's columns of a row, the first at `to`: in whole words where
-// it has all eight and they are aligned, one by one at a row's ends.
+// Stores the thread's columns of a row, the first at `to`: whole where it has all
+// eight and they are aligned, one by one at a row's ends.
 template <typename T, bool ALIGNED>
 __device__ __forceinline__ void store_cols(T *to, const Cols<ALIGNED> &c, bool active,
                                            const f32x2 (&v)[4])
@@ -292,10 +294,9 @@ __device__ __forceinline__ void store_cols(T *to, const Cols<ALIGNED> &c, bool a
     if constexpr (ALIGNED) {
         if (active && c.any()) st8_whole(to, pack8<T>(v));
     } else {
-        if (!active) return;
-        if (c.all() && reinterpret_cast<uintptr_t>(to) % (8 * sizeof(T)) == 0) {
+        if (active && c.whole) {
             st8_whole(to, pack8<T>(v));
-        } else {
+        } else if (active) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float2 h = halves(v[e / 2]);
@@ -382,7 +383,8 @@ struct TeamSum {
 
     __device__ __forceinline__ TeamSum(TeamSlots &s, const ResidualNormArgs &a)
         : slots(s), parity(0), tpr(a.plan.tpr), warps(a.plan.teams > 1 ? 1 : a.plan.threads / 32),
-          cluster(CLUSTER ? a.plan.cluster : 1), phases(0), extra(a.exchange_extra), dead(false), inv_columns(0.0f), inv_block(0.0f)
+          cluster(CLUSTER ? a.plan.cluster : 1), phases(0), extra(a.exchange_extra), dead(false),
+          inv_columns(0.0f), inv_block(0.0f)
     {
         if (cluster == 1) return;
         if (threadIdx.x == 0) {
@@ -439,22 +441,32 @@ struct TeamSum {
             v[k] = my_warp() < warps ? slots.warps[parity][k][my_warp()] : 0.0f;
     }
 
+    // A row whose sums did not arrive has no result.
+    __device__ __forceinline__ float or_nan(float v) const
+    {
+        return dead ? __uint_as_float(0x7fffffffu) : v;
+    }
+
     // This block's values to all blocks, and all blocks' into slots.blocks.  A
     // block sends its next values only after its threads have read all of these,
     // and nobody gets further than one exchange ahead of the others: two sets of
     // slots are enough.
     __device__ __forceinline__ void exchange(float4 v)
     {
-        uint64_t *bar = &slots.arrived[parity];
-        if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, unsigned(cluster) * 16u + extra);
-        if (int(threadIdx.x) < cluster) {
-            const int rank = int(cooperative_groups::this_cluster().block_rank());
-            send16(peer_address(smem_u32(&slots.blocks[parity][rank]), threadIdx.x), v,
-                   peer_address(smem_u32(bar), threadIdx.x));
-        }
-        if (!dead && !mbar_wait_bounded(bar, (phases >> parity) & 1u, kExchangeCycles)) {
-            dead = true;
-            atomicOr(&g_exchange_status, 2u);
+        if (!dead) {
+            uint64_t *bar = &slots.arrived[parity];
+            if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, unsigned(cluster) * 16u + extra);
+            if (int(threadIdx.x) < cluster) {
+                const int rank = int(cooperative_groups::this_cluster().block_rank());
+                send16(peer_address(smem_u32(&slots.blocks[parity][rank]), threadIdx.x), v,
+                       peer_address(smem_u32(bar), threadIdx.x));
+            }
+            // once a wait has run out, nothing arrives here again: the barrier's
+            // phase is still open, and takes no second arrival
+            if (!mbar_wait_bounded(bar, (phases >> parity) & 1u, kExchangeCycles)) {
+                dead = true;
+                atomicOr(&g_exchange_status, 2u);
+            }
         }
         phases ^= 1u << parity;
     }
@@ -480,6 +492,8 @@ struct TeamSum {
                 if (N > 2) v[N > 2 ? 2 : 0] += b.z;
                 if (N > 3) v[N > 3 ? 3 : 0] += b.w;
             }
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = or_nan(v[k]);
         }
         parity ^= 1;
     }
@@ -548,6 +562,7 @@ struct TeamSum {
                 const float dk = fmaf(v[k].x, c[k].y, -row);
                 r.y += fmaf(c[k].x * dk, dk, v[k].y);
             }
+            r.y = or_nan(r.y);
         }
         parity ^= 1;
         return r;

@@ -232,6 +232,8 @@ RowPtr row_ptr(const gbssim_residual_norm &d, const gbssim_rows &r, int dtype)
 }
 ParamPtr param_ptr(const gbssim_param &p) { return {p.data, p.dtype, p.per_sample != 0, p.per_sample ? p.sample_stride : 0}; }
 
+unsigned g_exchange_extra = 0;  // test hook, see gbssim_tune_exchange
+
 ResidualNormArgs make_args(const gbssim_residual_norm &d)
 {
     ResidualNormArgs a{};
@@ -250,6 +252,7 @@ ResidualNormArgs make_args(const gbssim_residual_norm &d)
     a.offset = d.weight_offset;
     a.eps = d.eps;
     a.inv_dim = float(1.0 / d.dim);
+    a.exchange_extra = g_exchange_extra;
     return a;
 }
 
@@ -314,6 +317,8 @@ extern "C" int gbssim_residual_norm_fwd(const gbssim_residual_norm *d, void *x_o
                    ? 0
                    : d->tokens;
     a.plan.uneven = !(even(a.x, a.plan) && even(a.y, a.plan));
+    a.plan.even_out = d->dim * a.plan.classes % 8 == 0 && out_aligned(x_out_or_null, d->res_dtype) &&
+                      out_aligned(u_or_null, d->blk_dtype);
     a.x_out = x_out_or_null;
     a.u = u_or_null;
     a.stats = reinterpret_cast<float4 *>(stats_or_null);
@@ -405,6 +410,9 @@ extern "C" int gbssim_residual_norm_bwd(const gbssim_residual_norm *d,
                    : d->tokens;
     a.plan.uneven = !(even(a.x, a.plan) && even(a.y, a.plan) && even(a.gate_rows, a.plan) &&
                       even(a.gx, a.plan) && even(a.gu, a.plan));
+    a.plan.even_out = d->dim * a.plan.classes % 8 == 0 && out_aligned(grads->x, d->res_dtype) &&
+                      out_aligned(grads->y, d->blk_dtype) &&
+                      (!d->gate_rows.data || out_aligned(grads->gate, d->blk_dtype));
     a.stats = const_cast<float4 *>(reinterpret_cast<const float4 *>(stats));
     a.dx = grads->x;
     a.dy = grads->y;
@@ -420,3 +428,11 @@ extern "C" int gbssim_residual_norm_bwd(const gbssim_residual_norm *d,
     return cuda_fail(residual_norm_bwd_launch(a, d->res_dtype, d->blk_dtype, g,
                                               static_cast<cudaStream_t>(stream)));
 }
+
+#ifdef GBSSIM_TEST_HOOKS
+// ---- test build only (csrc/gbssim_test_hooks.h)
+extern "C" void gbssim_tune_exchange(int extra_bytes)
+{
+    g_exchange_extra = extra_bytes > 0 ? unsigned(extra_bytes) : 0u;
+}
+#endif

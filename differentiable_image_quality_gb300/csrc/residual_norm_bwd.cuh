@@ -14,7 +14,7 @@
 // y^ are formed again from x, y and the saved statistics, not stored.  Column
 // sums stay in registers over a block's rows (float32), go to a partial per
 // block, and a second kernel adds the partials in a fixed order.
-#include <algorithm>
+#pragma once
 
 #include "residual_norm.cuh"
 
@@ -105,11 +105,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const unsigned mine = smem_u32(ring) + threadIdx.x * 16, over = mine + kStages * stage_bytes;
 
     int r = rows.first + team * rows.step, left = rows.count - team;  // the team's row; none if <= 0
-    const int shift_x = SR::shift_of(a.x, a.tokens, rows.first, c),
-              shift_y = SY::shift_of(a.y, a.tokens, rows.first, c),
-              shift_gx = SR::shift_of(a.gx, a.tokens, rows.first, c),
-              shift_gu = SY::shift_of(a.gu, a.tokens, rows.first, c),
-              shift_g = SY::shift_of(a.gate_rows, a.tokens, rows.first, c);
+    const int shift_x = SR::shift_of(a.x, a.tokens, rows.first, -rows.shift),
+              shift_y = SY::shift_of(a.y, a.tokens, rows.first, -rows.shift),
+              shift_gx = SR::shift_of(a.gx, a.tokens, rows.first, -rows.shift),
+              shift_gu = SY::shift_of(a.gu, a.tokens, rows.first, -rows.shift),
+              shift_g = SY::shift_of(a.gate_rows, a.tokens, rows.first, -rows.shift);
     int ahead = r, ahead_left = left;
     unsigned to = mine;
     constexpr bool kShared = sizeof(R) == 4 || sizeof(Y) == 4;  // lanes copy for one another
@@ -257,78 +257,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (LAYER) write_sum(a, c, a.sum_e, se, scratch);
 }
 
-// ------------------------------------------------------- the parameters' gradients
-
-constexpr int kFinishCols = 8, kFinishLanes = 64;
-
-__device__ __forceinline__ void store_param(const ParamGrad &g, int group, int dim, int col, float v)
-{
-    if (!g.p) return;
-    const long long i = (g.per_sample ? (long long)group * dim : 0) + col;
-    if (g.type == GBSSIM_F32) static_cast<float *>(g.p)[i] = v;
-    else if (g.type == GBSSIM_BF16) static_cast<bf16 *>(g.p)[i] = from_f32<bf16>(v);
-    else static_cast<f16 *>(g.p)[i] = from_f32<f16>(v);
-}
-
-// Adds the blocks' partials.  A block takes 8 columns (one sector of each
-// partial), 64 threads of a column every 64th partial each, then their sums in
-// order.  blockIdx.y < groups: the gradients that each group has of its own; the
-// last: those shared by all.
-__global__ void __launch_bounds__(kFinishCols * kFinishLanes)
-    residual_norm_finish_kernel(const __grid_constant__ ResidualNormArgs a,
-                                const __grid_constant__ ParamGrads g, int shared_block)
-{
-    __shared__ float part[5][kFinishLanes][kFinishCols];
-    const int cx = threadIdx.x % kFinishCols, lane = threadIdx.x / kFinishCols;
-    const int col = int(blockIdx.x) * kFinishCols + cx;
-    const bool shared = int(blockIdx.y) == shared_block;
-    const int each = a.plan.classes * a.plan.splits;  // partials of a group
-    const int p0 = shared ? 0 : int(blockIdx.y) * each;
-    const int p1 = shared ? a.plan.groups * each : p0 + each;
-    const bool full = a.gate_rows.p != nullptr;
-    // sums of A, F, C, E over partials whose factors are the same; the factors
-    const auto factors = [&](int group, float &gate, float &w, float &b) {
-        gate = a.gate.p && !full ? param_at(a.gate, group, col) : 1.0f;
-        w = a.w1.p ? param_at(a.w1, group, col) + a.offset : 1.0f;
-        b = a.b1.p ? param_at(a.b1, group, col) : 0.0f;
-    };
-    // dg, dw1, db1, dw2, db2
-    float v[5] = {};
-    pdl_wait();
-    if (col < a.dim && p0 < p1) {
-        const bool vary = shared && (a.gate.stride || a.w1.stride || a.b1.stride);
-        float gate, w, b;
-        if (!vary) factors(p0 / each, gate, w, b);
-        const long long pitch = (long long)a.sums * a.dim;
-        const float *src = a.partials + (p0 + lane) * pitch + col;
-#pragma unroll 4
-        for (int p = p0 + lane; p < p1; p += kFinishLanes, src += kFinishLanes * pitch) {
-            const float A = a.sum_a >= 0 ? __ldcg(src + (long long)a.sum_a * a.dim) : 0.0f;
-            const float F = a.sum_f >= 0 ? __ldcg(src + (long long)a.sum_f * a.dim) : 0.0f;
-            const float C = a.sum_c >= 0 ? __ldcg(src + (long long)a.sum_c * a.dim) : 0.0f;
-            const float E = a.sum_e >= 0 ? __ldcg(src + (long long)a.sum_e * a.dim) : 0.0f;
-            if (vary) factors(p / each, gate, w, b);
-            v[0] += fmaf(w, A, b * F);
-            v[1] = fmaf(gate, A, v[1]);
-            v[2] = fmaf(gate, F, v[2]);
-            v[3] += C;
-            v[4] += E;
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < 5; ++k) part[k][lane][cx] = v[k];
-    __syncthreads();
-    if (threadIdx.x < 5 * kFinishCols) {
-        const int k = threadIdx.x / kFinishCols, x = threadIdx.x % kFinishCols;
-        const int to = int(blockIdx.x) * kFinishCols + x;
-        float s = 0.0f;
-#pragma unroll 16
-        for (int l = 0; l < kFinishLanes; ++l) s += part[k][l][x];
-        const ParamGrad &out = k == 0 ? g.gate : k == 1 ? g.w1 : k == 2 ? g.b1 : k == 3 ? g.w2 : g.b2;
-        if (to < a.dim && bool(out.per_sample) != shared) store_param(out, int(blockIdx.y), a.dim, to, s);
-    }
-}
-
 template <typename R, typename Y, bool ALIGNED, bool FULL, int NORMS, bool ANY>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
@@ -363,38 +291,4 @@ cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 }
 
 }  // namespace
-
-cudaError_t residual_norm_bwd_status(unsigned *flags, bool clear) { return exchange_status(flags, clear); }
-
-cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk,
-                                     const ParamGrads &g, cudaStream_t s)
-{
-    cudaError_t e = cudaSuccess;
-    if (a.plan.grid > 0) {
-        if (res == GBSSIM_F32) {
-            e = blk == GBSSIM_F32    ? launch<float, float>(a, s)
-                : blk == GBSSIM_BF16 ? launch<float, bf16>(a, s)
-                                     : launch<float, f16>(a, s);
-        } else {
-            e = res == GBSSIM_BF16 ? launch<bf16, bf16>(a, s) : launch<f16, f16>(a, s);
-        }
-    }
-    if (e != cudaSuccess || a.sums == 0) return e;
-    bool own = false, shared = false;
-    for (const ParamGrad *p : {&g.gate, &g.w1, &g.b1, &g.w2, &g.b2})
-        if (p->p) (p->per_sample ? own : shared) = true;
-    const int shared_block = own ? a.plan.groups : 0;
-    const unsigned ny = unsigned(shared_block + (shared ? 1 : 0));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned((a.dim + kFinishCols - 1) / kFinishCols), ny);
-    cfg.blockDim = dim3(kFinishCols * kFinishLanes);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, residual_norm_finish_kernel, a, g, shared_block);
-}
-
 }  // namespace gbssim

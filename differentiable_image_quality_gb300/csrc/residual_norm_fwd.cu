@@ -88,9 +88,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const unsigned mine = smem_u32(ring) + threadIdx.x * 16, over = mine + kStages * stage_bytes;
 
     int r = rows.first + team * rows.step, left = rows.count - team;  // the team's row; none if <= 0
-    const int shift_x = SR::shift_of(a.x, a.tokens, rows.first, c),
-              shift_y = SY::shift_of(a.y, a.tokens, rows.first, c),
-              shift_g = SY::shift_of(a.gate_rows, a.tokens, rows.first, c);
+    const int shift_x = SR::shift_of(a.x, a.tokens, rows.first, -rows.shift),
+              shift_y = SY::shift_of(a.y, a.tokens, rows.first, -rows.shift),
+              shift_g = SY::shift_of(a.gate_rows, a.tokens, rows.first, -rows.shift);
     int ahead = r, ahead_left = left;
     unsigned to = mine;
     constexpr bool kShared = sizeof(R) == 4 || sizeof(Y) == 4;  // lanes copy for one another

@@ -438,6 +438,46 @@ def test_many_rows_past_32_bits(pkg):
         assert torch.equal(big[-5:], small)
 
 
+def test_more_samples_than_a_grid_dimension(pkg):
+    """Parameters of 70000 samples: their gradients are 70000 groups of rows."""
+    check(pkg, *make((70000, 1, 8), F32, BF16, per_sample=True))
+
+
+def test_exchange_between_blocks_that_runs_out(pkg):
+    """Rows of several blocks: a wait for another block's sums is bounded.  The test
+    build announces more bytes than are sent: the outputs come out NaN, the device
+    says so, and the next call is as ever."""
+    import ctypes
+
+    from differentiable_image_quality_gb300 import _abi
+
+    t, g, how = make((1, 3, 9000), BF16, BF16, pre="layer")
+    args = {k: t[k] for k in NAMES[2:]}
+
+    def step():
+        x_out, u, stats = pkg.residual_norm_fwd(t["x"], t["y"], want_stats=True, **args, **how)
+        grads = pkg.residual_norm_bwd(g["x"], g["u"], t["x"], t["y"], stats, **args, **how)
+        torch.cuda.synchronize()
+        return x_out, u, *grads
+
+    want = step()
+    with _abi.using_test_library() as lib:
+        flags = ctypes.c_uint()
+        assert lib.gbssim_device_status(ctypes.byref(flags)) == 0 and flags.value == 0
+        lib.gbssim_tune_exchange(16)
+        try:
+            x_out, u = pkg.residual_norm_fwd(t["x"], t["y"], **args, **how)[:2]
+            torch.cuda.synchronize()
+        finally:
+            lib.gbssim_tune_exchange(0)
+        assert bool(x_out.isnan().all()) and bool(u.isnan().all())
+        assert lib.gbssim_device_status(ctypes.byref(flags)) == 0
+        assert flags.value == 2  # GBSSIM_DEV_EXCHANGE_TIMEOUT
+        again = step()
+        assert lib.gbssim_device_status(ctypes.byref(flags)) == 0 and flags.value == 0
+    assert all(torch.equal(a, b) for a, b in zip(want, again))
+
+
 def test_refusals(pkg):
     t, g, how = make((2, 6, 64))
     x, y, args = t["x"], t["y"], {k: t[k] for k in NAMES[2:]}
