@@ -308,11 +308,10 @@ __device__ __forceinline__ void store_group(O *p, const float (&v)[V])
 
 // Chunk k: elements [k E - pad, (k + 1) E - pad) of the tensor, E = kScaleElems.
 // Whole chunks whose groups are aligned in both tensors take one access a group.
-// Where 16-bit gradients and their output reach a group's boundary at different
-// elements (apart), the gradients' own aligned words go through shared memory and
-// come out again as the output's groups.  The first and last chunk of a tensor,
-// and float32 gradients apart from their output, take one element a lane, which
-// still fills whole lines a warp.
+// Where gradients and their output reach a group's boundary at different elements
+// (apart), the gradients' own aligned words go through shared memory and come out
+// again as the output's groups.  The first and last chunk of a tensor take one
+// element a lane.
 template <typename T, typename O>
 __device__ __noinline__ void scale_chunk(const void *gv, void *ov, long long n, unsigned k,
                                          int pad, bool apart, float c, uint4 *stage)
@@ -321,32 +320,28 @@ __device__ __noinline__ void scale_chunk(const void *gv, void *ov, long long n, 
     const T *g = static_cast<const T *>(gv);
     O *o = static_cast<O *>(ov);
     long long e0 = (long long)k * kScaleElems - pad;
-    if constexpr (sizeof(T) == 2) {
-        constexpr int kWords = kScaleElems * 2 / 16;
-        if (apart && e0 >= 8 && e0 + kScaleElems + 8 <= n) {
-            const uintptr_t at = reinterpret_cast<uintptr_t>(g + e0);
-            const T *word = reinterpret_cast<const T *>(at & ~uintptr_t(15));
-            const int shift = int(at & 15) / 2;
-            uint4 r[kWords / kThreads];
+    if (apart && e0 >= 8 && e0 + kScaleElems + 8 <= n) {
+        constexpr int kWords = kScaleElems * int(sizeof(T)) / 16;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(g + e0);
+        const uint4 *word = reinterpret_cast<const uint4 *>(at & ~uintptr_t(15));
+        uint4 r[kWords / kThreads];
 #pragma unroll
-            for (int j = 0; j < kWords / kThreads; ++j)
-                r[j] = ld_stream16(word + (threadIdx.x + j * kThreads) * 8);
-            __syncthreads();  // the chunk before has been read out
+        for (int j = 0; j < kWords / kThreads; ++j) r[j] = ld_stream16(word + threadIdx.x + j * kThreads);
+        __syncthreads();  // the chunk before has been read out
 #pragma unroll
-            for (int j = 0; j < kWords / kThreads; ++j) stage[threadIdx.x + j * kThreads] = r[j];
-            if (threadIdx.x == 0) stage[kWords] = ld_stream16(word + kWords * 8);
-            __syncthreads();
-            const T *in = reinterpret_cast<const T *>(stage) + shift + threadIdx.x * V;
-            o += e0 + threadIdx.x * V;
+        for (int j = 0; j < kWords / kThreads; ++j) stage[threadIdx.x + j * kThreads] = r[j];
+        if (threadIdx.x == 0) stage[kWords] = ld_stream16(word + kWords);
+        __syncthreads();
+        const T *in = reinterpret_cast<const T *>(stage) + int(at & 15) / int(sizeof(T)) + threadIdx.x * V;
+        o += e0 + threadIdx.x * V;
 #pragma unroll
-            for (int j = 0; j < kEach / V; ++j) {
-                float v[V];
+        for (int j = 0; j < kEach / V; ++j) {
+            float v[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = to_f32(in[j * (kThreads * V) + i]) * c;
-                store_group<O, V>(o + j * (kThreads * V), v);
-            }
-            return;
+            for (int i = 0; i < V; ++i) v[i] = to_f32(in[j * (kThreads * V) + i]) * c;
+            store_group<O, V>(o + j * (kThreads * V), v);
         }
+        return;
     }
     if (!apart && e0 >= 0 && e0 + kScaleElems <= n) {
         g += e0 + threadIdx.x * V;
@@ -396,7 +391,7 @@ template <int CAP>
 __global__ void __launch_bounds__(kThreads, 4)
     grad_scale_kernel(const __grid_constant__ ScaleTable<CAP> t)
 {
-    __shared__ uint4 stage[kScaleElems * 2 / 16 + 1];
+    __shared__ uint4 stage[kScaleElems * 4 / 16 + 1];
     pdl_wait();
     const float c = __ldcg(t.coef);
     if (t.in_place && c == 1.0f) return;  // 1 * g is g, to the bit
