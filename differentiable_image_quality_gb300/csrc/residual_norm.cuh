@@ -25,6 +25,8 @@ namespace gbssim {
 constexpr int kColsPerThread = 8;
 constexpr int kFwdThreads = 1024, kBwdThreads = 512;  // of a block, at most
 constexpr int kSmallBlock = 128;  // threads of a block that holds several teams
+// Threads an SM holds of the backward's kernel that needs fewest registers (96).
+constexpr int kBwdResidentPlain = 640;
 constexpr int kMaxDim = 16384;    // 2 forward or 4 backward blocks
 
 struct RowPtr {
@@ -97,6 +99,22 @@ cudaError_t residual_norm_cluster_room(ClusterRoom *room);
 cudaError_t residual_norm_fwd_launch(const ResidualNormArgs &a, int res, int blk, cudaStream_t s);
 cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk,
                                      const ParamGrads &g, cudaStream_t s);
+// Which of the backward's kernels a call takes.
+inline int residual_norm_bwd_norms(const ResidualNormArgs &a)
+{
+    if (a.b1.p || a.sum_f >= 0) return 2;
+    return a.post == GBSSIM_ROW_LAYER || a.pre == GBSSIM_ROW_LAYER || a.sum_e >= 0 ? 1 : 0;
+}
+inline bool residual_norm_bwd_any(const ResidualNormArgs &a)
+{
+    return !a.y.p || !a.gx.p || !a.gu.p || !a.dx || !a.dy || a.tokens != 0 || a.plan.cluster > 1 ||
+           a.plan.uneven;
+}
+inline bool residual_norm_bwd_plain(const ResidualNormArgs &a)
+{
+    return !a.gate_rows.p && !residual_norm_bwd_any(a) && residual_norm_bwd_norms(a) == 0;
+}
+
 cudaError_t residual_norm_bwd_f32_launch(const ResidualNormArgs &a, int blk, cudaStream_t s);
 cudaError_t residual_norm_bwd_16_launch(const ResidualNormArgs &a, int blk, cudaStream_t s);
 // Kernel-side failures on the current device since the last call that cleared them.

@@ -78,7 +78,7 @@ __device__ __forceinline__ void write_sum(const ResidualNormArgs &a, const Cols<
 // bias, 1 they may but for a bias of the post norm, 2 they may.  ANY: whatever a call may ask for; without it all four inputs and both
 // outputs are there, one stride reaches every row, and a block has whole rows.
 template <typename R, typename Y, bool ALIGNED, bool FULL, int NORMS, bool ANY>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(NORMS == 0 && !FULL && !ANY ? kBwdResidentPlain : kBwdThreads, 1)
     residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a)
 {
     using SR = Staged<R, ALIGNED, ANY>;
@@ -269,11 +269,8 @@ cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 template <typename R, typename Y, bool ALIGNED>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    const bool any = !a.y.p || !a.gx.p || !a.gu.p || !a.dx || !a.dy || a.tokens != 0 ||
-                     a.plan.cluster > 1 || a.plan.uneven;
-    const int norms = a.b1.p || a.sum_f >= 0 ? 2
-                      : a.post == GBSSIM_ROW_LAYER || a.pre == GBSSIM_ROW_LAYER || a.sum_e >= 0 ? 1
-                                                                                              : 0;
+    const bool any = residual_norm_bwd_any(a);
+    const int norms = residual_norm_bwd_norms(a);
     if (a.gate_rows.p)
         return any         ? launch<R, Y, ALIGNED, true, 2, true>(a, s)
                : norms > 0 ? launch<R, Y, ALIGNED, true, 2, false>(a, s)
