@@ -2,7 +2,11 @@
 //
 // Bound by memory: x and y are read once, x' and u written once, and both
 // norms' statistics are taken from the row held in registers, in float32.  u
-// comes from x' before its rounding.
+// comes from x' before its rounding.  What has to be hidden is the chain of two
+// sums over the row: by the rows of other blocks, and by copying the next row
+// meanwhile.  65536 x 4096 bfloat16, root-mean-square norms: 332 to 359 us for
+// 2.15 GB (88 to 95 % of the copy rate); 8192 x 1152 conditioned, float32
+// stream: 29 us (57 %, instruction issue).
 #include "residual_norm.cuh"
 
 namespace gbssim {

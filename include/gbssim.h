@@ -299,7 +299,8 @@ int gbssim_grad_clip(const void *const *grads, void *const *outs, const long lon
  * Types: x and x' are res_dtype; y, u and a gate of its own per row blk_dtype;
  * res_dtype is blk_dtype or float32.  Each parameter has its own type.
  * Arithmetic is float32; each output is rounded once, and u is formed from x'
- * before x' is rounded.  Rows that hold a NaN or an infinity affect no others.
+ * before x' is rounded.  Sums of a row's squares have to stay within float32's
+ * range.  Rows that hold a NaN or an infinity affect no others.
  *
  * Shapes: batch x tokens rows, either of which may be 0 or 1; dim from 1 to
  * 16384.  Inputs may have any non-negative strides between rows (element
