@@ -338,17 +338,79 @@ __device__ __forceinline__ float param_at(const ParamPtr &p, int group, int col)
                                    : load_param1<f16>(p.p, i);
 }
 
-// The thread's eight values of a parameter plus `offset`; `missing` where it is null.
+// The thread's eight values of a parameter as they lie in memory.  A block asks for
+// all its parameters before it converts the first: one after the other, each
+// waited about a microsecond, which is what a call of a few rows then took.
+struct RawParam {
+    uint32_t w[8];  // two 16-bit values a word (the first four words), or one value a word
+    bool packed;
+};
+
 template <bool ALIGNED>
-__device__ __forceinline__ void load_param(const ParamPtr &p, int group, const Cols<ALIGNED> &c,
-                                           float offset, float missing, f32x2 (&v)[4])
+__device__ __forceinline__ RawParam fetch_param(const ParamPtr &p, int group, const Cols<ALIGNED> &c)
 {
-    float f[8];
+    RawParam r;
+    r.packed = false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        f[e] = !p.p ? missing : (c.has(e) ? param_at(p, group, c.first + e) + offset : 0.0f);
+    for (int e = 0; e < 8; ++e) r.w[e] = 0u;
+    if (!p.p) return r;
+    const bool wide = p.type == GBSSIM_F32;
+    const unsigned char *at =
+        static_cast<const unsigned char *>(p.p) + (group * p.stride + c.first) * (wide ? 4 : 2);
+    if (c.all() && (reinterpret_cast<uintptr_t>(at) & 15) == 0) {
+        const uint4 lo = __ldg(reinterpret_cast<const uint4 *>(at));
+        r.w[0] = lo.x; r.w[1] = lo.y; r.w[2] = lo.z; r.w[3] = lo.w;
+        r.packed = !wide;
+        if (wide) {
+            const uint4 hi = __ldg(reinterpret_cast<const uint4 *>(at) + 1);
+            r.w[4] = hi.x; r.w[5] = hi.y; r.w[6] = hi.z; r.w[7] = hi.w;
+        }
+    } else if (wide) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = pair(f[2 * e], f[2 * e + 1]);
+        for (int e = 0; e < 8; ++e)
+            if (c.has(e)) r.w[e] = __ldg(reinterpret_cast<const uint32_t *>(at) + e);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c.has(e)) r.w[e] = __ldg(reinterpret_cast<const unsigned short *>(at) + e);
+    }
+    return r;
+}
+
+// The values plus `offset`; `missing` where the parameter is null.
+template <bool ALIGNED>
+__device__ __forceinline__ void param_values(const ParamPtr &p, const RawParam &r,
+                                             const Cols<ALIGNED> &c, float offset, float missing,
+                                             f32x2 (&v)[4])
+{
+    if (!p.p) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = both(missing);
+        return;
+    }
+    if (p.type == GBSSIM_F32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = pair(__uint_as_float(r.w[2 * e]), __uint_as_float(r.w[2 * e + 1]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t w = r.packed ? r.w[e] : r.w[2 * e] | r.w[2 * e + 1] << 16;
+            const float2 h = p.type == GBSSIM_BF16 ? unpack2<bf16>(w) : unpack2<f16>(w);
+            v[e] = pair(h.x, h.y);
+        }
+    }
+    if (offset != 0.0f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = add2(v[e], both(offset));
+    }
+    if (!c.all()) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 h = halves(v[e]);
+            v[e] = pair(c.has(2 * e) ? h.x : 0.0f, c.has(2 * e + 1) ? h.y : 0.0f);
+        }
+    }
 }
 
 // ------------------------------------------------------ sums over a team

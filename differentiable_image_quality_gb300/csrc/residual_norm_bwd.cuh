@@ -140,16 +140,22 @@ __global__ void __launch_bounds__(NORMS == 0 && !FULL && !ANY ? kBwdResidentPlai
     for (int i = 0; i < kStages - 1; ++i) fetch();
 
     f32x2 w1[4], b1[4], w2[4];  // with the gate of the column in w1 and b1, unless FULL
-    load_param(a.w1, rows.group, c, a.offset, 1.0f, w1);
-    load_param(a.w2, rows.group, c, a.offset, 1.0f, w2);
-    if (BIAS1) load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
-    if (!FULL && a.gate.p) {
-        f32x2 g[4];
-        load_param(a.gate, rows.group, c, 0.0f, 1.0f, g);
+    {
+        const RawParam r1 = fetch_param(a.w1, rows.group, c), r2 = fetch_param(a.w2, rows.group, c);
+        RawParam rg, rb1;
+        if (!FULL) rg = fetch_param(a.gate, rows.group, c);
+        if (BIAS1) rb1 = fetch_param(a.b1, rows.group, c);
+        param_values(a.w1, r1, c, a.offset, 1.0f, w1);
+        param_values(a.w2, r2, c, a.offset, 1.0f, w2);
+        if (BIAS1) param_values(a.b1, rb1, c, 0.0f, 0.0f, b1);
+        if (!FULL) {
+            f32x2 g[4];
+            param_values(a.gate, rg, c, 0.0f, 1.0f, g);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            w1[e] = mul2(w1[e], g[e]);
-            if (BIAS1) b1[e] = mul2(b1[e], g[e]);
+            for (int e = 0; e < 4; ++e) {
+                w1[e] = mul2(w1[e], g[e]);
+                if (BIAS1) b1[e] = mul2(b1[e], g[e]);
+            }
         }
     }
     const f32x2 scale = both(a.scale);

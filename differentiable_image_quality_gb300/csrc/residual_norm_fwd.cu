@@ -120,13 +120,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // post and gate of a column in one factor and one summand; a gate of its
     // own per row stays apart
     f32x2 w1[4], b1[4], w2[4], b2[4];
-    load_param(a.w1, rows.group, c, a.offset, 1.0f, w1);
-    load_param(a.w2, rows.group, c, a.offset, 1.0f, w2);
-    if (BIAS1) load_param(a.b1, rows.group, c, 0.0f, 0.0f, b1);
-    if (LAYER) load_param(a.b2, rows.group, c, 0.0f, 0.0f, b2);
-    if (a.gate.p) {
+    {
+        const RawParam rg = fetch_param(a.gate, rows.group, c), r1 = fetch_param(a.w1, rows.group, c),
+                       r2 = fetch_param(a.w2, rows.group, c);
+        RawParam rb1, rb2;
+        if (BIAS1) rb1 = fetch_param(a.b1, rows.group, c);
+        if (LAYER) rb2 = fetch_param(a.b2, rows.group, c);
         f32x2 g[4];
-        load_param(a.gate, rows.group, c, 0.0f, 1.0f, g);
+        param_values(a.gate, rg, c, 0.0f, 1.0f, g);
+        param_values(a.w1, r1, c, a.offset, 1.0f, w1);
+        param_values(a.w2, r2, c, a.offset, 1.0f, w2);
+        if (BIAS1) param_values(a.b1, rb1, c, 0.0f, 0.0f, b1);
+        if (LAYER) param_values(a.b2, rb2, c, 0.0f, 0.0f, b2);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             w1[e] = mul2(w1[e], g[e]);
