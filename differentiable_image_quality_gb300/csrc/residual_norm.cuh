@@ -8,6 +8,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 
 #include <cooperative_groups.h>
 
@@ -61,6 +62,7 @@ struct RowPlan {
     int groups, group_rows, splits;
     int threads;
     unsigned grid;     // groups * classes * splits * cluster
+    int device;
 };
 
 struct ResidualNormArgs {
@@ -679,16 +681,21 @@ constexpr int stages_of(int units, int per_sm)
     return fit < 1 ? 1 : fit > 2 ? 2 : fit;
 }
 
+// asked: of this kernel alone, one bit for each device on which it may use more
+// shared memory than it may without asking.
 template <class Kernel>
-cudaError_t launch_staged(Kernel kernel, const ResidualNormArgs &a, int units, int stages,
-                          cudaStream_t s)
+cudaError_t launch_staged(Kernel kernel, std::atomic<unsigned long long> &asked,
+                          const ResidualNormArgs &a, int units, int stages, cudaStream_t s)
 {
     const int smem = stages * units * 16 * a.plan.threads;
-    if (smem > 40 * 1024) {  // with the static arrays: above what needs no asking for
+    const unsigned long long bit = a.plan.device < 64 ? 1ull << a.plan.device : 0ull;
+    // (with the static arrays, 40 KB are below what needs no asking for)
+    if (smem > 40 * 1024 && !(asked.load(std::memory_order_relaxed) & bit)) {
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    kStagedBlock);
         if (e != cudaSuccess) return e;
+        asked.fetch_or(bit, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.plan.grid);

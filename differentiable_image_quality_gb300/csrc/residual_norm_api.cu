@@ -135,6 +135,7 @@ constexpr int kMaxPlanSms = 256;
 // What a plan has to know of the device.
 struct Room {
     int sms, clusters2, clusters4;
+    int device;
 };
 
 // Read once per device.
@@ -153,7 +154,7 @@ int device_room(Room *out)
         e = residual_norm_cluster_room(&c);
         if (e != cudaSuccess) return cuda_fail(e);
         if (c.of2 < 1 || c.of4 < 1) return cuda_fail(cudaErrorInvalidConfiguration);
-        r = {std::min(sms, kMaxPlanSms), std::min(c.of2, kMaxPlanSms / 2), std::min(c.of4, kMaxPlanSms / 4)};
+        r = {std::min(sms, kMaxPlanSms), std::min(c.of2, kMaxPlanSms / 2), std::min(c.of4, kMaxPlanSms / 4), dev};
     }
     *out = r;
     return GBSSIM_OK;
@@ -164,6 +165,7 @@ int device_room(Room *out)
 RowPlan make_plan(const gbssim_residual_norm &d, int most_threads, int resident, const Room &room)
 {
     RowPlan p{};
+    p.device = room.device;
     bool own = false;
     for (const gbssim_param *q : {&d.gate, &d.post_weight, &d.post_bias, &d.pre_weight, &d.pre_bias})
         own = own || (q->data && q->per_sample);
@@ -336,7 +338,7 @@ extern "C" int gbssim_residual_norm_fwd(const gbssim_residual_norm *d, void *x_o
 extern "C" size_t gbssim_residual_norm_workspace_bytes(const gbssim_residual_norm *d)
 {
     if (check_desc(d) != GBSSIM_OK || row_count(*d) == 0) return 0;
-    const RowPlan p = make_plan(*d, kBwdThreads, kBwdResidentPlain, {kMaxPlanSms, kMaxPlanSms / 2, kMaxPlanSms / 4});
+    const RowPlan p = make_plan(*d, kBwdThreads, kBwdResidentPlain, {kMaxPlanSms, kMaxPlanSms / 2, kMaxPlanSms / 4, 0});
     return size_t(p.groups) * p.classes * p.splits * kMaxSums * d->dim * sizeof(float);
 }
 

@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(NORMS == 0 && !FULL && !ANY ? kBwdResidentPlai
 template <typename R, typename Y, bool ALIGNED, bool FULL, int NORMS, bool ANY>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    return launch_staged(residual_norm_bwd_kernel<R, Y, ALIGNED, FULL, NORMS, ANY>, a,
+    static std::atomic<unsigned long long> asked{0};
+    return launch_staged(residual_norm_bwd_kernel<R, Y, ALIGNED, FULL, NORMS, ANY>, asked, a,
                          bwd_units<R, Y, ALIGNED, FULL>(), bwd_stages<R, Y, ALIGNED, FULL>(), s);
 }
 

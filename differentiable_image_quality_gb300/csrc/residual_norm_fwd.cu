@@ -191,7 +191,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 template <typename R, typename Y, bool ALIGNED, int NORMS, bool ANY>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    return launch_staged(residual_norm_fwd_kernel<R, Y, ALIGNED, NORMS, ANY>, a,
+    static std::atomic<unsigned long long> asked{0};
+    return launch_staged(residual_norm_fwd_kernel<R, Y, ALIGNED, NORMS, ANY>, asked, a,
                          fwd_units<R, Y, ALIGNED, ANY>(), fwd_stages<R, Y, ALIGNED, ANY>(), s);
 }
 
