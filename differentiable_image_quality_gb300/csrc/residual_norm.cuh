@@ -109,12 +109,12 @@ inline int residual_norm_bwd_norms(const ResidualNormArgs &a)
 }
 inline bool residual_norm_bwd_any(const ResidualNormArgs &a)
 {
-    return !a.y.p || !a.gx.p || !a.gu.p || !a.dx || !a.dy || a.tokens != 0 || a.plan.cluster > 1 ||
-           a.plan.uneven;
+    return !a.y.p || !a.gx.p || !a.gu.p || !a.dx || !a.dy || a.tokens != 0 || a.plan.uneven;
 }
 inline bool residual_norm_bwd_plain(const ResidualNormArgs &a)
 {
-    return !a.gate_rows.p && !residual_norm_bwd_any(a) && residual_norm_bwd_norms(a) == 0;
+    return !a.gate_rows.p && !residual_norm_bwd_any(a) && a.plan.cluster == 1 &&
+           residual_norm_bwd_norms(a) == 0;
 }
 
 cudaError_t residual_norm_bwd_f32_launch(const ResidualNormArgs &a, int blk, cudaStream_t s);

@@ -80,9 +80,10 @@ __device__ __forceinline__ void write_sum(const ResidualNormArgs &a, const Cols<
 
 // FULL: a gate of its own per row.  NORMS: 0 neither subtracts a mean nor has a
 // bias, 1 they may but for a bias of the post norm, 2 they may.  ANY: whatever a call may ask for; without it all four inputs and both
-// outputs are there, one stride reaches every row, and a block has whole rows.
-template <typename R, typename Y, bool ALIGNED, bool FULL, int NORMS, bool ANY>
-__global__ void __launch_bounds__(NORMS == 0 && !FULL && !ANY ? kBwdResidentPlain : kBwdThreads, 1)
+// outputs are there and one stride reaches every row.  CLUSTER: blocks may share
+// rows.
+template <typename R, typename Y, bool ALIGNED, bool FULL, int NORMS, bool ANY, bool CLUSTER>
+__global__ void __launch_bounds__(NORMS == 0 && !FULL && !CLUSTER ? kBwdResidentPlain : kBwdThreads, 1)
     residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a)
 {
     using SR = Staged<R, ALIGNED, ANY>;
@@ -93,10 +94,10 @@ __global__ void __launch_bounds__(NORMS == 0 && !FULL && !ANY ? kBwdResidentPlai
     __shared__ TeamSlots slots;
     __shared__ float scratch[kSmallBlock * 8];
     if (a.sums) pdl_trigger();  // the kernel that adds the partials waits for all of this one
-    const int cluster = ANY ? a.plan.cluster : 1;
+    const int cluster = CLUSTER ? a.plan.cluster : 1;
     const BlockRows rows(a, cluster);
     const Cols<ALIGNED> c(a, cluster, rows.shift);
-    TeamSum<ANY> sum(slots, a);
+    TeamSum<CLUSTER> sum(slots, a);
     const int team = a.plan.teams > 1 ? int(threadIdx.x) / a.plan.tpr : 0;
     const int step = rows.step * a.plan.teams;  // rows from one of the team's to its next
     const int pitch = a.plan.threads * 16;
@@ -267,11 +268,11 @@ __global__ void __launch_bounds__(NORMS == 0 && !FULL && !ANY ? kBwdResidentPlai
     if (LAYER) write_sum(a, c, a.sum_e, se, scratch);
 }
 
-template <typename R, typename Y, bool ALIGNED, bool FULL, int NORMS, bool ANY>
+template <typename R, typename Y, bool ALIGNED, bool FULL, int NORMS, bool ANY, bool CLUSTER>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
     static std::atomic<unsigned long long> asked{0};
-    return launch_staged(residual_norm_bwd_kernel<R, Y, ALIGNED, FULL, NORMS, ANY>, asked, a,
+    return launch_staged(residual_norm_bwd_kernel<R, Y, ALIGNED, FULL, NORMS, ANY, CLUSTER>, asked, a,
                          bwd_units<R, Y, ALIGNED, FULL>(), bwd_stages<R, Y, ALIGNED, FULL>(), s);
 }
 
@@ -280,16 +281,19 @@ cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 template <typename R, typename Y, bool ALIGNED>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    const bool any = residual_norm_bwd_any(a);
+    const bool any = residual_norm_bwd_any(a), cluster = a.plan.cluster > 1;
     const int norms = residual_norm_bwd_norms(a);
     if (a.gate_rows.p)
-        return any         ? launch<R, Y, ALIGNED, true, 2, true>(a, s)
-               : norms > 0 ? launch<R, Y, ALIGNED, true, 2, false>(a, s)
-                           : launch<R, Y, ALIGNED, true, 0, false>(a, s);
-    return any          ? launch<R, Y, ALIGNED, false, 2, true>(a, s)
-           : norms == 2 ? launch<R, Y, ALIGNED, false, 2, false>(a, s)
-           : norms == 1 ? launch<R, Y, ALIGNED, false, 1, false>(a, s)
-                        : launch<R, Y, ALIGNED, false, 0, false>(a, s);
+        return any || cluster ? launch<R, Y, ALIGNED, true, 2, true, true>(a, s)
+               : norms > 0    ? launch<R, Y, ALIGNED, true, 2, false, false>(a, s)
+                              : launch<R, Y, ALIGNED, true, 0, false, false>(a, s);
+    if (any) return launch<R, Y, ALIGNED, false, 2, true, true>(a, s);
+    if (cluster)
+        return norms > 0 ? launch<R, Y, ALIGNED, false, 2, false, true>(a, s)
+                         : launch<R, Y, ALIGNED, false, 0, false, true>(a, s);
+    return norms == 2   ? launch<R, Y, ALIGNED, false, 2, false, false>(a, s)
+           : norms == 1 ? launch<R, Y, ALIGNED, false, 1, false, false>(a, s)
+                        : launch<R, Y, ALIGNED, false, 0, false, false>(a, s);
 }
 
 template <typename R, typename Y>

@@ -67,9 +67,10 @@ __device__ __forceinline__ RowStats row_stats(const f32x2 (&v)[4], const Cols<AL
 }
 
 // NORMS: 0 neither subtracts a mean nor has a bias, 1 they may but for a bias of
-// the post norm, 2 they may.  ANY: whatever a call may ask for; without it y and u are there, gates are columns', one stride reaches
-// every row, and a block has whole rows.
-template <typename R, typename Y, bool ALIGNED, int NORMS, bool ANY>
+// the post norm, 2 they may.  ANY: whatever a call may ask for; without it y and u
+// are there, gates are columns', and one stride reaches every row.  CLUSTER: blocks
+// may share rows.
+template <typename R, typename Y, bool ALIGNED, int NORMS, bool ANY, bool CLUSTER>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     residual_norm_fwd_kernel(const __grid_constant__ ResidualNormArgs a)
 {
@@ -79,10 +80,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     constexpr bool LAYER = NORMS > 0, BIAS1 = NORMS == 2;
     extern __shared__ uint4 ring[];
     __shared__ TeamSlots slots;
-    const int cluster = ANY ? a.plan.cluster : 1;
+    const int cluster = CLUSTER ? a.plan.cluster : 1;
     const BlockRows rows(a, cluster);
     const Cols<ALIGNED> c(a, cluster, rows.shift);
-    TeamSum<ANY> sum(slots, a);
+    TeamSum<CLUSTER> sum(slots, a);
     if (LAYER) sum.count_columns(c.upto - c.from);
     const int team = a.plan.teams > 1 ? int(threadIdx.x) / a.plan.tpr : 0;
     const int step = rows.step * a.plan.teams;  // rows from one of the team's to its next
@@ -188,11 +189,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     sum.finish();
 }
 
-template <typename R, typename Y, bool ALIGNED, int NORMS, bool ANY>
+template <typename R, typename Y, bool ALIGNED, int NORMS, bool ANY, bool CLUSTER>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
     static std::atomic<unsigned long long> asked{0};
-    return launch_staged(residual_norm_fwd_kernel<R, Y, ALIGNED, NORMS, ANY>, asked, a,
+    return launch_staged(residual_norm_fwd_kernel<R, Y, ALIGNED, NORMS, ANY, CLUSTER>, asked, a,
                          fwd_units<R, Y, ALIGNED, ANY>(), fwd_stages<R, Y, ALIGNED, ANY>(), s);
 }
 
@@ -201,12 +202,17 @@ cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 template <typename R, typename Y, bool ALIGNED>
 cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 {
-    if (!a.y.p || !a.u || a.gate_rows.p || a.tokens != 0 || a.plan.cluster > 1 || a.plan.uneven)
-        return launch<R, Y, ALIGNED, 2, true>(a, s);
-    if (a.b1.p) return launch<R, Y, ALIGNED, 2, false>(a, s);
-    if (a.post == GBSSIM_ROW_LAYER || a.pre == GBSSIM_ROW_LAYER || a.b2.p)
-        return launch<R, Y, ALIGNED, 1, false>(a, s);
-    return launch<R, Y, ALIGNED, 0, false>(a, s);
+    const int norms = a.b1.p                                                                 ? 2
+                      : a.post == GBSSIM_ROW_LAYER || a.pre == GBSSIM_ROW_LAYER || a.b2.p ? 1
+                                                                                            : 0;
+    if (!a.y.p || !a.u || a.gate_rows.p || a.tokens != 0 || a.plan.uneven)
+        return launch<R, Y, ALIGNED, 2, true, true>(a, s);
+    if (a.plan.cluster > 1)
+        return norms > 0 ? launch<R, Y, ALIGNED, 2, false, true>(a, s)
+                         : launch<R, Y, ALIGNED, 0, false, true>(a, s);
+    return norms == 2   ? launch<R, Y, ALIGNED, 2, false, false>(a, s)
+           : norms == 1 ? launch<R, Y, ALIGNED, 1, false, false>(a, s)
+                        : launch<R, Y, ALIGNED, 0, false, false>(a, s);
 }
 
 template <typename R, typename Y>
@@ -219,7 +225,7 @@ cudaError_t launch(const ResidualNormArgs &a, cudaStream_t s)
 
 cudaError_t residual_norm_cluster_room(ClusterRoom *room)
 {
-    const auto kernel = residual_norm_fwd_kernel<float, float, true, 2, true>;
+    const auto kernel = residual_norm_fwd_kernel<float, float, true, 2, true, true>;
     constexpr int kAlone = 120 * 1024;  // shared memory that leaves an SM room for one block
     cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedBlock);
