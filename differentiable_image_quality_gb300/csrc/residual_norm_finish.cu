@@ -21,14 +21,15 @@ __device__ __forceinline__ void store_param(const ParamGrad &g, int group, int d
 }
 
 // Adds the blocks' partials.  A block takes 8 columns (one sector of each
-// partial), 64 threads of a column every 64th partial each, then their sums in
-// order.  Part y < groups of the grid makes the gradients that each group has of its
+// partial), 64 threads of a column every 64th partial each, then their sums in a
+// fixed order.  Part y < groups of the grid makes the gradients that each group has of its
 // own, the last those shared by all.
 __global__ void __launch_bounds__(kFinishCols * kFinishLanes)
     residual_norm_finish_kernel(const __grid_constant__ ResidualNormArgs a,
                                 const __grid_constant__ ParamGrads g, int shared_part)
 {
-    __shared__ float part[5][kFinishLanes][kFinishCols];
+    constexpr int kWarps = kFinishCols * kFinishLanes / 32;
+    __shared__ float part[5][kWarps][kFinishCols];
     const int cx = threadIdx.x % kFinishCols, lane = threadIdx.x / kFinishCols;
     const int across = (a.dim + kFinishCols - 1) / kFinishCols;  // blocks of a part
     const int y = int(blockIdx.x) / across, first = (int(blockIdx.x) - y * across) * kFinishCols;
@@ -67,15 +68,20 @@ __global__ void __launch_bounds__(kFinishCols * kFinishLanes)
             v[4] += E;
         }
     }
+    // a warp holds four threads of each column
 #pragma unroll
-    for (int k = 0; k < 5; ++k) part[k][lane][cx] = v[k];
+    for (int k = 0; k < 5; ++k) {
+        v[k] += __shfl_xor_sync(0xffffffffu, v[k], 8);
+        v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
+        if ((threadIdx.x & 31) < kFinishCols) part[k][threadIdx.x / 32][cx] = v[k];
+    }
     __syncthreads();
     if (threadIdx.x < 5 * kFinishCols) {
         const int k = threadIdx.x / kFinishCols, x = threadIdx.x % kFinishCols;
         const int to = first + x;
         float s = 0.0f;
-#pragma unroll 16
-        for (int l = 0; l < kFinishLanes; ++l) s += part[k][l][x];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) s += part[k][w][x];
         const ParamGrad &out = k == 0 ? g.gate : k == 1 ? g.w1 : k == 2 ? g.b1 : k == 3 ? g.w2 : g.b2;
         if (to < a.dim && bool(out.per_sample) != shared) store_param(out, y, a.dim, to, s);
     }
