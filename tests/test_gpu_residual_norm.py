@@ -260,6 +260,24 @@ def test_strides_and_alignment(pkg, dim, tokens):
     check(pkg, t, g, how)
 
 
+@pytest.mark.parametrize("dim", [8200, 9001, 12344])
+@pytest.mark.parametrize("gate,post,pre", [("rows", "rms", "layer"), ("dim", None, "rms"),
+                                           (None, "layer", None), ("dim", "rms", "rms")])
+def test_rows_shared_by_blocks(pkg, dim, gate, post, pre):
+    for pair in ((BF16, BF16), (F32, F16)):
+        check(pkg, *make((2, 40, dim), *pair, gate=gate, post=post, pre=pre, bias=gate == "rows"))
+
+
+@pytest.mark.parametrize("dim,tokens", [(70, 60), (1002, 40), (8202, 40)])
+def test_rows_whose_alignment_changes_within_a_block(pkg, dim, tokens):
+    """Slices of rows one element wider: every row of a block starts elsewhere."""
+    for pair in ((F32, F32), (BF16, BF16)):
+        t, g, how = make((2, tokens, dim + 1), *pair, pre="layer", gate="rows")
+        for k in t:
+            t[k] = t[k][..., :dim].contiguous() if t[k].dim() == 1 else t[k][..., :dim]
+        check(pkg, t, {k: v[..., 1:] for k, v in g.items()}, how)
+
+
 @pytest.mark.parametrize("which", ["x", "u"])
 def test_one_gradient_missing(pkg, which):
     t, g, how = make((2, 9, 200), F32, BF16, post="layer", pre="layer", gate="rows")
