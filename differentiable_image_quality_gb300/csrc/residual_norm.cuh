@@ -79,9 +79,16 @@ struct ResidualNormArgs {
     // backward
     RowPtr gx, gu;
     void *dx, *dy, *dgate_rows;
-    float *partials;   // [groups * classes * splits][sums][dim]
+    float *partials;   // [groups * classes * splits][sums][dim], then what is folded of them
     int sum_a, sum_f, sum_c, sum_e, sums;  // places of the column sums, -1: not wanted
 };
+
+// Partials beyond kMostUnfolded are first folded, kFoldedPartials into one set of
+// the five parameters' gradients.  The extra kernel costs calls of 500 to 2000
+// partials 10 to 24 us (3000 rows of 1001: 24 -> 42) and gains from 4000 on (512
+// samples of 16 rows of 1001 columns: 104 -> 96; 8000 of 2: 426 -> 353).  16, 32, 64
+// and 256 in a set: 319, 316, 349 and 557 us for those 8000.
+constexpr int kMostUnfolded = 2048, kFoldedPartials = 32;
 
 // Outputs of the parameters' gradients.
 struct ParamGrad {

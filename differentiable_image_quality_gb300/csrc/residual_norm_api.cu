@@ -339,7 +339,10 @@ extern "C" size_t gbssim_residual_norm_workspace_bytes(const gbssim_residual_nor
 {
     if (check_desc(d) != GBSSIM_OK || row_count(*d) == 0) return 0;
     const RowPlan p = make_plan(*d, kBwdThreads, kBwdResidentPlain, {kMaxPlanSms, kMaxPlanSms / 2, kMaxPlanSms / 4, 0});
-    return size_t(p.groups) * p.classes * p.splits * kMaxSums * d->dim * sizeof(float);
+    const size_t partials = size_t(p.groups) * p.classes * p.splits;
+    const size_t folded =
+        partials > kMostUnfolded ? (partials + kFoldedPartials - 1) / kFoldedPartials * 5 : 0;
+    return (partials * kMaxSums + folded) * d->dim * sizeof(float);
 }
 
 extern "C" int gbssim_residual_norm_bwd(const gbssim_residual_norm *d,

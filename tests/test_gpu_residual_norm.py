@@ -461,6 +461,18 @@ def test_more_samples_than_a_grid_dimension(pkg):
     check(pkg, *make((70000, 1, 8), F32, BF16, per_sample=True))
 
 
+@pytest.mark.parametrize("shape", [(300, 40, 1001), (3000, 2, 72), (2049, 1, 24), (33, 400, 7),
+                                   (65, 16, 306)])
+@pytest.mark.parametrize("own", [("gate",), ("post_weight", "post_bias"), ("pre_bias",)])
+def test_many_samples_with_some_parameters_of_their_own(pkg, shape, own):
+    """Gradients per sample and shared ones from the same sums, of many samples."""
+    t, g, how = make(shape, F32, BF16, pre="layer", per_sample=True)
+    for k in NAMES[2:]:
+        if k not in own:
+            t[k] = t[k][0].contiguous()
+    check(pkg, t, g, how)
+
+
 def test_exchange_between_blocks_that_runs_out(pkg):
     """Rows of several blocks: a wait for another block's sums is bounded.  The test
     build announces more bytes than are sent: the outputs come out NaN, the device
