@@ -160,9 +160,18 @@ int device_room(Room *out)
     return GBSSIM_OK;
 }
 
+// Rows of one class that a sample with parameters of its own must have for its rows
+// to be parted into classes.  The forward gains from one on (8 rows a sample of 1001
+// columns in 64 samples: 9.9 -> 6.2 us, 16 in 512: 68 -> 27).  The backward pays a
+// set of partial sums per class: 16 rows of 1001 in 512 samples 90 us, parted 96, and
+// in 8000 samples 1016, parted 1128; 32 in 64 samples 43, parted 37.  Without such
+// parameters the classes always pay (24 rows: forward 7.2 -> 4.3, backward 10.4 -> 7.4).
+constexpr int kFwdClassRows = 1, kBwdClassRows = 4;
+
 // Blocks are planned to run all at once: a block works through its rows in a
 // loop, so that any left over would double the time.
-RowPlan make_plan(const gbssim_residual_norm &d, int most_threads, int resident, const Room &room)
+RowPlan make_plan(const gbssim_residual_norm &d, int most_threads, int resident, int class_rows,
+                  const Room &room)
 {
     RowPlan p{};
     p.device = room.device;
@@ -172,11 +181,10 @@ RowPlan make_plan(const gbssim_residual_norm &d, int most_threads, int resident,
     const long long rows = row_count(d);
     p.groups = own ? d.batch : 1;
     p.group_rows = own ? d.tokens : int(rows);
-    // Parting rows into classes costs a set of partial sums per class: not where
-    // a class would have only a few rows.  The widest rows fill a cluster's threads
-    // without a shift.
+    // Samples with parameters of their own may have too few rows to part into
+    // classes.  The widest rows fill a cluster's threads without a shift.
     p.classes = d.dim % 8 == 0 ? 1 : d.dim % 4 == 0 ? 2 : d.dim % 2 == 0 ? 4 : 8;
-    if (p.group_rows < 8 * p.classes || d.dim + 7 > kMaxDim) p.classes = 1;
+    if ((own && p.group_rows < class_rows * p.classes) || d.dim + 7 > kMaxDim) p.classes = 1;
     const int chunks = (d.dim + (p.classes > 1 ? 7 : 0) + kColsPerThread - 1) / kColsPerThread;
     // A cluster's blocks have 512 threads at most, so that the forward has two on an
     // SM: 4000 x 13000 took 152 us with four blocks a row, 185 with two.
@@ -318,7 +326,7 @@ extern "C" int gbssim_residual_norm_fwd(const gbssim_residual_norm *d, void *x_o
     Room room{};
     if ((rc = device_room(&room))) return rc;
     ResidualNormArgs a = make_args(*d);
-    a.plan = make_plan(*d, kFwdThreads, kFwdThreads, room);
+    a.plan = make_plan(*d, kFwdThreads, kFwdThreads, kFwdClassRows, room);
     if (!grid_fits(a.plan)) return GBSSIM_ESHAPE;
     a.plan.aligned = inputs_aligned(*d) && out_aligned(x_out_or_null, d->res_dtype) &&
                      out_aligned(u_or_null, d->blk_dtype);
@@ -338,7 +346,8 @@ extern "C" int gbssim_residual_norm_fwd(const gbssim_residual_norm *d, void *x_o
 extern "C" size_t gbssim_residual_norm_workspace_bytes(const gbssim_residual_norm *d)
 {
     if (check_desc(d) != GBSSIM_OK || row_count(*d) == 0) return 0;
-    const RowPlan p = make_plan(*d, kBwdThreads, kBwdResidentPlain, {kMaxPlanSms, kMaxPlanSms / 2, kMaxPlanSms / 4, 0});
+    const RowPlan p = make_plan(*d, kBwdThreads, kBwdResidentPlain, kBwdClassRows,
+                                {kMaxPlanSms, kMaxPlanSms / 2, kMaxPlanSms / 4, 0});
     const size_t partials = size_t(p.groups) * p.classes * p.splits;
     const size_t folded =
         partials > kMostUnfolded ? (partials + kFoldedPartials - 1) / kFoldedPartials * 5 : 0;
@@ -410,7 +419,7 @@ extern "C" int gbssim_residual_norm_bwd(const gbssim_residual_norm *d,
     ResidualNormArgs a = make_args(*d);
     a.gx = row_ptr(*d, gx, d->res_dtype);
     a.gu = row_ptr(*d, gu, d->blk_dtype);
-    a.plan = make_plan(*d, kBwdThreads, kBwdThreads, room);
+    a.plan = make_plan(*d, kBwdThreads, kBwdThreads, kBwdClassRows, room);
     a.plan.aligned = inputs_aligned(*d) && rows_aligned(*d, gx, d->res_dtype) &&
                      rows_aligned(*d, gu, d->blk_dtype) && out_aligned(grads->x, d->res_dtype) &&
                      out_aligned(grads->y, d->blk_dtype) &&
@@ -433,7 +442,7 @@ extern "C" int gbssim_residual_norm_bwd(const gbssim_residual_norm *d,
     // the kernel for the plainest calls leaves room for more blocks: 71050 x 964
     // bfloat16 took 223 us with 512 threads an SM, 204 with 640
     if (residual_norm_bwd_plain(a) && (a.plan.aligned || d->blk_dtype != GBSSIM_F32))
-        replan_blocks(a.plan, make_plan(*d, kBwdThreads, kBwdResidentPlain, room));
+        replan_blocks(a.plan, make_plan(*d, kBwdThreads, kBwdResidentPlain, kBwdClassRows, room));
     ParamGrads g{};
     if (!d->gate_rows.data) g.gate = {grads->gate, d->gate.dtype, a.gate.per_sample};
     g.w1 = {grads->post_weight, d->post_weight.dtype, a.w1.per_sample};
