@@ -10,7 +10,8 @@
 // and can be captured in a CUDA graph.  Tensors are cut into chunks of 32 KB; a
 // block takes a contiguous run of chunks, whatever tensors they belong to, so
 // the work is even for any mix of sizes, and the order of every sum depends on
-// the sizes alone: the same inputs give the same bits.
+// the sizes, the alignments and the device alone: the same inputs give the same
+// bits.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -25,7 +26,7 @@ namespace gbssim {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlocksPerSm = 8;
+constexpr int kBlocksPerSm = 8;        // the norm of 1.0 G bfloat16: 290 us, 4 302, 5 308, 6 323
 constexpr int kMaxBlocks = 2048;       // of one norm launch: sizes the workspace
 constexpr int kVecs = 8;               // 16-byte words a thread holds of a norm chunk
 constexpr int kChunkWords = kThreads * kVecs;  // 32 KB
@@ -64,6 +65,8 @@ struct ScaleTable {
 };
 
 constexpr unsigned char kApart = 8;  // gradient and output are not aligned alike
+// Two sizes of tables, as a launch copies all of its parameters: 26 tensors, time
+// on the host, norm 21.5 us with the small one, 24.5 with the large, clip 27.0 and 31.2.
 constexpr int kCapSmall = 32, kCapLarge = 1024;
 static_assert(sizeof(ScaleTable<kCapLarge>) <= 32764, "kernel parameter space");
 static_assert(sizeof(NormTable<kCapLarge>) <= 32764, "kernel parameter space");
