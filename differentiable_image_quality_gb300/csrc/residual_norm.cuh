@@ -83,12 +83,14 @@ struct ResidualNormArgs {
     int sum_a, sum_f, sum_c, sum_e, sums;  // places of the column sums, -1: not wanted
 };
 
-// Partials beyond kMostUnfolded are first folded, kFoldedPartials into one set of
-// the five parameters' gradients.  The extra kernel costs calls of 500 to 2000
-// partials 10 to 24 us (3000 rows of 1001: 24 -> 42) and gains from 4000 on (512
-// samples of 16 rows of 1001 columns: 104 -> 96; 8000 of 2: 426 -> 353).  16, 32, 64
-// and 256 in a set: 319, 316, 349 and 557 us for those 8000.
-constexpr int kMostUnfolded = 2048, kFoldedPartials = 32;
+// The gradients that many samples share, where others are per sample.  Partials are
+// first folded, kFoldedPartials into one set of the five gradients, where more groups
+// have factors of their own than a column has threads, and where there are more than
+// kMostUnfolded: backward, bfloat16, folded and not, 1000 x 8 x 1024 52 and 44 us, 8000 x 2 x
+// 1024 221 and 201, 16000 x 2 x 256 186 and 200.  8, 16, 32 and 64 in a set: 31, 33, 38 and
+// 47 us at 512 x 8 x 1024, 427, 402, 393 and 390 at 8000 x 16 x 306.
+constexpr int kFinishLanes = 64;  // threads of a column that add its partials
+constexpr int kMostUnfolded = 8192, kFoldedPartials = 16;
 
 // Outputs of the parameters' gradients.
 struct ParamGrad {
@@ -331,20 +333,6 @@ __device__ __forceinline__ void store_cols(T *to, const Cols<ALIGNED> &c, bool a
             }
         }
     }
-}
-
-template <typename T>
-__device__ __forceinline__ float load_param1(const void *p, long long i)
-{
-    return to_f32(static_cast<const T *>(p)[i]);
-}
-
-__device__ __forceinline__ float param_at(const ParamPtr &p, int group, int col)
-{
-    const long long i = group * p.stride + col;
-    return p.type == GBSSIM_F32    ? load_param1<float>(p.p, i)
-           : p.type == GBSSIM_BF16 ? load_param1<bf16>(p.p, i)
-                                   : load_param1<f16>(p.p, i);
 }
 
 // The thread's eight values of a parameter as they lie in memory.  A block asks for

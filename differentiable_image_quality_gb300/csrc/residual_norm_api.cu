@@ -381,7 +381,7 @@ extern "C" size_t gbssim_residual_norm_workspace_bytes(const gbssim_residual_nor
                                 {kMaxPlanSms, kMaxPlanSms / 2, kMaxPlanSms / 4, 0, true});
     const size_t partials = size_t(p.groups) * p.classes * p.splits;
     const size_t folded =
-        partials > kMostUnfolded ? (partials + kFoldedPartials - 1) / kFoldedPartials * 5 : 0;
+        p.groups > kFinishLanes ? (partials + kFoldedPartials - 1) / kFoldedPartials * 5 : 0;
     return (partials * kMaxSums + folded) * d->dim * sizeof(float);
 }
 

@@ -1,10 +1,13 @@
 // The second part of the residual norm's backward: the parameters' gradients from
 // the blocks' column sums.  Its reads are the partials, some megabytes in most
 // calls; what it costs there is the time of a few dependent loads, so a column's
-// partials go to 64 threads.  Calls of thousands of samples with parameters of
-// their own have many groups of few partials instead: there a thread takes a
-// column of a group, and what all groups share is folded 64 partials at a time
-// first (16000 rows of 1001 columns in 8000 samples: 7.1 ms without that).
+// partials go to 64 threads, and a thread asks for all that it reads at once (8 x 600
+// x 1024 with a gate per sample 33 us one after the other, 29 so).  Calls of many
+// samples with parameters of their own have many groups of few partials instead:
+// there a thread takes a column of a group, and what all groups share is folded 16
+// partials at a time first (16000 rows of 1001 columns in 8000 samples: 7.1 ms
+// without that, 0.33 with).  Four blocks an SM in those: 8000 x 16 x 1001 940 us, 962
+// with the two that the registers would leave.
 #include <climits>
 
 #include "residual_norm.cuh"
@@ -12,11 +15,12 @@
 namespace gbssim {
 namespace {
 
-constexpr int kFinishCols = 8, kFinishLanes = 64;
-// A group's partials go to one thread a column where they are fewer than this and
-// the groups more: 64 lanes would idle and the grid be long (512 samples of 16 rows
-// of 1001 columns: 96 us, 353 with 64 threads a column; 64 samples of 32: 37, 65).
-constexpr int kFewPartials = 32;
+constexpr int kFinishCols = 8;
+// Gradients that groups have of their own: from this many on a thread takes one, its
+// partials one after the other, where 64 threads a column would make a long grid
+// (backward, bfloat16, all parameters per sample: 4 x 400 x 4096 39 us, 32 so;
+// 24 x 300 x 1024 41, 27; below, 8 x 1024 x 1152 33, 35 so, 2 x 400 x 4096 26, 31).
+constexpr int kManyOwn = 12288;
 constexpr int kGroupThreads = 256;
 
 __device__ __forceinline__ void store_param(const ParamGrad &g, int group, int dim, int col, float v)
@@ -33,25 +37,50 @@ __device__ __forceinline__ const ParamGrad &output(const ParamGrads &g, int k)
     return k == 0 ? g.gate : k == 1 ? g.w1 : k == 2 ? g.b1 : k == 3 ? g.w2 : g.b2;
 }
 
-// The gradients of gate, w1, b1, w2, b2 at one column, added up over partials.
-struct ColumnGrads {
-    float v[5] = {};
-    // what turns A and F into the gradients, of one group
-    float gate, w, b;
-    __device__ __forceinline__ void factors(const ResidualNormArgs &a, int group, int col)
+// A parameter's value at a column as it lies in memory: all are asked for before
+// the first is converted.
+__device__ __forceinline__ uint32_t ask(const ParamPtr &p, int group, int col)
+{
+    if (!p.p) return 0;
+    const long long i = group * p.stride + col;
+    return p.type == GBSSIM_F32 ? __ldg(static_cast<const uint32_t *>(p.p) + i)
+                                : __ldg(static_cast<const unsigned short *>(p.p) + i);
+}
+
+__device__ __forceinline__ float told(const ParamPtr &p, uint32_t v)
+{
+    return p.type == GBSSIM_F32    ? __uint_as_float(v)
+           : p.type == GBSSIM_BF16 ? __uint_as_float(v << 16)
+                                   : __half2float(__ushort_as_half((unsigned short)v));
+}
+
+// What turns A and F into the gradients of a group's gate, w1 and b1.
+struct Factors {
+    uint32_t gate, w, b;
+    __device__ __forceinline__ void fetch(const ResidualNormArgs &a, int group, int col)
     {
-        gate = a.gate.p && !a.gate_rows.p ? param_at(a.gate, group, col) : 1.0f;
-        w = a.w1.p ? param_at(a.w1, group, col) + a.offset : 1.0f;
-        b = a.b1.p ? param_at(a.b1, group, col) : 0.0f;
+        gate = a.gate_rows.p ? 0 : ask(a.gate, group, col);
+        w = ask(a.w1, group, col);
+        b = ask(a.b1, group, col);
     }
-    __device__ __forceinline__ void add(const ResidualNormArgs &a, long long p, int col)
+};
+
+// The column sums of a thread's partials, and the gradients they make.
+struct ColumnSums {
+    float A = 0.0f, F = 0.0f, C = 0.0f, E = 0.0f;
+
+    __device__ __forceinline__ ColumnSums operator+(const ColumnSums &o) const
     {
-        const float *src = a.partials + p * a.sums * a.dim + col;
-        const float A = a.sum_a >= 0 ? __ldcg(src + (long long)a.sum_a * a.dim) : 0.0f;
-        const float F = a.sum_f >= 0 ? __ldcg(src + (long long)a.sum_f * a.dim) : 0.0f;
-        const float C = a.sum_c >= 0 ? __ldcg(src + (long long)a.sum_c * a.dim) : 0.0f;
-        const float E = a.sum_e >= 0 ? __ldcg(src + (long long)a.sum_e * a.dim) : 0.0f;
-        v[0] += fmaf(w, A, b * F);
+        ColumnSums s;
+        s.A = A + o.A, s.F = F + o.F, s.C = C + o.C, s.E = E + o.E;
+        return s;
+    }
+    // adds to the gradients of gate, w1, b1, w2, b2
+    __device__ __forceinline__ void add_to(float (&v)[5], const ResidualNormArgs &a, const Factors &f) const
+    {
+        const float gate = a.gate.p && !a.gate_rows.p ? told(a.gate, f.gate) : 1.0f;
+        const float w = a.w1.p ? told(a.w1, f.w) + a.offset : 1.0f;
+        v[0] += fmaf(w, A, told(a.b1, f.b) * F);
         v[1] = fmaf(gate, A, v[1]);
         v[2] = fmaf(gate, F, v[2]);
         v[3] += C;
@@ -59,8 +88,51 @@ struct ColumnGrads {
     }
 };
 
+// Reads partials: only the sums that the outputs of one kind (per sample or shared)
+// are made of.
+struct Reader {
+    const float *p;
+    long long step;         // from a partial to the next
+    long long a, f, c, e;   // -1: not wanted
+    __device__ __forceinline__ Reader(const ResidualNormArgs &n, const ParamGrads &g, bool shared, int col)
+        : p(n.partials + col), step((long long)n.sums * n.dim)
+    {
+        const bool first = wants(g.gate, shared) || wants(g.w1, shared) || wants(g.b1, shared);
+        a = first && n.sum_a >= 0 ? (long long)n.sum_a * n.dim : -1;
+        f = first && n.sum_f >= 0 ? (long long)n.sum_f * n.dim : -1;
+        c = wants(g.w2, shared) ? (long long)n.sum_c * n.dim : -1;
+        e = wants(g.b2, shared) ? (long long)n.sum_e * n.dim : -1;
+    }
+    static __device__ __forceinline__ bool wants(const ParamGrad &g, bool shared)
+    {
+        return g.p && bool(g.per_sample) != shared;
+    }
+    __device__ __forceinline__ ColumnSums at(long long i, bool there) const
+    {
+        const float *q = p + i * step;
+        ColumnSums s;
+        if (there && a >= 0) s.A = __ldcg(q + a);
+        if (there && f >= 0) s.F = __ldcg(q + f);
+        if (there && c >= 0) s.C = __ldcg(q + c);
+        if (there && e >= 0) s.E = __ldcg(q + e);
+        return s;
+    }
+    // partials begin, begin + by, ... below end, four of them at a time
+    __device__ __forceinline__ ColumnSums over(long long begin, long long end, int by) const
+    {
+        ColumnSums s;
+        for (long long i = begin; i < end; i += 4 * by) {
+            ColumnSums t[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[k] = at(i + k * by, i + k * by < end);
+            s = s + ((t[0] + t[1]) + (t[2] + t[3]));
+        }
+        return s;
+    }
+};
+
 // Whether groups have different factors.
-__device__ __forceinline__ bool factors_vary(const ResidualNormArgs &a)
+__host__ __device__ inline bool factors_vary(const ResidualNormArgs &a)
 {
     return a.gate.stride || a.w1.stride || a.b1.stride;
 }
@@ -92,7 +164,8 @@ __device__ __forceinline__ void finish_columns(float (&v)[5], const ResidualNorm
 
 // A block takes 8 columns (one sector of each partial), 64 threads of a column
 // every 64th partial each.  Part y < groups of the grid makes the gradients that
-// each group has of its own, the last those shared by all.
+// each group has of its own, the last those shared by all: where groups have
+// factors of their own (at most 64 then), a thread's partials are of one group.
 __global__ void __launch_bounds__(kFinishCols * kFinishLanes)
     residual_norm_finish_kernel(const __grid_constant__ ResidualNormArgs a,
                                 const __grid_constant__ ParamGrads g, int shared_part)
@@ -100,66 +173,79 @@ __global__ void __launch_bounds__(kFinishCols * kFinishLanes)
     const int lane = threadIdx.x / kFinishCols;
     const int across = (a.dim + kFinishCols - 1) / kFinishCols;  // blocks of a part
     const int y = int(blockIdx.x) / across, first = (int(blockIdx.x) - y * across) * kFinishCols;
-    const int col = first + threadIdx.x % kFinishCols;
+    const int col = min(first + int(threadIdx.x) % kFinishCols, a.dim - 1);
     const bool shared = y == shared_part;
     const int each = a.plan.classes * a.plan.splits;  // partials of a group
-    const int p0 = shared ? 0 : y * each;
-    const int p1 = shared ? a.plan.groups * each : p0 + each;
-    ColumnGrads c;
+    const bool vary = shared && each > 0 && factors_vary(a);
+    const int by = vary ? kFinishLanes / a.plan.groups : kFinishLanes;
+    const int group = !shared ? y : vary ? min(lane / by, a.plan.groups - 1) : 0;
+    const long long p0 = (long long)group * each;
+    const long long p1 = shared && !vary ? (long long)a.plan.groups * each : p0 + each;
+    Factors f{};
+    if (a.plan.groups > 0) f.fetch(a, group, col);
+    const Reader r(a, g, shared, col);
+    float v[5] = {};
     pdl_wait();
-    if (col < a.dim && p0 < p1) {
-        const bool vary = shared && factors_vary(a);
-        if (!vary) c.factors(a, p0 / each, col);
-#pragma unroll 4
-        for (long long p = p0 + lane; p < p1; p += kFinishLanes) {
-            if (vary) c.factors(a, int(p) / each, col);
-            c.add(a, p, col);
-        }
-    }
-    finish_columns(c.v, a, g, first, y, shared);
+    // (threads past the last group's have no partials)
+    r.over(vary && lane >= by * a.plan.groups ? p1 : p0 + (vary ? lane % by : lane), p1, by).add_to(v, a, f);
+    finish_columns(v, a, g, first, y, shared);
 }
 
 // The gradients that groups have of their own, a thread for a column of a group.
-__global__ void __launch_bounds__(kGroupThreads)
+__global__ void __launch_bounds__(kGroupThreads, 4)
     residual_norm_groups_kernel(const __grid_constant__ ResidualNormArgs a,
                                 const __grid_constant__ ParamGrads g)
 {
     const int across = (a.dim + kGroupThreads - 1) / kGroupThreads;
     const int group = int(blockIdx.x) / across;
-    const int col = (int(blockIdx.x) - group * across) * kGroupThreads + threadIdx.x;
-    const int each = a.plan.classes * a.plan.splits;
+    const int at = (int(blockIdx.x) - group * across) * kGroupThreads + threadIdx.x;
+    const int col = min(at, a.dim - 1), each = a.plan.classes * a.plan.splits;
+    Factors f;
+    f.fetch(a, group, col);
+    const Reader r(a, g, false, col);
+    float v[5] = {};
+    pdl_trigger();
     pdl_wait();
-    if (col >= a.dim) return;
-    ColumnGrads c;
-    c.factors(a, group, col);
-#pragma unroll 4
-    for (int p = 0; p < each; ++p) c.add(a, (long long)group * each + p, col);
+    r.over((long long)group * each, ((long long)group + 1) * each, 1).add_to(v, a, f);
 #pragma unroll
     for (int k = 0; k < 5; ++k)
-        if (output(g, k).per_sample) store_param(output(g, k), group, a.dim, col, c.v[k]);
+        if (at < a.dim && output(g, k).per_sample) store_param(output(g, k), group, a.dim, at, v[k]);
 }
 
 // kFoldedPartials partials of all groups into one set of the five gradients.
-__global__ void __launch_bounds__(kGroupThreads)
-    residual_norm_fold_kernel(const __grid_constant__ ResidualNormArgs a, float *folded, int partials)
+__global__ void __launch_bounds__(kGroupThreads, 4)
+    residual_norm_fold_kernel(const __grid_constant__ ResidualNormArgs a,
+                              const __grid_constant__ ParamGrads g, float *folded, int partials)
 {
     const int across = (a.dim + kGroupThreads - 1) / kGroupThreads;
     const int chunk = int(blockIdx.x) / across;
-    const int col = (int(blockIdx.x) - chunk * across) * kGroupThreads + threadIdx.x;
-    const int each = a.plan.classes * a.plan.splits;
-    pdl_wait();
-    if (col >= a.dim) return;
+    const int at = (int(blockIdx.x) - chunk * across) * kGroupThreads + threadIdx.x;
+    const int col = min(at, a.dim - 1), each = a.plan.classes * a.plan.splits;
     const int p0 = chunk * kFoldedPartials, count = min(kFoldedPartials, partials - p0);
-    const bool vary = factors_vary(a);
-    ColumnGrads c;
-    c.factors(a, p0 / each, col);
-#pragma unroll 4
-    for (int i = 0; i < count; ++i) {
-        if (vary && (p0 + i) % each == 0) c.factors(a, (p0 + i) / each, col);
-        c.add(a, p0 + i, col);
-    }
+    const Reader r(a, g, true, col);
+    float v[5] = {};
+    pdl_trigger();
+    pdl_wait();
+    if (factors_vary(a)) {
+        for (int i = 0; i < count; i += 4) {
+            Factors f[4];
+            ColumnSums t[4];
 #pragma unroll
-    for (int k = 0; k < 5; ++k) folded[((long long)chunk * 5 + k) * a.dim + col] = c.v[k];
+            for (int k = 0; k < 4; ++k) {
+                f[k].fetch(a, (p0 + min(i + k, count - 1)) / each, col);
+                t[k] = r.at(p0 + i + k, i + k < count);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[k].add_to(v, a, f[k]);
+        }
+    } else {
+        Factors f;
+        f.fetch(a, 0, col);
+        r.over(p0, (long long)p0 + count, 1).add_to(v, a, f);
+    }
+    if (at >= a.dim) return;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) folded[((long long)chunk * 5 + k) * a.dim + at] = v[k];
 }
 
 // The gradients shared by all groups, from the folded ones.
@@ -219,9 +305,10 @@ cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk
     const int threads = kFinishCols * kFinishLanes;
     const long long across = up(a.dim, kFinishCols);
     // (without rows there are no partials, and all gradients are zero)
-    const bool few = own && each < kFewPartials && a.plan.groups > kFewPartials && partials > 0;
-    const bool many = shared && partials > kMostUnfolded;
-    if (few) {
+    const bool many_own = own && (long long)a.plan.groups * a.dim >= kManyOwn && partials > 0;
+    const bool many = shared && partials > 0 && a.plan.groups > kFinishLanes &&
+                      (factors_vary(a) || partials > kMostUnfolded);
+    if (many_own) {
         e = launch_next(residual_norm_groups_kernel, a.plan.groups * up(a.dim, kGroupThreads),
                         kGroupThreads, s, a, g);
         own = false;
@@ -230,7 +317,7 @@ cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk
         float *folded = a.partials + partials * a.sums * a.dim;
         const int n = int(partials), chunks = int(up(partials, kFoldedPartials));
         e = launch_next(residual_norm_fold_kernel, chunks * up(a.dim, kGroupThreads), kGroupThreads, s,
-                        a, folded, n);
+                        a, g, folded, n);
         if (e == cudaSuccess)
             e = launch_next(residual_norm_finish_folded_kernel, across, threads, s, a, g,
                             static_cast<const float *>(folded), chunks);

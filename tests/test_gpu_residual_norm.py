@@ -473,6 +473,31 @@ def test_many_samples_with_some_parameters_of_their_own(pkg, shape, own):
     check(pkg, t, g, how)
 
 
+@pytest.mark.parametrize("shape", [(0, 5, 64), (2, 0, 64), (70, 0, 24)])
+@pytest.mark.parametrize("own", [("gate",), ("post_weight", "pre_bias"), NAMES[2:]])
+def test_no_rows_with_parameters_per_sample(pkg, shape, own):
+    t, g, how = make(shape, F32, BF16, per_sample=True)
+    for k in NAMES[2:]:
+        if k not in own:
+            t[k] = torch.ones(shape[-1], device="cuda")
+    args = {k: t[k] for k in NAMES[2:]}
+    stats = pkg.residual_norm_fwd(t["x"], t["y"], want_stats=True, **args, **how)[2]
+    grads = pkg.residual_norm_bwd(g["x"], g["u"], t["x"], t["y"], stats, **args, **how)
+    for k, v in zip(NAMES, grads):
+        assert v.shape == t[k].shape and bool((v == 0).all())
+
+
+@pytest.mark.parametrize("own", [("gate",), ("post_weight",), ("pre_weight", "pre_bias")])
+@pytest.mark.parametrize("shape", [(5, 60, 264), (64, 3, 1001), (7, 130, 4096), (20, 40, 256)])
+@pytest.mark.parametrize("par", [F16, BF16])
+def test_shared_and_own_parameters_of_a_few_samples(pkg, shape, own, par):
+    t, g, how = make(shape, F32, BF16, par, post="layer", per_sample=True)
+    for k in NAMES[2:]:
+        if k not in own:
+            t[k] = t[k][0].contiguous()
+    check(pkg, t, g, how)
+
+
 def test_exchange_between_blocks_that_runs_out(pkg):
     """Rows of several blocks: a wait for another block's sums is bounded.  The test
     build announces more bytes than are sent: the outputs come out NaN, the device
