@@ -14,8 +14,8 @@
 // written once.  x^ and y^ are formed again from x, y and the saved statistics,
 // not stored.  Column sums stay in registers over a block's rows (float32), go
 // to a partial per block, and a second kernel adds the partials in a fixed
-// order.  32400 x 4096 bfloat16 with a gate per row: 386 us for 2.1 GB (81 % of
-// the copy rate); 71050 x 964 bfloat16 202 us (60 %), 32400 x 1001 float16 136 us
+// order.  32400 x 4096 bfloat16 with a gate per row: 385 us for 2.1 GB (81 % of
+// the copy rate); 71050 x 964 bfloat16 199 us (61 %), 32400 x 1001 float16 133 us
 // (42 %): instruction issue, and with 96 to 128 registers a thread only 16 to 20
 // warps to cover a row's two sums.
 #pragma once
