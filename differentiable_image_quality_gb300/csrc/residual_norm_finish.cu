@@ -1,12 +1,12 @@
 // The second part of the residual norm's backward: the parameters' gradients from
 // the blocks' column sums.  Its reads are the partials, some megabytes in most
 // calls; what it costs there is the time of a few dependent loads, so a column's
-// partials go to 64 threads, and a thread asks for all that it reads at once (8 x 600
-// x 1024 with a gate per sample 33 us one after the other, 29 so).  Calls of many
+// partials go to 16 to 64 threads, and a thread asks for all that it reads at once (8 x
+// 2000 x 256 with a gate per sample 23 us one after the other, 18 so).  Calls of many
 // samples with parameters of their own have many groups of few partials instead:
 // there a thread takes a column of a group, and what all groups share is folded 16
 // partials at a time first (16000 rows of 1001 columns in 8000 samples: 7.1 ms
-// without that, 0.33 with).  Four blocks an SM in those: 8000 x 16 x 1001 940 us, 962
+// without that, 0.31 with).  Four blocks an SM in those: 8000 x 16 x 1001 940 us, 962
 // with the two that the registers would leave.
 #include <climits>
 
@@ -137,47 +137,48 @@ __host__ __device__ inline bool factors_vary(const ResidualNormArgs &a)
     return a.gate.stride || a.w1.stride || a.b1.stride;
 }
 
-// Adds v over the block's 64 threads of a column, in a fixed order, and stores the
-// outputs that are per sample, or those that are not.
+// Adds v over the block's LANES threads of each of its COLS columns, in a fixed order,
+// and stores the outputs that are per sample, or those that are not.
+template <int COLS, int LANES>
 __device__ __forceinline__ void finish_columns(float (&v)[5], const ResidualNormArgs &a,
                                                const ParamGrads &g, int first, int group, bool shared)
 {
-    constexpr int kWarps = kFinishCols * kFinishLanes / 32;
-    __shared__ float part[5][kWarps][kFinishCols];
-    // a warp holds four threads of each column
+    constexpr int kWarps = COLS * LANES / 32;
+    __shared__ float part[5][kWarps][COLS];
 #pragma unroll
     for (int k = 0; k < 5; ++k) {
-        v[k] += __shfl_xor_sync(0xffffffffu, v[k], 8);
-        v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
-        if ((threadIdx.x & 31) < kFinishCols) part[k][threadIdx.x / 32][threadIdx.x & 7] = v[k];
+#pragma unroll
+        for (int off = COLS; off < 32; off *= 2) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+        if ((threadIdx.x & 31) < COLS) part[k][threadIdx.x / 32][threadIdx.x & 31] = v[k];
     }
     __syncthreads();
-    if (threadIdx.x < 5 * kFinishCols) {
-        const int k = threadIdx.x / kFinishCols, to = first + threadIdx.x % kFinishCols;
+    if (threadIdx.x < 5 * COLS) {
+        const int k = threadIdx.x / COLS, to = first + threadIdx.x % COLS;
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += part[k][w][threadIdx.x % kFinishCols];
+        for (int w = 0; w < kWarps; ++w) s += part[k][w][threadIdx.x % COLS];
         const ParamGrad &out = output(g, k);
         if (to < a.dim && bool(out.per_sample) != shared) store_param(out, group, a.dim, to, s);
     }
 }
 
-// A block takes 8 columns (one sector of each partial), 64 threads of a column
-// every 64th partial each.  Part y < groups of the grid makes the gradients that
-// each group has of its own, the last those shared by all: where groups have
-// factors of their own (at most 64 then), a thread's partials are of one group.
-__global__ void __launch_bounds__(kFinishCols * kFinishLanes)
+// A block takes COLS columns (whole sectors of each partial), LANES threads of a
+// column every LANES-th partial each.  Part y < groups of the grid makes the gradients
+// that each group has of its own, the last those shared by all: where groups have
+// factors of their own (at most LANES groups then), a thread's partials are of one.
+template <int COLS, int LANES>
+__global__ void __launch_bounds__(COLS * LANES)
     residual_norm_finish_kernel(const __grid_constant__ ResidualNormArgs a,
                                 const __grid_constant__ ParamGrads g, int shared_part)
 {
-    const int lane = threadIdx.x / kFinishCols;
-    const int across = (a.dim + kFinishCols - 1) / kFinishCols;  // blocks of a part
-    const int y = int(blockIdx.x) / across, first = (int(blockIdx.x) - y * across) * kFinishCols;
-    const int col = min(first + int(threadIdx.x) % kFinishCols, a.dim - 1);
+    const int lane = threadIdx.x / COLS;
+    const int across = (a.dim + COLS - 1) / COLS;  // blocks of a part
+    const int y = int(blockIdx.x) / across, first = (int(blockIdx.x) - y * across) * COLS;
+    const int col = min(first + int(threadIdx.x) % COLS, a.dim - 1);
     const bool shared = y == shared_part;
     const int each = a.plan.classes * a.plan.splits;  // partials of a group
     const bool vary = shared && each > 0 && factors_vary(a);
-    const int by = vary ? kFinishLanes / a.plan.groups : kFinishLanes;
+    const int by = vary ? LANES / a.plan.groups : LANES;
     const int group = !shared ? y : vary ? min(lane / by, a.plan.groups - 1) : 0;
     const long long p0 = (long long)group * each;
     const long long p1 = shared && !vary ? (long long)a.plan.groups * each : p0 + each;
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kFinishCols * kFinishLanes)
     pdl_wait();
     // (threads past the last group's have no partials)
     r.over(vary && lane >= by * a.plan.groups ? p1 : p0 + (vary ? lane % by : lane), p1, by).add_to(v, a, f);
-    finish_columns(v, a, g, first, y, shared);
+    finish_columns<COLS, LANES>(v, a, g, first, y, shared);
 }
 
 // The gradients that groups have of their own, a thread for a column of a group.
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kFinishCols * kFinishLanes)
 #pragma unroll
             for (int k = 0; k < 5; ++k) v[k] += __ldcg(folded + ((long long)c * 5 + k) * a.dim + col);
     }
-    finish_columns(v, a, g, first, 0, true);
+    finish_columns<kFinishCols, kFinishLanes>(v, a, g, first, 0, true);
 }
 
 // Each of these kernels may start while the one ahead of it ends.
@@ -302,8 +303,6 @@ cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk
         if (p->p) (p->per_sample ? own : shared) = true;
     const int each = a.plan.classes * a.plan.splits;
     const long long partials = (long long)a.plan.groups * each;
-    const int threads = kFinishCols * kFinishLanes;
-    const long long across = up(a.dim, kFinishCols);
     // (without rows there are no partials, and all gradients are zero)
     const bool many_own = own && (long long)a.plan.groups * a.dim >= kManyOwn && partials > 0;
     const bool many = shared && partials > 0 && a.plan.groups > kFinishLanes &&
@@ -319,14 +318,28 @@ cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk
         e = launch_next(residual_norm_fold_kernel, chunks * up(a.dim, kGroupThreads), kGroupThreads, s,
                         a, g, folded, n);
         if (e == cudaSuccess)
-            e = launch_next(residual_norm_finish_folded_kernel, across, threads, s, a, g,
+            e = launch_next(residual_norm_finish_folded_kernel, up(a.dim, kFinishCols),
+                            kFinishCols * kFinishLanes, s, a, g,
                             static_cast<const float *>(folded), chunks);
         shared = false;
     }
     if (e != cudaSuccess || !(own || shared)) return e;
-    const int shared_part = own ? a.plan.groups : 0;
-    return launch_next(residual_norm_finish_kernel, across * (shared_part + (shared ? 1 : 0)), threads,
-                       s, a, g, shared_part);
+    // Blocks that all run at once: 64 threads a column, for the shortest chain of loads.
+    // Otherwise fewer of them, by how many partials there are, and more columns a
+    // block.  Backward, bfloat16, a gate per sample, with 8 columns of 64, 16 of 32 and
+    // 16 of 16: 3000 x 1024 (256 blocks of the first) 18, 21, 23 us; 4000 x 2048 (512) 32,
+    // 30, 30; 3000 x 4096 47, 45, 43; 1000 x 8192 49, 42, 40; 32 x 200 x 306 31, 29, 34;
+    // 8 x 600 x 1024 29, 25, 26.
+    constexpr int kLongGrid = 304, kFewPartials = 160;
+    const int shared_part = own ? a.plan.groups : 0, parts = shared_part + (shared ? 1 : 0);
+    const int most_groups = shared && factors_vary(a) ? a.plan.groups : 0;
+    if (parts * up(a.dim, kFinishCols) <= kLongGrid || most_groups > 32)
+        return launch_next(residual_norm_finish_kernel<kFinishCols, kFinishLanes>,
+                           parts * up(a.dim, kFinishCols), kFinishCols * kFinishLanes, s, a, g, shared_part);
+    if (partials > kFewPartials || most_groups > 16)
+        return launch_next(residual_norm_finish_kernel<16, 32>, parts * up(a.dim, 16), 512, s, a, g,
+                           shared_part);
+    return launch_next(residual_norm_finish_kernel<16, 16>, parts * up(a.dim, 16), 256, s, a, g, shared_part);
 }
 
 }  // namespace gbssim
