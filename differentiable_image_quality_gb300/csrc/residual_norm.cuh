@@ -374,7 +374,9 @@ __device__ __forceinline__ RawParam fetch_param(const ParamPtr &p, int group, co
     return r;
 }
 
-// The values plus `offset`; `missing` where the parameter is null.
+// The values plus `offset`; `missing` where the parameter is null.  Either way zero in
+// columns that the row does not have: a mean puts something into y^ and x^ there, and
+// this factor keeps it out of the row's sums.
 template <bool ALIGNED>
 __device__ __forceinline__ void param_values(const ParamPtr &p, const RawParam &r,
                                              const Cols<ALIGNED> &c, float offset, float missing,
@@ -383,9 +385,7 @@ __device__ __forceinline__ void param_values(const ParamPtr &p, const RawParam &
     if (!p.p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = both(missing);
-        return;
-    }
-    if (p.type == GBSSIM_F32) {
+    } else if (p.type == GBSSIM_F32) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             v[e] = pair(__uint_as_float(r.w[2 * e]), __uint_as_float(r.w[2 * e + 1]));
@@ -397,7 +397,7 @@ __device__ __forceinline__ void param_values(const ParamPtr &p, const RawParam &
             v[e] = pair(h.x, h.y);
         }
     }
-    if (offset != 0.0f) {
+    if (p.p && offset != 0.0f) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = add2(v[e], both(offset));
     }

@@ -571,3 +571,37 @@ def test_refusals(pkg):
         pkg.residual_norm_bwd(g["x"], None, x, y, stats[:1])
     with pytest.raises(ValueError):
         pkg.residual_norm_bwd(g["x"].to(BF16), None, x, y, stats)
+
+
+def without(t, names):
+    """The inputs with these parameters left out, and y's mean twice its deviation."""
+    t = {k: v for k, v in t.items() if k not in names}
+    t["y"] = (t["y"].float() + 1.6).to(t["y"].dtype)
+    return t
+
+
+@pytest.mark.parametrize("post,pre", list(itertools.product([None, "rms", "layer"], repeat=2)))
+@pytest.mark.parametrize("gate", [None, "dim", "rows"])
+@pytest.mark.parametrize("names", [("post_weight",), ("pre_weight",), ("post_weight", "pre_weight"),
+                                   NAMES[3:]], ids=str)
+def test_norms_without_weights(pkg, post, pre, gate, names):
+    """A weight that is left out is one in the row's columns, and nothing beside them."""
+    for dim in (72, 515):
+        t, g, how = make((2, 9, dim), F32, BF16, post=post, pre=pre, gate=gate, scale=0.5)
+        check(pkg, without(t, names), g, how)
+
+
+@pytest.mark.parametrize("dim", DIMS + [960, 1408, 2880])
+@pytest.mark.parametrize("pair", [(F32, F32), (BF16, BF16), (F32, F16)], ids=str)
+@pytest.mark.parametrize("post,pre", [("layer", "rms"), ("layer", "layer"), ("rms", "layer")])
+def test_widths_without_parameters(pkg, dim, pair, post, pre):
+    t, g, how = make((2, 7, dim), *pair, post=post, pre=pre, seed=dim)
+    check(pkg, without(t, NAMES[2:]), g, how)
+
+
+@pytest.mark.parametrize("dim", [8200, 9001, 12344])
+@pytest.mark.parametrize("gate", [None, "dim", "rows"])
+def test_rows_shared_by_blocks_without_weights(pkg, dim, gate):
+    for post, pre in (("layer", "rms"), ("layer", "layer"), ("rms", "layer")):
+        t, g, how = make((2, 40, dim), BF16, BF16, gate=gate, post=post, pre=pre)
+        check(pkg, without(t, NAMES[3:]), g, how)
