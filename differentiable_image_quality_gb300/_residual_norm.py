@@ -128,7 +128,7 @@ def _describe(x, y, gate, post_norm, post_weight, post_bias, pre_norm, pre_weigh
             raise ValueError("u has the type of y")
         y_rows = _rows("y", y, ext)
         if gate is not None:
-            if _gate_is_rows(gate, x):
+            if _gate_is_rows(gate, x, y, ext):
                 if _check("gate", gate, index) != blk:
                     raise TypeError(f"a gate per row must have the type of y, got {gate.dtype}")
                 gate_rows = _rows("gate", gate, ext)
@@ -146,8 +146,12 @@ def _describe(x, y, gate, post_norm, post_weight, post_bias, pre_norm, pre_weigh
     return desc, ext, index, u_type
 
 
-def _gate_is_rows(gate, x) -> bool:
-    return isinstance(gate, torch.Tensor) and gate.dim() > 1 and gate.shape == x.shape
+def _gate_is_rows(gate, x, y, ext) -> bool:
+    """A gate of x's shape is one per row, except beside one token a sample: there it is
+    also one per sample, [samples, 1, dim], and has to be where its type is its own."""
+    if not isinstance(gate, torch.Tensor) or gate.dim() < 2 or gate.shape != x.shape:
+        return False
+    return gate.dim() < 3 or ext[1] != 1 or gate.dtype == y.dtype
 
 
 def residual_norm_fwd(x, y=None, gate=None, *, post_norm=None, post_weight=None, post_bias=None,
@@ -285,9 +289,10 @@ def fused_residual_norm(x, y=None, gate=None, *, post_norm=None, post_weight=Non
     tensors of one shape [..., dim], dim up to 16384; with three or more
     dimensions the first counts samples.  Weights, biases and the gate are [dim],
     or [samples, dim] (conditioned norms and gates; [samples, 1, dim] as well);
-    the gate may also have the shape of x.  y and u are float32, bfloat16 or
-    float16, x the same or float32; parameters have any of the three.  Rows may
-    lie at any stride, the columns of a row next to one another.
+    the gate may also have the shape of x, one factor for every element of y and of
+    y's type.  y and u are float32, bfloat16 or float16, x the same or float32;
+    parameters have any of the three.  Rows may lie at any stride, the columns of a
+    row next to one another.
 
     Without y only the norm is taken: u = pre(x), of type u_dtype (default x's),
     and x_out is x -- the norm before the first block.  Arithmetic is float32,

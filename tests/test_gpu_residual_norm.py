@@ -605,3 +605,21 @@ def test_rows_shared_by_blocks_without_weights(pkg, dim, gate):
     for post, pre in (("layer", "rms"), ("layer", "layer"), ("rms", "layer")):
         t, g, how = make((2, 40, dim), BF16, BF16, gate=gate, post=post, pre=pre)
         check(pkg, without(t, NAMES[3:]), g, how)
+
+
+@pytest.mark.parametrize("shape", [(5, 1, 128), (1, 1, 72), (3, 1, 1, 72), (2, 1, 1001)], ids=str)
+@pytest.mark.parametrize("pair", [(F32, BF16), (BF16, BF16), (F16, F16)], ids=str)
+def test_gate_of_each_sample_beside_one_token(pkg, shape, pair):
+    """A gate [samples, 1, dim] has a type of its own however many tokens there are,
+    and may be a chunk of something wider."""
+    for tokens in (1, 2):
+        wide = (shape[0], tokens, *shape[2:])
+        t, g, how = make(wide, *pair, pre="layer")
+        mod = torch.randn(*shape[:-1], 3 * shape[-1], device="cuda")
+        t["gate"] = mod[..., shape[-1]:2 * shape[-1]]
+        check(pkg, t, g, how)
+    leaves = {k: v.detach().clone().requires_grad_() for k, v in t.items()}
+    x_out, u = pkg.fused_residual_norm(leaves["x"], leaves["y"],
+                                       **{k: leaves[k] for k in NAMES[2:]}, **how)
+    torch.autograd.backward((x_out, u), (g["x"], g["u"]))
+    assert leaves["gate"].grad.shape == shape and leaves["gate"].grad.dtype == F32
