@@ -90,9 +90,9 @@ def grad_norm(grads, norm_type=2.0) -> torch.Tensor:
     with _memory.on_device(ts.device):
         out = torch.empty((), dtype=torch.float32, device=ts.tensors[0].device)
         stream = _memory.stream_of(ts.device)
-        ws = _memory.zeroed_scratch(out.device, stream, lib.gbssim_grad_workspace_bytes(n))
-        st = lib.gbssim_grad_norm(_at(ts.addresses), _at(ts.counts), ts.codes, n, p,
-                                  out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+        with _memory.zeroed_scratch(out.device, stream, lib.gbssim_grad_workspace_bytes(n)) as ws:
+            st = lib.gbssim_grad_norm(_at(ts.addresses), _at(ts.counts), ts.codes, n, p,
+                                      out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
     _abi.check("gbssim_grad_norm", st)
     return out
 
@@ -128,10 +128,10 @@ def clip_grads(grads, max_norm: float, norm_type=2.0, out=None) -> torch.Tensor:
     with _memory.on_device(ts.device):
         norm = torch.empty((), dtype=torch.float32, device=ts.tensors[0].device)
         stream = _memory.stream_of(ts.device)
-        ws = _memory.zeroed_scratch(norm.device, stream, lib.gbssim_grad_workspace_bytes(n))
-        st = lib.gbssim_grad_clip(_at(ts.addresses), _at(outs.addresses), _at(ts.counts), ts.codes,
-                                  outs.codes, n, p, limit, norm.data_ptr(), ws.data_ptr(),
-                                  ws.numel(), stream)
+        with _memory.zeroed_scratch(norm.device, stream, lib.gbssim_grad_workspace_bytes(n)) as ws:
+            st = lib.gbssim_grad_clip(_at(ts.addresses), _at(outs.addresses), _at(ts.counts),
+                                      ts.codes, outs.codes, n, p, limit, norm.data_ptr(),
+                                      ws.data_ptr(), ws.numel(), stream)
     _abi.check("gbssim_grad_clip", st)
     torch.autograd.graph.increment_version(outs.tensors)
     return norm

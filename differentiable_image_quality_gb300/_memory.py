@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import contextlib
+import threading
 
 import torch
 
@@ -26,16 +27,51 @@ def empty_like(t: torch.Tensor) -> torch.Tensor:
         torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def zeroed_scratch(device: torch.device, stream: int, nbytes: int) -> torch.Tensor:
-    """Scratch for calls on one stream of one device, zero-filled before its
-    first use; every call leaves its completion counter zero, and the calls of
-    a stream run one after another, so they share one buffer.  A call that is
-    being captured into a graph gets a buffer of its own, whose zero fill is
-    part of the graph: a replay then depends on no buffer of later calls."""
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    buf = _scratch.get((device.index, stream))
-    if buf is None or buf.numel() < nbytes:
-        buf = torch.zeros(max(nbytes, 1 << 16), dtype=torch.uint8, device=device)
-        _scratch[(device.index, stream)] = buf
-    return buf
+class _Scratch:
+    """The buffer of a stream, and the lock of the call that uses it."""
+
+    __slots__ = ("lock", "buffer")
+
+    def __init__(self):
+        self.lock = threading.RLock()  # a finalizer may make a call within a call
+        self.buffer = None
+
+
+class zeroed_scratch:
+    """Scratch for one call of the library on a stream: ``with`` gives a buffer that is
+    zero-filled before its first use, and is the call's alone until the block ends.
+
+    Every call leaves its completion counter zero, and what calls put on a stream
+    runs one after another, so a stream's calls share one buffer.  The lock keeps
+    the launches of a call together: another host thread's on the same stream
+    would otherwise come between them, and leave its own results in the buffer.  A
+    call that is being captured into a graph gets a buffer of its own, whose zero
+    fill is part of the graph: a replay then depends on no buffer of later calls."""
+
+    __slots__ = ("device", "stream", "nbytes", "scratch")
+
+    def __init__(self, device: torch.device, stream: int, nbytes: int):
+        self.device, self.stream, self.nbytes, self.scratch = device, stream, nbytes, None
+
+    def __enter__(self) -> torch.Tensor:
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(self.nbytes, dtype=torch.uint8, device=self.device)
+        key = (self.device.index, self.stream)
+        scratch = _scratch.get(key)
+        if scratch is None:
+            scratch = _scratch.setdefault(key, _Scratch())
+        scratch.lock.acquire()
+        self.scratch = scratch
+        try:
+            buffer = scratch.buffer
+            if buffer is None or buffer.numel() < self.nbytes:
+                buffer = scratch.buffer = torch.zeros(max(self.nbytes, 1 << 16), dtype=torch.uint8,
+                                                      device=self.device)
+        except BaseException:
+            scratch.lock.release()
+            raise
+        return buffer
+
+    def __exit__(self, *error) -> None:
+        if self.scratch is not None:
+            self.scratch.lock.release()

@@ -264,7 +264,9 @@ typedef enum { GBSSIM_F32 = 0, GBSSIM_BF16 = 1, GBSSIM_F16 = 2 } gbssim_dtype;
 typedef enum { GBSSIM_NORM_INF = 0, GBSSIM_NORM_1 = 1, GBSSIM_NORM_2 = 2 } gbssim_norm_type;
 
 /* Workspace bytes for n tensors.  Same zero-fill rule as gbssim_workspace_bytes;
- * 16-byte aligned. */
+ * 16-byte aligned.  A call's launches leave partial sums and c for one another in
+ * it: calls that host threads make at the same time must not share one, not even
+ * on one stream. */
 size_t gbssim_grad_workspace_bytes(int n);
 
 /* grads, counts, dtypes: HOST arrays of n device addresses, element counts and
@@ -352,7 +354,8 @@ typedef struct {
 } gbssim_residual_norm_grads;
 
 /* Workspace bytes of the backward (0 without rows, or for an invalid description);
- * 16-byte aligned, contents arbitrary. */
+ * 16-byte aligned, contents arbitrary.  As for gbssim_grad_workspace_bytes, calls
+ * made at the same time must not share one, not even on one stream. */
 size_t gbssim_residual_norm_workspace_bytes(const gbssim_residual_norm *desc);
 
 /* Backward from the gradients of x' (res_dtype) and u (blk_dtype); either may be NULL

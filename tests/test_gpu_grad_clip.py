@@ -8,6 +8,7 @@ output's type: half an ulp, 2^-24 float32, 2^-8 bfloat16, 2^-11 float16 (and
 2^-25 where float16 is subnormal).
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -231,3 +232,41 @@ def test_in_a_graph(pkg):
         ref = norm64(new)
         check_norm(norm, ref)
         check_scaled(outs, new, 0.5, ref)
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_two_threads_on_one_stream(pkg, many):
+    """Calls of two host threads on the stream that both have by default: each
+    scales by its own norm."""
+    sizes = [301] * 1100 if many else [40000, 17]
+    lists = [make(sizes, [F32, BF16], seed=s, scale=10.0**-s) for s in (0, 3)]
+    rounds = 40 if many else 400
+    want = []
+    for ts in lists:
+        outs = [torch.empty_like(t) for t in ts]
+        want.append((pkg.clip_grads(ts, 1e-4, out=outs), torch.cat([o.float() for o in outs])))
+    flat = [torch.empty((rounds, sum(sizes)), device="cuda") for _ in lists]
+    got, errors = [None, None], []
+    torch.cuda.synchronize()
+    start = threading.Barrier(2)
+
+    def work(k):
+        try:
+            start.wait(30)
+            got[k] = [pkg.clip_grads(lists[k], 1e-4, out=list(row.split(sizes))) for row in flat[k]]
+        except Exception as e:  # noqa: BLE001 - reported below
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for k, (norm, out) in enumerate(want):
+        assert all(torch.equal(n, norm) for n in got[k])
+        coef = min(1.0, 1e-4 / (float(norm) + 1e-6))
+        whole = torch.cat([t.float() for t in lists[k]]).double() * coef
+        err = (flat[k].double() - whole).abs().amax(0)
+        assert bool((err <= whole.abs() * (2.0**-24 + 2.5e-6) + 2.0**-149).all())

@@ -1,7 +1,10 @@
 """Host-side checks of the gradient norm and clipping: every refusal comes back
 before any CUDA call."""
+import contextlib
 import ctypes
 import math
+import threading
+import time
 
 import pytest
 import torch
@@ -107,3 +110,59 @@ def test_parameters_without_gradients():
     p = torch.nn.Parameter(torch.zeros(3))
     assert float(pkg.clip_grad_norm_([p], 1.0)) == 0.0
     assert float(pkg.clip_grad_norm_(p, 1.0)) == 0.0
+
+
+def test_threads_on_one_stream_share_no_workspace(monkeypatch):
+    """A call of several launches keeps its workspace to itself until it returns, also
+    against another host thread on its stream (a stand-in for the library here)."""
+    from differentiable_image_quality_gb300 import _abi, _grad_clip, _memory
+
+    class Library:
+        def __init__(self):
+            self.inside, self.shared, self.calls, self.lock = [], False, 0, threading.Lock()
+
+        def gbssim_grad_workspace_bytes(self, n):
+            return 1024
+
+        def call(self, workspace):
+            with self.lock:
+                self.shared = self.shared or workspace in self.inside
+                self.inside.append(workspace)
+                self.calls += 1
+            time.sleep(0.05)
+            with self.lock:
+                self.inside.remove(workspace)
+            return 0
+
+        def gbssim_grad_norm(self, *a):
+            return self.call(a[6])
+
+        def gbssim_grad_clip(self, *a):
+            return self.call(a[9])
+
+    lib = Library()
+    monkeypatch.setattr(_abi, "load", lambda: lib)
+    monkeypatch.setattr(_grad_clip, "_get_device", lambda t: 0)
+    monkeypatch.setattr(_memory, "on_device", lambda index: contextlib.nullcontext())
+    monkeypatch.setattr(_memory, "stream_of", lambda index: 11)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    _grad_clip.grad_norm([torch.zeros(3)])  # the stream's workspace is there
+    start, errors = threading.Barrier(4), []
+
+    def work(k):
+        try:
+            start.wait(30)
+            if k % 2:
+                _grad_clip.grad_norm([torch.zeros(3)])
+            else:
+                _grad_clip.clip_grads([torch.zeros(3)], 1.0)
+        except Exception as e:  # noqa: BLE001 - reported below
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors, errors
+    assert lib.calls == 5 and not lib.shared
