@@ -49,9 +49,11 @@ without autograd.  These take float32, bfloat16 and float16.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
-from . import _abi
+from . import _abi, _memory
 from ._abi import SAME, VALID, GbssimError
 from ._grad_clip import clip_grad_norm_, clip_grads, grad_norm
 from ._residual_norm import fused_residual_norm, residual_norm_bwd, residual_norm_fwd
@@ -135,21 +137,15 @@ def saved_bytes(shape, want_grad2: bool) -> int:
 _ws_cache: dict = {}
 
 
-def _workspace(device: torch.device, nbytes: int) -> torch.Tensor:
-    """A zero-filled scratch buffer per (device, current stream), grown on
-    demand (256-byte aligned, as the caching allocator returns).  The library
-    leaves its counter zero after every completed call, and calls on one stream
-    run one after another, so a stream's calls can share its buffer; calls on
-    different streams get different buffers and may run at the same time."""
-    stream = torch.cuda.current_stream(device)
-    key = (device.type, device.index, stream.cuda_stream)
-    buf = _ws_cache.get(key)
-    if buf is None or buf.numel() < nbytes:
-        # allocated on the stream that will use it: the caching allocator orders
-        # its zero-fill before that stream's later work
-        buf = torch.zeros(max(nbytes, 4096), dtype=torch.uint8, device=device)
-        _ws_cache[key] = buf
-    return buf
+def _workspace(given, device: torch.device, nbytes: int):
+    """The workspace of a call as a context: the given one, or the scratch of the current
+    stream, which is this call's alone until it has made its launches (256-byte
+    aligned, as the caching allocator returns).  Calls on different streams get
+    different buffers and may run at the same time."""
+    if given is not None:
+        return contextlib.nullcontext(given)
+    stream = torch.cuda.current_stream(device).cuda_stream
+    return _memory.stream_scratch(_ws_cache, device, stream, nbytes, 4096)
 
 
 # ----------------------------------------------------------------- thin wrappers
@@ -161,13 +157,12 @@ def ssim_fwd(img1, img2, padding, out_mean, out_map=None, saved=None, want_grad2
     pad = _pad(padding)
     lib = _abi.load()
     need = int(lib.gbssim_workspace_bytes(N, C, H, W, pad))
-    if workspace is None:
-        workspace = _workspace(img1.device, need)
-    st = lib.ssim_fwd(_abi.ptr(img1), _abi.ptr(img2), N, C, H, W, pad, _abi.ptr(out_mean),
-                      _abi.ptr(out_map), _abi.ptr(saved),
-                      0 if saved is None else saved.numel() * saved.element_size(),
-                      int(bool(want_grad2)), _abi.ptr(workspace),
-                      workspace.numel() * workspace.element_size(), _stream(img1))
+    with _workspace(workspace, img1.device, need) as ws:
+        st = lib.ssim_fwd(_abi.ptr(img1), _abi.ptr(img2), N, C, H, W, pad, _abi.ptr(out_mean),
+                          _abi.ptr(out_map), _abi.ptr(saved),
+                          0 if saved is None else saved.numel() * saved.element_size(),
+                          int(bool(want_grad2)), _abi.ptr(ws),
+                          ws.numel() * ws.element_size(), _stream(img1))
     _abi.check("ssim_fwd", st)
 
 
@@ -188,13 +183,12 @@ def ssim3d_fwd(img1, img2, padding, out_mean, out_map=None, saved=None, want_gra
     pad = _pad(padding)
     lib = _abi.load()
     need = int(lib.gbssim3d_workspace_bytes(N, C, D, H, W, pad))
-    if workspace is None:
-        workspace = _workspace(img1.device, need)
-    st = lib.ssim3d_fwd(_abi.ptr(img1), _abi.ptr(img2), N, C, D, H, W, pad, _abi.ptr(out_mean),
-                        _abi.ptr(out_map), _abi.ptr(saved),
-                        0 if saved is None else saved.numel() * saved.element_size(),
-                        int(bool(want_grad2)), _abi.ptr(workspace),
-                        workspace.numel() * workspace.element_size(), _stream(img1))
+    with _workspace(workspace, img1.device, need) as ws:
+        st = lib.ssim3d_fwd(_abi.ptr(img1), _abi.ptr(img2), N, C, D, H, W, pad, _abi.ptr(out_mean),
+                            _abi.ptr(out_map), _abi.ptr(saved),
+                            0 if saved is None else saved.numel() * saved.element_size(),
+                            int(bool(want_grad2)), _abi.ptr(ws),
+                            ws.numel() * ws.element_size(), _stream(img1))
     _abi.check("ssim3d_fwd", st)
 
 
@@ -203,14 +197,17 @@ def ssim3d_bwd(dL, img1, img2, padding, grad1, grad2=None, saved=None, workspace
     N, C, D, H, W = img1.shape
     pad = _pad(padding)
     lib = _abi.load()
-    if saved is None and workspace is None:
-        workspace = _workspace(img1.device, int(lib.gbssim3d_workspace_bytes(N, C, D, H, W, pad)))
-    st = lib.ssim3d_bwd(_abi.ptr(dL), _abi.ptr(img1), _abi.ptr(img2), N, C, D, H, W, pad,
-                        _abi.ptr(saved),
-                        0 if saved is None else saved.numel() * saved.element_size(),
-                        _abi.ptr(grad1), _abi.ptr(grad2), _abi.ptr(workspace),
-                        0 if workspace is None else workspace.numel() * workspace.element_size(),
-                        _stream(img1))
+    if saved is not None:  # a scaling pass: no workspace needed
+        held = contextlib.nullcontext(workspace)
+    else:
+        held = _workspace(workspace, img1.device,
+                          int(lib.gbssim3d_workspace_bytes(N, C, D, H, W, pad)))
+    with held as ws:
+        st = lib.ssim3d_bwd(_abi.ptr(dL), _abi.ptr(img1), _abi.ptr(img2), N, C, D, H, W, pad,
+                            _abi.ptr(saved),
+                            0 if saved is None else saved.numel() * saved.element_size(),
+                            _abi.ptr(grad1), _abi.ptr(grad2), _abi.ptr(ws),
+                            0 if ws is None else ws.numel() * ws.element_size(), _stream(img1))
     _abi.check("ssim3d_bwd", st)
 
 
@@ -221,12 +218,12 @@ def ssim_fwd_bwd(img1, img2, padding, dL, out_mean, grad1, grad2=None, out_map=N
     N, C, H, W = img1.shape
     pad = _pad(padding)
     lib = _abi.load()
-    if workspace is None:
-        workspace = _workspace(img1.device, int(lib.gbssim_workspace_bytes(N, C, H, W, pad)))
-    st = lib.ssim_fwd_bwd(_abi.ptr(img1), _abi.ptr(img2), N, C, H, W, pad, _abi.ptr(dL),
-                          _abi.ptr(out_mean), _abi.ptr(out_map), _abi.ptr(grad1), _abi.ptr(grad2),
-                          _abi.ptr(workspace), workspace.numel() * workspace.element_size(),
-                          _stream(img1))
+    need = int(lib.gbssim_workspace_bytes(N, C, H, W, pad))
+    with _workspace(workspace, img1.device, need) as ws:
+        st = lib.ssim_fwd_bwd(_abi.ptr(img1), _abi.ptr(img2), N, C, H, W, pad, _abi.ptr(dL),
+                              _abi.ptr(out_mean), _abi.ptr(out_map), _abi.ptr(grad1),
+                              _abi.ptr(grad2), _abi.ptr(ws), ws.numel() * ws.element_size(),
+                              _stream(img1))
     _abi.check("ssim_fwd_bwd", st)
 
 
@@ -237,13 +234,12 @@ def ssim3d_fwd_bwd(img1, img2, padding, dL, out_mean, grad1, grad2=None, out_map
     N, C, D, H, W = img1.shape
     pad = _pad(padding)
     lib = _abi.load()
-    if workspace is None:
-        workspace = _workspace(img1.device,
-                               int(lib.gbssim3d_workspace_bytes(N, C, D, H, W, pad)))
-    st = lib.ssim3d_fwd_bwd(_abi.ptr(img1), _abi.ptr(img2), N, C, D, H, W, pad, _abi.ptr(dL),
-                            _abi.ptr(out_mean), _abi.ptr(out_map), _abi.ptr(grad1),
-                            _abi.ptr(grad2), _abi.ptr(workspace),
-                            workspace.numel() * workspace.element_size(), _stream(img1))
+    need = int(lib.gbssim3d_workspace_bytes(N, C, D, H, W, pad))
+    with _workspace(workspace, img1.device, need) as ws:
+        st = lib.ssim3d_fwd_bwd(_abi.ptr(img1), _abi.ptr(img2), N, C, D, H, W, pad, _abi.ptr(dL),
+                                _abi.ptr(out_mean), _abi.ptr(out_map), _abi.ptr(grad1),
+                                _abi.ptr(grad2), _abi.ptr(ws), ws.numel() * ws.element_size(),
+                                _stream(img1))
     _abi.check("ssim3d_fwd_bwd", st)
 
 
@@ -272,8 +268,6 @@ def ssim_pyramid(img1, img2, padding, octaves: int, want_maps: bool = False, out
     if need == 0:
         raise ValueError(f"invalid shape {tuple(img1.shape)} for {octaves} octaves "
                          f"with padding {padding!r}")
-    if workspace is None:
-        workspace = _workspace(img1.device, need)
     if out_means is None:
         out_means = torch.empty((int(octaves), 3, N), dtype=torch.float32, device=img1.device)
     nf = int(lib.gbssim_pyramid_map_floats(N, C, H, W, pad, int(octaves)))
@@ -285,9 +279,10 @@ def ssim_pyramid(img1, img2, padding, octaves: int, want_maps: bool = False, out
                          f"on {img1.device}")
     if out_means.shape != (int(octaves), 3, N) or out_means.dtype != torch.float32:
         raise ValueError(f"out_means must be a float32 tensor of shape ({int(octaves)}, 3, {N})")
-    st = lib.ssim_pyramid(_abi.ptr(img1), _abi.ptr(img2), N, C, H, W, pad, int(octaves),
-                          _abi.ptr(out_means), _abi.ptr(maps), _abi.ptr(workspace),
-                          workspace.numel() * workspace.element_size(), _stream(img1))
+    with _workspace(workspace, img1.device, need) as ws:
+        st = lib.ssim_pyramid(_abi.ptr(img1), _abi.ptr(img2), N, C, H, W, pad, int(octaves),
+                              _abi.ptr(out_means), _abi.ptr(maps), _abi.ptr(ws),
+                              ws.numel() * ws.element_size(), _stream(img1))
     _abi.check("ssim_pyramid", st)
     views = None
     if maps is not None:

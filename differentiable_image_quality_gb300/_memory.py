@@ -27,51 +27,58 @@ def empty_like(t: torch.Tensor) -> torch.Tensor:
         torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-class _Scratch:
-    """The buffer of a stream, and the lock of the call that uses it."""
+class _Buffer:
+    """The scratch of a stream, and the lock of the call that uses it."""
 
-    __slots__ = ("lock", "buffer")
+    __slots__ = ("lock", "tensor")
 
     def __init__(self):
         self.lock = threading.RLock()  # a finalizer may make a call within a call
-        self.buffer = None
+        self.tensor = None
 
 
-class zeroed_scratch:
-    """Scratch for one call of the library on a stream: ``with`` gives a buffer that is
-    zero-filled before its first use, and is the call's alone until the block ends.
+class stream_scratch:
+    """``with`` gives the scratch that the calls on a stream share (one of ``buffers``),
+    zero-filled before its first use, grown on demand; it is one call's alone until
+    the block ends.
 
     Every call leaves its completion counter zero, and what calls put on a stream
-    runs one after another, so a stream's calls share one buffer.  The lock keeps
-    the launches of a call together: another host thread's on the same stream
-    would otherwise come between them, and leave its own results in the buffer.  A
-    call that is being captured into a graph gets a buffer of its own, whose zero
-    fill is part of the graph: a replay then depends on no buffer of later calls."""
+    runs one after another, so one buffer serves them all.  The lock keeps the
+    launches of a call together: another host thread's on the same stream would
+    otherwise come between them, and leave its own results in the buffer."""
 
-    __slots__ = ("device", "stream", "nbytes", "scratch")
+    __slots__ = ("buffers", "device", "stream", "nbytes", "least", "held")
 
-    def __init__(self, device: torch.device, stream: int, nbytes: int):
-        self.device, self.stream, self.nbytes, self.scratch = device, stream, nbytes, None
+    def __init__(self, buffers: dict, device: torch.device, stream: int, nbytes: int, least: int):
+        self.buffers, self.device, self.stream = buffers, device, stream
+        self.nbytes, self.least = nbytes, least
 
     def __enter__(self) -> torch.Tensor:
-        if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(self.nbytes, dtype=torch.uint8, device=self.device)
         key = (self.device.index, self.stream)
-        scratch = _scratch.get(key)
-        if scratch is None:
-            scratch = _scratch.setdefault(key, _Scratch())
-        scratch.lock.acquire()
-        self.scratch = scratch
+        held = self.buffers.get(key)
+        if held is None:
+            held = self.buffers.setdefault(key, _Buffer())
+        held.lock.acquire()
+        self.held = held
         try:
-            buffer = scratch.buffer
-            if buffer is None or buffer.numel() < self.nbytes:
-                buffer = scratch.buffer = torch.zeros(max(self.nbytes, 1 << 16), dtype=torch.uint8,
-                                                      device=self.device)
+            if held.tensor is None or held.tensor.numel() < self.nbytes:
+                # allocated on the stream that will use it: the caching allocator orders
+                # its zero fill before that stream's later work
+                held.tensor = torch.zeros(max(self.nbytes, self.least), dtype=torch.uint8,
+                                          device=self.device)
         except BaseException:
-            scratch.lock.release()
+            held.lock.release()
             raise
-        return buffer
+        return held.tensor
 
     def __exit__(self, *error) -> None:
-        if self.scratch is not None:
-            self.scratch.lock.release()
+        self.held.lock.release()
+
+
+def zeroed_scratch(device: torch.device, stream: int, nbytes: int):
+    """The stream's scratch for one call, as a context.  A call that is being captured
+    into a graph gets a buffer of its own, whose zero fill is part of the graph: a
+    replay then depends on no buffer of later calls."""
+    if torch.cuda.is_current_stream_capturing():
+        return contextlib.nullcontext(torch.zeros(nbytes, dtype=torch.uint8, device=device))
+    return stream_scratch(_scratch, device, stream, nbytes, 1 << 16)
