@@ -177,6 +177,7 @@ def residual_norm_fwd(x, y=None, gate=None, *, post_norm=None, post_weight=None,
         _check("x_out", x_out, index)
         if x_out.shape != x.shape or x_out.dtype != x.dtype or not x_out.is_contiguous():
             raise ValueError("x_out must be contiguous and have the shape and type of x")
+    given = x_out is not None
     with _memory.on_device(index):
         if x_out is None and y is not None:
             x_out = _memory.empty_like(x)
@@ -193,8 +194,9 @@ def residual_norm_fwd(x, y=None, gate=None, *, post_norm=None, post_weight=None,
     _abi.check("gbssim_residual_norm_fwd", st)
     if y is None:
         return x, u, stats
-    if x_out is x:
-        torch.autograd.graph.increment_version(x)
+    # a view or a buffer counts as written, like x itself (inference tensors count nothing)
+    if given and not x_out.is_inference():
+        torch.autograd.graph.increment_version(x_out)
     return x_out, u, stats
 
 

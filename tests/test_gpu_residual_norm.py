@@ -623,3 +623,21 @@ def test_gate_of_each_sample_beside_one_token(pkg, shape, pair):
                                        **{k: leaves[k] for k in NAMES[2:]}, **how)
     torch.autograd.backward((x_out, u), (g["x"], g["u"]))
     assert leaves["gate"].grad.shape == shape and leaves["gate"].grad.dtype == F32
+
+
+def test_given_output_counts_as_written(pkg):
+    """Autograd refuses a backward through what an output has overwritten."""
+    t, g, how = make((2, 9, 72))
+    args = {k: t[k] for k in NAMES[2:]}
+    for x_out in (torch.empty_like(t["x"]), t["x"].clone().view(18, 72).view(2, 9, 72)):
+        version = x_out._version
+        pkg.residual_norm_fwd(t["x"], t["y"], x_out=x_out, **args, **how)
+        assert x_out._version > version
+    x, w = t["x"].clone(), torch.ones(72, device="cuda", requires_grad=True)
+    saved = (x * w).sum()
+    pkg.residual_norm_fwd(x, t["y"], x_out=x.view(x.shape), **args, **how)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        saved.backward()
+    with torch.inference_mode():
+        buffer = torch.empty_like(x)
+    pkg.residual_norm_fwd(x, t["y"], x_out=buffer, **args, **how)
