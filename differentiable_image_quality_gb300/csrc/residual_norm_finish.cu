@@ -332,6 +332,7 @@ cudaError_t residual_norm_bwd_launch(const ResidualNormArgs &a, int res, int blk
     // 8 x 600 x 1024 29, 25, 26.
     constexpr int kLongGrid = 304, kFewPartials = 160;
     const int shared_part = own ? a.plan.groups : 0, parts = shared_part + (shared ? 1 : 0);
+    if (parts == 0) return cudaSuccess;  // no samples: their own gradients are empty
     const int most_groups = shared && factors_vary(a) ? a.plan.groups : 0;
     if (parts * up(a.dim, kFinishCols) <= kLongGrid || most_groups > 32)
         return launch_next(residual_norm_finish_kernel<kFinishCols, kFinishLanes>,

@@ -641,3 +641,28 @@ def test_given_output_counts_as_written(pkg):
     with torch.inference_mode():
         buffer = torch.empty_like(x)
     pkg.residual_norm_fwd(x, t["y"], x_out=buffer, **args, **how)
+
+
+def test_no_samples_by_the_c_interface(pkg):
+    """Without samples, gradients that samples have of their own are empty, wherever
+    they were to be written: nothing to do, and shared ones are zero."""
+    from differentiable_image_quality_gb300 import _abi, _residual_norm as rn
+
+    lib = _abi.load()
+    own = torch.ones(64, device="cuda")
+    shared = torch.ones(64, device="cuda")
+    out = [torch.full((64,), 7.0, device="cuda") for _ in range(2)]
+    none, at = (0, 0, 0), (shared.data_ptr(), 0, 64)
+    for tokens in (0, 5):
+        for wants_shared in (False, True):
+            desc = rn._DESC.pack(0, tokens, 64, 0, 0, 1, 1, 1.0, 0.0, 1e-6, *at, *at, *none,
+                                 0, 0, 0, 0, own.data_ptr(), 0, 1, 64, 0, 0, 0, 0,
+                                 shared.data_ptr(), 0, 0, 0, 0, 0, 0, 0)
+            grads = rn._GRADS.pack(0, 0, 0, out[0].data_ptr(), 0,
+                                   out[1].data_ptr() if wants_shared else 0, 0)
+            st = lib.gbssim_residual_norm_bwd(desc, None, None, None, grads, None, 0,
+                                              torch.cuda.current_stream().cuda_stream)
+            assert st == 0, (tokens, wants_shared)
+            torch.cuda.synchronize()
+            assert bool((out[0] == 7.0).all())
+    assert bool((out[1] == 0.0).all())
