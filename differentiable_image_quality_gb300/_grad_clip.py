@@ -106,7 +106,8 @@ def clip_grads(grads, max_norm: float, norm_type=2.0, out=None) -> torch.Tensor:
     gradients, say); the gradients then stay as they are.  grads and norm_type
     are those of grad_norm.  A norm that is not finite is returned, not raised
     (raising would need a copy to the host): NaN makes every gradient NaN,
-    infinity makes the finite ones 0."""
+    infinity makes the finite ones 0, unless max_norm is infinite, which scales
+    nothing."""
     p = _norm_type(norm_type)
     limit = float(max_norm)
     if not limit >= 0.0:

@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(kThreads)
         *t.norm = norm;
         if (t.coef) {
             const float c = t.max_norm / (norm + kClipEps);
-            *t.coef = c > 1.0f ? 1.0f : c;  // a NaN stays
+            // no limit, no clipping, also where that is inf / inf; a norm's NaN stays
+            *t.coef = c > 1.0f || (isinf(t.max_norm) && !isnan(norm)) ? 1.0f : c;
         }
         *t.counter = 0u;
     }

@@ -257,8 +257,9 @@ int ssim3d_fwd_bwd(const float *img1, const float *img2, int N, int C, int D, in
  * that in double; values whose squares leave float32's range are summed in
  * double throughout.  g * c is formed in float32 and rounded once.  A NaN
  * anywhere makes norm and c NaN; an infinity makes norm infinite and c zero
- * (so finite gradients become 0, infinite ones NaN): the caller decides, from
- * the norm, whether to skip the step. */
+ * (so finite gradients become 0, infinite ones NaN), or 1 where max_norm is
+ * infinite too (no limit, nothing is scaled): the caller decides, from the norm,
+ * whether to skip the step. */
 
 typedef enum { GBSSIM_F32 = 0, GBSSIM_BF16 = 1, GBSSIM_F16 = 2 } gbssim_dtype;
 typedef enum { GBSSIM_NORM_INF = 0, GBSSIM_NORM_1 = 1, GBSSIM_NORM_2 = 2 } gbssim_norm_type;

@@ -270,3 +270,17 @@ def test_two_threads_on_one_stream(pkg, many):
         whole = torch.cat([t.float() for t in lists[k]]).double() * coef
         err = (flat[k].double() - whole).abs().amax(0)
         assert bool((err <= whole.abs() * (2.0**-24 + 2.5e-6) + 2.0**-149).all())
+
+
+@pytest.mark.parametrize("p", [2, 1, math.inf])
+def test_no_limit_and_infinity(pkg, p):
+    """An infinite limit clips nothing, an infinite norm included; a NaN stays one."""
+    for value in (math.inf, -math.inf, math.nan):
+        ts = make([5000, 100], [F32, F16])
+        ts[1][37] = value
+        before = [t.clone() for t in ts]
+        norm = float(pkg.clip_grads(ts, math.inf, p))
+        if math.isnan(value):
+            assert math.isnan(norm) and all(bool(x.isnan().all()) for x in ts)
+        else:
+            assert norm == math.inf and all(torch.equal(a, b) for a, b in zip(ts, before))
