@@ -31,6 +31,13 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
+def _same_order(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether dense tensors of one shape have their elements in one order: the strides
+    of dimensions of one element, or of no element at all, reach nothing."""
+    return a.numel() == 0 or all(s == t or n == 1
+                                 for s, t, n in zip(a.stride(), b.stride(), a.shape))
+
+
 _is_contiguous, _numel, _get_device, _data_ptr = (
     torch.Tensor.is_contiguous, torch.Tensor.numel, torch.Tensor.get_device, torch.Tensor.data_ptr)
 
@@ -122,7 +129,7 @@ def clip_grads(grads, max_norm: float, norm_type=2.0, out=None) -> torch.Tensor:
             raise ValueError("grads and out must be on one device")
         for g, o in zip(ts.tensors, outs.tensors):
             if o.shape != g.shape or (not (ts.contiguous and outs.contiguous)
-                                      and o.stride() != g.stride()):
+                                      and not _same_order(g, o)):
                 raise ValueError(f"out must have the gradients' shapes and strides: {tuple(o.shape)}"
                                  f" {o.stride()} for {tuple(g.shape)} {g.stride()}")
     lib = _abi.load()

@@ -284,3 +284,17 @@ def test_no_limit_and_infinity(pkg, p):
             assert math.isnan(norm) and all(bool(x.isnan().all()) for x in ts)
         else:
             assert norm == math.inf and all(torch.equal(a, b) for a, b in zip(ts, before))
+
+
+def test_strides_that_reach_no_element(pkg):
+    """Dimensions of one element may have any stride, beside tensors of any order."""
+    g = [torch.randn(4, 6, 5, 8, device="cuda").to(memory_format=torch.channels_last),
+         torch.randn(1, 5, device="cuda"), torch.randn(7, 1, 3, 1, device="cuda")]
+    outs = [torch.empty_like(g[0]), torch.empty(5, device="cuda").as_strided((1, 5), (1, 1)),
+            torch.empty(21, device="cuda").as_strided((7, 1, 3, 1), (3, 99, 1, 50))]
+    ref = norm64(g)
+    check_norm(pkg.clip_grads(g, 0.1, out=outs), ref)
+    check_scaled(outs, g, 0.1, ref)
+    other = torch.empty((4, 6, 5, 8), device="cuda")  # dense, in another order
+    with pytest.raises(ValueError):
+        pkg.clip_grads(g[:2], 1.0, out=[other, outs[1]])
