@@ -90,7 +90,7 @@ def _param(name: str, p, ndim, ext, index) -> tuple:
         if dim > 1 and p.stride(0) != 1:
             raise ValueError(f"{name} must be contiguous")
         return p.data_ptr(), code, 0, 0
-    if (ndim >= 3 and shape[0] == batch and shape[-1] == dim and len(shape) in (2, ndim)
+    if (ndim >= 3 and len(shape) in (2, ndim) and shape[0] == batch and shape[-1] == dim
             and p.numel() == batch * dim):
         if dim > 1 and p.stride(-1) != 1:
             raise ValueError(f"the last dimension of {name} must have stride 1")

@@ -666,3 +666,12 @@ def test_no_samples_by_the_c_interface(pkg):
             torch.cuda.synchronize()
             assert bool((out[0] == 7.0).all())
     assert bool((out[1] == 0.0).all())
+
+
+def test_parameter_without_dimensions(pkg):
+    t, g, how = make((2, 6, 64))
+    for name in NAMES[3:]:
+        with pytest.raises(ValueError, match=name):
+            pkg.fused_residual_norm(t["x"], t["y"], **{name: torch.ones((), device="cuda")})
+    with pytest.raises(ValueError, match="gate"):
+        pkg.fused_residual_norm(t["x"], t["y"], torch.ones((), device="cuda"))
