@@ -47,8 +47,8 @@ class Denoiser(torch.nn.Module):
             torch.nn.Linear(TOKENS, TOKENS) for _ in range(depth))
         self.up = torch.nn.ModuleList(torch.nn.Linear(dim, 2 * dim) for _ in range(depth))
         self.down = torch.nn.ModuleList(torch.nn.Linear(2 * dim, dim) for _ in range(depth))
-        self.post = torch.nn.ParameterList(
-            torch.nn.Parameter(torch.ones(dim)) for _ in range(2 * depth))
+        self.post = torch.nn.ParameterList(  # as differences from one, like the norms before
+            torch.nn.Parameter(torch.zeros(dim)) for _ in range(2 * depth))
         self.head = torch.nn.Linear(dim, PATCH_DIM)
         torch.nn.init.zeros_(self.head.weight)
         torch.nn.init.zeros_(self.head.bias)
