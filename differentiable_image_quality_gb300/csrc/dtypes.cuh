@@ -110,16 +110,6 @@ __device__ __forceinline__ Raw8<T> pack8(const float (&v)[8])
     return r;
 }
 
-// p: 16-byte aligned.
-template <typename T>
-__device__ __forceinline__ Raw8<T> ld8_stream(const T *p)
-{
-    Raw8<T> r;
-    r.w[0] = ld_stream16(p);
-    if constexpr (sizeof(T) == 4) r.w[1] = ld_stream16(p + 4);
-    return r;
-}
-
 template <typename T>
 __device__ __forceinline__ void st8(T *p, const Raw8<T> &r)
 {
