@@ -101,3 +101,49 @@ def test_fused_ssim_autograd_on_two_streams_at_once(oracle_mod):
         for got, ref in ((t1.grad, g1), (t2.grad, g2)):
             err = np.max(np.abs(got.cpu().numpy() - ref)) / np.max(np.abs(ref))
             assert err <= 1e-4, f"{shape} {padding}: gradient error {err:.2e}"
+
+
+def test_two_threads_on_one_stream():
+    """Volumes of two sizes from two host threads on the default stream, with the
+    wrappers' own scratch: three kernels a call, none between another call's."""
+    import torch
+
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import differentiable_image_quality_gb300 as pkg
+
+    pairs = [[torch.from_numpy(v).cuda() for v in uniform_pair(shape, 31 + k, std=0.08)]
+             for k, shape in enumerate([(1, 1, 20, 21, 22), (1, 2, 16, 40, 33)])]
+
+    def call(k, mean, grad):
+        dl = torch.ones(1, device="cuda")
+        pkg.ssim3d_fwd_bwd(*pairs[k], "same", dl, mean, grad)
+
+    rounds = 200
+    means = [torch.empty(rounds, device="cuda") for _ in pairs]
+    grads = [torch.empty((rounds, *p[0].shape), device="cuda") for p in pairs]
+    want = []
+    for k, p in enumerate(pairs):
+        mean, grad = torch.empty(1, device="cuda"), torch.empty_like(p[0])
+        call(k, mean, grad)
+        want.append((mean, grad))
+    torch.cuda.synchronize()
+    start, errors = threading.Barrier(2), []
+
+    def worker(k):
+        try:
+            start.wait(30)
+            for i in range(rounds):
+                call(k, means[k][i:i + 1], grads[k][i])
+        except Exception as e:  # noqa: BLE001 - reported below
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=worker, args=(k,)) for k in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for k, (mean, grad) in enumerate(want):
+        assert bool((means[k] == mean).all()) and bool((grads[k] == grad).all())
