@@ -20,7 +20,8 @@ train=False is the inference mode (and a later backward recomputes).  The
 choice is per call: a grad-enabled forward that no backward will follow (a
 validation loss under autograd) should pass train=False, which skips the
 gradient work the stored path does inside the forward.  Calls on different
-CUDA streams may run concurrently: each stream gets its own scratch buffer.
+CUDA streams may run concurrently: each stream gets its own scratch buffer; host
+threads that call on one stream take turns with its buffer.
 
 The thin wrappers ssim_fwd / ssim_bwd / ssim3d_fwd / ssim3d_bwd expose the C
 ABI calls one to one on torch tensors.

@@ -286,8 +286,8 @@ def fused_residual_norm(x, y=None, gate=None, *, post_norm=None, post_weight=Non
         u     = pre(x_out)                   (None with pre_norm=None)
 
     Returns (x_out, u).  A norm is "rms", v / sqrt(mean(v^2) + eps), or "layer",
-    which subtracts the mean first; then (weight + weight_offset) and bias apply,
-    each optional.  x, the residual stream, and y, the block's output, are CUDA
+    which subtracts the mean first; then (weight + weight_offset), one offset for both
+    norms, and bias apply, each optional.  x, the residual stream, and y, the block's output, are CUDA
     tensors of one shape [..., dim], dim up to 16384; with three or more
     dimensions the first counts samples.  Weights, biases and the gate are [dim],
     or [samples, dim] (conditioned norms and gates; [samples, 1, dim] as well);

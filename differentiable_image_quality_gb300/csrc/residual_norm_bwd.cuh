@@ -79,9 +79,9 @@ __device__ __forceinline__ void write_sum(const ResidualNormArgs &a, const Cols<
 }
 
 // FULL: a gate of its own per row.  NORMS: 0 neither subtracts a mean nor has a
-// bias, 1 they may but for a bias of the post norm, 2 they may.  ANY: whatever a call may ask for; without it all four inputs and both
-// outputs are there and one stride reaches every row.  CLUSTER: blocks may share
-// rows.
+// bias, 1 they may but for a bias of the post norm, 2 they may.  ANY: whatever a call
+// may ask for; without it all four inputs and both outputs are there and one stride
+// reaches every row.  CLUSTER: blocks may share rows.
 template <typename R, typename Y, bool ALIGNED, bool FULL, int NORMS, bool ANY, bool CLUSTER>
 __global__ void __launch_bounds__(NORMS == 0 && !FULL && !CLUSTER ? kBwdResidentPlain : kBwdThreads, 1)
     residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a)

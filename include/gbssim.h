@@ -297,7 +297,7 @@ int gbssim_grad_clip(const void *const *grads, void *const *outs, const long lon
  * with m the row's mean (LAYER; zero for RMS) and r = 1 / sqrt(mean((. - m)^2) +
  * eps); ROW_NONE leaves a norm out (m = 0, r = 1).  A missing weight is 1
  * (without o), a missing bias 0, a missing gate 1.  s is residual_scale, o is
- * weight_offset (1 for weights stored as a difference from one).
+ * weight_offset, of both norms (1 for weights stored as a difference from one).
  *
  * Types: x and x' are res_dtype; y, u and a gate of its own per row blk_dtype;
  * res_dtype is blk_dtype or float32.  Each parameter has its own type.
