@@ -54,6 +54,8 @@ SIGNATURES = {
     "gbssim_residual_norm_fwd": (_i, [_vp, _vp, _vp, _fp, _vp]),
     "gbssim_residual_norm_workspace_bytes": (_sz, [_vp]),
     "gbssim_residual_norm_bwd": (_i, [_vp, _vp, _vp, _fp, _vp, _vp, _sz, _vp]),
+    "gbssim_attention_workspace_bytes": (_sz, [_vp, _i]),
+    "gbssim_attention_fwd": (_i, [_vp, _vp, _fp, _vp, _sz, _vp]),
 }
 # exported only by the test build (libgbssim_test.so, csrc/gbssim_test_hooks.h):
 # forced row segments, the staging and exchange modes that drive the tests of the
@@ -63,6 +65,7 @@ TEST_SIGNATURES = {
     "gbssim_tune_staging": (None, [_i]),
     "gbssim_tune_fwd_split": (None, [_i]),
     "gbssim_tune_exchange": (None, [_i]),
+    "gbssim_tune_attention": (None, [_i]),
     "gbssim_test_stage_dump2d": (_i, [_fp, _fp, _i, _i, _i, _i, _i, _fp, _fp, _fp, _fp, _vp]),
 }
 

@@ -1,0 +1,135 @@
+"""Attention between the tokens of a batch: torch tensors to gbssim_attention_fwd
+and gbssim_attention_bwd."""
+from __future__ import annotations
+
+import struct
+
+import torch
+
+from . import _abi, _memory
+
+_MAX_DIM = 128
+
+# gbssim_attention
+_DESC = struct.Struct("@8if" + "Pqqq" * 3 + "PPP")
+_NO_TENSOR = (0, 0, 0, 0)
+
+
+def _check(name: str, t, index, dtype) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    if dtype is None:
+        if t.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    elif t.dtype != dtype:
+        raise TypeError(f"{name} must have the type of q, {dtype}, got {t.dtype}")
+
+
+def _as_read(t: torch.Tensor) -> torch.Tensor:
+    """t where the copy unit can read it in place, else a dense copy: heads side by side
+    in memory, strides and address multiples of 16 bytes, no element twice."""
+    shape, stride = t.shape, t.stride()
+    if t.numel() == 0 or (stride[-1] == 1 and t.data_ptr() % 16 == 0 and
+                          all(n == 1 or (s > 0 and s % 8 == 0)
+                              for n, s in zip(shape[:-1], stride[:-1]))):
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
+def _heads(t: torch.Tensor) -> tuple:
+    """(address, batch, token and head stride)."""
+    if t.numel() == 0:
+        return _NO_TENSOR
+    s = t.stride()
+    return t.data_ptr(), (s[0] if len(s) == 4 else 0), s[-3], s[-2]
+
+
+def _counts(name: str, t, index, n) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
+        raise TypeError(f"{name} must be an int32 CUDA tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be contiguous of shape "
+                         f"({'sequences + 1' if n is None else n},), got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _describe(q, k, v, causal, scale, kv_lengths, offsets, kv_offsets):
+    """(packed description, the tensors it points to, device index), all checked."""
+    _check("q", q, None, None)
+    index = q.get_device()
+    _check("k", k, index, q.dtype)
+    _check("v", v, index, q.dtype)
+    packed = offsets is not None
+    ndim = 3 if packed else 4
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != ndim:
+            raise ValueError(f"{name} must have {ndim} dimensions, "
+                             f"[{'' if packed else 'batch, '}tokens, heads, dim], "
+                             f"got {tuple(t.shape)}")
+    if k.shape != v.shape:
+        raise ValueError(f"k and v must have one shape, got {tuple(k.shape)} and {tuple(v.shape)}")
+    heads, dim = q.shape[-2:]
+    kv_heads = k.shape[-2]
+    if k.shape[-1] != dim or (not packed and k.shape[0] != q.shape[0]):
+        raise ValueError(f"q, k and v must agree in batch and dim, got {tuple(q.shape)} and "
+                         f"{tuple(k.shape)}")
+    if dim % 8 or not 8 <= dim <= _MAX_DIM:
+        raise ValueError(f"dim must be a multiple of 8 up to {_MAX_DIM}, got {dim}")
+    if kv_heads < 1 or heads < 1 or heads % kv_heads:
+        raise ValueError(f"the heads of q must be a multiple of k's, got {heads} and {kv_heads}")
+    scale = dim ** -0.5 if scale is None else float(scale)
+    if not 0.0 < scale < float("inf"):
+        raise ValueError(f"scale must be positive and finite, got {scale}")
+    lengths = q_off = k_off = 0
+    if packed:
+        if kv_lengths is not None:
+            raise ValueError("a packed batch has offsets, no kv_lengths")
+        q_off = _counts("offsets", offsets, index, None)
+        if offsets.shape[0] < 1:
+            raise ValueError("offsets must have at least one element")
+        if kv_offsets is None:
+            if k.shape[0] != q.shape[0]:
+                raise ValueError("without kv_offsets, k has the rows of q")
+            kv_offsets = offsets
+        k_off = _counts("kv_offsets", kv_offsets, index, offsets.shape[0])
+        sequences = offsets.shape[0] - 1
+    else:
+        if kv_offsets is not None:
+            raise ValueError("kv_offsets need offsets")
+        sequences = q.shape[0]
+        if kv_lengths is not None:
+            lengths = _counts("kv_lengths", kv_lengths, index, sequences)
+    q, k, v = _as_read(q), _as_read(k), _as_read(v)
+    desc = _DESC.pack(sequences, q.shape[-3], k.shape[-3], heads, kv_heads, dim,
+                      _abi.DTYPES[q.dtype], bool(causal), scale, *_heads(q), *_heads(k),
+                      *_heads(v), lengths, q_off, k_off)
+    return desc, (q, k, v), index
+
+
+def _stats_shape(q) -> tuple:
+    return (*q.shape[:-3], q.shape[-2], q.shape[-3])
+
+
+def attention_fwd(q, k, v, *, causal=False, scale=None, kv_lengths=None, offsets=None,
+                  kv_offsets=None, want_stats=False):
+    """The forward without autograd (fused_attention has the arguments).
+
+    Returns (out, lse): out dense, of q's shape and type; lse, with want_stats, the
+    logarithm of each row's sum of exponentials, float32 [batch, heads, tokens]
+    ([heads, rows] of a packed batch), which attention_bwd needs; else None."""
+    desc, kept, index = _describe(q, k, v, causal, scale, kv_lengths, offsets, kv_offsets)
+    lib = _abi.load()
+    with _memory.on_device(index):
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(_stats_shape(q), dtype=torch.float32, device=q.device) \
+            if want_stats else None
+        nbytes = lib.gbssim_attention_workspace_bytes(desc, 0)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+        st = lib.gbssim_attention_fwd(desc, out.data_ptr(), _abi.ptr(lse), _abi.ptr(ws), nbytes,
+                                      _memory.stream_of(index))
+    _abi.check("gbssim_attention_fwd", st)
+    return out, lse

@@ -1,0 +1,157 @@
+// What the attention kernels share: the shape of a call, where a block's queries
+// and keys lie, bounded waits.
+#pragma once
+
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "dtypes.cuh"
+#include "tensor_core.cuh"
+
+namespace gbssim {
+
+// Queries and keys come in tiles of 128 rows, the lanes of tensor memory.
+constexpr int kAttnTile = 128;
+constexpr int kAttnMaxDim = 128;
+
+struct AttnShape {
+    int sequences;           // samples, or sequences of a packed batch
+    int q_tokens, k_tokens;  // of a sample, or rows of the packed tensors
+    int heads, kv_heads, group, dim;
+    int causal, packed;
+    const int *kv_lengths, *q_offsets, *k_offsets;
+};
+
+// Where a block's queries and keys lie.
+struct AttnPlace {
+    int batch;          // outermost coordinate of the tensors
+    int q_row, k_row;   // of the sequence's first query and key
+    int queries, keys;  // of the sequence
+    int shift;          // causal: query i sees keys up to i + shift
+    int tile;           // which tile of the sequence
+    int tiles_before;   // of the sequences before it (packed)
+};
+
+// Offsets that do not ascend or leave the tensors are brought into range, so that
+// no row outside them is read or written whatever they hold.  Behind the last
+// sequence comes one more, of the rows that are left and without a partner: its
+// outputs are zeros.
+__device__ __forceinline__ void packed_span(const int *offsets, int sequences, int rows, int s,
+                                            int &first, int &count)
+{
+    first = s == 0 ? 0 : min(max(__ldg(offsets + s), 0), rows);
+    const int end = s >= sequences ? rows : min(max(__ldg(offsets + s + 1), first), rows);
+    count = end - first;
+}
+
+// The sequence and tile of `index`, tiles of `rows` rows of the queries or (BY_KEYS)
+// the keys, all of a sequence's before the next one's; false behind the last.  By
+// a whole warp.
+template <bool BY_KEYS>
+__device__ __forceinline__ bool find_place(const AttnShape &s, int index, int rows, AttnPlace &p)
+{
+    if (!s.packed) {
+        const int most = BY_KEYS ? s.k_tokens : s.q_tokens;
+        const int tiles = (most + rows - 1) / rows;
+        p.batch = index / tiles;
+        p.tile = index - p.batch * tiles;
+        p.tiles_before = p.batch * tiles;
+        p.q_row = p.k_row = 0;
+        p.queries = s.q_tokens;
+        p.keys = s.kv_lengths ? min(max(__ldg(s.kv_lengths + p.batch), 0), s.k_tokens) : s.k_tokens;
+        p.shift = s.k_tokens - s.q_tokens;
+        return p.batch < s.sequences;
+    }
+    const int lane = threadIdx.x % 32;
+    const int *offsets = BY_KEYS ? s.k_offsets : s.q_offsets;
+    const int total = BY_KEYS ? s.k_tokens : s.q_tokens;
+    int before = 0;
+    for (int base = 0; base <= s.sequences; base += 32) {
+        int first = 0, count = 0;
+        if (base + lane <= s.sequences) packed_span(offsets, s.sequences, total, base + lane, first, count);
+        const int tiles = (count + rows - 1) / rows;
+        int sum = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int up = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += up;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + sum > index);
+        if (past) {
+            const int l = __ffs(past) - 1, q = base + l;
+            p.tiles_before = before + __shfl_sync(0xffffffffu, sum - tiles, l);
+            p.tile = index - p.tiles_before;
+            p.batch = 0;
+            packed_span(s.q_offsets, s.sequences, s.q_tokens, q, p.q_row, p.queries);
+            packed_span(s.k_offsets, s.sequences, s.k_tokens, q, p.k_row, p.keys);
+            // the rows behind the last sequences have no partners
+            if (q == s.sequences) (BY_KEYS ? p.queries : p.keys) = 0;
+            p.shift = p.keys - p.queries;
+            return true;
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return false;
+}
+
+// Most tiles of `rows` rows that a call can have.
+inline long long most_tiles(const AttnShape &s, int tokens, int rows)
+{
+    if (s.packed) return (long long)tokens / rows + s.sequences + 1;
+    return (long long)s.sequences * ((tokens + rows - 1) / rows);
+}
+
+// Waits of at most about a second each.  A wait that runs out marks the block:
+// every other wait of the block then ends too, its roles leave their loops, and what
+// they have in flight is waited for before tensor memory is freed.
+constexpr long long kAttnWaitCycles = 2'000'000'000LL;
+constexpr long long kAttnDrainCycles = 500'000'000LL;
+
+__device__ __forceinline__ bool attn_wait_slow(uint64_t *bar, unsigned parity, volatile unsigned *failed)
+{
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*failed) return false;
+        if (clock64() - t0 > kAttnWaitCycles) {
+            *failed = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ bool attn_wait(uint64_t *bar, unsigned parity, volatile unsigned *failed)
+{
+    return mbar_try_wait(bar, parity) || attn_wait_slow(bar, parity, failed);
+}
+
+// By a whole warp, which then goes one way.
+__device__ __forceinline__ bool attn_wait_warp(uint64_t *bar, unsigned parity, volatile unsigned *failed)
+{
+    return __all_sync(0xffffffffu, attn_wait(bar, parity, failed));
+}
+
+// ------------------------------------------------------------------- forward
+
+struct AttnFwdArgs {
+    CUtensorMap q, k, v;
+    AttnShape s;
+    float scale_log2;
+    int tile_heads;   // heads of a tile: 1, or the group's where all its rows fit one tile
+    int tile_tokens;  // tokens of a tile
+    int splits;       // parts of the keys
+    int tiles;        // of q_tokens (batch form), or the most there can be (packed)
+    int ragged;       // keys may end before the tensor does
+    unsigned extra;   // test hook, see gbssim_tune_attention
+    void *out;
+    float *lse;       // or null
+    float *part_out, *part_lse;  // of each part, where there are several
+};
+
+cudaError_t attention_fwd_launch(const AttnFwdArgs &a, int dtype, int q_tiles, cudaStream_t stream);
+cudaError_t attention_fwd_status(unsigned *flags, bool clear);
+cudaError_t attention_join_launch(const AttnFwdArgs &a, int dtype, cudaStream_t stream);
+
+}  // namespace gbssim

@@ -1,0 +1,219 @@
+// Entry points of attention: argument checks and launch planning.
+#include <climits>
+#include <cmath>
+
+#include "api_host.cuh"
+#include "attention.cuh"
+#include "tensor_map.cuh"
+
+using namespace gbssim;
+
+namespace {
+
+struct Extent {
+    const void *p;
+    size_t bytes;
+};
+
+bool meet(const Extent &a, const Extent &b)
+{
+    return a.bytes && b.bytes && overlaps(a.p, a.bytes, b.p, b.bytes);
+}
+
+bool is_packed(const gbssim_attention &d) { return d.q_offsets != nullptr; }
+int samples(const gbssim_attention &d) { return is_packed(d) ? 1 : d.sequences; }
+
+long long q_rows(const gbssim_attention &d) { return (long long)samples(d) * d.q_tokens; }
+long long k_rows(const gbssim_attention &d) { return (long long)samples(d) * d.k_tokens; }
+
+Extent heads_extent(const gbssim_attention &d, const gbssim_heads &t, int tokens, int heads)
+{
+    const int n = samples(d);
+    if (!t.data || n == 0 || tokens == 0) return {nullptr, 0};
+    const long long last = (n - 1) * t.batch_stride + (tokens - 1) * t.token_stride +
+                           (heads - 1) * t.head_stride + d.dim;
+    return {t.data, size_t(last) * 2};
+}
+
+Extent dense_extent(const gbssim_attention &d, const void *p, long long rows, int heads)
+{
+    return {p, p ? size_t(rows) * heads * d.dim * 2 : 0};
+}
+
+Extent floats(const gbssim_attention &d, const float *p)
+{
+    return {p, p ? size_t(q_rows(d)) * d.heads * 4 : 0};
+}
+
+bool multiple16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Strides of extents above one: positive multiples of 16 bytes, below 2^40 bytes.
+int check_stride(long long stride, int extent)
+{
+    if (extent < 2) return GBSSIM_OK;
+    if (stride < 1) return GBSSIM_EINVAL;
+    if (stride >= (1LL << 39)) return GBSSIM_ESHAPE;
+    return stride % 8 ? GBSSIM_EALIGN : GBSSIM_OK;
+}
+
+int check_heads(const gbssim_attention &d, const gbssim_heads &t, int tokens, int heads)
+{
+    const int n = samples(d);
+    if (n == 0 || tokens == 0) return GBSSIM_OK;
+    if (!t.data) return GBSSIM_EINVAL;
+    if (!multiple16(t.data)) return GBSSIM_EALIGN;
+    int rc;
+    if ((rc = check_stride(t.batch_stride, n)) || (rc = check_stride(t.token_stride, tokens)) ||
+        (rc = check_stride(t.head_stride, heads)))
+        return rc;
+    return GBSSIM_OK;
+}
+
+int check_desc(const gbssim_attention *d)
+{
+    if (!d) return GBSSIM_EINVAL;
+    if (d->dtype != GBSSIM_BF16 && d->dtype != GBSSIM_F16) return GBSSIM_EINVAL;
+    if (!(d->scale > 0.0f) || !std::isfinite(d->scale)) return GBSSIM_EINVAL;
+    if ((d->q_offsets != nullptr) != (d->k_offsets != nullptr)) return GBSSIM_EINVAL;
+    if (d->q_offsets && d->kv_lengths) return GBSSIM_EINVAL;
+    if (d->sequences < 0 || d->q_tokens < 0 || d->k_tokens < 0) return GBSSIM_ESHAPE;
+    if (d->dim < 8 || d->dim > kAttnMaxDim || d->dim % 8) return GBSSIM_ESHAPE;
+    if (d->kv_heads < 1 || d->heads < d->kv_heads || d->heads % d->kv_heads) return GBSSIM_ESHAPE;
+    if (d->q_tokens > INT_MAX / 4 || d->k_tokens > INT_MAX / 4 || d->sequences > INT_MAX / 4 ||
+        d->heads > 65536)
+        return GBSSIM_ESHAPE;
+    for (const int *p : {d->kv_lengths, d->q_offsets, d->k_offsets})
+        if (reinterpret_cast<uintptr_t>(p) % 4) return GBSSIM_EALIGN;
+    int rc;
+    if ((rc = check_heads(*d, d->q, d->q_tokens, d->heads)) ||
+        (rc = check_heads(*d, d->k, d->k_tokens, d->kv_heads)) ||
+        (rc = check_heads(*d, d->v, d->k_tokens, d->kv_heads)))
+        return rc;
+    return GBSSIM_OK;
+}
+
+AttnShape shape_of(const gbssim_attention &d)
+{
+    return {d.sequences, d.q_tokens, d.k_tokens, d.heads, d.kv_heads, d.heads / d.kv_heads, d.dim,
+            d.causal != 0, is_packed(d), d.kv_lengths, d.q_offsets, d.k_offsets};
+}
+
+// A stride that nothing is read along has to be a valid one all the same.
+long long any_stride(long long stride, int extent) { return extent > 1 ? stride : 8; }
+
+bool encode(CUtensorMap &m, const gbssim_attention &d, const gbssim_heads &t, int tokens, int heads,
+            int box_heads, int box_tokens)
+{
+    const int n = samples(d);
+    // no key at all: nothing is read, but the map is a valid one
+    const bool none = tokens == 0;
+    return encode_heads_map(m, none ? d.q.data : t.data, d.dtype == GBSSIM_BF16, d.dim, heads,
+                            std::max(tokens, 1), n, any_stride(t.head_stride, none ? 1 : heads),
+                            any_stride(t.token_stride, tokens), any_stride(t.batch_stride, none ? 1 : n),
+                            box_heads, box_tokens);
+}
+
+// Blocks that a plan counts on: one to an SM.
+constexpr int kPlanBlocks = 152;
+
+struct FwdPlan {
+    int tile_heads, tile_tokens, q_tiles, splits;
+    long long tiles;
+};
+
+FwdPlan plan_fwd(const gbssim_attention &d)
+{
+    const AttnShape s = shape_of(d);
+    FwdPlan p{1, kAttnTile, 1, 1, 0};
+    // a sample whose queries of all the heads of a group fit one tile reads its keys once
+    // for the group
+    if (!s.packed && s.group > 1 && (long long)s.q_tokens * s.group <= kAttnTile) {
+        p.tile_heads = s.group;
+        p.tile_tokens = s.q_tokens;
+    }
+    const long long heads = s.heads / p.tile_heads;
+    if (p.tile_heads == 1 && s.q_tokens > kAttnTile &&
+        most_tiles(s, s.q_tokens, 2 * kAttnTile) * heads >= kPlanBlocks)
+        p.q_tiles = 2;
+    const int rows = p.tile_tokens * p.q_tiles;
+    p.tiles = s.packed ? most_tiles(s, s.q_tokens, rows) : (s.q_tokens + rows - 1) / rows;
+    const long long blocks = p.tiles * samples(d) * heads;
+    const long long key_tiles = (s.k_tokens + kAttnTile - 1) / kAttnTile;
+    if (!s.packed && blocks > 0 && 2 * blocks <= kPlanBlocks && key_tiles >= 8)
+        p.splits = int(std::min<long long>(kPlanBlocks / blocks, key_tiles / 4));
+    return p;
+}
+
+size_t part_floats(const gbssim_attention &d, const FwdPlan &p)
+{
+    if (p.splits == 1) return 0;
+    return size_t(p.splits) * q_rows(d) * d.heads * (d.dim + 1);
+}
+
+unsigned g_extra = 0;  // test hook, see gbssim_tune_attention
+
+}  // namespace
+
+extern "C" size_t gbssim_attention_workspace_bytes(const gbssim_attention *d, int backward)
+{
+    if (check_desc(d) != GBSSIM_OK || q_rows(*d) == 0) return 0;
+    if (backward) return 0;
+    return part_floats(*d, plan_fwd(*d)) * sizeof(float);
+}
+
+extern "C" int gbssim_attention_fwd(const gbssim_attention *d, void *out, float *lse_or_null,
+                                    void *workspace, size_t workspace_bytes, void *stream)
+{
+    const CallRange range("gbssim_attention_fwd");
+    int rc = check_desc(d);
+    if (rc != GBSSIM_OK) return rc;
+    if (q_rows(*d) == 0) return GBSSIM_OK;
+    if (!out) return GBSSIM_EINVAL;
+    if (!multiple16(out) || reinterpret_cast<uintptr_t>(lse_or_null) % 4) return GBSSIM_EALIGN;
+    const FwdPlan p = plan_fwd(*d);
+    const size_t need = part_floats(*d, p) * sizeof(float);
+    if (need && (!workspace || !multiple16(workspace) || workspace_bytes < need)) return GBSSIM_EWORKSPACE;
+    const Extent in[3] = {heads_extent(*d, d->q, d->q_tokens, d->heads),
+                          heads_extent(*d, d->k, d->k_tokens, d->kv_heads),
+                          heads_extent(*d, d->v, d->k_tokens, d->kv_heads)};
+    const Extent outs[3] = {dense_extent(*d, out, q_rows(*d), d->heads), floats(*d, lse_or_null),
+                            {workspace, need}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Extent &e : in)
+            if (meet(outs[i], e)) return GBSSIM_EINVAL;
+        for (int j = 0; j < i; ++j)
+            if (meet(outs[i], outs[j])) return GBSSIM_EINVAL;
+    }
+    const AttnShape s = shape_of(*d);
+    const long long grid = p.tiles * samples(*d) * (s.heads / p.tile_heads) * p.splits;
+    if (grid > INT_MAX || q_rows(*d) * d->heads * (d->dim / 8) / 128 >= INT_MAX) return GBSSIM_ESHAPE;
+    AttnFwdArgs a{};
+    if (!encode(a.q, *d, d->q, d->q_tokens, d->heads, p.tile_heads, p.tile_tokens) ||
+        !encode(a.k, *d, d->k, d->k_tokens, d->kv_heads, 1, kAttnTile) ||
+        !encode(a.v, *d, d->v, d->k_tokens, d->kv_heads, 1, kAttnTile))
+        return cuda_fail(cudaErrorInvalidValue);
+    a.s = s;
+    a.scale_log2 = float(double(d->scale) * 1.4426950408889634);
+    a.tile_heads = p.tile_heads;
+    a.tile_tokens = p.tile_tokens;
+    a.splits = p.splits;
+    a.tiles = int(p.tiles);
+    a.ragged = s.packed || s.kv_lengths;
+    a.extra = g_extra;
+    a.out = out;
+    a.lse = lse_or_null;
+    a.part_out = static_cast<float *>(workspace);
+    a.part_lse = p.splits > 1 ? a.part_out + size_t(p.splits) * q_rows(*d) * d->heads * d->dim : nullptr;
+    cudaError_t e = attention_fwd_launch(a, d->dtype, p.q_tiles, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess && p.splits > 1)
+        e = attention_join_launch(a, d->dtype, static_cast<cudaStream_t>(stream));
+    return cuda_fail(e);
+}
+
+#ifdef GBSSIM_TEST_HOOKS
+// ---- test build only (csrc/gbssim_test_hooks.h)
+extern "C" void gbssim_tune_attention(int extra_bytes)
+{
+    g_extra = extra_bytes > 0 ? unsigned(extra_bytes) : 0u;
+}
+#endif

@@ -9,6 +9,7 @@
 
 #include "gbssim.h"
 #include "api_host.cuh"
+#include "attention.cuh"
 #include "common.cuh"
 #include "residual_norm.cuh"
 #include "ssim2d.cuh"
@@ -511,7 +512,8 @@ int gbssim_device_status(unsigned *flags_out)
     if (!flags_out) return GBSSIM_EINVAL;
     *flags_out = 0;
     for (const auto status : {ssim2d_staging_status, ssim3d_staging_status, residual_norm_fwd_status,
-                              residual_norm_bwd_f32_status, residual_norm_bwd_16_status}) {
+                              residual_norm_bwd_f32_status, residual_norm_bwd_16_status,
+                              attention_fwd_status}) {
         unsigned f = 0;
         const cudaError_t e = status(&f, true);
         if (e != cudaSuccess) return cuda_fail(e);

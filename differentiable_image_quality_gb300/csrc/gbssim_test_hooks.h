@@ -32,6 +32,10 @@ void gbssim_tune_fwd_split(int on);
  * status bit).  0 restores the product behaviour. */
 void gbssim_tune_exchange(int extra_bytes);
 
+/* The same for attention: bytes that every later forward and backward announces beyond
+ * its first copy's. */
+void gbssim_tune_attention(int extra_bytes);
+
 /* Stage-by-stage parity of the 2D gradient kernel: one run of the kernel of
  * ssim_fwd's stored variant with grad2 on img1 / img2 ([N, C, H, W] float32,
  * device) that also writes, for every output pixel of [N, C, Ho, Wo]:

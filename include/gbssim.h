@@ -84,10 +84,13 @@ void gbssim_window(float w[11]);
  *   bit 1 (GBSSIM_DEV_EXCHANGE_TIMEOUT): blocks of a residual norm that share a
  *   row (more than 4096 columns) waited about a second for one another's sums;
  *   that call's outputs are not valid.
+ *   bit 2 (GBSSIM_DEV_ATTENTION_TIMEOUT): a block of an attention call waited about a
+ *   second for a tile or a product; its rows of the outputs are NaN.
  * Synchronises the device: a diagnostic, not part of the hot path.  Returns
  * GBSSIM_OK, GBSSIM_EINVAL (null flags_out) or GBSSIM_ECUDA. */
 #define GBSSIM_DEV_STAGING_TIMEOUT 1u
 #define GBSSIM_DEV_EXCHANGE_TIMEOUT 2u
+#define GBSSIM_DEV_ATTENTION_TIMEOUT 4u
 int gbssim_device_status(unsigned *flags_out);
 
 /* ------------------------------------------------------------------ 2D ----- */
@@ -368,6 +371,66 @@ int gbssim_residual_norm_bwd(const gbssim_residual_norm *desc,
                              const gbssim_rows *grad_u_or_null, const float *stats,
                              const gbssim_residual_norm_grads *grads, void *workspace,
                              size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------ attention --- */
+/* Attention between the tokens of a batch, per head:
+ *   s_ij = scale q_i . k_j,   p_ij = exp(s_ij - lse_i),   o_i = sum_j p_ij v_j,
+ *   lse_i = log(sum_j exp(s_ij)),
+ * over the keys j that query i sees.  A query that sees none has o = 0 and lse =
+ * -infinity.  heads is a multiple of kv_heads: query head h reads the keys and
+ * values of head h / (heads / kv_heads).
+ *
+ * Batch form: q is [sequences, q_tokens, heads, dim], k and v [sequences, k_tokens,
+ * kv_heads, dim].  kv_lengths (device, [sequences], or NULL) says how many keys of a
+ * sample count, from 0 to k_tokens; what lies behind them is not used, whatever it
+ * holds.
+ * Packed form (q_offsets and k_offsets given, device, [sequences + 1], ascending
+ * from 0): sequences of any lengths, zero included, one behind the other in q
+ * [q_tokens, heads, dim] and in k and v [k_tokens, kv_heads, dim]; sequence s has
+ * the rows offsets[s] to offsets[s + 1] - 1 and sees no other's.  Rows behind the
+ * last sequence belong to none: their outputs and gradients are zeros.
+ * Lengths and offsets out of their range are brought into it: the results are then
+ * not specified, but nothing outside the tensors is touched.
+ *
+ * causal != 0: query i sees the keys up to i + (keys - queries), the last query all
+ * of them; keys and queries are the counts of the shapes (batch form, whatever
+ * kv_lengths says) or of the sequence (packed).
+ * A hidden key has p = 0 exactly.  A NaN or an infinity among the keys and values of
+ * a query's own sequence may reach its output although it does not see them.
+ *
+ * Types: bfloat16 or float16, one for all tensors.  Scores, statistics and sums are
+ * float32; p is rounded to the tensors' type for its product with v, each output
+ * once.  Shapes: any number of tokens, 0 and 1 included; dim a multiple of 8 up to
+ * 128.  Inputs have any positive strides that are multiples of 16 bytes, the
+ * elements of a head side by side, and start on 16 bytes; outputs are dense. */
+
+/* A [batch, tokens, heads, dim] tensor, strides in elements (the batch's is unused in
+ * the packed form). */
+typedef struct {
+    const void *data;
+    long long batch_stride, token_stride, head_stride;
+} gbssim_heads;
+
+typedef struct {
+    int sequences, q_tokens, k_tokens;
+    int heads, kv_heads, dim;
+    int dtype;    /* GBSSIM_BF16 or GBSSIM_F16 */
+    int causal;
+    float scale;  /* positive */
+    gbssim_heads q, k, v;
+    const int *kv_lengths, *q_offsets, *k_offsets;
+} gbssim_attention;
+
+/* Workspace bytes of the forward, or with backward != 0 the backward (0 for an invalid
+ * description); 16-byte aligned, contents arbitrary.  Calls made at the same time must
+ * not share one, not even on one stream. */
+size_t gbssim_attention_workspace_bytes(const gbssim_attention *desc, int backward);
+
+/* Forward.
+ *   out  dense, of q's shape.
+ *   lse  [sequences, heads, q_tokens] (packed: [heads, q_tokens]) float32, or NULL. */
+int gbssim_attention_fwd(const gbssim_attention *desc, void *out, float *lse_or_null,
+                         void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
