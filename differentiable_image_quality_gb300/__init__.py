@@ -56,7 +56,7 @@ import torch
 
 from . import _abi, _memory
 from ._abi import SAME, VALID, GbssimError
-from ._attention import attention_fwd
+from ._attention import attention_bwd, attention_fwd, fused_attention
 from ._grad_clip import clip_grad_norm_, clip_grads, grad_norm
 from ._residual_norm import fused_residual_norm, residual_norm_bwd, residual_norm_fwd
 
@@ -80,7 +80,9 @@ __all__ = [
     "fused_residual_norm",
     "residual_norm_fwd",
     "residual_norm_bwd",
+    "fused_attention",
     "attention_fwd",
+    "attention_bwd",
     "GbssimError",
     "VALID",
     "SAME",

@@ -56,6 +56,7 @@ SIGNATURES = {
     "gbssim_residual_norm_bwd": (_i, [_vp, _vp, _vp, _fp, _vp, _vp, _sz, _vp]),
     "gbssim_attention_workspace_bytes": (_sz, [_vp, _i]),
     "gbssim_attention_fwd": (_i, [_vp, _vp, _fp, _vp, _sz, _vp]),
+    "gbssim_attention_bwd": (_i, [_vp, _vp, _vp, _fp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 # exported only by the test build (libgbssim_test.so, csrc/gbssim_test_hooks.h):
 # forced row segments, the staging and exchange modes that drive the tests of the

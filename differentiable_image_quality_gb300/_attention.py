@@ -12,6 +12,7 @@ _MAX_DIM = 128
 
 # gbssim_attention
 _DESC = struct.Struct("@8if" + "Pqqq" * 3 + "PPP")
+_HEADS = struct.Struct("@Pqqq")  # gbssim_heads
 _NO_TENSOR = (0, 0, 0, 0)
 
 
@@ -133,3 +134,87 @@ def attention_fwd(q, k, v, *, causal=False, scale=None, kv_lengths=None, offsets
                                       _memory.stream_of(index))
     _abi.check("gbssim_attention_fwd", st)
     return out, lse
+
+
+def _like(name, t, index, shape, dtype):
+    _check(name, t, index, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def attention_bwd(g_out, q, k, v, out, lse, *, causal=False, scale=None, kv_lengths=None,
+                  offsets=None, kv_offsets=None, needs=(True, True, True)):
+    """The backward without autograd: from the gradient of out, the forward's arguments
+    and what it returned (out and lse), the gradients of (q, k, v), dense, of their
+    types and shapes; None where ``needs`` is false."""
+    desc, kept, index = _describe(q, k, v, causal, scale, kv_lengths, offsets, kv_offsets)
+    _like("g_out", g_out, index, q.shape, q.dtype)
+    _like("out", out, index, q.shape, q.dtype)
+    if not out.is_contiguous():
+        raise ValueError("out must be the forward's: contiguous")
+    if not isinstance(lse, torch.Tensor) or lse.get_device() != index or \
+            lse.dtype != torch.float32 or lse.shape != _stats_shape(q) or \
+            not lse.is_contiguous():
+        raise ValueError(f"lse must be the forward's: contiguous float32 {_stats_shape(q)}")
+    lib = _abi.load()
+    with _memory.on_device(index):
+        g_out = _as_read(g_out)
+        grads = [torch.empty(t.shape, dtype=t.dtype, device=t.device) if n else None
+                 for t, n in zip((q, k, v), needs)]
+        nbytes = lib.gbssim_attention_workspace_bytes(desc, 1)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        st = lib.gbssim_attention_bwd(desc, _HEADS.pack(*_heads(g_out)), out.data_ptr(),
+                                      lse.data_ptr(), *[_abi.ptr(g) for g in grads], ws.data_ptr(),
+                                      nbytes, _memory.stream_of(index))
+    _abi.check("gbssim_attention_bwd", st)
+    return tuple(grads)
+
+
+class _FusedAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, how):
+        wanted = True in ctx.needs_input_grad
+        out, lse = attention_fwd(q, k, v, want_stats=wanted, **how)
+        if wanted:
+            ctx.how = how
+            ctx.save_for_backward(q, k, v, out, lse, how["kv_lengths"], how["offsets"],
+                                  how["kv_offsets"])
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, g_out):
+        q, k, v, out, lse, kv_lengths, offsets, kv_offsets = ctx.saved_tensors
+        return (*attention_bwd(g_out, q, k, v, out, lse, causal=ctx.how["causal"],
+                               scale=ctx.how["scale"], kv_lengths=kv_lengths, offsets=offsets,
+                               kv_offsets=kv_offsets, needs=ctx.needs_input_grad[:3]), None)
+
+
+def fused_attention(q, k, v, *, causal=False, scale=None, kv_lengths=None, offsets=None,
+                    kv_offsets=None):
+    """Softmax attention, differentiable in q, k and v: per head
+
+        out_i = sum_j softmax_j(scale * q_i . k_j) v_j
+
+    over the keys j that query i sees; zero where it sees none.
+
+    q is [batch, tokens, heads, dim], k and v [batch, keys, kv_heads, dim], bfloat16 or
+    float16, dim a multiple of 8 up to 128; heads is a multiple of kv_heads, whose
+    neighbouring query heads share keys and values.  scale, positive, is dim ** -0.5 by
+    default.  With ``causal``, query i sees the keys up to i + (keys - tokens): the last
+    query sees all.  ``kv_lengths``, int32 [batch] on the GPU, are how many of a sample's
+    keys count; what lies behind them is not used and gets a zero gradient.
+
+    Packed batches: with ``offsets``, int32 [sequences + 1] on the GPU, ascending from 0, q
+    is [rows, heads, dim] and sequence s its rows offsets[s] to offsets[s + 1] - 1, of any
+    length; k and v likewise by ``kv_offsets`` (offsets by default).  Rows behind the last
+    sequence get zeros.  The lengths stay on the GPU: nothing waits for them.
+
+    Tensors are read in place at any strides, a head's elements side by side on 16-byte
+    boundaries; others (expanded ones, odd addresses) are copied first.  Scores,
+    statistics and sums are float32, probabilities are rounded to the tensors' type for
+    their products, outputs once; results repeat bit for bit.  One query over many keys
+    (a token at a time) splits the keys over the GPU."""
+    how = {"causal": bool(causal), "scale": scale, "kv_lengths": kv_lengths, "offsets": offsets,
+           "kv_offsets": kv_offsets}
+    return _FusedAttention.apply(q, k, v, how)

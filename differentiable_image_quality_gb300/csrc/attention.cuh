@@ -31,7 +31,7 @@ struct AttnPlace {
     int queries, keys;  // of the sequence
     int shift;          // causal: query i sees keys up to i + shift
     int tile;           // which tile of the sequence
-    int tiles_before;   // of the sequences before it (packed)
+    int q_tiles_before; // of the queries of the sequences before it, in tiles of 128
 };
 
 // Offsets that do not ascend or leave the tensors are brought into range, so that
@@ -57,7 +57,7 @@ __device__ __forceinline__ bool find_place(const AttnShape &s, int index, int ro
         const int tiles = (most + rows - 1) / rows;
         p.batch = index / tiles;
         p.tile = index - p.batch * tiles;
-        p.tiles_before = p.batch * tiles;
+        p.q_tiles_before = p.batch * ((s.q_tokens + kAttnTile - 1) / kAttnTile);
         p.q_row = p.k_row = 0;
         p.queries = s.q_tokens;
         p.keys = s.kv_lengths ? min(max(__ldg(s.kv_lengths + p.batch), 0), s.k_tokens) : s.k_tokens;
@@ -65,33 +65,42 @@ __device__ __forceinline__ bool find_place(const AttnShape &s, int index, int ro
         return p.batch < s.sequences;
     }
     const int lane = threadIdx.x % 32;
-    const int *offsets = BY_KEYS ? s.k_offsets : s.q_offsets;
-    const int total = BY_KEYS ? s.k_tokens : s.q_tokens;
-    int before = 0;
+    int before = 0, q_before = 0;
     for (int base = 0; base <= s.sequences; base += 32) {
-        int first = 0, count = 0;
-        if (base + lane <= s.sequences) packed_span(offsets, s.sequences, total, base + lane, first, count);
-        const int tiles = (count + rows - 1) / rows;
-        int sum = tiles;
+        int q_first = 0, queries = 0, k_first = 0, keys = 0;
+        if (base + lane <= s.sequences) {
+            packed_span(s.q_offsets, s.sequences, s.q_tokens, base + lane, q_first, queries);
+            packed_span(s.k_offsets, s.sequences, s.k_tokens, base + lane, k_first, keys);
+        }
+        const int tiles = ((BY_KEYS ? keys : queries) + rows - 1) / rows;
+        const int q_tiles = (queries + kAttnTile - 1) / kAttnTile;
+        int sum = tiles, q_sum = q_tiles;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const int up = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += up;
+            const int q_up = __shfl_up_sync(0xffffffffu, q_sum, d);
+            if (lane >= d) {
+                sum += up;
+                q_sum += q_up;
+            }
         }
         const unsigned past = __ballot_sync(0xffffffffu, before + sum > index);
         if (past) {
-            const int l = __ffs(past) - 1, q = base + l;
-            p.tiles_before = before + __shfl_sync(0xffffffffu, sum - tiles, l);
-            p.tile = index - p.tiles_before;
+            const int l = __ffs(past) - 1;
+            p.tile = index - before - __shfl_sync(0xffffffffu, sum - tiles, l);
+            p.q_tiles_before = q_before + __shfl_sync(0xffffffffu, q_sum - q_tiles, l);
             p.batch = 0;
-            packed_span(s.q_offsets, s.sequences, s.q_tokens, q, p.q_row, p.queries);
-            packed_span(s.k_offsets, s.sequences, s.k_tokens, q, p.k_row, p.keys);
+            p.q_row = __shfl_sync(0xffffffffu, q_first, l);
+            p.k_row = __shfl_sync(0xffffffffu, k_first, l);
+            p.queries = __shfl_sync(0xffffffffu, queries, l);
+            p.keys = __shfl_sync(0xffffffffu, keys, l);
             // the rows behind the last sequences have no partners
-            if (q == s.sequences) (BY_KEYS ? p.queries : p.keys) = 0;
+            if (base + l == s.sequences) (BY_KEYS ? p.queries : p.keys) = 0;
             p.shift = p.keys - p.queries;
             return true;
         }
         before += __shfl_sync(0xffffffffu, sum, 31);
+        q_before += __shfl_sync(0xffffffffu, q_sum, 31);
     }
     return false;
 }
@@ -153,5 +162,26 @@ struct AttnFwdArgs {
 cudaError_t attention_fwd_launch(const AttnFwdArgs &a, int dtype, int q_tiles, cudaStream_t stream);
 cudaError_t attention_fwd_status(unsigned *flags, bool clear);
 cudaError_t attention_join_launch(const AttnFwdArgs &a, int dtype, cudaStream_t stream);
+
+// ------------------------------------------------------------------ backward
+
+struct AttnBwdArgs {
+    CUtensorMap q, k, v, g;  // g: the output's gradient
+    AttnShape s;
+    float scale, scale_log2;
+    int q_tiles, k_tiles;  // in all samples, or the most there can be (packed)
+    int ragged;
+    unsigned extra;  // test hook, see gbssim_tune_attention
+    // for the row sums
+    const void *out, *g_data, *v_data;
+    long long g_batch, g_token, g_head, v_batch, v_token, v_head;  // strides, elements
+    const float *lse;
+    void *dq, *dk, *dv;      // each may be null
+    float *stats;            // [heads][q_tiles][2][128]
+    unsigned *largest;       // [2][kv_heads]: |g|, |v|, as bits (float16)
+};
+
+cudaError_t attention_bwd_launch(const AttnBwdArgs &a, int dtype, cudaStream_t stream);
+cudaError_t attention_bwd_status(unsigned *flags, bool clear);
 
 }  // namespace gbssim

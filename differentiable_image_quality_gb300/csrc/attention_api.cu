@@ -80,7 +80,7 @@ int check_desc(const gbssim_attention *d)
     if (d->dim < 8 || d->dim > kAttnMaxDim || d->dim % 8) return GBSSIM_ESHAPE;
     if (d->kv_heads < 1 || d->heads < d->kv_heads || d->heads % d->kv_heads) return GBSSIM_ESHAPE;
     if (d->q_tokens > INT_MAX / 4 || d->k_tokens > INT_MAX / 4 || d->sequences > INT_MAX / 4 ||
-        d->heads > 65536)
+        d->heads > 65535)
         return GBSSIM_ESHAPE;
     for (const int *p : {d->kv_lengths, d->q_offsets, d->k_offsets})
         if (reinterpret_cast<uintptr_t>(p) % 4) return GBSSIM_EALIGN;
@@ -105,9 +105,10 @@ bool encode(CUtensorMap &m, const gbssim_attention &d, const gbssim_heads &t, in
             int box_heads, int box_tokens)
 {
     const int n = samples(d);
-    // no key at all: nothing is read, but the map is a valid one
+    // without a token nothing is read, but the map is a valid one
     const bool none = tokens == 0;
-    return encode_heads_map(m, none ? d.q.data : t.data, d.dtype == GBSSIM_BF16, d.dim, heads,
+    const void *const some = d.q_tokens ? d.q.data : d.k.data;
+    return encode_heads_map(m, none ? some : t.data, d.dtype == GBSSIM_BF16, d.dim, heads,
                             std::max(tokens, 1), n, any_stride(t.head_stride, none ? 1 : heads),
                             any_stride(t.token_stride, tokens), any_stride(t.batch_stride, none ? 1 : n),
                             box_heads, box_tokens);
@@ -150,6 +151,14 @@ size_t part_floats(const gbssim_attention &d, const FwdPlan &p)
     return size_t(p.splits) * q_rows(d) * d.heads * (d.dim + 1);
 }
 
+// The backward's row sums, in tiles of 128 queries, and the largest |g| and |v| of each
+// key head.
+size_t bwd_bytes(const gbssim_attention &d)
+{
+    return size_t(d.heads) * most_tiles(shape_of(d), d.q_tokens, kAttnTile) * 2 * kAttnTile * sizeof(float) +
+           size_t(2) * d.kv_heads * sizeof(unsigned);
+}
+
 unsigned g_extra = 0;  // test hook, see gbssim_tune_attention
 
 }  // namespace
@@ -157,7 +166,7 @@ unsigned g_extra = 0;  // test hook, see gbssim_tune_attention
 extern "C" size_t gbssim_attention_workspace_bytes(const gbssim_attention *d, int backward)
 {
     if (check_desc(d) != GBSSIM_OK || q_rows(*d) == 0) return 0;
-    if (backward) return 0;
+    if (backward) return bwd_bytes(*d);
     return part_floats(*d, plan_fwd(*d)) * sizeof(float);
 }
 
@@ -208,6 +217,73 @@ extern "C" int gbssim_attention_fwd(const gbssim_attention *d, void *out, float 
     if (e == cudaSuccess && p.splits > 1)
         e = attention_join_launch(a, d->dtype, static_cast<cudaStream_t>(stream));
     return cuda_fail(e);
+}
+
+extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_heads *grad_out, const void *out,
+                                    const float *lse, void *grad_q_or_null, void *grad_k_or_null,
+                                    void *grad_v_or_null, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const CallRange range("gbssim_attention_bwd");
+    int rc = check_desc(d);
+    if (rc != GBSSIM_OK) return rc;
+    const bool queries = q_rows(*d) > 0, keys = k_rows(*d) > 0;
+    if (!queries && !keys) return GBSSIM_OK;
+    if (!grad_out || (queries && (!out || !lse))) return GBSSIM_EINVAL;
+    if ((rc = check_heads(*d, *grad_out, d->q_tokens, d->heads))) return rc;
+    for (const void *p : {out, static_cast<const void *>(grad_q_or_null), static_cast<const void *>(grad_k_or_null),
+                          static_cast<const void *>(grad_v_or_null)})
+        if (!multiple16(p)) return GBSSIM_EALIGN;
+    if (reinterpret_cast<uintptr_t>(lse) % 4) return GBSSIM_EALIGN;
+    const size_t need = queries ? bwd_bytes(*d) : 0;
+    if (need && (!workspace || !multiple16(workspace) || workspace_bytes < need)) return GBSSIM_EWORKSPACE;
+    const Extent in[6] = {heads_extent(*d, d->q, d->q_tokens, d->heads),
+                          heads_extent(*d, d->k, d->k_tokens, d->kv_heads),
+                          heads_extent(*d, d->v, d->k_tokens, d->kv_heads),
+                          heads_extent(*d, *grad_out, d->q_tokens, d->heads),
+                          dense_extent(*d, out, q_rows(*d), d->heads), floats(*d, lse)};
+    const Extent outs[4] = {dense_extent(*d, grad_q_or_null, q_rows(*d), d->heads),
+                            dense_extent(*d, grad_k_or_null, k_rows(*d), d->kv_heads),
+                            dense_extent(*d, grad_v_or_null, k_rows(*d), d->kv_heads),
+                            {workspace, need}};
+    for (int i = 0; i < 4; ++i) {
+        for (const Extent &e : in)
+            if (meet(outs[i], e)) return GBSSIM_EINVAL;
+        for (int j = 0; j < i; ++j)
+            if (meet(outs[i], outs[j])) return GBSSIM_EINVAL;
+    }
+    const AttnShape s = shape_of(*d);
+    const long long q_tiles = queries ? most_tiles(s, d->q_tokens, kAttnTile) : 0;
+    const long long k_tiles = keys ? most_tiles(s, d->k_tokens, kAttnTile) : 0;
+    if (q_tiles * d->heads + k_tiles * d->kv_heads > INT_MAX || q_tiles + k_tiles > INT_MAX) return GBSSIM_ESHAPE;
+    AttnBwdArgs a{};
+    if (!encode(a.q, *d, d->q, d->q_tokens, d->heads, 1, kAttnTile) ||
+        !encode(a.k, *d, d->k, d->k_tokens, d->kv_heads, 1, kAttnTile) ||
+        !encode(a.v, *d, d->v, d->k_tokens, d->kv_heads, 1, kAttnTile) ||
+        !encode(a.g, *d, *grad_out, d->q_tokens, d->heads, 1, kAttnTile))
+        return cuda_fail(cudaErrorInvalidValue);
+    a.s = s;
+    a.scale = d->scale;
+    a.scale_log2 = float(double(d->scale) * 1.4426950408889634);
+    a.q_tiles = int(q_tiles);
+    a.k_tiles = int(k_tiles);
+    a.ragged = s.packed || s.kv_lengths;
+    a.extra = g_extra;
+    a.out = out;
+    a.g_data = grad_out->data;
+    a.g_batch = grad_out->batch_stride;
+    a.g_token = grad_out->token_stride;
+    a.g_head = grad_out->head_stride;
+    a.v_data = d->v.data;
+    a.v_batch = d->v.batch_stride;
+    a.v_token = d->v.token_stride;
+    a.v_head = d->v.head_stride;
+    a.lse = lse;
+    a.dq = queries ? grad_q_or_null : nullptr;
+    a.dk = keys ? grad_k_or_null : nullptr;
+    a.dv = keys ? grad_v_or_null : nullptr;
+    a.stats = static_cast<float *>(workspace);
+    a.largest = queries ? reinterpret_cast<unsigned *>(a.stats + size_t(d->heads) * q_tiles * 2 * kAttnTile) : nullptr;
+    return cuda_fail(attention_bwd_launch(a, d->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 #ifdef GBSSIM_TEST_HOOKS

@@ -1,0 +1,730 @@
+// Attention backward.  From the output's gradient g, with D_i = g_i . o_i:
+//   p_ij = exp(s_ij - lse_i),  dp_ij = g_i . v_j,  ds_ij = p_ij (dp_ij - D_i),
+//   dv_j = sum_i p_ij g_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j.
+//
+// Blocks of two kinds in one launch: those of 128 keys go over the queries and sum
+// dk and dv, those of 128 queries over the keys and sum dq.  Both form p and ds
+// again, seven products instead of five, and every sum stays in one block: no
+// partial gradients in memory, no atomics, results that repeat bit for bit.
+#include "attention.cuh"
+
+namespace gbssim {
+namespace {
+
+using namespace tc;
+
+__device__ unsigned g_attention_status;
+
+template <int DP>
+constexpr int tile_bytes()
+{
+    return DP / kSlabCols * kSlabBytes;
+}
+
+// float16 leaves little room below: probabilities go into their product times 2^14,
+// and ds times a power of two for each key head, chosen from the largest |g| and
+// |v| so that no product of them overflows.  bfloat16 needs neither.
+constexpr float kProbBits = 14.0f;
+template <typename T>
+constexpr bool kScaled = std::is_same<T, f16>::value;
+
+struct Scales {
+    float ds;  // of dp - D
+    float inv_p, inv_ds;
+};
+
+template <typename T>
+__device__ __forceinline__ Scales scales_of(const AttnBwdArgs &a, int kv_head)
+{
+    if (!kScaled<T> || !a.largest) return {1.0f, 1.0f, 1.0f};
+    const float g = __uint_as_float(__ldg(a.largest + kv_head));
+    const float v = __uint_as_float(__ldg(a.largest + a.s.kv_heads + kv_head));
+    // |dp - D| <= 2 dim |g| |v|, since o is a mean of v
+    const float most = 2.0f * a.s.dim * g * v;
+    int bits = 0;
+    if (most > 0.0f && most < INFINITY) bits = min(max(14 - ilogbf(most), -100), 100);
+    const float up = exp2f(float(bits)), p = exp2f(kProbBits);
+    return {up / p, 1.0f / p, 1.0f / up};
+}
+
+// ------------------------------------------------------------------- row sums
+
+// Per row -log2(e) lse (plus the bits that float16 probabilities are moved by) and -D,
+// in tiles of 128 queries; rows that the sequence does not have, and those that see
+// no key, have -infinity: their probabilities are zero.  16 lanes read a row.
+constexpr int kSumThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float largest8(const uint4 &w)
+{
+    float m = 0.0f;
+    for (uint32_t x : {w.x, w.y, w.z, w.w}) {
+        const float2 f = unpack2<T>(x & 0x7fff7fffu);
+        // as bits, so that a NaN is the largest
+        m = __uint_as_float(max(max(__float_as_uint(f.x), __float_as_uint(f.y)), __float_as_uint(m)));
+    }
+    return m;
+}
+
+template <typename T>
+__device__ void store_largest(float m, unsigned *to)
+{
+    unsigned b = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    if (threadIdx.x % 32 == 0 && b) atomicMax(to, b);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnBwdArgs a)
+{
+    __shared__ AttnPlace place;
+    __shared__ int there;
+    const AttnShape &s = a.s;
+    const bool values = int(blockIdx.x) >= a.q_tiles;  // the largest |v| (float16)
+    const int head = blockIdx.y;
+    if (values && head >= s.kv_heads) return;
+    if (threadIdx.x < 32) {
+        AttnPlace p;
+        const bool ok = values ? find_place<true>(s, blockIdx.x - a.q_tiles, kAttnTile, p)
+                               : find_place<false>(s, blockIdx.x, kAttnTile, p);
+        if (threadIdx.x == 0) {
+            place = p;
+            there = ok;
+        }
+    }
+    __syncthreads();
+    if (!there) return;
+    const AttnPlace pl = place;
+    const int lane = threadIdx.x % 16, team = threadIdx.x / 16;
+    const bool mine = lane * 8 < s.dim;
+    float largest = 0.0f;
+    if (values) {
+        for (int r = team; r < kAttnTile; r += kSumThreads / 16) {
+            const int t = pl.tile * kAttnTile + r;
+            if (!mine || t >= pl.keys) continue;
+            const long long at = pl.batch * a.v_batch + (long long)(pl.k_row + t) * a.v_token + head * a.v_head;
+            const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v_data) + at + lane * 8);
+            largest = __uint_as_float(max(__float_as_uint(largest), __float_as_uint(largest8<T>(w))));
+        }
+        __syncwarp();
+        store_largest<T>(largest, a.largest + s.kv_heads + head);
+        return;
+    }
+    float *const stats = a.stats + ((long long)head * a.q_tiles + pl.q_tiles_before + pl.tile) * 2 * kAttnTile;
+    for (int r = team; r < kAttnTile; r += kSumThreads / 16) {
+        const int t = pl.tile * kAttnTile + r;
+        float sum = 0.0f;
+        if (mine && t < pl.queries) {
+            const long long row = (long long)pl.batch * s.q_tokens + pl.q_row + t;
+            const T *const o = static_cast<const T *>(a.out) + (row * s.heads + head) * s.dim + lane * 8;
+            const T *const g = static_cast<const T *>(a.g_data) + pl.batch * a.g_batch +
+                               (long long)(pl.q_row + t) * a.g_token + head * a.g_head + lane * 8;
+            Raw8<T> ro, rg;
+            ro.w[0] = *reinterpret_cast<const uint4 *>(o);
+            rg.w[0] = *reinterpret_cast<const uint4 *>(g);
+            float x[8], y[8];
+            unpack8<T>(ro, x);
+            unpack8<T>(rg, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+            if constexpr (kScaled<T>)
+                largest = __uint_as_float(max(__float_as_uint(largest), __float_as_uint(largest8<T>(rg.w[0]))));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int d = 8; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) {
+            float l = -INFINITY;
+            if (t < pl.queries) {
+                const float lse = a.lse[((long long)pl.batch * s.heads + head) * s.q_tokens + pl.q_row + t];
+                if (lse != -INFINITY) l = (kScaled<T> ? kProbBits : 0.0f) - lse * 1.4426950408889634f;
+            }
+            stats[r] = l;
+            stats[kAttnTile + r] = -sum;
+        }
+    }
+    if constexpr (kScaled<T>) {
+        __syncwarp();
+        store_largest<T>(largest, a.largest + head / s.group);
+    }
+}
+
+// ------------------------------------------------------------------ gradients
+
+constexpr int kBwdThreads = 320;  // eight warps on the tiles, one copies, one issues products
+
+struct BwdShared {
+    uint64_t own_full, full[8], empty[8], s_full[2], dp_full, p_full, ds_full, done, patched, drained;
+    AttnPlace place;
+    int there;
+    unsigned tmem, failed;
+};
+
+template <int DP>
+constexpr int key_stages()  // pairs of a query tile and its gradient
+{
+    return DP == 64 ? 4 : 2;
+}
+template <int DP>
+constexpr int query_stages()  // single tiles, keys and values in turn
+{
+    return DP == 64 ? 8 : 5;
+}
+
+constexpr int kStatsBytes = 2 * kAttnTile * 4;
+
+template <int DP>
+constexpr size_t bwd_smem()
+{
+    constexpr size_t by_keys = size_t(2 + 2 * key_stages<DP>()) * tile_bytes<DP>() + key_stages<DP>() * kStatsBytes;
+    constexpr size_t by_queries = size_t(2 + query_stages<DP>()) * tile_bytes<DP>();
+    return (by_keys > by_queries ? by_keys : by_queries) + sizeof(BwdShared) + 1024;
+}
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, unsigned bytes, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
+template <int DP>
+__device__ __forceinline__ void load_tile(char *dst, const CUtensorMap *map, int head, int token, int batch,
+                                          uint64_t *bar)
+{
+#pragma unroll
+    for (int c = 0; c < DP / kSlabCols; ++c)
+        tma_load_4d(dst + c * kSlabBytes, map, c * kSlabCols, head, token, batch, bar);
+}
+
+// Zeros in the rows from `rows` on, by a warp.
+template <int DP>
+__device__ __forceinline__ void zero_rows(char *tile, int rows)
+{
+    for (int i = rows * 8 + int(threadIdx.x % 32); i < kAttnTile * 8; i += 32)
+#pragma unroll
+        for (int c = 0; c < DP / kSlabCols; ++c)
+            reinterpret_cast<uint4 *>(tile + c * kSlabBytes)[i] = make_uint4(0, 0, 0, 0);
+}
+
+// D = A B^T of two tiles of 128 rows, their columns summed over.
+__device__ __forceinline__ void product_k(unsigned d, unsigned a, unsigned b, int steps, unsigned idesc)
+{
+    for (int i = 0; i < steps; ++i) {
+        const unsigned at = (i / 4) * kSlabBytes + (i % 4) * kStepK;
+        mma(d, desc_k(a + at), desc_k(b + at), idesc, i > 0);
+    }
+}
+
+// D (+)= A B: A [128, 128] in tensor memory, its two halves of 64 columns 64 columns
+// apart, B's rows summed over.
+__device__ __forceinline__ void product_rows(unsigned d, unsigned a, unsigned b, unsigned idesc, bool add)
+{
+    const uint64_t desc = desc_mn(b, kSlabBytes);
+#pragma unroll
+    for (int i = 0; i < kAttnTile / 16; ++i)
+        mma_ta(d, a + (i / 4) * 64 + (i % 4) * 8, advance(desc, i * kStepMn), idesc, add || i > 0);
+}
+
+// 64 values as 32 columns of the A operand.
+template <typename T>
+__device__ __forceinline__ void store_half(unsigned at, const float (&v)[64])
+{
+#pragma unroll
+    for (int i = 0; i < 64; i += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = pack2<T>(v[i + 2 * e], v[i + 2 * e + 1]);
+        st16(at + i / 2, w);
+    }
+}
+
+// A thread's row of an accumulator, columns [from, to), times `scale` to memory; zeros
+// where `none`, NaN where the block failed.
+template <typename T>
+__device__ __forceinline__ void store_row(unsigned at, int from, int to, float scale, bool none, bool ok, bool mine,
+                                          T *out)
+{
+    for (int i = from; i < to; i += 16) {
+        uint32_t r[16];
+        __syncwarp();
+        ld16(at + i, r);
+        wait_ld();
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = !ok ? NAN : none ? 0.0f : __uint_as_float(r[e]) * scale;
+#pragma unroll
+        for (int h = 0; h < 16; h += 8) {
+            if (!mine || i + h >= to) continue;
+            float (&q)[8] = *reinterpret_cast<float (*)[8]>(v + h);
+            st8<T>(out + i + h, pack8<T>(q));
+        }
+    }
+}
+
+// 128 keys of a key head against all queries that see them.  Lanes are keys, columns
+// queries.  Tensor memory: scores, then p in their place; dp, then ds in its place;
+// dv; dk.  While the warps form p of a tile, the products of ds of the last one run;
+// while they form ds, those of p and the next scores.
+template <typename T, int DP>
+__device__ void by_keys(const AttnBwdArgs &a, char *base, BwdShared &sh, int kv_head)
+{
+    constexpr int kTile = tile_bytes<DP>();
+    constexpr int kStages = key_stages<DP>();
+    const AttnShape &s = a.s;
+    const AttnPlace pl = sh.place;
+    volatile unsigned *const failed = &sh.failed;
+    const unsigned tmem = sh.tmem;
+    const unsigned s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 256 + DP;
+    char *const ring = base + 2 * kTile;
+    char *const ring_stats = ring + 2 * kStages * kTile;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    const int first = pl.tile * kAttnTile;  // key
+    const int all = (pl.queries + kAttnTile - 1) / kAttnTile;
+    // the first tile of queries that sees the first key
+    const int from = s.causal ? min(max(first - pl.shift, 0) / kAttnTile, all) : 0;
+    const int tiles = all - from, total = first < pl.keys ? tiles * s.group : 0;
+
+    if (warp == 8) {
+        int issued = 0;
+        if (lane == 0 && total > 0) {
+            mbar_arrive_expect_tx(&sh.own_full, 2 * kTile + a.extra);
+            load_tile<DP>(base, &a.k, kv_head, pl.k_row + first, pl.batch, &sh.own_full);
+            load_tile<DP>(base + kTile, &a.v, kv_head, pl.k_row + first, pl.batch, &sh.own_full);
+        }
+        bool ok = true;
+        int patches = 0;
+        for (int it = 0, g = 0, t = from; ok && it < total; ++it) {
+            const int stage = it % kStages, head = kv_head * s.group + g;
+            if (it >= kStages) ok = attn_wait_warp(&sh.empty[stage], (it / kStages - 1) & 1, failed);
+            if (!ok) break;
+            // rows behind the sequence's are another's: zeros in their place
+            const int rows = pl.queries - t * kAttnTile;
+            const bool patch = s.packed && rows < kAttnTile;
+            char *const tile = ring + 2 * stage * kTile;
+            if (lane == 0) {
+                uint64_t *const bar = patch ? &sh.patched : &sh.full[stage];
+                mbar_arrive_expect_tx(bar, 2 * kTile + kStatsBytes);
+                load_tile<DP>(tile, &a.q, head, pl.q_row + t * kAttnTile, pl.batch, bar);
+                load_tile<DP>(tile + kTile, &a.g, head, pl.q_row + t * kAttnTile, pl.batch, bar);
+                bulk_load(ring_stats + stage * kStatsBytes,
+                          a.stats + ((long long)head * a.q_tiles + pl.q_tiles_before + t) * 2 * kAttnTile,
+                          kStatsBytes, bar);
+            }
+            if (patch) {
+                ok = attn_wait_warp(&sh.patched, patches++ & 1, failed);
+                zero_rows<DP>(tile, rows);
+                zero_rows<DP>(tile + kTile, rows);
+                fence_proxy();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.full[stage]);
+            }
+            issued = it + 1;
+            if (++t == all) {
+                t = from;
+                ++g;
+            }
+        }
+        if (*failed && lane == 0) {
+            if (total > 0) mbar_wait_bounded(&sh.own_full, 0, kAttnDrainCycles);
+            for (int it = max(0, issued - kStages); it < issued; ++it)
+                mbar_wait_bounded(&sh.full[it % kStages], (it / kStages) & 1, kAttnDrainCycles);
+            atomicOr(&g_attention_status, 4u);
+        }
+    } else if (warp == 9) {
+        if (lane == 0 && total > 0) {
+            const int steps = (s.dim + 15) / 16;
+            const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
+            const unsigned k_u = smem_u32(base), v_u = k_u + kTile, ring_u = smem_u32(ring);
+            bool ok = attn_wait(&sh.own_full, 0, failed) && attn_wait(&sh.full[0], 0, failed);
+            if (ok) {
+                product_k(s_at, k_u, ring_u, steps, id_s);
+                commit(&sh.s_full[0]);
+                product_k(dp_at, v_u, ring_u + kTile, steps, id_s);
+                commit(&sh.dp_full);
+            }
+            for (int it = 0; ok && it < total; ++it) {
+                const unsigned tile = ring_u + 2 * (it % kStages) * kTile;
+                const int nx = (it + 1) % kStages;
+                const unsigned next = ring_u + 2 * nx * kTile;
+                const bool more = it + 1 < total;
+                if (!(ok = attn_wait(&sh.p_full, it & 1, failed))) break;
+                fence_after();
+                product_rows(dv_at, s_at, tile + kTile, id_d, it > 0);
+                if (more) {
+                    if (!(ok = attn_wait(&sh.full[nx], ((it + 1) / kStages) & 1, failed))) break;
+                    product_k(s_at, k_u, next, steps, id_s);
+                    commit(&sh.s_full[0]);
+                }
+                if (!(ok = attn_wait(&sh.ds_full, it & 1, failed))) break;
+                fence_after();
+                product_rows(dk_at, dp_at, tile, id_d, it > 0);
+                commit(&sh.empty[it % kStages]);
+                if (more) {
+                    product_k(dp_at, v_u, next + kTile, steps, id_s);
+                    commit(&sh.dp_full);
+                }
+            }
+            if (ok) {
+                commit(&sh.done);
+            } else {
+                commit(&sh.drained);
+                mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
+            }
+        }
+    } else {
+        const int half = warp / 4, row = threadIdx.x % 128;
+        const unsigned lanes = unsigned(warp % 4) << 21;
+        const unsigned my_s = s_at + lanes + half * 64, my_dp = dp_at + lanes + half * 64;
+        const int key = first + row;
+        const Scales sc = scales_of<T>(a, kv_head);
+        const f32x2 c2 = both(a.scale_log2);
+        bool ok = true;
+        for (int it = 0, t = from; it < total; ++it) {
+            const int stage = it % kStages;
+            const float *const stats = reinterpret_cast<const float *>(ring_stats + stage * kStatsBytes) + half * 64;
+            // columns before `hidden` are queries that do not see this key
+            const int hidden = key >= pl.keys ? 64
+                               : s.causal     ? key - pl.shift - t * kAttnTile - half * 64
+                                              : 0;
+            const bool masked = __any_sync(0xffffffffu, hidden > 0);
+            ok = attn_wait_warp(&sh.full[stage], (it / kStages) & 1, failed) &&
+                 attn_wait_warp(&sh.s_full[0], it & 1, failed);
+            if (!ok) break;
+            fence_after();
+            float p[64];
+            ld32(my_s, reinterpret_cast<uint32_t *>(p));
+            ld32(my_s + 32, reinterpret_cast<uint32_t *>(p) + 32);
+            wait_ld();
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+                const float4 l = *reinterpret_cast<const float4 *>(stats + i);
+                const float2 x = halves(fma2(pair(p[i], p[i + 1]), c2, pair(l.x, l.y)));
+                const float2 y = halves(fma2(pair(p[i + 2], p[i + 3]), c2, pair(l.z, l.w)));
+                p[i] = exp2_fast(x.x);
+                p[i + 1] = exp2_fast(x.y);
+                p[i + 2] = exp2_fast(y.x);
+                p[i + 3] = exp2_fast(y.y);
+            }
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) p[i] = i < hidden ? 0.0f : p[i];
+            }
+            store_half<T>(my_s, p);
+            wait_st();
+            fence_before();
+            mbar_arrive(&sh.p_full);
+            ok = attn_wait_warp(&sh.dp_full, it & 1, failed);
+            if (!ok) break;
+            fence_after();
+            float d[64];
+            ld32(my_dp, reinterpret_cast<uint32_t *>(d));
+            ld32(my_dp + 32, reinterpret_cast<uint32_t *>(d) + 32);
+            wait_ld();
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+                const float4 n = *reinterpret_cast<const float4 *>(stats + kAttnTile + i);
+                f32x2 x = add2(pair(d[i], d[i + 1]), pair(n.x, n.y));
+                f32x2 y = add2(pair(d[i + 2], d[i + 3]), pair(n.z, n.w));
+                if constexpr (kScaled<T>) {
+                    x = mul2(x, both(sc.ds));
+                    y = mul2(y, both(sc.ds));
+                }
+                const float2 u = halves(mul2(x, pair(p[i], p[i + 1])));
+                const float2 w = halves(mul2(y, pair(p[i + 2], p[i + 3])));
+                d[i] = u.x;
+                d[i + 1] = u.y;
+                d[i + 2] = w.x;
+                d[i + 3] = w.y;
+            }
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) d[i] = i < hidden ? 0.0f : d[i];
+            }
+            store_half<T>(my_dp, d);
+            wait_st();
+            fence_before();
+            mbar_arrive(&sh.ds_full);
+            if (++t == all) t = from;
+        }
+        if (ok && total > 0) ok = attn_wait_warp(&sh.done, 0, failed);
+        fence_after();
+        const int count = s.packed ? pl.keys : s.k_tokens;
+        const bool mine = key < count, none = total == 0 || key >= pl.keys;
+        const long long at = ((long long)pl.batch * s.k_tokens + pl.k_row + key) * s.kv_heads + kv_head;
+        T *const out = static_cast<T *>(half ? a.dk : a.dv);
+        store_row<T>((half ? dk_at : dv_at) + lanes, 0, s.dim, half ? a.scale * sc.inv_ds : sc.inv_p, none, ok,
+                     mine && out, out + at * s.dim);
+    }
+}
+
+// 128 queries of a head against all keys that they see.  Lanes are queries, columns
+// keys.  Tensor memory: two tiles of scores, so that the next one's are there when
+// they are wanted; dp, then ds in its place; dq.
+template <typename T, int DP>
+__device__ void by_queries(const AttnBwdArgs &a, char *base, BwdShared &sh, int head)
+{
+    constexpr int kTile = tile_bytes<DP>();
+    constexpr int kStages = query_stages<DP>();
+    const AttnShape &s = a.s;
+    const AttnPlace pl = sh.place;
+    volatile unsigned *const failed = &sh.failed;
+    const unsigned tmem = sh.tmem;
+    const unsigned s_at = tmem, dp_at = tmem + 256, dq_at = tmem + 384;
+    char *const ring = base + 2 * kTile;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int kv_head = head / s.group;
+
+    const int first = pl.tile * kAttnTile;  // query
+    int seen = pl.keys;
+    if (s.causal) seen = min(seen, min(first + kAttnTile, pl.queries) + pl.shift);
+    const int total = seen <= 0 ? 0 : (seen + kAttnTile - 1) / kAttnTile;
+
+    if (warp == 8) {
+        int issued = 0;
+        if (lane == 0 && total > 0) {
+            mbar_arrive_expect_tx(&sh.own_full, 2 * kTile + a.extra);
+            load_tile<DP>(base, &a.q, head, pl.q_row + first, pl.batch, &sh.own_full);
+            load_tile<DP>(base + kTile, &a.g, head, pl.q_row + first, pl.batch, &sh.own_full);
+        }
+        bool ok = true;
+        for (int it = 0; ok && it < 2 * total; ++it) {
+            const int stage = it % kStages, j = it / 2;
+            if (it >= kStages) ok = attn_wait_warp(&sh.empty[stage], (it / kStages - 1) & 1, failed);
+            if (!ok) break;
+            // keys behind the last one may be anything: zeros in their place
+            const int rows = pl.keys - j * kAttnTile;
+            const bool key = it % 2 == 0, patch = key && a.ragged && rows < kAttnTile;
+            char *const tile = ring + stage * kTile;
+            if (lane == 0) {
+                uint64_t *const bar = patch ? &sh.patched : &sh.full[stage];
+                mbar_arrive_expect_tx(bar, kTile);
+                load_tile<DP>(tile, key ? &a.k : &a.v, kv_head, pl.k_row + j * kAttnTile, pl.batch, bar);
+            }
+            if (patch) {
+                ok = attn_wait_warp(&sh.patched, 0, failed);
+                zero_rows<DP>(tile, rows);
+                fence_proxy();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.full[stage]);
+            }
+            issued = it + 1;
+        }
+        if (*failed && lane == 0) {
+            if (total > 0) mbar_wait_bounded(&sh.own_full, 0, kAttnDrainCycles);
+            for (int it = max(0, issued - kStages); it < issued; ++it)
+                mbar_wait_bounded(&sh.full[it % kStages], (it / kStages) & 1, kAttnDrainCycles);
+            atomicOr(&g_attention_status, 4u);
+        }
+    } else if (warp == 9) {
+        if (lane == 0 && total > 0) {
+            const int steps = (s.dim + 15) / 16;
+            const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
+            const unsigned q_u = smem_u32(base), g_u = q_u + kTile, ring_u = smem_u32(ring);
+            const auto wait_tile = [&](int it) {
+                return attn_wait(&sh.full[it % kStages], (it / kStages) & 1, failed);
+            };
+            const auto tile_of = [&](int it) { return ring_u + (it % kStages) * kTile; };
+            const auto scores = [&](int j) {
+                if (!wait_tile(2 * j)) return false;
+                product_k(s_at + (j & 1) * 128, q_u, tile_of(2 * j), steps, id_s);
+                commit(&sh.s_full[j & 1]);
+                return true;
+            };
+            const auto products = [&](int j) {
+                if (!wait_tile(2 * j + 1)) return false;
+                product_k(dp_at, g_u, tile_of(2 * j + 1), steps, id_s);
+                commit(&sh.dp_full);
+                commit(&sh.empty[(2 * j + 1) % kStages]);
+                return true;
+            };
+            bool ok = attn_wait(&sh.own_full, 0, failed) && scores(0) && products(0);
+            if (ok && total > 1) ok = scores(1);
+            for (int j = 0; ok && j < total; ++j) {
+                if (!(ok = attn_wait(&sh.ds_full, j & 1, failed))) break;
+                fence_after();
+                product_rows(dq_at, dp_at, tile_of(2 * j), id_d, j > 0);
+                commit(&sh.empty[(2 * j) % kStages]);
+                if (j + 1 < total && !(ok = products(j + 1))) break;
+                if (j + 2 < total) ok = scores(j + 2);
+            }
+            if (ok) {
+                commit(&sh.done);
+            } else {
+                commit(&sh.drained);
+                mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
+            }
+        }
+    } else {
+        const int half = warp / 4, row = threadIdx.x % 128;
+        const unsigned lanes = unsigned(warp % 4) << 21;
+        const int query = first + row;
+        const float *const stats =
+            a.stats + ((long long)head * a.q_tiles + pl.q_tiles_before + pl.tile) * 2 * kAttnTile;
+        const f32x2 c2 = both(a.scale_log2), l2 = both(stats[row]);
+        const Scales sc = scales_of<T>(a, kv_head);
+        const f32x2 n2 = both(stats[kAttnTile + row] * sc.ds);
+        const int end = s.causal ? min(pl.keys, query + 1 + pl.shift) : pl.keys;
+        bool ok = true;
+        for (int j = 0; j < total; ++j) {
+            const unsigned my_s = s_at + lanes + (j & 1) * 128 + half * 64, my_dp = dp_at + lanes + half * 64;
+            const int left = end - j * kAttnTile - half * 64;
+            const bool masked = __any_sync(0xffffffffu, left < 64);
+            ok = attn_wait_warp(&sh.s_full[j & 1], (j >> 1) & 1, failed);
+            if (!ok) break;
+            fence_after();
+            float p[64], d[64];
+            ld32(my_s, reinterpret_cast<uint32_t *>(p));
+            ld32(my_s + 32, reinterpret_cast<uint32_t *>(p) + 32);
+            wait_ld();
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+                const float2 x = halves(fma2(pair(p[i], p[i + 1]), c2, l2));
+                p[i] = exp2_fast(x.x);
+                p[i + 1] = exp2_fast(x.y);
+            }
+            ok = attn_wait_warp(&sh.dp_full, j & 1, failed);
+            if (!ok) break;
+            fence_after();
+            ld32(my_dp, reinterpret_cast<uint32_t *>(d));
+            ld32(my_dp + 32, reinterpret_cast<uint32_t *>(d) + 32);
+            wait_ld();
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+                f32x2 x = pair(d[i], d[i + 1]);
+                x = kScaled<T> ? fma2(x, both(sc.ds), n2) : add2(x, n2);
+                const float2 u = halves(mul2(x, pair(p[i], p[i + 1])));
+                d[i] = u.x;
+                d[i + 1] = u.y;
+            }
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) d[i] = i < left ? d[i] : 0.0f;
+            }
+            store_half<T>(my_dp, d);
+            wait_st();
+            fence_before();
+            mbar_arrive(&sh.ds_full);
+        }
+        if (ok && total > 0) ok = attn_wait_warp(&sh.done, 0, failed);
+        fence_after();
+        const long long at = ((long long)pl.batch * s.q_tokens + pl.q_row + query) * s.heads + head;
+        const int cut = min(s.dim, 64);
+        store_row<T>(dq_at + lanes, half ? cut : 0, half ? s.dim : cut, a.scale * sc.inv_ds, total == 0, ok,
+                     query < pl.queries, static_cast<T *>(a.dq) + at * s.dim);
+    }
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __grid_constant__ AttnBwdArgs a)
+{
+    extern __shared__ char raw[];
+    char *const base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    BwdShared &sh = *reinterpret_cast<BwdShared *>(base + bwd_smem<DP>() - 1024 - sizeof(BwdShared));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const AttnShape &s = a.s;
+    const bool keys_wanted = a.dk || a.dv;
+    const unsigned key_blocks = keys_wanted ? unsigned(a.k_tiles) * s.kv_heads : 0;
+    const bool keys = blockIdx.x < key_blocks;
+    const unsigned u = keys ? blockIdx.x : blockIdx.x - key_blocks;
+    // causal: falling work, that of the first keys and of the last queries before the
+    // others; else a head's blocks one after another, which share its tiles in L2
+    int head, index;
+    if (s.causal) {
+        const int heads = keys ? s.kv_heads : s.heads;
+        head = u % heads;
+        const int i = u / heads;
+        if (s.packed) {
+            index = keys ? i : a.q_tiles - 1 - i;
+        } else {
+            const int tiles = (keys ? a.k_tiles : a.q_tiles) / s.sequences;
+            const int tile = keys ? i / s.sequences : tiles - 1 - i / s.sequences;
+            index = i % s.sequences * tiles + tile;
+        }
+    } else {
+        const int tiles = keys ? a.k_tiles : a.q_tiles;
+        head = u / tiles;
+        index = u % tiles;
+    }
+    if (warp == 8) {
+        AttnPlace place;
+        const bool there = keys ? find_place<true>(s, index, kAttnTile, place)
+                                : find_place<false>(s, index, kAttnTile, place);
+        if (lane == 0) {
+            sh.place = place;
+            sh.there = there;
+            sh.failed = 0;
+            for (uint64_t *b : {&sh.own_full, &sh.s_full[0], &sh.s_full[1], &sh.dp_full, &sh.done, &sh.patched,
+                                &sh.drained})
+                mbar_init(b, 1);
+            for (int i = 0; i < 8; ++i) {
+                mbar_init(&sh.full[i], 1);
+                mbar_init(&sh.empty[i], 1);
+            }
+            mbar_init(&sh.p_full, 256);
+            mbar_init(&sh.ds_full, 256);
+            mbar_init_fence();
+        }
+    }
+    if (warp == 9) alloc_all(&sh.tmem);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (sh.there) {
+        if (keys)
+            by_keys<T, DP>(a, base, sh, head);
+        else
+            by_queries<T, DP>(a, base, sh, head);
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        fence_after();
+        free_all(sh.tmem);
+    }
+}
+
+template <typename T, int DP>
+cudaError_t launch(const AttnBwdArgs &a, cudaStream_t stream)
+{
+    constexpr size_t smem = bwd_smem<DP>();
+    static_assert(smem <= 232448, "a block's shared memory");
+    cudaError_t e = cudaFuncSetAttribute(attention_bwd_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(smem));
+    if (e != cudaSuccess) return e;
+    if (kScaled<T> && a.largest) {
+        e = cudaMemsetAsync(a.largest, 0, size_t(2) * a.s.kv_heads * sizeof(unsigned), stream);
+        if (e != cudaSuccess) return e;
+    }
+    const dim3 grid(unsigned(a.q_tiles + (kScaled<T> ? a.k_tiles : 0)), unsigned(a.s.heads));
+    if (a.q_tiles > 0) attention_sums_kernel<T><<<grid, kSumThreads, 0, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const long long blocks = (a.dk || a.dv ? (long long)a.k_tiles * a.s.kv_heads : 0) +
+                             (a.dq ? (long long)a.q_tiles * a.s.heads : 0);
+    if (blocks > 0) attention_bwd_kernel<T, DP><<<unsigned(blocks), kBwdThreads, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t attention_bwd_launch(const AttnBwdArgs &a, int dtype, cudaStream_t stream)
+{
+    if (dtype == GBSSIM_BF16) return a.s.dim <= 64 ? launch<bf16, 64>(a, stream) : launch<bf16, 128>(a, stream);
+    return a.s.dim <= 64 ? launch<f16, 64>(a, stream) : launch<f16, 128>(a, stream);
+}
+
+cudaError_t attention_bwd_status(unsigned *flags, bool clear)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(flags, g_attention_status, sizeof(unsigned));
+    if (e == cudaSuccess && clear && *flags) {
+        const unsigned zero = 0;
+        e = cudaMemcpyToSymbol(g_attention_status, &zero, sizeof(unsigned));
+    }
+    return e;
+}
+
+}  // namespace gbssim

@@ -513,7 +513,7 @@ int gbssim_device_status(unsigned *flags_out)
     *flags_out = 0;
     for (const auto status : {ssim2d_staging_status, ssim3d_staging_status, residual_norm_fwd_status,
                               residual_norm_bwd_f32_status, residual_norm_bwd_16_status,
-                              attention_fwd_status}) {
+                              attention_fwd_status, attention_bwd_status}) {
         unsigned f = 0;
         const cudaError_t e = status(&f, true);
         if (e != cudaSuccess) return cuda_fail(e);

@@ -432,6 +432,20 @@ size_t gbssim_attention_workspace_bytes(const gbssim_attention *desc, int backwa
 int gbssim_attention_fwd(const gbssim_attention *desc, void *out, float *lse_or_null,
                          void *workspace, size_t workspace_bytes, void *stream);
 
+/* Backward from the gradient of out (any strides that q may have):
+ *   p_ij as above, from lse;  D_i = grad_out_i . out_i;
+ *   ds_ij = p_ij (grad_out_i . v_j - D_i),
+ *   grad_q_i = scale sum_j ds_ij k_j,  grad_k_j = scale sum_i ds_ij q_i,
+ *   grad_v_j = sum_i p_ij grad_out_i,
+ * the last two over all query heads that share the key head.  desc is the forward's,
+ * out and lse what it wrote.  Outputs are dense, of q's, k's and v's shapes, and
+ * overwritten; NULL: not wanted.  p and ds are rounded to the tensors' type for their
+ * products (in float16 times powers of two that keep small gradients), sums are
+ * float32. */
+int gbssim_attention_bwd(const gbssim_attention *desc, const gbssim_heads *grad_out, const void *out,
+                         const float *lse, void *grad_q_or_null, void *grad_k_or_null,
+                         void *grad_v_or_null, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -150,3 +150,269 @@ def test_forward_key_lengths(pkg, Tq, causal):
     for b, n in enumerate(lengths):
         check_sequence(out[b], lse[b], q[b], k[b, :n], v[b, :n], D ** -0.5,
                        visible(Tq, Tk, causal, Tk)[:, :n])
+
+
+# ------------------------------------------------------------------ backward
+
+def definition_bwd(g, q, k, v, out, scale, seen, lse):
+    """Gradients of one sequence in float64, and the largest errors they may have.
+
+    With u and e as above: p is off by relative w = u + 2 e + 2^-18 (its rounding for dv,
+    the score's and lse's errors), dp - D by the float32 sums' (dim + 8) 2^-22 of
+    absolute sums, and by u sum|g o| since D takes the rounded output; ds is rounded once
+    more (u).  float16 scales by powers of two, whose rounding is u too; below them it
+    keeps 2^-24 of the scaled range: 2^-39 of the bound 2 dim |g| |v| on dp.  The sums of
+    n products lose n 2^-22 at most; each gradient is rounded once (u)."""
+    group = q.shape[1] // k.shape[1]
+    half = v.dtype == HF
+    u = torch.finfo(v.dtype).eps / 2
+    dim, n, m = q.shape[-1], q.shape[0], k.shape[0]
+    q, k, v, g, out = (t.double() for t in (q, k, v, g, out))
+    wide_k, wide_v = (t.repeat_interleave(group, 1) for t in (k, v))
+
+    def heads(t):  # sums of the heads that share
+        return t.unflatten(1, (k.shape[1], group)).sum(2)
+
+    step = (dim + 8) * 2.0 ** -22
+    s = torch.einsum("ihd,jhd->hij", q, wide_k) * scale
+    e = torch.einsum("ihd,jhd->hij", q.abs(), wide_k.abs()) * scale * step
+    p = torch.exp(s - lse.nan_to_num(neginf=0.0)[..., None]).masked_fill(~seen, 0.0)
+    e = e.masked_fill(~seen, 0.0)
+    most = e.amax(-1, keepdim=True) if m else e.sum(-1, keepdim=True)
+    w = u + e + most + 2.0 ** -18
+    dp = torch.einsum("ihd,jhd->hij", g, wide_v)
+    dp_abs = torch.einsum("ihd,jhd->hij", g.abs(), wide_v.abs())
+    exact_o = torch.einsum("hij,jhd->ihd", p, wide_v)
+    D = (g * exact_o).sum(-1).T[..., None]
+    D_err = (g * (out - exact_o)).sum(-1).abs().T[..., None] + \
+        (g * out).abs().sum(-1).T[..., None] * step
+    ds = p * (dp - D)
+    floor = (2 * dim * g.abs().max() * v.abs().max()) * 2.0 ** -38 if half and g.numel() and m else 0.0
+    ds_err = ds.abs() * (w + u) + p * (dp_abs * step + D_err) * (1 + w) + seen * floor
+    p_err = p * w + (seen * 2.0 ** -38 if half else 0.0)
+    ax = lambda *t: torch.einsum(*t)  # noqa: E731
+    dq = ax("hij,jhd->ihd", ds, wide_k) * scale
+    dk = heads(ax("hij,ihd->jhd", ds, q)) * scale
+    dv = heads(ax("hij,ihd->jhd", p, g))
+    dq_err = (ax("hij,jhd->ihd", ds_err, wide_k.abs()) +
+              ax("hij,jhd->ihd", ds.abs(), wide_k.abs()) * (m + 8) * 2.0 ** -22) * scale
+    dk_err = heads(ax("hij,ihd->jhd", ds_err, q.abs()) +
+                   ax("hij,ihd->jhd", ds.abs(), q.abs()) * (n * group + 8) * 2.0 ** -22) * scale
+    dv_err = heads(ax("hij,ihd->jhd", p_err, g.abs()) +
+                   ax("hij,ihd->jhd", p, g.abs()) * (n * group + 8) * 2.0 ** -22)
+    # the least float16 is 2^-24
+    tiny = 2.0 ** -25 if half else 1e-30
+    return [(t, err * (1 + u) + u * t.abs() + tiny) for t, err in ((dq, dq_err), (dk, dk_err),
+                                                                  (dv, dv_err))]
+
+
+def check_gradients(got, g, q, k, v, out, scale, seen):
+    _, lse, _, _ = definition(q, k, v, scale, seen)
+    for name, t, (ref, bound) in zip("qkv", got, definition_bwd(g, q, k, v, out, scale, seen, lse)):
+        ratio = ((t.double() - ref).abs() / bound)
+        assert (ratio <= 1).all(), (name, ratio.max().item())
+
+
+@pytest.mark.parametrize("case", [c for c in BATCHES if c[2] <= 2000], ids=str)
+def test_backward_batch(pkg, case):
+    B, Tq, Tk, H, K, D, dtype, causal = case
+    q, k, v = inputs(4, B, Tq, Tk, H, K, D, dtype)
+    g = normal(torch.Generator(device="cuda").manual_seed(5), *q.shape, dtype=dtype, std=0.1)
+    out, lse = pkg.attention_fwd(q, k, v, causal=causal, want_stats=True)
+    got = pkg.attention_bwd(g, q, k, v, out, lse, causal=causal)
+    for t, like in zip(got, (q, k, v)):
+        assert t.shape == like.shape and t.dtype == dtype and t.is_contiguous()
+    for b in range(B):
+        check_gradients([t[b] for t in got], g[b], q[b], k[b], v[b], out[b], D ** -0.5,
+                        visible(Tq, Tk, causal, Tk))
+
+
+@pytest.mark.parametrize("tail", [0, 9])
+@pytest.mark.parametrize("case", PACKS, ids=str)
+def test_backward_packed(pkg, case, tail):
+    lengths, H, K, D, dtype, causal = case
+    ends, offsets = pack_offsets(lengths)
+    n = ends[-1] + tail
+    q, k, v = inputs(6, None, n, n, H, K, D, dtype)
+    g = normal(torch.Generator(device="cuda").manual_seed(7), *q.shape, dtype=dtype, std=0.1)
+    if tail:  # what lies behind the last sequence reaches nothing
+        for t in (q, k, v, g):
+            t[ends[-1]:] = float("nan")
+    out, lse = pkg.attention_fwd(q, k, v, causal=causal, offsets=offsets, want_stats=True)
+    got = pkg.attention_bwd(g, q, k, v, out, lse, causal=causal, offsets=offsets)
+    for a, b in zip(ends, ends[1:]):
+        check_gradients([t[a:b] for t in got], g[a:b], q[a:b], k[a:b], v[a:b], out[a:b],
+                        D ** -0.5, visible(b - a, b - a, causal, b - a))
+    for t in got:
+        assert (t[ends[-1]:] == 0).all()
+
+
+def test_packed_sequences_do_not_meet(pkg):
+    """A sequence full of NaN beside others changes nothing in them."""
+    lengths, H, D = [40, 77, 130, 5], 3, 64
+    ends, offsets = pack_offsets(lengths)
+    q, k, v = inputs(8, None, ends[-1], ends[-1], H, H, D, BF)
+    g = normal(torch.Generator(device="cuda").manual_seed(9), *q.shape)
+
+    def run():
+        out, lse = pkg.attention_fwd(q, k, v, offsets=offsets, want_stats=True)
+        return (out, *pkg.attention_bwd(g, q, k, v, out, lse, offsets=offsets))
+
+    before = run()
+    for t in (q, k, v, g):
+        t[ends[1]:ends[2]] = float("nan")
+    after = run()
+    for x, y in zip(before, after):
+        assert torch.equal(x[:ends[1]], y[:ends[1]]) and torch.equal(x[ends[2]:], y[ends[2]:])
+        assert y[ends[1]:ends[2]].isnan().all()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_backward_key_lengths(pkg, causal):
+    B, Tq, Tk, H, K, D = 5, 150, 400, 4, 2, 80
+    q, k, v = inputs(10, B, Tq, Tk, H, K, D, BF)
+    g = normal(torch.Generator(device="cuda").manual_seed(11), *q.shape)
+    lengths = [400, 0, 1, 128, 277]
+    for b, n in enumerate(lengths):
+        k[b, n:] = float("inf")
+        v[b, n:] = float("nan")
+    kv = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out, lse = pkg.attention_fwd(q, k, v, causal=causal, kv_lengths=kv, want_stats=True)
+    got = pkg.attention_bwd(g, q, k, v, out, lse, causal=causal, kv_lengths=kv)
+    for b, n in enumerate(lengths):
+        check_gradients([got[0][b], got[1][b, :n], got[2][b, :n]], g[b], q[b], k[b, :n], v[b, :n],
+                        out[b], D ** -0.5, visible(Tq, Tk, causal, Tk)[:, :n])
+        assert (got[1][b, n:] == 0).all() and (got[2][b, n:] == 0).all()
+
+
+def test_cross_packed(pkg):
+    """Queries and keys packed by offsets of their own, sequences without the one or the
+    other among them."""
+    ql, kl, H, K, D = [100, 0, 33, 200], [70, 50, 0, 300], 4, 2, 128
+    qe, qo = pack_offsets(ql)
+    ke, ko = pack_offsets(kl)
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    q, g = normal(gen, qe[-1], H, D), normal(gen, qe[-1], H, D)
+    k, v = normal(gen, ke[-1] + 3, K, D), normal(gen, ke[-1] + 3, K, D)
+    out, lse = pkg.attention_fwd(q, k, v, offsets=qo, kv_offsets=ko, want_stats=True)
+    got = pkg.attention_bwd(g, q, k, v, out, lse, offsets=qo, kv_offsets=ko)
+    for a, b, c, d in zip(qe, qe[1:], ke, ke[1:]):
+        seen = visible(b - a, d - c, False, 0)
+        check_sequence(out[a:b], lse[:, a:b], q[a:b], k[c:d], v[c:d], D ** -0.5, seen)
+        check_gradients([got[0][a:b], got[1][c:d], got[2][c:d]], g[a:b], q[a:b], k[c:d], v[c:d],
+                        out[a:b], D ** -0.5, seen)
+    assert (got[1][ke[-1]:] == 0).all()
+
+
+def test_small_float16_gradients(pkg):
+    """Gradients far below float16's normal range times a probability keep their digits."""
+    B, T, H, D = 1, 700, 2, 64
+    q, k, v = inputs(13, B, T, T, H, H, D, HF)
+    g = normal(torch.Generator(device="cuda").manual_seed(14), *q.shape, dtype=HF, std=2.0 ** -8)
+    out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
+    got = pkg.attention_bwd(g, q, k, v, out, lse)
+    check_gradients([t[0] for t in got], g[0], q[0], k[0], v[0], out[0], D ** -0.5,
+                    visible(T, T, False, T))
+
+
+@pytest.mark.parametrize("needs", [(True, False, False), (False, True, False), (False, False, True)])
+def test_single_gradients(pkg, needs):
+    q, k, v = inputs(15, 2, 140, 260, 4, 2, 64, BF)
+    g = normal(torch.Generator(device="cuda").manual_seed(16), *q.shape)
+    out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
+    every = pkg.attention_bwd(g, q, k, v, out, lse)
+    some = pkg.attention_bwd(g, q, k, v, out, lse, needs=needs)
+    for n, x, y in zip(needs, every, some):
+        assert torch.equal(x, y) if n else y is None
+
+
+def test_autograd_strided(pkg):
+    """q, k and v as they lie in one product, and heads before tokens; an expanded
+    gradient."""
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    B, T, H, K, D = 2, 200, 4, 2, 72
+    wide = normal(gen, B, T, (H + 2 * K) * D).requires_grad_()
+    q, k, v = (t.unflatten(-1, (-1, D)) for t in wide.split([H * D, K * D, K * D], -1))
+    out = pkg.fused_attention(q, k, v, causal=True)
+    plain = pkg.fused_attention(q.detach().contiguous(), k.detach().contiguous(),
+                                v.detach().contiguous(), causal=True)
+    assert torch.equal(out, plain)
+    turned = [t.detach().transpose(1, 2).contiguous().transpose(1, 2) for t in (q, k, v)]
+    assert torch.equal(pkg.fused_attention(*turned, causal=True), plain)
+    out.sum().backward()  # its gradient is one element, expanded
+    leaves = [t.detach().clone().requires_grad_() for t in (q, k, v)]
+    pkg.fused_attention(*leaves, causal=True).backward(torch.ones_like(plain))
+    want = torch.cat([t.grad.flatten(2) for t in leaves], -1)
+    assert torch.equal(wide.grad, want)
+
+
+def test_copies_what_cannot_be_read_in_place(pkg):
+    q, k, v = inputs(18, 2, 50, 50, 2, 2, 64, BF)
+    out = pkg.fused_attention(q, k, v)
+    odd = [torch.empty(t.numel() + 1, dtype=BF, device="cuda")[1:].view(t.shape).copy_(t)
+           for t in (q, k, v)]
+    assert torch.equal(pkg.fused_attention(*odd), out)
+    one = k[:, :, :1]
+    assert torch.equal(pkg.fused_attention(q, one.expand(-1, -1, 2, -1), v[:, :, :1].expand(-1, -1, 2, -1)),
+                       pkg.fused_attention(q, one, v[:, :, :1]))
+
+
+def test_differences(pkg):
+    """The gradient against central differences of the forward, along the gradient.
+
+    What they may differ by is what the definition's own differ by in float64 (the
+    step's third-order term) and what the outputs' errors add up to, each weighted by
+    the loss's |g|, and the gradient's own."""
+    T, H, D = 64, 2, 32
+    q, k, v = inputs(19, 1, T, T, H, H, D, HF)
+    gen = torch.Generator(device="cuda").manual_seed(20)
+    g = normal(gen, *q.shape, dtype=HF, std=0.1)
+    out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
+    grads = pkg.attention_bwd(g, q, k, v, out, lse)
+    seen = visible(T, T, False, T)
+    wide = [t[0].double().requires_grad_() for t in (q, k, v)]
+    ref, ref_lse = definition(*wide, D ** -0.5, seen)[:2]
+    exact = torch.autograd.grad(ref, wide, g[0].double())
+    bounds = definition_bwd(g[0], q[0], k[0], v[0], out[0], D ** -0.5, seen, ref_lse.detach())
+    for i in range(3):
+        d = grads[i].double() / grads[i].double().norm()
+        moved, ours, theirs, rounding = [], [], [], 0.0
+        for sign in (1, -1):
+            at = [q, k, v]
+            at[i] = (at[i].double() + sign * d).to(HF)
+            moved.append(at[i][0].double())
+            ours.append(pkg.attention_fwd(*at)[0][0].double())
+            right, _, bound, _ = definition(*[t[0] for t in at], D ** -0.5, seen)
+            theirs.append(right)
+            rounding += (bound * g[0].abs()).sum()
+        step = moved[0] - moved[1]
+        change = ((ours[0] - ours[1]) * g[0].double()).sum()
+        truth = ((theirs[0] - theirs[1]) * g[0].double()).sum()
+        along = (step * grads[i][0].double()).sum()
+        curve = (truth - (step * exact[i]).sum()).abs()
+        slack = (step.abs() * bounds[i][1]).sum()
+        assert curve <= 0.2 * along.abs()  # the step is small enough to tell
+        assert (change - along).abs() <= curve + rounding + slack
+
+
+def test_repeats_bit_for_bit(pkg):
+    q, k, v = inputs(21, 2, 1030, 1030, 8, 2, 128, BF)
+    g = normal(torch.Generator(device="cuda").manual_seed(22), *q.shape)
+    first = None
+    for _ in range(3):
+        out, lse = pkg.attention_fwd(q, k, v, causal=True, want_stats=True)
+        all_ = (out, lse, *pkg.attention_bwd(g, q, k, v, out, lse, causal=True))
+        first = first or all_
+        assert all(torch.equal(x, y) for x, y in zip(first, all_))
+
+
+def test_no_queries_and_no_keys(pkg):
+    q, k, v = inputs(23, 2, 0, 30, 2, 2, 64, BF)
+    out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
+    assert out.shape == q.shape
+    dq, dk, dv = pkg.attention_bwd(out, q, k, v, out, lse)
+    assert dq.shape == q.shape and (dk == 0).all() and (dv == 0).all()
+    q, k, v = inputs(24, 2, 30, 0, 2, 2, 64, BF)
+    out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
+    dq, dk, dv = pkg.attention_bwd(out, q, k, v, out, lse)
+    assert (out == 0).all() and (dq == 0).all() and dk.shape == k.shape
