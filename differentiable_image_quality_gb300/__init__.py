@@ -59,6 +59,7 @@ from ._abi import SAME, VALID, GbssimError
 from ._attention import attention_bwd, attention_fwd, fused_attention
 from ._grad_clip import clip_grad_norm_, clip_grads, grad_norm
 from ._residual_norm import fused_residual_norm, residual_norm_bwd, residual_norm_fwd
+from ._rotary import fused_rotary, rotary, rotary_frequencies
 
 __all__ = [
     "fused_ssim",
@@ -80,6 +81,9 @@ __all__ = [
     "fused_residual_norm",
     "residual_norm_fwd",
     "residual_norm_bwd",
+    "rotary_frequencies",
+    "rotary",
+    "fused_rotary",
     "fused_attention",
     "attention_fwd",
     "attention_bwd",

@@ -54,6 +54,7 @@ SIGNATURES = {
     "gbssim_residual_norm_fwd": (_i, [_vp, _vp, _vp, _fp, _vp]),
     "gbssim_residual_norm_workspace_bytes": (_sz, [_vp]),
     "gbssim_residual_norm_bwd": (_i, [_vp, _vp, _vp, _fp, _vp, _vp, _sz, _vp]),
+    "gbssim_rotary_turn": (_i, [_vp, _vp, _vp, _vp]),
     "gbssim_attention_workspace_bytes": (_sz, [_vp, _i]),
     "gbssim_attention_fwd": (_i, [_vp, _vp, _fp, _vp, _sz, _vp]),
     "gbssim_attention_bwd": (_i, [_vp, _vp, _vp, _fp, _vp, _vp, _vp, _vp, _sz, _vp]),

@@ -150,21 +150,19 @@ def attention_bwd(g_out, q, k, v, out, lse, *, causal=False, scale=None, kv_leng
     desc, kept, index = _describe(q, k, v, causal, scale, kv_lengths, offsets, kv_offsets)
     _like("g_out", g_out, index, q.shape, q.dtype)
     _like("out", out, index, q.shape, q.dtype)
-    if not out.is_contiguous():
-        raise ValueError("out must be the forward's: contiguous")
     if not isinstance(lse, torch.Tensor) or lse.get_device() != index or \
             lse.dtype != torch.float32 or lse.shape != _stats_shape(q) or \
             not lse.is_contiguous():
         raise ValueError(f"lse must be the forward's: contiguous float32 {_stats_shape(q)}")
     lib = _abi.load()
     with _memory.on_device(index):
-        g_out = _as_read(g_out)
+        g_out, out = _as_read(g_out), _as_read(out)
         grads = [torch.empty(t.shape, dtype=t.dtype, device=t.device) if n else None
                  for t, n in zip((q, k, v), needs)]
         nbytes = lib.gbssim_attention_workspace_bytes(desc, 1)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        st = lib.gbssim_attention_bwd(desc, _HEADS.pack(*_heads(g_out)), out.data_ptr(),
-                                      lse.data_ptr(), *[_abi.ptr(g) for g in grads], ws.data_ptr(),
+        st = lib.gbssim_attention_bwd(desc, _HEADS.pack(*_heads(g_out)),
+                                      _HEADS.pack(*_heads(out)), lse.data_ptr(), *[_abi.ptr(g) for g in grads], ws.data_ptr(),
                                       nbytes, _memory.stream_of(index))
     _abi.check("gbssim_attention_bwd", st)
     return tuple(grads)

@@ -174,7 +174,8 @@ struct AttnBwdArgs {
     unsigned extra;  // test hook, see gbssim_tune_attention
     // for the row sums
     const void *out, *g_data, *v_data;
-    long long g_batch, g_token, g_head, v_batch, v_token, v_head;  // strides, elements
+    long long o_batch, o_token, o_head;  // strides, elements
+    long long g_batch, g_token, g_head, v_batch, v_token, v_head;
     const float *lse;
     void *dq, *dk, *dv;      // each may be null
     float *stats;            // [heads][q_tiles][2][128]

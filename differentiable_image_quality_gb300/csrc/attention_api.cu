@@ -219,7 +219,7 @@ extern "C" int gbssim_attention_fwd(const gbssim_attention *d, void *out, float 
     return cuda_fail(e);
 }
 
-extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_heads *grad_out, const void *out,
+extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_heads *grad_out, const gbssim_heads *out,
                                     const float *lse, void *grad_q_or_null, void *grad_k_or_null,
                                     void *grad_v_or_null, void *workspace, size_t workspace_bytes, void *stream)
 {
@@ -228,10 +228,11 @@ extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_head
     if (rc != GBSSIM_OK) return rc;
     const bool queries = q_rows(*d) > 0, keys = k_rows(*d) > 0;
     if (!queries && !keys) return GBSSIM_OK;
-    if (!grad_out || (queries && (!out || !lse))) return GBSSIM_EINVAL;
-    if ((rc = check_heads(*d, *grad_out, d->q_tokens, d->heads))) return rc;
-    for (const void *p : {out, static_cast<const void *>(grad_q_or_null), static_cast<const void *>(grad_k_or_null),
-                          static_cast<const void *>(grad_v_or_null)})
+    if (!grad_out || !out || (queries && !lse)) return GBSSIM_EINVAL;
+    if ((rc = check_heads(*d, *grad_out, d->q_tokens, d->heads)) ||
+        (rc = check_heads(*d, *out, d->q_tokens, d->heads)))
+        return rc;
+    for (const void *p : {grad_q_or_null, grad_k_or_null, grad_v_or_null})
         if (!multiple16(p)) return GBSSIM_EALIGN;
     if (reinterpret_cast<uintptr_t>(lse) % 4) return GBSSIM_EALIGN;
     const size_t need = queries ? bwd_bytes(*d) : 0;
@@ -240,7 +241,7 @@ extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_head
                           heads_extent(*d, d->k, d->k_tokens, d->kv_heads),
                           heads_extent(*d, d->v, d->k_tokens, d->kv_heads),
                           heads_extent(*d, *grad_out, d->q_tokens, d->heads),
-                          dense_extent(*d, out, q_rows(*d), d->heads), floats(*d, lse)};
+                          heads_extent(*d, *out, d->q_tokens, d->heads), floats(*d, lse)};
     const Extent outs[4] = {dense_extent(*d, grad_q_or_null, q_rows(*d), d->heads),
                             dense_extent(*d, grad_k_or_null, k_rows(*d), d->kv_heads),
                             dense_extent(*d, grad_v_or_null, k_rows(*d), d->kv_heads),
@@ -268,7 +269,10 @@ extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_head
     a.k_tiles = int(k_tiles);
     a.ragged = s.packed || s.kv_lengths;
     a.extra = g_extra;
-    a.out = out;
+    a.out = out->data;
+    a.o_batch = out->batch_stride;
+    a.o_token = out->token_stride;
+    a.o_head = out->head_stride;
     a.g_data = grad_out->data;
     a.g_batch = grad_out->batch_stride;
     a.g_token = grad_out->token_stride;

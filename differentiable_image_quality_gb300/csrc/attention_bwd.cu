@@ -114,8 +114,8 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
         const int t = pl.tile * kAttnTile + r;
         float sum = 0.0f;
         if (mine && t < pl.queries) {
-            const long long row = (long long)pl.batch * s.q_tokens + pl.q_row + t;
-            const T *const o = static_cast<const T *>(a.out) + (row * s.heads + head) * s.dim + lane * 8;
+            const T *const o = static_cast<const T *>(a.out) + pl.batch * a.o_batch +
+                               (long long)(pl.q_row + t) * a.o_token + head * a.o_head + lane * 8;
             const T *const g = static_cast<const T *>(a.g_data) + pl.batch * a.g_batch +
                                (long long)(pl.q_row + t) * a.g_token + head * a.g_head + lane * 8;
             Raw8<T> ro, rg;

@@ -38,10 +38,17 @@ inline bool encode_heads_map(CUtensorMap &m, const void *data, bool bf, int dim,
                                    cuuint64_t(batch_stride) * 2};
     const cuuint32_t box[4] = {64, cuuint32_t(box_heads), cuuint32_t(box_tokens), 1};
     const cuuint32_t steps[4] = {1, 1, 1, 1};
-    return encode(&m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                  const_cast<void *>(data), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const auto once = [&] {
+        return encode(&m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                      const_cast<void *>(data), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (once()) return true;
+    // a host thread that has not used the device yet (autograd's, before its first
+    // launch) has no current context, which this driver call does not make by itself
+    int device = 0;
+    return cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess && once();
 }
 
 }  // namespace gbssim

@@ -372,6 +372,50 @@ int gbssim_residual_norm_bwd(const gbssim_residual_norm *desc,
                              const gbssim_residual_norm_grads *grads, void *workspace,
                              size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------- rotary positions --- */
+/* A [batch, tokens, heads, dim] tensor, strides in elements (the batch's is unused in
+ * the packed form). */
+typedef struct {
+    const void *data;
+    long long batch_stride, token_stride, head_stride;
+} gbssim_heads;
+
+/* Positions as rotations: the head's columns form pairs, pair p of axis a(p) turns by
+ * the angle x f_p, x the token's position on that axis (a patch's row or column, a
+ * frame's time, a voxel's coordinates) and f_p its frequency:
+ *   (u, v) -> (u cos - v sin, u sin + v cos),   with inverse != 0 by the negative angle,
+ * which undoes it and is its gradient.  The pairs of the axes follow one another: n =
+ * pairs[0] + ... in all, 2 n <= dim; GBSSIM_ROTARY_HALF pairs columns p and p + n,
+ * GBSSIM_ROTARY_ADJACENT 2 p and 2 p + 1.  Columns from 2 n on are copied.
+ *
+ * Angles are taken modulo a turn in 64-bit fixed point, to within the rounding of
+ * f_p / (2 pi) to float64 times the position: far positions are as exact as near ones.
+ * A float32 position that is NaN, infinite or above 9e18 makes its token's turned
+ * columns of that axis NaN.  Results are rounded once from float32.
+ *
+ * Shapes: batch x tokens tokens (0 and 1 included), dim from 2 to 512, up to 65535
+ * heads in each of two tensors that share their positions (queries and keys; 0 heads:
+ * absent), any non-negative strides, the columns of a head side by side.  Outputs are
+ * dense [batch, tokens, heads, dim] and must not overlap any input. */
+#define GBSSIM_ROTARY_AXES 4
+typedef enum { GBSSIM_POS_I32 = 0, GBSSIM_POS_I64 = 1, GBSSIM_POS_F32 = 2 } gbssim_pos_type;
+typedef enum { GBSSIM_ROTARY_HALF = 0, GBSSIM_ROTARY_ADJACENT = 1 } gbssim_rotary_layout;
+
+typedef struct {
+    int batch, tokens, q_heads, k_heads, dim;
+    int dtype;                     /* gbssim_dtype */
+    int layout, inverse;
+    int axes, pairs[GBSSIM_ROTARY_AXES];
+    int pos_type;
+    gbssim_heads q, k;
+    const void *positions;         /* device, [batch, tokens, axes], an axis after the other */
+    long long pos_batch_stride, pos_token_stride; /* elements, >= 0 */
+    const double *frequencies;     /* device, [n]: radians for one unit of position */
+} gbssim_rotary;
+
+/* One launch; no workspace. */
+int gbssim_rotary_turn(const gbssim_rotary *desc, void *q_out, void *k_out, void *stream);
+
 /* ------------------------------------------------------------ attention --- */
 /* Attention between the tokens of a batch, per head:
  *   s_ij = scale q_i . k_j,   p_ij = exp(s_ij - lse_i),   o_i = sum_j p_ij v_j,
@@ -404,13 +448,6 @@ int gbssim_residual_norm_bwd(const gbssim_residual_norm *desc,
  * 128.  Inputs have any positive strides that are multiples of 16 bytes, the
  * elements of a head side by side, and start on 16 bytes; outputs are dense. */
 
-/* A [batch, tokens, heads, dim] tensor, strides in elements (the batch's is unused in
- * the packed form). */
-typedef struct {
-    const void *data;
-    long long batch_stride, token_stride, head_stride;
-} gbssim_heads;
-
 typedef struct {
     int sequences, q_tokens, k_tokens;
     int heads, kv_heads, dim;
@@ -432,18 +469,18 @@ size_t gbssim_attention_workspace_bytes(const gbssim_attention *desc, int backwa
 int gbssim_attention_fwd(const gbssim_attention *desc, void *out, float *lse_or_null,
                          void *workspace, size_t workspace_bytes, void *stream);
 
-/* Backward from the gradient of out (any strides that q may have):
+/* Backward from the gradient of out and out itself (any strides that q may have):
  *   p_ij as above, from lse;  D_i = grad_out_i . out_i;
  *   ds_ij = p_ij (grad_out_i . v_j - D_i),
  *   grad_q_i = scale sum_j ds_ij k_j,  grad_k_j = scale sum_i ds_ij q_i,
  *   grad_v_j = sum_i p_ij grad_out_i,
  * the last two over all query heads that share the key head.  desc is the forward's,
- * out and lse what it wrote.  Outputs are dense, of q's, k's and v's shapes, and
+ * out and lse are what it wrote.  Outputs are dense, of q's, k's and v's shapes, and
  * overwritten; NULL: not wanted.  p and ds are rounded to the tensors' type for their
  * products (in float16 times powers of two that keep small gradients), sums are
  * float32. */
-int gbssim_attention_bwd(const gbssim_attention *desc, const gbssim_heads *grad_out, const void *out,
-                         const float *lse, void *grad_q_or_null, void *grad_k_or_null,
+int gbssim_attention_bwd(const gbssim_attention *desc, const gbssim_heads *grad_out,
+                         const gbssim_heads *out, const float *lse, void *grad_q_or_null, void *grad_k_or_null,
                          void *grad_v_or_null, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus

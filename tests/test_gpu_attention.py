@@ -416,3 +416,28 @@ def test_no_queries_and_no_keys(pkg):
     out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
     dq, dk, dv = pkg.attention_bwd(out, q, k, v, out, lse)
     assert (out == 0).all() and (dq == 0).all() and dk.shape == k.shape
+
+
+def test_backward_first_on_a_new_thread(pkg):
+    """A host thread whose first use of the device is the backward, as autograd's may be."""
+    import threading
+
+    q, k, v = inputs(25, 1, 64, 64, 2, 2, 64, BF)
+    out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
+    want = pkg.attention_bwd(out, q, k, v, out, lse)
+    got = []
+    t = threading.Thread(target=lambda: got.extend(pkg.attention_bwd(out, q, k, v, out, lse)))
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(got) == 3
+
+
+def test_output_strides(pkg):
+    """The backward takes the output at any strides."""
+    q, k, v = inputs(26, 2, 70, 70, 4, 2, 72, BF)
+    out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
+    turned = out.transpose(1, 2).contiguous().transpose(1, 2)
+    for a, b in zip(pkg.attention_bwd(out, q, k, v, out, lse),
+                    pkg.attention_bwd(turned, q, k, v, turned, lse)):
+        assert torch.equal(a, b)
