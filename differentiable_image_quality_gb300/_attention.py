@@ -9,6 +9,7 @@ import torch
 from . import _abi, _memory
 
 _MAX_DIM = 128
+_CODES = {t: _abi.DTYPES[t] for t in (torch.bfloat16, torch.float16)}
 
 # gbssim_attention
 _DESC = struct.Struct("@8if" + "Pqqq" * 3 + "PPP")
@@ -16,35 +17,41 @@ _HEADS = struct.Struct("@Pqqq")  # gbssim_heads
 _NO_TENSOR = (0, 0, 0, 0)
 
 
-def _check(name: str, t, index, dtype) -> None:
+def _refuse(name: str, t, index, dtype) -> None:
+    """Why t is no tensor of dtype (None: bfloat16 or float16) on device index."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if index is not None and t.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     if dtype is None:
-        if t.dtype not in (torch.bfloat16, torch.float16):
-            raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-    elif t.dtype != dtype:
-        raise TypeError(f"{name} must have the type of q, {dtype}, got {t.dtype}")
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    raise TypeError(f"{name} must have the type of q, {dtype}, got {t.dtype}")
 
 
-def _as_read(t: torch.Tensor) -> torch.Tensor:
-    """t where the copy unit can read it in place, else a dense copy: heads side by side
-    in memory, strides and address multiples of 16 bytes, no element twice."""
-    shape, stride = t.shape, t.stride()
-    if t.numel() == 0 or (stride[-1] == 1 and t.data_ptr() % 16 == 0 and
-                          all(n == 1 or (s > 0 and s % 8 == 0)
-                              for n, s in zip(shape[:-1], stride[:-1]))):
-        return t
-    return t.clone(memory_format=torch.contiguous_format)
-
-
-def _heads(t: torch.Tensor) -> tuple:
-    """(address, batch, token and head stride)."""
-    if t.numel() == 0:
+def _place(t: torch.Tensor, kept: list) -> tuple:
+    """(address, batch, token and head stride) of t where the copy unit can read it in
+    place, else of a dense copy, which goes to ``kept``: a head's elements side by side,
+    strides and address multiples of 16 bytes, no element twice."""
+    shape, stride, at = t.shape, t.stride(), t.data_ptr()
+    if len(shape) == 4:
+        n, tokens, heads, dim = shape
+        batch, token, head, one = stride
+    else:
+        n, batch = 1, 0
+        tokens, heads, dim = shape
+        token, head, one = stride
+    if at % 16 == 0 and one == 1 and (token | head | batch) % 8 == 0 and \
+            token > 0 and head > 0 and (batch > 0 or n == 1):
+        return at, batch, token, head
+    if n == 0 or tokens == 0:
         return _NO_TENSOR
-    s = t.stride()
-    return t.data_ptr(), (s[0] if len(s) == 4 else 0), s[-3], s[-2]
+    # the stride along a single element counts for nothing
+    if at % 16 or one != 1 or any(m > 1 and (s < 1 or s % 8) for m, s in
+                                  ((n, batch), (tokens, token), (heads, head))):
+        t = t.clone(memory_format=torch.contiguous_format)
+        kept.append(t)
+        return t.data_ptr(), tokens * heads * dim, heads * dim, dim
+    return at, batch, token, head
 
 
 def _counts(name: str, t, index, n) -> int:
@@ -58,26 +65,28 @@ def _counts(name: str, t, index, n) -> int:
     return t.data_ptr()
 
 
-def _describe(q, k, v, causal, scale, kv_lengths, offsets, kv_offsets):
-    """(packed description, the tensors it points to, device index), all checked."""
-    _check("q", q, None, None)
-    index = q.get_device()
-    _check("k", k, index, q.dtype)
-    _check("v", v, index, q.dtype)
+def _describe(q, k, v, causal, scale, kv_lengths, offsets, kv_offsets, kept):
+    """(packed description, device index), all checked; copies it points to go to
+    ``kept``."""
+    code = _CODES.get(q.dtype) if isinstance(q, torch.Tensor) and q.is_cuda else None
+    if code is None:
+        _refuse("q", q, None, None)
+    index, dtype = q.get_device(), q.dtype
+    for name, t in (("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype != dtype:
+            _refuse(name, t, index, dtype)
     packed = offsets is not None
-    ndim = 3 if packed else 4
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dim() != ndim:
-            raise ValueError(f"{name} must have {ndim} dimensions, "
-                             f"[{'' if packed else 'batch, '}tokens, heads, dim], "
-                             f"got {tuple(t.shape)}")
-    if k.shape != v.shape:
-        raise ValueError(f"k and v must have one shape, got {tuple(k.shape)} and {tuple(v.shape)}")
-    heads, dim = q.shape[-2:]
-    kv_heads = k.shape[-2]
-    if k.shape[-1] != dim or (not packed and k.shape[0] != q.shape[0]):
-        raise ValueError(f"q, k and v must agree in batch and dim, got {tuple(q.shape)} and "
-                         f"{tuple(k.shape)}")
+    q_shape, k_shape = q.shape, k.shape
+    if k_shape != v.shape:
+        raise ValueError(f"k and v must have one shape, got {tuple(k_shape)} and {tuple(v.shape)}")
+    if len(q_shape) != (3 if packed else 4) or len(k_shape) != len(q_shape):
+        raise ValueError(f"q, k and v must be [{'' if packed else 'batch, '}tokens, heads, dim], "
+                         f"got {tuple(q_shape)} and {tuple(k_shape)}")
+    tokens, heads, dim = q_shape[-3:]
+    keys, kv_heads, k_dim = k_shape[-3:]
+    if k_dim != dim or (not packed and k_shape[0] != q_shape[0]):
+        raise ValueError(f"q, k and v must agree in batch and dim, got {tuple(q_shape)} and "
+                         f"{tuple(k_shape)}")
     if dim % 8 or not 8 <= dim <= _MAX_DIM:
         raise ValueError(f"dim must be a multiple of 8 up to {_MAX_DIM}, got {dim}")
     if kv_heads < 1 or heads < 1 or heads % kv_heads:
@@ -93,7 +102,7 @@ def _describe(q, k, v, causal, scale, kv_lengths, offsets, kv_offsets):
         if offsets.shape[0] < 1:
             raise ValueError("offsets must have at least one element")
         if kv_offsets is None:
-            if k.shape[0] != q.shape[0]:
+            if keys != tokens:
                 raise ValueError("without kv_offsets, k has the rows of q")
             kv_offsets = offsets
         k_off = _counts("kv_offsets", kv_offsets, index, offsets.shape[0])
@@ -101,14 +110,12 @@ def _describe(q, k, v, causal, scale, kv_lengths, offsets, kv_offsets):
     else:
         if kv_offsets is not None:
             raise ValueError("kv_offsets need offsets")
-        sequences = q.shape[0]
+        sequences = q_shape[0]
         if kv_lengths is not None:
             lengths = _counts("kv_lengths", kv_lengths, index, sequences)
-    q, k, v = _as_read(q), _as_read(k), _as_read(v)
-    desc = _DESC.pack(sequences, q.shape[-3], k.shape[-3], heads, kv_heads, dim,
-                      _abi.DTYPES[q.dtype], bool(causal), scale, *_heads(q), *_heads(k),
-                      *_heads(v), lengths, q_off, k_off)
-    return desc, (q, k, v), index
+    return _DESC.pack(sequences, tokens, keys, heads, kv_heads, dim, code, bool(causal), scale,
+                      *_place(q, kept), *_place(k, kept), *_place(v, kept), lengths, q_off,
+                      k_off), index
 
 
 def _stats_shape(q) -> tuple:
@@ -122,24 +129,27 @@ def attention_fwd(q, k, v, *, causal=False, scale=None, kv_lengths=None, offsets
     Returns (out, lse): out dense, of q's shape and type; lse, with want_stats, the
     logarithm of each row's sum of exponentials, float32 [batch, heads, tokens]
     ([heads, rows] of a packed batch), which attention_bwd needs; else None."""
-    desc, kept, index = _describe(q, k, v, causal, scale, kv_lengths, offsets, kv_offsets)
+    kept = []
+    desc, index = _describe(q, k, v, causal, scale, kv_lengths, offsets, kv_offsets, kept)
     lib = _abi.load()
     with _memory.on_device(index):
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _memory.empty_like(q)
         lse = torch.empty(_stats_shape(q), dtype=torch.float32, device=q.device) \
             if want_stats else None
         nbytes = lib.gbssim_attention_workspace_bytes(desc, 0)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
         st = lib.gbssim_attention_fwd(desc, out.data_ptr(), _abi.ptr(lse), _abi.ptr(ws), nbytes,
                                       _memory.stream_of(index))
-    _abi.check("gbssim_attention_fwd", st)
+    if st:
+        _abi.check("gbssim_attention_fwd", st)
     return out, lse
 
 
-def _like(name, t, index, shape, dtype):
-    _check(name, t, index, dtype)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _like(name, t, index, q):
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or t.dtype != q.dtype:
+        _refuse(name, t, index, q.dtype)
+    if t.shape != q.shape:
+        raise ValueError(f"{name} must have shape {tuple(q.shape)}, got {tuple(t.shape)}")
 
 
 def attention_bwd(g_out, q, k, v, out, lse, *, causal=False, scale=None, kv_lengths=None,
@@ -147,24 +157,24 @@ def attention_bwd(g_out, q, k, v, out, lse, *, causal=False, scale=None, kv_leng
     """The backward without autograd: from the gradient of out, the forward's arguments
     and what it returned (out and lse), the gradients of (q, k, v), dense, of their
     types and shapes; None where ``needs`` is false."""
-    desc, kept, index = _describe(q, k, v, causal, scale, kv_lengths, offsets, kv_offsets)
-    _like("g_out", g_out, index, q.shape, q.dtype)
-    _like("out", out, index, q.shape, q.dtype)
+    kept = []
+    desc, index = _describe(q, k, v, causal, scale, kv_lengths, offsets, kv_offsets, kept)
+    _like("g_out", g_out, index, q)
+    _like("out", out, index, q)
     if not isinstance(lse, torch.Tensor) or lse.get_device() != index or \
             lse.dtype != torch.float32 or lse.shape != _stats_shape(q) or \
             not lse.is_contiguous():
         raise ValueError(f"lse must be the forward's: contiguous float32 {_stats_shape(q)}")
     lib = _abi.load()
     with _memory.on_device(index):
-        g_out, out = _as_read(g_out), _as_read(out)
-        grads = [torch.empty(t.shape, dtype=t.dtype, device=t.device) if n else None
-                 for t, n in zip((q, k, v), needs)]
+        g, o = _HEADS.pack(*_place(g_out, kept)), _HEADS.pack(*_place(out, kept))
+        grads = [_memory.empty_like(t) if n else None for t, n in zip((q, k, v), needs)]
         nbytes = lib.gbssim_attention_workspace_bytes(desc, 1)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        st = lib.gbssim_attention_bwd(desc, _HEADS.pack(*_heads(g_out)),
-                                      _HEADS.pack(*_heads(out)), lse.data_ptr(), *[_abi.ptr(g) for g in grads], ws.data_ptr(),
-                                      nbytes, _memory.stream_of(index))
-    _abi.check("gbssim_attention_bwd", st)
+        st = lib.gbssim_attention_bwd(desc, g, o, lse.data_ptr(), *map(_abi.ptr, grads),
+                                      ws.data_ptr(), nbytes, _memory.stream_of(index))
+    if st:
+        _abi.check("gbssim_attention_bwd", st)
     return tuple(grads)
 
 

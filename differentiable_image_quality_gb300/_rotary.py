@@ -1,6 +1,7 @@
 """Rotary positions with several axes: torch tensors to gbssim_rotary_turn."""
 from __future__ import annotations
 
+import operator
 import struct
 
 import torch
@@ -14,6 +15,7 @@ _MAX_AXES, _MAX_DIM = 4, 512
 # gbssim_rotary
 _DESC = struct.Struct("@14i" + "Pqqq" * 2 + "PqqP")
 _NO_TENSOR = (0, 0, 0, 0)
+_NO_PAIRS = (0,) * _MAX_AXES
 
 
 def rotary_frequencies(pairs, base: float = 10000.0, device=None) -> torch.Tensor:
@@ -45,7 +47,7 @@ def _heads(name: str, t) -> tuple:
     if t is None:
         return _NO_TENSOR
     s = t.stride()
-    if t.shape[-1] > 1 and s[-1] != 1 and t.numel():
+    if s[-1] != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError(f"the last dimension of {name} must have stride 1, got {s}")
     return t.data_ptr(), (s[0] if len(s) == 4 else 0), s[-3], s[-2]
 
@@ -60,22 +62,25 @@ def _describe(q, k, positions, frequencies, pairs, layout, inverse):
         way = _LAYOUTS[layout]
     except (KeyError, TypeError):
         raise ValueError(f"layout must be 'half' or 'adjacent', got {layout!r}") from None
-    pairs = tuple(int(n) for n in pairs)
-    n, dim, axes = sum(pairs), q.shape[-1], len(pairs)
+    shape = q.shape
+    tokens, heads, dim = shape[-3:]
+    pairs = [operator.index(m) for m in pairs]
+    n, axes = sum(pairs), len(pairs)
     if not 1 <= axes <= _MAX_AXES or min(pairs) < 1:
         raise ValueError(f"pairs must be one to {_MAX_AXES} positive numbers, got {pairs}")
     if not 2 <= dim <= _MAX_DIM or 2 * n > dim:
         raise ValueError(f"dim must be at most {_MAX_DIM} and hold {n} pairs, got {dim}")
-    if not isinstance(positions, torch.Tensor) or positions.dtype not in _POSITIONS:
+    kind = _POSITIONS.get(positions.dtype) if isinstance(positions, torch.Tensor) else None
+    if kind is None:
         raise TypeError("positions must be an int32, int64 or float32 CUDA tensor")
     if positions.get_device() != index:
         raise ValueError(f"positions must be on cuda:{index}, got {positions.device}")
-    batch, tokens = (q.shape[0] if q.dim() == 4 else 1), q.shape[-3]
-    shape = positions.shape
-    if shape[-1:] != (axes,) or tuple(shape[:-1]) not in ((tokens,), tuple(q.shape[:-2])):
+    at = positions.shape
+    if at != (tokens, axes) and at != (*shape[:-2], axes):
         raise ValueError(f"positions must have shape ({tokens}, {axes}) or "
-                         f"{(*q.shape[:-2], axes)}, got {tuple(shape)}")
-    if axes > 1 and positions.stride(-1) != 1 and positions.numel():
+                         f"{(*shape[:-2], axes)}, got {tuple(at)}")
+    steps = positions.stride()
+    if steps[-1] != 1 and axes > 1 and positions.numel():
         raise ValueError("the last dimension of positions must have stride 1")
     if not isinstance(frequencies, torch.Tensor) or frequencies.dtype != torch.float64:
         raise TypeError("frequencies must be a float64 CUDA tensor")
@@ -84,13 +89,11 @@ def _describe(q, k, positions, frequencies, pairs, layout, inverse):
     if frequencies.shape != (n,) or not frequencies.is_contiguous():
         raise ValueError(f"frequencies must be contiguous of shape ({n},), got "
                          f"{tuple(frequencies.shape)}")
-    desc = _DESC.pack(batch, tokens, q.shape[-2], 0 if k is None else k.shape[-2], dim,
-                      _abi.DTYPES[q.dtype], way, bool(inverse), axes,
-                      *pairs, *(0,) * (_MAX_AXES - axes), _POSITIONS[positions.dtype],
-                      *_heads("q", q), *_heads("k", k), positions.data_ptr(),
-                      positions.stride(0) if len(shape) == 3 else 0, positions.stride(-2),
-                      frequencies.data_ptr())
-    return desc, index
+    return _DESC.pack(shape[0] if len(shape) == 4 else 1, tokens, heads,
+                      0 if k is None else k.shape[-2], dim, _abi.DTYPES[q.dtype], way,
+                      bool(inverse), axes, *pairs, *_NO_PAIRS[axes:], kind, *_heads("q", q),
+                      *_heads("k", k), positions.data_ptr(), steps[0] if len(at) == 3 else 0,
+                      steps[-2], frequencies.data_ptr()), index
 
 
 def rotary(q, k, positions, frequencies, pairs, *, layout="half", inverse=False):
@@ -99,11 +102,12 @@ def rotary(q, k, positions, frequencies, pairs, *, layout="half", inverse=False)
     outputs' gradients to its inputs'."""
     desc, index = _describe(q, k, positions, frequencies, pairs, layout, inverse)
     with _memory.on_device(index):
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        q_out = _memory.empty_like(q)
+        k_out = None if k is None else _memory.empty_like(k)
         st = _abi.load().gbssim_rotary_turn(desc, q_out.data_ptr(), _abi.ptr(k_out),
                                             _memory.stream_of(index))
-    _abi.check("gbssim_rotary_turn", st)
+    if st:
+        _abi.check("gbssim_rotary_turn", st)
     return q_out, k_out
 
 

@@ -5,6 +5,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "dtypes.cuh"
@@ -140,6 +141,20 @@ __device__ __forceinline__ bool attn_wait(uint64_t *bar, unsigned parity, volati
 __device__ __forceinline__ bool attn_wait_warp(uint64_t *bar, unsigned parity, volatile unsigned *failed)
 {
     return __all_sync(0xffffffffu, attn_wait(bar, parity, failed));
+}
+
+// A kernel's shared memory, asked for once on each device (1.5 us a call otherwise).
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel kernel, std::atomic<unsigned long long> &done, size_t bytes)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // ------------------------------------------------------------------- forward

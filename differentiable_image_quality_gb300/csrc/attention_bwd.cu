@@ -692,8 +692,8 @@ cudaError_t launch(const AttnBwdArgs &a, cudaStream_t stream)
 {
     constexpr size_t smem = bwd_smem<DP>();
     static_assert(smem <= 232448, "a block's shared memory");
-    cudaError_t e = cudaFuncSetAttribute(attention_bwd_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         int(smem));
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(attention_bwd_kernel<T, DP>, done, smem);
     if (e != cudaSuccess) return e;
     if (kScaled<T> && a.largest) {
         e = cudaMemsetAsync(a.largest, 0, size_t(2) * a.s.kv_heads * sizeof(unsigned), stream);

@@ -382,8 +382,8 @@ cudaError_t launch(const AttnFwdArgs &a, cudaStream_t stream)
 {
     constexpr size_t smem = fwd_smem<DP, QT>();
     static_assert(smem <= 232448, "a block's shared memory");
-    const cudaError_t e = cudaFuncSetAttribute(attention_fwd_kernel<T, DP, QT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = allow_smem(attention_fwd_kernel<T, DP, QT>, done, smem);
     if (e != cudaSuccess) return e;
     const long long grid = (long long)a.splits * a.tiles * (a.s.packed ? 1 : a.s.sequences) *
                            (a.s.heads / a.tile_heads);
