@@ -16,6 +16,7 @@ namespace gbssim {
 // Queries and keys come in tiles of 128 rows, the lanes of tensor memory.
 constexpr int kAttnTile = 128;
 constexpr int kAttnMaxDim = 128;
+constexpr int kAttnBlocks = 152;  // that run at once: one to an SM
 
 struct AttnShape {
     int sequences;           // samples, or sequences of a packed batch
@@ -167,6 +168,7 @@ struct AttnFwdArgs {
     int tile_tokens;  // tokens of a tile
     int splits;       // parts of the keys
     int tiles;        // of q_tokens (batch form), or the most there can be (packed)
+    unsigned items;   // of all blocks
     int ragged;       // keys may end before the tensor does
     unsigned extra;   // test hook, see gbssim_tune_attention
     void *out;

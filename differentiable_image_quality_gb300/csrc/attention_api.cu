@@ -114,9 +114,6 @@ bool encode(CUtensorMap &m, const gbssim_attention &d, const gbssim_heads &t, in
                             box_heads, box_tokens);
 }
 
-// Blocks that a plan counts on: one to an SM.
-constexpr int kPlanBlocks = 152;
-
 struct FwdPlan {
     int tile_heads, tile_tokens, q_tiles, splits;
     long long tiles;
@@ -134,14 +131,14 @@ FwdPlan plan_fwd(const gbssim_attention &d)
     }
     const long long heads = s.heads / p.tile_heads;
     if (p.tile_heads == 1 && s.q_tokens > kAttnTile &&
-        most_tiles(s, s.q_tokens, 2 * kAttnTile) * heads >= kPlanBlocks)
+        most_tiles(s, s.q_tokens, 2 * kAttnTile) * heads >= kAttnBlocks)
         p.q_tiles = 2;
     const int rows = p.tile_tokens * p.q_tiles;
     p.tiles = s.packed ? most_tiles(s, s.q_tokens, rows) : (s.q_tokens + rows - 1) / rows;
     const long long blocks = p.tiles * samples(d) * heads;
     const long long key_tiles = (s.k_tokens + kAttnTile - 1) / kAttnTile;
-    if (!s.packed && blocks > 0 && 2 * blocks <= kPlanBlocks && key_tiles >= 8)
-        p.splits = int(std::min<long long>(kPlanBlocks / blocks, key_tiles / 4));
+    if (!s.packed && blocks > 0 && 2 * blocks <= kAttnBlocks && key_tiles >= 8)
+        p.splits = int(std::min<long long>(kAttnBlocks / blocks, key_tiles / 4));
     return p;
 }
 
@@ -194,8 +191,8 @@ extern "C" int gbssim_attention_fwd(const gbssim_attention *d, void *out, float 
             if (meet(outs[i], outs[j])) return GBSSIM_EINVAL;
     }
     const AttnShape s = shape_of(*d);
-    const long long grid = p.tiles * samples(*d) * (s.heads / p.tile_heads) * p.splits;
-    if (grid > INT_MAX || q_rows(*d) * d->heads * (d->dim / 8) / 128 >= INT_MAX) return GBSSIM_ESHAPE;
+    const long long items = p.tiles * samples(*d) * (s.heads / p.tile_heads) * p.splits;
+    if (items > INT_MAX || q_rows(*d) * d->heads * (d->dim / 8) / 128 >= INT_MAX) return GBSSIM_ESHAPE;
     AttnFwdArgs a{};
     if (!encode(a.q, *d, d->q, d->q_tokens, d->heads, p.tile_heads, p.tile_tokens) ||
         !encode(a.k, *d, d->k, d->k_tokens, d->kv_heads, 1, kAttnTile) ||
@@ -207,6 +204,7 @@ extern "C" int gbssim_attention_fwd(const gbssim_attention *d, void *out, float 
     a.tile_tokens = p.tile_tokens;
     a.splits = p.splits;
     a.tiles = int(p.tiles);
+    a.items = unsigned(items);
     a.ragged = s.packed || s.kv_lengths;
     a.extra = g_extra;
     a.out = out;

@@ -208,25 +208,6 @@ __device__ __forceinline__ void zero_rows(char *tile, int rows)
             reinterpret_cast<uint4 *>(tile + c * kSlabBytes)[i] = make_uint4(0, 0, 0, 0);
 }
 
-// D = A B^T of two tiles of 128 rows, their columns summed over.
-__device__ __forceinline__ void product_k(unsigned d, unsigned a, unsigned b, int steps, unsigned idesc)
-{
-    for (int i = 0; i < steps; ++i) {
-        const unsigned at = (i / 4) * kSlabBytes + (i % 4) * kStepK;
-        mma(d, desc_k(a + at), desc_k(b + at), idesc, i > 0);
-    }
-}
-
-// D (+)= A B: A [128, 128] in tensor memory, its two halves of 64 columns 64 columns
-// apart, B's rows summed over.
-__device__ __forceinline__ void product_rows(unsigned d, unsigned a, unsigned b, unsigned idesc, bool add)
-{
-    const uint64_t desc = desc_mn(b, kSlabBytes);
-#pragma unroll
-    for (int i = 0; i < kAttnTile / 16; ++i)
-        mma_ta(d, a + (i / 4) * 64 + (i % 4) * 8, advance(desc, i * kStepMn), idesc, add || i > 0);
-}
-
 // 64 values as 32 columns of the A operand.
 template <typename T>
 __device__ __forceinline__ void store_half(unsigned at, const float (&v)[64])
@@ -337,33 +318,34 @@ __device__ void by_keys(const AttnBwdArgs &a, char *base, BwdShared &sh, int kv_
         if (lane == 0 && total > 0) {
             const int steps = (s.dim + 15) / 16;
             const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
-            const unsigned k_u = smem_u32(base), v_u = k_u + kTile, ring_u = smem_u32(ring);
+            const Desc k_tile = desc_k(smem_u32(base)), v_tile = advance(k_tile, kTile);
+            const Desc ring_k = desc_k(smem_u32(ring)), ring_mn = desc_mn(smem_u32(ring));
             bool ok = attn_wait(&sh.own_full, 0, failed) && attn_wait(&sh.full[0], 0, failed);
             if (ok) {
-                product_k(s_at, k_u, ring_u, steps, id_s);
+                product_k<DP / 16>(s_at, k_tile, ring_k, steps, id_s);
                 commit(&sh.s_full[0]);
-                product_k(dp_at, v_u, ring_u + kTile, steps, id_s);
+                product_k<DP / 16>(dp_at, v_tile, advance(ring_k, kTile), steps, id_s);
                 commit(&sh.dp_full);
             }
             for (int it = 0; ok && it < total; ++it) {
-                const unsigned tile = ring_u + 2 * (it % kStages) * kTile;
+                const Desc tile = advance(ring_mn, 2 * (it % kStages) * kTile);
                 const int nx = (it + 1) % kStages;
-                const unsigned next = ring_u + 2 * nx * kTile;
+                const Desc next = advance(ring_k, 2 * nx * kTile);
                 const bool more = it + 1 < total;
                 if (!(ok = attn_wait(&sh.p_full, it & 1, failed))) break;
                 fence_after();
-                product_rows(dv_at, s_at, tile + kTile, id_d, it > 0);
+                product_rows<64>(dv_at, s_at, advance(tile, kTile), id_d, it > 0);
                 if (more) {
                     if (!(ok = attn_wait(&sh.full[nx], ((it + 1) / kStages) & 1, failed))) break;
-                    product_k(s_at, k_u, next, steps, id_s);
+                    product_k<DP / 16>(s_at, k_tile, next, steps, id_s);
                     commit(&sh.s_full[0]);
                 }
                 if (!(ok = attn_wait(&sh.ds_full, it & 1, failed))) break;
                 fence_after();
-                product_rows(dk_at, dp_at, tile, id_d, it > 0);
+                product_rows<64>(dk_at, dp_at, tile, id_d, it > 0);
                 commit(&sh.empty[it % kStages]);
                 if (more) {
-                    product_k(dp_at, v_u, next + kTile, steps, id_s);
+                    product_k<DP / 16>(dp_at, v_tile, advance(next, kTile), steps, id_s);
                     commit(&sh.dp_full);
                 }
             }
@@ -522,20 +504,21 @@ __device__ void by_queries(const AttnBwdArgs &a, char *base, BwdShared &sh, int 
         if (lane == 0 && total > 0) {
             const int steps = (s.dim + 15) / 16;
             const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
-            const unsigned q_u = smem_u32(base), g_u = q_u + kTile, ring_u = smem_u32(ring);
+            const Desc q_tile = desc_k(smem_u32(base)), g_tile = advance(q_tile, kTile);
+            const Desc ring_k = desc_k(smem_u32(ring)), ring_mn = desc_mn(smem_u32(ring));
             const auto wait_tile = [&](int it) {
                 return attn_wait(&sh.full[it % kStages], (it / kStages) & 1, failed);
             };
-            const auto tile_of = [&](int it) { return ring_u + (it % kStages) * kTile; };
+            const auto tile_of = [&](Desc ring, int it) { return advance(ring, (it % kStages) * kTile); };
             const auto scores = [&](int j) {
                 if (!wait_tile(2 * j)) return false;
-                product_k(s_at + (j & 1) * 128, q_u, tile_of(2 * j), steps, id_s);
+                product_k<DP / 16>(s_at + (j & 1) * 128, q_tile, tile_of(ring_k, 2 * j), steps, id_s);
                 commit(&sh.s_full[j & 1]);
                 return true;
             };
             const auto products = [&](int j) {
                 if (!wait_tile(2 * j + 1)) return false;
-                product_k(dp_at, g_u, tile_of(2 * j + 1), steps, id_s);
+                product_k<DP / 16>(dp_at, g_tile, tile_of(ring_k, 2 * j + 1), steps, id_s);
                 commit(&sh.dp_full);
                 commit(&sh.empty[(2 * j + 1) % kStages]);
                 return true;
@@ -545,7 +528,7 @@ __device__ void by_queries(const AttnBwdArgs &a, char *base, BwdShared &sh, int 
             for (int j = 0; ok && j < total; ++j) {
                 if (!(ok = attn_wait(&sh.ds_full, j & 1, failed))) break;
                 fence_after();
-                product_rows(dq_at, dp_at, tile_of(2 * j), id_d, j > 0);
+                product_rows<64>(dq_at, dp_at, tile_of(ring_mn, 2 * j), id_d, j > 0);
                 commit(&sh.empty[(2 * j) % kStages]);
                 if (j + 1 < total && !(ok = products(j + 1))) break;
                 if (j + 2 < total) ok = scores(j + 2);

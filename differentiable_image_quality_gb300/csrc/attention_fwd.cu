@@ -22,10 +22,8 @@ constexpr int tile_bytes()
 }
 
 struct FwdShared {
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
     uint64_t kv_full[8], kv_empty[8], patched, drained;
-    AttnPlace place;
-    int there;
     unsigned tmem, failed;
 };
 
@@ -41,13 +39,88 @@ constexpr size_t fwd_smem()
 // any row needs it.
 constexpr float kLateMax = 8.0f;
 
+// One block's share of the work: a tile (or two) of queries of a head, against some of
+// the keys.
+template <int QT>
+struct FwdItem {
+    AttnPlace pl;
+    int head, kv_head, split;
+    int first;           // query
+    int j0, j1[QT], end; // key tiles: from j0, per tile of queries to j1
+};
+
+// The index-th of the call's, by a whole warp.  Those of one head follow one another,
+// so that its keys stay in L2; causal ones by falling work instead, the longest first.
+template <int QT>
+__device__ __forceinline__ void find_item(const AttnFwdArgs &a, unsigned u, FwdItem<QT> &w)
+{
+    const AttnShape &s = a.s;
+    const int head_blocks = s.heads / a.tile_heads;
+    const int batches = s.packed ? 1 : s.sequences;
+    w.split = u % a.splits;
+    u /= a.splits;
+    int tile, batch;
+    if (s.causal) {
+        w.head = u % head_blocks;
+        u /= head_blocks;
+        batch = u % batches;
+        tile = a.tiles - 1 - u / batches;
+    } else {
+        tile = u % a.tiles;
+        u /= a.tiles;
+        w.head = u % head_blocks;
+        batch = u / head_blocks;
+    }
+    w.kv_head = a.tile_heads > 1 ? w.head : w.head / s.group;
+    if (!find_place<false>(s, batch * a.tiles + tile, a.tile_tokens * QT, w.pl)) {
+        w.pl = {};  // packed: fewer tiles than there could be
+    }
+    w.first = w.pl.tile * a.tile_tokens * QT;
+    int most = 0;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int from = w.first + t * a.tile_tokens;
+        const int rows = min(a.tile_tokens, w.pl.queries - from);
+        int seen = w.pl.keys;
+        if (s.causal) seen = min(seen, from + rows + w.pl.shift);
+        w.j1[t] = rows <= 0 || seen <= 0 ? 0 : (seen + kAttnTile - 1) / kAttnTile;
+        most = max(most, w.j1[t]);
+    }
+    const int per = (most + a.splits - 1) / a.splits;
+    w.j0 = w.split * per;
+    w.end = w.j0;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        w.j1[t] = max(w.j0, min(w.j1[t], w.j0 + per));
+        w.end = max(w.end, w.j1[t]);
+    }
+}
+
+// A block's n-th item: to and fro, so that falling work evens out between the blocks.
+__device__ __forceinline__ unsigned item_of(unsigned n)
+{
+    return n * gridDim.x + (n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// Threads: four warps for each tile of queries, then a warp that copies, one that issues
+// products and, beside two tiles, two that only give their registers up.
+template <int QT>
+constexpr int fwd_threads()
+{
+    return QT * 128 + (QT == 2 ? 128 : 64);
+}
+// Registers of a thread at the launch (168), and after the warps without tiles have
+// given some up: 2 x 208 + 88 = 3 x 168.
+constexpr int kTileRegisters = 208, kOtherRegisters = 88;
+
 template <typename T, int DP, int QT>
-__global__ void __launch_bounds__(QT * 128 + 64, 1) attention_fwd_kernel(const __grid_constant__ AttnFwdArgs a)
+__global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(const __grid_constant__ AttnFwdArgs a)
 {
     using namespace tc;
     constexpr int kStages = stages<DP>();
     constexpr int kTile = tile_bytes<DP>();
     constexpr int kSlabs = DP / kSlabCols;
+    constexpr int kCopy = QT * 4, kIssue = QT * 4 + 1;  // warps
     extern __shared__ char raw[];
     char *const base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     char *const ring = base + QT * kTile;
@@ -55,288 +128,288 @@ __global__ void __launch_bounds__(QT * 128 + 64, 1) attention_fwd_kernel(const _
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const AttnShape &s = a.s;
-    const int head_blocks = s.heads / a.tile_heads;
-    const int tiles = a.tiles, batches = s.packed ? 1 : s.sequences;
-
-    // Blocks of one head follow one another, so that its keys stay in L2; causal ones
-    // by falling work instead, the longest first.
-    unsigned u = blockIdx.x;
-    const int split = u % a.splits;
-    u /= a.splits;
-    int tile, head, batch;
-    if (s.causal) {
-        head = u % head_blocks;
-        u /= head_blocks;
-        batch = u % batches;
-        tile = tiles - 1 - u / batches;
-    } else {
-        tile = u % tiles;
-        u /= tiles;
-        head = u % head_blocks;
-        batch = u / head_blocks;
-    }
-    const int kv_head = a.tile_heads > 1 ? head : head / s.group;
-
-    if (warp == QT * 4) {
-        AttnPlace place;
-        const bool there = find_place<false>(s, batch * tiles + tile, a.tile_tokens * QT, place);
-        if (lane == 0) {
-            sh.place = place;
-            sh.there = there;
-            sh.failed = 0;
-            for (int i = 0; i < QT; ++i) {
-                mbar_init(&sh.q_full[i], 1);
-                mbar_init(&sh.s_full[i], 1);
-                mbar_init(&sh.p_full[i], 128);
-                mbar_init(&sh.o_full[i], 1);
-            }
-            for (int i = 0; i < kStages; ++i) {
-                mbar_init(&sh.kv_full[i], 1);
-                mbar_init(&sh.kv_empty[i], 1);
-            }
-            mbar_init(&sh.patched, 1);
-            mbar_init(&sh.drained, 1);
-            mbar_init_fence();
+    if (warp == kCopy && lane == 0) {
+        for (const CUtensorMap *m : {&a.q, &a.k, &a.v}) prefetch_map(m);
+        sh.failed = 0;
+        for (int i = 0; i < QT; ++i) {
+            mbar_init(&sh.q_full[i], 1);
+            mbar_init(&sh.q_empty[i], 1);
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i][0], 128);
+            mbar_init(&sh.p_full[i][1], 128);
+            mbar_init(&sh.o_full[i], 1);
         }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.kv_full[i], 1);
+            mbar_init(&sh.kv_empty[i], 1);
+        }
+        mbar_init(&sh.patched, 1);
+        mbar_init(&sh.drained, 1);
+        mbar_init_fence();
     }
-    if (warp == QT * 4 + 1) alloc_all(&sh.tmem);
+    if (warp == kIssue) alloc_all(&sh.tmem);
     fence_before();
     __syncthreads();
     fence_after();
-    const AttnPlace pl = sh.place;
     volatile unsigned *const failed = &sh.failed;
     const unsigned tmem = sh.tmem;
 
-    // this block's key tiles: from j0, per tile of queries to j1[w]
-    const int first = pl.tile * a.tile_tokens * QT;
-    int j1[QT], last = 0;
-    int most = 0;
-#pragma unroll
-    for (int w = 0; w < QT; ++w) {
-        const int rows = min(a.tile_tokens, pl.queries - first - w * a.tile_tokens);
-        int seen = pl.keys;
-        if (s.causal) seen = min(seen, first + w * a.tile_tokens + rows + pl.shift);
-        j1[w] = !sh.there || rows <= 0 || seen <= 0 ? 0 : (seen + kAttnTile - 1) / kAttnTile;
-        most = max(most, j1[w]);
-    }
-    const int per = (most + a.splits - 1) / a.splits, j0 = split * per;
-#pragma unroll
-    for (int w = 0; w < QT; ++w) {
-        j1[w] = max(j0, min(j1[w], j0 + per));
-        last = max(last, j1[w]);
-    }
-
-    if (warp == QT * 4) {
+    if (warp == kCopy) {
         // ---- copies: queries, then keys and values in turn
+        if constexpr (QT == 2) release_registers<kOtherRegisters>();
         const unsigned box = unsigned(kSlabs * kRowBytes) * a.tile_heads * a.tile_tokens;
-        int issued = 0;
-        if (lane == 0 && last > j0) {
-            for (int w = 0; w < QT; ++w) {
-                if (j1[w] <= j0) continue;
-                mbar_arrive_expect_tx(&sh.q_full[w], box + (w == 0 ? a.extra : 0));
-                for (int c = 0; c < kSlabs; ++c)
-                    tma_load_4d(base + w * kTile + c * kSlabBytes, &a.q, c * kSlabCols,
-                                head * a.tile_heads, pl.q_row + first + w * a.tile_tokens, pl.batch,
-                                &sh.q_full[w]);
-            }
-        }
-        const int n = 2 * (last - j0);
+        int it = 0, patches = 0, uses[QT] = {};
         bool ok = true;
-        for (int it = 0; ok && it < n; ++it) {
-            const int slot = it % kStages, j = j0 + it / 2;
-            const bool value = it & 1;
-            // values behind the last key may be anything: a tile that holds some has them
-            // zeroed before it is used, since 0 times an infinity or NaN is not 0
-            const bool patch = value && a.ragged && (j + 1) * kAttnTile > pl.keys;
-            if (it >= kStages) ok = attn_wait_warp(&sh.kv_empty[slot], (it / kStages - 1) & 1, failed);
-            if (!ok) break;
-            char *const dst = ring + slot * kTile;
-            if (lane == 0) {
-                uint64_t *const bar = patch ? &sh.patched : &sh.kv_full[slot];
-                mbar_arrive_expect_tx(bar, kTile);
-                for (int c = 0; c < kSlabs; ++c)
-                    tma_load_4d(dst + c * kSlabBytes, value ? &a.v : &a.k, c * kSlabCols, kv_head,
-                                pl.k_row + j * kAttnTile, pl.batch, bar);
-            }
-            issued = it + 1;
-            if (patch) {
-                ok = attn_wait_warp(&sh.patched, 0, failed);
-                const int rows = pl.keys - j * kAttnTile;  // the last tile: one at least
-                for (int i = rows * 8 + lane; i < kAttnTile * 8; i += 32)
+        for (unsigned n = 0, u; ok && (u = item_of(n)) < a.items; ++n) {
+            FwdItem<QT> w;
+            find_item(a, u, w);
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                if (!ok || w.j1[t] <= w.j0) continue;
+                if (uses[t] > 0) ok = attn_wait_warp(&sh.q_empty[t], (uses[t] - 1) & 1, failed);
+                if (!ok) continue;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sh.q_full[t], box + (t == 0 ? a.extra : 0));
                     for (int c = 0; c < kSlabs; ++c)
-                        reinterpret_cast<uint4 *>(dst + c * kSlabBytes)[i] = make_uint4(0, 0, 0, 0);
-                fence_proxy();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.kv_full[slot]);
+                        tma_load_4d(base + t * kTile + c * kSlabBytes, &a.q, c * kSlabCols, w.head * a.tile_heads,
+                                    w.pl.q_row + w.first + t * a.tile_tokens, w.pl.batch, &sh.q_full[t]);
+                }
+                ++uses[t];
+            }
+            for (int i = 2 * w.j0; ok && i < 2 * w.end; ++i) {
+                const int slot = it % kStages, j = i / 2;
+                const bool value = i & 1;
+                // values behind the last key may be anything: a tile that holds some has them
+                // zeroed before it is used, since 0 times an infinity or NaN is not 0
+                const bool patch = value && a.ragged && (j + 1) * kAttnTile > w.pl.keys;
+                if (it >= kStages) ok = attn_wait_warp(&sh.kv_empty[slot], (it / kStages - 1) & 1, failed);
+                if (!ok) break;
+                char *const dst = ring + slot * kTile;
+                if (lane == 0) {
+                    uint64_t *const bar = patch ? &sh.patched : &sh.kv_full[slot];
+                    mbar_arrive_expect_tx(bar, kTile);
+                    for (int c = 0; c < kSlabs; ++c)
+                        tma_load_4d(dst + c * kSlabBytes, value ? &a.v : &a.k, c * kSlabCols, w.kv_head,
+                                    w.pl.k_row + j * kAttnTile, w.pl.batch, bar);
+                }
+                if (patch) {
+                    ok = attn_wait_warp(&sh.patched, patches++ & 1, failed);
+                    const int rows = w.pl.keys - j * kAttnTile;  // the last tile: one at least
+                    for (int e = rows * 8 + lane; e < kAttnTile * 8; e += 32)
+                        for (int c = 0; c < kSlabs; ++c)
+                            reinterpret_cast<uint4 *>(dst + c * kSlabBytes)[e] = make_uint4(0, 0, 0, 0);
+                    fence_proxy();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.kv_full[slot]);
+                }
+                ++it;
             }
         }
         if (*failed && lane == 0) {
             // what is still in flight lands first
-            for (int it = max(0, issued - kStages); it < issued; ++it)
-                mbar_wait_bounded(&sh.kv_full[it % kStages], (it / kStages) & 1, kAttnDrainCycles);
+            for (int i = max(0, it - kStages); i < it; ++i)
+                mbar_wait_bounded(&sh.kv_full[i % kStages], (i / kStages) & 1, kAttnDrainCycles);
+            for (int t = 0; t < QT; ++t)
+                if (uses[t] > 0) mbar_wait_bounded(&sh.q_full[t], (uses[t] - 1) & 1, kAttnDrainCycles);
             atomicOr(&g_attention_status, 4u);
         }
-    } else if (warp == QT * 4 + 1) {
-        // ---- products
-        if (lane == 0 && last > j0) {
-            const int k_steps = (s.dim + 15) / 16;
-            const unsigned id_s = instr_desc<T>(kAttnTile, false);
-            const unsigned id_o = instr_desc<T>(k_steps * 16, true);
-            const unsigned ring_u = smem_u32(ring), q_u = smem_u32(base);
-            const auto scores = [&](int w, int slot) {
-                const unsigned k_tile = ring_u + slot * kTile, q_tile = q_u + w * kTile;
-                for (int i = 0; i < k_steps; ++i) {
-                    const unsigned at = (i / 4) * kSlabBytes + (i % 4) * kStepK;
-                    mma(tmem + w * kAttnTile, desc_k(q_tile + at), desc_k(k_tile + at), id_s, i > 0);
-                }
-                commit(&sh.s_full[w]);
-            };
-            bool ok = attn_wait(&sh.kv_full[0], 0, failed);
+    } else if (warp == kIssue) {
+        // ---- products, by one thread
+        if constexpr (QT == 2) release_registers<kOtherRegisters>();
+        const int k_steps = (s.dim + 15) / 16;
+        const unsigned id_s = instr_desc<T>(kAttnTile, false);
+        const unsigned id_o = instr_desc<T>(k_steps * 16, true);
+        const Desc k_ring = desc_k(smem_u32(ring)), v_ring = desc_mn(smem_u32(ring));
+        const Desc q_tiles = desc_k(smem_u32(base));
+        const auto scores = [&](int t, int slot) {
+            product_k<DP / 16>(tmem + t * kAttnTile, advance(q_tiles, t * kTile), advance(k_ring, slot * kTile),
+                               k_steps, id_s);
+            commit(&sh.s_full[t]);
+        };
+        int it = 0, uses[QT] = {}, halves[QT] = {};
+        bool ok = true;
+        for (unsigned n = 0, u; ok && (u = item_of(n)) < a.items; ++n) {
+            FwdItem<QT> w;
+            find_item(a, u, w);
+            const int count = w.end - w.j0;
+            if (lane == 0 && count > 0) {
+                ok = attn_wait(&sh.kv_full[it % kStages], (it / kStages) & 1, failed);
 #pragma unroll
-            for (int w = 0; w < QT; ++w) {
-                if (!ok || j1[w] <= j0) continue;
-                ok = attn_wait(&sh.q_full[w], 0, failed);
-                if (ok) scores(w, 0);
-            }
-            if (ok) commit(&sh.kv_empty[0]);
-            for (int j = j0; ok && j < last; ++j) {
-                const int it = 2 * (j - j0) + 1, v_slot = it % kStages, k_slot = (it + 1) % kStages;
-                const bool more = j + 1 < last;
-                ok = attn_wait(&sh.kv_full[v_slot], (it / kStages) & 1, failed);
-                if (ok && more) ok = attn_wait(&sh.kv_full[k_slot], ((it + 1) / kStages) & 1, failed);
-                const uint64_t v_desc = desc_mn(ring_u + v_slot * kTile, kSlabBytes);
-#pragma unroll
-                for (int w = 0; w < QT; ++w) {
-                    if (!ok || j >= j1[w]) continue;
-                    ok = attn_wait(&sh.p_full[w], (j - j0) & 1, failed);
+                for (int t = 0; t < QT; ++t) {
+                    if (!ok || w.j1[t] <= w.j0) continue;
+                    ok = attn_wait(&sh.q_full[t], uses[t] & 1, failed);
                     if (!ok) continue;
                     fence_after();
-                    for (int i = 0; i < kAttnTile / 16; ++i)
-                        mma_ta(tmem + QT * kAttnTile + w * DP, tmem + w * kAttnTile + i * 8,
-                               advance(v_desc, i * kStepMn), id_o, j > j0 || i > 0);
-                    if (j + 1 < j1[w])
-                        scores(w, k_slot);
-                    else
-                        commit(&sh.o_full[w]);
+                    scores(t, it % kStages);
+                    if (w.j1[t] == w.j0 + 1) commit(&sh.q_empty[t]);
                 }
-                if (ok) {
-                    commit(&sh.kv_empty[v_slot]);
-                    if (more) commit(&sh.kv_empty[k_slot]);
-                }
-            }
-            if (!ok) {
-                commit(&sh.drained);
-                mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
-            }
-        }
-    } else if (sh.there) {
-        // ---- softmax: a thread has a row
-        const int w = warp / 4, row = threadIdx.x % 128;
-        const unsigned lanes = unsigned(warp % 4) << 21;
-        const unsigned s_at = tmem + lanes + w * kAttnTile;
-        const unsigned o_at = tmem + lanes + QT * kAttnTile + w * DP;
-        const int token = first + w * a.tile_tokens + row / a.tile_heads;
-        const int row_head = head * a.tile_heads + row % a.tile_heads;
-        const bool mine = row < a.tile_tokens * a.tile_heads && token < pl.queries;
-        const int seen = s.causal ? min(pl.keys, token + 1 + pl.shift) : pl.keys;
-        const int end = QT == 1 || w == 0 ? j1[0] : j1[QT - 1];
-        const float c = a.scale_log2;
-        float top = -INFINITY, sum = 0.0f;
-        bool ok = true;
-        for (int j = j0; j < end; ++j) {
-            ok = attn_wait_warp(&sh.s_full[w], (j - j0) & 1, failed);
-            if (!ok) break;
-            fence_after();
-            uint32_t r[128];
-            float *const v = reinterpret_cast<float *>(r);
+                if (ok) commit(&sh.kv_empty[it % kStages]);
+                for (int j = w.j0; ok && j < w.end; ++j) {
+                    const int vi = it + 2 * (j - w.j0) + 1, v_slot = vi % kStages, k_slot = (vi + 1) % kStages;
+                    const bool more = j + 1 < w.end;
+                    ok = attn_wait(&sh.kv_full[v_slot], (vi / kStages) & 1, failed);
+                    if (ok && more) ok = attn_wait(&sh.kv_full[k_slot], ((vi + 1) / kStages) & 1, failed);
+                    const Desc v_tile = advance(v_ring, v_slot * kTile);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ld32(s_at + 32 * i, r + 32 * i);
-            wait_ld();
-            const int left = seen - j * kAttnTile;
-            if (__any_sync(0xffffffffu, left < kAttnTile)) {
-#pragma unroll
-                for (int i = 0; i < 128; ++i) v[i] = i < left ? v[i] : -INFINITY;
-            }
-            float m[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-            for (int i = 4; i < 128; ++i) m[i % 4] = fmaxf(m[i % 4], v[i]);
-            const float now = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
-            if (__any_sync(0xffffffffu, now > top + kLateMax)) {
-                const float next = fmaxf(top, now);
-                const float f = next == -INFINITY ? 1.0f : exp2_fast(top - next);
-                top = next;
-                sum *= f;
-                if (j > j0) {
-                    for (int i = 0; i < DP; i += 16) {
-                        uint32_t o[16];
-                        ld16(o_at + i, o);
-                        wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        st16(o_at + i, o);
+                    for (int t = 0; t < QT; ++t) {
+                        if (!ok || j >= w.j1[t]) continue;
+                        const unsigned o_at = tmem + QT * kAttnTile + t * DP, p_at = tmem + t * kAttnTile;
+                        // the first half of the probabilities goes ahead of the second; its
+                        // threads have read the last item's sums before
+                        ok = attn_wait(&sh.p_full[t][0], halves[t] & 1, failed);
+                        if (!ok) continue;
+                        fence_after();
+                        product_half(o_at, p_at, v_tile, id_o, j > w.j0);
+                        ok = attn_wait(&sh.p_full[t][1], halves[t] & 1, failed);
+                        if (!ok) continue;
+                        fence_after();
+                        product_half(o_at, p_at + 32, advance(v_tile, step_mn(4)), id_o, true);
+                        ++halves[t];
+                        if (j + 1 < w.j1[t]) {
+                            scores(t, k_slot);
+                            if (j + 2 == w.j1[t]) commit(&sh.q_empty[t]);
+                        } else {
+                            commit(&sh.o_full[t]);
+                        }
+                    }
+                    if (ok) {
+                        commit(&sh.kv_empty[v_slot]);
+                        if (more) commit(&sh.kv_empty[k_slot]);
                     }
                 }
             }
-            const float off = top == -INFINITY ? 0.0f : -top;
-            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            it += 2 * count;
 #pragma unroll
-            for (int i = 0; i < 128; i += 32) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float x = exp2_fast(fmaf(v[i + 2 * e], c, off));
-                    const float y = exp2_fast(fmaf(v[i + 2 * e + 1], c, off));
-                    part[2 * (e % 2)] += x;
-                    part[2 * (e % 2) + 1] += y;
-                    p[e] = pack2<T>(x, y);
-                }
-                st16(s_at + i / 2, p);
-            }
-            sum += (part[0] + part[1]) + (part[2] + part[3]);
-            wait_st();
-            fence_before();
-            mbar_arrive(&sh.p_full[w]);
+            for (int t = 0; t < QT; ++t) uses[t] += w.j1[t] > w.j0;
         }
-        if (ok && end > j0) ok = attn_wait_warp(&sh.o_full[w], 0, failed);
-        fence_after();
-        const float scale = ok ? (sum == 0.0f ? 0.0f : 1.0f / sum) : NAN;
-        const float lse = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
-        // dense rows [batch, token, head], of all parts where the keys are split
-        const long long at = ((long long)pl.batch * s.q_tokens + pl.q_row + token) * s.heads + row_head;
-        const long long rows = (long long)batches * s.q_tokens * s.heads;
-        const long long lse_at =
-            ((long long)pl.batch * s.heads + row_head) * s.q_tokens + pl.q_row + token;
-        T *const out = static_cast<T *>(a.out) + at * s.dim;
-        float *const part = a.part_out + (split * rows + at) * s.dim;
-        for (int i = 0; i < s.dim; i += 16) {
-            uint32_t o[16];
-            __syncwarp();
-            if (end > j0) {
-                ld16(o_at + i, o);
+        if (!ok && lane == 0) {
+            commit(&sh.drained);
+            mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
+        }
+    } else if (warp < kCopy) {
+        // ---- softmax: a thread has a row
+        if constexpr (QT == 2) take_registers<kTileRegisters>();
+        const int t = warp / 4, row = threadIdx.x % 128;
+        const unsigned lanes = unsigned(warp % 4) << 21;
+        const unsigned s_at = tmem + lanes + t * kAttnTile;
+        const unsigned o_at = tmem + lanes + QT * kAttnTile + t * DP;
+        const float c = a.scale_log2;
+        const long long rows = (long long)(s.packed ? 1 : s.sequences) * s.q_tokens * s.heads;
+        int tiles = 0, uses = 0;
+        bool ok = true;
+        for (unsigned n = 0, u; (u = item_of(n)) < a.items; ++n) {
+            FwdItem<QT> w;
+            find_item(a, u, w);
+            const int token = w.first + t * a.tile_tokens + row / a.tile_heads;
+            const int row_head = w.head * a.tile_heads + row % a.tile_heads;
+            const bool mine = row < a.tile_tokens * a.tile_heads && token < w.pl.queries;
+            const int seen = s.causal ? min(w.pl.keys, token + 1 + w.pl.shift) : w.pl.keys;
+            const int end = QT == 1 || t == 0 ? w.j1[0] : w.j1[QT - 1];
+            float top = -INFINITY, sum = 0.0f;
+            for (int j = w.j0; ok && j < end; ++j) {
+                ok = attn_wait_warp(&sh.s_full[t], tiles & 1, failed);
+                if (!ok) break;
+                fence_after();
+                uint32_t r[128];
+                float *const v = reinterpret_cast<float *>(r);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ld32(s_at + 32 * i, r + 32 * i);
                 wait_ld();
-            }
-            float v[16];
+                const int left = seen - j * kAttnTile;
+                if (__any_sync(0xffffffffu, left < kAttnTile)) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = end > j0 && sum != 0.0f ? __uint_as_float(o[e]) * scale : (ok ? 0.0f : NAN);
+                    for (int i = 0; i < 128; ++i) v[i] = i < left ? v[i] : -INFINITY;
+                }
+                float m[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-            for (int h = 0; h < 16; h += 8) {
-                if (!mine || i + h >= s.dim) continue;
-                float (&q)[8] = *reinterpret_cast<float (*)[8]>(v + h);
-                if (a.splits > 1)
-                    st8<float>(part + i + h, pack8<float>(q));
-                else
-                    st8<T>(out + i + h, pack8<T>(q));
+                for (int i = 4; i < 128; i += 2) m[i / 2 % 4] = fmaxf(fmaxf(m[i / 2 % 4], v[i]), v[i + 1]);
+                const float now = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
+                if (__any_sync(0xffffffffu, now > top + kLateMax)) {
+                    const float next = fmaxf(top, now);
+                    const float f = next == -INFINITY ? 1.0f : exp2_fast(top - next);
+                    top = next;
+                    sum *= f;
+                    if (j > w.j0) {
+                        for (int i = 0; i < DP; i += 16) {
+                            uint32_t o[16];
+                            ld16(o_at + i, o);
+                            wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            st16(o_at + i, o);
+                        }
+                    }
+                }
+                const float off = top == -INFINITY ? 0.0f : -top;
+                const f32x2 c2 = both(c), off2 = both(off);
+                f32x2 part[2] = {0, 0};
+#pragma unroll
+                for (int i = 0; i < 128; i += 32) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = halves(fma2(pair(v[i + 2 * e], v[i + 2 * e + 1]), c2, off2));
+                        const float y = exp2_fast(x.x), z = exp2_fast(x.y);
+                        part[e % 2] = add2(part[e % 2], pair(y, z));
+                        p[e] = pack2<T>(y, z);
+                    }
+                    st16(s_at + i / 2, p);
+                    if (i % 64 == 32) {
+                        wait_st();
+                        fence_before();
+                        mbar_arrive(&sh.p_full[t][i / 64]);
+                    }
+                }
+                sum += sum2(add2(part[0], part[1]));
+                ++tiles;
             }
+            const bool some = end > w.j0;
+            if (some && ok) ok = attn_wait_warp(&sh.o_full[t], uses & 1, failed);
+            uses += some;
+            fence_after();
+            const float scale = ok ? (sum == 0.0f ? 0.0f : 1.0f / sum) : NAN;
+            const float lse = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+            // dense rows [batch, token, head], of all parts where the keys are split
+            const long long at =
+                ((long long)w.pl.batch * s.q_tokens + w.pl.q_row + token) * s.heads + row_head;
+            const long long lse_at =
+                ((long long)w.pl.batch * s.heads + row_head) * s.q_tokens + w.pl.q_row + token;
+            T *const out = static_cast<T *>(a.out) + at * s.dim;
+            float *const part = a.part_out + (w.split * rows + at) * s.dim;
+            for (int i = 0; i < s.dim; i += 32) {
+                uint32_t o[32];
+                __syncwarp();
+                if (some) {
+                    ld32(o_at + i, o);
+                    wait_ld();
+                }
+                float v[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    v[e] = some && sum != 0.0f ? __uint_as_float(o[e]) * scale : (ok ? 0.0f : NAN);
+#pragma unroll
+                for (int h = 0; h < 32; h += 8) {
+                    if (!mine || i + h >= s.dim) continue;
+                    float (&q)[8] = *reinterpret_cast<float (*)[8]>(v + h);
+                    if (a.splits > 1)
+                        st8<float>(part + i + h, pack8<float>(q));
+                    else
+                        st8<T>(out + i + h, pack8<T>(q));
+                }
+            }
+            if (mine && a.splits > 1)
+                a.part_lse[w.split * rows + lse_at] = lse;
+            else if (mine && a.lse)
+                a.lse[lse_at] = lse;
         }
-        if (mine && a.splits > 1)
-            a.part_lse[split * rows + lse_at] = lse;
-        else if (mine && a.lse)
-            a.lse[lse_at] = lse;
+    } else {
+        if constexpr (QT == 2) release_registers<kOtherRegisters>();
     }
     __syncwarp();
     fence_before();
     __syncthreads();
-    if (warp == QT * 4 + 1) {
+    if (warp == kIssue) {
         fence_after();
         free_all(tmem);
     }
@@ -385,9 +458,8 @@ cudaError_t launch(const AttnFwdArgs &a, cudaStream_t stream)
     static std::atomic<unsigned long long> done{0};
     const cudaError_t e = allow_smem(attention_fwd_kernel<T, DP, QT>, done, smem);
     if (e != cudaSuccess) return e;
-    const long long grid = (long long)a.splits * a.tiles * (a.s.packed ? 1 : a.s.sequences) *
-                           (a.s.heads / a.tile_heads);
-    attention_fwd_kernel<T, DP, QT><<<unsigned(grid), QT * 128 + 64, smem, stream>>>(a);
+    const unsigned grid = std::min(a.items, unsigned(kAttnBlocks));
+    attention_fwd_kernel<T, DP, QT><<<grid, fwd_threads<QT>(), smem, stream>>>(a);
     return cudaGetLastError();
 }
 

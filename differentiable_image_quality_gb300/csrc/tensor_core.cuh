@@ -9,6 +9,8 @@
 // (MN-major); only the descriptor differs.
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 #include "dtypes.cuh"
 
@@ -23,30 +25,28 @@ constexpr int kSlabBytes = kTileRows * kRowBytes;
 // ---------------------------------------------------------------- descriptors
 
 // Shared-memory matrix descriptor: start address, the two byte offsets between the
-// 8-row groups of the swizzle's pattern, 128-byte swizzle.
-__device__ __forceinline__ uint64_t make_desc(unsigned smem, unsigned leading, unsigned stride)
-{
-    return uint64_t((smem & 0x3ffffu) >> 4) | uint64_t(leading >> 4) << 16 |
-           uint64_t(stride >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
-}
+// 8-row groups of the swizzle's pattern, 128-byte swizzle.  Only the low word
+// depends on the address, and steps add to it: one thread issues all products, 64
+// cycles apart at full rate, so what it spends on each counts (descriptors formed
+// anew for each product: half that rate).
+struct Desc {
+    unsigned lo, hi;
+};
 
-// Summed index along the rows' bytes: 8 rows are 1024 bytes; a step of 16 elements
-// is 32 bytes further on.
-__device__ __forceinline__ uint64_t desc_k(unsigned slab) { return make_desc(slab, 16, 1024); }
-constexpr unsigned kStepK = 32;
-
-// Summed index counts the rows: slabs of 64 columns lie `slab_bytes` apart; a step
-// of 16 rows is 2048 bytes further on.
-__device__ __forceinline__ uint64_t desc_mn(unsigned slab, unsigned slab_bytes)
+__device__ __forceinline__ Desc make_desc(unsigned smem, unsigned leading, unsigned stride)
 {
-    return make_desc(slab, slab_bytes, 1024);
+    return {(smem & 0x3ffffu) >> 4 | (leading >> 4) << 16, (stride >> 4) | 1u << 14 | 2u << 29};
 }
-constexpr unsigned kStepMn = 16 * kRowBytes;
+__device__ __forceinline__ Desc advance(Desc d, unsigned bytes) { return {d.lo + (bytes >> 4), d.hi}; }
 
-__device__ __forceinline__ uint64_t advance(uint64_t desc, unsigned bytes)
-{
-    return desc + (bytes >> 4);
-}
+// Summed index along the rows' bytes: 8 rows are 1024 bytes.  Step i of 16 elements.
+__device__ __forceinline__ Desc desc_k(unsigned slab) { return make_desc(slab, 16, 1024); }
+__device__ __forceinline__ constexpr unsigned step_k(int i) { return (i / 4) * kSlabBytes + (i % 4) * 32; }
+
+// Summed index counts the rows: slabs of 64 columns lie kSlabBytes apart.  Step i of 16
+// rows.
+__device__ __forceinline__ Desc desc_mn(unsigned slab) { return make_desc(slab, kSlabBytes, 1024); }
+__device__ __forceinline__ constexpr unsigned step_mn(int i) { return i * 16 * kRowBytes; }
 
 // Instruction descriptor: float32 accumulator, both operands of type T, M = 128 rows,
 // n columns; b_mn: the second operand's summed index counts its rows.
@@ -61,23 +61,52 @@ __device__ __forceinline__ unsigned instr_desc(int n, bool b_mn)
 // ----------------------------------------------------------------- instructions
 
 // D (+)= A B, A and B in shared memory; by one thread.
-__device__ __forceinline__ void mma(unsigned d, uint64_t a, uint64_t b, unsigned idesc, bool add)
+__device__ __forceinline__ void mma(unsigned d, Desc a, Desc b, unsigned idesc, bool add)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b),
-        "r"(idesc), "r"(unsigned(add))
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %6, 0;\n"
+        " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d), "r"(a.lo), "r"(a.hi),
+        "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(unsigned(add))
         : "memory");
 }
 
 // The same with A in tensor memory (two 16-bit elements a column).
-__device__ __forceinline__ void mma_ta(unsigned d, unsigned a, uint64_t b, unsigned idesc, bool add)
+__device__ __forceinline__ void mma_ta(unsigned d, unsigned a, Desc b, unsigned idesc, bool add)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b),
-        "r"(idesc), "r"(unsigned(add))
+        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.u32 p, %5, 0;\n"
+        " mov.b64 b, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d), "r"(a), "r"(b.lo),
+        "r"(b.hi), "r"(idesc), "r"(unsigned(add))
         : "memory");
+}
+
+// D = A B^T of two tiles of 128 rows, their columns summed over in `steps` of 16, at most
+// MOST.
+template <int MOST>
+__device__ __forceinline__ void product_k(unsigned d, Desc a, Desc b, int steps, unsigned idesc)
+{
+#pragma unroll
+    for (int i = 0; i < MOST; ++i)
+        if (i == 0 || i < steps) mma(d, advance(a, step_k(i)), advance(b, step_k(i)), idesc, i > 0);
+}
+
+// D (+)= A B: A [128, 64] in tensor memory, B's 64 rows summed over.
+__device__ __forceinline__ void product_half(unsigned d, unsigned a, Desc b, unsigned idesc, bool add)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mma_ta(d, a + i * 8, advance(b, step_mn(i)), idesc, i > 0 || add);
+}
+
+// D (+)= A B: A [128, 128] in tensor memory, its two halves of 64 columns HALF columns of
+// tensor memory apart, B's 128 rows summed over.
+template <int HALF>
+__device__ __forceinline__ void product_rows(unsigned d, unsigned a, Desc b, unsigned idesc, bool add)
+{
+#pragma unroll
+    for (int i = 0; i < kTileRows / 16; ++i)
+        mma_ta(d, a + (i / 4) * HALF + (i % 4) * 8, advance(b, step_mn(i)), idesc, i > 0 || add);
 }
 
 // Arrives on the barrier when all products issued by this thread so far are done.
@@ -153,6 +182,24 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar)
 __device__ __forceinline__ void fence_proxy()
 {
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+}
+
+// A warpgroup's registers per thread, given up or taken from what others of the block
+// gave up (of those that it was launched with).
+template <int N>
+__device__ __forceinline__ void release_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
 }
 
 // 2^x by the hardware instruction (relative error about 2^-22).
