@@ -138,11 +138,28 @@ __device__ __forceinline__ bool attn_wait(uint64_t *bar, unsigned parity, volati
     return mbar_try_wait(bar, parity) || attn_wait_slow(bar, parity, failed);
 }
 
+// A place in a ring of N buffers and the parity of its round, without divisions.
+template <int N>
+struct RingAt {
+    int slot = 0;
+    unsigned parity = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == N) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+};
+
 // By a whole warp, which then goes one way.
 __device__ __forceinline__ bool attn_wait_warp(uint64_t *bar, unsigned parity, volatile unsigned *failed)
 {
     return __all_sync(0xffffffffu, attn_wait(bar, parity, failed));
 }
+
+// A value that all lanes have, where the compiler knows that they do.
+__device__ __forceinline__ unsigned uniform(unsigned v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // A kernel's shared memory, asked for once on each device (1.5 us a call otherwise).
 template <typename Kernel>

@@ -256,11 +256,11 @@ __device__ void by_keys(const AttnBwdArgs &a, char *base, BwdShared &sh, int kv_
     const AttnShape &s = a.s;
     const AttnPlace pl = sh.place;
     volatile unsigned *const failed = &sh.failed;
-    const unsigned tmem = sh.tmem;
+    const unsigned tmem = uniform(sh.tmem);
     const unsigned s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 256 + DP;
     char *const ring = base + 2 * kTile;
     char *const ring_stats = ring + 2 * kStages * kTile;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
 
     const int first = pl.tile * kAttnTile;  // key
     const int all = (pl.queries + kAttnTile - 1) / kAttnTile;
@@ -315,44 +315,46 @@ __device__ void by_keys(const AttnBwdArgs &a, char *base, BwdShared &sh, int kv_
             atomicOr(&g_attention_status, 4u);
         }
     } else if (warp == 9) {
-        if (lane == 0 && total > 0) {
+        if (total > 0) {
+            const unsigned leader = elect_leader();
             const int steps = (s.dim + 15) / 16;
             const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
+            const unsigned s_full = smem_u32(sh.s_full), dp_full = smem_u32(&sh.dp_full), empty = smem_u32(sh.empty);
             const Desc k_tile = desc_k(smem_u32(base)), v_tile = advance(k_tile, kTile);
             const Desc ring_k = desc_k(smem_u32(ring)), ring_mn = desc_mn(smem_u32(ring));
-            bool ok = attn_wait(&sh.own_full, 0, failed) && attn_wait(&sh.full[0], 0, failed);
+            bool ok = attn_wait_warp(&sh.own_full, 0, failed) && attn_wait_warp(&sh.full[0], 0, failed);
             if (ok) {
-                product_k<DP / 16>(s_at, k_tile, ring_k, steps, id_s);
-                commit(&sh.s_full[0]);
-                product_k<DP / 16>(dp_at, v_tile, advance(ring_k, kTile), steps, id_s);
-                commit(&sh.dp_full);
+                product_k<DP / 16>(s_at, k_tile, ring_k, steps, id_s, leader);
+                commit(s_full, leader);
+                product_k<DP / 16>(dp_at, v_tile, advance(ring_k, kTile), steps, id_s, leader);
+                commit(dp_full, leader);
             }
             for (int it = 0; ok && it < total; ++it) {
                 const Desc tile = advance(ring_mn, 2 * (it % kStages) * kTile);
                 const int nx = (it + 1) % kStages;
                 const Desc next = advance(ring_k, 2 * nx * kTile);
                 const bool more = it + 1 < total;
-                if (!(ok = attn_wait(&sh.p_full, it & 1, failed))) break;
+                if (!(ok = attn_wait_warp(&sh.p_full, it & 1, failed))) break;
                 fence_after();
-                product_rows<64>(dv_at, s_at, advance(tile, kTile), id_d, it > 0);
+                product_rows<64>(dv_at, s_at, advance(tile, kTile), id_d, it > 0, leader);
                 if (more) {
-                    if (!(ok = attn_wait(&sh.full[nx], ((it + 1) / kStages) & 1, failed))) break;
-                    product_k<DP / 16>(s_at, k_tile, next, steps, id_s);
-                    commit(&sh.s_full[0]);
+                    if (!(ok = attn_wait_warp(&sh.full[nx], ((it + 1) / kStages) & 1, failed))) break;
+                    product_k<DP / 16>(s_at, k_tile, next, steps, id_s, leader);
+                    commit(s_full, leader);
                 }
-                if (!(ok = attn_wait(&sh.ds_full, it & 1, failed))) break;
+                if (!(ok = attn_wait_warp(&sh.ds_full, it & 1, failed))) break;
                 fence_after();
-                product_rows<64>(dk_at, dp_at, tile, id_d, it > 0);
-                commit(&sh.empty[it % kStages]);
+                product_rows<64>(dk_at, dp_at, tile, id_d, it > 0, leader);
+                commit(empty + 8 * (it % kStages), leader);
                 if (more) {
-                    product_k<DP / 16>(dp_at, v_tile, advance(next, kTile), steps, id_s);
-                    commit(&sh.dp_full);
+                    product_k<DP / 16>(dp_at, v_tile, advance(next, kTile), steps, id_s, leader);
+                    commit(dp_full, leader);
                 }
             }
             if (ok) {
-                commit(&sh.done);
+                commit(smem_u32(&sh.done), leader);
             } else {
-                commit(&sh.drained);
+                commit(smem_u32(&sh.drained), leader);
                 mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
             }
         }
@@ -453,10 +455,10 @@ __device__ void by_queries(const AttnBwdArgs &a, char *base, BwdShared &sh, int 
     const AttnShape &s = a.s;
     const AttnPlace pl = sh.place;
     volatile unsigned *const failed = &sh.failed;
-    const unsigned tmem = sh.tmem;
+    const unsigned tmem = uniform(sh.tmem);
     const unsigned s_at = tmem, dp_at = tmem + 256, dq_at = tmem + 384;
     char *const ring = base + 2 * kTile;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int kv_head = head / s.group;
 
     const int first = pl.tile * kAttnTile;  // query
@@ -501,42 +503,48 @@ __device__ void by_queries(const AttnBwdArgs &a, char *base, BwdShared &sh, int 
             atomicOr(&g_attention_status, 4u);
         }
     } else if (warp == 9) {
-        if (lane == 0 && total > 0) {
+        if (total > 0) {
+            const unsigned leader = elect_leader();
             const int steps = (s.dim + 15) / 16;
             const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
+            const unsigned s_full = smem_u32(sh.s_full), dp_full = smem_u32(&sh.dp_full), empty = smem_u32(sh.empty);
             const Desc q_tile = desc_k(smem_u32(base)), g_tile = advance(q_tile, kTile);
             const Desc ring_k = desc_k(smem_u32(ring)), ring_mn = desc_mn(smem_u32(ring));
-            const auto wait_tile = [&](int it) {
-                return attn_wait(&sh.full[it % kStages], (it / kStages) & 1, failed);
-            };
-            const auto tile_of = [&](Desc ring, int it) { return advance(ring, (it % kStages) * kTile); };
+            // two places in the ring: of the tile that comes next, and of the keys that ds is
+            // waiting for
+            RingAt<kStages> at, keys;
+            const auto tile_here = [&] { return attn_wait_warp(&sh.full[at.slot], at.parity, failed); };
             const auto scores = [&](int j) {
-                if (!wait_tile(2 * j)) return false;
-                product_k<DP / 16>(s_at + (j & 1) * 128, q_tile, tile_of(ring_k, 2 * j), steps, id_s);
-                commit(&sh.s_full[j & 1]);
+                if (!tile_here()) return false;
+                product_k<DP / 16>(s_at + (j & 1) * 128, q_tile, advance(ring_k, at.slot * kTile), steps, id_s, leader);
+                commit(s_full + 8 * (j & 1), leader);
+                at.next();
                 return true;
             };
-            const auto products = [&](int j) {
-                if (!wait_tile(2 * j + 1)) return false;
-                product_k<DP / 16>(dp_at, g_tile, tile_of(ring_k, 2 * j + 1), steps, id_s);
-                commit(&sh.dp_full);
-                commit(&sh.empty[(2 * j + 1) % kStages]);
+            const auto products = [&] {
+                if (!tile_here()) return false;
+                product_k<DP / 16>(dp_at, g_tile, advance(ring_k, at.slot * kTile), steps, id_s, leader);
+                commit(dp_full, leader);
+                commit(empty + 8 * at.slot, leader);
+                at.next();
                 return true;
             };
-            bool ok = attn_wait(&sh.own_full, 0, failed) && scores(0) && products(0);
+            bool ok = attn_wait_warp(&sh.own_full, 0, failed) && scores(0) && products();
             if (ok && total > 1) ok = scores(1);
             for (int j = 0; ok && j < total; ++j) {
-                if (!(ok = attn_wait(&sh.ds_full, j & 1, failed))) break;
+                if (!(ok = attn_wait_warp(&sh.ds_full, j & 1, failed))) break;
                 fence_after();
-                product_rows<64>(dq_at, dp_at, tile_of(ring_mn, 2 * j), id_d, j > 0);
-                commit(&sh.empty[(2 * j) % kStages]);
-                if (j + 1 < total && !(ok = products(j + 1))) break;
+                product_rows<64>(dq_at, dp_at, advance(ring_mn, keys.slot * kTile), id_d, j > 0, leader);
+                commit(empty + 8 * keys.slot, leader);
+                keys.next();
+                keys.next();
+                if (j + 1 < total && !(ok = products())) break;
                 if (j + 2 < total) ok = scores(j + 2);
             }
             if (ok) {
-                commit(&sh.done);
+                commit(smem_u32(&sh.done), leader);
             } else {
-                commit(&sh.drained);
+                commit(smem_u32(&sh.drained), leader);
                 mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
             }
         }
@@ -606,7 +614,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
     extern __shared__ char raw[];
     char *const base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     BwdShared &sh = *reinterpret_cast<BwdShared *>(base + bwd_smem<DP>() - 1024 - sizeof(BwdShared));
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const AttnShape &s = a.s;
     const bool keys_wanted = a.dk || a.dv;
     const unsigned key_blocks = keys_wanted ? unsigned(a.k_tiles) * s.kv_heads : 0;

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
     char *const ring = base + QT * kTile;
     FwdShared &sh = *reinterpret_cast<FwdShared *>(ring + kStages * kTile);
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const AttnShape &s = a.s;
     if (warp == kCopy && lane == 0) {
         for (const CUtensorMap *m : {&a.q, &a.k, &a.v}) prefetch_map(m);
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
     __syncthreads();
     fence_after();
     volatile unsigned *const failed = &sh.failed;
-    const unsigned tmem = sh.tmem;
+    const unsigned tmem = uniform(sh.tmem);
 
     if (warp == kCopy) {
         // ---- copies: queries, then keys and values in turn
@@ -214,77 +214,82 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
             atomicOr(&g_attention_status, 4u);
         }
     } else if (warp == kIssue) {
-        // ---- products, by one thread
+        // ---- products
         if constexpr (QT == 2) release_registers<kOtherRegisters>();
+        const unsigned leader = elect_leader();
         const int k_steps = (s.dim + 15) / 16;
         const unsigned id_s = instr_desc<T>(kAttnTile, false);
         const unsigned id_o = instr_desc<T>(k_steps * 16, true);
         const Desc k_ring = desc_k(smem_u32(ring)), v_ring = desc_mn(smem_u32(ring));
         const Desc q_tiles = desc_k(smem_u32(base));
+        const unsigned full = smem_u32(sh.kv_full), empty = smem_u32(sh.kv_empty);
+        const unsigned q_empty = smem_u32(sh.q_empty), s_full = smem_u32(sh.s_full), o_full = smem_u32(sh.o_full);
         const auto scores = [&](int t, int slot) {
             product_k<DP / 16>(tmem + t * kAttnTile, advance(q_tiles, t * kTile), advance(k_ring, slot * kTile),
-                               k_steps, id_s);
-            commit(&sh.s_full[t]);
+                               k_steps, id_s, leader);
+            commit(s_full + 8 * t, leader);
         };
-        int it = 0, uses[QT] = {}, halves[QT] = {};
+        RingAt<kStages> at;
+        unsigned uses[QT] = {}, phase[QT] = {};
         bool ok = true;
+        const auto keys_here = [&] { return attn_wait_warp(&sh.kv_full[at.slot], at.parity, failed); };
         for (unsigned n = 0, u; ok && (u = item_of(n)) < a.items; ++n) {
             FwdItem<QT> w;
             find_item(a, u, w);
-            const int count = w.end - w.j0;
-            if (lane == 0 && count > 0) {
-                ok = attn_wait(&sh.kv_full[it % kStages], (it / kStages) & 1, failed);
+            if (w.end <= w.j0) continue;
+            ok = keys_here();
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                if (!ok || w.j1[t] <= w.j0) continue;
+                ok = attn_wait_warp(&sh.q_full[t], uses[t] & 1, failed);
+                if (!ok) continue;
+                ++uses[t];
+                fence_after();
+                scores(t, at.slot);
+                if (w.j1[t] == w.j0 + 1) commit(q_empty + 8 * t, leader);
+            }
+            if (ok) commit(empty + 8 * at.slot, leader);
+            at.next();
+            ok = ok && keys_here();
+            for (int j = w.j0; ok && j < w.end; ++j) {
+                const int v_slot = at.slot;
+                const Desc v_tile = advance(v_ring, v_slot * kTile);
+                at.next();
+                const bool more = j + 1 < w.end;
+                bool here = !more;  // the next keys
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
-                    if (!ok || w.j1[t] <= w.j0) continue;
-                    ok = attn_wait(&sh.q_full[t], uses[t] & 1, failed);
-                    if (!ok) continue;
+                    if (j >= w.j1[t]) continue;
+                    const unsigned o_at = tmem + QT * kAttnTile + t * DP, p_at = tmem + t * kAttnTile;
+                    // the first half of the probabilities goes ahead of the second; its
+                    // threads have read the last item's sums before
+                    if (!(ok = ok && attn_wait_warp(&sh.p_full[t][0], phase[t], failed))) continue;
                     fence_after();
-                    scores(t, it % kStages);
-                    if (w.j1[t] == w.j0 + 1) commit(&sh.q_empty[t]);
+                    product_half(o_at, p_at, v_tile, id_o, j > w.j0, leader);
+                    if (!(ok = attn_wait_warp(&sh.p_full[t][1], phase[t], failed))) continue;
+                    fence_after();
+                    product_half(o_at, p_at + 32, advance(v_tile, step_mn(4)), id_o, true, leader);
+                    phase[t] ^= 1;
+                    if (!here) here = ok = keys_here();
+                    if (!ok) continue;
+                    if (j + 1 < w.j1[t]) {
+                        scores(t, at.slot);
+                        if (j + 2 == w.j1[t]) commit(q_empty + 8 * t, leader);
+                    } else {
+                        commit(o_full + 8 * t, leader);
+                    }
                 }
-                if (ok) commit(&sh.kv_empty[it % kStages]);
-                for (int j = w.j0; ok && j < w.end; ++j) {
-                    const int vi = it + 2 * (j - w.j0) + 1, v_slot = vi % kStages, k_slot = (vi + 1) % kStages;
-                    const bool more = j + 1 < w.end;
-                    ok = attn_wait(&sh.kv_full[v_slot], (vi / kStages) & 1, failed);
-                    if (ok && more) ok = attn_wait(&sh.kv_full[k_slot], ((vi + 1) / kStages) & 1, failed);
-                    const Desc v_tile = advance(v_ring, v_slot * kTile);
-#pragma unroll
-                    for (int t = 0; t < QT; ++t) {
-                        if (!ok || j >= w.j1[t]) continue;
-                        const unsigned o_at = tmem + QT * kAttnTile + t * DP, p_at = tmem + t * kAttnTile;
-                        // the first half of the probabilities goes ahead of the second; its
-                        // threads have read the last item's sums before
-                        ok = attn_wait(&sh.p_full[t][0], halves[t] & 1, failed);
-                        if (!ok) continue;
-                        fence_after();
-                        product_half(o_at, p_at, v_tile, id_o, j > w.j0);
-                        ok = attn_wait(&sh.p_full[t][1], halves[t] & 1, failed);
-                        if (!ok) continue;
-                        fence_after();
-                        product_half(o_at, p_at + 32, advance(v_tile, step_mn(4)), id_o, true);
-                        ++halves[t];
-                        if (j + 1 < w.j1[t]) {
-                            scores(t, k_slot);
-                            if (j + 2 == w.j1[t]) commit(&sh.q_empty[t]);
-                        } else {
-                            commit(&sh.o_full[t]);
-                        }
-                    }
-                    if (ok) {
-                        commit(&sh.kv_empty[v_slot]);
-                        if (more) commit(&sh.kv_empty[k_slot]);
-                    }
+                if (!ok) break;
+                commit(empty + 8 * v_slot, leader);
+                if (more) {
+                    commit(empty + 8 * at.slot, leader);
+                    at.next();
+                    ok = keys_here();
                 }
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            it += 2 * count;
-#pragma unroll
-            for (int t = 0; t < QT; ++t) uses[t] += w.j1[t] > w.j0;
         }
-        if (!ok && lane == 0) {
-            commit(&sh.drained);
+        if (!ok) {
+            commit(smem_u32(&sh.drained), leader);
             mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
         }
     } else if (warp < kCopy) {

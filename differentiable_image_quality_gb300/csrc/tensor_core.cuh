@@ -60,61 +60,80 @@ __device__ __forceinline__ unsigned instr_desc(int n, bool b_mn)
 
 // ----------------------------------------------------------------- instructions
 
-// D (+)= A B, A and B in shared memory; by one thread.
-__device__ __forceinline__ void mma(unsigned d, Desc a, Desc b, unsigned idesc, bool add)
+// The products are issued by a whole warp that goes one way, with a predicate that one
+// lane has (`leader`): the compiler then keeps descriptors in the warp's uniform
+// registers, where these instructions want them.  One lane in a branch of its own had
+// to move them there for each product and issued one in 75 cycles beside busy warps,
+// where the tensor cores take 64.
+
+// 1 in one lane of the warp, 0 in the others.
+__device__ __forceinline__ unsigned elect_leader()
+{
+    unsigned r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r;
+}
+
+// D (+)= A B, A and B in shared memory.
+__device__ __forceinline__ void mma(unsigned d, Desc a, Desc b, unsigned idesc, bool add, unsigned leader)
 {
     asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.u32 p, %6, 0;\n"
+        "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.u32 p, %6, 0;\n setp.ne.u32 q, %7, 0;\n"
         " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d), "r"(a.lo), "r"(a.hi),
-        "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(unsigned(add))
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d), "r"(a.lo), "r"(a.hi),
+        "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(unsigned(add)), "r"(leader)
         : "memory");
 }
 
 // The same with A in tensor memory (two 16-bit elements a column).
-__device__ __forceinline__ void mma_ta(unsigned d, unsigned a, Desc b, unsigned idesc, bool add)
+__device__ __forceinline__ void mma_ta(unsigned d, unsigned a, Desc b, unsigned idesc, bool add, unsigned leader)
 {
     asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.u32 p, %5, 0;\n"
+        "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.u32 p, %5, 0;\n setp.ne.u32 q, %6, 0;\n"
         " mov.b64 b, {%2, %3};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d), "r"(a), "r"(b.lo),
-        "r"(b.hi), "r"(idesc), "r"(unsigned(add))
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d), "r"(a), "r"(b.lo),
+        "r"(b.hi), "r"(idesc), "r"(unsigned(add)), "r"(leader)
         : "memory");
 }
 
 // D = A B^T of two tiles of 128 rows, their columns summed over in `steps` of 16, at most
 // MOST.
 template <int MOST>
-__device__ __forceinline__ void product_k(unsigned d, Desc a, Desc b, int steps, unsigned idesc)
+__device__ __forceinline__ void product_k(unsigned d, Desc a, Desc b, int steps, unsigned idesc, unsigned leader)
 {
 #pragma unroll
     for (int i = 0; i < MOST; ++i)
-        if (i == 0 || i < steps) mma(d, advance(a, step_k(i)), advance(b, step_k(i)), idesc, i > 0);
+        if (i == 0 || i < steps) mma(d, advance(a, step_k(i)), advance(b, step_k(i)), idesc, i > 0, leader);
 }
 
 // D (+)= A B: A [128, 64] in tensor memory, B's 64 rows summed over.
-__device__ __forceinline__ void product_half(unsigned d, unsigned a, Desc b, unsigned idesc, bool add)
+__device__ __forceinline__ void product_half(unsigned d, unsigned a, Desc b, unsigned idesc, bool add,
+                                             unsigned leader)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mma_ta(d, a + i * 8, advance(b, step_mn(i)), idesc, i > 0 || add);
+    for (int i = 0; i < 4; ++i) mma_ta(d, a + i * 8, advance(b, step_mn(i)), idesc, i > 0 || add, leader);
 }
 
 // D (+)= A B: A [128, 128] in tensor memory, its two halves of 64 columns HALF columns of
 // tensor memory apart, B's 128 rows summed over.
 template <int HALF>
-__device__ __forceinline__ void product_rows(unsigned d, unsigned a, Desc b, unsigned idesc, bool add)
+__device__ __forceinline__ void product_rows(unsigned d, unsigned a, Desc b, unsigned idesc, bool add,
+                                             unsigned leader)
 {
 #pragma unroll
     for (int i = 0; i < kTileRows / 16; ++i)
-        mma_ta(d, a + (i / 4) * HALF + (i % 4) * 8, advance(b, step_mn(i)), idesc, i > 0 || add);
+        mma_ta(d, a + (i / 4) * HALF + (i % 4) * 8, advance(b, step_mn(i)), idesc, i > 0 || add, leader);
 }
 
-// Arrives on the barrier when all products issued by this thread so far are done.
-__device__ __forceinline__ void commit(uint64_t *bar)
+// Arrives on the barrier (by its shared-memory address) when all products issued by the
+// leader so far are done.
+__device__ __forceinline__ void commit(unsigned bar, unsigned leader)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(
-                     smem_u32(bar))
-                 : "memory");
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+        "r"(leader)
+        : "memory");
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
