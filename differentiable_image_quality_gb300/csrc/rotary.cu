@@ -7,10 +7,11 @@
 // times the position, wraps by itself, so far positions lose nothing; sine and
 // cosine then see at most half a turn, in float32.
 //
-// Bound by memory: every element is read and written once.  A block forms the
-// sines and cosines of some tokens once, in shared memory, for all their heads of
-// both tensors; a thread keeps those of its eight columns in registers for four
-// heads at a time, whose loads are under way together.
+// Bound by memory: every element is read and written once.  A thread has eight columns
+// of a token (in the layout of halves, four of each half) and goes over the token's
+// heads with their sines and cosines in registers, four heads' loads under way
+// together and the first ones before it knows the angles.  Nothing but the
+// frequencies' fractions is in shared memory, so that no thread waits for another.
 #include <algorithm>
 #include <climits>
 #include <mutex>
@@ -23,7 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 256, kMaxRotaryDim = 512;
-constexpr int kHeadsAtOnce = 4;
+constexpr int kHeadsAtOnce = 2;
 constexpr int kNoAngle = 255;  // in an axis's place: the frequency is NaN or infinite
 
 struct RotaryTensor {
@@ -41,15 +42,13 @@ struct RotaryArgs {
     int pos_type, axes, ends[GBSSIM_ROTARY_AXES];  // pairs up to and with each axis
     int batch, tokens, dim, pairs, adjacent;
     float sign;
-    int block_tokens;
 };
 
-// How a thread's eight columns find their partners.
+// How a thread's columns find their partners.
 enum Mode {
-    kHalves,     // a chunk of the first half and one of the second, n a multiple of 8
-    kAdjacent,   // neighbours: within the chunk
-    kWindow,     // eight columns anywhere else in the row, at any offset
-    kSingle      // a column a thread: any alignment
+    kHalves,    // V columns of the first half and V of the second
+    kAdjacent,  // neighbours, within eight columns
+    kSingle     // a pair or a column a thread: any alignment
 };
 
 // The fraction of a turn that a unit of position is, times 2^64.
@@ -60,7 +59,10 @@ __device__ __forceinline__ unsigned long long turn_fraction(double f)
     return t < 1.0 ? (unsigned long long)(t * 18446744073709551616.0) : 0ull;
 }
 
-// cos and sin of position x fraction.
+// cos and sin of position x fraction.  Where results are rounded to 16 bits (2^-8, 2^-11)
+// the hardware's approximations do, which are within 2^-21 over a turn; they take a
+// tenth of the instructions of the exact functions.
+template <bool EXACT>
 __device__ __forceinline__ float2 turn_of(const RotaryArgs &a, const void *pos, long long at, unsigned long long f)
 {
     unsigned long long phase;
@@ -78,55 +80,103 @@ __device__ __forceinline__ float2 turn_of(const RotaryArgs &a, const void *pos, 
         phase = (unsigned long long)(long long)whole * f + __umul64hi(f, (unsigned long long)part << 32);
         if (x < 0.0f) phase = 0ull - phase;
     }
+    const float turned = float(int(unsigned(phase >> 32)));  // 2^-31 half turns
     float s, c;
-    sincospif(float(int(unsigned(phase >> 32))) * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
+    if constexpr (EXACT)
+        sincospif(turned * 4.656612873077393e-10f, &s, &c);
+    else
+        __sincosf(turned * 1.4629180792671596e-9f, &s, &c);
     return make_float2(c, s * a.sign);
 }
 
-template <typename T>
-__device__ __forceinline__ Raw8<T> load8(const T *p)
+// V consecutive elements as they lie in memory: 4 to 32 bytes.
+template <typename T, int V>
+struct Words {
+    static constexpr int kWords = V * int(sizeof(T)) / 4;
+    uint32_t w[kWords];
+};
+
+template <typename T, int V>
+__device__ __forceinline__ Words<T, V> load(const T *p)
 {
-    Raw8<T> r;
-    const uint4 *const w = reinterpret_cast<const uint4 *>(p);
+    Words<T, V> r;
+    if constexpr (r.kWords >= 4) {
 #pragma unroll
-    for (int i = 0; i < int(sizeof(r.w) / 16); ++i) r.w[i] = ld_stream16(w + i);
+        for (int i = 0; i < r.kWords; i += 4) {
+            const uint4 x = ld_stream16(reinterpret_cast<const uint32_t *>(p) + i);
+            r.w[i] = x.x;
+            r.w[i + 1] = x.y;
+            r.w[i + 2] = x.z;
+            r.w[i + 3] = x.w;
+        }
+    } else if constexpr (r.kWords == 2) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+        r.w[0] = x.x;
+        r.w[1] = x.y;
+    } else {
+        r.w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    }
     return r;
 }
 
-// Eight columns of a row from `first` on, which may be any; those outside read zeros.
-template <typename T>
-__device__ __forceinline__ Raw8<T> load_window(const T *row, int first, int dim)
+template <typename T, int V>
+__device__ __forceinline__ void store(T *p, const Words<T, V> &r)
 {
-    constexpr int kWord = 16 / int(sizeof(T));
-    const int w0 = first >= 0 ? first / kWord : -((-first + kWord - 1) / kWord);
-    Wide8<T> wide;
+    if constexpr (r.kWords >= 4) {
 #pragma unroll
-    for (int i = 0; i < Wide8<T>::kUnits; ++i) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (w0 + i >= 0 && (w0 + i) * kWord < dim) w = reinterpret_cast<const uint4 *>(row)[w0 + i];
-        wide.w[4 * i] = w.x;
-        wide.w[4 * i + 1] = w.y;
-        wide.w[4 * i + 2] = w.z;
-        wide.w[4 * i + 3] = w.w;
+        for (int i = 0; i < r.kWords; i += 4)
+            reinterpret_cast<uint4 *>(p)[i / 4] = make_uint4(r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]);
+    } else if constexpr (r.kWords == 2) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
+    } else {
+        *reinterpret_cast<uint32_t *>(p) = r.w[0];
     }
-    return shift_down<T>(wide, first - w0 * kWord);
 }
 
-// Table of a token in shared memory: per column the factor of its own value and that
-// of its partner's, [2][dim] (kHalves, kAdjacent: per pair, [2][dim / 2 or pairs]).
-template <Mode M>
-__device__ __forceinline__ int table_width(const RotaryArgs &a)
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Words<T, V> &r, float (&v)[V])
 {
-    return M == kWindow ? a.dim : M == kAdjacent ? a.dim / 2 : a.pairs;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+        if constexpr (sizeof(T) == 4) {
+            v[i] = __uint_as_float(r.w[i]);
+            v[i + 1] = __uint_as_float(r.w[i + 1]);
+        } else {
+            const float2 x = unpack2<T>(r.w[i / 2]);
+            v[i] = x.x;
+            v[i + 1] = x.y;
+        }
+    }
 }
 
-template <typename T, Mode M>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a)
+template <typename T, int V>
+__device__ __forceinline__ Words<T, V> pack(const float (&v)[V])
 {
-    extern __shared__ __align__(16) float table[];
+    Words<T, V> r;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+        if constexpr (sizeof(T) == 4) {
+            r.w[i] = __float_as_uint(v[i]);
+            r.w[i + 1] = __float_as_uint(v[i + 1]);
+        } else {
+            r.w[i / 2] = pack2<T>(v[i], v[i + 1]);
+        }
+    }
+    return r;
+}
+
+// How the work is cut: a head's columns go to `lanes` threads, its token's heads in
+// turn to `parts` of them, so that neighbouring threads read neighbouring heads.
+struct Cut {
+    int lanes, parts;
+};
+
+template <typename T, Mode M, int V>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, const Cut cut)
+{
     __shared__ unsigned long long fraction[kMaxPairs];
     __shared__ unsigned char axis_of[kMaxPairs];
-    const int n = a.pairs, width = table_width<M>(a);
+    const int n = a.pairs;
     for (int i = threadIdx.x; i < n; i += kThreads) {
         int axis = 0;
         while (i >= a.ends[axis]) ++axis;
@@ -134,193 +184,196 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a)
         axis_of[i] = static_cast<unsigned char>(isfinite(f) ? axis : kNoAngle);
         fraction[i] = turn_fraction(f);
     }
-    const long long rows = (long long)a.batch * a.tokens;
-    // lanes of a head: chunks of eight columns (kHalves: of both halves), or columns
-    const int lanes = M == kHalves ? n / 8 + (a.dim - 2 * n) / 8 : M == kSingle ? a.dim - n : a.dim / 8;
-    const int teams = kThreads / min(lanes, kThreads);
-    const int team = threadIdx.x / lanes, lane0 = threadIdx.x - team * lanes;
-    const int heads = a.t[0].heads + a.t[1].heads;
-    const int groups = (heads + kHeadsAtOnce - 1) / kHeadsAtOnce;
-
-    for (long long base = (long long)blockIdx.x * a.block_tokens; base < rows;
-         base += (long long)gridDim.x * a.block_tokens) {
-        const int count = int(min((long long)a.block_tokens, rows - base));
-        __syncthreads();
-        for (int i = threadIdx.x; i < count * n; i += kThreads) {
-            const int t = i / n, p = i - t * n;
-            const long long row = base + t, b = row / a.tokens;
+    __syncthreads();
+    const int end = a.t[0].heads + a.t[1].heads, step = cut.parts;
+    const long long items = (long long)a.batch * a.tokens * cut.parts * cut.lanes;
+    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < items; i += (long long)gridDim.x * kThreads) {
+        long long row, b;
+        int lane, first;
+        if (items <= 0xffffffffLL) {  // divisions of 32 bits take a fifth of the time
+            const unsigned team = unsigned(i) / unsigned(cut.lanes), r = team / unsigned(cut.parts);
+            lane = int(unsigned(i) - team * cut.lanes);
+            first = int(team - r * cut.parts);
+            row = r;
+            b = r / unsigned(a.tokens);
+        } else {
+            const long long team = i / cut.lanes;
+            row = team / cut.parts;
+            lane = int(i - team * cut.lanes);
+            first = int(team - row * cut.parts);
+            b = row / a.tokens;
+        }
+        const long long token = row - b * a.tokens;
+        const long long pos = b * a.pos_batch + token * a.pos_token;
+        const auto turn = [&](int p) {
             const int axis = axis_of[p];
-            float2 cs = make_float2(NAN, NAN);
-            if (axis != kNoAngle)
-                cs = turn_of(a, a.positions, b * a.pos_batch + (row - b * a.tokens) * a.pos_token + axis,
-                             fraction[p]);
-            float *const own = table + 2 * t * width, *const other = own + width;
-            if constexpr (M == kWindow) {
-                own[p] = own[p + n] = cs.x;
-                other[p] = -cs.y;
-                other[p + n] = cs.y;
-            } else {
-                own[p] = cs.x;
-                other[p] = cs.y;
-            }
-        }
-        if constexpr (M == kWindow || M == kAdjacent) {  // columns without a position
-            const int turned = M == kWindow ? 2 * n : n, rest = width - turned;
-            for (int i = threadIdx.x; i < count * rest; i += kThreads) {
-                float *const own = table + 2 * (i / rest) * width + turned + i % rest;
-                own[0] = 1.0f;
-                own[width] = 0.0f;
-            }
-        }
-        __syncthreads();
-        if (team >= teams) continue;
-        for (int item = team; item < count * groups; item += teams) {
-            const int t = item / groups, first = (item - t * groups) * kHeadsAtOnce;
-            const long long row = base + t, b = row / a.tokens, token = row - b * a.tokens;
-            const float *const own = table + 2 * t * width, *const other = own + width;
-            const auto in = [&](int h) {
-                const RotaryTensor &x = h < a.t[0].heads ? a.t[0] : a.t[1];
-                return static_cast<const T *>(x.in) + b * x.batch + token * x.token +
-                       (h < a.t[0].heads ? h : h - a.t[0].heads) * x.head;
-            };
-            const auto out = [&](int h) {
-                const RotaryTensor &x = h < a.t[0].heads ? a.t[0] : a.t[1];
-                return static_cast<T *>(x.out) +
-                       (row * x.heads + (h < a.t[0].heads ? h : h - a.t[0].heads)) * a.dim;
-            };
-            if constexpr (M == kSingle) {
-                for (int lane = lane0; lane < a.dim - n; lane += kThreads) {
-                    const bool turned = lane < n;
-                    const int u = !turned ? lane + n : a.adjacent ? 2 * lane : lane;
-                    const int v = a.adjacent ? u + 1 : u + n;
-                    const float c = turned ? own[lane] : 1.0f, s = turned ? other[lane] : 0.0f;
-                    for (int h = first; h < min(first + kHeadsAtOnce, heads); ++h) {
-                        const T *const x = in(h);
-                        T *const y = out(h);
-                        if (!turned) {
-                            y[u] = x[u];
-                            continue;
-                        }
-                        const float xu = to_f32(x[u]), xv = to_f32(x[v]);
-                        y[u] = from_f32<T>(xu * c - xv * s);
-                        y[v] = from_f32<T>(xu * s + xv * c);
+            return axis == kNoAngle ? make_float2(NAN, NAN) : turn_of<sizeof(T) == 4>(a, a.positions, pos + axis, fraction[p]);
+        };
+        // the rows of this token's heads: the first tensor's, then the second's
+        const T *const in0 = static_cast<const T *>(a.t[0].in) + b * a.t[0].batch + token * a.t[0].token;
+        const T *const in1 = static_cast<const T *>(a.t[1].in) + b * a.t[1].batch + token * a.t[1].token;
+        T *const out0 = static_cast<T *>(a.t[0].out) + row * a.t[0].heads * a.dim;
+        T *const out1 = static_cast<T *>(a.t[1].out) + row * a.t[1].heads * a.dim;
+        const auto in = [&](int h) {
+            return h < a.t[0].heads ? in0 + h * a.t[0].head : in1 + (h - a.t[0].heads) * a.t[1].head;
+        };
+        const auto out = [&](int h) {
+            return h < a.t[0].heads ? out0 + h * a.dim : out1 + (h - a.t[0].heads) * a.dim;
+        };
+
+        if constexpr (M == kSingle) {
+            const bool turned = lane < n;
+            const int u = !turned ? lane + n : a.adjacent ? 2 * lane : lane;
+            const int v = a.adjacent ? u + 1 : u + n;
+            const float2 cs = turned ? turn(lane) : make_float2(1.0f, 0.0f);
+            constexpr int kGroup = 8;
+            for (int g = first; g < end; g += kGroup * step) {
+                T xu[kGroup], xv[kGroup];
+#pragma unroll
+                for (int e = 0; e < kGroup; ++e) {
+                    const int h = g + e * step;
+                    if (h >= end) continue;
+                    const T *const x = in(h);
+                    xu[e] = x[u];
+                    if (turned) xv[e] = x[v];
+                }
+#pragma unroll
+                for (int e = 0; e < kGroup; ++e) {
+                    const int h = g + e * step;
+                    if (h >= end) continue;
+                    T *const y = out(h);
+                    if (turned) {
+                        const float p = to_f32(xu[e]), q = to_f32(xv[e]);
+                        y[u] = from_f32<T>(p * cs.x - q * cs.y);
+                        y[v] = from_f32<T>(p * cs.y + q * cs.x);
+                    } else {
+                        y[u] = xu[e];
                     }
                 }
+            }
+        } else if constexpr (M == kHalves) {
+            const int chunks = n / V;
+            if (lane >= chunks) {  // columns without a position
+                const int at = 2 * n + (lane - chunks) * V;
+#pragma unroll 4
+                for (int h = first; h < end; h += step) store<T, V>(out(h) + at, load<T, V>(in(h) + at));
                 continue;
             }
-            const int lane = lane0;
-            if constexpr (M == kHalves) {
-                const int chunks = n / 8;
-                if (lane >= chunks) {  // columns without a position
-                    const int at = 2 * n + (lane - chunks) * 8;
+            // two buffers, so that a group's loads are under way while the last one is turned
+            Words<T, V> u[2][kHeadsAtOnce], v[2][kHeadsAtOnce];
+            const auto fetch = [&](int h, int buf) {
 #pragma unroll
-                    for (int i = 0; i < kHeadsAtOnce; ++i)
-                        if (first + i < heads) st8<T>(out(first + i) + at, load8<T>(in(first + i) + at));
-                    continue;
-                }
-                float c[8], s[8];
-#pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(own + lane * 8 + e);
-                    const float4 y = *reinterpret_cast<const float4 *>(other + lane * 8 + e);
-                    c[e] = x.x; c[e + 1] = x.y; c[e + 2] = x.z; c[e + 3] = x.w;
-                    s[e] = y.x; s[e + 1] = y.y; s[e + 2] = y.z; s[e + 3] = y.w;
-                }
-                Raw8<T> u[kHeadsAtOnce], v[kHeadsAtOnce];
-#pragma unroll
-                for (int i = 0; i < kHeadsAtOnce; ++i)
-                    if (first + i < heads) {
-                        u[i] = load8<T>(in(first + i) + lane * 8);
-                        v[i] = load8<T>(in(first + i) + n + lane * 8);
+                for (int e = 0; e < kHeadsAtOnce; ++e)
+                    if (h + e * step < end) {
+                        const T *const x = in(h + e * step) + lane * V;
+                        u[buf][e] = load<T, V>(x);
+                        v[buf][e] = load<T, V>(x + n);
                     }
+            };
+            float c[V], s[V];
+            const auto turn_heads = [&](int h, int buf) {
 #pragma unroll
-                for (int i = 0; i < kHeadsAtOnce; ++i)
-                    if (first + i < heads) {
-                        float x[8], y[8], p[8], q[8];
-                        unpack8<T>(u[i], x);
-                        unpack8<T>(v[i], y);
+                for (int e = 0; e < kHeadsAtOnce; ++e)
+                    if (h + e * step < end) {
+                        float x[V], y[V], p[V], q[V];
+                        unpack<T, V>(u[buf][e], x);
+                        unpack<T, V>(v[buf][e], y);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            p[e] = x[e] * c[e] - y[e] * s[e];
-                            q[e] = x[e] * s[e] + y[e] * c[e];
+                        for (int j = 0; j < V; ++j) {
+                            p[j] = x[j] * c[j] - y[j] * s[j];
+                            q[j] = x[j] * s[j] + y[j] * c[j];
                         }
-                        T *const to = out(first + i) + lane * 8;
-                        st8<T>(to, pack8<T>(p));
-                        st8<T>(to + n, pack8<T>(q));
+                        T *const to = out(h + e * step) + lane * V;
+                        store<T, V>(to, pack<T, V>(p));
+                        store<T, V>(to + n, pack<T, V>(q));
                     }
-            } else if constexpr (M == kAdjacent) {
-                const float4 c = *reinterpret_cast<const float4 *>(own + lane * 4);
-                const float4 s = *reinterpret_cast<const float4 *>(other + lane * 4);
-                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-                Raw8<T> u[kHeadsAtOnce];
+            };
+            fetch(first, 0);
 #pragma unroll
-                for (int i = 0; i < kHeadsAtOnce; ++i)
-                    if (first + i < heads) u[i] = load8<T>(in(first + i) + lane * 8);
+            for (int e = 0; e < V; ++e) {
+                const float2 cs = turn(lane * V + e);
+                c[e] = cs.x;
+                s[e] = cs.y;
+            }
+            const int group = kHeadsAtOnce * step;
+            for (int h = first; h < end; h += 2 * group) {
+                fetch(h + group, 1);
+                turn_heads(h, 0);
+                fetch(h + 2 * group, 0);
+                turn_heads(h + group, 1);
+            }
+        } else {
+            Words<T, 8> u[2][kHeadsAtOnce];
+            const auto fetch = [&](int h, int buf) {
 #pragma unroll
-                for (int i = 0; i < kHeadsAtOnce; ++i)
-                    if (first + i < heads) {
+                for (int e = 0; e < kHeadsAtOnce; ++e)
+                    if (h + e * step < end) u[buf][e] = load<T, 8>(in(h + e * step) + lane * 8);
+            };
+            float c[4], s[4];
+            // a pair without a position is turned by nothing; it has to keep a NaN to itself
+            const int here = min(max(n - lane * 4, 0), 4);
+            const auto turn_heads = [&](int h, int buf) {
+#pragma unroll
+                for (int e = 0; e < kHeadsAtOnce; ++e)
+                    if (h + e * step < end) {
                         float x[8], p[8];
-                        unpack8<T>(u[i], x);
+                        unpack<T, 8>(u[buf][e], x);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            p[2 * e] = x[2 * e] * cc[e] - x[2 * e + 1] * ss[e];
-                            p[2 * e + 1] = x[2 * e] * ss[e] + x[2 * e + 1] * cc[e];
+                        for (int j = 0; j < 4; ++j) {
+                            p[2 * j] = j < here ? x[2 * j] * c[j] - x[2 * j + 1] * s[j] : x[2 * j];
+                            p[2 * j + 1] = j < here ? x[2 * j] * s[j] + x[2 * j + 1] * c[j] : x[2 * j + 1];
                         }
-                        st8<T>(out(first + i) + lane * 8, pack8<T>(p));
+                        store<T, 8>(out(h + e * step) + lane * 8, pack<T, 8>(p));
                     }
-            } else if constexpr (M == kWindow) {
-                const int at = lane * 8;
-                float c[8], s[8];
+            };
+            fetch(first, 0);
 #pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(own + at + e);
-                    const float4 y = *reinterpret_cast<const float4 *>(other + at + e);
-                    c[e] = x.x; c[e + 1] = x.y; c[e + 2] = x.z; c[e + 3] = x.w;
-                    s[e] = y.x; s[e + 1] = y.y; s[e + 2] = y.z; s[e + 3] = y.w;
-                }
-                const bool up = at < n, down = at + 8 > n && at < 2 * n;
-                for (int h = first; h < min(first + kHeadsAtOnce, heads); ++h) {
-                    const T *const row_in = in(h);
-                    float x[8], y[8], z[8];
-                    unpack8<T>(load8<T>(row_in + at), x);
-                    if (up) unpack8<T>(load_window<T>(row_in, at + n, a.dim), y);
-                    if (down) unpack8<T>(load_window<T>(row_in, at - n, a.dim), z);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int j = at + e;
-                        // a column without a position keeps its value, whatever lies beside it
-                        if (j < 2 * n) x[e] = x[e] * c[e] + (j < n ? y[e] : z[e]) * s[e];
-                    }
-                    st8<T>(out(h) + at, pack8<T>(x));
-                }
+            for (int e = 0; e < 4; ++e) {
+                const float2 cs = e < here ? turn(lane * 4 + e) : make_float2(1.0f, 0.0f);
+                c[e] = cs.x;
+                s[e] = cs.y;
+            }
+            const int group = kHeadsAtOnce * step;
+            for (int h = first; h < end; h += 2 * group) {
+                fetch(h + group, 1);
+                turn_heads(h, 0);
+                fetch(h + 2 * group, 0);
+                turn_heads(h + group, 1);
             }
         }
     }
 }
 
-template <typename T, Mode M>
-cudaError_t launch(RotaryArgs a, cudaStream_t stream)
+template <typename T, Mode M, int V>
+cudaError_t launch(const RotaryArgs &a, cudaStream_t stream)
 {
-    const int width = M == kWindow ? a.dim : M == kAdjacent ? a.dim / 2 : a.pairs;
     const long long rows = (long long)a.batch * a.tokens;
-    // enough blocks for eight on each SM before a block takes more than a token
-    constexpr int kMostTokens = 16, kBlocks = 152 * 8;
-    a.block_tokens = int(std::min<long long>({kMostTokens, std::max<long long>(1, rows / kBlocks),
-                                              std::max(1, 4096 / width)}));
-    const long long blocks = std::min<long long>(ceil_div(rows, a.block_tokens), kBlocks);
-    const size_t smem = size_t(2) * a.block_tokens * width * sizeof(float);
-    rotary_kernel<T, M><<<unsigned(blocks), kThreads, smem, stream>>>(a);
+    const int heads = a.t[0].heads + a.t[1].heads;
+    Cut cut;
+    cut.lanes = M == kHalves ? a.pairs / V + (a.dim - 2 * a.pairs) / V : M == kSingle ? a.dim - a.pairs : a.dim / V;
+    // Few tokens: threads share a token's heads, four each at least, until they fill the
+    // GPU.  Many: one thread for all of them, which forms their sines and cosines once
+    // (65536 x 20 heads of 128, bfloat16: one thread 129 us, two 136, four 152), but two
+    // in float32, whose rows are twice as long (32400 x 24 heads of 88: 121, 108).
+    constexpr long long kRoom = 152LL * 1024;
+    const long long most = std::max(1, heads / 4), wanted = ceil_div(kRoom, rows * cut.lanes);
+    cut.parts = int(std::min(most, std::max<long long>(wanted, sizeof(T) == 4 ? 2 : 1)));
+    const long long items = rows * cut.lanes * cut.parts;
+    const long long blocks = std::min<long long>(ceil_div(items, kThreads), 1 << 20);
+    rotary_kernel<T, M, V><<<unsigned(blocks), kThreads, 0, stream>>>(a, cut);
     return cudaGetLastError();
 }
 
+// v: columns that a thread may take at once.
 template <typename T>
-cudaError_t launch_mode(const RotaryArgs &a, Mode m, cudaStream_t stream)
+cudaError_t launch_mode(const RotaryArgs &a, int v, cudaStream_t stream)
 {
-    switch (m) {
-    case kHalves: return launch<T, kHalves>(a, stream);
-    case kAdjacent: return launch<T, kAdjacent>(a, stream);
-    case kWindow: return launch<T, kWindow>(a, stream);
-    default: return launch<T, kSingle>(a, stream);
+    if (a.adjacent) return v == 8 ? launch<T, kAdjacent, 8>(a, stream) : launch<T, kSingle, 1>(a, stream);
+    switch (v) {
+    case 8: return launch<T, kHalves, 8>(a, stream);
+    case 4: return launch<T, kHalves, 4>(a, stream);
+    case 2: return launch<T, kHalves, 2>(a, stream);
+    default: return launch<T, kSingle, 1>(a, stream);
     }
 }
 
@@ -350,13 +403,28 @@ int check_heads(const gbssim_rotary &d, const gbssim_heads &t, int heads)
     return reinterpret_cast<uintptr_t>(t.data) % dtype_bytes(d.dtype) ? GBSSIM_EALIGN : GBSSIM_OK;
 }
 
-bool whole_words(const gbssim_rotary &d, const gbssim_heads &t, const void *out, int heads)
+// Whether every row of the tensor and of its output starts on a multiple of `bytes`.
+bool aligned(const gbssim_rotary &d, const gbssim_heads &t, const void *out, int heads, int bytes)
 {
     if (!heads) return true;
-    const int word = 16 / dtype_bytes(d.dtype);
-    return reinterpret_cast<uintptr_t>(t.data) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
-           (d.batch < 2 || t.batch_stride % word == 0) && (d.tokens < 2 || t.token_stride % word == 0) &&
-           (heads < 2 || t.head_stride % word == 0);
+    const int size = dtype_bytes(d.dtype);
+    const auto on = [&](long long n) { return n * size % bytes == 0; };
+    return reinterpret_cast<uintptr_t>(t.data) % bytes == 0 && reinterpret_cast<uintptr_t>(out) % bytes == 0 &&
+           on(d.dim) && (d.batch < 2 || on(t.batch_stride)) && (d.tokens < 2 || on(t.token_stride)) &&
+           (heads < 2 || on(t.head_stride));
+}
+
+// How many columns a thread can take at once: as many as both halves, the rest of a row
+// and the alignment of every row allow.
+int columns(const gbssim_rotary &d, int pairs, const void *q_out, const void *k_out)
+{
+    const bool adjacent = d.layout == GBSSIM_ROTARY_ADJACENT;
+    for (int v = adjacent ? 8 : 4; v > 1; v /= 2) {
+        const int bytes = std::min(16, v * dtype_bytes(d.dtype));
+        if (d.dim % v || (!adjacent && (pairs % v || (d.dim - 2 * pairs) % v))) continue;
+        if (aligned(d, d.q, q_out, d.q_heads, bytes) && aligned(d, d.k, k_out, d.k_heads, bytes)) return v;
+    }
+    return 1;
 }
 
 }  // namespace
@@ -416,11 +484,9 @@ extern "C" int gbssim_rotary_turn(const gbssim_rotary *d, void *q_out, void *k_o
     a.dim = d->dim;
     a.adjacent = d->layout == GBSSIM_ROTARY_ADJACENT;
     a.sign = d->inverse ? -1.0f : 1.0f;
-    Mode m = kSingle;
-    if (d->dim % 8 == 0 && whole_words(*d, d->q, q_out, d->q_heads) && whole_words(*d, d->k, k_out, d->k_heads))
-        m = a.adjacent ? kAdjacent : a.pairs % 8 == 0 ? kHalves : kWindow;
+    const int v = columns(*d, a.pairs, q_out, k_out);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return cuda_fail(d->dtype == GBSSIM_F32    ? launch_mode<float>(a, m, st)
-                     : d->dtype == GBSSIM_BF16 ? launch_mode<bf16>(a, m, st)
-                                               : launch_mode<f16>(a, m, st));
+    return cuda_fail(d->dtype == GBSSIM_F32    ? launch_mode<float>(a, v, st)
+                     : d->dtype == GBSSIM_BF16 ? launch_mode<bf16>(a, v, st)
+                                               : launch_mode<f16>(a, v, st));
 }

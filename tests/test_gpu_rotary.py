@@ -2,7 +2,9 @@
 
 Tolerance: the angle, a fraction of a half turn rounded to float32, is off by at most
 pi 2^-25, sine and cosine by 2^-23 more (two units in the last place), the two products
-and their sum by 3 2^-24: less than 2^-21 (|u| + |v|) together.  For positions x and
+and their sum by 3 2^-24: less than 2^-21 (|u| + |v|) together.  16-bit types take the
+hardware's sine and cosine, off by 2^-21.1 at most between -pi and pi: less than 2^-20
+(|u| + |v|) together.  For positions x and
 frequencies f, f / (2 pi) in float64 loses 2^-52 x f, the fraction of 2^64 another 2^-61
 x, a float32 position's cut 2^-32 f.  The result is rounded once: half a step of its type.
 """
@@ -45,7 +47,7 @@ def definition(x, positions, frequencies, pairs, layout, sign=1.0):
     out[..., columns[1]] = u * sin + v * cos
     far = (at.abs() * (frequencies.abs() * 2.0 ** -51 + 2.0 ** -61) +
            frequencies.abs() * 2.0 ** -32)[..., None, :]
-    size = (2.0 ** -21 + far) * (u.abs() + v.abs())
+    size = (2.0 ** (-21 if x.dtype == F32 else -20) + far) * (u.abs() + v.abs())
     bound[..., columns[0]] = bound[..., columns[1]] = size
     u = torch.finfo(x.dtype).eps / 2
     rounding = u * out.abs() + (2.0 ** -25 if x.dtype == HF else 0.0)
