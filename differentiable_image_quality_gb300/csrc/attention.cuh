@@ -204,6 +204,8 @@ struct AttnBwdArgs {
     AttnShape s;
     float scale, scale_log2;
     int q_tiles, k_tiles;  // in all samples, or the most there can be (packed)
+    unsigned key_items, items;  // of all blocks: tiles of keys, and with those of queries
+    int queries_wanted;
     int ragged;
     unsigned extra;  // test hook, see gbssim_tune_attention
     // for the row sums

@@ -283,6 +283,9 @@ extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_head
     a.dq = queries ? grad_q_or_null : nullptr;
     a.dk = keys ? grad_k_or_null : nullptr;
     a.dv = keys ? grad_v_or_null : nullptr;
+    a.key_items = a.dk || a.dv ? unsigned(k_tiles * d->kv_heads) : 0;
+    a.queries_wanted = a.dq != nullptr;
+    a.items = a.key_items + (a.dq ? unsigned(q_tiles * d->heads) : 0);
     a.stats = static_cast<float *>(workspace);
     a.largest = queries ? reinterpret_cast<unsigned *>(a.stats + size_t(d->heads) * q_tiles * 2 * kAttnTile) : nullptr;
     return cuda_fail(attention_bwd_launch(a, d->dtype, static_cast<cudaStream_t>(stream)));

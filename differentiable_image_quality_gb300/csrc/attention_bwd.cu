@@ -152,12 +152,60 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
 
 constexpr int kBwdThreads = 320;  // eight warps on the tiles, one copies, one issues products
 
+// Barriers of one of the two kinds of work.  Each goes from item to item with its
+// phases running on.
+struct BwdBarriers {
+    uint64_t own_full, own_empty, full[8], empty[8], s_full[2], dp_full, p_full, ds_full, done, patched;
+};
+
 struct BwdShared {
-    uint64_t own_full, full[8], empty[8], s_full[2], dp_full, p_full, ds_full, done, patched, drained;
-    AttnPlace place;
-    int there;
+    BwdBarriers keys, queries;
+    uint64_t keys_stored, drained;
     unsigned tmem, failed;
 };
+
+// An item: a tile of keys of a key head, or of queries of a head.
+struct BwdItem {
+    AttnPlace pl;
+    bool there;
+    int head;
+};
+
+// The n-th item of this block; to and fro, so that falling work evens out.  Those of
+// keys come first.
+__device__ __forceinline__ unsigned item_of(unsigned n)
+{
+    return n * gridDim.x + (n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// By a whole warp.  Causal: falling work, that of the first keys and of the last queries
+// before the others; else a head's items one after another, which share its tiles in
+// L2.
+template <bool KEYS>
+__device__ __forceinline__ void find_item(const AttnBwdArgs &a, unsigned u, BwdItem &w)
+{
+    const AttnShape &s = a.s;
+    if (!KEYS) u -= a.key_items;
+    const int all = KEYS ? a.k_tiles : a.q_tiles;
+    int index;
+    if (s.causal) {
+        const int heads = KEYS ? s.kv_heads : s.heads;
+        w.head = u % heads;
+        const int i = u / heads;
+        if (s.packed) {
+            index = KEYS ? i : all - 1 - i;
+        } else {
+            const int tiles = all / s.sequences;
+            const int tile = KEYS ? i / s.sequences : tiles - 1 - i / s.sequences;
+            index = i % s.sequences * tiles + tile;
+        }
+    } else {
+        w.head = u / all;
+        index = u % all;
+    }
+    w.there = find_place<KEYS>(s, index, kAttnTile, w.pl);
+    if (!w.there) w.pl = {};  // packed: fewer tiles than there could be
+}
 
 template <int DP>
 constexpr int key_stages()  // pairs of a query tile and its gradient
@@ -248,363 +296,433 @@ __device__ __forceinline__ void store_row(unsigned at, int from, int to, float s
 // queries.  Tensor memory: scores, then p in their place; dp, then ds in its place;
 // dv; dk.  While the warps form p of a tile, the products of ds of the last one run;
 // while they form ds, those of p and the next scores.
+struct KeySpan {
+    int first;        // key
+    int from, all;    // tiles of queries: from the first that sees the first key
+    int total;        // of all heads of the group
+};
+
+__device__ __forceinline__ KeySpan key_span(const AttnShape &s, const BwdItem &w)
+{
+    KeySpan k;
+    k.first = w.pl.tile * kAttnTile;
+    k.all = (w.pl.queries + kAttnTile - 1) / kAttnTile;
+    k.from = s.causal ? min(max(k.first - w.pl.shift, 0) / kAttnTile, k.all) : 0;
+    k.total = w.there && k.first < w.pl.keys ? (k.all - k.from) * s.group : 0;
+    return k;
+}
+
 template <typename T, int DP>
-__device__ void by_keys(const AttnBwdArgs &a, char *base, BwdShared &sh, int kv_head)
+__device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdShared &sh, int warp, unsigned tmem,
+                                        unsigned &n, bool &ok)
 {
     constexpr int kTile = tile_bytes<DP>();
     constexpr int kStages = key_stages<DP>();
     const AttnShape &s = a.s;
-    const AttnPlace pl = sh.place;
+    BwdBarriers &bar = sh.keys;
     volatile unsigned *const failed = &sh.failed;
-    const unsigned tmem = uniform(sh.tmem);
     const unsigned s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 256 + DP;
     char *const ring = base + 2 * kTile;
     char *const ring_stats = ring + 2 * kStages * kTile;
-    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
-
-    const int first = pl.tile * kAttnTile;  // key
-    const int all = (pl.queries + kAttnTile - 1) / kAttnTile;
-    // the first tile of queries that sees the first key
-    const int from = s.causal ? min(max(first - pl.shift, 0) / kAttnTile, all) : 0;
-    const int tiles = all - from, total = first < pl.keys ? tiles * s.group : 0;
+    const int lane = threadIdx.x % 32;
 
     if (warp == 8) {
-        int issued = 0;
-        if (lane == 0 && total > 0) {
-            mbar_arrive_expect_tx(&sh.own_full, 2 * kTile + a.extra);
-            load_tile<DP>(base, &a.k, kv_head, pl.k_row + first, pl.batch, &sh.own_full);
-            load_tile<DP>(base + kTile, &a.v, kv_head, pl.k_row + first, pl.batch, &sh.own_full);
+        int it = 0;
+        unsigned uses = 0, patches = 0;
+        for (unsigned u; ok && (u = item_of(n)) < a.key_items; ++n) {
+            BwdItem w;
+            find_item<true>(a, u, w);
+            const KeySpan k = key_span(s, w);
+            const AttnPlace &pl = w.pl;
+            for (int i = 0, g = 0, t = k.from; ok && i < k.total; ++i, ++it) {
+                // the ring runs on while the last item's keys are still in use; they are
+                // asked for before the ring would wait for their products
+                if (i == min(kStages - 1, k.total - 1)) {
+                    if (uses > 0) ok = attn_wait_warp(&bar.own_empty, (uses - 1) & 1, failed);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bar.own_full, 2 * kTile + a.extra);
+                        load_tile<DP>(base, &a.k, w.head, pl.k_row + k.first, pl.batch, &bar.own_full);
+                        load_tile<DP>(base + kTile, &a.v, w.head, pl.k_row + k.first, pl.batch, &bar.own_full);
+                    }
+                    ++uses;
+                }
+                const int stage = it % kStages, head = w.head * s.group + g;
+                if (it >= kStages) ok = attn_wait_warp(&bar.empty[stage], (it / kStages - 1) & 1, failed);
+                if (!ok) break;
+                // rows behind the sequence's are another's: zeros in their place
+                const int rows = pl.queries - t * kAttnTile;
+                const bool patch = s.packed && rows < kAttnTile;
+                char *const tile = ring + 2 * stage * kTile;
+                if (lane == 0) {
+                    uint64_t *const to = patch ? &bar.patched : &bar.full[stage];
+                    mbar_arrive_expect_tx(to, 2 * kTile + kStatsBytes);
+                    load_tile<DP>(tile, &a.q, head, pl.q_row + t * kAttnTile, pl.batch, to);
+                    load_tile<DP>(tile + kTile, &a.g, head, pl.q_row + t * kAttnTile, pl.batch, to);
+                    bulk_load(ring_stats + stage * kStatsBytes,
+                              a.stats + ((long long)head * a.q_tiles + pl.q_tiles_before + t) * 2 * kAttnTile,
+                              kStatsBytes, to);
+                }
+                if (patch) {
+                    ok = attn_wait_warp(&bar.patched, patches++ & 1, failed);
+                    zero_rows<DP>(tile, rows);
+                    zero_rows<DP>(tile + kTile, rows);
+                    fence_proxy();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.full[stage]);
+                }
+                if (++t == k.all) {
+                    t = k.from;
+                    ++g;
+                }
+            }
         }
-        bool ok = true;
-        int patches = 0;
-        for (int it = 0, g = 0, t = from; ok && it < total; ++it) {
-            const int stage = it % kStages, head = kv_head * s.group + g;
-            if (it >= kStages) ok = attn_wait_warp(&sh.empty[stage], (it / kStages - 1) & 1, failed);
-            if (!ok) break;
-            // rows behind the sequence's are another's: zeros in their place
-            const int rows = pl.queries - t * kAttnTile;
-            const bool patch = s.packed && rows < kAttnTile;
-            char *const tile = ring + 2 * stage * kTile;
-            if (lane == 0) {
-                uint64_t *const bar = patch ? &sh.patched : &sh.full[stage];
-                mbar_arrive_expect_tx(bar, 2 * kTile + kStatsBytes);
-                load_tile<DP>(tile, &a.q, head, pl.q_row + t * kAttnTile, pl.batch, bar);
-                load_tile<DP>(tile + kTile, &a.g, head, pl.q_row + t * kAttnTile, pl.batch, bar);
-                bulk_load(ring_stats + stage * kStatsBytes,
-                          a.stats + ((long long)head * a.q_tiles + pl.q_tiles_before + t) * 2 * kAttnTile,
-                          kStatsBytes, bar);
-            }
-            if (patch) {
-                ok = attn_wait_warp(&sh.patched, patches++ & 1, failed);
-                zero_rows<DP>(tile, rows);
-                zero_rows<DP>(tile + kTile, rows);
-                fence_proxy();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.full[stage]);
-            }
-            issued = it + 1;
-            if (++t == all) {
-                t = from;
-                ++g;
-            }
-        }
-        if (*failed && lane == 0) {
-            if (total > 0) mbar_wait_bounded(&sh.own_full, 0, kAttnDrainCycles);
-            for (int it = max(0, issued - kStages); it < issued; ++it)
-                mbar_wait_bounded(&sh.full[it % kStages], (it / kStages) & 1, kAttnDrainCycles);
-            atomicOr(&g_attention_status, 4u);
+        if (!ok) {
+            if (uses > 0) mbar_wait_bounded(&bar.own_full, (uses - 1) & 1, kAttnDrainCycles);
+            for (int i = max(0, it - kStages); i < it; ++i)
+                mbar_wait_bounded(&bar.full[i % kStages], (i / kStages) & 1, kAttnDrainCycles);
+        } else if (uses > 0 && a.queries_wanted) {
+            // the other kind's tiles take the place of these
+            ok = attn_wait_warp(&bar.own_empty, (uses - 1) & 1, failed);
         }
     } else if (warp == 9) {
-        if (total > 0) {
-            const unsigned leader = elect_leader();
-            const int steps = (s.dim + 15) / 16;
-            const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
-            const unsigned s_full = smem_u32(sh.s_full), dp_full = smem_u32(&sh.dp_full), empty = smem_u32(sh.empty);
-            const Desc k_tile = desc_k(smem_u32(base)), v_tile = advance(k_tile, kTile);
-            const Desc ring_k = desc_k(smem_u32(ring)), ring_mn = desc_mn(smem_u32(ring));
-            bool ok = attn_wait_warp(&sh.own_full, 0, failed) && attn_wait_warp(&sh.full[0], 0, failed);
-            if (ok) {
-                product_k<DP / 16>(s_at, k_tile, ring_k, steps, id_s, leader);
-                commit(s_full, leader);
-                product_k<DP / 16>(dp_at, v_tile, advance(ring_k, kTile), steps, id_s, leader);
-                commit(dp_full, leader);
-            }
-            for (int it = 0; ok && it < total; ++it) {
-                const Desc tile = advance(ring_mn, 2 * (it % kStages) * kTile);
-                const int nx = (it + 1) % kStages;
-                const Desc next = advance(ring_k, 2 * nx * kTile);
+        const unsigned leader = elect_leader();
+        const int steps = (s.dim + 15) / 16;
+        const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
+        const unsigned s_full = smem_u32(bar.s_full), dp_full = smem_u32(&bar.dp_full), empty = smem_u32(bar.empty);
+        const Desc k_tile = desc_k(smem_u32(base)), v_tile = advance(k_tile, kTile);
+        const Desc ring_k = desc_k(smem_u32(ring)), ring_mn = desc_mn(smem_u32(ring));
+        RingAt<kStages> at;
+        unsigned uses = 0, phase = 0;
+        for (unsigned u; ok && (u = item_of(n)) < a.key_items; ++n) {
+            BwdItem w;
+            find_item<true>(a, u, w);
+            const int total = key_span(s, w).total;
+            if (total == 0) continue;
+            ok = attn_wait_warp(&bar.own_full, uses++ & 1, failed) &&
+                 attn_wait_warp(&bar.full[at.slot], at.parity, failed);
+            if (!ok) break;
+            fence_after();
+            product_k<DP / 16>(s_at, k_tile, advance(ring_k, 2 * at.slot * kTile), steps, id_s, leader);
+            commit(s_full, leader);
+            product_k<DP / 16>(dp_at, v_tile, advance(ring_k, (2 * at.slot + 1) * kTile), steps, id_s, leader);
+            commit(dp_full, leader);
+            for (int it = 0; it < total; ++it, phase ^= 1) {
+                const int slot = at.slot;
+                const Desc tile = advance(ring_mn, 2 * slot * kTile);
+                at.next();
+                const Desc next = advance(ring_k, 2 * at.slot * kTile);
                 const bool more = it + 1 < total;
-                if (!(ok = attn_wait_warp(&sh.p_full, it & 1, failed))) break;
+                if (!(ok = attn_wait_warp(&bar.p_full, phase, failed))) break;
                 fence_after();
                 product_rows<64>(dv_at, s_at, advance(tile, kTile), id_d, it > 0, leader);
                 if (more) {
-                    if (!(ok = attn_wait_warp(&sh.full[nx], ((it + 1) / kStages) & 1, failed))) break;
+                    if (!(ok = attn_wait_warp(&bar.full[at.slot], at.parity, failed))) break;
                     product_k<DP / 16>(s_at, k_tile, next, steps, id_s, leader);
                     commit(s_full, leader);
                 }
-                if (!(ok = attn_wait_warp(&sh.ds_full, it & 1, failed))) break;
+                if (!(ok = attn_wait_warp(&bar.ds_full, phase, failed))) break;
                 fence_after();
                 product_rows<64>(dk_at, dp_at, tile, id_d, it > 0, leader);
-                commit(empty + 8 * (it % kStages), leader);
+                commit(empty + 8 * slot, leader);
                 if (more) {
                     product_k<DP / 16>(dp_at, v_tile, advance(next, kTile), steps, id_s, leader);
                     commit(dp_full, leader);
                 }
             }
-            if (ok) {
-                commit(smem_u32(&sh.done), leader);
-            } else {
-                commit(smem_u32(&sh.drained), leader);
-                mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
-            }
+            if (!ok) break;
+            commit(smem_u32(&bar.done), leader);
+            commit(smem_u32(&bar.own_empty), leader);
         }
     } else {
         const int half = warp / 4, row = threadIdx.x % 128;
         const unsigned lanes = unsigned(warp % 4) << 21;
         const unsigned my_s = s_at + lanes + half * 64, my_dp = dp_at + lanes + half * 64;
-        const int key = first + row;
-        const Scales sc = scales_of<T>(a, kv_head);
         const f32x2 c2 = both(a.scale_log2);
-        bool ok = true;
-        for (int it = 0, t = from; it < total; ++it) {
-            const int stage = it % kStages;
-            const float *const stats = reinterpret_cast<const float *>(ring_stats + stage * kStatsBytes) + half * 64;
-            // columns before `hidden` are queries that do not see this key
-            const int hidden = key >= pl.keys ? 64
-                               : s.causal     ? key - pl.shift - t * kAttnTile - half * 64
-                                              : 0;
-            const bool masked = __any_sync(0xffffffffu, hidden > 0);
-            ok = attn_wait_warp(&sh.full[stage], (it / kStages) & 1, failed) &&
-                 attn_wait_warp(&sh.s_full[0], it & 1, failed);
-            if (!ok) break;
-            fence_after();
-            float p[64];
-            ld32(my_s, reinterpret_cast<uint32_t *>(p));
-            ld32(my_s + 32, reinterpret_cast<uint32_t *>(p) + 32);
-            wait_ld();
+        RingAt<kStages> at;
+        unsigned uses = 0, phase = 0;
+        for (unsigned u; (u = item_of(n)) < a.key_items; ++n) {
+            BwdItem w;
+            find_item<true>(a, u, w);
+            const KeySpan k = key_span(s, w);
+            const AttnPlace &pl = w.pl;
+            const int key = k.first + row;
+            const Scales sc = scales_of<T>(a, w.head);
+            for (int it = 0, t = k.from; ok && it < k.total; ++it, phase ^= 1) {
+                const float *const stats =
+                    reinterpret_cast<const float *>(ring_stats + at.slot * kStatsBytes) + half * 64;
+                // columns before `hidden` are queries that do not see this key
+                const int hidden = key >= pl.keys ? 64
+                                   : s.causal     ? key - pl.shift - t * kAttnTile - half * 64
+                                                  : 0;
+                const bool masked = __any_sync(0xffffffffu, hidden > 0);
+                ok = attn_wait_warp(&bar.full[at.slot], at.parity, failed) &&
+                     attn_wait_warp(&bar.s_full[0], phase, failed);
+                if (!ok) break;
+                at.next();
+                fence_after();
+                float p[64];
+                ld32(my_s, reinterpret_cast<uint32_t *>(p));
+                ld32(my_s + 32, reinterpret_cast<uint32_t *>(p) + 32);
+                wait_ld();
 #pragma unroll
-            for (int i = 0; i < 64; i += 4) {
-                const float4 l = *reinterpret_cast<const float4 *>(stats + i);
-                const float2 x = halves(fma2(pair(p[i], p[i + 1]), c2, pair(l.x, l.y)));
-                const float2 y = halves(fma2(pair(p[i + 2], p[i + 3]), c2, pair(l.z, l.w)));
-                p[i] = exp2_fast(x.x);
-                p[i + 1] = exp2_fast(x.y);
-                p[i + 2] = exp2_fast(y.x);
-                p[i + 3] = exp2_fast(y.y);
-            }
-            if (masked) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) p[i] = i < hidden ? 0.0f : p[i];
-            }
-            store_half<T>(my_s, p);
-            wait_st();
-            fence_before();
-            mbar_arrive(&sh.p_full);
-            ok = attn_wait_warp(&sh.dp_full, it & 1, failed);
-            if (!ok) break;
-            fence_after();
-            float d[64];
-            ld32(my_dp, reinterpret_cast<uint32_t *>(d));
-            ld32(my_dp + 32, reinterpret_cast<uint32_t *>(d) + 32);
-            wait_ld();
-#pragma unroll
-            for (int i = 0; i < 64; i += 4) {
-                const float4 n = *reinterpret_cast<const float4 *>(stats + kAttnTile + i);
-                f32x2 x = add2(pair(d[i], d[i + 1]), pair(n.x, n.y));
-                f32x2 y = add2(pair(d[i + 2], d[i + 3]), pair(n.z, n.w));
-                if constexpr (kScaled<T>) {
-                    x = mul2(x, both(sc.ds));
-                    y = mul2(y, both(sc.ds));
+                for (int i = 0; i < 64; i += 4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(stats + i);
+                    const float2 x = halves(fma2(pair(p[i], p[i + 1]), c2, pair(l.x, l.y)));
+                    const float2 y = halves(fma2(pair(p[i + 2], p[i + 3]), c2, pair(l.z, l.w)));
+                    p[i] = exp2_fast(x.x);
+                    p[i + 1] = exp2_fast(x.y);
+                    p[i + 2] = exp2_fast(y.x);
+                    p[i + 3] = exp2_fast(y.y);
                 }
-                const float2 u = halves(mul2(x, pair(p[i], p[i + 1])));
-                const float2 w = halves(mul2(y, pair(p[i + 2], p[i + 3])));
-                d[i] = u.x;
-                d[i + 1] = u.y;
-                d[i + 2] = w.x;
-                d[i + 3] = w.y;
-            }
-            if (masked) {
+                if (masked) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) d[i] = i < hidden ? 0.0f : d[i];
+                    for (int i = 0; i < 64; ++i) p[i] = i < hidden ? 0.0f : p[i];
+                }
+                store_half<T>(my_s, p);
+                wait_st();
+                fence_before();
+                mbar_arrive(&bar.p_full);
+                ok = attn_wait_warp(&bar.dp_full, phase, failed);
+                if (!ok) break;
+                fence_after();
+                float d[64];
+                ld32(my_dp, reinterpret_cast<uint32_t *>(d));
+                ld32(my_dp + 32, reinterpret_cast<uint32_t *>(d) + 32);
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < 64; i += 4) {
+                    const float4 m = *reinterpret_cast<const float4 *>(stats + kAttnTile + i);
+                    f32x2 x = add2(pair(d[i], d[i + 1]), pair(m.x, m.y));
+                    f32x2 y = add2(pair(d[i + 2], d[i + 3]), pair(m.z, m.w));
+                    if constexpr (kScaled<T>) {
+                        x = mul2(x, both(sc.ds));
+                        y = mul2(y, both(sc.ds));
+                    }
+                    const float2 e = halves(mul2(x, pair(p[i], p[i + 1])));
+                    const float2 f = halves(mul2(y, pair(p[i + 2], p[i + 3])));
+                    d[i] = e.x;
+                    d[i + 1] = e.y;
+                    d[i + 2] = f.x;
+                    d[i + 3] = f.y;
+                }
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) d[i] = i < hidden ? 0.0f : d[i];
+                }
+                store_half<T>(my_dp, d);
+                wait_st();
+                fence_before();
+                mbar_arrive(&bar.ds_full);
+                if (++t == k.all) t = k.from;
             }
-            store_half<T>(my_dp, d);
-            wait_st();
-            fence_before();
-            mbar_arrive(&sh.ds_full);
-            if (++t == all) t = from;
+            if (k.total > 0 && ok) ok = attn_wait_warp(&bar.done, uses & 1, failed);
+            uses += k.total > 0;
+            fence_after();
+            const int count = !w.there ? 0 : s.packed ? pl.keys : s.k_tokens;
+            const bool mine = w.there && key < count, none = k.total == 0 || key >= pl.keys;
+            const long long out_at = ((long long)pl.batch * s.k_tokens + pl.k_row + key) * s.kv_heads + w.head;
+            T *const out = static_cast<T *>(half ? a.dk : a.dv);
+            store_row<T>((half ? dk_at : dv_at) + lanes, 0, s.dim, half ? a.scale * sc.inv_ds : sc.inv_p, none, ok,
+                         mine && out, out + out_at * s.dim);
         }
-        if (ok && total > 0) ok = attn_wait_warp(&sh.done, 0, failed);
-        fence_after();
-        const int count = s.packed ? pl.keys : s.k_tokens;
-        const bool mine = key < count, none = total == 0 || key >= pl.keys;
-        const long long at = ((long long)pl.batch * s.k_tokens + pl.k_row + key) * s.kv_heads + kv_head;
-        T *const out = static_cast<T *>(half ? a.dk : a.dv);
-        store_row<T>((half ? dk_at : dv_at) + lanes, 0, s.dim, half ? a.scale * sc.inv_ds : sc.inv_p, none, ok,
-                     mine && out, out + at * s.dim);
+        // the sums are read: tensor memory is the other kind's
+        fence_before();
+        mbar_arrive(&sh.keys_stored);
     }
 }
 
 // 128 queries of a head against all keys that they see.  Lanes are queries, columns
 // keys.  Tensor memory: two tiles of scores, so that the next one's are there when
 // they are wanted; dp, then ds in its place; dq.
+__device__ __forceinline__ int query_tiles(const AttnShape &s, const BwdItem &w)
+{
+    int seen = w.pl.keys;
+    if (s.causal) seen = min(seen, min((w.pl.tile + 1) * kAttnTile, w.pl.queries) + w.pl.shift);
+    return !w.there || seen <= 0 ? 0 : (seen + kAttnTile - 1) / kAttnTile;
+}
+
 template <typename T, int DP>
-__device__ void by_queries(const AttnBwdArgs &a, char *base, BwdShared &sh, int head)
+__device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, BwdShared &sh, int warp, unsigned tmem,
+                                           unsigned &n, bool &ok)
 {
     constexpr int kTile = tile_bytes<DP>();
     constexpr int kStages = query_stages<DP>();
     const AttnShape &s = a.s;
-    const AttnPlace pl = sh.place;
+    BwdBarriers &bar = sh.queries;
     volatile unsigned *const failed = &sh.failed;
-    const unsigned tmem = uniform(sh.tmem);
     const unsigned s_at = tmem, dp_at = tmem + 256, dq_at = tmem + 384;
     char *const ring = base + 2 * kTile;
-    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
-    const int kv_head = head / s.group;
-
-    const int first = pl.tile * kAttnTile;  // query
-    int seen = pl.keys;
-    if (s.causal) seen = min(seen, min(first + kAttnTile, pl.queries) + pl.shift);
-    const int total = seen <= 0 ? 0 : (seen + kAttnTile - 1) / kAttnTile;
+    const int lane = threadIdx.x % 32;
 
     if (warp == 8) {
+        RingAt<kStages> at;
         int issued = 0;
-        if (lane == 0 && total > 0) {
-            mbar_arrive_expect_tx(&sh.own_full, 2 * kTile + a.extra);
-            load_tile<DP>(base, &a.q, head, pl.q_row + first, pl.batch, &sh.own_full);
-            load_tile<DP>(base + kTile, &a.g, head, pl.q_row + first, pl.batch, &sh.own_full);
-        }
-        bool ok = true;
-        for (int it = 0; ok && it < 2 * total; ++it) {
-            const int stage = it % kStages, j = it / 2;
-            if (it >= kStages) ok = attn_wait_warp(&sh.empty[stage], (it / kStages - 1) & 1, failed);
-            if (!ok) break;
-            // keys behind the last one may be anything: zeros in their place
-            const int rows = pl.keys - j * kAttnTile;
-            const bool key = it % 2 == 0, patch = key && a.ragged && rows < kAttnTile;
-            char *const tile = ring + stage * kTile;
-            if (lane == 0) {
-                uint64_t *const bar = patch ? &sh.patched : &sh.full[stage];
-                mbar_arrive_expect_tx(bar, kTile);
-                load_tile<DP>(tile, key ? &a.k : &a.v, kv_head, pl.k_row + j * kAttnTile, pl.batch, bar);
+        unsigned uses = 0, patches = 0;
+        for (unsigned u; ok && (u = item_of(n)) < a.items; ++n) {
+            BwdItem w;
+            find_item<false>(a, u, w);
+            const int total = query_tiles(s, w), kv_head = w.head / s.group;
+            const AttnPlace &pl = w.pl;
+            for (int it = 0; ok && it < 2 * total; ++it) {
+                if (it == min(kStages - 2, 2 * total - 1)) {  // as above
+                    if (uses > 0) ok = attn_wait_warp(&bar.own_empty, (uses - 1) & 1, failed);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const int row = pl.q_row + pl.tile * kAttnTile;
+                        mbar_arrive_expect_tx(&bar.own_full, 2 * kTile + a.extra);
+                        load_tile<DP>(base, &a.q, w.head, row, pl.batch, &bar.own_full);
+                        load_tile<DP>(base + kTile, &a.g, w.head, row, pl.batch, &bar.own_full);
+                    }
+                    ++uses;
+                }
+                const int j = it / 2;
+                if (issued >= kStages) ok = attn_wait_warp(&bar.empty[at.slot], at.parity ^ 1, failed);
+                if (!ok) break;
+                // keys behind the last one may be anything: zeros in their place
+                const int rows = pl.keys - j * kAttnTile;
+                const bool key = it % 2 == 0, patch = key && a.ragged && rows < kAttnTile;
+                char *const tile = ring + at.slot * kTile;
+                if (lane == 0) {
+                    uint64_t *const to = patch ? &bar.patched : &bar.full[at.slot];
+                    mbar_arrive_expect_tx(to, kTile);
+                    load_tile<DP>(tile, key ? &a.k : &a.v, kv_head, pl.k_row + j * kAttnTile, pl.batch, to);
+                }
+                if (patch) {
+                    ok = attn_wait_warp(&bar.patched, patches++ & 1, failed);
+                    zero_rows<DP>(tile, rows);
+                    fence_proxy();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.full[at.slot]);
+                }
+                ++issued;
+                at.next();
             }
-            if (patch) {
-                ok = attn_wait_warp(&sh.patched, 0, failed);
-                zero_rows<DP>(tile, rows);
-                fence_proxy();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.full[stage]);
-            }
-            issued = it + 1;
         }
-        if (*failed && lane == 0) {
-            if (total > 0) mbar_wait_bounded(&sh.own_full, 0, kAttnDrainCycles);
-            for (int it = max(0, issued - kStages); it < issued; ++it)
-                mbar_wait_bounded(&sh.full[it % kStages], (it / kStages) & 1, kAttnDrainCycles);
-            atomicOr(&g_attention_status, 4u);
+        if (!ok) {
+            if (uses > 0) mbar_wait_bounded(&bar.own_full, (uses - 1) & 1, kAttnDrainCycles);
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                mbar_wait_bounded(&bar.full[i % kStages], (i / kStages) & 1, kAttnDrainCycles);
         }
     } else if (warp == 9) {
-        if (total > 0) {
-            const unsigned leader = elect_leader();
-            const int steps = (s.dim + 15) / 16;
-            const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
-            const unsigned s_full = smem_u32(sh.s_full), dp_full = smem_u32(&sh.dp_full), empty = smem_u32(sh.empty);
-            const Desc q_tile = desc_k(smem_u32(base)), g_tile = advance(q_tile, kTile);
-            const Desc ring_k = desc_k(smem_u32(ring)), ring_mn = desc_mn(smem_u32(ring));
-            // two places in the ring: of the tile that comes next, and of the keys that ds is
-            // waiting for
-            RingAt<kStages> at, keys;
-            const auto tile_here = [&] { return attn_wait_warp(&sh.full[at.slot], at.parity, failed); };
-            const auto scores = [&](int j) {
-                if (!tile_here()) return false;
-                product_k<DP / 16>(s_at + (j & 1) * 128, q_tile, advance(ring_k, at.slot * kTile), steps, id_s, leader);
-                commit(s_full + 8 * (j & 1), leader);
-                at.next();
-                return true;
-            };
-            const auto products = [&] {
-                if (!tile_here()) return false;
-                product_k<DP / 16>(dp_at, g_tile, advance(ring_k, at.slot * kTile), steps, id_s, leader);
-                commit(dp_full, leader);
-                commit(empty + 8 * at.slot, leader);
-                at.next();
-                return true;
-            };
-            bool ok = attn_wait_warp(&sh.own_full, 0, failed) && scores(0) && products();
-            if (ok && total > 1) ok = scores(1);
-            for (int j = 0; ok && j < total; ++j) {
-                if (!(ok = attn_wait_warp(&sh.ds_full, j & 1, failed))) break;
+        const unsigned leader = elect_leader();
+        const int steps = (s.dim + 15) / 16;
+        const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
+        const unsigned s_full = smem_u32(bar.s_full), dp_full = smem_u32(&bar.dp_full), empty = smem_u32(bar.empty);
+        const Desc q_tile = desc_k(smem_u32(base)), g_tile = advance(q_tile, kTile);
+        const Desc ring_k = desc_k(smem_u32(ring)), ring_mn = desc_mn(smem_u32(ring));
+        // two places in the ring: of the tile that comes next, and of the keys that ds is
+        // waiting for
+        RingAt<kStages> at, keys;
+        unsigned uses = 0, phase = 0, issued = 0;
+        const auto tile_here = [&] { return attn_wait_warp(&bar.full[at.slot], at.parity, failed); };
+        const auto scores = [&] {
+            if (!tile_here()) return false;
+            product_k<DP / 16>(s_at + (issued & 1) * 128, q_tile, advance(ring_k, at.slot * kTile), steps, id_s,
+                               leader);
+            commit(s_full + 8 * (issued & 1), leader);
+            ++issued;
+            at.next();
+            return true;
+        };
+        const auto products = [&] {
+            if (!tile_here()) return false;
+            product_k<DP / 16>(dp_at, g_tile, advance(ring_k, at.slot * kTile), steps, id_s, leader);
+            commit(dp_full, leader);
+            commit(empty + 8 * at.slot, leader);
+            at.next();
+            return true;
+        };
+        ok = attn_wait_warp(&sh.keys_stored, 0, failed);
+        for (unsigned u; ok && (u = item_of(n)) < a.items; ++n) {
+            BwdItem w;
+            find_item<false>(a, u, w);
+            const int total = query_tiles(s, w);
+            if (total == 0) continue;
+            ok = attn_wait_warp(&bar.own_full, uses++ & 1, failed);
+            if (!ok) break;
+            fence_after();
+            ok = scores() && products();
+            if (ok && total > 1) ok = scores();
+            for (int j = 0; ok && j < total; ++j, phase ^= 1) {
+                if (!(ok = attn_wait_warp(&bar.ds_full, phase, failed))) break;
                 fence_after();
                 product_rows<64>(dq_at, dp_at, advance(ring_mn, keys.slot * kTile), id_d, j > 0, leader);
                 commit(empty + 8 * keys.slot, leader);
                 keys.next();
                 keys.next();
                 if (j + 1 < total && !(ok = products())) break;
-                if (j + 2 < total) ok = scores(j + 2);
+                if (j + 2 < total) ok = scores();
             }
-            if (ok) {
-                commit(smem_u32(&sh.done), leader);
-            } else {
-                commit(smem_u32(&sh.drained), leader);
-                mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
-            }
+            if (!ok) break;
+            commit(smem_u32(&bar.done), leader);
+            commit(smem_u32(&bar.own_empty), leader);
         }
     } else {
         const int half = warp / 4, row = threadIdx.x % 128;
         const unsigned lanes = unsigned(warp % 4) << 21;
-        const int query = first + row;
-        const float *const stats =
-            a.stats + ((long long)head * a.q_tiles + pl.q_tiles_before + pl.tile) * 2 * kAttnTile;
-        const f32x2 c2 = both(a.scale_log2), l2 = both(stats[row]);
-        const Scales sc = scales_of<T>(a, kv_head);
-        const f32x2 n2 = both(stats[kAttnTile + row] * sc.ds);
-        const int end = s.causal ? min(pl.keys, query + 1 + pl.shift) : pl.keys;
-        bool ok = true;
-        for (int j = 0; j < total; ++j) {
-            const unsigned my_s = s_at + lanes + (j & 1) * 128 + half * 64, my_dp = dp_at + lanes + half * 64;
-            const int left = end - j * kAttnTile - half * 64;
-            const bool masked = __any_sync(0xffffffffu, left < 64);
-            ok = attn_wait_warp(&sh.s_full[j & 1], (j >> 1) & 1, failed);
-            if (!ok) break;
+        const f32x2 c2 = both(a.scale_log2);
+        unsigned uses = 0, tiles = 0;
+        for (unsigned u; (u = item_of(n)) < a.items; ++n) {
+            BwdItem w;
+            find_item<false>(a, u, w);
+            if (!w.there) continue;
+            const AttnPlace &pl = w.pl;
+            const int total = query_tiles(s, w), query = pl.tile * kAttnTile + row;
+            const float *const stats =
+                a.stats + ((long long)w.head * a.q_tiles + pl.q_tiles_before + pl.tile) * 2 * kAttnTile;
+            const f32x2 l2 = both(stats[row]);
+            const Scales sc = scales_of<T>(a, w.head / s.group);
+            const f32x2 n2 = both(stats[kAttnTile + row] * sc.ds);
+            const int end = s.causal ? min(pl.keys, query + 1 + pl.shift) : pl.keys;
+            for (int j = 0; ok && j < total; ++j, ++tiles) {
+                const unsigned my_s = s_at + lanes + (tiles & 1) * 128 + half * 64, my_dp = dp_at + lanes + half * 64;
+                const int left = end - j * kAttnTile - half * 64;
+                const bool masked = __any_sync(0xffffffffu, left < 64);
+                ok = attn_wait_warp(&bar.s_full[tiles & 1], (tiles >> 1) & 1, failed);
+                if (!ok) break;
+                fence_after();
+                float p[64], d[64];
+                ld32(my_s, reinterpret_cast<uint32_t *>(p));
+                ld32(my_s + 32, reinterpret_cast<uint32_t *>(p) + 32);
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    const float2 x = halves(fma2(pair(p[i], p[i + 1]), c2, l2));
+                    p[i] = exp2_fast(x.x);
+                    p[i + 1] = exp2_fast(x.y);
+                }
+                ok = attn_wait_warp(&bar.dp_full, tiles & 1, failed);
+                if (!ok) break;
+                fence_after();
+                ld32(my_dp, reinterpret_cast<uint32_t *>(d));
+                ld32(my_dp + 32, reinterpret_cast<uint32_t *>(d) + 32);
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    f32x2 x = pair(d[i], d[i + 1]);
+                    x = kScaled<T> ? fma2(x, both(sc.ds), n2) : add2(x, n2);
+                    const float2 e = halves(mul2(x, pair(p[i], p[i + 1])));
+                    d[i] = e.x;
+                    d[i + 1] = e.y;
+                }
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) d[i] = i < left ? d[i] : 0.0f;
+                }
+                store_half<T>(my_dp, d);
+                wait_st();
+                fence_before();
+                mbar_arrive(&bar.ds_full);
+            }
+            if (ok && total > 0) ok = attn_wait_warp(&bar.done, uses & 1, failed);
+            uses += total > 0;
             fence_after();
-            float p[64], d[64];
-            ld32(my_s, reinterpret_cast<uint32_t *>(p));
-            ld32(my_s + 32, reinterpret_cast<uint32_t *>(p) + 32);
-            wait_ld();
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-                const float2 x = halves(fma2(pair(p[i], p[i + 1]), c2, l2));
-                p[i] = exp2_fast(x.x);
-                p[i + 1] = exp2_fast(x.y);
-            }
-            ok = attn_wait_warp(&sh.dp_full, j & 1, failed);
-            if (!ok) break;
-            fence_after();
-            ld32(my_dp, reinterpret_cast<uint32_t *>(d));
-            ld32(my_dp + 32, reinterpret_cast<uint32_t *>(d) + 32);
-            wait_ld();
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-                f32x2 x = pair(d[i], d[i + 1]);
-                x = kScaled<T> ? fma2(x, both(sc.ds), n2) : add2(x, n2);
-                const float2 u = halves(mul2(x, pair(p[i], p[i + 1])));
-                d[i] = u.x;
-                d[i + 1] = u.y;
-            }
-            if (masked) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) d[i] = i < left ? d[i] : 0.0f;
-            }
-            store_half<T>(my_dp, d);
-            wait_st();
-            fence_before();
-            mbar_arrive(&sh.ds_full);
+            const long long out_at = ((long long)pl.batch * s.q_tokens + pl.q_row + query) * s.heads + w.head;
+            const int cut = min(s.dim, 64);
+            store_row<T>(dq_at + lanes, half ? cut : 0, half ? s.dim : cut, a.scale * sc.inv_ds, total == 0, ok,
+                         query < pl.queries, static_cast<T *>(a.dq) + out_at * s.dim);
         }
-        if (ok && total > 0) ok = attn_wait_warp(&sh.done, 0, failed);
-        fence_after();
-        const long long at = ((long long)pl.batch * s.q_tokens + pl.q_row + query) * s.heads + head;
-        const int cut = min(s.dim, 64);
-        store_row<T>(dq_at + lanes, half ? cut : 0, half ? s.dim : cut, a.scale * sc.inv_ds, total == 0, ok,
-                     query < pl.queries, static_cast<T *>(a.dq) + at * s.dim);
     }
 }
 
@@ -615,66 +733,46 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
     char *const base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     BwdShared &sh = *reinterpret_cast<BwdShared *>(base + bwd_smem<DP>() - 1024 - sizeof(BwdShared));
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
-    const AttnShape &s = a.s;
-    const bool keys_wanted = a.dk || a.dv;
-    const unsigned key_blocks = keys_wanted ? unsigned(a.k_tiles) * s.kv_heads : 0;
-    const bool keys = blockIdx.x < key_blocks;
-    const unsigned u = keys ? blockIdx.x : blockIdx.x - key_blocks;
-    // causal: falling work, that of the first keys and of the last queries before the
-    // others; else a head's blocks one after another, which share its tiles in L2
-    int head, index;
-    if (s.causal) {
-        const int heads = keys ? s.kv_heads : s.heads;
-        head = u % heads;
-        const int i = u / heads;
-        if (s.packed) {
-            index = keys ? i : a.q_tiles - 1 - i;
-        } else {
-            const int tiles = (keys ? a.k_tiles : a.q_tiles) / s.sequences;
-            const int tile = keys ? i / s.sequences : tiles - 1 - i / s.sequences;
-            index = i % s.sequences * tiles + tile;
-        }
-    } else {
-        const int tiles = keys ? a.k_tiles : a.q_tiles;
-        head = u / tiles;
-        index = u % tiles;
-    }
-    if (warp == 8) {
-        AttnPlace place;
-        const bool there = keys ? find_place<true>(s, index, kAttnTile, place)
-                                : find_place<false>(s, index, kAttnTile, place);
-        if (lane == 0) {
-            sh.place = place;
-            sh.there = there;
-            sh.failed = 0;
-            for (uint64_t *b : {&sh.own_full, &sh.s_full[0], &sh.s_full[1], &sh.dp_full, &sh.done, &sh.patched,
-                                &sh.drained})
-                mbar_init(b, 1);
+    if (warp == 8 && lane == 0) {
+        for (const CUtensorMap *m : {&a.q, &a.k, &a.v, &a.g}) prefetch_map(m);
+        sh.failed = 0;
+        for (BwdBarriers *b : {&sh.keys, &sh.queries}) {
+            for (uint64_t *x : {&b->own_full, &b->own_empty, &b->s_full[0], &b->s_full[1], &b->dp_full, &b->done,
+                                &b->patched})
+                mbar_init(x, 1);
             for (int i = 0; i < 8; ++i) {
-                mbar_init(&sh.full[i], 1);
-                mbar_init(&sh.empty[i], 1);
+                mbar_init(&b->full[i], 1);
+                mbar_init(&b->empty[i], 1);
             }
-            mbar_init(&sh.p_full, 256);
-            mbar_init(&sh.ds_full, 256);
-            mbar_init_fence();
+            mbar_init(&b->p_full, 256);
+            mbar_init(&b->ds_full, 256);
         }
+        mbar_init(&sh.keys_stored, 256);
+        mbar_init(&sh.drained, 1);
+        mbar_init_fence();
     }
     if (warp == 9) alloc_all(&sh.tmem);
     fence_before();
     __syncthreads();
     fence_after();
-    if (sh.there) {
-        if (keys)
-            by_keys<T, DP>(a, base, sh, head);
-        else
-            by_queries<T, DP>(a, base, sh, head);
+    const unsigned tmem = uniform(sh.tmem);
+    unsigned n = 0;
+    bool ok = true;
+    by_keys<T, DP>(a, base, sh, warp, tmem, n, ok);
+    // a block that failed has every role leave; those on the tiles still write their
+    // NaN
+    if (ok || warp < 8) by_queries<T, DP>(a, base, sh, warp, tmem, n, ok);
+    if (!ok && warp == 9) {
+        commit(smem_u32(&sh.drained), elect_leader());
+        mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
     }
+    if (!ok && warp == 8 && lane == 0) atomicOr(&g_attention_status, 4u);
     __syncwarp();
     fence_before();
     __syncthreads();
     if (warp == 9) {
         fence_after();
-        free_all(sh.tmem);
+        free_all(tmem);
     }
 }
 
@@ -694,9 +792,8 @@ cudaError_t launch(const AttnBwdArgs &a, cudaStream_t stream)
     if (a.q_tiles > 0) attention_sums_kernel<T><<<grid, kSumThreads, 0, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const long long blocks = (a.dk || a.dv ? (long long)a.k_tiles * a.s.kv_heads : 0) +
-                             (a.dq ? (long long)a.q_tiles * a.s.heads : 0);
-    if (blocks > 0) attention_bwd_kernel<T, DP><<<unsigned(blocks), kBwdThreads, smem, stream>>>(a);
+    if (a.items > 0)
+        attention_bwd_kernel<T, DP><<<std::min(a.items, unsigned(kAttnBlocks)), kBwdThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
