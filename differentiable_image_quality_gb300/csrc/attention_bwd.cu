@@ -212,10 +212,18 @@ constexpr int key_stages()  // pairs of a query tile and its gradient
 {
     return DP == 64 ? 4 : 2;
 }
+// Rings of keys and of values: a tile of values is free after its product, one of keys
+// only after the sums that ds goes into, so they do not wait for one another (in one
+// ring of five, heads of 128, values came late: 8 x 8192 took 604 us for 5xx).
 template <int DP>
-constexpr int query_stages()  // single tiles, keys and values in turn
+constexpr int key_slots()
 {
-    return DP == 64 ? 8 : 5;
+    return DP == 64 ? 4 : 3;
+}
+template <int DP>
+constexpr int value_slots()
+{
+    return DP == 64 ? 4 : 2;
 }
 
 constexpr int kStatsBytes = 2 * kAttnTile * 4;
@@ -224,7 +232,7 @@ template <int DP>
 constexpr size_t bwd_smem()
 {
     constexpr size_t by_keys = size_t(2 + 2 * key_stages<DP>()) * tile_bytes<DP>() + key_stages<DP>() * kStatsBytes;
-    constexpr size_t by_queries = size_t(2 + query_stages<DP>()) * tile_bytes<DP>();
+    constexpr size_t by_queries = size_t(2 + key_slots<DP>() + value_slots<DP>()) * tile_bytes<DP>();
     return (by_keys > by_queries ? by_keys : by_queries) + sizeof(BwdShared) + 1024;
 }
 
@@ -293,9 +301,12 @@ __device__ __forceinline__ void store_row(unsigned at, int from, int to, float s
 }
 
 // 128 keys of a key head against all queries that see them.  Lanes are keys, columns
-// queries.  Tensor memory: scores, then p in their place; dp, then ds in its place;
-// dv; dk.  While the warps form p of a tile, the products of ds of the last one run;
-// while they form ds, those of p and the next scores.
+// queries.  Tensor memory: scores, then p in their place; dp; dv; dk.  Heads of more than
+// 64 columns: ds in dp's place; while the warps form p of a tile, the products of ds of
+// the last one run; while they form ds, those of p and the next scores.  Narrower
+// heads leave room for two tiles of scores, and beside p for ds: the next scores are
+// there when they are wanted, and the next dp waits for nothing but that the last one
+// has been read (8 x 8192 x 64: see below).
 struct KeySpan {
     int first;        // key
     int from, all;    // tiles of queries: from the first that sees the first key
@@ -321,7 +332,8 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
     const AttnShape &s = a.s;
     BwdBarriers &bar = sh.keys;
     volatile unsigned *const failed = &sh.failed;
-    const unsigned s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 256 + DP;
+    constexpr bool kTwo = DP == 64;
+    const unsigned s_at = tmem, dp_at = tmem + (kTwo ? 256 : 128), dv_at = dp_at + 128, dk_at = dv_at + DP;
     char *const ring = base + 2 * kTile;
     char *const ring_stats = ring + 2 * kStages * kTile;
     const int lane = threadIdx.x % 32;
@@ -392,43 +404,51 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
         const unsigned s_full = smem_u32(bar.s_full), dp_full = smem_u32(&bar.dp_full), empty = smem_u32(bar.empty);
         const Desc k_tile = desc_k(smem_u32(base)), v_tile = advance(k_tile, kTile);
         const Desc ring_k = desc_k(smem_u32(ring)), ring_mn = desc_mn(smem_u32(ring));
-        RingAt<kStages> at;
-        unsigned uses = 0, phase = 0;
+        // places in the ring: of the next tile of queries for scores, for dp, and of the one
+        // that p and ds are waiting for
+        RingAt<kStages> at, dp_of, sum_of;
+        unsigned uses = 0, phase = 0, scored = 0;
+        const auto scores = [&] {
+            if (!attn_wait_warp(&bar.full[at.slot], at.parity, failed)) return false;
+            const unsigned buf = kTwo ? scored & 1 : 0;
+            product_k<DP / 16>(s_at + buf * 128, k_tile, advance(ring_k, 2 * at.slot * kTile), steps, id_s, leader);
+            commit(s_full + 8 * buf, leader);
+            ++scored;
+            at.next();
+            return true;
+        };
+        const auto products = [&] {  // of a tile that has its scores: it is here
+            product_k<DP / 16>(dp_at, v_tile, advance(ring_k, (2 * dp_of.slot + 1) * kTile), steps, id_s, leader);
+            commit(dp_full, leader);
+            dp_of.next();
+        };
         for (unsigned u; ok && (u = item_of(n)) < a.key_items; ++n) {
             BwdItem w;
             find_item<true>(a, u, w);
             const int total = key_span(s, w).total;
             if (total == 0) continue;
-            ok = attn_wait_warp(&bar.own_full, uses++ & 1, failed) &&
-                 attn_wait_warp(&bar.full[at.slot], at.parity, failed);
+            ok = attn_wait_warp(&bar.own_full, uses++ & 1, failed);
             if (!ok) break;
             fence_after();
-            product_k<DP / 16>(s_at, k_tile, advance(ring_k, 2 * at.slot * kTile), steps, id_s, leader);
-            commit(s_full, leader);
-            product_k<DP / 16>(dp_at, v_tile, advance(ring_k, (2 * at.slot + 1) * kTile), steps, id_s, leader);
-            commit(dp_full, leader);
+            if (!(ok = scores())) break;
+            products();
+            if (kTwo && total > 1 && !(ok = scores())) break;
             for (int it = 0; it < total; ++it, phase ^= 1) {
-                const int slot = at.slot;
-                const Desc tile = advance(ring_mn, 2 * slot * kTile);
-                at.next();
-                const Desc next = advance(ring_k, 2 * at.slot * kTile);
+                const Desc tile = advance(ring_mn, 2 * sum_of.slot * kTile);
+                const unsigned p_at = s_at + (kTwo ? phase * 128 : 0), ds_at = kTwo ? p_at + 32 : dp_at;
                 const bool more = it + 1 < total;
                 if (!(ok = attn_wait_warp(&bar.p_full, phase, failed))) break;
                 fence_after();
-                product_rows<64>(dv_at, s_at, advance(tile, kTile), id_d, it > 0, leader);
-                if (more) {
-                    if (!(ok = attn_wait_warp(&bar.full[at.slot], at.parity, failed))) break;
-                    product_k<DP / 16>(s_at, k_tile, next, steps, id_s, leader);
-                    commit(s_full, leader);
-                }
+                product_rows<64>(dv_at, p_at, advance(tile, kTile), id_d, it > 0, leader);
+                if (!kTwo && more && !(ok = scores())) break;
                 if (!(ok = attn_wait_warp(&bar.ds_full, phase, failed))) break;
                 fence_after();
-                product_rows<64>(dk_at, dp_at, tile, id_d, it > 0, leader);
-                commit(empty + 8 * slot, leader);
-                if (more) {
-                    product_k<DP / 16>(dp_at, v_tile, advance(next, kTile), steps, id_s, leader);
-                    commit(dp_full, leader);
-                }
+                if (kTwo && more) products();
+                product_rows<64>(dk_at, ds_at, tile, id_d, it > 0, leader);
+                commit(empty + 8 * sum_of.slot, leader);
+                sum_of.next();
+                if (!kTwo && more) products();
+                if (kTwo && it + 2 < total && !(ok = scores())) break;
             }
             if (!ok) break;
             commit(smem_u32(&bar.done), leader);
@@ -437,10 +457,10 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
     } else {
         const int half = warp / 4, row = threadIdx.x % 128;
         const unsigned lanes = unsigned(warp % 4) << 21;
-        const unsigned my_s = s_at + lanes + half * 64, my_dp = dp_at + lanes + half * 64;
+        const unsigned my_dp = dp_at + lanes + half * 64;
         const f32x2 c2 = both(a.scale_log2);
         RingAt<kStages> at;
-        unsigned uses = 0, phase = 0;
+        unsigned uses = 0, phase = 0, tiles = 0;
         for (unsigned u; (u = item_of(n)) < a.key_items; ++n) {
             BwdItem w;
             find_item<true>(a, u, w);
@@ -456,9 +476,11 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                                    : s.causal     ? key - pl.shift - t * kAttnTile - half * 64
                                                   : 0;
                 const bool masked = __any_sync(0xffffffffu, hidden > 0);
+                const unsigned my_s = s_at + lanes + (kTwo ? phase * 128 : 0) + half * 64;
                 ok = attn_wait_warp(&bar.full[at.slot], at.parity, failed) &&
-                     attn_wait_warp(&bar.s_full[0], phase, failed);
+                     attn_wait_warp(&bar.s_full[kTwo ? phase : 0], kTwo ? tiles >> 1 & 1 : phase, failed);
                 if (!ok) break;
+                ++tiles;
                 at.next();
                 fence_after();
                 float p[64];
@@ -510,7 +532,7 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
 #pragma unroll
                     for (int i = 0; i < 64; ++i) d[i] = i < hidden ? 0.0f : d[i];
                 }
-                store_half<T>(my_dp, d);
+                store_half<T>(kTwo ? my_s + 32 : my_dp, d);
                 wait_st();
                 fence_before();
                 mbar_arrive(&bar.ds_full);
@@ -534,7 +556,8 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
 
 // 128 queries of a head against all keys that they see.  Lanes are queries, columns
 // keys.  Tensor memory: two tiles of scores, so that the next one's are there when
-// they are wanted; dp, then ds in its place; dq.
+// they are wanted, then ds in their place, so that the next dp waits for nothing but
+// that the last one has been read; dp; dq.
 __device__ __forceinline__ int query_tiles(const AttnShape &s, const BwdItem &w)
 {
     int seen = w.pl.keys;
@@ -547,25 +570,28 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
                                            unsigned &n, bool &ok)
 {
     constexpr int kTile = tile_bytes<DP>();
-    constexpr int kStages = query_stages<DP>();
+    constexpr int kKeys = key_slots<DP>(), kValues = value_slots<DP>();
     const AttnShape &s = a.s;
     BwdBarriers &bar = sh.queries;
     volatile unsigned *const failed = &sh.failed;
     const unsigned s_at = tmem, dp_at = tmem + 256, dq_at = tmem + 384;
-    char *const ring = base + 2 * kTile;
+    char *const k_ring = base + 2 * kTile, *const v_ring = k_ring + kKeys * kTile;
+    uint64_t *const k_full = bar.full, *const v_full = bar.full + kKeys;
+    uint64_t *const k_empty = bar.empty, *const v_empty = bar.empty + kKeys;
     const int lane = threadIdx.x % 32;
 
     if (warp == 8) {
-        RingAt<kStages> at;
-        int issued = 0;
+        RingAt<kKeys> k_at;
+        RingAt<kValues> v_at;
+        int issued = 0;  // pairs
         unsigned uses = 0, patches = 0;
         for (unsigned u; ok && (u = item_of(n)) < a.items; ++n) {
             BwdItem w;
             find_item<false>(a, u, w);
             const int total = query_tiles(s, w), kv_head = w.head / s.group;
             const AttnPlace &pl = w.pl;
-            for (int it = 0; ok && it < 2 * total; ++it) {
-                if (it == min(kStages - 2, 2 * total - 1)) {  // as above
+            for (int j = 0; ok && j < total; ++j) {
+                if (j == min(1, total - 1)) {  // as above
                     if (uses > 0) ok = attn_wait_warp(&bar.own_empty, (uses - 1) & 1, failed);
                     if (!ok) break;
                     if (lane == 0) {
@@ -576,61 +602,68 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
                     }
                     ++uses;
                 }
-                const int j = it / 2;
-                if (issued >= kStages) ok = attn_wait_warp(&bar.empty[at.slot], at.parity ^ 1, failed);
+                if (issued >= kKeys) ok = attn_wait_warp(&k_empty[k_at.slot], k_at.parity ^ 1, failed);
                 if (!ok) break;
                 // keys behind the last one may be anything: zeros in their place
-                const int rows = pl.keys - j * kAttnTile;
-                const bool key = it % 2 == 0, patch = key && a.ragged && rows < kAttnTile;
-                char *const tile = ring + at.slot * kTile;
+                const int rows = pl.keys - j * kAttnTile, row = pl.k_row + j * kAttnTile;
+                const bool patch = a.ragged && rows < kAttnTile;
+                char *const tile = k_ring + k_at.slot * kTile;
                 if (lane == 0) {
-                    uint64_t *const to = patch ? &bar.patched : &bar.full[at.slot];
+                    uint64_t *const to = patch ? &bar.patched : &k_full[k_at.slot];
                     mbar_arrive_expect_tx(to, kTile);
-                    load_tile<DP>(tile, key ? &a.k : &a.v, kv_head, pl.k_row + j * kAttnTile, pl.batch, to);
+                    load_tile<DP>(tile, &a.k, kv_head, row, pl.batch, to);
                 }
                 if (patch) {
                     ok = attn_wait_warp(&bar.patched, patches++ & 1, failed);
                     zero_rows<DP>(tile, rows);
                     fence_proxy();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.full[at.slot]);
+                    if (lane == 0) mbar_arrive(&k_full[k_at.slot]);
                 }
                 ++issued;
-                at.next();
+                k_at.next();
+                if (ok && issued > kValues) ok = attn_wait_warp(&v_empty[v_at.slot], v_at.parity ^ 1, failed);
+                if (lane == 0) {  // also after a failure: both rings have as many on their way
+                    mbar_arrive_expect_tx(&v_full[v_at.slot], kTile);
+                    load_tile<DP>(v_ring + v_at.slot * kTile, &a.v, kv_head, row, pl.batch, &v_full[v_at.slot]);
+                }
+                v_at.next();
             }
         }
         if (!ok) {
             if (uses > 0) mbar_wait_bounded(&bar.own_full, (uses - 1) & 1, kAttnDrainCycles);
-            for (int i = max(0, issued - kStages); i < issued; ++i)
-                mbar_wait_bounded(&bar.full[i % kStages], (i / kStages) & 1, kAttnDrainCycles);
+            for (int i = max(0, issued - kKeys); i < issued; ++i)
+                mbar_wait_bounded(&k_full[i % kKeys], (i / kKeys) & 1, kAttnDrainCycles);
+            for (int i = max(0, issued - kValues); i < issued; ++i)
+                mbar_wait_bounded(&v_full[i % kValues], (i / kValues) & 1, kAttnDrainCycles);
         }
     } else if (warp == 9) {
         const unsigned leader = elect_leader();
         const int steps = (s.dim + 15) / 16;
         const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
-        const unsigned s_full = smem_u32(bar.s_full), dp_full = smem_u32(&bar.dp_full), empty = smem_u32(bar.empty);
+        const unsigned s_full = smem_u32(bar.s_full), dp_full = smem_u32(&bar.dp_full);
         const Desc q_tile = desc_k(smem_u32(base)), g_tile = advance(q_tile, kTile);
-        const Desc ring_k = desc_k(smem_u32(ring)), ring_mn = desc_mn(smem_u32(ring));
-        // two places in the ring: of the tile that comes next, and of the keys that ds is
-        // waiting for
-        RingAt<kStages> at, keys;
-        unsigned uses = 0, phase = 0, issued = 0;
-        const auto tile_here = [&] { return attn_wait_warp(&bar.full[at.slot], at.parity, failed); };
+        const Desc keys_k = desc_k(smem_u32(k_ring)), keys_mn = desc_mn(smem_u32(k_ring));
+        const Desc values_k = desc_k(smem_u32(v_ring));
+        // the next keys and values, and the keys that ds is waiting for
+        RingAt<kKeys> k_at, sum_of;
+        RingAt<kValues> v_at;
+        unsigned uses = 0, phase = 0, scored = 0;
         const auto scores = [&] {
-            if (!tile_here()) return false;
-            product_k<DP / 16>(s_at + (issued & 1) * 128, q_tile, advance(ring_k, at.slot * kTile), steps, id_s,
+            if (!attn_wait_warp(&k_full[k_at.slot], k_at.parity, failed)) return false;
+            product_k<DP / 16>(s_at + (scored & 1) * 128, q_tile, advance(keys_k, k_at.slot * kTile), steps, id_s,
                                leader);
-            commit(s_full + 8 * (issued & 1), leader);
-            ++issued;
-            at.next();
+            commit(s_full + 8 * (scored & 1), leader);
+            ++scored;
+            k_at.next();
             return true;
         };
         const auto products = [&] {
-            if (!tile_here()) return false;
-            product_k<DP / 16>(dp_at, g_tile, advance(ring_k, at.slot * kTile), steps, id_s, leader);
+            if (!attn_wait_warp(&v_full[v_at.slot], v_at.parity, failed)) return false;
+            product_k<DP / 16>(dp_at, g_tile, advance(values_k, v_at.slot * kTile), steps, id_s, leader);
             commit(dp_full, leader);
-            commit(empty + 8 * at.slot, leader);
-            at.next();
+            commit(smem_u32(&v_empty[v_at.slot]), leader);
+            v_at.next();
             return true;
         };
         ok = attn_wait_warp(&sh.keys_stored, 0, failed);
@@ -647,11 +680,11 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
             for (int j = 0; ok && j < total; ++j, phase ^= 1) {
                 if (!(ok = attn_wait_warp(&bar.ds_full, phase, failed))) break;
                 fence_after();
-                product_rows<64>(dq_at, dp_at, advance(ring_mn, keys.slot * kTile), id_d, j > 0, leader);
-                commit(empty + 8 * keys.slot, leader);
-                keys.next();
-                keys.next();
                 if (j + 1 < total && !(ok = products())) break;
+                product_rows<64>(dq_at, s_at + phase * 128, advance(keys_mn, sum_of.slot * kTile), id_d, j > 0,
+                                 leader);
+                commit(smem_u32(&k_empty[sum_of.slot]), leader);
+                sum_of.next();
                 if (j + 2 < total) ok = scores();
             }
             if (!ok) break;
@@ -710,7 +743,7 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
 #pragma unroll
                     for (int i = 0; i < 64; ++i) d[i] = i < left ? d[i] : 0.0f;
                 }
-                store_half<T>(my_dp, d);
+                store_half<T>(my_s, d);
                 wait_st();
                 fence_before();
                 mbar_arrive(&bar.ds_full);
