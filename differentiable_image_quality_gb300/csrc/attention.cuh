@@ -175,6 +175,25 @@ inline cudaError_t allow_smem(Kernel kernel, std::atomic<unsigned long long> &do
     return e;
 }
 
+// A launch whose blocks may start while the kernel ahead on the stream ends; they wait
+// for it (pdl_wait) before they touch what it wrote.
+template <typename Args>
+inline cudaError_t launch_after(void (*kernel)(Args), unsigned grid, unsigned threads, size_t smem,
+                                cudaStream_t stream, const Args &a)
+{
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 // ------------------------------------------------------------------- forward
 
 struct AttnFwdArgs {

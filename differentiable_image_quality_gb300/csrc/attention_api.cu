@@ -137,8 +137,10 @@ FwdPlan plan_fwd(const gbssim_attention &d)
     p.tiles = s.packed ? most_tiles(s, s.q_tokens, rows) : (s.q_tokens + rows - 1) / rows;
     const long long blocks = p.tiles * samples(d) * heads;
     const long long key_tiles = (s.k_tokens + kAttnTile - 1) / kAttnTile;
+    // Few blocks and many keys: parts of two tiles at least, which a tile's 1.1 us and
+    // the join's 4 us make worth it from eight tiles on.
     if (!s.packed && blocks > 0 && 2 * blocks <= kAttnBlocks && key_tiles >= 8)
-        p.splits = int(std::min<long long>(kAttnBlocks / blocks, key_tiles / 4));
+        p.splits = int(std::min<long long>(kAttnBlocks / blocks, key_tiles / 2));
     return p;
 }
 

@@ -51,7 +51,7 @@ __device__ __forceinline__ Scales scales_of(const AttnBwdArgs &a, int kv_head)
 
 // Per row -log2(e) lse (plus the bits that float16 probabilities are moved by) and -D,
 // in tiles of 128 queries; rows that the sequence does not have, and those that see
-// no key, have -infinity: their probabilities are zero.  16 lanes read a row.
+// no key, have -infinity: their probabilities are zero.
 constexpr int kSumThreads = 256;
 
 template <typename T>
@@ -73,14 +73,18 @@ __device__ void store_largest(float m, unsigned *to)
     if (threadIdx.x % 32 == 0 && b) atomicMax(to, b);
 }
 
-template <typename T>
+// LANES read a row, eight columns each; a thread's rows are asked for together (one after
+// the other, 14000 x 16 rows of 64 took 67 us).
+template <typename T, int LANES>
 __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnBwdArgs a)
 {
+    constexpr int kTeams = kSumThreads / LANES, kRows = kAttnTile / kTeams;
     __shared__ AttnPlace place;
     __shared__ int there;
     const AttnShape &s = a.s;
     const bool values = int(blockIdx.x) >= a.q_tiles;  // the largest |v| (float16)
     const int head = blockIdx.y;
+    pdl_trigger();
     if (values && head >= s.kv_heads) return;
     if (threadIdx.x < 32) {
         AttnPlace p;
@@ -94,57 +98,58 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
     __syncthreads();
     if (!there) return;
     const AttnPlace pl = place;
-    const int lane = threadIdx.x % 16, team = threadIdx.x / 16;
+    const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
     const bool mine = lane * 8 < s.dim;
-    float largest = 0.0f;
-    if (values) {
-        for (int r = team; r < kAttnTile; r += kSumThreads / 16) {
-            const int t = pl.tile * kAttnTile + r;
-            if (!mine || t >= pl.keys) continue;
-            const long long at = pl.batch * a.v_batch + (long long)(pl.k_row + t) * a.v_token + head * a.v_head;
-            const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v_data) + at + lane * 8);
-            largest = __uint_as_float(max(__float_as_uint(largest), __float_as_uint(largest8<T>(w))));
-        }
-        __syncwarp();
-        store_largest<T>(largest, a.largest + s.kv_heads + head);
-        return;
+    const int first = pl.tile * kAttnTile + team, rows = values ? pl.keys : pl.queries;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const T *const x = values ? static_cast<const T *>(a.v_data) + pl.batch * a.v_batch + pl.k_row * a.v_token +
+                                    head * a.v_head + lane * 8
+                              : static_cast<const T *>(a.g_data) + pl.batch * a.g_batch + pl.q_row * a.g_token +
+                                    head * a.g_head + lane * 8;
+    const long long step = values ? a.v_token : a.g_token;
+    Raw8<T> rx[kRows], ro[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int t = first + i * kTeams;
+        rx[i].w[0] = mine && t < rows ? *reinterpret_cast<const uint4 *>(x + t * step) : zero;
     }
-    float *const stats = a.stats + ((long long)head * a.q_tiles + pl.q_tiles_before + pl.tile) * 2 * kAttnTile;
-    for (int r = team; r < kAttnTile; r += kSumThreads / 16) {
-        const int t = pl.tile * kAttnTile + r;
-        float sum = 0.0f;
-        if (mine && t < pl.queries) {
-            const T *const o = static_cast<const T *>(a.out) + pl.batch * a.o_batch +
-                               (long long)(pl.q_row + t) * a.o_token + head * a.o_head + lane * 8;
-            const T *const g = static_cast<const T *>(a.g_data) + pl.batch * a.g_batch +
-                               (long long)(pl.q_row + t) * a.g_token + head * a.g_head + lane * 8;
-            Raw8<T> ro, rg;
-            ro.w[0] = *reinterpret_cast<const uint4 *>(o);
-            rg.w[0] = *reinterpret_cast<const uint4 *>(g);
-            float x[8], y[8];
-            unpack8<T>(ro, x);
-            unpack8<T>(rg, y);
+    if (!values) {
+        const T *const o = static_cast<const T *>(a.out) + pl.batch * a.o_batch + pl.q_row * a.o_token +
+                           head * a.o_head + lane * 8;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
-            if constexpr (kScaled<T>)
-                largest = __uint_as_float(max(__float_as_uint(largest), __float_as_uint(largest8<T>(rg.w[0]))));
+        for (int i = 0; i < kRows; ++i) {
+            const int t = first + i * kTeams;
+            ro[i].w[0] = mine && t < rows ? *reinterpret_cast<const uint4 *>(o + t * a.o_token) : zero;
         }
-        __syncwarp();
+        float *const stats =
+            a.stats + ((long long)head * a.q_tiles + pl.q_tiles_before + pl.tile) * 2 * kAttnTile;
 #pragma unroll
-        for (int d = 8; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0) {
-            float l = -INFINITY;
-            if (t < pl.queries) {
-                const float lse = a.lse[((long long)pl.batch * s.heads + head) * s.q_tokens + pl.q_row + t];
-                if (lse != -INFINITY) l = (kScaled<T> ? kProbBits : 0.0f) - lse * 1.4426950408889634f;
+        for (int i = 0; i < kRows; ++i) {
+            const int t = first + i * kTeams;
+            float u[8], v[8], sum = 0.0f;
+            unpack8<T>(rx[i], u);
+            unpack8<T>(ro[i], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(u[e], v[e], sum);
+#pragma unroll
+            for (int d = LANES / 2; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (lane == 0) {
+                float l = -INFINITY;
+                if (t < rows) {
+                    const float lse = a.lse[((long long)pl.batch * s.heads + head) * s.q_tokens + pl.q_row + t];
+                    if (lse != -INFINITY) l = (kScaled<T> ? kProbBits : 0.0f) - lse * 1.4426950408889634f;
+                }
+                stats[team + i * kTeams] = l;
+                stats[kAttnTile + team + i * kTeams] = -sum;
             }
-            stats[r] = l;
-            stats[kAttnTile + r] = -sum;
         }
     }
     if constexpr (kScaled<T>) {
-        __syncwarp();
-        store_largest<T>(largest, a.largest + head / s.group);
+        float largest = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            largest = __uint_as_float(max(__float_as_uint(largest), __float_as_uint(largest8<T>(rx[i].w[0]))));
+        store_largest<T>(largest, a.largest + (values ? s.kv_heads + head : head / s.group));
     }
 }
 
@@ -789,6 +794,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
     __syncthreads();
     fence_after();
     const unsigned tmem = uniform(sh.tmem);
+    pdl_wait();  // the row sums
     unsigned n = 0;
     bool ok = true;
     by_keys<T, DP>(a, base, sh, warp, tmem, n, ok);
@@ -822,12 +828,19 @@ cudaError_t launch(const AttnBwdArgs &a, cudaStream_t stream)
         if (e != cudaSuccess) return e;
     }
     const dim3 grid(unsigned(a.q_tiles + (kScaled<T> ? a.k_tiles : 0)), unsigned(a.s.heads));
-    if (a.q_tiles > 0) attention_sums_kernel<T><<<grid, kSumThreads, 0, stream>>>(a);
+    if (a.q_tiles > 0) {
+        if (a.s.dim <= 32)
+            attention_sums_kernel<T, 4><<<grid, kSumThreads, 0, stream>>>(a);
+        else if (a.s.dim <= 64)
+            attention_sums_kernel<T, 8><<<grid, kSumThreads, 0, stream>>>(a);
+        else
+            attention_sums_kernel<T, 16><<<grid, kSumThreads, 0, stream>>>(a);
+    }
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (a.items > 0)
-        attention_bwd_kernel<T, DP><<<std::min(a.items, unsigned(kAttnBlocks)), kBwdThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    if (a.items == 0) return cudaSuccess;
+    return launch_after(attention_bwd_kernel<T, DP>, std::min(a.items, unsigned(kAttnBlocks)), kBwdThreads, smem,
+                        stream, a);
 }
 
 }  // namespace
