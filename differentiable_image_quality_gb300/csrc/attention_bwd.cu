@@ -70,7 +70,8 @@ template <typename T>
 __device__ void store_largest(float m, unsigned *to)
 {
     unsigned b = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    if (threadIdx.x % 32 == 0 && b) atomicMax(to, b);
+    // hardly a warp has more than the others had: most need no atomic
+    if (threadIdx.x % 32 == 0 && b > __ldcg(to)) atomicMax(to, b);
 }
 
 // LANES read a row, eight columns each; a thread's rows are asked for together (one after
@@ -155,7 +156,11 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
 
 // ------------------------------------------------------------------ gradients
 
-constexpr int kBwdThreads = 320;  // eight warps on the tiles, one copies, one issues products
+// Sixteen warps on the tiles, four beside one another on a tile's columns, so that each
+// SM partition has four to hide their waits in (with two, 8192 x 8 heads of 64 took
+// 370 us); then one warp that copies and one that issues products.
+constexpr int kWarps = 16, kColumns = 32;  // columns of a warp's part of a tile
+constexpr int kBwdThreads = (kWarps + 2) * 32;
 
 // Barriers of one of the two kinds of work.  Each goes from item to item with its
 // phases running on.
@@ -269,17 +274,14 @@ __device__ __forceinline__ void zero_rows(char *tile, int rows)
             reinterpret_cast<uint4 *>(tile + c * kSlabBytes)[i] = make_uint4(0, 0, 0, 0);
 }
 
-// 64 values as 32 columns of the A operand.
+// A warp's 32 values of a row as 16 columns of the A operand.
 template <typename T>
-__device__ __forceinline__ void store_half(unsigned at, const float (&v)[64])
+__device__ __forceinline__ void store_part(unsigned at, const float (&v)[kColumns])
 {
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 64; i += 32) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = pack2<T>(v[i + 2 * e], v[i + 2 * e + 1]);
-        st16(at + i / 2, w);
-    }
+    for (int e = 0; e < 16; ++e) w[e] = pack2<T>(v[2 * e], v[2 * e + 1]);
+    st16(at, w);
 }
 
 // A thread's row of an accumulator, columns [from, to), times `scale` to memory; zeros
@@ -343,7 +345,7 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
     char *const ring_stats = ring + 2 * kStages * kTile;
     const int lane = threadIdx.x % 32;
 
-    if (warp == 8) {
+    if (warp == kWarps) {
         int it = 0;
         unsigned uses = 0, patches = 0;
         for (unsigned u; ok && (u = item_of(n)) < a.key_items; ++n) {
@@ -402,7 +404,7 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
             // the other kind's tiles take the place of these
             ok = attn_wait_warp(&bar.own_empty, (uses - 1) & 1, failed);
         }
-    } else if (warp == 9) {
+    } else if (warp == kWarps + 1) {
         const unsigned leader = elect_leader();
         const int steps = (s.dim + 15) / 16;
         const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
@@ -440,16 +442,16 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
             if (kTwo && total > 1 && !(ok = scores())) break;
             for (int it = 0; it < total; ++it, phase ^= 1) {
                 const Desc tile = advance(ring_mn, 2 * sum_of.slot * kTile);
-                const unsigned p_at = s_at + (kTwo ? phase * 128 : 0), ds_at = kTwo ? p_at + 32 : dp_at;
+                const unsigned p_at = s_at + (kTwo ? phase * 128 : 0), ds_at = kTwo ? p_at + 16 : dp_at;
                 const bool more = it + 1 < total;
                 if (!(ok = attn_wait_warp(&bar.p_full, phase, failed))) break;
                 fence_after();
-                product_rows<64>(dv_at, p_at, advance(tile, kTile), id_d, it > 0, leader);
+                product_parts(dv_at, p_at, advance(tile, kTile), id_d, it > 0, leader);
                 if (!kTwo && more && !(ok = scores())) break;
                 if (!(ok = attn_wait_warp(&bar.ds_full, phase, failed))) break;
                 fence_after();
                 if (kTwo && more) products();
-                product_rows<64>(dk_at, ds_at, tile, id_d, it > 0, leader);
+                product_parts(dk_at, ds_at, tile, id_d, it > 0, leader);
                 commit(empty + 8 * sum_of.slot, leader);
                 sum_of.next();
                 if (!kTwo && more) products();
@@ -460,9 +462,9 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
             commit(smem_u32(&bar.own_empty), leader);
         }
     } else {
-        const int half = warp / 4, row = threadIdx.x % 128;
+        const int part = warp / 4, row = threadIdx.x % 128;
         const unsigned lanes = unsigned(warp % 4) << 21;
-        const unsigned my_dp = dp_at + lanes + half * 64;
+        const unsigned my_dp = dp_at + lanes + part * kColumns;
         const f32x2 c2 = both(a.scale_log2);
         RingAt<kStages> at;
         unsigned uses = 0, phase = 0, tiles = 0;
@@ -475,25 +477,24 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
             const Scales sc = scales_of<T>(a, w.head);
             for (int it = 0, t = k.from; ok && it < k.total; ++it, phase ^= 1) {
                 const float *const stats =
-                    reinterpret_cast<const float *>(ring_stats + at.slot * kStatsBytes) + half * 64;
+                    reinterpret_cast<const float *>(ring_stats + at.slot * kStatsBytes) + part * kColumns;
                 // columns before `hidden` are queries that do not see this key
-                const int hidden = key >= pl.keys ? 64
-                                   : s.causal     ? key - pl.shift - t * kAttnTile - half * 64
+                const int hidden = key >= pl.keys ? kColumns
+                                   : s.causal     ? key - pl.shift - t * kAttnTile - part * kColumns
                                                   : 0;
                 const bool masked = __any_sync(0xffffffffu, hidden > 0);
-                const unsigned my_s = s_at + lanes + (kTwo ? phase * 128 : 0) + half * 64;
+                const unsigned my_s = s_at + lanes + (kTwo ? phase * 128 : 0) + part * kColumns;
                 ok = attn_wait_warp(&bar.full[at.slot], at.parity, failed) &&
                      attn_wait_warp(&bar.s_full[kTwo ? phase : 0], kTwo ? tiles >> 1 & 1 : phase, failed);
                 if (!ok) break;
                 ++tiles;
                 at.next();
                 fence_after();
-                float p[64];
+                float p[kColumns];
                 ld32(my_s, reinterpret_cast<uint32_t *>(p));
-                ld32(my_s + 32, reinterpret_cast<uint32_t *>(p) + 32);
                 wait_ld();
 #pragma unroll
-                for (int i = 0; i < 64; i += 4) {
+                for (int i = 0; i < kColumns; i += 4) {
                     const float4 l = *reinterpret_cast<const float4 *>(stats + i);
                     const float2 x = halves(fma2(pair(p[i], p[i + 1]), c2, pair(l.x, l.y)));
                     const float2 y = halves(fma2(pair(p[i + 2], p[i + 3]), c2, pair(l.z, l.w)));
@@ -504,21 +505,20 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                 }
                 if (masked) {
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) p[i] = i < hidden ? 0.0f : p[i];
+                    for (int i = 0; i < kColumns; ++i) p[i] = i < hidden ? 0.0f : p[i];
                 }
-                store_half<T>(my_s, p);
+                store_part<T>(my_s, p);
                 wait_st();
                 fence_before();
                 mbar_arrive(&bar.p_full);
                 ok = attn_wait_warp(&bar.dp_full, phase, failed);
                 if (!ok) break;
                 fence_after();
-                float d[64];
+                float d[kColumns];
                 ld32(my_dp, reinterpret_cast<uint32_t *>(d));
-                ld32(my_dp + 32, reinterpret_cast<uint32_t *>(d) + 32);
                 wait_ld();
 #pragma unroll
-                for (int i = 0; i < 64; i += 4) {
+                for (int i = 0; i < kColumns; i += 4) {
                     const float4 m = *reinterpret_cast<const float4 *>(stats + kAttnTile + i);
                     f32x2 x = add2(pair(d[i], d[i + 1]), pair(m.x, m.y));
                     f32x2 y = add2(pair(d[i + 2], d[i + 3]), pair(m.z, m.w));
@@ -535,9 +535,9 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                 }
                 if (masked) {
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) d[i] = i < hidden ? 0.0f : d[i];
+                    for (int i = 0; i < kColumns; ++i) d[i] = i < hidden ? 0.0f : d[i];
                 }
-                store_half<T>(kTwo ? my_s + 32 : my_dp, d);
+                store_part<T>(kTwo ? my_s + 16 : my_dp, d);
                 wait_st();
                 fence_before();
                 mbar_arrive(&bar.ds_full);
@@ -549,9 +549,12 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
             const int count = !w.there ? 0 : s.packed ? pl.keys : s.k_tokens;
             const bool mine = w.there && key < count, none = k.total == 0 || key >= pl.keys;
             const long long out_at = ((long long)pl.batch * s.k_tokens + pl.k_row + key) * s.kv_heads + w.head;
-            T *const out = static_cast<T *>(half ? a.dk : a.dv);
-            store_row<T>((half ? dk_at : dv_at) + lanes, 0, s.dim, half ? a.scale * sc.inv_ds : sc.inv_p, none, ok,
-                         mine && out, out + out_at * s.dim);
+            // two parts store dv, two dk, half of the columns each
+            const bool is_dk = part >= 2;
+            const int cut = min(s.dim, (s.dim / 2 + 15) / 16 * 16);
+            T *const out = static_cast<T *>(is_dk ? a.dk : a.dv);
+            store_row<T>((is_dk ? dk_at : dv_at) + lanes, part & 1 ? cut : 0, part & 1 ? s.dim : cut,
+                         is_dk ? a.scale * sc.inv_ds : sc.inv_p, none, ok, mine && out, out + out_at * s.dim);
         }
         // the sums are read: tensor memory is the other kind's
         fence_before();
@@ -585,7 +588,7 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
     uint64_t *const k_empty = bar.empty, *const v_empty = bar.empty + kKeys;
     const int lane = threadIdx.x % 32;
 
-    if (warp == 8) {
+    if (warp == kWarps) {
         RingAt<kKeys> k_at;
         RingAt<kValues> v_at;
         int issued = 0;  // pairs
@@ -642,7 +645,7 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
             for (int i = max(0, issued - kValues); i < issued; ++i)
                 mbar_wait_bounded(&v_full[i % kValues], (i / kValues) & 1, kAttnDrainCycles);
         }
-    } else if (warp == 9) {
+    } else if (warp == kWarps + 1) {
         const unsigned leader = elect_leader();
         const int steps = (s.dim + 15) / 16;
         const unsigned id_s = instr_desc<T>(kAttnTile, false), id_d = instr_desc<T>(steps * 16, true);
@@ -686,7 +689,7 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
                 if (!(ok = attn_wait_warp(&bar.ds_full, phase, failed))) break;
                 fence_after();
                 if (j + 1 < total && !(ok = products())) break;
-                product_rows<64>(dq_at, s_at + phase * 128, advance(keys_mn, sum_of.slot * kTile), id_d, j > 0,
+                product_parts(dq_at, s_at + phase * 128, advance(keys_mn, sum_of.slot * kTile), id_d, j > 0,
                                  leader);
                 commit(smem_u32(&k_empty[sum_of.slot]), leader);
                 sum_of.next();
@@ -697,7 +700,7 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
             commit(smem_u32(&bar.own_empty), leader);
         }
     } else {
-        const int half = warp / 4, row = threadIdx.x % 128;
+        const int part = warp / 4, row = threadIdx.x % 128;
         const unsigned lanes = unsigned(warp % 4) << 21;
         const f32x2 c2 = both(a.scale_log2);
         unsigned uses = 0, tiles = 0;
@@ -714,18 +717,18 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
             const f32x2 n2 = both(stats[kAttnTile + row] * sc.ds);
             const int end = s.causal ? min(pl.keys, query + 1 + pl.shift) : pl.keys;
             for (int j = 0; ok && j < total; ++j, ++tiles) {
-                const unsigned my_s = s_at + lanes + (tiles & 1) * 128 + half * 64, my_dp = dp_at + lanes + half * 64;
-                const int left = end - j * kAttnTile - half * 64;
-                const bool masked = __any_sync(0xffffffffu, left < 64);
+                const unsigned my_s = s_at + lanes + (tiles & 1) * 128 + part * kColumns;
+                const unsigned my_dp = dp_at + lanes + part * kColumns;
+                const int left = end - j * kAttnTile - part * kColumns;
+                const bool masked = __any_sync(0xffffffffu, left < kColumns);
                 ok = attn_wait_warp(&bar.s_full[tiles & 1], (tiles >> 1) & 1, failed);
                 if (!ok) break;
                 fence_after();
-                float p[64], d[64];
+                float p[kColumns], d[kColumns];
                 ld32(my_s, reinterpret_cast<uint32_t *>(p));
-                ld32(my_s + 32, reinterpret_cast<uint32_t *>(p) + 32);
                 wait_ld();
 #pragma unroll
-                for (int i = 0; i < 64; i += 2) {
+                for (int i = 0; i < kColumns; i += 2) {
                     const float2 x = halves(fma2(pair(p[i], p[i + 1]), c2, l2));
                     p[i] = exp2_fast(x.x);
                     p[i + 1] = exp2_fast(x.y);
@@ -734,10 +737,9 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
                 if (!ok) break;
                 fence_after();
                 ld32(my_dp, reinterpret_cast<uint32_t *>(d));
-                ld32(my_dp + 32, reinterpret_cast<uint32_t *>(d) + 32);
                 wait_ld();
 #pragma unroll
-                for (int i = 0; i < 64; i += 2) {
+                for (int i = 0; i < kColumns; i += 2) {
                     f32x2 x = pair(d[i], d[i + 1]);
                     x = kScaled<T> ? fma2(x, both(sc.ds), n2) : add2(x, n2);
                     const float2 e = halves(mul2(x, pair(p[i], p[i + 1])));
@@ -746,9 +748,9 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
                 }
                 if (masked) {
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) d[i] = i < left ? d[i] : 0.0f;
+                    for (int i = 0; i < kColumns; ++i) d[i] = i < left ? d[i] : 0.0f;
                 }
-                store_half<T>(my_s, d);
+                store_part<T>(my_s, d);
                 wait_st();
                 fence_before();
                 mbar_arrive(&bar.ds_full);
@@ -757,9 +759,8 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
             uses += total > 0;
             fence_after();
             const long long out_at = ((long long)pl.batch * s.q_tokens + pl.q_row + query) * s.heads + w.head;
-            const int cut = min(s.dim, 64);
-            store_row<T>(dq_at + lanes, half ? cut : 0, half ? s.dim : cut, a.scale * sc.inv_ds, total == 0, ok,
-                         query < pl.queries, static_cast<T *>(a.dq) + out_at * s.dim);
+            store_row<T>(dq_at + lanes, min(s.dim, part * 32), min(s.dim, part * 32 + 32), a.scale * sc.inv_ds,
+                         total == 0, ok, query < pl.queries, static_cast<T *>(a.dq) + out_at * s.dim);
         }
     }
 }
@@ -771,7 +772,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
     char *const base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     BwdShared &sh = *reinterpret_cast<BwdShared *>(base + bwd_smem<DP>() - 1024 - sizeof(BwdShared));
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
-    if (warp == 8 && lane == 0) {
+    if (warp == kWarps && lane == 0) {
         for (const CUtensorMap *m : {&a.q, &a.k, &a.v, &a.g}) prefetch_map(m);
         sh.failed = 0;
         for (BwdBarriers *b : {&sh.keys, &sh.queries}) {
@@ -782,14 +783,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
                 mbar_init(&b->full[i], 1);
                 mbar_init(&b->empty[i], 1);
             }
-            mbar_init(&b->p_full, 256);
-            mbar_init(&b->ds_full, 256);
+            mbar_init(&b->p_full, kWarps * 32);
+            mbar_init(&b->ds_full, kWarps * 32);
         }
-        mbar_init(&sh.keys_stored, 256);
+        mbar_init(&sh.keys_stored, kWarps * 32);
         mbar_init(&sh.drained, 1);
         mbar_init_fence();
     }
-    if (warp == 9) alloc_all(&sh.tmem);
+    if (warp == kWarps + 1) alloc_all(&sh.tmem);
     fence_before();
     __syncthreads();
     fence_after();
@@ -800,16 +801,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
     by_keys<T, DP>(a, base, sh, warp, tmem, n, ok);
     // a block that failed has every role leave; those on the tiles still write their
     // NaN
-    if (ok || warp < 8) by_queries<T, DP>(a, base, sh, warp, tmem, n, ok);
-    if (!ok && warp == 9) {
+    if (ok || warp < kWarps) by_queries<T, DP>(a, base, sh, warp, tmem, n, ok);
+    if (!ok && warp == kWarps + 1) {
         commit(smem_u32(&sh.drained), elect_leader());
         mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
     }
-    if (!ok && warp == 8 && lane == 0) atomicOr(&g_attention_status, 4u);
+    if (!ok && warp == kWarps && lane == 0) atomicOr(&g_attention_status, 4u);
     __syncwarp();
     fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kWarps + 1) {
         fence_after();
         free_all(tmem);
     }

@@ -114,15 +114,14 @@ __device__ __forceinline__ void product_half(unsigned d, unsigned a, Desc b, uns
     for (int i = 0; i < 4; ++i) mma_ta(d, a + i * 8, advance(b, step_mn(i)), idesc, i > 0 || add, leader);
 }
 
-// D (+)= A B: A [128, 128] in tensor memory, its two halves of 64 columns HALF columns of
-// tensor memory apart, B's 128 rows summed over.
-template <int HALF>
-__device__ __forceinline__ void product_rows(unsigned d, unsigned a, Desc b, unsigned idesc, bool add,
-                                             unsigned leader)
+// D (+)= A B: A [128, 128] in tensor memory, its quarters of 32 columns (16 of tensor
+// memory) 32 columns of tensor memory apart, B's 128 rows summed over.
+__device__ __forceinline__ void product_parts(unsigned d, unsigned a, Desc b, unsigned idesc, bool add,
+                                              unsigned leader)
 {
 #pragma unroll
     for (int i = 0; i < kTileRows / 16; ++i)
-        mma_ta(d, a + (i / 4) * HALF + (i % 4) * 8, advance(b, step_mn(i)), idesc, i > 0 || add, leader);
+        mma_ta(d, a + (i / 2) * 32 + (i % 2) * 8, advance(b, step_mn(i)), idesc, i > 0 || add, leader);
 }
 
 // Arrives on the barrier (by its shared-memory address) when all products issued by the
