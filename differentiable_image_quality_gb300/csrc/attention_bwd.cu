@@ -66,91 +66,109 @@ __device__ __forceinline__ float largest8(const uint4 &w)
     return m;
 }
 
-template <typename T>
-__device__ void store_largest(float m, unsigned *to)
-{
-    unsigned b = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    // hardly a warp has more than the others had: most need no atomic
-    if (threadIdx.x % 32 == 0 && b > __ldcg(to)) atomicMax(to, b);
-}
+// A block has 32 tokens and up to 64 heads, whose rows lie one behind the other in
+// memory; LANES read a row, eight columns each, and a thread asks for four rows
+// together.  (A block to a tile of one head, rows far apart: 14000 x 16 rows of 64 took
+// 79 us.)  The sums go to the tiles through shared memory.
+constexpr int kSumTokens = 32, kSumHeads = 64, kSumRows = 4;
 
-// LANES read a row, eight columns each; a thread's rows are asked for together (one after
-// the other, 14000 x 16 rows of 64 took 67 us).
 template <typename T, int LANES>
-__global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnBwdArgs a)
+__global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnBwdArgs a, const unsigned q_blocks)
 {
-    constexpr int kTeams = kSumThreads / LANES, kRows = kAttnTile / kTeams;
+    constexpr int kTeams = kSumThreads / LANES;
     __shared__ AttnPlace place;
     __shared__ int there;
+    __shared__ float sums[kSumHeads][kSumTokens + 1];
+    __shared__ unsigned most[kSumHeads];  // the largest of each head, as bits (float16)
     const AttnShape &s = a.s;
-    const bool values = int(blockIdx.x) >= a.q_tiles;  // the largest |v| (float16)
-    const int head = blockIdx.y;
+    const bool values = blockIdx.x >= q_blocks;  // the largest |v| (float16)
+    const int from = blockIdx.y * kSumHeads, heads = min(kSumHeads, (values ? s.kv_heads : s.heads) - from);
     pdl_trigger();
-    if (values && head >= s.kv_heads) return;
+    if (heads <= 0) return;
     if (threadIdx.x < 32) {
         AttnPlace p;
-        const bool ok = values ? find_place<true>(s, blockIdx.x - a.q_tiles, kAttnTile, p)
-                               : find_place<false>(s, blockIdx.x, kAttnTile, p);
+        const bool ok = values ? find_place<true>(s, blockIdx.x - q_blocks, kSumTokens, p)
+                               : find_place<false>(s, blockIdx.x, kSumTokens, p);
         if (threadIdx.x == 0) {
             place = p;
             there = ok;
         }
+    } else if (threadIdx.x - 32 < kSumHeads) {
+        most[threadIdx.x - 32] = 0;
     }
     __syncthreads();
     if (!there) return;
     const AttnPlace pl = place;
     const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
     const bool mine = lane * 8 < s.dim;
-    const int first = pl.tile * kAttnTile + team, rows = values ? pl.keys : pl.queries;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const T *const x = values ? static_cast<const T *>(a.v_data) + pl.batch * a.v_batch + pl.k_row * a.v_token +
-                                    head * a.v_head + lane * 8
-                              : static_cast<const T *>(a.g_data) + pl.batch * a.g_batch + pl.q_row * a.g_token +
-                                    head * a.g_head + lane * 8;
-    const long long step = values ? a.v_token : a.g_token;
-    Raw8<T> rx[kRows], ro[kRows];
+    const int first = pl.tile * kSumTokens, rows = values ? pl.keys : pl.queries;
+    const int count = max(0, min(kSumTokens, rows - first));
+    const T *const x = values ? static_cast<const T *>(a.v_data) + pl.batch * a.v_batch +
+                                    (long long)(pl.k_row + first) * a.v_token + from * a.v_head + lane * 8
+                              : static_cast<const T *>(a.g_data) + pl.batch * a.g_batch +
+                                    (long long)(pl.q_row + first) * a.g_token + from * a.g_head + lane * 8;
+    const long long x_token = values ? a.v_token : a.g_token, x_head = values ? a.v_head : a.g_head;
+    const T *const o = static_cast<const T *>(a.out) + pl.batch * a.o_batch +
+                       (long long)(pl.q_row + first) * a.o_token + from * a.o_head + lane * 8;
+    const int all = count * heads;
+    for (int base = 0; base < all; base += kTeams * kSumRows) {  // all threads alike: they shuffle
+        Raw8<T> rx[kSumRows], ro[kSumRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int t = first + i * kTeams;
-        rx[i].w[0] = mine && t < rows ? *reinterpret_cast<const uint4 *>(x + t * step) : zero;
-    }
-    if (!values) {
-        const T *const o = static_cast<const T *>(a.out) + pl.batch * a.o_batch + pl.q_row * a.o_token +
-                           head * a.o_head + lane * 8;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int t = first + i * kTeams;
-            ro[i].w[0] = mine && t < rows ? *reinterpret_cast<const uint4 *>(o + t * a.o_token) : zero;
+        for (int i = 0; i < kSumRows; ++i) {
+            const int r = base + i * kTeams + team, t = r / heads, h = r - t * heads;
+            rx[i].w[0] = ro[i].w[0] = make_uint4(0, 0, 0, 0);
+            if (!mine || r >= all) continue;
+            rx[i].w[0] = *reinterpret_cast<const uint4 *>(x + t * x_token + h * x_head);
+            if (!values) ro[i].w[0] = *reinterpret_cast<const uint4 *>(o + t * a.o_token + h * a.o_head);
         }
-        float *const stats =
-            a.stats + ((long long)head * a.q_tiles + pl.q_tiles_before + pl.tile) * 2 * kAttnTile;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int t = first + i * kTeams;
-            float u[8], v[8], sum = 0.0f;
-            unpack8<T>(rx[i], u);
-            unpack8<T>(ro[i], v);
+        for (int i = 0; i < kSumRows; ++i) {
+            const int r = base + i * kTeams + team, t = r / heads, h = r - t * heads;
+            if (!values) {
+                float u[8], v[8], sum = 0.0f;
+                unpack8<T>(rx[i], u);
+                unpack8<T>(ro[i], v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(u[e], v[e], sum);
+                for (int e = 0; e < 8; ++e) sum = fmaf(u[e], v[e], sum);
+                __syncwarp();
 #pragma unroll
-            for (int d = LANES / 2; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            if (lane == 0) {
-                float l = -INFINITY;
-                if (t < rows) {
-                    const float lse = a.lse[((long long)pl.batch * s.heads + head) * s.q_tokens + pl.q_row + t];
-                    if (lse != -INFINITY) l = (kScaled<T> ? kProbBits : 0.0f) - lse * 1.4426950408889634f;
-                }
-                stats[team + i * kTeams] = l;
-                stats[kAttnTile + team + i * kTeams] = -sum;
+                for (int d = LANES / 2; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (lane == 0 && r < all) sums[h][t] = sum;
+            }
+            if constexpr (kScaled<T>) {
+                unsigned m = __float_as_uint(largest8<T>(rx[i].w[0]));
+                __syncwarp();
+#pragma unroll
+                for (int d = LANES / 2; d; d /= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+                if (lane == 0 && r < all) atomicMax(&most[h], m);
             }
         }
     }
+    __syncthreads();
     if constexpr (kScaled<T>) {
-        float largest = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
-            largest = __uint_as_float(max(__float_as_uint(largest), __float_as_uint(largest8<T>(rx[i].w[0]))));
-        store_largest<T>(largest, a.largest + (values ? s.kv_heads + head : head / s.group));
+        // hardly a block has more than the others had: most need no atomic in memory
+        const int h = threadIdx.x;
+        if (h < heads) {
+            unsigned *const to = a.largest + (values ? s.kv_heads + from + h : (from + h) / s.group);
+            if (most[h] > __ldcg(to)) atomicMax(to, most[h]);
+        }
+    }
+    if (values) return;
+    // the sequence's last block also has the rows that its last tile does not have
+    const int end = first + kSumTokens >= rows ? (rows + kAttnTile - 1) / kAttnTile * kAttnTile : first + kSumTokens;
+    const int width = end - first;
+    for (int i = threadIdx.x; i < heads * width; i += kSumThreads) {
+        const int h = i / width, r = i - h * width, t = first + r, head = from + h;
+        float l = -INFINITY, sum = 0.0f;
+        if (r < count) {
+            const float lse = a.lse[((long long)pl.batch * s.heads + head) * s.q_tokens + pl.q_row + t];
+            if (lse != -INFINITY) l = (kScaled<T> ? kProbBits : 0.0f) - lse * 1.4426950408889634f;
+            sum = sums[h][r];
+        }
+        float *const stats =
+            a.stats + ((long long)head * a.q_tiles + pl.q_tiles_before + t / kAttnTile) * 2 * kAttnTile;
+        stats[t % kAttnTile] = l;
+        stats[kAttnTile + t % kAttnTile] = -sum;
     }
 }
 
@@ -828,14 +846,16 @@ cudaError_t launch(const AttnBwdArgs &a, cudaStream_t stream)
         e = cudaMemsetAsync(a.largest, 0, size_t(2) * a.s.kv_heads * sizeof(unsigned), stream);
         if (e != cudaSuccess) return e;
     }
-    const dim3 grid(unsigned(a.q_tiles + (kScaled<T> ? a.k_tiles : 0)), unsigned(a.s.heads));
     if (a.q_tiles > 0) {
+        const unsigned q_blocks = unsigned(most_tiles(a.s, a.s.q_tokens, kSumTokens));
+        const unsigned v_blocks = kScaled<T> ? unsigned(most_tiles(a.s, a.s.k_tokens, kSumTokens)) : 0;
+        const dim3 grid(q_blocks + v_blocks, unsigned((a.s.heads + kSumHeads - 1) / kSumHeads));
         if (a.s.dim <= 32)
-            attention_sums_kernel<T, 4><<<grid, kSumThreads, 0, stream>>>(a);
+            attention_sums_kernel<T, 4><<<grid, kSumThreads, 0, stream>>>(a, q_blocks);
         else if (a.s.dim <= 64)
-            attention_sums_kernel<T, 8><<<grid, kSumThreads, 0, stream>>>(a);
+            attention_sums_kernel<T, 8><<<grid, kSumThreads, 0, stream>>>(a, q_blocks);
         else
-            attention_sums_kernel<T, 16><<<grid, kSumThreads, 0, stream>>>(a);
+            attention_sums_kernel<T, 16><<<grid, kSumThreads, 0, stream>>>(a, q_blocks);
     }
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
