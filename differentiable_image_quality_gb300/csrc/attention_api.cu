@@ -45,6 +45,8 @@ Extent floats(const gbssim_attention &d, const float *p)
     return {p, p ? size_t(q_rows(d)) * d.heads * 4 : 0};
 }
 
+Extent ints(const int *p, int n) { return {p, p ? size_t(n) * 4 : 0}; }
+
 bool multiple16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // Strides of extents above one: positive multiples of 16 bytes, below 2^40 bytes.
@@ -181,9 +183,12 @@ extern "C" int gbssim_attention_fwd(const gbssim_attention *d, void *out, float 
     const FwdPlan p = plan_fwd(*d);
     const size_t need = part_floats(*d, p) * sizeof(float);
     if (need && (!workspace || !multiple16(workspace) || workspace_bytes < need)) return GBSSIM_EWORKSPACE;
-    const Extent in[3] = {heads_extent(*d, d->q, d->q_tokens, d->heads),
+    const Extent in[6] = {heads_extent(*d, d->q, d->q_tokens, d->heads),
                           heads_extent(*d, d->k, d->k_tokens, d->kv_heads),
-                          heads_extent(*d, d->v, d->k_tokens, d->kv_heads)};
+                          heads_extent(*d, d->v, d->k_tokens, d->kv_heads),
+                          ints(d->kv_lengths, d->sequences),
+                          ints(d->q_offsets, d->sequences + 1),
+                          ints(d->k_offsets, d->sequences + 1)};
     const Extent outs[3] = {dense_extent(*d, out, q_rows(*d), d->heads), floats(*d, lse_or_null),
                             {workspace, need}};
     for (int i = 0; i < 3; ++i) {
@@ -237,9 +242,12 @@ extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_head
     if (reinterpret_cast<uintptr_t>(lse) % 4) return GBSSIM_EALIGN;
     const size_t need = queries ? bwd_bytes(*d) : 0;
     if (need && (!workspace || !multiple16(workspace) || workspace_bytes < need)) return GBSSIM_EWORKSPACE;
-    const Extent in[6] = {heads_extent(*d, d->q, d->q_tokens, d->heads),
+    const Extent in[9] = {heads_extent(*d, d->q, d->q_tokens, d->heads),
                           heads_extent(*d, d->k, d->k_tokens, d->kv_heads),
                           heads_extent(*d, d->v, d->k_tokens, d->kv_heads),
+                          ints(d->kv_lengths, d->sequences),
+                          ints(d->q_offsets, d->sequences + 1),
+                          ints(d->k_offsets, d->sequences + 1),
                           heads_extent(*d, *grad_out, d->q_tokens, d->heads),
                           heads_extent(*d, *out, d->q_tokens, d->heads), floats(*d, lse)};
     const Extent outs[4] = {dense_extent(*d, grad_q_or_null, q_rows(*d), d->heads),

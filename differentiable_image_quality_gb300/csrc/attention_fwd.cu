@@ -332,7 +332,9 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
                 for (int i = 4; i < 128; i += 2) m[i / 2 % 4] = fmaxf(fmaxf(m[i / 2 % 4], v[i]), v[i + 1]);
                 const float now = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
                 if (__any_sync(0xffffffffu, now > top + kLateMax)) {
-                    const float next = fmaxf(top, now);
+                    // each row by itself: what else is in the tile (rows that are no query
+                    // among them) changes no bit of it
+                    const float next = now > top + kLateMax ? now : top;
                     const float f = next == -INFINITY ? 1.0f : exp2_fast(top - next);
                     top = next;
                     sum *= f;

@@ -51,12 +51,14 @@ enum Mode {
     kSingle     // a pair or a column a thread: any alignment
 };
 
-// The fraction of a turn that a unit of position is, times 2^64.
+// The fraction of a turn that a unit of position is, times 2^64; of a negative frequency
+// from its magnitude, whose fraction is exact.
 __device__ __forceinline__ unsigned long long turn_fraction(double f)
 {
-    double t = f * 0.15915494309189535;  // 1 / (2 pi)
+    double t = fabs(f) * 0.15915494309189535;  // 1 / (2 pi)
     t -= floor(t);
-    return t < 1.0 ? (unsigned long long)(t * 18446744073709551616.0) : 0ull;
+    const unsigned long long part = t < 1.0 ? (unsigned long long)(t * 18446744073709551616.0) : 0ull;
+    return f < 0.0 ? 0ull - part : part;
 }
 
 // cos and sin of position x fraction.  Where results are rounded to 16 bits (2^-8, 2^-11)

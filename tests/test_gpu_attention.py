@@ -441,3 +441,251 @@ def test_output_strides(pkg):
     for a, b in zip(pkg.attention_bwd(out, q, k, v, out, lse),
                     pkg.attention_bwd(turned, q, k, v, turned, lse)):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------- streams, graphs, failures
+
+def test_waits_that_run_out(pkg):
+    """Copies announced larger than they are: the bounded waits run out, the rows of
+    those blocks are NaN, the device status says so, and the next call is right."""
+    import ctypes
+
+    q, k, v = inputs(30, 1, 200, 200, 2, 1, 64, BF)
+    g = normal(torch.Generator(device="cuda").manual_seed(31), *q.shape)
+
+    def step():
+        out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
+        return (out, lse, *pkg.attention_bwd(g, q, k, v, out, lse))
+
+    flags = ctypes.c_uint(0)
+    with pkg._abi.using_test_library() as lib:
+        want = step()
+        assert lib.gbssim_device_status(ctypes.byref(flags)) == 0 and flags.value == 0
+        lib.gbssim_tune_attention(16)
+        try:
+            out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
+            torch.cuda.synchronize()
+            grads = pkg.attention_bwd(g, q, k, v, want[0], want[1])
+            torch.cuda.synchronize()
+        finally:
+            lib.gbssim_tune_attention(0)
+        for t in (out, lse, *grads):
+            assert t.isnan().all()
+        assert lib.gbssim_device_status(ctypes.byref(flags)) == 0
+        assert flags.value == 4  # GBSSIM_DEV_ATTENTION_TIMEOUT
+        again = step()
+        assert lib.gbssim_device_status(ctypes.byref(flags)) == 0 and flags.value == 0
+    assert all(torch.equal(a, b) for a, b in zip(want, again))
+
+
+# batch form with few blocks (keys in parts), packed, float16
+GRAPHS = [dict(shape=((1, 2, 4, 64), (1, 1500, 2, 64)), dtype=BF, packed=None),
+          dict(shape=((300, 4, 72), (300, 2, 72)), dtype=HF, packed=[100, 0, 170])]
+
+
+@pytest.mark.parametrize("case", GRAPHS, ids=["batch", "packed"])
+def test_in_a_graph(pkg, case):
+    """Captured with the backward, replayed on new inputs and new offsets; two graphs
+    whose replays overlap on two streams do not share memory."""
+    q_shape, k_shape = case["shape"]
+
+    def make(seed):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        t = [normal(gen, *s, dtype=case["dtype"]) for s in (q_shape, k_shape, k_shape, q_shape)]
+        offsets = None
+        if case["packed"]:
+            lengths = case["packed"][seed % 3:] + case["packed"][:seed % 3]
+            offsets = pack_offsets(lengths)[1]
+        return t, offsets
+
+    def step(t, offsets):
+        q, k, v, g = t
+        out, lse = pkg.attention_fwd(q, k, v, offsets=offsets, want_stats=True)
+        return (out, lse, *pkg.attention_bwd(g, q, k, v, out, lse, offsets=offsets))
+
+    graphs = []
+    for n in range(2):
+        held, offsets = make(40 + n)
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            step(held, offsets)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            got = step(held, offsets)
+        graphs.append((graph, stream, held, offsets, got))
+    for seed in (50, 51, 52):
+        want = []
+        for n, (graph, stream, held, offsets, got) in enumerate(graphs):
+            fresh, fresh_offsets = make(seed + 10 * n)
+            want.append([t.clone() for t in step(fresh, fresh_offsets)])
+            for a, b in zip(held, fresh):
+                a.copy_(b)
+            if offsets is not None:
+                offsets.copy_(fresh_offsets)
+        torch.cuda.synchronize()
+        for graph, stream, *_ in graphs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (*_, got), ref in zip(graphs, want):
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_streams_and_threads(pkg):
+    """Calls from two host threads, on the default stream and on streams of their own."""
+    import threading
+
+    sets = [inputs(60 + n, 1, 1 + 70 * n, 1500, 4, 2, 64, BF) for n in range(2)]
+
+    def step(n):
+        q, k, v = sets[n]
+        out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
+        return (out, *pkg.attention_bwd(out, q, k, v, out, lse))
+
+    want = [step(n) for n in range(2)]
+    torch.cuda.synchronize()
+    for own in (False, True):
+        got, errors = [[], []], []
+
+        def worker(n):
+            try:
+                with torch.cuda.stream(torch.cuda.Stream() if own else torch.cuda.default_stream()):
+                    for _ in range(50):
+                        got[n].append(step(n))
+            except Exception as e:  # noqa: BLE001 - reported below
+                errors.append(repr(e))
+
+        threads = [threading.Thread(target=worker, args=(n,)) for n in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        torch.cuda.synchronize()
+        assert not errors, errors
+        for n in range(2):
+            assert len(got[n]) == 50
+            for r in got[n]:
+                assert all(torch.equal(a, b) for a, b in zip(r, want[n]))
+
+
+def test_bad_offsets_touch_nothing_else(pkg):
+    """Lengths and offsets out of their range: no result is promised, but every row that is
+    written is one of the outputs', and the next call is right."""
+    q, k, v = inputs(70, None, 200, 200, 2, 2, 64, BF)
+    good = pack_offsets([120, 80])[1]
+    want = pkg.attention_fwd(q, k, v, offsets=good)[0]
+    for bad in ([5, 400, -7], [0, 2 ** 31 - 1, 200], [-2 ** 31, 100, 50]):
+        offsets = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        out, lse = pkg.attention_fwd(q, k, v, offsets=offsets, want_stats=True)
+        pkg.attention_bwd(out, q, k, v, out, lse, offsets=offsets)
+    q4, k4, v4 = (t.view(2, 100, 2, 64) for t in (q, k, v))
+    lengths = torch.tensor([-5, 1000], dtype=torch.int32, device="cuda")
+    out = pkg.attention_fwd(q4, k4, v4, kv_lengths=lengths)[0]
+    assert (out[0] == 0).all() and torch.equal(out[1:], pkg.attention_fwd(q4[1:], k4[1:], v4[1:])[0])
+    assert torch.equal(pkg.attention_fwd(q, k, v, offsets=good)[0], want)
+
+
+def test_refusals(pkg):
+    q, k, v = inputs(71, 2, 10, 20, 4, 2, 64, BF)
+    off = torch.tensor([0, 10], dtype=torch.int32, device="cuda")
+
+    def bad(error, *a, **kw):
+        with pytest.raises(error):
+            pkg.fused_attention(*a, **kw)
+
+    bad(TypeError, q.float(), k.float(), v.float())
+    bad(TypeError, q, k.to(HF), v)
+    bad(TypeError, q, k, v.cpu())
+    bad(ValueError, q, k, v[:, :5])
+    bad(ValueError, q, k[:1], v[:1])
+    bad(ValueError, q[:, :, :3], k, v)
+    bad(ValueError, q[..., :60], k[..., :60], v[..., :60])
+    bad(ValueError, q[..., :56], k, v)
+    bad(ValueError, q[0], k[0], v[0])
+    bad(ValueError, q, k, v, offsets=off)
+    bad(ValueError, q, k, v, kv_offsets=off)
+    bad(ValueError, q[0], k[0], v[0], offsets=off)  # other rows without offsets of their own
+    bad(ValueError, q[0], k[0], v[0], offsets=off, kv_offsets=off[:1])
+    bad(ValueError, q[0], k[0], v[0], offsets=off, kv_lengths=off)
+    bad(TypeError, q, k, v, kv_lengths=[10, 20])
+    bad(TypeError, q, k, v, kv_lengths=off.long())
+    bad(ValueError, q, k, v, kv_lengths=off[:1])
+    bad(TypeError, q, k, v, kv_lengths=off.cpu())
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        bad(ValueError, q, k, v, scale=scale)
+    out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
+    for args in ((out[:1], q, k, v, out, lse), (out, q, k, v, out[:, :5], lse),
+                 (out, q, k, v, out, lse.transpose(1, 2)), (out, q, k, v, out, lse.double())):
+        with pytest.raises(ValueError):
+            pkg.attention_bwd(*args)
+    with pytest.raises(TypeError):
+        pkg.attention_bwd(out.float(), q, k, v, out, lse)
+
+
+# ------------------------------------------------------------- as they are used together
+
+def test_a_block_of_a_transformer(pkg):
+    """The norm before a block, q, k and v of one product, their positions, attention, the
+    output's product and the norms around the residual sum, against the same in float64,
+    with every gradient.
+
+    Each of the eleven tensors between the operators is rounded to bfloat16 (relative 2^-9
+    as a root mean square, 2^-8 at most), probabilities and their gradients once more:
+    errors that are independent add up to less than 2^-8 sqrt(13) of a gradient's norm
+    forward and back, 2 % taken together."""
+    gen = torch.Generator(device="cuda").manual_seed(80)
+    B, side, H, K, D, dim = 2, 9, 4, 2, 32, 128
+    T = side * side
+    x = normal(gen, B, T, dim, dtype=torch.float32)
+    w_in = normal(gen, (H + 2 * K) * D, dim, std=dim ** -0.5)
+    w_out = normal(gen, dim, H * D, std=(H * D) ** -0.5)
+    gain = (1 + 0.1 * torch.randn(dim, generator=gen, device="cuda"))
+    at = torch.stack(torch.meshgrid(torch.arange(side), torch.arange(side), indexing="ij"),
+                     -1).view(T, 2).cuda()
+    pairs = (8, 8)
+    f = pkg.rotary_frequencies(pairs)
+    g_x, g_u = normal(gen, B, T, dim, dtype=torch.float32), normal(gen, B, T, dim)
+
+    leaves = [t.clone().requires_grad_() for t in (x, w_in, w_out, gain)]
+    lx, li, lo, lg = leaves
+    _, u = pkg.fused_residual_norm(lx, pre_weight=lg, u_dtype=BF)
+    q, k, v = (t.unflatten(-1, (-1, D)) for t in (u @ li.T).split([H * D, K * D, K * D], -1))
+    q, k = pkg.fused_rotary(q, k, at, f, pairs)
+    y = pkg.fused_attention(q, k, v, causal=True).flatten(2) @ lo.T
+    x1, u1 = pkg.fused_residual_norm(lx, y, post_norm="rms", pre_weight=lg)
+    got = torch.autograd.grad((x1, u1), leaves, (g_x, g_u))
+
+    wide = [t.double().requires_grad_() for t in (x, w_in, w_out, gain)]
+    wx, wi, wo, wg = wide
+    rms = lambda t: t * (t.square().mean(-1, keepdim=True) + 1e-6).rsqrt()  # noqa: E731
+    q, k, v = (t.unflatten(-1, (-1, D)) for t in
+               ((rms(wx) * wg) @ wi.T).split([H * D, K * D, K * D], -1))
+    angle = (at.double()[:, [0] * 8 + [1] * 8] * f)[:, None]
+    turn = lambda t: torch.cat([t[..., :16] * angle.cos() - t[..., 16:] * angle.sin(),  # noqa: E731
+                                t[..., :16] * angle.sin() + t[..., 16:] * angle.cos()], -1)
+    q, k, v = turn(q), turn(k).repeat_interleave(H // K, 2), v.repeat_interleave(H // K, 2)
+    s = torch.einsum("bihd,bjhd->bhij", q, k) * D ** -0.5
+    s = s.masked_fill(torch.ones(T, T, dtype=torch.bool, device="cuda").triu(1), -float("inf"))
+    o = torch.einsum("bhij,bjhd->bihd", s.softmax(-1), v).flatten(2)
+    r1 = wx + rms(o @ wo.T)
+    ref_u = rms(r1) * wg
+    ref = torch.autograd.grad((r1, ref_u), wide, (g_x.double(), g_u.double()))
+    for a, b in ((x1, r1), (u1, ref_u), *zip(got, ref)):
+        assert (a.double() - b).norm() <= 0.02 * b.norm()
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1500, 4, 2, 64), (1, 4, 3000, 4, 2, 64),
+                                   (1, 50, 900, 2, 2, 128)], ids=str)
+def test_rows_do_not_depend_on_others(pkg, shape):
+    """Rows of a tile that are no query hold whatever shared memory held: results repeat bit
+    for bit whatever ran before."""
+    q, k, v = inputs(72, *shape, BF)
+    want = pkg.attention_fwd(q, k, v, want_stats=True)
+    loud = [300 * t for t in inputs(73, 2, 300, 300, 8, 8, 128, BF)]
+    for n in range(20):
+        if n % 2:
+            pkg.attention_fwd(*loud)
+        got = pkg.attention_fwd(q, k, v, want_stats=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), n

@@ -193,3 +193,55 @@ def test_empty(pkg):
     q = torch.empty(2, 0, 3, 16, device="cuda")
     out, _ = pkg.rotary(q, None, torch.empty(0, 1, dtype=torch.int32, device="cuda"), f, (4,))
     assert out.shape == q.shape
+
+
+def test_in_a_graph_and_on_another_stream(pkg):
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    pairs = (8, 8)
+    f, at = pkg.rotary_frequencies(pairs), torch.randint(0, 64, (50, 2), generator=gen, device="cuda")
+    q = normal(gen, 2, 50, 4, 32, dtype=BF)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        first = pkg.rotary(q, None, at, f, pairs)[0]
+    stream.synchronize()
+    assert torch.equal(first, pkg.rotary(q, None, at, f, pairs)[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = pkg.rotary(q, None, at, f, pairs, inverse=True)[0]
+    q.copy_(normal(gen, *q.shape, dtype=BF))
+    at.add_(3)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, pkg.rotary(q, None, at, f, pairs, inverse=True)[0])
+
+
+def test_refusals(pkg):
+    f = pkg.rotary_frequencies((4, 4))
+    q, at = torch.zeros(2, 6, 3, 32, device="cuda"), torch.zeros(6, 2, device="cuda")
+
+    def bad(error, q=q, k=None, at=at, f=f, pairs=(4, 4), **kw):
+        with pytest.raises(error):
+            pkg.fused_rotary(q, k, at, f, pairs, **kw)
+
+    bad(TypeError, q=q.double())
+    bad(TypeError, at=at.half())
+    bad(TypeError, f=f.float())
+    bad(TypeError, pairs=(4.0, 4.0))
+    bad(TypeError, k=q.cpu())
+    bad(ValueError, at=at.cpu())
+    bad(ValueError, f=f.cpu())
+    bad(ValueError, layout="interleaved")
+    bad(ValueError, pairs=(4, 5))
+    bad(ValueError, pairs=(8, 0))
+    bad(ValueError, pairs=())
+    bad(ValueError, pairs=(8,))
+    bad(ValueError, at=at[:5])
+    bad(ValueError, at=at.expand(3, 6, 2))
+    bad(ValueError, at=torch.zeros(2, 6, device="cuda").T)
+    bad(ValueError, k=q[:, :5])
+    bad(ValueError, k=q.bfloat16())
+    bad(ValueError, q=q[0, 0])
+    bad(ValueError, q=q.transpose(-1, -2).contiguous().transpose(-1, -2))
+    bad(ValueError, q=torch.zeros(2, 6, 1, 514, device="cuda"))
+    bad(ValueError, q=q[..., :14])
