@@ -178,14 +178,14 @@ inline cudaError_t allow_smem(Kernel kernel, std::atomic<unsigned long long> &do
 // A launch whose blocks may start while the kernel ahead on the stream ends; they wait
 // for it (pdl_wait) before they touch what it wrote.
 template <typename Args>
-inline cudaError_t launch_after(void (*kernel)(Args), unsigned grid, unsigned threads, size_t smem,
+inline cudaError_t launch_after(void (*kernel)(Args), dim3 grid, unsigned threads, size_t smem,
                                 cudaStream_t stream, const Args &a)
 {
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -224,6 +224,8 @@ struct AttnBwdArgs {
     float scale, scale_log2;
     int q_tiles, k_tiles;  // in all samples, or the most there can be (packed)
     unsigned key_items, items;  // of all blocks: tiles of keys, and with those of queries
+    int key_parts;              // that the query heads of a key head are parted into
+    float *parts;               // [key_parts][dv, dk] float32, where there are several
     int queries_wanted;
     int ragged;
     unsigned extra;  // test hook, see gbssim_tune_attention

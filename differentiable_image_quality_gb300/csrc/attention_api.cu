@@ -152,12 +152,38 @@ size_t part_floats(const gbssim_attention &d, const FwdPlan &p)
     return size_t(p.splits) * q_rows(d) * d.heads * (d.dim + 1);
 }
 
+// An item of keys goes over the queries of all heads that share them: with few key heads
+// a few items are long, and the others' blocks wait.  Then several blocks take some of
+// the heads each, and their sums are added after them: where the longest item is above
+// the average block's work and the parts save more than the 4 us of adding them (a tile
+// takes 0.8 us or more; 5 sequences of up to 600 tokens, 24 heads on 3 of 96: 70 us,
+// parted 56; 2048 tokens, 32 heads on 4 of 128: 227, 187).
+int key_parts(const gbssim_attention &d)
+{
+    const AttnShape s = shape_of(d);
+    if (s.group == 1 || d.q_tokens == 0 || d.k_tokens == 0) return 1;
+    const long long n = s.packed ? std::max(1, d.sequences) : 1;  // lengths are not known here
+    const auto tiles = [&](int tokens) { return (tokens / n + kAttnTile - 1) / kAttnTile; };
+    const long long q = tiles(d.q_tokens), k = tiles(d.k_tokens);
+    const long long work = std::max(1, d.sequences) * q * k * (d.kv_heads * s.group + d.heads) / kAttnBlocks;
+    const long long longest = q * s.group, most = std::max<long long>(work, 1);
+    const int parts = int(std::min<long long>(s.group, (longest + most - 1) / most));
+    return parts > 1 && longest - longest / parts >= 6 ? parts : 1;
+}
+
 // The backward's row sums, in tiles of 128 queries, and the largest |g| and |v| of each
-// key head.
+// key head; then the parts of dv and dk.
+size_t sums_bytes(const gbssim_attention &d)
+{
+    const size_t n = size_t(d.heads) * most_tiles(shape_of(d), d.q_tokens, kAttnTile) * 2 * kAttnTile * sizeof(float) +
+                     size_t(2) * d.kv_heads * sizeof(unsigned);
+    return (n + 15) / 16 * 16;
+}
+
 size_t bwd_bytes(const gbssim_attention &d)
 {
-    return size_t(d.heads) * most_tiles(shape_of(d), d.q_tokens, kAttnTile) * 2 * kAttnTile * sizeof(float) +
-           size_t(2) * d.kv_heads * sizeof(unsigned);
+    const int parts = key_parts(d);
+    return sums_bytes(d) + (parts > 1 ? size_t(2) * parts * k_rows(d) * d.kv_heads * d.dim * sizeof(float) : 0);
 }
 
 unsigned g_extra = 0;  // test hook, see gbssim_tune_attention
@@ -263,7 +289,7 @@ extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_head
     const AttnShape s = shape_of(*d);
     const long long q_tiles = queries ? most_tiles(s, d->q_tokens, kAttnTile) : 0;
     const long long k_tiles = keys ? most_tiles(s, d->k_tokens, kAttnTile) : 0;
-    if (q_tiles * d->heads + k_tiles * d->kv_heads > INT_MAX || q_tiles + k_tiles > INT_MAX) return GBSSIM_ESHAPE;
+    if (q_tiles * d->heads + k_tiles * d->heads > INT_MAX || k_rows(*d) * d->kv_heads > INT_MAX || q_tiles + k_tiles > INT_MAX) return GBSSIM_ESHAPE;
     AttnBwdArgs a{};
     if (!encode(a.q, *d, d->q, d->q_tokens, d->heads, 1, kAttnTile) ||
         !encode(a.k, *d, d->k, d->k_tokens, d->kv_heads, 1, kAttnTile) ||
@@ -293,7 +319,10 @@ extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_head
     a.dq = queries ? grad_q_or_null : nullptr;
     a.dk = keys ? grad_k_or_null : nullptr;
     a.dv = keys ? grad_v_or_null : nullptr;
-    a.key_items = a.dk || a.dv ? unsigned(k_tiles * d->kv_heads) : 0;
+    a.key_parts = queries ? key_parts(*d) : 1;
+    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + (queries ? sums_bytes(*d) : 0));
+    a.key_items = a.dk || a.dv ? unsigned(k_tiles * d->kv_heads * a.key_parts) : 0;
+    if (!a.key_items) a.key_parts = 1;
     a.queries_wanted = a.dq != nullptr;
     a.items = a.key_items + (a.dq ? unsigned(q_tiles * d->heads) : 0);
     a.stats = static_cast<float *>(workspace);

@@ -196,7 +196,7 @@ struct BwdShared {
 struct BwdItem {
     AttnPlace pl;
     bool there;
-    int head;
+    int head, part;  // part of the query heads that share a key head
 };
 
 // The n-th item of this block; to and fro, so that falling work evens out.  Those of
@@ -214,6 +214,8 @@ __device__ __forceinline__ void find_item(const AttnBwdArgs &a, unsigned u, BwdI
 {
     const AttnShape &s = a.s;
     if (!KEYS) u -= a.key_items;
+    w.part = KEYS ? u % a.key_parts : 0;
+    if (KEYS) u /= a.key_parts;
     const int all = KEYS ? a.k_tiles : a.q_tiles;
     int index;
     if (s.causal) {
@@ -325,6 +327,28 @@ __device__ __forceinline__ void store_row(unsigned at, int from, int to, float s
     }
 }
 
+// Adds up the parts of dv and dk, eight columns a thread.
+constexpr int kJoinThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) attention_join_keys_kernel(const AttnBwdArgs a)
+{
+    const AttnShape &s = a.s;
+    const long long all = (long long)(s.packed ? 1 : s.sequences) * s.k_tokens * s.kv_heads * s.dim;
+    const long long i = ((long long)blockIdx.x * kJoinThreads + threadIdx.x) * 8;
+    T *const out = static_cast<T *>(blockIdx.y ? a.dk : a.dv);
+    pdl_wait();
+    if (i >= all || !out) return;
+    float v[8] = {};
+    for (int p = 0; p < a.key_parts; ++p) {
+        const float4 *const x = reinterpret_cast<const float4 *>(a.parts + (2LL * p + blockIdx.y) * all + i);
+        const float4 lo = x[0], hi = x[1];
+        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+    }
+    st8<T>(out + i, pack8<T>(v));
+}
+
 // 128 keys of a key head against all queries that see them.  Lanes are keys, columns
 // queries.  Tensor memory: scores, then p in their place; dp; dv; dk.  Heads of more than
 // 64 columns: ds in dp's place; while the warps form p of a tile, the products of ds of
@@ -335,16 +359,20 @@ __device__ __forceinline__ void store_row(unsigned at, int from, int to, float s
 struct KeySpan {
     int first;        // key
     int from, all;    // tiles of queries: from the first that sees the first key
-    int total;        // of all heads of the group
+    int head;         // first query head
+    int total;        // tiles of all its query heads
 };
 
-__device__ __forceinline__ KeySpan key_span(const AttnShape &s, const BwdItem &w)
+__device__ __forceinline__ KeySpan key_span(const AttnBwdArgs &a, const BwdItem &w)
 {
+    const AttnShape &s = a.s;
+    const int per = (s.group + a.key_parts - 1) / a.key_parts;
     KeySpan k;
+    k.head = w.head * s.group + w.part * per;
     k.first = w.pl.tile * kAttnTile;
     k.all = (w.pl.queries + kAttnTile - 1) / kAttnTile;
     k.from = s.causal ? min(max(k.first - w.pl.shift, 0) / kAttnTile, k.all) : 0;
-    k.total = w.there && k.first < w.pl.keys ? (k.all - k.from) * s.group : 0;
+    k.total = w.there && k.first < w.pl.keys ? (k.all - k.from) * max(0, min(per, s.group - w.part * per)) : 0;
     return k;
 }
 
@@ -369,7 +397,7 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
         for (unsigned u; ok && (u = item_of(n)) < a.key_items; ++n) {
             BwdItem w;
             find_item<true>(a, u, w);
-            const KeySpan k = key_span(s, w);
+            const KeySpan k = key_span(a, w);
             const AttnPlace &pl = w.pl;
             for (int i = 0, g = 0, t = k.from; ok && i < k.total; ++i, ++it) {
                 // the ring runs on while the last item's keys are still in use; they are
@@ -384,7 +412,7 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                     }
                     ++uses;
                 }
-                const int stage = it % kStages, head = w.head * s.group + g;
+                const int stage = it % kStages, head = k.head + g;
                 if (it >= kStages) ok = attn_wait_warp(&bar.empty[stage], (it / kStages - 1) & 1, failed);
                 if (!ok) break;
                 // rows behind the sequence's are another's: zeros in their place
@@ -450,7 +478,7 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
         for (unsigned u; ok && (u = item_of(n)) < a.key_items; ++n) {
             BwdItem w;
             find_item<true>(a, u, w);
-            const int total = key_span(s, w).total;
+            const int total = key_span(a, w).total;
             if (total == 0) continue;
             ok = attn_wait_warp(&bar.own_full, uses++ & 1, failed);
             if (!ok) break;
@@ -489,7 +517,7 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
         for (unsigned u; (u = item_of(n)) < a.key_items; ++n) {
             BwdItem w;
             find_item<true>(a, u, w);
-            const KeySpan k = key_span(s, w);
+            const KeySpan k = key_span(a, w);
             const AttnPlace &pl = w.pl;
             const int key = k.first + row;
             const Scales sc = scales_of<T>(a, w.head);
@@ -570,9 +598,17 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
             // two parts store dv, two dk, half of the columns each
             const bool is_dk = part >= 2;
             const int cut = min(s.dim, (s.dim / 2 + 15) / 16 * 16);
-            T *const out = static_cast<T *>(is_dk ? a.dk : a.dv);
-            store_row<T>((is_dk ? dk_at : dv_at) + lanes, part & 1 ? cut : 0, part & 1 ? s.dim : cut,
-                         is_dk ? a.scale * sc.inv_ds : sc.inv_p, none, ok, mine && out, out + out_at * s.dim);
+            const unsigned at_sum = (is_dk ? dk_at : dv_at) + lanes;
+            const int c0 = part & 1 ? cut : 0, c1 = part & 1 ? s.dim : cut;
+            const float scale = is_dk ? a.scale * sc.inv_ds : sc.inv_p;
+            if (a.key_parts == 1) {
+                T *const out = static_cast<T *>(is_dk ? a.dk : a.dv);
+                store_row<T>(at_sum, c0, c1, scale, none, ok, mine && out, out + out_at * s.dim);
+            } else {
+                const long long all = (long long)(s.packed ? 1 : s.sequences) * s.k_tokens * s.kv_heads;
+                float *const out = a.parts + ((2LL * w.part + is_dk) * all + out_at) * s.dim;
+                store_row<float>(at_sum, c0, c1, scale, none, ok, mine, out);
+            }
         }
         // the sums are read: tensor memory is the other kind's
         fence_before();
@@ -814,6 +850,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
     fence_after();
     const unsigned tmem = uniform(sh.tmem);
     pdl_wait();  // the row sums
+    pdl_trigger();  // what adds up the parts waits for the end of this kernel
     unsigned n = 0;
     bool ok = true;
     by_keys<T, DP>(a, base, sh, warp, tmem, n, ok);
@@ -860,8 +897,12 @@ cudaError_t launch(const AttnBwdArgs &a, cudaStream_t stream)
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (a.items == 0) return cudaSuccess;
-    return launch_after(attention_bwd_kernel<T, DP>, std::min(a.items, unsigned(kAttnBlocks)), kBwdThreads, smem,
-                        stream, a);
+    e = launch_after(attention_bwd_kernel<T, DP>, dim3(std::min(a.items, unsigned(kAttnBlocks))), kBwdThreads, smem,
+                     stream, a);
+    if (e != cudaSuccess || a.key_parts == 1) return e;
+    const long long n = (long long)(a.s.packed ? 1 : a.s.sequences) * a.s.k_tokens * a.s.kv_heads * a.s.dim / 8;
+    return launch_after(attention_join_keys_kernel<T>, dim3(unsigned((n + kJoinThreads - 1) / kJoinThreads), 2),
+                        kJoinThreads, 0, stream, a);
 }
 
 }  // namespace

@@ -92,6 +92,8 @@ BATCHES = [
     (2, 1500, 1500, 32, 8, 128, BF, True),
     (1, 5, 0, 2, 1, 64, BF, False),
     (1, 255, 3, 2, 2, 56, HF, False),
+    (1, 1500, 300, 16, 1, 64, BF, False),   # query heads of a key head in parts
+    (2, 700, 260, 21, 3, 96, HF, True),
 ]
 
 
@@ -113,6 +115,7 @@ PACKS = [
     ([0, 0, 17, 256, 0], 3, 3, 72, HF, True),
     ([1] * 70 + [513], 2, 1, 40, BF, True),
     ([1000, 3, 900, 128, 256, 511], 8, 8, 64, HF, False),
+    ([600, 75, 0, 333, 140], 24, 3, 96, HF, True),  # query heads of a key head in parts
 ]
 
 
@@ -315,9 +318,10 @@ def test_small_float16_gradients(pkg):
                     visible(T, T, False, T))
 
 
+@pytest.mark.parametrize("shape", [(2, 140, 260, 4, 2, 64), (1, 1500, 300, 16, 1, 64)], ids=str)
 @pytest.mark.parametrize("needs", [(True, False, False), (False, True, False), (False, False, True)])
-def test_single_gradients(pkg, needs):
-    q, k, v = inputs(15, 2, 140, 260, 4, 2, 64, BF)
+def test_single_gradients(pkg, needs, shape):
+    q, k, v = inputs(15, *shape, BF)
     g = normal(torch.Generator(device="cuda").manual_seed(16), *q.shape)
     out, lse = pkg.attention_fwd(q, k, v, want_stats=True)
     every = pkg.attention_bwd(g, q, k, v, out, lse)
