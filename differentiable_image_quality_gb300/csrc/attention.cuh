@@ -162,14 +162,22 @@ __device__ __forceinline__ bool attn_wait_warp(uint64_t *bar, unsigned parity, v
 __device__ __forceinline__ unsigned uniform(unsigned v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // A kernel's shared memory, asked for once on each device (1.5 us a call otherwise).
+// `registers`: what its warpgroups' threads have after they have shared them out anew, one
+// of each of `groups`; more than the kernel is launched with would be waited for without
+// end, so such a build is refused.
 template <typename Kernel>
-inline cudaError_t allow_smem(Kernel kernel, std::atomic<unsigned long long> &done, size_t bytes)
+inline cudaError_t allow_smem(Kernel kernel, std::atomic<unsigned long long> &done, size_t bytes, int registers = 0,
+                              int groups = 1)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
     if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kernel);
+    if (e == cudaSuccess && (attr.numRegs + 7) / 8 * 8 * groups < registers) e = cudaErrorLaunchOutOfResources;
+    if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
@@ -237,6 +245,7 @@ struct AttnBwdArgs {
     void *dq, *dk, *dv;      // each may be null
     float *stats;            // [heads][q_tiles][2][128]
     unsigned *largest;       // [2][kv_heads]: |g|, |v|, as bits (float16)
+    unsigned *counter;       // of items taken
 };
 
 cudaError_t attention_bwd_launch(const AttnBwdArgs &a, int dtype, cudaStream_t stream);

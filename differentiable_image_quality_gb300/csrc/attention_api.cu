@@ -172,11 +172,12 @@ int key_parts(const gbssim_attention &d)
 }
 
 // The backward's row sums, in tiles of 128 queries, and the largest |g| and |v| of each
-// key head; then the parts of dv and dk.
+// key head, the counter of items; then the parts of dv and dk.
 size_t sums_bytes(const gbssim_attention &d)
 {
-    const size_t n = size_t(d.heads) * most_tiles(shape_of(d), d.q_tokens, kAttnTile) * 2 * kAttnTile * sizeof(float) +
-                     size_t(2) * d.kv_heads * sizeof(unsigned);
+    const long long tiles = d.q_tokens ? most_tiles(shape_of(d), d.q_tokens, kAttnTile) : 0;
+    const size_t n = size_t(d.heads) * tiles * 2 * kAttnTile * sizeof(float) +
+                     size_t(2 * d.kv_heads + 1) * sizeof(unsigned);
     return (n + 15) / 16 * 16;
 }
 
@@ -192,8 +193,9 @@ unsigned g_extra = 0;  // test hook, see gbssim_tune_attention
 
 extern "C" size_t gbssim_attention_workspace_bytes(const gbssim_attention *d, int backward)
 {
-    if (check_desc(d) != GBSSIM_OK || q_rows(*d) == 0) return 0;
-    if (backward) return bwd_bytes(*d);
+    if (check_desc(d) != GBSSIM_OK) return 0;
+    if (backward) return q_rows(*d) || k_rows(*d) ? bwd_bytes(*d) : 0;
+    if (q_rows(*d) == 0) return 0;
     return part_floats(*d, plan_fwd(*d)) * sizeof(float);
 }
 
@@ -266,7 +268,7 @@ extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_head
     for (const void *p : {grad_q_or_null, grad_k_or_null, grad_v_or_null})
         if (!multiple16(p)) return GBSSIM_EALIGN;
     if (reinterpret_cast<uintptr_t>(lse) % 4) return GBSSIM_EALIGN;
-    const size_t need = queries ? bwd_bytes(*d) : 0;
+    const size_t need = bwd_bytes(*d);
     if (need && (!workspace || !multiple16(workspace) || workspace_bytes < need)) return GBSSIM_EWORKSPACE;
     const Extent in[9] = {heads_extent(*d, d->q, d->q_tokens, d->heads),
                           heads_extent(*d, d->k, d->k_tokens, d->kv_heads),
@@ -320,13 +322,15 @@ extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_head
     a.dk = keys ? grad_k_or_null : nullptr;
     a.dv = keys ? grad_v_or_null : nullptr;
     a.key_parts = queries ? key_parts(*d) : 1;
-    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + (queries ? sums_bytes(*d) : 0));
+    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + sums_bytes(*d));
     a.key_items = a.dk || a.dv ? unsigned(k_tiles * d->kv_heads * a.key_parts) : 0;
     if (!a.key_items) a.key_parts = 1;
     a.queries_wanted = a.dq != nullptr;
     a.items = a.key_items + (a.dq ? unsigned(q_tiles * d->heads) : 0);
     a.stats = static_cast<float *>(workspace);
-    a.largest = queries ? reinterpret_cast<unsigned *>(a.stats + size_t(d->heads) * q_tiles * 2 * kAttnTile) : nullptr;
+    unsigned *const words = reinterpret_cast<unsigned *>(a.stats + size_t(d->heads) * q_tiles * 2 * kAttnTile);
+    a.largest = queries ? words : nullptr;
+    a.counter = words + 2 * d->kv_heads;
     return cuda_fail(attention_bwd_launch(a, d->dtype, static_cast<cudaStream_t>(stream)));
 }
 

@@ -6,6 +6,8 @@
 // dk and dv, those of 128 queries over the keys and sum dq.  Both form p and ds
 // again, seven products instead of five, and every sum stays in one block: no
 // partial gradients in memory, no atomics, results that repeat bit for bit.
+#include <climits>
+
 #include "attention.cuh"
 
 namespace gbssim {
@@ -84,6 +86,7 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
     const bool values = blockIdx.x >= q_blocks;  // the largest |v| (float16)
     const int from = blockIdx.y * kSumHeads, heads = min(kSumHeads, (values ? s.kv_heads : s.heads) - from);
     pdl_trigger();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.counter = 0;  // of the blocks' items
     if (heads <= 0) return;
     if (threadIdx.x < 32) {
         AttnPlace p;
@@ -186,24 +189,36 @@ struct BwdBarriers {
     uint64_t own_full, own_empty, full[8], empty[8], s_full[2], dp_full, p_full, ds_full, done, patched;
 };
 
-struct BwdShared {
-    BwdBarriers keys, queries;
-    uint64_t keys_stored, drained;
-    unsigned tmem, failed;
-};
+constexpr int kItemSlots = 4;
 
-// An item: a tile of keys of a key head, or of queries of a head.
+// An item: a tile of keys of a key head, or of queries of a head, and what goes over it.
 struct BwdItem {
     AttnPlace pl;
     bool there;
-    int head, part;  // part of the query heads that share a key head
+    int head, part;    // part of the query heads that share a key head
+    int from, all;     // keys: tiles of queries, from the first that sees the first key
+    int q_head;        // keys: the first query head
+    int total;         // tiles that the block goes over
+    unsigned u;        // its number
 };
 
-// The n-th item of this block; to and fro, so that falling work evens out.  Those of
-// keys come first.
-__device__ __forceinline__ unsigned item_of(unsigned n)
+struct BwdShared {
+    BwdBarriers keys, queries;
+    uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+    uint64_t keys_stored, drained;
+    BwdItem item[kItemSlots], none;  // none: after the last
+    unsigned tmem, failed;
+};
+
+// Which item comes next: blocks take them from a counter, the longest first, so that
+// they end together whatever the lengths (dealt out beforehand, 4 x 4096 queries
+// against 2333, 1000, 400 and 1800 keys took 600 us).  The warp that copies asks and
+// tells the others of the block what it is through a ring.  In a
+// block that failed it takes what is left, for the others to write NaN.
+__device__ __forceinline__ bool wait_item(BwdShared &sh, uint64_t *bar, unsigned parity)
 {
-    return n * gridDim.x + (n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    return attn_wait_warp(bar, parity, &sh.failed) ||
+           __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kAttnDrainCycles));
 }
 
 // By a whole warp.  Causal: falling work, that of the first keys and of the last queries
@@ -235,7 +250,55 @@ __device__ __forceinline__ void find_item(const AttnBwdArgs &a, unsigned u, BwdI
     }
     w.there = find_place<KEYS>(s, index, kAttnTile, w.pl);
     if (!w.there) w.pl = {};  // packed: fewer tiles than there could be
+    const AttnPlace &pl = w.pl;
+    if (KEYS) {
+        const int per = (s.group + a.key_parts - 1) / a.key_parts, first = pl.tile * kAttnTile;
+        w.q_head = w.head * s.group + w.part * per;
+        w.all = (pl.queries + kAttnTile - 1) / kAttnTile;
+        w.from = s.causal ? min(max(first - pl.shift, 0) / kAttnTile, w.all) : 0;
+        w.total = w.there && first < pl.keys ? (w.all - w.from) * max(0, min(per, s.group - w.part * per)) : 0;
+    } else {
+        int seen = pl.keys;
+        if (s.causal) seen = min(seen, min((pl.tile + 1) * kAttnTile, pl.queries) + pl.shift);
+        w.total = !w.there || seen <= 0 ? 0 : (seen + kAttnTile - 1) / kAttnTile;
+    }
 }
+
+// The copying warp's n-th item; one that is as many as there are or more ends the work.  It
+// asks when it has asked for all tiles of the last one, a few before the others have
+// gone over them: an item that waited in a block any longer would keep another block
+// idle at the end (asked for an item ahead, 8192 x 8 heads of 64 took 375 us for 333).
+__device__ __forceinline__ BwdItem publish_item(const AttnBwdArgs &a, BwdShared &sh, unsigned &n)
+{
+    const unsigned slot = n % kItemSlots;
+    BwdItem w{};
+    if (threadIdx.x % 32 == 0) w.u = atomicAdd(a.counter, 1u);
+    w.u = uniform(w.u);
+    if (w.u < a.key_items)
+        find_item<true>(a, w.u, w);
+    else if (w.u < a.items)
+        find_item<false>(a, w.u, w);
+    if (n >= kItemSlots && !wait_item(sh, &sh.item_empty[slot], (n / kItemSlots - 1) & 1)) return sh.none;
+    ++n;
+    if (threadIdx.x % 32 == 0) {
+        sh.item[slot] = w;
+        mbar_arrive(&sh.item_full[slot]);
+    }
+    return w;
+}
+
+// The others' n-th.
+__device__ __forceinline__ BwdItem take_item(BwdShared &sh, unsigned &n)
+{
+    const unsigned slot = n % kItemSlots;
+    if (!wait_item(sh, &sh.item_full[slot], (n / kItemSlots) & 1)) return sh.none;
+    ++n;
+    const BwdItem w = sh.item[slot];
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(&sh.item_empty[slot]);
+    return w;
+}
+
 
 template <int DP>
 constexpr int key_stages()  // pairs of a query tile and its gradient
@@ -356,29 +419,9 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_keys_kernel(const
 // heads leave room for two tiles of scores, and beside p for ds: the next scores are
 // there when they are wanted, and the next dp waits for nothing but that the last one
 // has been read (8 x 8192 x 64: see below).
-struct KeySpan {
-    int first;        // key
-    int from, all;    // tiles of queries: from the first that sees the first key
-    int head;         // first query head
-    int total;        // tiles of all its query heads
-};
-
-__device__ __forceinline__ KeySpan key_span(const AttnBwdArgs &a, const BwdItem &w)
-{
-    const AttnShape &s = a.s;
-    const int per = (s.group + a.key_parts - 1) / a.key_parts;
-    KeySpan k;
-    k.head = w.head * s.group + w.part * per;
-    k.first = w.pl.tile * kAttnTile;
-    k.all = (w.pl.queries + kAttnTile - 1) / kAttnTile;
-    k.from = s.causal ? min(max(k.first - w.pl.shift, 0) / kAttnTile, k.all) : 0;
-    k.total = w.there && k.first < w.pl.keys ? (k.all - k.from) * max(0, min(per, s.group - w.part * per)) : 0;
-    return k;
-}
-
 template <typename T, int DP>
 __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdShared &sh, int warp, unsigned tmem,
-                                        unsigned &n, bool &ok)
+                                        unsigned &n, BwdItem &w, bool &ok)
 {
     constexpr int kTile = tile_bytes<DP>();
     constexpr int kStages = key_stages<DP>();
@@ -394,25 +437,25 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
     if (warp == kWarps) {
         int it = 0;
         unsigned uses = 0, patches = 0;
-        for (unsigned u; ok && (u = item_of(n)) < a.key_items; ++n) {
-            BwdItem w;
-            find_item<true>(a, u, w);
-            const KeySpan k = key_span(a, w);
-            const AttnPlace &pl = w.pl;
-            for (int i = 0, g = 0, t = k.from; ok && i < k.total; ++i, ++it) {
+        for (; w.u < a.key_items; w = publish_item(a, sh, n)) {
+            if (!ok) continue;
+            const AttnPlace pl = w.pl;
+            const int kv_head = w.head, q_head = w.q_head, from = w.from, all = w.all, total = w.total;
+            const int first = pl.tile * kAttnTile;
+            for (int i = 0, g = 0, t = from; ok && i < total; ++i, ++it) {
                 // the ring runs on while the last item's keys are still in use; they are
                 // asked for before the ring would wait for their products
-                if (i == min(kStages - 1, k.total - 1)) {
+                if (i == min(kStages - 1, total - 1)) {
                     if (uses > 0) ok = attn_wait_warp(&bar.own_empty, (uses - 1) & 1, failed);
                     if (!ok) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&bar.own_full, 2 * kTile + a.extra);
-                        load_tile<DP>(base, &a.k, w.head, pl.k_row + k.first, pl.batch, &bar.own_full);
-                        load_tile<DP>(base + kTile, &a.v, w.head, pl.k_row + k.first, pl.batch, &bar.own_full);
+                        load_tile<DP>(base, &a.k, kv_head, pl.k_row + first, pl.batch, &bar.own_full);
+                        load_tile<DP>(base + kTile, &a.v, kv_head, pl.k_row + first, pl.batch, &bar.own_full);
                     }
                     ++uses;
                 }
-                const int stage = it % kStages, head = k.head + g;
+                const int stage = it % kStages, head = q_head + g;
                 if (it >= kStages) ok = attn_wait_warp(&bar.empty[stage], (it / kStages - 1) & 1, failed);
                 if (!ok) break;
                 // rows behind the sequence's are another's: zeros in their place
@@ -436,8 +479,8 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.full[stage]);
                 }
-                if (++t == k.all) {
-                    t = k.from;
+                if (++t == all) {
+                    t = from;
                     ++g;
                 }
             }
@@ -475,17 +518,15 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
             commit(dp_full, leader);
             dp_of.next();
         };
-        for (unsigned u; ok && (u = item_of(n)) < a.key_items; ++n) {
-            BwdItem w;
-            find_item<true>(a, u, w);
-            const int total = key_span(a, w).total;
-            if (total == 0) continue;
+        for (; uniform(w.u) < a.key_items; w = take_item(sh, n)) {
+            const int total = uniform(w.total);
+            if (!ok || total == 0) continue;
             ok = attn_wait_warp(&bar.own_full, uses++ & 1, failed);
-            if (!ok) break;
+            if (!ok) continue;
             fence_after();
-            if (!(ok = scores())) break;
+            if (!(ok = scores())) continue;
             products();
-            if (kTwo && total > 1 && !(ok = scores())) break;
+            if (kTwo && total > 1 && !(ok = scores())) continue;
             for (int it = 0; it < total; ++it, phase ^= 1) {
                 const Desc tile = advance(ring_mn, 2 * sum_of.slot * kTile);
                 const unsigned p_at = s_at + (kTwo ? phase * 128 : 0), ds_at = kTwo ? p_at + 16 : dp_at;
@@ -503,7 +544,7 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                 if (!kTwo && more) products();
                 if (kTwo && it + 2 < total && !(ok = scores())) break;
             }
-            if (!ok) break;
+            if (!ok) continue;
             commit(smem_u32(&bar.done), leader);
             commit(smem_u32(&bar.own_empty), leader);
         }
@@ -514,20 +555,18 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
         const f32x2 c2 = both(a.scale_log2);
         RingAt<kStages> at;
         unsigned uses = 0, phase = 0, tiles = 0;
-        for (unsigned u; (u = item_of(n)) < a.key_items; ++n) {
-            BwdItem w;
-            find_item<true>(a, u, w);
-            const KeySpan k = key_span(a, w);
-            const AttnPlace &pl = w.pl;
-            const int key = k.first + row;
+        for (; w.u < a.key_items; w = take_item(sh, n)) {
+            const int total = w.total;
             const Scales sc = scales_of<T>(a, w.head);
-            for (int it = 0, t = k.from; ok && it < k.total; ++it, phase ^= 1) {
+            // columns before hidden0 - 128 t are queries of tile t that do not see this key
+            const int key0 = w.pl.tile * kAttnTile + row;
+            const int hidden0 = key0 >= w.pl.keys ? INT_MAX
+                                : s.causal         ? max(key0 - w.pl.shift - part * kColumns, 0)
+                                                   : 0;
+            for (int it = 0, t = w.from; ok && it < total; ++it, phase ^= 1) {
                 const float *const stats =
                     reinterpret_cast<const float *>(ring_stats + at.slot * kStatsBytes) + part * kColumns;
-                // columns before `hidden` are queries that do not see this key
-                const int hidden = key >= pl.keys ? kColumns
-                                   : s.causal     ? key - pl.shift - t * kAttnTile - part * kColumns
-                                                  : 0;
+                const int hidden = hidden0 == INT_MAX ? kColumns : hidden0 - t * kAttnTile;
                 const bool masked = __any_sync(0xffffffffu, hidden > 0);
                 const unsigned my_s = s_at + lanes + (kTwo ? phase * 128 : 0) + part * kColumns;
                 ok = attn_wait_warp(&bar.full[at.slot], at.parity, failed) &&
@@ -587,13 +626,14 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                 wait_st();
                 fence_before();
                 mbar_arrive(&bar.ds_full);
-                if (++t == k.all) t = k.from;
+                if (++t == w.all) t = w.from;
             }
-            if (k.total > 0 && ok) ok = attn_wait_warp(&bar.done, uses & 1, failed);
-            uses += k.total > 0;
+            if (total > 0 && ok) ok = attn_wait_warp(&bar.done, uses & 1, failed);
+            uses += total > 0;
             fence_after();
-            const int count = !w.there ? 0 : s.packed ? pl.keys : s.k_tokens;
-            const bool mine = w.there && key < count, none = k.total == 0 || key >= pl.keys;
+            const AttnPlace pl = w.pl;
+            const int key = pl.tile * kAttnTile + row, count = s.packed ? pl.keys : s.k_tokens;
+            const bool mine = w.there && key < count, none = total == 0 || key >= pl.keys;
             const long long out_at = ((long long)pl.batch * s.k_tokens + pl.k_row + key) * s.kv_heads + w.head;
             // two parts store dv, two dk, half of the columns each
             const bool is_dk = part >= 2;
@@ -620,16 +660,9 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
 // keys.  Tensor memory: two tiles of scores, so that the next one's are there when
 // they are wanted, then ds in their place, so that the next dp waits for nothing but
 // that the last one has been read; dp; dq.
-__device__ __forceinline__ int query_tiles(const AttnShape &s, const BwdItem &w)
-{
-    int seen = w.pl.keys;
-    if (s.causal) seen = min(seen, min((w.pl.tile + 1) * kAttnTile, w.pl.queries) + w.pl.shift);
-    return !w.there || seen <= 0 ? 0 : (seen + kAttnTile - 1) / kAttnTile;
-}
-
 template <typename T, int DP>
 __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, BwdShared &sh, int warp, unsigned tmem,
-                                           unsigned &n, bool &ok)
+                                           unsigned &n, BwdItem &w, bool &ok)
 {
     constexpr int kTile = tile_bytes<DP>();
     constexpr int kKeys = key_slots<DP>(), kValues = value_slots<DP>();
@@ -647,11 +680,10 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
         RingAt<kValues> v_at;
         int issued = 0;  // pairs
         unsigned uses = 0, patches = 0;
-        for (unsigned u; ok && (u = item_of(n)) < a.items; ++n) {
-            BwdItem w;
-            find_item<false>(a, u, w);
-            const int total = query_tiles(s, w), kv_head = w.head / s.group;
-            const AttnPlace &pl = w.pl;
+        for (; w.u < a.items; w = publish_item(a, sh, n)) {
+            if (!ok) continue;
+            const AttnPlace pl = w.pl;
+            const int total = w.total, head = w.head, kv_head = head / s.group;
             for (int j = 0; ok && j < total; ++j) {
                 if (j == min(1, total - 1)) {  // as above
                     if (uses > 0) ok = attn_wait_warp(&bar.own_empty, (uses - 1) & 1, failed);
@@ -659,8 +691,8 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
                     if (lane == 0) {
                         const int row = pl.q_row + pl.tile * kAttnTile;
                         mbar_arrive_expect_tx(&bar.own_full, 2 * kTile + a.extra);
-                        load_tile<DP>(base, &a.q, w.head, row, pl.batch, &bar.own_full);
-                        load_tile<DP>(base + kTile, &a.g, w.head, row, pl.batch, &bar.own_full);
+                        load_tile<DP>(base, &a.q, head, row, pl.batch, &bar.own_full);
+                        load_tile<DP>(base + kTile, &a.g, head, row, pl.batch, &bar.own_full);
                     }
                     ++uses;
                 }
@@ -728,14 +760,12 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
             v_at.next();
             return true;
         };
-        ok = attn_wait_warp(&sh.keys_stored, 0, failed);
-        for (unsigned u; ok && (u = item_of(n)) < a.items; ++n) {
-            BwdItem w;
-            find_item<false>(a, u, w);
-            const int total = query_tiles(s, w);
-            if (total == 0) continue;
+        ok = ok && attn_wait_warp(&sh.keys_stored, 0, failed);
+        for (; uniform(w.u) < a.items; w = take_item(sh, n)) {
+            const int total = uniform(w.total);
+            if (!ok || total == 0) continue;
             ok = attn_wait_warp(&bar.own_full, uses++ & 1, failed);
-            if (!ok) break;
+            if (!ok) continue;
             fence_after();
             ok = scores() && products();
             if (ok && total > 1) ok = scores();
@@ -749,7 +779,7 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
                 sum_of.next();
                 if (j + 2 < total) ok = scores();
             }
-            if (!ok) break;
+            if (!ok) continue;
             commit(smem_u32(&bar.done), leader);
             commit(smem_u32(&bar.own_empty), leader);
         }
@@ -758,18 +788,15 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
         const unsigned lanes = unsigned(warp % 4) << 21;
         const f32x2 c2 = both(a.scale_log2);
         unsigned uses = 0, tiles = 0;
-        for (unsigned u; (u = item_of(n)) < a.items; ++n) {
-            BwdItem w;
-            find_item<false>(a, u, w);
+        for (; w.u < a.items; w = take_item(sh, n)) {
             if (!w.there) continue;
-            const AttnPlace &pl = w.pl;
-            const int total = query_tiles(s, w), query = pl.tile * kAttnTile + row;
+            const int total = w.total;
             const float *const stats =
-                a.stats + ((long long)w.head * a.q_tiles + pl.q_tiles_before + pl.tile) * 2 * kAttnTile;
+                a.stats + ((long long)w.head * a.q_tiles + w.pl.q_tiles_before + w.pl.tile) * 2 * kAttnTile;
             const f32x2 l2 = both(stats[row]);
             const Scales sc = scales_of<T>(a, w.head / s.group);
             const f32x2 n2 = both(stats[kAttnTile + row] * sc.ds);
-            const int end = s.causal ? min(pl.keys, query + 1 + pl.shift) : pl.keys;
+            const int end = s.causal ? min(w.pl.keys, w.pl.tile * kAttnTile + row + 1 + w.pl.shift) : w.pl.keys;
             for (int j = 0; ok && j < total; ++j, ++tiles) {
                 const unsigned my_s = s_at + lanes + (tiles & 1) * 128 + part * kColumns;
                 const unsigned my_dp = dp_at + lanes + part * kColumns;
@@ -812,6 +839,8 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
             if (ok && total > 0) ok = attn_wait_warp(&bar.done, uses & 1, failed);
             uses += total > 0;
             fence_after();
+            const AttnPlace pl = w.pl;
+            const int query = pl.tile * kAttnTile + row;
             const long long out_at = ((long long)pl.batch * s.q_tokens + pl.q_row + query) * s.heads + w.head;
             store_row<T>(dq_at + lanes, min(s.dim, part * 32), min(s.dim, part * 32 + 32), a.scale * sc.inv_ds,
                          total == 0, ok, query < pl.queries, static_cast<T *>(a.dq) + out_at * s.dim);
@@ -829,6 +858,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
     if (warp == kWarps && lane == 0) {
         for (const CUtensorMap *m : {&a.q, &a.k, &a.v, &a.g}) prefetch_map(m);
         sh.failed = 0;
+        sh.none = {};
+        sh.none.u = UINT_MAX;
         for (BwdBarriers *b : {&sh.keys, &sh.queries}) {
             for (uint64_t *x : {&b->own_full, &b->own_empty, &b->s_full[0], &b->s_full[1], &b->dp_full, &b->done,
                                 &b->patched})
@@ -839,6 +870,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
             }
             mbar_init(&b->p_full, kWarps * 32);
             mbar_init(&b->ds_full, kWarps * 32);
+        }
+        for (int i = 0; i < kItemSlots; ++i) {
+            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_empty[i], kWarps + 1);
         }
         mbar_init(&sh.keys_stored, kWarps * 32);
         mbar_init(&sh.drained, 1);
@@ -851,12 +886,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
     const unsigned tmem = uniform(sh.tmem);
     pdl_wait();  // the row sums
     pdl_trigger();  // what adds up the parts waits for the end of this kernel
-    unsigned n = 0;
     bool ok = true;
-    by_keys<T, DP>(a, base, sh, warp, tmem, n, ok);
-    // a block that failed has every role leave; those on the tiles still write their
-    // NaN
-    if (ok || warp < kWarps) by_queries<T, DP>(a, base, sh, warp, tmem, n, ok);
+    unsigned n = 0;
+    BwdItem w = warp == kWarps ? publish_item(a, sh, n) : take_item(sh, n);
+    by_keys<T, DP>(a, base, sh, warp, tmem, n, w, ok);
+    by_queries<T, DP>(a, base, sh, warp, tmem, n, w, ok);
     if (!ok && warp == kWarps + 1) {
         commit(smem_u32(&sh.drained), elect_leader());
         mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
@@ -893,6 +927,9 @@ cudaError_t launch(const AttnBwdArgs &a, cudaStream_t stream)
             attention_sums_kernel<T, 8><<<grid, kSumThreads, 0, stream>>>(a, q_blocks);
         else
             attention_sums_kernel<T, 16><<<grid, kSumThreads, 0, stream>>>(a, q_blocks);
+    } else {
+        e = cudaMemsetAsync(a.counter, 0, sizeof(unsigned), stream);
+        if (e != cudaSuccess) return e;
     }
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

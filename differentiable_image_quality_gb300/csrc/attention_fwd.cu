@@ -490,7 +490,8 @@ cudaError_t launch(const AttnFwdArgs &a, cudaStream_t stream)
     constexpr size_t smem = fwd_smem<DP, QT>();
     static_assert(smem <= 232448, "a block's shared memory");
     static std::atomic<unsigned long long> done{0};
-    const cudaError_t e = allow_smem(attention_fwd_kernel<T, DP, QT>, done, smem);
+    const cudaError_t e = allow_smem(attention_fwd_kernel<T, DP, QT>, done, smem,
+                                     QT == 2 ? 2 * kTileRegisters + kOtherRegisters : 0, 3);
     if (e != cudaSuccess) return e;
     const unsigned grid = std::min(a.items, unsigned(kAttnBlocks));
     attention_fwd_kernel<T, DP, QT><<<grid, fwd_threads<QT>(), smem, stream>>>(a);

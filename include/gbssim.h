@@ -85,7 +85,8 @@ void gbssim_window(float w[11]);
  *   row (more than 4096 columns) waited about a second for one another's sums;
  *   that call's outputs are not valid.
  *   bit 2 (GBSSIM_DEV_ATTENTION_TIMEOUT): a block of an attention call waited about a
- *   second for a tile or a product; its rows of the outputs are NaN.
+ *   second for a tile or a product; that call's outputs are not valid, rows that it had
+ *   not written yet are NaN.
  * Synchronises the device: a diagnostic, not part of the hot path.  Returns
  * GBSSIM_OK, GBSSIM_EINVAL (null flags_out) or GBSSIM_ECUDA. */
 #define GBSSIM_DEV_STAGING_TIMEOUT 1u

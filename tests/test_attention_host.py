@@ -133,8 +133,9 @@ def test_no_rows_is_no_work(lib):
     assert fwd(lib, desc(q_tokens=0, q=Heads())) == 0
     assert fwd(lib, desc(sequences=0, q=Heads(), k=Heads(), v=Heads())) == 0
     assert bwd(lib, desc(sequences=0)) == 0
+    assert lib.gbssim_attention_workspace_bytes(ctypes.byref(desc(q_tokens=0)), 0) == 0
     for backward in (0, 1):
-        assert lib.gbssim_attention_workspace_bytes(ctypes.byref(desc(q_tokens=0)), backward) == 0
+        assert lib.gbssim_attention_workspace_bytes(ctypes.byref(desc(sequences=0)), backward) == 0
 
 
 def test_python_refuses_cpu_tensors():
