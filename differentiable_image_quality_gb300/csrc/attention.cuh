@@ -213,6 +213,7 @@ struct AttnFwdArgs {
     int splits;       // parts of the keys
     int tiles;        // of q_tokens (batch form), or the most there can be (packed)
     unsigned items;   // of all blocks
+    unsigned *counter;  // of items taken, or null: dealt out beforehand
     int ragged;       // keys may end before the tensor does
     unsigned extra;   // test hook, see gbssim_tune_attention
     void *out;

@@ -118,13 +118,14 @@ bool encode(CUtensorMap &m, const gbssim_attention &d, const gbssim_heads &t, in
 
 struct FwdPlan {
     int tile_heads, tile_tokens, q_tiles, splits;
-    long long tiles;
+    long long tiles, items;
+    bool counted;  // items are taken from a counter
 };
 
 FwdPlan plan_fwd(const gbssim_attention &d)
 {
     const AttnShape s = shape_of(d);
-    FwdPlan p{1, kAttnTile, 1, 1, 0};
+    FwdPlan p{1, kAttnTile, 1, 1, 0, 0, false};
     // a sample whose queries of all the heads of a group fit one tile reads its keys once
     // for the group
     if (!s.packed && s.group > 1 && (long long)s.q_tokens * s.group <= kAttnTile) {
@@ -143,13 +144,15 @@ FwdPlan plan_fwd(const gbssim_attention &d)
     // the join's 4 us make worth it from eight tiles on.
     if (!s.packed && blocks > 0 && 2 * blocks <= kAttnBlocks && key_tiles >= 8)
         p.splits = int(std::min<long long>(kAttnBlocks / blocks, key_tiles / 2));
+    p.items = blocks * p.splits;
+    p.counted = (s.packed || s.kv_lengths) && p.items > 2 * kAttnBlocks;
     return p;
 }
 
-size_t part_floats(const gbssim_attention &d, const FwdPlan &p)
+size_t fwd_bytes(const gbssim_attention &d, const FwdPlan &p)
 {
-    if (p.splits == 1) return 0;
-    return size_t(p.splits) * q_rows(d) * d.heads * (d.dim + 1);
+    if (p.counted) return 16;
+    return p.splits == 1 ? 0 : size_t(p.splits) * q_rows(d) * d.heads * (d.dim + 1) * sizeof(float);
 }
 
 // An item of keys goes over the queries of all heads that share them: with few key heads
@@ -196,7 +199,7 @@ extern "C" size_t gbssim_attention_workspace_bytes(const gbssim_attention *d, in
     if (check_desc(d) != GBSSIM_OK) return 0;
     if (backward) return q_rows(*d) || k_rows(*d) ? bwd_bytes(*d) : 0;
     if (q_rows(*d) == 0) return 0;
-    return part_floats(*d, plan_fwd(*d)) * sizeof(float);
+    return fwd_bytes(*d, plan_fwd(*d));
 }
 
 extern "C" int gbssim_attention_fwd(const gbssim_attention *d, void *out, float *lse_or_null,
@@ -209,7 +212,7 @@ extern "C" int gbssim_attention_fwd(const gbssim_attention *d, void *out, float 
     if (!out) return GBSSIM_EINVAL;
     if (!multiple16(out) || reinterpret_cast<uintptr_t>(lse_or_null) % 4) return GBSSIM_EALIGN;
     const FwdPlan p = plan_fwd(*d);
-    const size_t need = part_floats(*d, p) * sizeof(float);
+    const size_t need = fwd_bytes(*d, p);
     if (need && (!workspace || !multiple16(workspace) || workspace_bytes < need)) return GBSSIM_EWORKSPACE;
     const Extent in[6] = {heads_extent(*d, d->q, d->q_tokens, d->heads),
                           heads_extent(*d, d->k, d->k_tokens, d->kv_heads),
@@ -226,8 +229,7 @@ extern "C" int gbssim_attention_fwd(const gbssim_attention *d, void *out, float 
             if (meet(outs[i], outs[j])) return GBSSIM_EINVAL;
     }
     const AttnShape s = shape_of(*d);
-    const long long items = p.tiles * samples(*d) * (s.heads / p.tile_heads) * p.splits;
-    if (items > INT_MAX || q_rows(*d) * d->heads * (d->dim / 8) / 128 >= INT_MAX) return GBSSIM_ESHAPE;
+    if (p.items > INT_MAX || q_rows(*d) * d->heads * (d->dim / 8) / 128 >= INT_MAX) return GBSSIM_ESHAPE;
     AttnFwdArgs a{};
     if (!encode(a.q, *d, d->q, d->q_tokens, d->heads, p.tile_heads, p.tile_tokens) ||
         !encode(a.k, *d, d->k, d->k_tokens, d->kv_heads, 1, kAttnTile) ||
@@ -239,14 +241,18 @@ extern "C" int gbssim_attention_fwd(const gbssim_attention *d, void *out, float 
     a.tile_tokens = p.tile_tokens;
     a.splits = p.splits;
     a.tiles = int(p.tiles);
-    a.items = unsigned(items);
+    a.items = unsigned(p.items);
+    a.counter = p.counted ? static_cast<unsigned *>(workspace) : nullptr;
     a.ragged = s.packed || s.kv_lengths;
     a.extra = g_extra;
     a.out = out;
     a.lse = lse_or_null;
     a.part_out = static_cast<float *>(workspace);
     a.part_lse = p.splits > 1 ? a.part_out + size_t(p.splits) * q_rows(*d) * d->heads * d->dim : nullptr;
-    cudaError_t e = attention_fwd_launch(a, d->dtype, p.q_tiles, static_cast<cudaStream_t>(stream));
+    cudaError_t e = cudaSuccess;
+    if (p.counted) e = cudaMemsetAsync(workspace, 0, sizeof(unsigned), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e);
+    e = attention_fwd_launch(a, d->dtype, p.q_tiles, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess && p.splits > 1)
         e = attention_join_launch(a, d->dtype, static_cast<cudaStream_t>(stream));
     return cuda_fail(e);

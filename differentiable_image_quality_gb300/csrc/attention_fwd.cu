@@ -1,5 +1,7 @@
 // Attention forward: s = scale q k^T, p = softmax over the keys that a query sees,
 // o = p v, and each row's log-sum for the backward.
+#include <climits>
+
 #include "attention.cuh"
 
 namespace gbssim {
@@ -21,24 +23,6 @@ constexpr int tile_bytes()
     return DP / tc::kSlabCols * tc::kSlabBytes;
 }
 
-struct FwdShared {
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
-    uint64_t kv_full[8], kv_empty[8], patched, drained;
-    unsigned tmem, failed;
-};
-
-template <int DP, int QT>
-constexpr size_t fwd_smem()
-{
-    return size_t(QT + stages<DP>()) * tile_bytes<DP>() + sizeof(FwdShared) + 1024;
-}
-
-// The rescaling of a row's accumulator is put off until its maximum has grown by
-// this much (of the exponent, base 2): probabilities stay below 2^8, which float32
-// sums and either 16-bit type hold without loss, and after the first tiles hardly
-// any row needs it.
-constexpr float kLateMax = 8.0f;
-
 // One block's share of the work: a tile (or two) of queries of a head, against some of
 // the keys.
 template <int QT>
@@ -47,7 +31,31 @@ struct FwdItem {
     int head, kv_head, split;
     int first;           // query
     int j0, j1[QT], end; // key tiles: from j0, per tile of queries to j1
+    unsigned u;          // its number
 };
+
+constexpr int kItemSlots = 4;
+
+template <int QT>
+struct FwdShared {
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
+    uint64_t kv_full[8], kv_empty[8], patched, drained;
+    uint64_t item_full[kItemSlots], item_empty[kItemSlots];
+    FwdItem<QT> item[kItemSlots], none;  // none: after the last
+    unsigned tmem, failed;
+};
+
+template <int DP, int QT>
+constexpr size_t fwd_smem()
+{
+    return size_t(QT + stages<DP>()) * tile_bytes<DP>() + sizeof(FwdShared<QT>) + 1024;
+}
+
+// The rescaling of a row's accumulator is put off until its maximum has grown by
+// this much (of the exponent, base 2): probabilities stay below 2^8, which float32
+// sums and either 16-bit type hold without loss, and after the first tiles hardly
+// any row needs it.
+constexpr float kLateMax = 8.0f;
 
 // The index-th of the call's, by a whole warp.  Those of one head follow one another,
 // so that its keys stay in L2; causal ones by falling work instead, the longest first.
@@ -102,6 +110,52 @@ __device__ __forceinline__ unsigned item_of(unsigned n)
     return n * gridDim.x + (n & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
+template <int QT>
+__device__ __forceinline__ bool wait_item(FwdShared<QT> &sh, uint64_t *bar, unsigned parity)
+{
+    return attn_wait_warp(bar, parity, &sh.failed) ||
+           __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kAttnDrainCycles));
+}
+
+// The copying warp's n-th item, told to the others of the block through a ring: dealt out
+// beforehand, or where lengths differ taken from a counter, so that the blocks end
+// together (24 sequences of up to 1500 tokens, 16 heads of 64: 115 us dealt out, 96 taken;
+// setting the counter costs 2 us).  One that is as many as there are or more ends the
+// work.  A block that failed takes what is left, for its rows to become NaN.
+template <int QT>
+__device__ __forceinline__ FwdItem<QT> publish_item(const AttnFwdArgs &a, FwdShared<QT> &sh, unsigned &n)
+{
+    const unsigned slot = n % kItemSlots;
+    FwdItem<QT> w{};
+    if (a.counter) {
+        if (threadIdx.x % 32 == 0) w.u = atomicAdd(a.counter, 1u);
+        w.u = uniform(w.u);
+    } else {
+        w.u = item_of(n);
+    }
+    if (w.u < a.items) find_item(a, w.u, w);
+    if (n >= kItemSlots && !wait_item(sh, &sh.item_empty[slot], (n / kItemSlots - 1) & 1)) return sh.none;
+    ++n;
+    if (threadIdx.x % 32 == 0) {
+        sh.item[slot] = w;
+        tc::mbar_arrive(&sh.item_full[slot]);
+    }
+    return w;
+}
+
+// The others' n-th.
+template <int QT>
+__device__ __forceinline__ FwdItem<QT> take_item(FwdShared<QT> &sh, unsigned &n)
+{
+    const unsigned slot = n % kItemSlots;
+    if (!wait_item(sh, &sh.item_full[slot], (n / kItemSlots) & 1)) return sh.none;
+    ++n;
+    const FwdItem<QT> w = sh.item[slot];
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) tc::mbar_arrive(&sh.item_empty[slot]);
+    return w;
+}
+
 // Threads: four warps for each tile of queries, then a warp that copies, one that issues
 // products and, beside two tiles, two that only give their registers up.
 template <int QT>
@@ -124,7 +178,7 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
     extern __shared__ char raw[];
     char *const base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     char *const ring = base + QT * kTile;
-    FwdShared &sh = *reinterpret_cast<FwdShared *>(ring + kStages * kTile);
+    FwdShared<QT> &sh = *reinterpret_cast<FwdShared<QT> *>(ring + kStages * kTile);
 
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const AttnShape &s = a.s;
@@ -143,6 +197,12 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
             mbar_init(&sh.kv_full[i], 1);
             mbar_init(&sh.kv_empty[i], 1);
         }
+        for (int i = 0; i < kItemSlots; ++i) {
+            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_empty[i], QT * 4 + 1);
+        }
+        sh.none = {};
+        sh.none.u = UINT_MAX;
         mbar_init(&sh.patched, 1);
         mbar_init(&sh.drained, 1);
         mbar_init_fence();
@@ -161,9 +221,9 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
         const unsigned box = unsigned(kSlabs * kRowBytes) * a.tile_heads * a.tile_tokens;
         int it = 0, patches = 0, uses[QT] = {};
         bool ok = true;
-        for (unsigned n = 0, u; ok && (u = item_of(n)) < a.items; ++n) {
-            FwdItem<QT> w;
-            find_item(a, u, w);
+        unsigned n = 0;
+        for (FwdItem<QT> w = publish_item(a, sh, n); w.u < a.items; w = publish_item(a, sh, n)) {
+            if (!ok) continue;
 #pragma unroll
             for (int t = 0; t < QT; ++t) {
                 if (!ok || w.j1[t] <= w.j0) continue;
@@ -234,10 +294,14 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
         unsigned uses[QT] = {}, phase[QT] = {};
         bool ok = true;
         const auto keys_here = [&] { return attn_wait_warp(&sh.kv_full[at.slot], at.parity, failed); };
-        for (unsigned n = 0, u; ok && (u = item_of(n)) < a.items; ++n) {
-            FwdItem<QT> w;
-            find_item(a, u, w);
-            if (w.end <= w.j0) continue;
+        unsigned n = 0;
+        for (FwdItem<QT> w = take_item(sh, n); w.u < a.items; w = take_item(sh, n)) {
+            // known to be the same in all lanes
+            w.j0 = uniform(w.j0);
+            w.end = uniform(w.end);
+#pragma unroll
+            for (int t = 0; t < QT; ++t) w.j1[t] = uniform(w.j1[t]);
+            if (!ok || w.end <= w.j0) continue;
             ok = keys_here();
 #pragma unroll
             for (int t = 0; t < QT; ++t) {
@@ -304,9 +368,8 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
         const long long rows = (long long)(s.packed ? 1 : s.sequences) * s.q_tokens * s.heads;
         int tiles = 0, uses = 0;
         bool ok = true;
-        for (unsigned n = 0, u; (u = item_of(n)) < a.items; ++n) {
-            FwdItem<QT> w;
-            find_item(a, u, w);
+        unsigned n = 0;
+        for (FwdItem<QT> w = take_item(sh, n); w.u < a.items; w = take_item(sh, n)) {
             const int token = w.first + t * a.tile_tokens + row / a.tile_heads;
             const int row_head = w.head * a.tile_heads + row % a.tile_heads;
             const bool mine = row < a.tile_tokens * a.tile_heads && token < w.pl.queries;
