@@ -186,7 +186,7 @@ constexpr int kBwdThreads = (kWarps + 2) * 32;
 // Barriers of one of the two kinds of work.  Each goes from item to item with its
 // phases running on.
 struct BwdBarriers {
-    uint64_t own_full, own_empty, full[8], empty[8], s_full[2], dp_full, p_full, ds_full, done, patched;
+    uint64_t own_full, own_empty, full[8], empty[8], s_full[2], p_full[2], dp_full, ds_full, done, patched;
 };
 
 constexpr int kItemSlots = 4;
@@ -418,7 +418,8 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_keys_kernel(const
 // the last one run; while they form ds, those of p and the next scores.  Narrower
 // heads leave room for two tiles of scores, and beside p for ds: the next scores are
 // there when they are wanted, and the next dp waits for nothing but that the last one
-// has been read (8 x 8192 x 64: see below).
+// has been read.  A warp may then be a tile ahead of another with p, so that p has a
+// barrier for each of the two.
 template <typename T, int DP>
 __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdShared &sh, int warp, unsigned tmem,
                                         unsigned &n, BwdItem &w, bool &ok)
@@ -503,7 +504,7 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
         // places in the ring: of the next tile of queries for scores, for dp, and of the one
         // that p and ds are waiting for
         RingAt<kStages> at, dp_of, sum_of;
-        unsigned uses = 0, phase = 0, scored = 0;
+        unsigned uses = 0, phase = 0, scored = 0, tiles = 0;
         const auto scores = [&] {
             if (!attn_wait_warp(&bar.full[at.slot], at.parity, failed)) return false;
             const unsigned buf = kTwo ? scored & 1 : 0;
@@ -531,7 +532,8 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                 const Desc tile = advance(ring_mn, 2 * sum_of.slot * kTile);
                 const unsigned p_at = s_at + (kTwo ? phase * 128 : 0), ds_at = kTwo ? p_at + 16 : dp_at;
                 const bool more = it + 1 < total;
-                if (!(ok = attn_wait_warp(&bar.p_full, phase, failed))) break;
+                if (!(ok = attn_wait_warp(&bar.p_full[kTwo ? phase : 0], kTwo ? tiles >> 1 & 1 : phase, failed))) break;
+                ++tiles;
                 fence_after();
                 product_parts(dv_at, p_at, advance(tile, kTile), id_d, it > 0, leader);
                 if (!kTwo && more && !(ok = scores())) break;
@@ -563,11 +565,16 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
             const int hidden0 = key0 >= w.pl.keys ? INT_MAX
                                 : s.causal         ? max(key0 - w.pl.shift - part * kColumns, 0)
                                                    : 0;
+            // a query that sees one key has p = 1 and ds = 0, exactly: all of a sequence with
+            // one key, or the first that sees any, which sees the first key
+            const int alone = w.pl.keys == 1 ? kAttnTile : s.causal && key0 == 0 && w.pl.shift <= 0 ? 1 : 0;
             for (int it = 0, t = w.from; ok && it < total; ++it, phase ^= 1) {
                 const float *const stats =
                     reinterpret_cast<const float *>(ring_stats + at.slot * kStatsBytes) + part * kColumns;
                 const int hidden = hidden0 == INT_MAX ? kColumns : hidden0 - t * kAttnTile;
-                const bool masked = __any_sync(0xffffffffu, hidden > 0);
+                // its column among these, or those of all its tiles
+                const int blank = alone > 1 ? kColumns : alone ? 1 - w.pl.shift - part * kColumns - t * kAttnTile : hidden;
+                const bool masked = __any_sync(0xffffffffu, max(hidden, blank) > 0);
                 const unsigned my_s = s_at + lanes + (kTwo ? phase * 128 : 0) + part * kColumns;
                 ok = attn_wait_warp(&bar.full[at.slot], at.parity, failed) &&
                      attn_wait_warp(&bar.s_full[kTwo ? phase : 0], kTwo ? tiles >> 1 & 1 : phase, failed);
@@ -595,7 +602,7 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                 store_part<T>(my_s, p);
                 wait_st();
                 fence_before();
-                mbar_arrive(&bar.p_full);
+                mbar_arrive(&bar.p_full[kTwo ? phase : 0]);
                 ok = attn_wait_warp(&bar.dp_full, phase, failed);
                 if (!ok) break;
                 fence_after();
@@ -620,7 +627,7 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                 }
                 if (masked) {
 #pragma unroll
-                    for (int i = 0; i < kColumns; ++i) d[i] = i < hidden ? 0.0f : d[i];
+                    for (int i = 0; i < kColumns; ++i) d[i] = i < blank ? 0.0f : d[i];
                 }
                 store_part<T>(kTwo ? my_s + 16 : my_dp, d);
                 wait_st();
@@ -796,7 +803,8 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
             const f32x2 l2 = both(stats[row]);
             const Scales sc = scales_of<T>(a, w.head / s.group);
             const f32x2 n2 = both(stats[kAttnTile + row] * sc.ds);
-            const int end = s.causal ? min(w.pl.keys, w.pl.tile * kAttnTile + row + 1 + w.pl.shift) : w.pl.keys;
+            int end = s.causal ? min(w.pl.keys, w.pl.tile * kAttnTile + row + 1 + w.pl.shift) : w.pl.keys;
+            if (end == 1) end = 0;  // ds = 0, as above
             for (int j = 0; ok && j < total; ++j, ++tiles) {
                 const unsigned my_s = s_at + lanes + (tiles & 1) * 128 + part * kColumns;
                 const unsigned my_dp = dp_at + lanes + part * kColumns;
@@ -868,7 +876,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
                 mbar_init(&b->full[i], 1);
                 mbar_init(&b->empty[i], 1);
             }
-            mbar_init(&b->p_full, kWarps * 32);
+            mbar_init(&b->p_full[0], kWarps * 32);
+            mbar_init(&b->p_full[1], kWarps * 32);
             mbar_init(&b->ds_full, kWarps * 32);
         }
         for (int i = 0; i < kItemSlots; ++i) {
