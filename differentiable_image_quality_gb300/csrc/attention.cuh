@@ -239,9 +239,10 @@ struct AttnBwdArgs {
     int ragged;
     unsigned extra;  // test hook, see gbssim_tune_attention
     // for the row sums
-    const void *out, *g_data, *v_data;
+    const void *out, *g_data, *v_data, *q_data, *k_data;
     long long o_batch, o_token, o_head;  // strides, elements
     long long g_batch, g_token, g_head, v_batch, v_token, v_head;
+    long long q_batch, q_token, q_head, k_batch, k_token, k_head;
     const float *lse;
     void *dq, *dk, *dv;      // each may be null
     float *stats;            // [heads][q_tiles][2][128]

@@ -323,6 +323,14 @@ extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_head
     a.v_batch = d->v.batch_stride;
     a.v_token = d->v.token_stride;
     a.v_head = d->v.head_stride;
+    a.q_data = d->q.data;
+    a.q_batch = d->q.batch_stride;
+    a.q_token = d->q.token_stride;
+    a.q_head = d->q.head_stride;
+    a.k_data = d->k.data;
+    a.k_batch = d->k.batch_stride;
+    a.k_token = d->k.token_stride;
+    a.k_head = d->k.head_stride;
     a.lse = lse;
     a.dq = queries ? grad_q_or_null : nullptr;
     a.dk = keys ? grad_k_or_null : nullptr;

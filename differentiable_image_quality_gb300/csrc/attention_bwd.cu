@@ -74,7 +74,57 @@ __device__ __forceinline__ float largest8(const uint4 &w)
 // 79 us.)  The sums go to the tiles through shared memory.
 constexpr int kSumTokens = 32, kSumHeads = 64, kSumRows = 4;
 
+// Over few keys the output's rounding is a good part of dp - D: there D = sum_j p_ij dp_ij
+// in float32 instead, whose dots cost little.  A kernel of its own (FEW) for calls that
+// can have such sequences and are small, since the registers for it would slow down the
+// others.  By a whole warp, `g` a lane's eight columns of the row's gradient.
+constexpr int kFewKeys = 16, kFewTokens = 2048;
+
 template <typename T, int LANES>
+__device__ __forceinline__ float sum_of_few(const AttnBwdArgs &a, const AttnPlace &pl, int query, int head, bool mine,
+                                         const float (&g)[8])
+{
+    const AttnShape &s = a.s;
+    const int col = threadIdx.x % LANES * 8, kv_head = head / s.group;
+    const int seen = !mine ? 0 : s.causal ? min(pl.keys, query + 1 + pl.shift) : pl.keys;
+    float q[8] = {}, lse = 0.0f, sum = 0.0f;
+    if (seen > 0) {
+        Raw8<T> r;
+        r.w[0] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q_data) + pl.batch * a.q_batch +
+                                                  (long long)(pl.q_row + query) * a.q_token + head * a.q_head + col);
+        unpack8<T>(r, q);
+        lse = a.lse[((long long)pl.batch * s.heads + head) * s.q_tokens + pl.q_row + query] * 1.4426950408889634f;
+    }
+    for (int j = 0; j < pl.keys; ++j) {
+        float x = 0.0f, y = 0.0f;
+        if (j < seen) {
+            Raw8<T> rk, rv;
+            rk.w[0] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.k_data) + pl.batch * a.k_batch +
+                                                       (long long)(pl.k_row + j) * a.k_token + kv_head * a.k_head + col);
+            rv.w[0] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v_data) + pl.batch * a.v_batch +
+                                                       (long long)(pl.k_row + j) * a.v_token + kv_head * a.v_head + col);
+            float k[8], v[8];
+            unpack8<T>(rk, k);
+            unpack8<T>(rv, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x = fmaf(q[e], k[e], x);
+                y = fmaf(g[e], v[e], y);
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int d = LANES / 2; d; d /= 2) {
+            x += __shfl_xor_sync(0xffffffffu, x, d);
+            y += __shfl_xor_sync(0xffffffffu, y, d);
+        }
+        // a lane without columns has seen none: its team's sum is right in the others
+        if (j < seen) sum = fmaf(exp2_fast(fmaf(x, a.scale_log2, -lse)), y, sum);
+    }
+    return sum;
+}
+
+template <typename T, int LANES, bool FEW>
 __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnBwdArgs a, const unsigned q_blocks)
 {
     constexpr int kTeams = kSumThreads / LANES;
@@ -136,6 +186,8 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
                 __syncwarp();
 #pragma unroll
                 for (int d = LANES / 2; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                if (FEW && pl.keys <= kFewKeys)
+                    sum = sum_of_few<T, LANES>(a, pl, first + t, from + h, mine && r < all, u);
                 if (lane == 0 && r < all) sums[h][t] = sum;
             }
             if constexpr (kScaled<T>) {
@@ -930,12 +982,12 @@ cudaError_t launch(const AttnBwdArgs &a, cudaStream_t stream)
         const unsigned q_blocks = unsigned(most_tiles(a.s, a.s.q_tokens, kSumTokens));
         const unsigned v_blocks = kScaled<T> ? unsigned(most_tiles(a.s, a.s.k_tokens, kSumTokens)) : 0;
         const dim3 grid(q_blocks + v_blocks, unsigned((a.s.heads + kSumHeads - 1) / kSumHeads));
-        if (a.s.dim <= 32)
-            attention_sums_kernel<T, 4><<<grid, kSumThreads, 0, stream>>>(a, q_blocks);
-        else if (a.s.dim <= 64)
-            attention_sums_kernel<T, 8><<<grid, kSumThreads, 0, stream>>>(a, q_blocks);
-        else
-            attention_sums_kernel<T, 16><<<grid, kSumThreads, 0, stream>>>(a, q_blocks);
+        const bool few = a.s.k_tokens <= (a.ragged ? kFewTokens : kFewKeys);
+        const auto kernel = a.s.dim <= 32   ? few ? attention_sums_kernel<T, 4, true> : attention_sums_kernel<T, 4, false>
+                            : a.s.dim <= 64 ? few ? attention_sums_kernel<T, 8, true> : attention_sums_kernel<T, 8, false>
+                            : few           ? attention_sums_kernel<T, 16, true>
+                                            : attention_sums_kernel<T, 16, false>;
+        kernel<<<grid, kSumThreads, 0, stream>>>(a, q_blocks);
     } else {
         e = cudaMemsetAsync(a.counter, 0, sizeof(unsigned), stream);
         if (e != cudaSuccess) return e;

@@ -693,3 +693,43 @@ def test_rows_do_not_depend_on_others(pkg, shape):
             pkg.attention_fwd(*loud)
         got = pkg.attention_fwd(q, k, v, want_stats=True)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), n
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=str)
+@pytest.mark.parametrize("keys", [1, 2, 3, 16])
+def test_gradients_over_few_keys(pkg, keys, dtype):
+    """Where a query sees one key, its gradient and the key's are zero exactly; where it
+    sees a few, the output's rounding is not in them: ds is off by its own rounding (u)
+    and float32 sums alone."""
+    q, k, v = inputs(74, 2, 5, keys, 4, 2, 40, dtype)
+    g = normal(torch.Generator(device="cuda").manual_seed(75), *q.shape, dtype=dtype)
+    for causal in (False, True):
+        out, lse = pkg.attention_fwd(q, k, v, causal=causal, want_stats=True)
+        dq, dk, _ = pkg.attention_bwd(g, q, k, v, out, lse, causal=causal)
+        if keys == 1:
+            assert (dq == 0).all() and (dk == 0).all()
+            continue
+        for b in range(2):
+            seen = visible(5, keys, causal, keys)
+            _, ref_lse, _, _ = definition(q[b], k[b], v[b], 40 ** -0.5, seen)
+            exact = definition(q[b], k[b], v[b], 40 ** -0.5, seen)[0]
+            for t, (ref, bound) in zip((dq[b], dk[b]),
+                                       definition_bwd(g[b], q[b], k[b], v[b], exact, 40 ** -0.5,
+                                                      seen, ref_lse)):
+                assert ((t.double() - ref).abs() <= bound).all()
+        if causal and keys <= 5:
+            first = 5 - keys  # the first query that sees a key sees one
+            assert (dq[:, first] == 0).all()
+
+
+@pytest.mark.parametrize("shape", [(2, 2383, 2383, 16, 8, 16), (1, 3001, 3001, 3, 1, 64)], ids=str)
+def test_warps_apart(pkg, shape):
+    """Many tiles of narrow heads, where a block's warps may be a tile apart."""
+    q, k, v = inputs(76, *shape, BF)
+    g = normal(torch.Generator(device="cuda").manual_seed(77), *q.shape)
+    out, lse = pkg.attention_fwd(q, k, v, causal=True, want_stats=True)
+    want = pkg.attention_bwd(g, q, k, v, out, lse, causal=True)
+    assert all(t.isfinite().all() for t in want)
+    for _ in range(30):
+        got = pkg.attention_bwd(g, q, k, v, out, lse, causal=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
