@@ -46,7 +46,16 @@ into other tensors; and
 is what a transformer block does around its residual sum -- the norm after the
 block, its gate, the scaled sum, the norm before the next block -- in one pass,
 with its backward; residual_norm_fwd / residual_norm_bwd are the two calls
-without autograd.  These take float32, bfloat16 and float16.
+without autograd.  These take float32, bfloat16 and float16.  Between a block's
+tokens,
+
+    rotary_frequencies(pairs)
+    fused_rotary(q, k, positions, frequencies, pairs, layout="half")
+    fused_attention(q, k, v, causal=..., kv_lengths=..., offsets=...)
+
+are rotary positions on up to four axes and softmax attention (bfloat16 and
+float16; batches, key lengths, packed sequences, shared key heads), with their
+backward; rotary, attention_fwd and attention_bwd are the calls without autograd.
 """
 from __future__ import annotations
 
