@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
     if (heads <= 0) return;
     if (threadIdx.x < 32) {
         AttnPlace p;
-        const bool ok = values ? find_place<true>(s, blockIdx.x - q_blocks, kSumTokens, p)
-                               : find_place<false>(s, blockIdx.x, kSumTokens, p);
+        const bool ok = values ? find_place<true>(s, blockIdx.x - q_blocks, kSumTokens, p, nullptr)
+                               : find_place<false>(s, blockIdx.x, kSumTokens, p, nullptr);
         if (threadIdx.x == 0) {
             place = p;
             there = ok;
@@ -265,6 +265,7 @@ struct BwdShared {
     uint64_t item_full[kItemSlots], item_empty[kItemSlots];
     uint64_t keys_stored, drained;
     BwdItem item[kItemSlots], none;  // none: after the last
+    AttnCursor cursor;
     unsigned tmem, failed;
 };
 
@@ -283,7 +284,7 @@ __device__ __forceinline__ bool wait_item(BwdShared &sh, uint64_t *bar, unsigned
 // before the others; else a head's items one after another, which share its tiles in
 // L2.
 template <bool KEYS>
-__device__ __forceinline__ void find_item(const AttnBwdArgs &a, unsigned u, BwdItem &w)
+__device__ __forceinline__ void find_item(const AttnBwdArgs &a, unsigned u, BwdItem &w, AttnCursor *cursor)
 {
     const AttnShape &s = a.s;
     if (!KEYS) u -= a.key_items;
@@ -306,7 +307,7 @@ __device__ __forceinline__ void find_item(const AttnBwdArgs &a, unsigned u, BwdI
         w.head = u / all;
         index = u % all;
     }
-    w.there = find_place<KEYS>(s, index, kAttnTile, w.pl);
+    w.there = find_place<KEYS>(s, index, kAttnTile, w.pl, cursor);
     if (!w.there) w.pl = {};  // packed: fewer tiles than there could be
     const AttnPlace &pl = w.pl;
     if (KEYS) {
@@ -333,9 +334,9 @@ __device__ __forceinline__ BwdItem publish_item(const AttnBwdArgs &a, BwdShared 
     if (threadIdx.x % 32 == 0) w.u = atomicAdd(a.counter, 1u);
     w.u = uniform(w.u);
     if (w.u < a.key_items)
-        find_item<true>(a, w.u, w);
+        find_item<true>(a, w.u, w, &sh.cursor);
     else if (w.u < a.items)
-        find_item<false>(a, w.u, w);
+        find_item<false>(a, w.u, w, &sh.cursor);
     if (n >= kItemSlots && !wait_item(sh, &sh.item_empty[slot], (n / kItemSlots - 1) & 1)) return sh.none;
     ++n;
     if (threadIdx.x % 32 == 0) {
@@ -925,6 +926,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
         for (const CUtensorMap *m : {&a.q, &a.k, &a.v, &a.g}) prefetch_map(m);
         sh.failed = 0;
         sh.none = {};
+        sh.cursor = {};
         sh.none.u = UINT_MAX;
         for (BwdBarriers *b : {&sh.keys, &sh.queries}) {
             for (uint64_t *x : {&b->own_full, &b->own_empty, &b->s_full[0], &b->s_full[1], &b->dp_full, &b->done,

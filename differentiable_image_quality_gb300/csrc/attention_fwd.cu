@@ -52,6 +52,7 @@ struct FwdShared {
     uint64_t kv_full[8], kv_empty[8], patched, drained;
     uint64_t item_full[kItemSlots], item_empty[kItemSlots];
     FwdItem<QT> item[kItemSlots], none;  // none: after the last
+    AttnCursor cursor;
     unsigned tmem, failed;
 };
 
@@ -70,7 +71,7 @@ constexpr float kLateMax = 8.0f;
 // The index-th of the call's, by a whole warp.  Those of one head follow one another,
 // so that its keys stay in L2; causal ones by falling work instead, the longest first.
 template <int QT>
-__device__ __forceinline__ void find_item(const AttnFwdArgs &a, unsigned u, FwdItem<QT> &w)
+__device__ __forceinline__ void find_item(const AttnFwdArgs &a, unsigned u, FwdItem<QT> &w, AttnCursor *cursor)
 {
     const AttnShape &s = a.s;
     const int head_blocks = s.heads / a.tile_heads;
@@ -90,7 +91,7 @@ __device__ __forceinline__ void find_item(const AttnFwdArgs &a, unsigned u, FwdI
         batch = u / head_blocks;
     }
     w.kv_head = a.tile_heads > 1 ? w.head : w.head / s.group;
-    if (!find_place<false>(s, batch * a.tiles + tile, a.tile_tokens * QT, w.pl)) {
+    if (!find_place<false>(s, batch * a.tiles + tile, a.tile_tokens * QT, w.pl, cursor)) {
         w.pl = {};  // packed: fewer tiles than there could be
     }
     w.first = w.pl.tile * a.tile_tokens * QT;
@@ -143,7 +144,7 @@ __device__ __forceinline__ FwdItem<QT> publish_item(const AttnFwdArgs &a, FwdSha
     } else {
         w.u = item_of(n);
     }
-    if (w.u < a.items) find_item(a, w.u, w);
+    if (w.u < a.items) find_item(a, w.u, w, &sh.cursor);
     if (n >= kItemSlots && !wait_item(sh, &sh.item_empty[slot], (n / kItemSlots - 1) & 1)) return sh.none;
     ++n;
     if (threadIdx.x % 32 == 0) {
@@ -212,6 +213,7 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
             mbar_init(&sh.item_empty[i], QT * 4 + 1);
         }
         sh.none = {};
+        sh.cursor = {};
         sh.none.u = UINT_MAX;
         mbar_init(&sh.patched, 1);
         mbar_init(&sh.drained, 1);
