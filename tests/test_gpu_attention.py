@@ -8,6 +8,8 @@ probability is rounded once to the type: relative u.  So the output is off by at
 (u + 2 e + 2^-18) sum p|v| + u |o|: errors of the numerator, and the unrounded
 denominator's.
 """
+import random
+
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -305,6 +307,34 @@ def test_cross_packed(pkg):
         check_gradients([got[0][a:b], got[1][c:d], got[2][c:d]], g[a:b], q[a:b], k[c:d], v[c:d],
                         out[a:b], D ** -0.5, seen)
     assert (got[1][ke[-1]:] == 0).all()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_many_short_sequences(pkg, causal):
+    """More sequences than a block's searches pass at once, so that its items come from
+    far apart, a run of empty ones among them, the queries' and keys' lengths their own."""
+    rng = random.Random(13)
+    ql = [rng.choice((0, 1, 5, 17, 40)) for _ in range(500)]
+    kl = [rng.choice((0, 1, 9, 33, 150)) for _ in range(500)]
+    ql[200:300] = kl[180:280] = [0] * 100
+    H, K, D = 4, 2, 64
+    qe, qo = pack_offsets(ql)
+    ke, ko = pack_offsets(kl)
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    q, g = normal(gen, qe[-1] + 2, H, D), normal(gen, qe[-1] + 2, H, D)
+    k, v = normal(gen, ke[-1] + 3, K, D), normal(gen, ke[-1] + 3, K, D)
+    out, lse = pkg.attention_fwd(q, k, v, causal=causal, offsets=qo, kv_offsets=ko, want_stats=True)
+    got = pkg.attention_bwd(g, q, k, v, out, lse, causal=causal, offsets=qo, kv_offsets=ko)
+    for a, b, c, d in zip(qe, qe[1:], ke, ke[1:]):
+        if a == b:
+            assert (got[1][c:d] == 0).all() and (got[2][c:d] == 0).all()
+            continue
+        seen = visible(b - a, d - c, causal, d - c)
+        check_sequence(out[a:b], lse[:, a:b], q[a:b], k[c:d], v[c:d], D ** -0.5, seen)
+        check_gradients([got[0][a:b], got[1][c:d], got[2][c:d]], g[a:b], q[a:b], k[c:d], v[c:d],
+                        out[a:b], D ** -0.5, seen)
+    assert (out[qe[-1]:] == 0).all() and (got[0][qe[-1]:] == 0).all()
+    assert (got[1][ke[-1]:] == 0).all() and (got[2][ke[-1]:] == 0).all()
 
 
 def test_small_float16_gradients(pkg):
