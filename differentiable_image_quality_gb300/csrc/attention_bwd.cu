@@ -282,7 +282,8 @@ __device__ __forceinline__ bool wait_item(BwdShared &sh, uint64_t *bar, unsigned
 
 // By a whole warp.  Causal: falling work, that of the first keys and of the last queries
 // before the others; else a head's items one after another, which share its tiles in
-// L2.
+// L2, or packed a tile's heads, so that the search has a short way (200 sequences of up
+// to 600 tokens, 24 heads of 64: 904 -> 817 us).
 template <bool KEYS>
 __device__ __forceinline__ void find_item(const AttnBwdArgs &a, unsigned u, BwdItem &w, AttnCursor *cursor)
 {
@@ -292,12 +293,12 @@ __device__ __forceinline__ void find_item(const AttnBwdArgs &a, unsigned u, BwdI
     if (KEYS) u /= a.key_parts;
     const int all = KEYS ? a.k_tiles : a.q_tiles;
     int index;
-    if (s.causal) {
+    if (s.causal || s.packed) {
         const int heads = KEYS ? s.kv_heads : s.heads;
         w.head = u % heads;
         const int i = u / heads;
         if (s.packed) {
-            index = KEYS ? i : all - 1 - i;
+            index = KEYS || !s.causal ? i : all - 1 - i;
         } else {
             const int tiles = all / s.sequences;
             const int tile = KEYS ? i / s.sequences : tiles - 1 - i / s.sequences;

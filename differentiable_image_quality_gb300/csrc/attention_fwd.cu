@@ -70,6 +70,9 @@ constexpr float kLateMax = 8.0f;
 
 // The index-th of the call's, by a whole warp.  Those of one head follow one another,
 // so that its keys stay in L2; causal ones by falling work instead, the longest first.
+// Packed, a tile's heads follow one another, so that the search has a short way (24
+// sequences of up to 1500 tokens, 16 heads of 64: 95 -> 91 us; 200 of up to 600, 24 heads
+// of 64: 318 -> 276).
 template <int QT>
 __device__ __forceinline__ void find_item(const AttnFwdArgs &a, unsigned u, FwdItem<QT> &w, AttnCursor *cursor)
 {
@@ -84,6 +87,10 @@ __device__ __forceinline__ void find_item(const AttnFwdArgs &a, unsigned u, FwdI
         u /= head_blocks;
         batch = u % batches;
         tile = a.tiles - 1 - u / batches;
+    } else if (s.packed) {
+        w.head = u % head_blocks;
+        tile = u / head_blocks;
+        batch = 0;
     } else {
         tile = u % a.tiles;
         u /= a.tiles;
