@@ -309,8 +309,8 @@ def test_cross_packed(pkg):
     assert (got[1][ke[-1]:] == 0).all()
 
 
-@pytest.mark.parametrize("causal", [False, True])
-def test_many_short_sequences(pkg, causal):
+@pytest.mark.parametrize("causal, dtype", [(False, BF), (True, BF), (False, HF)])
+def test_many_short_sequences(pkg, causal, dtype):
     """More sequences than a block's searches pass at once, so that its items come from
     far apart, a run of empty ones among them, the queries' and keys' lengths their own."""
     rng = random.Random(13)
@@ -321,8 +321,8 @@ def test_many_short_sequences(pkg, causal):
     qe, qo = pack_offsets(ql)
     ke, ko = pack_offsets(kl)
     gen = torch.Generator(device="cuda").manual_seed(14)
-    q, g = normal(gen, qe[-1] + 2, H, D), normal(gen, qe[-1] + 2, H, D)
-    k, v = normal(gen, ke[-1] + 3, K, D), normal(gen, ke[-1] + 3, K, D)
+    q, g = (normal(gen, qe[-1] + 2, H, D, dtype=dtype) for _ in range(2))
+    k, v = (normal(gen, ke[-1] + 3, K, D, dtype=dtype) for _ in range(2))
     out, lse = pkg.attention_fwd(q, k, v, causal=causal, offsets=qo, kv_offsets=ko, want_stats=True)
     got = pkg.attention_bwd(g, q, k, v, out, lse, causal=causal, offsets=qo, kv_offsets=ko)
     for a, b, c, d in zip(qe, qe[1:], ke, ke[1:]):
