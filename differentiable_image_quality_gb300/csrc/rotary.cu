@@ -4,14 +4,14 @@
 // also the gradient.
 //
 // Angles are taken modulo a turn in fixed point: f / (2 pi) as a fraction of 2^64,
-// times the position, wraps by itself, so far positions lose nothing; sine and
-// cosine then see at most half a turn, in float32.
+// times the position, wraps by itself, so far positions lose nothing but that quotient's
+// rounding; sine and cosine then see at most half a turn, in float32.
 //
 // Bound by memory: every element is read and written once.  A thread has eight columns
 // of a token (in the layout of halves, four of each half) and goes over the token's
 // heads with their sines and cosines in registers, two heads' loads under way while it
 // turns the last two, and the first ones before it knows the angles.  Nothing but the
-// frequencies' fractions is in shared memory, so that no thread waits for another.
+// frequencies' turns is in shared memory, so that no thread waits for another.
 // 65536 tokens, 20 heads of 128, bfloat16 (671 MB): 127 us, 5.3 TB/s; 32400 tokens, 24
 // heads of 88, float32 (547 MB): 108 us; 512 tokens: 6.4 us.
 #include <algorithm>
@@ -20,6 +20,7 @@
 
 #include "api_host.cuh"
 #include "dtypes.cuh"
+#include "rotary_angle.cuh"
 
 namespace gbssim {
 namespace {
@@ -53,36 +54,25 @@ enum Mode {
     kSingle     // a pair or a column a thread: any alignment
 };
 
-// The fraction of a turn that a unit of position is, times 2^64; of a negative frequency
-// from its magnitude, whose fraction is exact.
-__device__ __forceinline__ unsigned long long turn_fraction(double f)
-{
-    double t = fabs(f) * 0.15915494309189535;  // 1 / (2 pi)
-    t -= floor(t);
-    const unsigned long long part = t < 1.0 ? (unsigned long long)(t * 18446744073709551616.0) : 0ull;
-    return f < 0.0 ? 0ull - part : part;
-}
+// A pair's axis, and a flag where its frequency is below zero.
+constexpr int kNegative = 64;
 
-// cos and sin of position x fraction.  Where results are rounded to 16 bits (2^-8, 2^-11)
+// cos and sin of position x frequency.  Where results are rounded to 16 bits (2^-8, 2^-11)
 // the hardware's approximations do, which are within 2^-21 over a turn; they take a
 // tenth of the instructions of the exact functions.
 template <bool EXACT>
-__device__ __forceinline__ float2 turn_of(const RotaryArgs &a, const void *pos, long long at, unsigned long long f)
+__device__ __forceinline__ float2 turn_of(const RotaryArgs &a, long long at, turns64 fraction, const turns64 &whole,
+                                          bool negative)
 {
-    unsigned long long phase;
+    turns64 phase;
     if (a.pos_type == GBSSIM_POS_I32) {
-        phase = (unsigned long long)(long long)static_cast<const int *>(pos)[at] * f;
+        phase = turn_phase((long long)static_cast<const int *>(a.positions)[at], fraction);
     } else if (a.pos_type == GBSSIM_POS_I64) {
-        phase = (unsigned long long)static_cast<const long long *>(pos)[at] * f;
+        phase = turn_phase(static_cast<const long long *>(a.positions)[at], fraction);
     } else {
-        const float x = static_cast<const float *>(pos)[at];
+        const float x = static_cast<const float *>(a.positions)[at];
         if (!(fabsf(x) < 9.0e18f)) return make_float2(NAN, NAN);
-        // the fraction of |x| has no bit that float32 does not hold; below 2^-32 of a
-        // unit it is cut
-        const float whole = floorf(fabsf(x));
-        const unsigned part = unsigned((fabsf(x) - whole) * 4294967296.0f);
-        phase = (unsigned long long)(long long)whole * f + __umul64hi(f, (unsigned long long)part << 32);
-        if (x < 0.0f) phase = 0ull - phase;
+        phase = turn_phase(x, fraction, whole, negative);
     }
     const float turned = float(int(unsigned(phase >> 32)));  // 2^-31 half turns
     float s, c;
@@ -178,15 +168,18 @@ struct Cut {
 template <typename T, Mode M, int V>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, const Cut cut)
 {
-    __shared__ unsigned long long fraction[kMaxPairs];
+    __shared__ turns64 fraction[kMaxPairs], whole[kMaxPairs];
     __shared__ unsigned char axis_of[kMaxPairs];
     const int n = a.pairs;
     for (int i = threadIdx.x; i < n; i += kThreads) {
         int axis = 0;
         while (i >= a.ends[axis]) ++axis;
         const double f = a.frequencies[i];
-        axis_of[i] = static_cast<unsigned char>(isfinite(f) ? axis : kNoAngle);
-        fraction[i] = turn_fraction(f);
+        const bool some = isfinite(f);
+        axis_of[i] = static_cast<unsigned char>(!some ? kNoAngle : f < 0.0 ? axis + kNegative : axis);
+        fraction[i] = some ? turn_fraction(f) : 0;
+        // (for other positions as well: 1 % of a long call's time)
+        whole[i] = some && a.pos_type == GBSSIM_POS_F32 ? whole_turns(f) : 0;
     }
     __syncthreads();
     const int end = a.t[0].heads + a.t[1].heads, step = cut.parts;
@@ -211,7 +204,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, co
         const long long pos = b * a.pos_batch + token * a.pos_token;
         const auto turn = [&](int p) {
             const int axis = axis_of[p];
-            return axis == kNoAngle ? make_float2(NAN, NAN) : turn_of<sizeof(T) == 4>(a, a.positions, pos + axis, fraction[p]);
+            if (axis == kNoAngle) return make_float2(NAN, NAN);
+            return turn_of<sizeof(T) == 4>(a, pos + axis % kNegative, fraction[p], whole[p], axis >= kNegative);
         };
         // the rows of this token's heads: the first tensor's, then the second's
         const T *const in0 = static_cast<const T *>(a.t[0].in) + b * a.t[0].batch + token * a.t[0].token;

@@ -389,8 +389,9 @@ typedef struct {
  * pairs[0] + ... in all, 2 n <= dim; GBSSIM_ROTARY_HALF pairs columns p and p + n,
  * GBSSIM_ROTARY_ADJACENT 2 p and 2 p + 1.  Columns from 2 n on are copied.
  *
- * Angles are taken modulo a turn in 64-bit fixed point, to within the rounding of
- * f_p / (2 pi) to float64 times the position: far positions are as exact as near ones.
+ * Angles are taken modulo a turn in 64-bit fixed point: what they lose is the rounding of
+ * f_p / (2 pi) to float64, times the position, and then float32's of less than half a turn.
+ * Frequencies are finite numbers of any size and sign (others make their pair NaN).
  * A float32 position that is NaN, infinite or above 9e18 makes its token's turned
  * columns of that axis NaN.  Results are rounded once from float32.
  *
