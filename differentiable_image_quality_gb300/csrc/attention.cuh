@@ -9,12 +9,11 @@
 
 #include "common.cuh"
 #include "dtypes.cuh"
+#include "packed.cuh"
 #include "tensor_core.cuh"
 
 namespace gbssim {
 
-// Queries and keys come in tiles of 128 rows, the lanes of tensor memory.
-constexpr int kAttnTile = 128;
 constexpr int kAttnMaxDim = 128;
 constexpr int kAttnBlocks = 152;  // that run at once: one to an SM
 
@@ -23,6 +22,7 @@ struct AttnShape {
     int q_tokens, k_tokens;  // of a sample, or rows of the packed tensors
     int heads, kv_heads, group, dim;
     int causal, packed;
+    int q_tiles;             // of 128 queries, or the most there can be (packed)
     const int *kv_lengths, *q_offsets, *k_offsets;
 };
 
@@ -35,18 +35,6 @@ struct AttnPlace {
     int tile;           // which tile of the sequence
     int q_tiles_before; // of the queries of the sequences before it, in tiles of 128
 };
-
-// Offsets that do not ascend or leave the tensors are brought into range, so that
-// no row outside them is read or written whatever they hold.  Behind the last
-// sequence comes one more, of the rows that are left and without a partner: its
-// outputs are zeros.
-__device__ __forceinline__ void packed_span(const int *offsets, int sequences, int rows, int s,
-                                            int &first, int &count)
-{
-    first = s == 0 ? 0 : min(max(__ldg(offsets + s), 0), rows);
-    const int end = s >= sequences ? rows : min(max(__ldg(offsets + s + 1), first), rows);
-    count = end - first;
-}
 
 // Where the last search of a packed batch ended: ahead of sequence `base` there are
 // `before` tiles of the keys or the queries.  A block's items lie close to one another, so
@@ -104,7 +92,7 @@ __device__ __forceinline__ bool find_place(const AttnShape &s, int index, int ro
         const int all = __shfl_sync(0xffffffffu, sum, 31), q_all = __shfl_sync(0xffffffffu, q_sum, 31);
         if (back) {
             c.before -= all;
-            c.q_before -= q_all;
+            c.q_before = max(c.q_before - q_all, 0);
             back = index < c.before && base > 0;
             if (back) {
                 c.base -= 32;
@@ -124,11 +112,12 @@ __device__ __forceinline__ bool find_place(const AttnShape &s, int index, int ro
             // the rows behind the last sequences have no partners
             if (base + l == s.sequences) (BY_KEYS ? p.queries : p.keys) = 0;
             p.shift = p.keys - p.queries;
+            keep_within(s.q_tiles, p.q_tiles_before, p.queries);
             found = true;
         } else {
             c.base += 32;
             c.before += all;
-            c.q_before += q_all;
+            c.q_before = add_tiles(c.q_before, q_all);
         }
     }
     if (kept) {

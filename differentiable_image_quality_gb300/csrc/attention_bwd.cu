@@ -149,11 +149,14 @@ __device__ __forceinline__ void skip_shares(const AttnShape &s, bool by_keys, in
         int first, queries, keys;
         packed_span(s.q_offsets, s.sequences, s.q_tokens, n, first, queries);
         packed_span(s.k_offsets, s.sequences, s.k_tokens, n, first, keys);
-        sum += ((by_keys ? keys : queries) + kSumTokens - 1) / kSumTokens;
-        q_sum += (queries + kAttnTile - 1) / kAttnTile;
+        sum = add_tiles(sum, ((by_keys ? keys : queries) + kSumTokens - 1) / kSumTokens);
+        q_sum = add_tiles(q_sum, (queries + kAttnTile - 1) / kAttnTile);
     }
-    sum = __reduce_add_sync(0xffffffffu, sum);
-    q_sum = __reduce_add_sync(0xffffffffu, q_sum);
+#pragma unroll
+    for (int d = 16; d; d /= 2) {
+        sum = add_tiles(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+        q_sum = add_tiles(q_sum, __shfl_xor_sync(0xffffffffu, q_sum, d));
+    }
     if (lane == 0) {
         tiles[warp] = sum;
         q_tiles[warp] = q_sum;
@@ -163,7 +166,7 @@ __device__ __forceinline__ void skip_shares(const AttnShape &s, bool by_keys, in
         for (int w = 0; w < kShares && c.before + tiles[w] <= index; ++w) {
             c.base += share;
             c.before += tiles[w];
-            c.q_before += q_tiles[w];
+            c.q_before = add_tiles(c.q_before, q_tiles[w]);
         }
     }
     __syncthreads();
