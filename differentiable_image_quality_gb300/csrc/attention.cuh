@@ -28,6 +28,7 @@ struct AttnShape {
 
 // Where a block's queries and keys lie.
 struct AttnPlace {
+    int sequence;       // packed: as many as there are where it is the rows behind them
     int batch;          // outermost coordinate of the tensors
     int q_row, k_row;   // of the sequence's first query and key
     int queries, keys;  // of the sequence
@@ -55,7 +56,7 @@ __device__ __forceinline__ bool find_place(const AttnShape &s, int index, int ro
     if (!s.packed) {
         const int most = BY_KEYS ? s.k_tokens : s.q_tokens;
         const int tiles = (most + rows - 1) / rows;
-        p.batch = index / tiles;
+        p.sequence = p.batch = index / tiles;
         p.tile = index - p.batch * tiles;
         p.q_tiles_before = p.batch * ((s.q_tokens + kAttnTile - 1) / kAttnTile);
         p.q_row = p.k_row = 0;
@@ -105,6 +106,7 @@ __device__ __forceinline__ bool find_place(const AttnShape &s, int index, int ro
             p.tile = index - c.before - __shfl_sync(0xffffffffu, sum - tiles, l);
             p.q_tiles_before = c.q_before + __shfl_sync(0xffffffffu, q_sum - q_tiles, l);
             p.batch = 0;
+            p.sequence = base + l;
             p.q_row = __shfl_sync(0xffffffffu, q_first, l);
             p.k_row = __shfl_sync(0xffffffffu, k_first, l);
             p.queries = __shfl_sync(0xffffffffu, queries, l);
@@ -267,7 +269,7 @@ struct AttnBwdArgs {
     const float *lse;
     void *dq, *dk, *dv;      // each may be null
     float *stats;            // [heads][q_tiles][2][128]
-    unsigned *largest;       // [2][kv_heads]: |g|, |v|, as bits (float16)
+    unsigned *largest;       // [sequences + 1][kv_heads][2]: |g|, |v|, as bits (float16)
     unsigned *counter;       // of items taken
 };
 

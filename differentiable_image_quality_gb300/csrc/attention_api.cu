@@ -176,13 +176,20 @@ int key_parts(const gbssim_attention &d)
     return parts > 1 && longest - longest / parts >= 6 ? parts : 1;
 }
 
-// The backward's row sums, in tiles of 128 queries, and the largest |g| and |v| of each
-// key head, the counter of items; then the parts of dv and dk.
+// Of each sequence's key heads, and of the rows behind the last one: the largest |g| and
+// |v|, which float16 takes its scales from.
+size_t largest_words(const gbssim_attention &d)
+{
+    return d.dtype == GBSSIM_F16 ? size_t(2) * (d.sequences + 1) * d.kv_heads : 0;
+}
+
+// The backward's row sums, in tiles of 128 queries, those, and the counter of items; then
+// the parts of dv and dk.
 size_t sums_bytes(const gbssim_attention &d)
 {
     const long long tiles = d.q_tokens ? most_tiles(shape_of(d), d.q_tokens, kAttnTile) : 0;
     const size_t n = size_t(d.heads) * tiles * 2 * kAttnTile * sizeof(float) +
-                     size_t(2 * d.kv_heads + 1) * sizeof(unsigned);
+                     (largest_words(d) + 1) * sizeof(unsigned);
     return (n + 15) / 16 * 16;
 }
 
@@ -345,8 +352,8 @@ extern "C" int gbssim_attention_bwd(const gbssim_attention *d, const gbssim_head
     a.items = a.key_items + (a.dq ? unsigned(q_tiles * d->heads) : 0);
     a.stats = static_cast<float *>(workspace);
     unsigned *const words = reinterpret_cast<unsigned *>(a.stats + size_t(d->heads) * q_tiles * 2 * kAttnTile);
-    a.largest = queries ? words : nullptr;
-    a.counter = words + 2 * d->kv_heads;
+    a.largest = words;
+    a.counter = words + largest_words(*d);
     return cuda_fail(attention_bwd_launch(a, d->dtype, static_cast<cudaStream_t>(stream)));
 }
 

@@ -30,30 +30,39 @@ constexpr int tile_bytes()
 }
 
 // float16 leaves little room below: probabilities go into their product times 2^14,
-// and ds times a power of two for each key head, chosen from the largest |g| and
-// |v| so that no product of them overflows.  bfloat16 needs neither.
-constexpr float kProbBits = 14.0f;
+// and ds times a power of two for each key head of a sequence, chosen from the largest
+// |g| and |v| there so that no product of them overflows.  bfloat16 needs neither.
+constexpr int kProbBits = 14;
 template <typename T>
 constexpr bool kScaled = std::is_same<T, f16>::value;
 
-struct Scales {
-    float ds;  // of dp - D
-    float inv_p, inv_ds;
-};
-
-template <typename T>
-__device__ __forceinline__ Scales scales_of(const AttnBwdArgs &a, int kv_head)
+__device__ __forceinline__ unsigned *largest_at(const AttnBwdArgs &a, int sequence, int kv_head)
 {
-    if (!kScaled<T> || !a.largest) return {1.0f, 1.0f, 1.0f};
-    const float g = __uint_as_float(__ldg(a.largest + kv_head));
-    const float v = __uint_as_float(__ldg(a.largest + a.s.kv_heads + kv_head));
-    // |dp - D| <= 2 dim |g| |v|, since o is a mean of v
-    const float most = 2.0f * a.s.dim * g * v;
-    int bits = 0;
-    if (most > 0.0f && most < INFINITY) bits = min(max(14 - ilogbf(most), -100), 100);
-    const float up = exp2f(float(bits)), p = exp2f(kProbBits);
-    return {up / p, 1.0f / p, 1.0f / up};
+    return a.largest + 2 * ((long long)sequence * a.s.kv_heads + kv_head);
 }
+
+// What an item's power of two comes from is asked for at its start, and looked at when its
+// first dp is here: waited for by the copying warp before the others know of the item, it
+// cost 24 packed images (16 heads of 64, 235 us) 8 us.
+template <typename T>
+__device__ __forceinline__ uint2 ask_largest(const AttnBwdArgs &a, int sequence, int kv_head)
+{
+    uint2 m{0, 0};
+    if constexpr (kScaled<T>)
+        asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(m.x), "=r"(m.y) : "l"(largest_at(a, sequence, kv_head)));
+    return m;
+}
+
+__device__ __forceinline__ int scale_bits(const uint2 &largest, int dim)
+{
+    const auto value = [](unsigned bits) { return __half2float(__ushort_as_half(static_cast<unsigned short>(bits))); };
+    // |dp - D| <= 2 dim |g| |v|, since o is a mean of v; above 2^-44 where it is not zero
+    const float most = 2.0f * dim * value(largest.x) * value(largest.y);
+    return most > 0.0f ? 14 + 127 - (__float_as_int(most) >> 23) : 0;
+}
+
+// 2^bits, from -126 to 127.
+__device__ __forceinline__ float power_of_two(int bits) { return __int_as_float((bits + 127) << 23); }
 
 // ------------------------------------------------------------------- row sums
 
@@ -62,16 +71,14 @@ __device__ __forceinline__ Scales scales_of(const AttnBwdArgs &a, int kv_head)
 // no key, have -infinity: their probabilities are zero.
 constexpr int kSumThreads = 256;
 
-template <typename T>
-__device__ __forceinline__ float largest8(const uint4 &w)
+// The largest magnitude, as float16's bits, of finite elements: what others make of theirs
+// is not finite whatever the scale.  Bits of magnitudes order as the magnitudes do; moved
+// up by 0x400 those of infinities and NaN are negative.
+__device__ __forceinline__ unsigned largest8(const uint4 &w)
 {
-    float m = 0.0f;
-    for (uint32_t x : {w.x, w.y, w.z, w.w}) {
-        const float2 f = unpack2<T>(x & 0x7fff7fffu);
-        // as bits, so that a NaN is the largest
-        m = __uint_as_float(max(max(__float_as_uint(f.x), __float_as_uint(f.y)), __float_as_uint(m)));
-    }
-    return m;
+    unsigned m = 0x04000400u;
+    for (uint32_t x : {w.x, w.y, w.z, w.w}) m = __vmaxs2(m, (x & 0x7fff7fffu) + 0x04000400u);
+    return max(m >> 16, m & 0xffffu) - 0x400u;
 }
 
 // A block has 32 tokens and up to 64 heads, whose rows lie one behind the other in
@@ -216,6 +223,9 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
     const long long x_token = values ? a.v_token : a.g_token, x_head = values ? a.v_head : a.g_head;
     const T *const o = static_cast<const T *>(a.out) + pl.batch * a.o_batch +
                        (long long)(pl.q_row + first) * a.o_token + from * a.o_head + lane * 8;
+    // rows that count for the largest: of a query that sees a key, of a key that has queries
+    const int counted = values ? (pl.queries > 0 ? 0 : INT_MAX)
+                        : pl.keys == 0 ? INT_MAX : s.causal ? -pl.shift - first : 0;
     const int all = count * heads;
     for (int base = 0; base < all; base += kTeams * kSumRows) {  // all threads alike: they shuffle
         Raw8<T> rx[kSumRows], ro[kSumRows];
@@ -244,7 +254,7 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
                 if (lane == 0 && r < all) sums[h][t] = sum;
             }
             if constexpr (kScaled<T>) {
-                unsigned m = __float_as_uint(largest8<T>(rx[i].w[0]));
+                unsigned m = t < counted ? 0 : largest8(rx[i].w[0]);
                 __syncwarp();
 #pragma unroll
                 for (int d = LANES / 2; d; d /= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -257,7 +267,7 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
         // hardly a block has more than the others had: most need no atomic in memory
         const int h = threadIdx.x;
         if (h < heads) {
-            unsigned *const to = a.largest + (values ? s.kv_heads + from + h : (from + h) / s.group);
+            unsigned *const to = largest_at(a, pl.sequence, values ? from + h : (from + h) / s.group) + values;
             if (most[h] > __ldcg(to)) atomicMax(to, most[h]);
         }
     }
@@ -270,7 +280,7 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
         float l = -INFINITY, sum = 0.0f;
         if (r < count) {
             const float lse = a.lse[((long long)pl.batch * s.heads + head) * s.q_tokens + pl.q_row + t];
-            if (lse != -INFINITY) l = (kScaled<T> ? kProbBits : 0.0f) - lse * 1.4426950408889634f;
+            if (lse != -INFINITY) l = (kScaled<T> ? float(kProbBits) : 0.0f) - lse * 1.4426950408889634f;
             sum = sums[h][r];
         }
         float *const stats =
@@ -666,7 +676,8 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
         unsigned uses = 0, phase = 0, tiles = 0;
         for (; w.u < a.key_items; w = take_item(sh, n)) {
             const int total = w.total;
-            const Scales sc = scales_of<T>(a, w.head);
+            const uint2 largest = ask_largest<T>(a, w.pl.sequence, w.head);
+            int bits = 0;  // ds times 2^bits (float16)
             // columns before hidden0 - 128 t are queries of tile t that do not see this key
             const int key0 = w.pl.tile * kAttnTile + row;
             const int hidden0 = key0 >= w.pl.keys ? INT_MAX
@@ -713,6 +724,8 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                 ok = attn_wait_warp(&bar.dp_full, phase, failed);
                 if (!ok) break;
                 fence_after();
+                if (kScaled<T> && it == 0) bits = scale_bits(largest, s.dim);
+                const f32x2 up2 = both(power_of_two(bits - kProbBits));  // p is there times 2^kProbBits
                 float d[kColumns];
                 ld32(my_dp, reinterpret_cast<uint32_t *>(d));
                 wait_ld();
@@ -722,8 +735,8 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                     f32x2 x = add2(pair(d[i], d[i + 1]), pair(m.x, m.y));
                     f32x2 y = add2(pair(d[i + 2], d[i + 3]), pair(m.z, m.w));
                     if constexpr (kScaled<T>) {
-                        x = mul2(x, both(sc.ds));
-                        y = mul2(y, both(sc.ds));
+                        x = mul2(x, up2);
+                        y = mul2(y, up2);
                     }
                     const float2 e = halves(mul2(x, pair(p[i], p[i + 1])));
                     const float2 f = halves(mul2(y, pair(p[i + 2], p[i + 3])));
@@ -754,7 +767,8 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
             const int cut = min(s.dim, (s.dim / 2 + 15) / 16 * 16);
             const unsigned at_sum = (is_dk ? dk_at : dv_at) + lanes;
             const int c0 = part & 1 ? cut : 0, c1 = part & 1 ? s.dim : cut;
-            const float scale = is_dk ? a.scale * sc.inv_ds : sc.inv_p;
+            float scale = is_dk ? a.scale : 1.0f;
+            if constexpr (kScaled<T>) scale *= power_of_two(is_dk ? -bits : -kProbBits);
             if (a.key_parts == 1) {
                 T *const out = static_cast<T *>(is_dk ? a.dk : a.dv);
                 store_row<T>(at_sum, c0, c1, scale, none, ok, mine && out, out + out_at * s.dim);
@@ -908,8 +922,9 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
             const float *const stats =
                 a.stats + ((long long)w.head * a.q_tiles + w.pl.q_tiles_before + w.pl.tile) * 2 * kAttnTile;
             const f32x2 l2 = both(stats[row]);
-            const Scales sc = scales_of<T>(a, w.head / s.group);
-            const f32x2 n2 = both(stats[kAttnTile + row] * sc.ds);
+            const float less = stats[kAttnTile + row];
+            const uint2 largest = ask_largest<T>(a, w.pl.sequence, w.head / s.group);
+            int bits = 0;  // as above
             int end = s.causal ? min(w.pl.keys, w.pl.tile * kAttnTile + row + 1 + w.pl.shift) : w.pl.keys;
             if (end == 1) end = 0;  // ds = 0, as above
             for (int j = 0; ok && j < total; ++j, ++tiles) {
@@ -932,12 +947,15 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
                 ok = attn_wait_warp(&bar.dp_full, tiles & 1, failed);
                 if (!ok) break;
                 fence_after();
+                if (kScaled<T> && j == 0) bits = scale_bits(largest, s.dim);
+                const float up = kScaled<T> ? power_of_two(bits - kProbBits) : 1.0f;
+                const f32x2 n2 = both(less * up);
                 ld32(my_dp, reinterpret_cast<uint32_t *>(d));
                 wait_ld();
 #pragma unroll
                 for (int i = 0; i < kColumns; i += 2) {
                     f32x2 x = pair(d[i], d[i + 1]);
-                    x = kScaled<T> ? fma2(x, both(sc.ds), n2) : add2(x, n2);
+                    x = kScaled<T> ? fma2(x, both(up), n2) : add2(x, n2);
                     const float2 e = halves(mul2(x, pair(p[i], p[i + 1])));
                     d[i] = e.x;
                     d[i + 1] = e.y;
@@ -957,8 +975,8 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
             const AttnPlace pl = w.pl;
             const int query = pl.tile * kAttnTile + row;
             const long long out_at = ((long long)pl.batch * s.q_tokens + pl.q_row + query) * s.heads + w.head;
-            store_row<T>(dq_at + lanes, min(s.dim, part * 32), min(s.dim, part * 32 + 32), a.scale * sc.inv_ds,
-                         total == 0, ok, query < pl.queries, static_cast<T *>(a.dq) + out_at * s.dim);
+            const float scale = kScaled<T> ? a.scale * power_of_two(-bits) : a.scale;
+            store_row<T>(dq_at + lanes, min(s.dim, part * 32), min(s.dim, part * 32 + 32), scale, total == 0, ok, query < pl.queries, static_cast<T *>(a.dq) + out_at * s.dim);
         }
     }
 }
@@ -1031,7 +1049,7 @@ cudaError_t launch(const AttnBwdArgs &a, cudaStream_t stream)
     cudaError_t e = allow_smem(attention_bwd_kernel<T, DP>, done, smem);
     if (e != cudaSuccess) return e;
     if (kScaled<T> && a.largest) {
-        e = cudaMemsetAsync(a.largest, 0, size_t(2) * a.s.kv_heads * sizeof(unsigned), stream);
+        e = cudaMemsetAsync(a.largest, 0, size_t(2) * (a.s.sequences + 1) * a.s.kv_heads * sizeof(unsigned), stream);
         if (e != cudaSuccess) return e;
     }
     if (a.q_tiles > 0) {

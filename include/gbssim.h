@@ -479,8 +479,9 @@ int gbssim_attention_fwd(const gbssim_attention *desc, void *out, float *lse_or_
  * the last two over all query heads that share the key head.  desc is the forward's,
  * out and lse are what it wrote.  Outputs are dense, of q's, k's and v's shapes, and
  * overwritten; NULL: not wanted.  p and ds are rounded to the tensors' type for their
- * products (in float16 times powers of two that keep small gradients), sums are
- * float32.  A query that sees one key has a zero gradient, exactly. */
+ * products (in float16 times powers of two that keep small gradients, one for each key
+ * head of a sequence, from its own finite |grad_out| and |v|), sums are float32.  A
+ * query that sees one key has a zero gradient, exactly. */
 int gbssim_attention_bwd(const gbssim_attention *desc, const gbssim_heads *grad_out,
                          const gbssim_heads *out, const float *lse, void *grad_q_or_null, void *grad_k_or_null,
                          void *grad_v_or_null, void *workspace, size_t workspace_bytes, void *stream);
