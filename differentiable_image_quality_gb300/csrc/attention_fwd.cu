@@ -63,10 +63,17 @@ constexpr size_t fwd_smem()
 }
 
 // The rescaling of a row's accumulator is put off until its maximum has grown by
-// this much (of the exponent, base 2): probabilities stay below 2^8, which float32
-// sums and either 16-bit type hold without loss, and after the first tiles hardly
-// any row needs it.
-constexpr float kLateMax = 8.0f;
+// kLate (of the exponent, base 2), so that after the first tiles hardly any row needs it:
+// probabilities stay below 2^kLate, which float32 sums and bfloat16 hold without loss.
+// float16 has room for little below 2^-14: there they go into their product times 2^kUp,
+// up to 2^15 together, so that what is 2^-25 of a row's largest keeps all its digits and
+// the least step is 2^-35 of it.  (8 x 1024, 16 heads of 72: 50.5 us with 8 and 7, 50.5
+// so, 51.8 with 3 and 12, 57.4 with 2 and 13; 8192, 16 heads of 64, scores of standard
+// deviation 3: 275, 290, 293, 297.)
+template <typename T>
+constexpr float kLate = std::is_same<T, f16>::value ? 4.0f : 8.0f;
+template <typename T>
+constexpr float kUp = std::is_same<T, f16>::value ? 11.0f : 0.0f;
 
 // The index-th of the call's, by a whole warp.  Those of one head follow one another,
 // so that its keys stay in L2; causal ones by falling work instead, the longest first.
@@ -413,10 +420,10 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
 #pragma unroll
                 for (int i = 4; i < 128; i += 2) m[i / 2 % 4] = fmaxf(fmaxf(m[i / 2 % 4], v[i]), v[i + 1]);
                 const float now = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c;
-                if (__any_sync(0xffffffffu, now > top + kLateMax)) {
+                if (__any_sync(0xffffffffu, now > top + kLate<T>)) {
                     // each row by itself: what else is in the tile (rows that are no query
                     // among them) changes no bit of it
-                    const float next = now > top + kLateMax ? now : top;
+                    const float next = now > top + kLate<T> ? now : top;
                     const float f = next == -INFINITY ? 1.0f : exp2_fast(top - next);
                     top = next;
                     sum *= f;
@@ -431,7 +438,7 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
                         }
                     }
                 }
-                const float off = top == -INFINITY ? 0.0f : -top;
+                const float off = top == -INFINITY ? 0.0f : kUp<T> - top;
                 const f32x2 c2 = both(c), off2 = both(off);
                 f32x2 part[2] = {0, 0};
 #pragma unroll
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
             fence_after();
             const float scale = ok ? (sum == 0.0f ? 0.0f : 1.0f / sum) : NAN;
             const float lse =
-                !ok ? NAN : sum == 0.0f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+                !ok ? NAN : sum == 0.0f ? -INFINITY : (top + (log2f(sum) - kUp<T>)) * 0.69314718055994531f;
             // dense rows [batch, token, head], of all parts where the keys are split
             const long long at =
                 ((long long)w.pl.batch * s.q_tokens + w.pl.q_row + token) * s.heads + row_head;

@@ -445,8 +445,9 @@ int gbssim_rotary_turn(const gbssim_rotary *desc, void *q_out, void *k_out, void
  * a query's own sequence may reach its output although it does not see them.
  *
  * Types: bfloat16 or float16, one for all tensors.  Scores, statistics and sums are
- * float32; p is rounded to the tensors' type for its product with v, each output
- * once.  Shapes: any number of tokens, 0 and 1 included; dim a multiple of 8 up to
+ * float32; p is rounded to the tensors' type for its product with v (in float16 times a
+ * power of two: what is 2^-25 of a row's largest keeps all digits, the least step is
+ * 2^-35 of it), each output once.  Shapes: any number of tokens, 0 and 1 included; dim a multiple of 8 up to
  * 128.  Inputs have any positive strides that are multiples of 16 bytes, the
  * elements of a head side by side, and start on 16 bytes; outputs are dense. */
 
