@@ -603,11 +603,11 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
                 }
             }
         }
-        if (!ok) {
+        if (!ok || !a.queries_wanted) {  // what is in flight lands before the block ends
             if (uses > 0) mbar_wait_bounded(&bar.own_full, (uses - 1) & 1, kAttnDrainCycles);
             for (int i = max(0, it - kStages); i < it; ++i)
                 mbar_wait_bounded(&bar.full[i % kStages], (i / kStages) & 1, kAttnDrainCycles);
-        } else if (uses > 0 && a.queries_wanted) {
+        } else if (uses > 0) {
             // the other kind's tiles take the place of these
             ok = attn_wait_warp(&bar.own_empty, (uses - 1) & 1, failed);
         }
@@ -852,13 +852,12 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
                 v_at.next();
             }
         }
-        if (!ok) {
-            if (uses > 0) mbar_wait_bounded(&bar.own_full, (uses - 1) & 1, kAttnDrainCycles);
-            for (int i = max(0, issued - kKeys); i < issued; ++i)
-                mbar_wait_bounded(&k_full[i % kKeys], (i / kKeys) & 1, kAttnDrainCycles);
-            for (int i = max(0, issued - kValues); i < issued; ++i)
-                mbar_wait_bounded(&v_full[i % kValues], (i / kValues) & 1, kAttnDrainCycles);
-        }
+        // what is in flight lands before the block ends
+        if (uses > 0) mbar_wait_bounded(&bar.own_full, (uses - 1) & 1, kAttnDrainCycles);
+        for (int i = max(0, issued - kKeys); i < issued; ++i)
+            mbar_wait_bounded(&k_full[i % kKeys], (i / kKeys) & 1, kAttnDrainCycles);
+        for (int i = max(0, issued - kValues); i < issued; ++i)
+            mbar_wait_bounded(&v_full[i % kValues], (i / kValues) & 1, kAttnDrainCycles);
     } else if (warp == kWarps + 1) {
         const unsigned leader = elect_leader();
         const int steps = (s.dim + 15) / 16;
@@ -1030,10 +1029,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attention_bwd_kernel(const __g
         commit(smem_u32(&sh.drained), elect_leader());
         mbar_wait_bounded(&sh.drained, 0, kAttnDrainCycles);
     }
-    if (!ok && warp == kWarps && lane == 0) atomicOr(&g_attention_status, 4u);
     __syncwarp();
     fence_before();
     __syncthreads();
+    // here, since a wait may have run out in any warp, and after the others had nothing to
+    // wait for any more
+    if (threadIdx.x == 0 && *static_cast<volatile unsigned *>(&sh.failed)) atomicOr(&g_attention_status, 4u);
     if (warp == kWarps + 1) {
         fence_after();
         free_all(tmem);

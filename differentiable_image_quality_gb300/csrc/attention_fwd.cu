@@ -292,13 +292,12 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
                 ++it;
             }
         }
-        if (*failed && lane == 0) {
-            // what is still in flight lands first
+        if (lane == 0) {
+            // what is still in flight lands before the block ends
             for (int i = max(0, it - kStages); i < it; ++i)
                 mbar_wait_bounded(&sh.kv_full[i % kStages], (i / kStages) & 1, kAttnDrainCycles);
             for (int t = 0; t < QT; ++t)
                 if (uses[t] > 0) mbar_wait_bounded(&sh.q_full[t], (uses[t] - 1) & 1, kAttnDrainCycles);
-            atomicOr(&g_attention_status, 4u);
         }
     } else if (warp == kIssue) {
         // ---- products
@@ -507,6 +506,9 @@ __global__ void __launch_bounds__(fwd_threads<QT>(), 1) attention_fwd_kernel(con
     __syncwarp();
     fence_before();
     __syncthreads();
+    // here, since a wait may have run out in any warp, and after the others had nothing to
+    // wait for any more
+    if (threadIdx.x == 0 && *failed) atomicOr(&g_attention_status, 4u);
     if (warp == kIssue) {
         fence_after();
         free_all(tmem);
