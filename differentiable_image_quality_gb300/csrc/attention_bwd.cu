@@ -89,53 +89,77 @@ constexpr int kSumTokens = 32, kSumHeads = 64, kSumRows = 4;
 constexpr int kShareSequences = 128;  // four steps of the search
 
 // Over few keys the output's rounding is a good part of dp - D: there D = sum_j p_ij dp_ij
-// in float32 instead, whose dots cost little.  A kernel of its own (FEW) for calls that
-// can have such sequences and are small, since the registers for it would slow down the
-// others.  By a whole warp, `g` a lane's eight columns of the row's gradient.
-constexpr int kFewKeys = 16, kFewTokens = 2048;
+// in float32 instead, whose dots cost little.  By a whole warp, LANES to a row of `g`, two
+// keys at a time: halves of the lanes add up one key's dots each, half of those s, the
+// others dp (each dot in all lanes: the sums of 4096 sequences of 16 tokens, 8 heads of 64, took
+// 357 us for 276).
+constexpr int kFewKeys = 16;
+
+// Eight columns as pairs, and their dot with others.
+template <typename T>
+__device__ __forceinline__ void load_pairs(const T *p, f32x2 (&v)[4])
+{
+    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 x = unpack2<T>(words[e]);
+        v[e] = pair(x.x, x.y);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float dot8(const T *p, const f32x2 (&v)[4])
+{
+    f32x2 u[4], sum = 0;
+    load_pairs<T>(p, u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum = fma2(u[e], v[e], sum);
+    return sum2(sum);
+}
 
 template <typename T, int LANES>
-__device__ __forceinline__ float sum_of_few(const AttnBwdArgs &a, const AttnPlace &pl, int query, int head, bool mine,
-                                         const float (&g)[8])
+__device__ __forceinline__ float sum_of_few(const AttnBwdArgs &a, const AttnPlace &pl, int query, int head, bool some,
+                                            const T *g_row)
 {
     const AttnShape &s = a.s;
-    const int col = threadIdx.x % LANES * 8, kv_head = head / s.group;
-    const int seen = !mine ? 0 : s.causal ? min(pl.keys, query + 1 + pl.shift) : pl.keys;
-    float q[8] = {}, lse = 0.0f, sum = 0.0f;
-    if (seen > 0) {
-        Raw8<T> r;
-        r.w[0] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q_data) + pl.batch * a.q_batch +
-                                                  (long long)(pl.q_row + query) * a.q_token + head * a.q_head + col);
-        unpack8<T>(r, q);
-        lse = a.lse[((long long)pl.batch * s.heads + head) * s.q_tokens + pl.q_row + query] * 1.4426950408889634f;
+    const int lane = threadIdx.x % LANES, col = lane * 8, kv_head = head / s.group;
+    const int seen = !some ? 0 : s.causal ? min(pl.keys, query + 1 + pl.shift) : pl.keys;
+    const int mine = col < s.dim ? seen : 0;  // keys that this lane has columns of
+    f32x2 g[4] = {}, q[4] = {};
+    float lse = 0.0f, sum = 0.0f;
+    if (mine > 0) {
+        load_pairs<T>(static_cast<const T *>(a.q_data) + pl.batch * a.q_batch + (long long)(pl.q_row + query) * a.q_token +
+                          head * a.q_head + col,
+                      q);
+        load_pairs<T>(g_row, g);
     }
-    for (int j = 0; j < pl.keys; ++j) {
-        float x = 0.0f, y = 0.0f;
-        if (j < seen) {
-            Raw8<T> rk, rv;
-            rk.w[0] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.k_data) + pl.batch * a.k_batch +
-                                                       (long long)(pl.k_row + j) * a.k_token + kv_head * a.k_head + col);
-            rv.w[0] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v_data) + pl.batch * a.v_batch +
-                                                       (long long)(pl.k_row + j) * a.v_token + kv_head * a.v_head + col);
-            float k[8], v[8];
-            unpack8<T>(rk, k);
-            unpack8<T>(rv, v);
+    if (seen > 0)
+        lse = a.lse[((long long)pl.batch * s.heads + head) * s.q_tokens + pl.q_row + query] * 1.4426950408889634f;
+    const T *k = static_cast<const T *>(a.k_data) + pl.batch * a.k_batch + pl.k_row * a.k_token + kv_head * a.k_head + col;
+    const T *v = static_cast<const T *>(a.v_data) + pl.batch * a.v_batch + pl.k_row * a.v_token + kv_head * a.v_head + col;
+    const int second = lane & 1;
+    const bool is_dp = lane & 2;
+    for (int j = 0; j < pl.keys; j += 2) {
+        float x[2], y[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x = fmaf(q[e], k[e], x);
-                y = fmaf(g[e], v[e], y);
-            }
+        for (int i = 0; i < 2; ++i) {
+            x[i] = j + i < mine ? dot8<T>(k, q) : 0.0f;
+            y[i] = j + i < mine ? dot8<T>(v, g) : 0.0f;
+            k += a.k_token;
+            v += a.v_token;
         }
         __syncwarp();
+        const float xs = (second ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, second ? x[0] : x[1], 1);
+        const float ys = (second ? y[1] : y[0]) + __shfl_xor_sync(0xffffffffu, second ? y[0] : y[1], 1);
+        float z = (is_dp ? ys : xs) + __shfl_xor_sync(0xffffffffu, is_dp ? xs : ys, 2);
 #pragma unroll
-        for (int d = LANES / 2; d; d /= 2) {
-            x += __shfl_xor_sync(0xffffffffu, x, d);
-            y += __shfl_xor_sync(0xffffffffu, y, d);
-        }
-        // a lane without columns has seen none: its team's sum is right in the others
-        if (j < seen) sum = fmaf(exp2_fast(fmaf(x, a.scale_log2, -lse)), y, sum);
+        for (int d = 4; d < LANES; d *= 2) z += __shfl_xor_sync(0xffffffffu, z, d);
+        const float dp = __shfl_xor_sync(0xffffffffu, z, 2);
+        if (!is_dp && j + second < seen) sum = fmaf(exp2_fast(fmaf(z, a.scale_log2, -lse)), dp, sum);
     }
-    return sum;
+    __syncwarp();
+    return sum + __shfl_xor_sync(0xffffffffu, sum, 1);  // in the first two lanes
 }
 
 // Where the search of a block of row sums starts: each warp counts the tiles of its share
@@ -179,8 +203,8 @@ __device__ __forceinline__ void skip_shares(const AttnShape &s, bool by_keys, in
     __syncthreads();
 }
 
-template <typename T, int LANES, bool FEW>
-__global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnBwdArgs a, const unsigned q_blocks)
+template <typename T, int LANES>
+__global__ void __launch_bounds__(kSumThreads, 4) attention_sums_kernel(const AttnBwdArgs a, const unsigned q_blocks)
 {
     constexpr int kTeams = kSumThreads / LANES;
     __shared__ AttnPlace place;
@@ -227,7 +251,8 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
     const int counted = values ? (pl.queries > 0 ? 0 : INT_MAX)
                         : pl.keys == 0 ? INT_MAX : s.causal ? -pl.shift - first : 0;
     const int all = count * heads;
-    for (int base = 0; base < all; base += kTeams * kSumRows) {  // all threads alike: they shuffle
+    const bool few = !values && pl.keys <= kFewKeys;
+    for (int base = 0; (kScaled<T> || !few) && base < all; base += kTeams * kSumRows) {  // all threads alike: they shuffle
         Raw8<T> rx[kSumRows], ro[kSumRows];
 #pragma unroll
         for (int i = 0; i < kSumRows; ++i) {
@@ -249,8 +274,6 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
                 __syncwarp();
 #pragma unroll
                 for (int d = LANES / 2; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                if (FEW && pl.keys <= kFewKeys)
-                    sum = sum_of_few<T, LANES>(a, pl, first + t, from + h, mine && r < all, u);
                 if (lane == 0 && r < all) sums[h][t] = sum;
             }
             if constexpr (kScaled<T>) {
@@ -261,6 +284,14 @@ __global__ void __launch_bounds__(kSumThreads) attention_sums_kernel(const AttnB
                 if (lane == 0 && r < all) atomicMax(&most[h], m);
             }
         }
+    }
+    // a loop of its own, so that the other's registers are enough; float16's sums are written
+    // anew by the threads that wrote them
+    for (int base = 0; few && base < all; base += kTeams) {
+        const int r = base + team, t = r / heads, h = r - t * heads;
+        const float sum =
+            sum_of_few<T, LANES>(a, pl, first + t, from + h, r < all, x + t * x_token + h * x_head);
+        if (lane == 0 && r < all) sums[h][t] = sum;
     }
     __syncthreads();
     if constexpr (kScaled<T>) {
@@ -1057,11 +1088,9 @@ cudaError_t launch(const AttnBwdArgs &a, cudaStream_t stream)
         const unsigned q_blocks = unsigned(most_tiles(a.s, a.s.q_tokens, kSumTokens));
         const unsigned v_blocks = kScaled<T> ? unsigned(most_tiles(a.s, a.s.k_tokens, kSumTokens)) : 0;
         const dim3 grid(q_blocks + v_blocks, unsigned((a.s.heads + kSumHeads - 1) / kSumHeads));
-        const bool few = a.s.k_tokens <= (a.ragged ? kFewTokens : kFewKeys);
-        const auto kernel = a.s.dim <= 32   ? few ? attention_sums_kernel<T, 4, true> : attention_sums_kernel<T, 4, false>
-                            : a.s.dim <= 64 ? few ? attention_sums_kernel<T, 8, true> : attention_sums_kernel<T, 8, false>
-                            : few           ? attention_sums_kernel<T, 16, true>
-                                            : attention_sums_kernel<T, 16, false>;
+        const auto kernel = a.s.dim <= 32   ? attention_sums_kernel<T, 4>
+                            : a.s.dim <= 64 ? attention_sums_kernel<T, 8>
+                                            : attention_sums_kernel<T, 16>;
         kernel<<<grid, kSumThreads, 0, stream>>>(a, q_blocks);
     } else {
         e = cudaMemsetAsync(a.counter, 0, sizeof(unsigned), stream);
