@@ -22,7 +22,6 @@ struct AttnShape {
     int q_tokens, k_tokens;  // of a sample, or rows of the packed tensors
     int heads, kv_heads, group, dim;
     int causal, packed;
-    int q_tiles;             // of 128 queries, or the most there can be (packed)
     const int *kv_lengths, *q_offsets, *k_offsets;
 };
 
@@ -114,7 +113,6 @@ __device__ __forceinline__ bool find_place(const AttnShape &s, int index, int ro
             // the rows behind the last sequences have no partners
             if (base + l == s.sequences) (BY_KEYS ? p.queries : p.keys) = 0;
             p.shift = p.keys - p.queries;
-            keep_within(s.q_tiles, p.q_tiles_before, p.queries);
             found = true;
         } else {
             c.base += 32;

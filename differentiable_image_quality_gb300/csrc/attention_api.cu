@@ -96,10 +96,8 @@ int check_desc(const gbssim_attention *d)
 
 AttnShape shape_of(const gbssim_attention &d)
 {
-    AttnShape s{d.sequences, d.q_tokens, d.k_tokens, d.heads, d.kv_heads, d.heads / d.kv_heads, d.dim,
-                d.causal != 0, is_packed(d), 0, d.kv_lengths, d.q_offsets, d.k_offsets};
-    s.q_tiles = d.q_tokens ? int(std::min<long long>(most_tiles(s, d.q_tokens, kAttnTile), INT_MAX)) : 0;
-    return s;
+    return {d.sequences, d.q_tokens, d.k_tokens, d.heads, d.kv_heads, d.heads / d.kv_heads, d.dim,
+            d.causal != 0, is_packed(d), d.kv_lengths, d.q_offsets, d.k_offsets};
 }
 
 // A stride that nothing is read along has to be a valid one all the same.

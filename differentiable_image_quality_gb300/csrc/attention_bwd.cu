@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(kSumThreads, 4) attention_sums_kernel(const At
     }
     if (values) return;
     // the sequence's last block also has the rows that its last tile does not have
-    const int end = first + kSumTokens >= rows ? (rows + kAttnTile - 1) / kAttnTile * kAttnTile : first + kSumTokens;
+    const int tiles = tiles_within(a.q_tiles, pl.q_tiles_before, (rows + kAttnTile - 1) / kAttnTile);
+    const int end = first + kSumTokens >= rows ? tiles * kAttnTile : min(first + kSumTokens, tiles * kAttnTile);
     const int width = end - first;
     for (int i = threadIdx.x; i < heads * width; i += kSumThreads) {
         const int h = i / width, r = i - h * width, t = first + r, head = from + h;
@@ -338,9 +339,9 @@ struct BwdBarriers {
 constexpr int kItemSlots = 4;
 
 // An item: a tile of keys of a key head, or of queries of a head, and what goes over it.
+// (Sixteen words: with seventeen, 4096 packed sequences of 128 tokens took 2 % longer.)
 struct BwdItem {
     AttnPlace pl;
-    bool there;
     int head, part;    // part of the query heads that share a key head
     int from, all;     // keys: tiles of queries, from the first that sees the first key
     int q_head;        // keys: the first query head
@@ -396,19 +397,19 @@ __device__ __forceinline__ void find_item(const AttnBwdArgs &a, unsigned u, BwdI
         w.head = u / all;
         index = u % all;
     }
-    w.there = find_place<KEYS>(s, index, kAttnTile, w.pl, cursor);
-    if (!w.there) w.pl = {};  // packed: fewer tiles than there could be
+    // packed: fewer tiles than there could be, then without rows
+    if (!find_place<KEYS>(s, index, kAttnTile, w.pl, cursor)) w.pl = {};
     const AttnPlace &pl = w.pl;
     if (KEYS) {
         const int per = (s.group + a.key_parts - 1) / a.key_parts, first = pl.tile * kAttnTile;
         w.q_head = w.head * s.group + w.part * per;
-        w.all = (pl.queries + kAttnTile - 1) / kAttnTile;
+        w.all = tiles_within(a.q_tiles, pl.q_tiles_before, (pl.queries + kAttnTile - 1) / kAttnTile);
         w.from = s.causal ? min(max(first - pl.shift, 0) / kAttnTile, w.all) : 0;
-        w.total = w.there && first < pl.keys ? (w.all - w.from) * max(0, min(per, s.group - w.part * per)) : 0;
+        w.total = first < pl.keys ? (w.all - w.from) * max(0, min(per, s.group - w.part * per)) : 0;
     } else {
         int seen = pl.keys;
         if (s.causal) seen = min(seen, min((pl.tile + 1) * kAttnTile, pl.queries) + pl.shift);
-        w.total = !w.there || seen <= 0 ? 0 : (seen + kAttnTile - 1) / kAttnTile;
+        w.total = seen <= 0 ? 0 : (seen + kAttnTile - 1) / kAttnTile;
     }
 }
 
@@ -791,7 +792,7 @@ __device__ __forceinline__ void by_keys(const AttnBwdArgs &a, char *base, BwdSha
             fence_after();
             const AttnPlace pl = w.pl;
             const int key = pl.tile * kAttnTile + row, count = s.packed ? pl.keys : s.k_tokens;
-            const bool mine = w.there && key < count, none = total == 0 || key >= pl.keys;
+            const bool mine = key < count, none = total == 0 || key >= pl.keys;
             const long long out_at = ((long long)pl.batch * s.k_tokens + pl.k_row + key) * s.kv_heads + w.head;
             // two parts store dv, two dk, half of the columns each
             const bool is_dk = part >= 2;
@@ -947,7 +948,6 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
         const f32x2 c2 = both(a.scale_log2);
         unsigned uses = 0, tiles = 0;
         for (; w.u < a.items; w = take_item(sh, n)) {
-            if (!w.there) continue;
             const int total = w.total;
             const float *const stats =
                 a.stats + ((long long)w.head * a.q_tiles + w.pl.q_tiles_before + w.pl.tile) * 2 * kAttnTile;

@@ -33,12 +33,12 @@ constexpr int kMostTiles = (1 << 30) - 1;
 
 __host__ __device__ inline int add_tiles(int a, int b) { return a + b < kMostTiles ? a + b : kMostTiles; }
 
-// ... and a sequence's queries end where the room does, `tiles` of 128 rows in all.
-__host__ __device__ inline void keep_within(int tiles, int &tiles_before, int &rows)
+// ... and of a sequence's tiles of queries those count that there is room for, `room` in
+// all, behind the ones before it.
+__host__ __device__ inline int tiles_within(int room, int before, int tiles)
 {
-    tiles_before = std::min(std::max(tiles_before, 0), tiles);
-    const int left = tiles - tiles_before;
-    if ((rows + kAttnTile - 1) / kAttnTile > left) rows = left * kAttnTile;
+    const int left = room - before;
+    return left < 0 ? 0 : left < tiles ? left : tiles;
 }
 
 }  // namespace gbssim
