@@ -151,7 +151,13 @@ def fused_rotary(q, k, positions, frequencies, pairs, *, layout="half"):
     q is [batch, tokens, heads, dim] or [tokens, heads, dim], float32, bfloat16 or
     float16, dim up to 512, k the same with its own number of heads, or None.  positions
     are int32, int64 or float32, [tokens, axes] for all samples or [batch, tokens, axes].
-    Angles are reduced in 64-bit fixed point: far positions are as exact as near ones.
+    Frequencies have any size and sign.  Angles are reduced in 64-bit fixed point: what far
+    positions lose is the rounding of f / (2 pi) to float64, times the position.
+    Positions and frequencies get no gradient, and are refused where they ask for one.
     Returns (q', k'), dense, rounded once from float32."""
+    if torch.is_grad_enabled():
+        for name, t in (("positions", positions), ("frequencies", frequencies)):
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{name} get no gradient here: detach them, or turn under no_grad")
     return _FusedRotary.apply(q, k, positions, frequencies,
                               {"pairs": tuple(pairs), "layout": layout})
