@@ -206,9 +206,10 @@ inline cudaError_t allow_smem(Kernel kernel, std::atomic<unsigned long long> &do
 
 // A launch whose blocks may start while the kernel ahead on the stream ends; they wait
 // for it (pdl_wait) before they touch what it wrote.
+// `kernel_ahead`: what is ahead is one; behind a copy or a fill nothing starts early.
 template <typename Args>
 inline cudaError_t launch_after(void (*kernel)(Args), dim3 grid, unsigned threads, size_t smem,
-                                cudaStream_t stream, const Args &a)
+                                cudaStream_t stream, const Args &a, bool kernel_ahead = true)
 {
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -219,7 +220,7 @@ inline cudaError_t launch_after(void (*kernel)(Args), dim3 grid, unsigned thread
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = &early;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = kernel_ahead;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 

@@ -1100,7 +1100,7 @@ cudaError_t launch(const AttnBwdArgs &a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     if (a.items == 0) return cudaSuccess;
     e = launch_after(attention_bwd_kernel<T, DP>, dim3(std::min(a.items, unsigned(kAttnBlocks))), kBwdThreads, smem,
-                     stream, a);
+                     stream, a, a.q_tiles > 0);
     if (e != cudaSuccess || a.key_parts == 1) return e;
     const long long n = (long long)(a.s.packed ? 1 : a.s.sequences) * a.s.k_tokens * a.s.kv_heads * a.s.dim / 8;
     return launch_after(attention_join_keys_kernel<T>, dim3(unsigned((n + kJoinThreads - 1) / kJoinThreads), 2),
