@@ -48,9 +48,9 @@ struct AttnCursor {
 
 // The sequence and tile of `index`, tiles of `rows` rows of the queries or (BY_KEYS)
 // the keys, all of a sequence's before the next one's; false behind the last.  By
-// a whole warp; `kept` is that warp's alone, zero before its first search, or null.
+// a whole warp; `kept` is that warp's alone, zero before its first search.
 template <bool BY_KEYS>
-__device__ __forceinline__ bool find_place(const AttnShape &s, int index, int rows, AttnPlace &p, AttnCursor *kept)
+__device__ __forceinline__ bool find_place(const AttnShape &s, int index, int rows, AttnPlace &p, AttnCursor &kept)
 {
     if (!s.packed) {
         const int most = BY_KEYS ? s.k_tokens : s.q_tokens;
@@ -66,7 +66,7 @@ __device__ __forceinline__ bool find_place(const AttnShape &s, int index, int ro
     }
     const int lane = threadIdx.x % 32;
     AttnCursor c{0, 0, 0, BY_KEYS};
-    if (kept && kept->by_keys == BY_KEYS && index >= kept->before / 2) c = *kept;
+    if (kept.by_keys == BY_KEYS && index >= kept.before / 2) c = kept;
     bool found = false;
     bool back = index < c.before;
     if (back) c.base -= 32;
@@ -120,11 +120,9 @@ __device__ __forceinline__ bool find_place(const AttnShape &s, int index, int ro
             c.q_before = add_tiles(c.q_before, q_all);
         }
     }
-    if (kept) {
-        __syncwarp();
-        if (lane == 0) *kept = c;
-        __syncwarp();
-    }
+    __syncwarp();
+    if (lane == 0) kept = c;
+    __syncwarp();
     return found;
 }
 

@@ -224,8 +224,8 @@ __global__ void __launch_bounds__(kSumThreads, 4) attention_sums_kernel(const At
     if (threadIdx.x < 32) {
         __syncwarp();
         AttnPlace p;
-        const bool ok = values ? find_place<true>(s, index, kSumTokens, p, &start)
-                               : find_place<false>(s, index, kSumTokens, p, &start);
+        const bool ok = values ? find_place<true>(s, index, kSumTokens, p, start)
+                               : find_place<false>(s, index, kSumTokens, p, start);
         if (threadIdx.x == 0) {
             place = p;
             there = ok;
@@ -374,7 +374,7 @@ __device__ __forceinline__ bool wait_item(BwdShared &sh, uint64_t *bar, unsigned
 // L2, or packed a tile's heads, so that the search has a short way (200 sequences of up
 // to 600 tokens, 24 heads of 64: 904 -> 817 us).
 template <bool KEYS>
-__device__ __forceinline__ void find_item(const AttnBwdArgs &a, unsigned u, BwdItem &w, AttnCursor *cursor)
+__device__ __forceinline__ void find_item(const AttnBwdArgs &a, unsigned u, BwdItem &w, AttnCursor &cursor)
 {
     const AttnShape &s = a.s;
     if (!KEYS) u -= a.key_items;
@@ -424,9 +424,9 @@ __device__ __forceinline__ BwdItem publish_item(const AttnBwdArgs &a, BwdShared 
     if (threadIdx.x % 32 == 0) w.u = atomicAdd(a.counter, 1u);
     w.u = uniform(w.u);
     if (w.u < a.key_items)
-        find_item<true>(a, w.u, w, &sh.cursor);
+        find_item<true>(a, w.u, w, sh.cursor);
     else if (w.u < a.items)
-        find_item<false>(a, w.u, w, &sh.cursor);
+        find_item<false>(a, w.u, w, sh.cursor);
     if (n >= kItemSlots && !wait_item(sh, &sh.item_empty[slot], (n / kItemSlots - 1) & 1)) return sh.none;
     ++n;
     if (threadIdx.x % 32 == 0) {

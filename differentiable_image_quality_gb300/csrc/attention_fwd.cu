@@ -81,7 +81,7 @@ constexpr float kUp = std::is_same<T, f16>::value ? 11.0f : 0.0f;
 // sequences of up to 1500 tokens, 16 heads of 64: 95 -> 91 us; 200 of up to 600, 24 heads
 // of 64: 318 -> 276).
 template <int QT>
-__device__ __forceinline__ void find_item(const AttnFwdArgs &a, unsigned u, FwdItem<QT> &w, AttnCursor *cursor)
+__device__ __forceinline__ void find_item(const AttnFwdArgs &a, unsigned u, FwdItem<QT> &w, AttnCursor &cursor)
 {
     const AttnShape &s = a.s;
     const int head_blocks = s.heads / a.tile_heads;
@@ -158,7 +158,7 @@ __device__ __forceinline__ FwdItem<QT> publish_item(const AttnFwdArgs &a, FwdSha
     } else {
         w.u = item_of(n);
     }
-    if (w.u < a.items) find_item(a, w.u, w, &sh.cursor);
+    if (w.u < a.items) find_item(a, w.u, w, sh.cursor);
     if (n >= kItemSlots && !wait_item(sh, &sh.item_empty[slot], (n / kItemSlots - 1) & 1)) return sh.none;
     ++n;
     if (threadIdx.x % 32 == 0) {
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     __shared__ float sums[kJoinThreads][9];
     const AttnShape &s = a.s;
     const int chunks = s.dim / 8, teams = kJoinThreads / chunks;
-    const long long rows = (long long)(s.packed ? 1 : s.sequences) * s.q_tokens * s.heads;
+    const long long rows = (long long)s.sequences * s.q_tokens * s.heads;  // (a packed batch has no parts)
     const long long row = blockIdx.x;
     const int head = int(row % s.heads);
     const long long token = row / s.heads;
@@ -605,7 +605,7 @@ cudaError_t attention_fwd_launch(const AttnFwdArgs &a, int dtype, int q_tiles, c
 
 cudaError_t attention_join_launch(const AttnFwdArgs &a, int dtype, cudaStream_t stream)
 {
-    const unsigned grid = unsigned((long long)(a.s.packed ? 1 : a.s.sequences) * a.s.q_tokens * a.s.heads);
+    const unsigned grid = unsigned((long long)a.s.sequences * a.s.q_tokens * a.s.heads);
     if (dtype == GBSSIM_BF16)
         return launch_after(attention_join_kernel<bf16>, grid, kJoinThreads, 0, stream, a);
     return launch_after(attention_join_kernel<f16>, grid, kJoinThreads, 0, stream, a);

@@ -16,7 +16,6 @@
 // heads of 88, float32 (547 MB): 108 us; 512 tokens: 6.4 us.
 #include <algorithm>
 #include <climits>
-#include <mutex>
 
 #include "api_host.cuh"
 #include "dtypes.cuh"
@@ -368,7 +367,6 @@ cudaError_t launch_mode(const RotaryArgs &a, int v, cudaStream_t stream)
 {
     if (a.adjacent) return v == 8 ? launch<T, kAdjacent, 8>(a, stream) : launch<T, kSingle, 1>(a, stream);
     switch (v) {
-    case 8: return launch<T, kHalves, 8>(a, stream);
     case 4: return launch<T, kHalves, 4>(a, stream);
     case 2: return launch<T, kHalves, 2>(a, stream);
     default: return launch<T, kSingle, 1>(a, stream);
