@@ -211,7 +211,9 @@ def fused_attention(q, k, v, *, causal=False, scale=None, kv_lengths=None, offse
     neighbouring query heads share keys and values.  scale, positive, is dim ** -0.5 by
     default.  With ``causal``, query i sees the keys up to i + (keys - tokens): the last
     query sees all.  ``kv_lengths``, int32 [batch] on the GPU, are how many of a sample's
-    keys count; what lies behind them is not used and gets a zero gradient.
+    keys count; what lies behind them is not used and gets a zero gradient.  They do not
+    move ``causal``'s diagonal, which ends at the last key of the shape: several new tokens
+    against caches of different lengths are a packed batch, where it ends at each one's own.
 
     Packed batches: with ``offsets``, int32 [sequences + 1] on the GPU, ascending from 0, q
     is [rows, heads, dim] and sequence s its rows offsets[s] to offsets[s + 1] - 1, of any

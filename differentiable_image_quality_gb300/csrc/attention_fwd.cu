@@ -7,8 +7,8 @@
 // unit 512 and its issue slots about 400 for the softmax, which depends on the first
 // product and feeds the second: so a block has two tiles of queries, one's softmax
 // beside the other's products, the sums in tensor memory, keys and values in a ring of
-// tiles that the copy unit runs ahead in.  16384 causal tokens, 16 heads of 128: 583 us,
-// 1.88 PFLOP/s, bound by the tensor cores; heads of 64 (8192, 16 heads: 282 us) by both
+// tiles that the copy unit runs ahead in.  16384 causal tokens, 16 heads of 128: 568 us,
+// 1.94 PFLOP/s, bound by the tensor cores (642 in long runs, by power); heads of 64 (8192, 16 heads: 282 us) by both
 // units at about half; one token over 65536 keys (268 MB) 45 us, bound by memory.
 #include <climits>
 

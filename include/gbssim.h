@@ -440,9 +440,11 @@ int gbssim_rotary_turn(const gbssim_rotary *desc, void *q_out, void *k_out, void
  *
  * causal != 0: query i sees the keys up to i + (keys - queries), the last query all
  * of them; keys and queries are the counts of the shapes (batch form, whatever
- * kv_lengths says) or of the sequence (packed).
+ * kv_lengths says: for samples that are padded behind their tokens) or of the sequence
+ * (packed: also for new tokens against caches of different lengths).
  * A hidden key has p = 0 exactly.  A NaN or an infinity among the keys and values of
- * a query's own sequence may reach its output although it does not see them.
+ * a query's own sequence may reach its output although it does not see them, and one
+ * among queries and gradients the gradients of its own sequence.
  *
  * Types: bfloat16 or float16, one for all tensors.  Scores, statistics and sums are
  * float32; p is rounded to the tensors' type for its product with v (in float16 times a
