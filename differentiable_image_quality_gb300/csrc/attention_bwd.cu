@@ -91,8 +91,8 @@ constexpr int kShareSequences = 128;  // four steps of the search
 // Over few keys the output's rounding is a good part of dp - D: there D = sum_j p_ij dp_ij
 // in float32 instead, whose dots cost little.  By a whole warp, LANES to a row of `g`, two
 // keys at a time: halves of the lanes add up one key's dots each, half of those s, the
-// others dp (each dot in all lanes: the sums of 4096 sequences of 16 tokens, 8 heads of 64, took
-// 357 us for 276).
+// others dp (each dot in all lanes: the sums of 4096 sequences of 16 tokens, 8 heads of 64,
+// took 357 us for 276).
 constexpr int kFewKeys = 16;
 
 // Eight columns as pairs, and their dot with others.
@@ -1006,7 +1006,8 @@ __device__ __forceinline__ void by_queries(const AttnBwdArgs &a, char *base, Bwd
             const int query = pl.tile * kAttnTile + row;
             const long long out_at = ((long long)pl.batch * s.q_tokens + pl.q_row + query) * s.heads + w.head;
             const float scale = kScaled<T> ? a.scale * power_of_two(-bits) : a.scale;
-            store_row<T>(dq_at + lanes, min(s.dim, part * 32), min(s.dim, part * 32 + 32), scale, total == 0, ok, query < pl.queries, static_cast<T *>(a.dq) + out_at * s.dim);
+            store_row<T>(dq_at + lanes, min(s.dim, part * 32), min(s.dim, part * 32 + 32), scale, total == 0, ok,
+                         query < pl.queries, static_cast<T *>(a.dq) + out_at * s.dim);
         }
     }
 }
